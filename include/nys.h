@@ -357,6 +357,129 @@ int nys_o1_states(const nys_o1* o, nys_states** st);
 /* Release the trace and the states.  NULL is a no-op. */
 int nys_o1_free(nys_o1* o);
 
+/* ---- Exact attention next to the landmark states ---------------------------
+ * What a serving layer needs around nys_seal and nys_step_batch: the outputs
+ * of the prompt itself (the seal writes none), and the decode of layers and
+ * requests that stay exact (Struct LayerKvCache keeps them in a plain KV
+ * cache), here a pool of pages.  The pages have no counterpart for these
+ * calls.
+ *
+ * Tensors are fp32, bf16 or fp16 (nys_dtype), all tensors of one call alike;
+ * query head h reads KV head h / (heads / kv_heads).  Products are taken of
+ * the stored values and summed in fp32; the softmax runs in fp32 (16-bit
+ * types round its weights once, to the same type, for the second product).
+ * The conventions at the top hold, except that pointers need only their
+ * element type's alignment: rows that are 16-byte aligned and head dims up to
+ * 128 take the tiled kernels, everything else a general one. */
+typedef enum { NYS_F32 = 0, NYS_BF16 = 1, NYS_F16 = 2 } nys_dtype;
+
+typedef struct {
+  int32_t heads;    /* query heads, a multiple of kv_heads, at most 64 a KV head */
+  int32_t kv_heads; /* KV heads, >= 1                                            */
+  int32_t d;        /* query/key head dim, positive multiple of 4, at most 256   */
+  int32_t dv;       /* value head dim, the same                                  */
+  int32_t dtype;    /* nys_dtype                                                 */
+  float scale;      /* of the scores; 0 = 1/sqrt(d), taken in f32                */
+} nys_attn_config;
+
+/* A [rows][heads][dim] tensor: element (r, h, c) is
+ * ((T*)data)[r * row_stride + h * head_stride + c]; strides are non-negative,
+ * in elements. */
+typedef struct {
+  void* data;
+  int64_t row_stride;
+  int64_t head_stride;
+} nys_rows;
+
+/* A pool of KV pages: k [n_pages][page][kv_heads][d], v [..][dv], contiguous. */
+typedef struct {
+  void* k;
+  void* v;
+  int64_t n_pages;
+  int32_t page; /* tokens a page, >= 1 */
+} nys_pool;
+
+/* Bits of the device status word that the calls below take (one int32 that
+ * the caller zeroed, or NULL): what the host cannot see when it enqueues.
+ * Kernels only ever set bits. */
+enum {
+  NYS_ATTN_GAVE_UP = 1,     /* a bounded wait (2 s) ran out: outputs invalid       */
+  NYS_ATTN_BAD_OFFSETS = 2, /* offsets decreased or left the tensors; they were
+                               taken as clamped into them                          */
+  NYS_ATTN_BAD_PAGE = 4,    /* a page number outside the pool, among those that a
+                               length reaches; its keys and values counted as 0    */
+  NYS_ATTN_BAD_LENGTH = 8,  /* a length below 0 or past its table; taken clamped   */
+  NYS_PLAN_BAD_LENGTH = 16, /* negative lengths (taken as 0 fresh tokens), or
+                               lengths that do not sum to `total`                  */
+  NYS_PLAN_NO_PAGES = 32,   /* the free list was too short: the tokens left without
+                               a page have slot -1                                 */
+  NYS_PLAN_TABLE_FULL = 64  /* a token past the table's last column: slot -1       */
+};
+
+/* Bytes of device workspace that nys_attn_prompt (n sequences, `rows` query
+ * rows in all) and nys_attn_shared (n requests, rows = n) use on this geometry
+ * to split long key ranges over more CTAs.  Host arithmetic only.  0 is a
+ * possible answer.  Errors: NYS_E_INVAL, NYS_E_UNSUPPORTED. */
+int nys_attn_workspace_bytes(const nys_attn_config* cfg, int64_t n, int64_t rows, size_t* bytes);
+
+/* Causal attention over packed prompts.  Sequence i's queries are rows
+ * q_off[i] .. q_off[i+1]-1 of q, its keys and values rows k_off[i] ..
+ * k_off[i+1]-1 of k and v (k_off NULL: q_off).  With nq queries and nk keys,
+ * query r sees keys 0 .. r + nk - nq: the last query sees all keys, so a
+ * prompt may be taken in parts and a single new token is nq = 1.  A query that
+ * sees no key gets 0 (and lse -INF).  q_off and k_off are device arrays of
+ * n + 1 int32, ascending within [0, q_rows] and [0, k_rows]; rows that no
+ * sequence covers are not written.  out [q_rows][heads][dv] as given by its
+ * strides; lse, if not NULL, fp32 [q_rows][heads], receives the log of the
+ * softmax's denominator.  Values of keys that a row does not see never reach
+ * it, whatever they are.
+ * workspace: nys_attn_workspace_bytes(cfg, n, q_rows) bytes, 256-byte aligned
+ * (smaller or NULL is allowed and means no splitting).
+ * Errors: NYS_E_INVAL, NYS_E_UNSUPPORTED, NYS_E_ALIGN (workspace), NYS_E_CUDA. */
+int nys_attn_prompt(const nys_attn_config* cfg, int64_t n, int64_t q_rows, int64_t k_rows,
+                    const int32_t* q_off, const int32_t* k_off, const nys_rows* q,
+                    const nys_rows* k, const nys_rows* v, const nys_rows* out, float* lse,
+                    void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
+
+/* One token of attention for n requests that share a prefix.  Request b's
+ * query (row b of q) sees the prefix's prefix_len keys, in pages
+ * prefix_pages[0 ..], and then its own lens[b] keys, in pages
+ * table[b * width + 0 ..] of the same pool, the new token's among them.  The
+ * prefix's keys are read once for all requests together.  prefix_len 0 is a
+ * plain paged decode.  A request without keys gets 0 (lse -INF).  prefix_pages
+ * (int32), lens (int32 [n]) and table (int32 [n][width]) are device arrays;
+ * entries past a length are not read.  lse, if not NULL, fp32 [n][heads].
+ * workspace: nys_attn_workspace_bytes(cfg, n, n) bytes, 256-byte aligned;
+ * less is NYS_E_BUF.
+ * Errors: NYS_E_INVAL, NYS_E_UNSUPPORTED, NYS_E_BUF, NYS_E_ALIGN, NYS_E_CUDA. */
+int nys_attn_shared(const nys_attn_config* cfg, int64_t n, const nys_pool* pool,
+                    const int32_t* prefix_pages, int32_t prefix_len, const int32_t* lens,
+                    const int32_t* table, int32_t width, const nys_rows* q, const nys_rows* out,
+                    float* lse, void* workspace, size_t workspace_bytes, int32_t* status,
+                    void* stream);
+
+/* Block tables and slots from request lengths, in one launch.  Request i holds
+ * cached[i] tokens, whose pages are in its table, and gets fresh[i] more.  New
+ * pages come from free_pages[0 .. n_free-1] in order: request i's first new
+ * page is number (sum of the pages that requests before it need) of that list.
+ * Writes the new columns of table [n][width] (others are left alone), q_off
+ * int32 [n+1] (exclusive sums of fresh), lens int32 [n] (cached + fresh), and
+ * for each of the `total` new tokens in request order its slot (int64,
+ * page * page_size + offset; -1 without a page) and its position in the
+ * request (int32).  taken[0] is how many pages left the free list.  All
+ * pointers are device pointers.  Errors: NYS_E_INVAL, NYS_E_CUDA. */
+int nys_kv_plan(int64_t n, int32_t page, const int32_t* cached, const int32_t* fresh,
+                const int32_t* free_pages, int64_t n_free, int32_t* table, int32_t width,
+                int64_t total, int32_t* q_off, int32_t* lens, int64_t* slots,
+                int32_t* positions, int32_t* taken, int32_t* status, void* stream);
+
+/* Write `tokens` new rows k and v into the pool's slots (slot s is row s mod
+ * page of page s / page); tokens whose slot lies outside the pool (-1) are
+ * skipped.  Of two tokens with one slot either may stay.  Errors: NYS_E_INVAL,
+ * NYS_E_UNSUPPORTED, NYS_E_CUDA. */
+int nys_kv_write(const nys_attn_config* cfg, const nys_pool* pool, int64_t tokens,
+                 const nys_rows* k, const nys_rows* v, const int64_t* slots, void* stream);
+
 /* Static description of a status code.  Never NULL. */
 const char* nys_strerror(int status);
 

@@ -28,6 +28,16 @@ NYS_E_SCRATCH = -9
 NYS_E_CAPACITY = -10
 NYS_RECT_AGGREGATE = 0
 NYS_RECT_FM = 1
+NYS_F32 = 0
+NYS_BF16 = 1
+NYS_F16 = 2
+NYS_ATTN_GAVE_UP = 1
+NYS_ATTN_BAD_OFFSETS = 2
+NYS_ATTN_BAD_PAGE = 4
+NYS_ATTN_BAD_LENGTH = 8
+NYS_PLAN_BAD_LENGTH = 16
+NYS_PLAN_NO_PAGES = 32
+NYS_PLAN_TABLE_FULL = 64
 
 # Every entry point include/nys.h declares.
 EXPORTED = ("nys_memory_bytes", "nys_alloc_states", "nys_free_states",
@@ -36,7 +46,8 @@ EXPORTED = ("nys_memory_bytes", "nys_alloc_states", "nys_free_states",
             "nys_seal_static", "nys_seal_ragged", "nys_o1_begin", "nys_o1_push_q",
             "nys_o1_seal", "nys_o1_sealed", "nys_o1_step", "nys_o1_memory_bytes",
             "nys_o1_states", "nys_o1_free", "nys_debug_stall_once",
-            "nys_debug_stall_replay_once")
+            "nys_debug_stall_replay_once", "nys_attn_workspace_bytes",
+            "nys_attn_prompt", "nys_attn_shared", "nys_kv_plan", "nys_kv_write")
 
 
 class NysConfig(ctypes.Structure):
@@ -63,6 +74,22 @@ class NysGroupInfo(ctypes.Structure):
     _fields_ = [("mode", ctypes.c_int32), ("m_eff", ctypes.c_int32),
                 ("t", ctypes.c_int32), ("win_len", ctypes.c_int32),
                 ("win_head", ctypes.c_int32), ("status", ctypes.c_int32)]
+
+
+class NysAttnConfig(ctypes.Structure):
+    _fields_ = [("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("dv", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class NysRows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class NysPool(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int64), ("page", ctypes.c_int32)]
 
 
 def _load():
@@ -95,6 +122,13 @@ def _load():
         "nys_o1_free": [VP],
         "nys_debug_stall_once": [VP, I32],
         "nys_debug_stall_replay_once": [VP],
+        "nys_attn_workspace_bytes": [P(NysAttnConfig), I64, I64, P(ctypes.c_size_t)],
+        "nys_attn_prompt": [P(NysAttnConfig), I64, I64, I64, VP, VP, P(NysRows), P(NysRows),
+                            P(NysRows), P(NysRows), VP, VP, ctypes.c_size_t, VP, VP],
+        "nys_attn_shared": [P(NysAttnConfig), I64, P(NysPool), VP, I32, VP, VP, I32,
+                            P(NysRows), P(NysRows), VP, VP, ctypes.c_size_t, VP, VP],
+        "nys_kv_plan": [I64, I32, VP, VP, VP, I64, VP, I32, I64, VP, VP, VP, VP, VP, VP, VP],
+        "nys_kv_write": [P(NysAttnConfig), P(NysPool), I64, P(NysRows), P(NysRows), VP, VP],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -206,6 +240,40 @@ def nys_config_of(handle):
     _check(_lib.nys_config_of(handle, ctypes.byref(cfg), ctypes.byref(n)),
            "nys_config_of")
     return cfg, n.value
+
+
+def nys_attn_workspace_bytes(cfg: NysAttnConfig, n: int, rows: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(_lib.nys_attn_workspace_bytes(ctypes.byref(cfg), n, rows, ctypes.byref(out)),
+           "nys_attn_workspace_bytes")
+    return out.value
+
+
+def nys_attn_prompt(cfg, n, q_rows, k_rows, q_off, k_off, q, k, v, out, lse=None,
+                    workspace=None, workspace_bytes=0, status=None, stream=0):
+    """q, k, v, out: NysRows; the offsets and the rest: device addresses."""
+    _check(_lib.nys_attn_prompt(cfg, n, q_rows, k_rows, q_off, k_off, q, k, v, out, lse,
+                                workspace, workspace_bytes, status, stream or None),
+           "nys_attn_prompt")
+
+
+def nys_attn_shared(cfg, n, pool, prefix_pages, prefix_len, lens, table, width, q, out,
+                    lse=None, workspace=None, workspace_bytes=0, status=None, stream=0):
+    """q, out: NysRows; pool: NysPool; the rest: device addresses."""
+    _check(_lib.nys_attn_shared(cfg, n, pool, prefix_pages, prefix_len, lens, table, width,
+                                q, out, lse, workspace, workspace_bytes, status,
+                                stream or None), "nys_attn_shared")
+
+
+def nys_kv_plan(n, page, cached, fresh, free_pages, n_free, table, width, total, q_off,
+                lens, slots, positions, taken, status=None, stream=0):
+    _check(_lib.nys_kv_plan(n, page, cached, fresh, free_pages, n_free, table, width, total,
+                            q_off, lens, slots, positions, taken, status, stream or None),
+           "nys_kv_plan")
+
+
+def nys_kv_write(cfg, pool, tokens, k, v, slots, stream=0):
+    _check(_lib.nys_kv_write(cfg, pool, tokens, k, v, slots, stream or None), "nys_kv_write")
 
 
 # ---------------------------------------------------------------- torch wrapper
@@ -480,3 +548,201 @@ class O1Layer:
             self.close()
         except Exception:
             pass
+
+
+# ------------------------------------------------- exact attention, paged cache
+def _dtype_code(dtype):
+    import torch
+    codes = {torch.float32: NYS_F32, torch.bfloat16: NYS_BF16, torch.float16: NYS_F16}
+    if dtype not in codes:
+        raise ValueError(f"dtype {dtype}: need float32, bfloat16 or float16")
+    return codes[dtype]
+
+
+def _rows(t, dtype, heads, dim, where):
+    """A [rows][heads][dim] CUDA tensor as NysRows: any row and head strides,
+    the last dimension contiguous."""
+    if t.dtype != dtype or not t.is_cuda:
+        raise ValueError(f"{where}: need a CUDA {dtype} tensor")
+    shape, st = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{where}: shape {tuple(shape)} != (rows, {heads}, {dim})")
+    if st[2] != 1 and dim > 1:
+        raise ValueError(f"{where}: the last dimension must be contiguous")
+    return NysRows(t.data_ptr(), st[0], st[1])
+
+
+def _ints(t, dtype, shape, where):
+    """Address of a contiguous CUDA integer tensor of `shape` (None: any length)."""
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{where}: need a contiguous CUDA {dtype} tensor")
+    if len(t.shape) != len(shape) or any(w is not None and w != g
+                                         for w, g in zip(shape, t.shape)):
+        raise ValueError(f"{where}: shape {tuple(t.shape)} != {tuple(shape)}")
+    return t.data_ptr()
+
+
+class _Status:
+    """A device status word that kernels set bits of (NYS_ATTN_*, NYS_PLAN_*)."""
+
+    def _init_status(self, torch, device):
+        self._status = torch.zeros(1, dtype=torch.int32, device=device)
+        self._status_ptr = self._status.data_ptr()
+
+    def status(self):
+        """The status bits since the last clear (synchronises)."""
+        return int(self._status.item())
+
+    def clear_status(self):
+        self._status.zero_()
+
+
+class PagedKV:
+    """A pool of KV pages of one layer: k [n_pages][page][kv_heads][d],
+    v [..][dv], allocated here or given.  Page numbers come from a PagePlan."""
+
+    def __init__(self, n_pages, page, kv_heads, d, dv, dtype=None, device="cuda", k=None, v=None):
+        import torch
+        self.torch = torch
+        self.dtype = torch.float32 if dtype is None else dtype
+        self.device = torch.device(device)
+        self.n_pages, self.page = n_pages, page
+        self.kv_heads, self.d, self.dv = kv_heads, d, dv
+        make = lambda c: torch.empty((n_pages, page, kv_heads, c), dtype=self.dtype,
+                                     device=self.device)
+        self.k = make(d) if k is None else k
+        self.v = make(dv) if v is None else v
+        for name, t, c in (("k", self.k, d), ("v", self.v, dv)):
+            if (t.dtype != self.dtype or not t.is_cuda or not t.is_contiguous()
+                    or tuple(t.shape) != (n_pages, page, kv_heads, c)):
+                raise ValueError(f"{name}: need a contiguous CUDA {self.dtype} tensor of shape "
+                                 f"{(n_pages, page, kv_heads, c)}")
+        self._cfg = NysAttnConfig(kv_heads, kv_heads, d, dv, _dtype_code(self.dtype), 0.0)
+        self._pool = NysPool(self.k.data_ptr(), self.v.data_ptr(), n_pages, page)
+
+    def write(self, k, v, slots):
+        """Rows k [tokens][kv_heads][d], v [..][dv] into slots int64 [tokens];
+        a slot of -1 is skipped."""
+        torch = self.torch
+        n = k.shape[0]
+        if v.shape[0] != n:
+            raise ValueError(f"v: {v.shape[0]} rows, k has {n}")
+        nys_kv_write(self._cfg, self._pool, n, _rows(k, self.dtype, self.kv_heads, self.d, "k"),
+                     _rows(v, self.dtype, self.kv_heads, self.dv, "v"),
+                     _ints(slots, torch.int64, (n,), "slots"),
+                     torch.cuda.current_stream(self.device).cuda_stream)
+
+
+class PagePlan(_Status):
+    """Block tables, slots and positions of a batch's next tokens, built on
+    the GPU from its lengths (nys_kv_plan): up to n requests, `width` pages a
+    request, `total` new tokens, `page` tokens a page.  The outputs are
+    tensors of this object: q_off int32 [n+1], lens int32 [n], slots int64
+    [total], positions int32 [total], taken int32 [1]."""
+
+    def __init__(self, n, width, total, page, device="cuda"):
+        import torch
+        self.torch = torch
+        self.device = torch.device(device)
+        self.n, self.width, self.total, self.page = n, width, total, page
+        make = lambda size, dt: torch.empty(size, dtype=dt, device=self.device)
+        self.q_off = make(n + 1, torch.int32)
+        self.lens = make(n, torch.int32)
+        self.slots = make(total, torch.int64)
+        self.positions = make(total, torch.int32)
+        self.taken = make(1, torch.int32)
+        self._init_status(torch, self.device)
+        self._out = [t.data_ptr() for t in (self.q_off, self.lens, self.slots, self.positions,
+                                            self.taken)]
+
+    def update(self, cached, fresh, free_pages, table):
+        """cached, fresh int32 [n]; free_pages int32 [any]; table int32
+        [n][width], whose new columns are filled in place."""
+        i32 = self.torch.int32
+        nys_kv_plan(self.n, self.page, _ints(cached, i32, (self.n,), "cached"),
+                    _ints(fresh, i32, (self.n,), "fresh"),
+                    _ints(free_pages, i32, (None,), "free_pages"), free_pages.shape[0],
+                    _ints(table, i32, (self.n, self.width), "table"), self.width, self.total,
+                    *self._out, self._status_ptr,
+                    self.torch.cuda.current_stream(self.device).cuda_stream)
+        return self
+
+
+class ExactAttention(_Status):
+    """Exact grouped-query attention of one layer's geometry: packed causal
+    prompts (``prompt``) and one token over a shared prefix and paged own keys
+    (``shared``).  The workspace grows on demand and is kept, so calls on one
+    object must be ordered (one stream, or events)."""
+
+    def __init__(self, heads, kv_heads, d, dv, dtype=None, scale=None, device="cuda"):
+        import torch
+        self.torch = torch
+        self.dtype = torch.float32 if dtype is None else dtype
+        self.device = torch.device(device)
+        self.heads, self.kv_heads, self.d, self.dv = heads, kv_heads, d, dv
+        self.cfg = NysAttnConfig(heads, kv_heads, d, dv, _dtype_code(self.dtype),
+                                 0.0 if scale is None else scale)
+        self._init_status(torch, self.device)
+        self._sizes = {}
+        self._work = None
+        self._work_ptr = None
+        nys_attn_workspace_bytes(self.cfg, 0, 0)   # refuses a bad geometry here
+
+    def _workspace(self, n, rows):
+        """(address, bytes) of a workspace for n sequences of `rows` rows."""
+        need = self._sizes.get((n, rows))
+        if need is None:
+            need = self._sizes[(n, rows)] = nys_attn_workspace_bytes(self.cfg, n, rows)
+        if need > 0 and (self._work is None or self._work.numel() < need):
+            self._work = self.torch.empty(need, dtype=self.torch.uint8, device=self.device)
+            self._work_ptr = self._work.data_ptr()
+        return self._work_ptr, need
+
+    def prompt(self, q, k, v, q_off, out, k_off=None, lse=None):
+        """Packed causal attention (nys_attn_prompt): q [rows][heads][d], k and
+        v [keys][kv_heads][d|dv], q_off and k_off int32 [n+1]; writes out
+        [rows][heads][dv] and, if given, lse fp32 [rows][heads]."""
+        torch = self.torch
+        n, rows, keys = q_off.shape[0] - 1, q.shape[0], k.shape[0]
+        if v.shape[0] != keys or out.shape[0] != rows:
+            raise ValueError("k and v, and q and out, must have as many rows as each other")
+        ws, ws_bytes = self._workspace(n, rows)
+        nys_attn_prompt(
+            self.cfg, n, rows, keys, _ints(q_off, torch.int32, (None,), "q_off"),
+            None if k_off is None else _ints(k_off, torch.int32, (n + 1,), "k_off"),
+            _rows(q, self.dtype, self.heads, self.d, "q"),
+            _rows(k, self.dtype, self.kv_heads, self.d, "k"),
+            _rows(v, self.dtype, self.kv_heads, self.dv, "v"),
+            _rows(out, self.dtype, self.heads, self.dv, "out"),
+            None if lse is None else _ptr(lse, torch.float32, (rows, self.heads), "lse"),
+            ws, ws_bytes, self._status_ptr,
+            torch.cuda.current_stream(self.device).cuda_stream)
+        return out
+
+    def shared(self, q, cache, lens, table, out, prefix_pages=None, prefix_len=0, lse=None):
+        """One token for each of n requests (nys_attn_shared): q [n][heads][d]
+        over the prefix's keys and lens[b] own keys in cache's pages table[b]
+        (lens int32 [n], table int32 [n][width]); writes out [n][heads][dv]."""
+        torch = self.torch
+        n = q.shape[0]
+        if (cache.dtype != self.dtype or cache.kv_heads != self.kv_heads or cache.d != self.d
+                or cache.dv != self.dv):
+            raise ValueError("the cache's geometry is not this attention's")
+        if out.shape[0] != n or len(table.shape) != 2:
+            raise ValueError("out must have q's rows, and table be [n][width]")
+        pages = None
+        if prefix_len > 0:
+            pages = _ints(prefix_pages, torch.int32, (None,), "prefix_pages")
+            if prefix_pages.shape[0] * cache.page < prefix_len:
+                raise ValueError("prefix_pages: too few pages for prefix_len")
+        ws, ws_bytes = self._workspace(n, n)
+        nys_attn_shared(
+            self.cfg, n, cache._pool, pages, prefix_len,
+            _ints(lens, torch.int32, (n,), "lens"),
+            _ints(table, torch.int32, (n, None), "table"), table.shape[1],
+            _rows(q, self.dtype, self.heads, self.d, "q"),
+            _rows(out, self.dtype, self.heads, self.dv, "out"),
+            None if lse is None else _ptr(lse, torch.float32, (n, self.heads), "lse"),
+            ws, ws_bytes, self._status_ptr,
+            torch.cuda.current_stream(self.device).cuda_stream)
+        return out
