@@ -4,7 +4,7 @@
 #include <cmath>
 #include <cstdint>
 
-#include "nys_attn.h"
+#include "nys_attn_tc.h"
 #include "nys_kv.h"
 
 namespace {
@@ -102,7 +102,9 @@ int nys_attn_prompt(const nys_attn_config* cfg, int64_t n, int64_t q_rows, int64
   a.scale = scale_of(*cfg);
   a.status = status;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return nys::launch_prompt_general(a, s) == cudaSuccess ? NYS_OK : NYS_E_CUDA;
+  const cudaError_t e =
+      nys::prompt_tc_fits(a) ? nys::launch_prompt_tc(a, s) : nys::launch_prompt_general(a, s);
+  return e == cudaSuccess ? NYS_OK : NYS_E_CUDA;
 }
 
 int nys_attn_shared(const nys_attn_config* cfg, int64_t n, const nys_pool* pool,

@@ -1,0 +1,149 @@
+// Shared parts of the tiled attention kernels: their launch arguments and the
+// cutting of a batch into units of work.
+#pragma once
+
+#include "nys_attn.h"
+#include "nys_tc.h"
+
+namespace nys {
+
+constexpr int kTileM = 128;  // rows of a query tile: (position, head of the group) pairs
+constexpr int kTileN = 128;  // keys of a tile
+constexpr int kUnitRing = 4;
+
+// One batch of a tiled launch.  Causal prompts: q_off and k_off give the
+// sequences.  Prefix of a shared batch (q_off null): one sequence of n_rows
+// query positions, every one of which sees all n_keys keys.
+struct TileArgs {
+  const int32_t *q_off, *k_off;
+  int64_t q_rows, k_rows;  // extents of the tensors
+  int32_t n, causal;
+  int32_t heads, kv_heads, group, tp;  // tp: positions of a query tile, 128 / group
+  int32_t d, dv;
+  int32_t splits;  // pieces that each unit's keys are cut into
+  float scale;
+  Rows out;             // results, where splits == 0
+  float* lse;           // [q_rows][heads] or null
+  float *part, *part_lse;  // pieces' results [split][q_rows][heads][dv], [..]; splits > 0
+  // Keys in pages (prefix): their numbers, tokens a page, pages in the pool.
+  const int32_t* pages;
+  int32_t page, box;
+  int64_t n_pages;
+  // Values and keys for the checks of unusual values, and the pages' own rows.
+  const void *k_raw, *v_raw;
+  int64_t k_row, k_head, v_row, v_head;
+  int32_t kv_y;  // 0 where all KV heads share one head's rows (head stride 0)
+  int32_t* status;
+};
+
+// One unit: two query tiles of one KV head that read the same keys ("pair"),
+// or, where the second tile would be empty, one tile whose key tiles two
+// streams take in turn.
+struct Unit {
+  int32_t valid;
+  int32_t q_row;    // first query row
+  int32_t np0, np1; // positions in the tiles; np1 == 0: one tile
+  int32_t kvh;
+  int32_t k_row;    // the sequence's first key row
+  int32_t kb;       // first key of the piece
+  int32_t nt;       // key tiles of the piece
+  int32_t nt0;      // of them, those the first tile reads (pair)
+  int32_t lim;      // keys that position 0 sees (may be <= 0)
+  int32_t nkl;      // keys the piece ends before
+  int32_t split;
+  int32_t edge;     // first key tile in which some row does not see some key
+  int32_t patch;    // set where such a tile holds a value that is not finite
+  int32_t pad[2];
+};
+
+struct TileMaps {
+  CUtensorMap q, k, v;
+};
+
+// Whether the tiled kernels take a prompt batch (16-bit types), and its launch.
+bool prompt_tc_fits(const PromptArgs& a);
+cudaError_t launch_prompt_tc(const PromptArgs& a, cudaStream_t stream);
+cudaError_t launch_attn_tc(const TileArgs& a, const TileMaps& m, int dtype, unsigned grid,
+                           cudaStream_t stream);
+
+#ifdef __CUDACC__
+// Walks the launch's units in order; one warp.  Within a sequence the query
+// tiles come last position first, because under the causal mask those are the
+// longest; KV heads of one position lie next to each other.
+struct UnitWalk {
+  int64_t before = 0;  // units of the sequences before the window
+  int s0 = 0;          // the window's first sequence, 32 of them
+  int q0, nq, k0, nk, pairs;
+  int64_t count, upto;  // this lane's sequence's units, and the inclusive sum
+
+  __device__ __forceinline__ void load(const TileArgs& a, int lane) {
+    const int i = s0 + lane;
+    q0 = nq = k0 = nk = 0;
+    if (i < a.n) {
+      if (a.q_off) {
+        bool bad = false;
+        seq_range(a.q_off, i, a.q_rows, q0, nq, bad);
+        seq_range(a.k_off, i, a.k_rows, k0, nk, bad);
+        if (bad) attn_report(a.status, NYS_ATTN_BAD_OFFSETS);
+      } else {
+        nq = (int)a.q_rows;
+        nk = (int)a.k_rows;
+      }
+    }
+    pairs = (nq + 2 * a.tp - 1) / (2 * a.tp);
+    count = (int64_t)pairs * a.kv_heads * (a.splits ? a.splits : 1);
+    upto = count;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+  }
+
+  // Unit number w (ascending from call to call) into `u` in every lane;
+  // u.valid == 0 past the last.
+  __device__ __forceinline__ void get(const TileArgs& a, int64_t w, int lane, Unit& u) {
+    u.valid = 0;
+    u.patch = 0;
+    for (;;) {
+      const int64_t all = __shfl_sync(0xffffffffu, upto, 31);
+      if (w < before + all) break;
+      before += all;
+      s0 += 32;
+      if (s0 >= a.n) return;
+      load(a, lane);
+    }
+    const int src = __ffs(__ballot_sync(0xffffffffu, before + upto > w)) - 1;
+    const int sq0 = __shfl_sync(0xffffffffu, q0, src), snq = __shfl_sync(0xffffffffu, nq, src);
+    const int sk0 = __shfl_sync(0xffffffffu, k0, src), snk = __shfl_sync(0xffffffffu, nk, src);
+    const int spairs = __shfl_sync(0xffffffffu, pairs, src);
+    int64_t r = w - before - __shfl_sync(0xffffffffu, upto - count, src);
+    const int ns = a.splits ? a.splits : 1;
+    u.split = (int)(r % ns);
+    r /= ns;
+    u.kvh = (int)(r % a.kv_heads);
+    const int pair = spairs - 1 - (int)(r / a.kv_heads);
+    const int p0 = pair * 2 * a.tp;
+    const int left = snq - p0;
+    u.np0 = min(left, a.tp);
+    u.np1 = min(max(left - a.tp, 0), a.tp);
+    u.q_row = sq0 + p0;
+    u.k_row = sk0;
+    // Keys that the first position sees, and the last of each tile.
+    u.lim = a.causal ? p0 + 1 + snk - snq : snk;
+    const int e0 = a.causal ? u.lim + u.np0 - 1 : snk;
+    const int e1 = a.causal ? e0 + u.np1 : snk;
+    const int t0 = (min(max(e0, 0), snk) + kTileN - 1) / kTileN;
+    const int t1 = (min(max(e1, 0), snk) + kTileN - 1) / kTileN;  // t1 >= t0
+    const int tb = (int)((int64_t)t1 * u.split / ns), te = (int)((int64_t)t1 * (u.split + 1) / ns);
+    u.kb = tb * kTileN;
+    u.nt = te - tb;
+    u.nt0 = min(max(t0 - tb, 0), u.nt);
+    u.nkl = min(snk, te * kTileN);
+    u.edge = max(min(u.lim, u.nkl) - u.kb, 0) / kTileN;
+    u.valid = 1;
+  }
+};
+#endif
+
+}  // namespace nys
