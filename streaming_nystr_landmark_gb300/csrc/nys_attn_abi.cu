@@ -59,7 +59,7 @@ int nys_attn_workspace_bytes(const nys_attn_config* cfg, int64_t n, int64_t rows
   const int rc = check_attn(cfg);
   if (rc) return rc;
   if (!bytes || n < 0 || rows < 0 || n > INT32_MAX || rows > INT32_MAX) return NYS_E_INVAL;
-  *bytes = 0;
+  *bytes = nys::attn_workspace(*cfg, n, rows);
   return NYS_OK;
 }
 
@@ -150,7 +150,9 @@ int nys_attn_shared(const nys_attn_config* cfg, int64_t n, const nys_pool* pool,
   a.scale = scale_of(*cfg);
   a.status = status;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return nys::launch_shared_general(a, s) == cudaSuccess ? NYS_OK : NYS_E_CUDA;
+  const cudaError_t e = nys::shared_tiled_fits(a) ? nys::launch_shared_tiled(a, workspace, s)
+                                                  : nys::launch_shared_general(a, s);
+  return e == cudaSuccess ? NYS_OK : NYS_E_CUDA;
 }
 
 int nys_kv_plan(int64_t n, int32_t page, const int32_t* cached, const int32_t* fresh,

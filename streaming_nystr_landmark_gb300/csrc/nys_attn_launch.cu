@@ -58,8 +58,120 @@ bool tileable(const Rows& r, int64_t rows, int heads, int elem, bool bcast) {
 }
 
 constexpr int kSms = 152;
+constexpr int kMostPieces = 64;
+
+int64_t div_up(int64_t x, int64_t y) { return (x + y - 1) / y; }
+int clamp_int(int64_t x, int lo, int hi) { return (int)(x < lo ? lo : (x > hi ? hi : x)); }
+
+// Units of the prefix launch before its keys are cut.
+int64_t prefix_units(int64_t n, int kv_heads, int group) {
+  return div_up(n, 2 * (kTileM / group)) * kv_heads;
+}
+// Pieces at most: enough for four rounds of CTAs.  Bounds the workspace, so it
+// depends on the batch alone.
+int most_prefix_pieces(int64_t n, int kv_heads, int group) {
+  return clamp_int(div_up(4 * kSms, prefix_units(n, kv_heads, group)), 1, kMostPieces);
+}
+int most_own_pieces(int64_t n, int kv_heads) {
+  return clamp_int(div_up(4 * kSms, n * kv_heads), 1, kMostPieces);
+}
+
+// How many pieces to cut `tiles` key tiles of `units` units into: the least of
+// rounds of CTAs x (tiles of a piece + what a unit costs besides, about three
+// tiles' time), with a little for writing and joining each piece.
+int pick_pieces(int64_t units, int64_t tiles, int most) {
+  int best = 1;
+  double cost = 1e300;
+  for (int p = 1; p <= most && p <= tiles; ++p) {
+    const double c = (double)div_up(units * p, kSms) * (double)(div_up(tiles, p) + 3) + 0.5 * p;
+    if (c < cost) {
+      cost = c;
+      best = p;
+    }
+  }
+  return best;
+}
+
+int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
 }  // namespace
+
+size_t attn_workspace(const nys_attn_config& c, int64_t n, int64_t rows) {
+  (void)rows;
+  if (n == 0 || c.d > 128 || c.dv > 128) return 0;
+  const int group = c.heads / c.kv_heads;
+  const int64_t pieces =
+      most_prefix_pieces(n, c.kv_heads, group) + most_own_pieces(n, c.kv_heads);
+  const size_t row = (size_t)n * c.heads;
+  return (size_t)pieces * row * ((size_t)c.dv + 1) * 4 + 256;
+}
+
+bool shared_tiled_fits(const SharedArgs& a) {
+  const int elem = a.dtype == NYS_F32 ? 4 : 2, unit = 16 / elem;
+  if (a.d > 128 || a.dv > 128 || a.d % unit || a.dv % unit || a.n_pages == 0) return false;
+  if (reinterpret_cast<uintptr_t>(a.k) % 16 || reinterpret_cast<uintptr_t>(a.v) % 16) return false;
+  if (a.n_pages * a.page > (1 << 30)) return false;
+  if (!tileable(a.q, a.n, a.heads, elem, false)) return false;
+  if (a.prefix_len > 0 && (a.page % 8 || a.dtype == NYS_F32)) return false;
+  return true;
+}
+
+cudaError_t launch_shared_tiled(const SharedArgs& s, void* workspace, cudaStream_t stream) {
+  const int64_t row = (int64_t)s.n * s.heads;
+  OwnArgs o{};
+  const int64_t units = prefix_units(s.n, s.kv_heads, s.group);
+  const int64_t tiles = div_up(s.prefix_len, kTileN);
+  if (s.prefix_len > 0)
+    o.prefix_pieces = pick_pieces(units, tiles, most_prefix_pieces(s.n, s.kv_heads, s.group));
+  const int64_t cap = (int64_t)s.width * s.page;
+  o.pieces = clamp_int(div_up(cap, 256), 1, most_own_pieces(s.n, s.kv_heads));
+  const int64_t pieces = o.prefix_pieces + (o.pieces > 1 ? o.pieces : 0);
+  o.part = static_cast<float*>(workspace);
+  o.part_lse = o.part + pieces * row * s.dv;
+  if (o.prefix_pieces > 0) {
+    TileArgs a{};
+    a.q_rows = s.n;
+    a.k_rows = s.prefix_len;
+    a.n = 1;
+    a.heads = s.heads;
+    a.kv_heads = s.kv_heads;
+    a.group = s.group;
+    a.tp = kTileM / s.group;
+    a.d = s.d;
+    a.dv = s.dv;
+    a.splits = o.prefix_pieces;
+    a.scale = s.scale;
+    a.part = o.part;
+    a.part_lse = o.part_lse;
+    a.pages = s.prefix_pages;
+    a.page = s.page;
+    a.box = gcd(s.page, kTileN);
+    a.n_pages = s.n_pages;
+    a.k_raw = s.k;
+    a.v_raw = s.v;
+    a.k_row = (int64_t)s.kv_heads * s.d;
+    a.k_head = s.d;
+    a.v_row = (int64_t)s.kv_heads * s.dv;
+    a.v_head = s.dv;
+    a.kv_y = 1;
+    a.status = s.status;
+    const bool bf16 = s.dtype == NYS_BF16;
+    const int64_t slots = s.n_pages * s.page;
+    TileMaps m;
+    if (!make_map(&m.q, bf16, s.q.p, s.n, s.heads, s.d, s.q.row, s.q.head, s.group, a.tp) ||
+        !make_map(&m.k, bf16, s.k, slots, s.kv_heads, s.d, a.k_row, a.k_head, 1, a.box) ||
+        !make_map(&m.v, bf16, s.v, slots, s.kv_heads, s.dv, a.v_row, a.v_head, 1, a.box))
+      return cudaErrorInvalidValue;
+    const int64_t all = units * o.prefix_pieces;
+    const cudaError_t e =
+        launch_attn_tc(a, m, s.dtype, (unsigned)(all < kSms ? all : kSms), stream);
+    if (e != cudaSuccess) return e;
+  }
+  const cudaError_t e = launch_own(s, o, stream);
+  if (e != cudaSuccess || o.pieces == 1) return e;
+  JoinArgs j{o.part, o.part_lse, (int32_t)pieces, s.heads, s.dv, s.n, s.out, s.lse};
+  return launch_join(j, s.dtype, stream);
+}
 
 bool prompt_tc_fits(const PromptArgs& a) {
   if (a.dtype == NYS_F32 || a.d > 128 || a.dv > 128 || a.d % 8 || a.dv % 8) return false;

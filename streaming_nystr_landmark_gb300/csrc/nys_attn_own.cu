@@ -1,0 +1,603 @@
+// Single-token attention over a request's own pages, and the joining of
+// partial results (flash form, nys_attn_general.cu):
+//
+//   for pieces x with maxima m_x, sums l_x and O_x = sum_j 2^{s_j - m_x} v_j:
+//   out = sum_x 2^{m_x - m} O_x / sum_x 2^{m_x - m} l_x,  m = max_x m_x.
+//
+// Bound by HBM: a request's keys and values are read once for all heads of
+// the group, and there is little arithmetic a byte.  A CTA of four warps
+// takes one (request, KV head, piece of its keys); each warp streams tiles of
+// its own through a private ring in shared memory with cp.async, no barrier
+// between warps until their results are joined, so that two CTAs a SM keep
+// ~130 KB of reads in flight.  Keys past the length and pages outside the pool
+// are filled with zeros and never read from memory.
+//
+// bf16 / fp16: tiles of 16 keys, mma.sync m16n8k16 with the group's heads as
+// the (padded) 16 rows -- the product is far too small for the 128-row
+// tensor-memory form and memory sets the time.  f32: tiles of 8 keys, lane =
+// four columns, exact f32 FMAs; the dot products of 8 keys x the heads finish in one
+// interleaved butterfly.
+#include <cmath>
+
+#include "nys_attn_tc.h"
+
+namespace nys {
+namespace {
+
+using namespace tc;
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLazy = 8.f;
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool fill) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(fill ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The piece of request b's keys that this CTA reads: [lo, hi).
+__device__ __forceinline__ void own_range(const SharedArgs& a, const OwnArgs& o, int b, int piece,
+                                          int& lo, int& hi) {
+  int64_t len = a.lens[b];
+  const int64_t cap = (int64_t)a.width * a.page;
+  if (len < 0 || len > cap) {
+    attn_report(a.status, NYS_ATTN_BAD_LENGTH);
+    len = len < 0 ? 0 : cap;
+  }
+  // Whole 64-key steps, so that the four warps share a piece evenly.
+  const int64_t steps = (len + 63) / 64;
+  lo = (int)(steps * piece / o.pieces * 64);
+  const int64_t h = steps * (piece + 1) / o.pieces * 64;
+  hi = (int)(h < len ? h : len);
+}
+
+// Row number (times KV heads) of key j of request b in the pool, -1 where its
+// page is not in it.
+__device__ __forceinline__ int64_t own_row(const SharedArgs& a, const int32_t* pages, int j) {
+  const int pi = j / a.page;
+  const int32_t pg = pages[pi];
+  if (pg < 0 || pg >= a.n_pages) {
+    attn_report(a.status, NYS_ATTN_BAD_PAGE);
+    return -1;
+  }
+  return (int64_t)pg * a.page + (j - pi * a.page);
+}
+
+template <typename T>
+__device__ __forceinline__ T narrow(float x);
+template <>
+__device__ __forceinline__ float narrow<float>(float x) {
+  return x;
+}
+template <>
+__device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float x) {
+  return __float2bfloat16_rn(x);
+}
+template <>
+__device__ __forceinline__ __half narrow<__half>(float x) {
+  return __float2half_rn(x);
+}
+
+// Joins the warps' results (log2 maxima m and sums l [warp][head], O
+// [warp][head][dv]) and, where this CTA has all of the request's own keys, the
+// prefix's pieces; thread = column.  heads: of this CTA, from h0.
+template <typename T, int HB>
+__device__ void join(const SharedArgs& a, const OwnArgs& o, const float* m, const float* l,
+                     const float* acc, int b, int h0, int heads, int piece) {
+  for (int h = threadIdx.x >> 5; h < heads; h += kWarps) {
+    const int lane = threadIdx.x & 31;
+    const int64_t row = (int64_t)b * a.heads + h0 + h;
+    const int64_t rows = (int64_t)a.n * a.heads;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, m[w * HB + h]);
+    // The prefix's pieces: lane = piece, log2 of their sums.
+    const int np = o.pieces == 1 ? o.prefix_pieces : 0;
+    float pl[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (lane + 32 * i < np) pl[i] = o.part_lse[(lane + 32 * i) * rows + row] * kLog2e;
+    float pt = fmaxf(pl[0], pl[1]);
+#pragma unroll
+    for (int s = 16; s; s >>= 1) pt = fmaxf(pt, __shfl_xor_sync(0xffffffffu, pt, s));
+    top = fmaxf(top, pt);
+    const float ref = top == -INFINITY ? 0.f : top;
+    float wf[kWarps], total = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      wf[w] = ex2(m[w * HB + h] - ref);
+      total = fmaf(l[w * HB + h], wf[w], total);
+    }
+    // (A piece's NaN must not vanish in the maximum: its factor is NaN.)
+    float pf[2] = {0.f, 0.f}, ps;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (lane + 32 * i < np) pf[i] = ex2(pl[i] - ref);
+    ps = pf[0] + pf[1];
+#pragma unroll
+    for (int s = 16; s; s >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, s);
+    total += ps;
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+    float y[4] = {0.f, 0.f, 0.f, 0.f};  // columns lane * 4 ..
+    const bool col = lane * 4 < a.dv;
+    if (col) {
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float4 x = *reinterpret_cast<const float4*>(acc + (w * HB + h) * a.dv + lane * 4);
+        y[0] = fmaf(x.x, wf[w], y[0]);
+        y[1] = fmaf(x.y, wf[w], y[1]);
+        y[2] = fmaf(x.z, wf[w], y[2]);
+        y[3] = fmaf(x.w, wf[w], y[3]);
+      }
+    }
+    for (int p = 0; p < np; ++p) {
+      const float f = __shfl_sync(0xffffffffu, p < 32 ? pf[0] : pf[1], p & 31);
+      if (col && f != 0.f) {
+        const float4 x = *reinterpret_cast<const float4*>(o.part + (p * rows + row) * a.dv + lane * 4);
+        y[0] = fmaf(x.x, f, y[0]);
+        y[1] = fmaf(x.y, f, y[1]);
+        y[2] = fmaf(x.z, f, y[2]);
+        y[3] = fmaf(x.w, f, y[3]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] *= inv;
+    const float lse = total == 0.f ? -INFINITY : fmaf(top, 0.6931471805599453f, logf(total));
+    if (o.pieces == 1) {
+      if (col) {
+        T* out = (T*)a.out.p + b * a.out.row + (h0 + h) * a.out.head + lane * 4;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) out[i] = narrow<T>(y[i]);
+      }
+      if (lane == 0 && a.lse) a.lse[row] = lse;
+    } else {
+      const int64_t at = (int64_t)(o.prefix_pieces + piece) * rows + row;
+      if (col) *reinterpret_cast<float4*>(o.part + at * a.dv + lane * 4) = make_float4(y[0], y[1], y[2], y[3]);
+      if (lane == 0) o.part_lse[at] = lse;
+    }
+  }
+}
+
+// ------------------------------------------------------------ bf16 and fp16
+constexpr int kHeads16 = 16;      // MMA rows: heads of a CTA
+constexpr int kKeys16 = 16;       // keys of a warp's tile
+constexpr int kStages16 = 3;
+constexpr int kRow16 = 272;       // bytes of a row in shared memory: 256 + 16, conflict-free
+constexpr int kStage16 = 2 * kKeys16 * kRow16;
+constexpr int kSmem16 = kWarps * kStages16 * kStage16;
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                      uint32_t b1) {
+  if (Type16<T>::kBf16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Grid: x = pieces, y = KV heads x blocks of 16 heads, z-major requests in x.
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2) own16_kernel(SharedArgs a, OwnArgs o) {
+  extern __shared__ __align__(128) unsigned char sm[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int piece = blockIdx.x % o.pieces, b = blockIdx.x / o.pieces;
+  const int blocks = (a.group + kHeads16 - 1) / kHeads16;
+  const int kvh = blockIdx.y / blocks, hb = blockIdx.y - kvh * blocks;
+  const int h0 = kvh * a.group + hb * kHeads16;
+  const int heads = min(kHeads16, a.group - hb * kHeads16);
+  int lo, hi;
+  own_range(a, o, b, piece, lo, hi);
+  const int32_t* pages = a.table + (int64_t)b * a.width;
+  const int dc = a.d >> 3, vc = a.dv >> 3;  // 16-byte chunks of a row
+  const int ks = (a.d + 15) >> 4, ns = (a.dv + 15) >> 4;
+  unsigned char* ring = sm + warp * kStages16 * kStage16;
+  // Columns that pad a dim to 16 hold zeros.
+  if ((a.d | a.dv) & 15) {
+    for (int i = tid * 16; i < kSmem16; i += kThreads * 16)
+      *reinterpret_cast<uint4*>(sm + i) = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+  }
+  // Tile t of this warp: keys lo + (t * kWarps + warp) * 16 ...
+  const int tiles = (hi - lo + kKeys16 - 1) / kKeys16;
+  const int mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
+  auto fetch = [&](int t) {
+    if (t < mine) {
+      unsigned char* st = ring + (t % kStages16) * kStage16;
+      const int j0 = lo + (t * kWarps + warp) * kKeys16;
+      // Lane l < 16 looks key l up; two lanes' worth of chunks a row follow.
+      int64_t row = -1;
+      if (lane < kKeys16 && j0 + lane < hi) row = own_row(a, pages, j0 + lane);
+      const int r0 = lane >> 4, c = lane & 15;
+#pragma unroll
+      for (int i = 0; i < kKeys16; i += 2) {
+        const int64_t at = __shfl_sync(0xffffffffu, row, i + r0) * a.kv_heads + kvh;
+        const bool have = at >= 0;
+        const uint32_t d0 = sptr(st + (i + r0) * kRow16 + c * 16);
+        if (c < dc) cp16(d0, (const T*)a.k + (have ? at : 0) * a.d + c * 8, have);
+        if (c < vc)
+          cp16(d0 + kKeys16 * kRow16, (const T*)a.v + (have ? at : 0) * a.dv + c * 8, have);
+      }
+    }
+    cp_commit();
+  };
+#pragma unroll
+  for (int t = 0; t < kStages16 - 1; ++t) fetch(t);
+
+  // The queries, as A fragments: rows lane / 4 and + 8, zero past the heads.
+  uint32_t q[8][4];
+  {
+    const int r = lane >> 2, c = (lane & 3) * 2;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int hh = r + (x & 1) * 8, cc = k * 16 + c + (x >> 1) * 8;
+        q[k][x] = 0;
+        if (hh < heads && cc < a.d)
+          q[k][x] = *reinterpret_cast<const uint32_t*>((const T*)a.q.p + b * a.q.row +
+                                                       (h0 + hh) * a.q.head + cc);
+      }
+  }
+  const float sc = a.scale * kLog2e;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float acc[16][4];
+#pragma unroll
+  for (int n = 0; n < 16; ++n)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) acc[n][x] = 0.f;
+
+  for (int t = 0; t < mine; ++t) {
+    cp_wait<kStages16 - 2>();
+    __syncwarp();
+    fetch(t + kStages16 - 1);
+    const uint32_t kb = sptr(ring + (t % kStages16) * kStage16), vb = kb + kKeys16 * kRow16;
+    float s[2][4] = {};
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < ks) {
+        uint32_t r[4];
+        ldsm4(r, kb + ((lane & 7) + (lane >> 4) * 8) * kRow16 + k * 32 + ((lane >> 3) & 1) * 16);
+        mma16<T>(s[0], q[k], r[0], r[1]);
+        mma16<T>(s[1], q[k], r[2], r[3]);
+      }
+    const int left = hi - (lo + (t * kWarps + warp) * kKeys16);  // keys of this tile
+    uint32_t p[4];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {  // rows lane / 4 and lane / 4 + 8
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (n * 8 + (lane & 3) * 2 + e >= left) s[n][x * 2 + e] = -INFINITY;
+      float top = fmaxf(fmaxf(s[0][x * 2], s[0][x * 2 + 1]), fmaxf(s[1][x * 2], s[1][x * 2 + 1]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2)) * sc;
+      const bool grow = m[x] == -INFINITY ? top > m[x] : top - m[x] > kLazy;
+      if (__any_sync(0xffffffffu, grow)) {
+        const float nm = fmaxf(m[x], top);
+        const float f = nm == m[x] ? 1.f : ex2(m[x] - nm);
+        m[x] = nm;
+        l[x] *= f;
+#pragma unroll
+        for (int n = 0; n < 16; ++n) {
+          acc[n][x * 2] *= f;
+          acc[n][x * 2 + 1] *= f;
+        }
+      }
+      const float ref = m[x] == -INFINITY ? 0.f : m[x];
+      float w[4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          w[n * 2 + e] = ex2(fmaf(s[n][x * 2 + e], sc, -ref));
+          l[x] += w[n * 2 + e];
+        }
+      p[x] = Type16<T>::pack(w[0], w[1]);
+      p[2 + x] = Type16<T>::pack(w[2], w[3]);
+    }
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+      if (n < ns) {
+        uint32_t r[4];
+        ldsm4t(r, vb + ((lane & 7) + ((lane >> 3) & 1) * 8) * kRow16 + n * 32 + (lane >> 4) * 16);
+        mma16<T>(acc[2 * n], p, r[0], r[1]);
+        mma16<T>(acc[2 * n + 1], p, r[2], r[3]);
+      }
+  }
+  cp_wait<0>();
+  __syncthreads();  // the ring becomes the warps' results
+  float* jm = reinterpret_cast<float*>(sm);
+  float* jl = jm + kWarps * kHeads16;
+  float* ja = jl + kWarps * kHeads16;
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
+    l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+    const int h = (lane >> 2) + x * 8;
+    if (h < heads) {
+      if ((lane & 3) == 0) {
+        jm[warp * kHeads16 + h] = m[x];
+        jl[warp * kHeads16 + h] = l[x];
+      }
+#pragma unroll
+      for (int n = 0; n < 16; ++n) {
+        const int c = n * 8 + (lane & 3) * 2;
+        if (c < a.dv)
+          *reinterpret_cast<float2*>(ja + (warp * kHeads16 + h) * a.dv + c) =
+              make_float2(acc[n][x * 2], acc[n][x * 2 + 1]);
+      }
+    }
+  }
+  __syncthreads();
+  join<T, kHeads16>(a, o, jm, jl, ja, b, h0, heads, piece);
+}
+
+// --------------------------------------------------------------------- f32
+constexpr int kKeys32 = 8;
+constexpr int kStages32 = 3;
+constexpr int kStage32 = 2 * kKeys32 * 512;
+constexpr int kSmem32 = kWarps * kStages32 * kStage32;
+
+// Sums each of V per-lane partials over the warp; lane gets the total of value
+// value_of<V>(lane).
+template <int V>
+__device__ __forceinline__ float sum_multi(float (&x)[V], int lane) {
+  constexpr int kSteps = V >= 32 ? 5 : V >= 16 ? 4 : V >= 8 ? 3 : 2;
+#pragma unroll
+  for (int st = 0; st < kSteps; ++st) {
+    const int half = V >> (st + 1), off = 16 >> st;
+    const bool up = lane & off;
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const float send = up ? x[i] : x[i + half];
+      const float keep = up ? x[i + half] : x[i];
+      x[i] = keep + __shfl_xor_sync(0xffffffffu, send, off);
+    }
+  }
+  float r = x[0];
+#pragma unroll
+  for (int off = 16 >> kSteps; off; off >>= 1) r += __shfl_xor_sync(0xffffffffu, r, off);
+  return r;
+}
+
+// HT heads at a time.  A value is (head, key) = head * KB + key: its lanes
+// are the top bits of the lane number, so a head's keys are neighbours.
+template <int HT>
+__global__ void __launch_bounds__(kThreads, 2) own32_kernel(SharedArgs a, OwnArgs o) {
+  extern __shared__ __align__(128) unsigned char sm[];
+  constexpr int KB = HT == 8 ? 4 : 8;  // keys of one butterfly
+  constexpr int V = HT * KB;
+  constexpr int kRep = 32 / V;         // lanes that hold one value
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int piece = blockIdx.x % o.pieces, b = blockIdx.x / o.pieces;
+  const int blocks = (a.group + HT - 1) / HT;
+  const int kvh = blockIdx.y / blocks, hb = blockIdx.y - kvh * blocks;
+  const int h0 = kvh * a.group + hb * HT;
+  const int heads = min(HT, a.group - hb * HT);
+  int lo, hi;
+  own_range(a, o, b, piece, lo, hi);
+  const int32_t* pages = a.table + (int64_t)b * a.width;
+  const bool kcol = lane * 4 < a.d, vcol = lane * 4 < a.dv;
+  unsigned char* ring = sm + warp * kStages32 * kStage32 + lane * 16;  // this lane's columns
+  const int tiles = (hi - lo + kKeys32 - 1) / kKeys32;
+  const int mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
+  auto fetch = [&](int t) {
+    if (t < mine) {
+      unsigned char* st = ring + (t % kStages32) * kStage32;
+      const int j0 = lo + (t * kWarps + warp) * kKeys32;
+      int64_t row = -1;
+      if (lane < kKeys32 && j0 + lane < hi) row = own_row(a, pages, j0 + lane);
+#pragma unroll
+      for (int i = 0; i < kKeys32; ++i) {
+        const int64_t at = __shfl_sync(0xffffffffu, row, i) * a.kv_heads + kvh;
+        const bool have = at >= 0;
+        if (kcol)
+          cp16(sptr(st + i * 512), (const float*)a.k + (have ? at : 0) * a.d + lane * 4, have);
+        if (vcol)
+          cp16(sptr(st + (kKeys32 + i) * 512), (const float*)a.v + (have ? at : 0) * a.dv + lane * 4,
+               have);
+      }
+    }
+    cp_commit();
+  };
+#pragma unroll
+  for (int t = 0; t < kStages32 - 1; ++t) fetch(t);
+
+  const float sc = a.scale * kLog2e;
+  float4 q[HT], acc[HT];
+#pragma unroll
+  for (int h = 0; h < HT; ++h) {
+    q[h] = acc[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (h < heads && kcol) {
+      const float* p = (const float*)a.q.p + b * a.q.row + (h0 + h) * a.q.head + lane * 4;
+      q[h] = make_float4(p[0] * sc, p[1] * sc, p[2] * sc, p[3] * sc);
+    }
+  }
+  const int val = lane / kRep, key_of = val % KB;  // this lane's (head, key)
+  float m = -INFINITY, l = 0.f;                    // of this lane's head
+  for (int t = 0; t < mine; ++t) {
+    cp_wait<kStages32 - 2>();  // (each lane reads back what it copied itself)
+    fetch(t + kStages32 - 1);
+    const unsigned char* st = ring + (t % kStages32) * kStage32;
+#pragma unroll
+    for (int g = 0; g < kKeys32; g += KB) {
+      const int left = hi - (lo + (t * kWarps + warp) * kKeys32) - g;
+      float x[V];
+#pragma unroll
+      for (int i = 0; i < KB; ++i) {
+        const float4 k = kcol ? *reinterpret_cast<const float4*>(st + (g + i) * 512)
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int h = 0; h < HT; ++h)
+          x[h * KB + i] = fmaf(q[h].x, k.x, fmaf(q[h].y, k.y, fmaf(q[h].z, k.z, q[h].w * k.w)));
+      }
+      float s = sum_multi<V>(x, lane);
+      if (key_of >= left) s = -INFINITY;
+      float top = s;
+#pragma unroll
+      for (int off = kRep * KB / 2; off >= kRep; off >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+      const bool grow = m == -INFINITY ? top > m : top - m > kLazy;
+      if (__any_sync(0xffffffffu, grow)) {
+        const float nm = fmaxf(m, top);
+        const float f = nm == m ? 1.f : ex2(m - nm);
+        m = nm;
+        l *= f;
+#pragma unroll
+        for (int h = 0; h < HT; ++h) {
+          const float fh = __shfl_sync(0xffffffffu, f, h * KB * kRep);
+          acc[h].x *= fh;
+          acc[h].y *= fh;
+          acc[h].z *= fh;
+          acc[h].w *= fh;
+        }
+      }
+      const float p = ex2(s - (m == -INFINITY ? 0.f : m));
+      l += p;
+#pragma unroll
+      for (int i = 0; i < KB; ++i) {
+        const float4 v = vcol ? *reinterpret_cast<const float4*>(st + (kKeys32 + g + i) * 512)
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int h = 0; h < HT; ++h) {
+          const float w = __shfl_sync(0xffffffffu, p, (h * KB + i) * kRep);
+          acc[h].x = fmaf(w, v.x, acc[h].x);
+          acc[h].y = fmaf(w, v.y, acc[h].y);
+          acc[h].z = fmaf(w, v.z, acc[h].z);
+          acc[h].w = fmaf(w, v.w, acc[h].w);
+        }
+      }
+    }
+  }
+  // l: the sum over a head's keys (lanes kRep apart).
+#pragma unroll
+  for (int off = kRep * KB / 2; off >= kRep; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+  cp_wait<0>();
+  __syncthreads();
+  float* jm = reinterpret_cast<float*>(sm);
+  float* jl = jm + kWarps * HT;
+  float* ja = jl + kWarps * HT;
+#pragma unroll
+  for (int h = 0; h < HT; ++h) {
+    if (lane == h * KB * kRep) {
+      jm[warp * HT + h] = m;
+      jl[warp * HT + h] = l;
+    }
+    if (vcol) *reinterpret_cast<float4*>(ja + (warp * HT + h) * a.dv + lane * 4) = acc[h];
+  }
+  __syncthreads();
+  join<float, HT>(a, o, jm, jl, ja, b, h0, heads, piece);
+}
+
+// Joins `pieces` partial results of each row; one warp a row.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) join_kernel(JoinArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t rows = a.rows * a.heads;
+  for (int64_t r = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); r < rows;
+       r += (int64_t)gridDim.x * kWarps) {
+    float top = -INFINITY;
+    for (int p = lane; p < a.pieces; p += 32) top = fmaxf(top, a.part_lse[p * rows + r]);
+#pragma unroll
+    for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+    const float ref = top == -INFINITY ? 0.f : top;
+    float total = 0.f;
+    float y[4] = {0.f, 0.f, 0.f, 0.f};
+    const bool col = lane * 4 < a.dv;
+    for (int p = 0; p < a.pieces; ++p) {
+      const float f = ex2((a.part_lse[p * rows + r] - ref) * kLog2e);
+      total += f;
+      if (col && f != 0.f) {
+        const float4 x = *reinterpret_cast<const float4*>(a.part + (p * rows + r) * a.dv + lane * 4);
+        y[0] = fmaf(x.x, f, y[0]);
+        y[1] = fmaf(x.y, f, y[1]);
+        y[2] = fmaf(x.z, f, y[2]);
+        y[3] = fmaf(x.w, f, y[3]);
+      }
+    }
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+    const int64_t row = r / a.heads;
+    const int h = (int)(r - row * a.heads);
+    if (col) {
+      T* out = (T*)a.out.p + row * a.out.row + h * a.out.head + lane * 4;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) out[i] = narrow<T>(y[i] * inv);
+    }
+    if (lane == 0 && a.lse) a.lse[r] = total == 0.f ? -INFINITY : top + logf(total);
+  }
+}
+
+template <typename K>
+cudaError_t allow(K kernel, int bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <int HT>
+cudaError_t launch32(const SharedArgs& a, const OwnArgs& o, cudaStream_t stream) {
+  static const cudaError_t ready = allow(own32_kernel<HT>, kSmem32);
+  if (ready != cudaSuccess) return ready;
+  const dim3 grid((unsigned)(a.n * o.pieces), (unsigned)(a.kv_heads * ((a.group + HT - 1) / HT)));
+  own32_kernel<HT><<<grid, kThreads, kSmem32, stream>>>(a, o);
+  return cudaGetLastError();
+}
+template <typename T>
+cudaError_t launch16(const SharedArgs& a, const OwnArgs& o, cudaStream_t stream) {
+  static const cudaError_t ready = allow(own16_kernel<T>, kSmem16);
+  if (ready != cudaSuccess) return ready;
+  const dim3 grid((unsigned)(a.n * o.pieces),
+                  (unsigned)(a.kv_heads * ((a.group + kHeads16 - 1) / kHeads16)));
+  own16_kernel<T><<<grid, kThreads, kSmem16, stream>>>(a, o);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_own(const SharedArgs& a, const OwnArgs& o, cudaStream_t stream) {
+  if (a.dtype == NYS_BF16) return launch16<__nv_bfloat16>(a, o, stream);
+  if (a.dtype == NYS_F16) return launch16<__half>(a, o, stream);
+  return a.group == 1   ? launch32<1>(a, o, stream)
+         : a.group == 2 ? launch32<2>(a, o, stream)
+         : a.group <= 4 ? launch32<4>(a, o, stream)
+                        : launch32<8>(a, o, stream);
+}
+
+cudaError_t launch_join(const JoinArgs& a, int dtype, cudaStream_t stream) {
+  const int64_t warps = a.rows * a.heads;
+  if (warps == 0) return cudaSuccess;
+  const int64_t want = (warps + kWarps - 1) / kWarps;
+  const unsigned grid = (unsigned)(want < 152 * 16 ? want : 152 * 16);
+  if (dtype == NYS_F32) join_kernel<float><<<grid, kThreads, 0, stream>>>(a);
+  else if (dtype == NYS_BF16) join_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(a);
+  else join_kernel<__half><<<grid, kThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace nys

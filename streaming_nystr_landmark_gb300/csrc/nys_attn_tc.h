@@ -60,6 +60,28 @@ struct TileMaps {
   CUtensorMap q, k, v;
 };
 
+// A request's own keys: how many pieces they are cut into, how many the
+// prefix was, and the pieces' results (the prefix's first).
+struct OwnArgs {
+  int32_t pieces, prefix_pieces;
+  float *part, *part_lse;
+};
+
+struct JoinArgs {
+  const float *part, *part_lse;
+  int32_t pieces, heads, dv;
+  int64_t rows;
+  Rows out;
+  float* lse;
+};
+
+// Workspace of the tiled kernels for n requests or `rows` query rows.
+size_t attn_workspace(const nys_attn_config& c, int64_t n, int64_t rows);
+bool shared_tiled_fits(const SharedArgs& a);
+cudaError_t launch_shared_tiled(const SharedArgs& a, void* workspace, cudaStream_t stream);
+cudaError_t launch_own(const SharedArgs& a, const OwnArgs& o, cudaStream_t stream);
+cudaError_t launch_join(const JoinArgs& a, int dtype, cudaStream_t stream);
+
 // Whether the tiled kernels take a prompt batch (16-bit types), and its launch.
 bool prompt_tc_fits(const PromptArgs& a);
 cudaError_t launch_prompt_tc(const PromptArgs& a, cudaStream_t stream);
