@@ -64,13 +64,13 @@ int64_t div_up(int64_t x, int64_t y) { return (x + y - 1) / y; }
 int clamp_int(int64_t x, int lo, int hi) { return (int)(x < lo ? lo : (x > hi ? hi : x)); }
 
 // Units of the prefix launch before its keys are cut.
-int64_t prefix_units(int64_t n, int kv_heads, int group) {
-  return div_up(n, 2 * (kTileM / group)) * kv_heads;
+int64_t prefix_units(int64_t n, int kv_heads, int group, int dtype) {
+  return div_up(n, (dtype == NYS_F32 ? 1 : 2) * (kTileM / group)) * kv_heads;
 }
 // Pieces at most: enough for four rounds of CTAs.  Bounds the workspace, so it
 // depends on the batch alone.
-int most_prefix_pieces(int64_t n, int kv_heads, int group) {
-  return clamp_int(div_up(4 * kSms, prefix_units(n, kv_heads, group)), 1, kMostPieces);
+int most_prefix_pieces(int64_t n, int kv_heads, int group, int dtype) {
+  return clamp_int(div_up(4 * kSms, prefix_units(n, kv_heads, group, dtype)), 1, kMostPieces);
 }
 int most_own_pieces(int64_t n, int kv_heads) {
   return clamp_int(div_up(4 * kSms, n * kv_heads), 1, kMostPieces);
@@ -101,7 +101,7 @@ size_t attn_workspace(const nys_attn_config& c, int64_t n, int64_t rows) {
   if (n == 0 || c.d > 128 || c.dv > 128) return 0;
   const int group = c.heads / c.kv_heads;
   const int64_t pieces =
-      most_prefix_pieces(n, c.kv_heads, group) + most_own_pieces(n, c.kv_heads);
+      most_prefix_pieces(n, c.kv_heads, group, c.dtype) + most_own_pieces(n, c.kv_heads);
   const size_t row = (size_t)n * c.heads;
   return (size_t)pieces * row * ((size_t)c.dv + 1) * 4 + 256;
 }
@@ -112,17 +112,17 @@ bool shared_tiled_fits(const SharedArgs& a) {
   if (reinterpret_cast<uintptr_t>(a.k) % 16 || reinterpret_cast<uintptr_t>(a.v) % 16) return false;
   if (a.n_pages * a.page > (1 << 30)) return false;
   if (!tileable(a.q, a.n, a.heads, elem, false)) return false;
-  if (a.prefix_len > 0 && (a.page % 8 || a.dtype == NYS_F32)) return false;
+  if (a.prefix_len > 0 && a.dtype != NYS_F32 && a.page % 8) return false;
   return true;
 }
 
 cudaError_t launch_shared_tiled(const SharedArgs& s, void* workspace, cudaStream_t stream) {
   const int64_t row = (int64_t)s.n * s.heads;
   OwnArgs o{};
-  const int64_t units = prefix_units(s.n, s.kv_heads, s.group);
+  const int64_t units = prefix_units(s.n, s.kv_heads, s.group, s.dtype);
   const int64_t tiles = div_up(s.prefix_len, kTileN);
   if (s.prefix_len > 0)
-    o.prefix_pieces = pick_pieces(units, tiles, most_prefix_pieces(s.n, s.kv_heads, s.group));
+    o.prefix_pieces = pick_pieces(units, tiles, most_prefix_pieces(s.n, s.kv_heads, s.group, s.dtype));
   const int64_t cap = (int64_t)s.width * s.page;
   o.pieces = clamp_int(div_up(cap, 256), 1, most_own_pieces(s.n, s.kv_heads));
   const int64_t pieces = o.prefix_pieces + (o.pieces > 1 ? o.pieces : 0);
@@ -155,6 +155,14 @@ cudaError_t launch_shared_tiled(const SharedArgs& s, void* workspace, cudaStream
     a.v_head = s.dv;
     a.kv_y = 1;
     a.status = s.status;
+    a.q = s.q;
+    a.per = s.dtype == NYS_F32 ? 1 : 2;
+    const int64_t all = units * o.prefix_pieces;
+    const unsigned grid = (unsigned)(all < kSms ? all : kSms);
+    cudaError_t e;
+    if (s.dtype == NYS_F32) {
+      e = launch_attn_tc32(a, grid, stream);
+    } else {
     const bool bf16 = s.dtype == NYS_BF16;
     const int64_t slots = s.n_pages * s.page;
     TileMaps m;
@@ -162,9 +170,8 @@ cudaError_t launch_shared_tiled(const SharedArgs& s, void* workspace, cudaStream
         !make_map(&m.k, bf16, s.k, slots, s.kv_heads, s.d, a.k_row, a.k_head, 1, a.box) ||
         !make_map(&m.v, bf16, s.v, slots, s.kv_heads, s.dv, a.v_row, a.v_head, 1, a.box))
       return cudaErrorInvalidValue;
-    const int64_t all = units * o.prefix_pieces;
-    const cudaError_t e =
-        launch_attn_tc(a, m, s.dtype, (unsigned)(all < kSms ? all : kSms), stream);
+    e = launch_attn_tc(a, m, s.dtype, grid, stream);
+    }
     if (e != cudaSuccess) return e;
   }
   const cudaError_t e = launch_own(s, o, stream);
@@ -174,14 +181,15 @@ cudaError_t launch_shared_tiled(const SharedArgs& s, void* workspace, cudaStream
 }
 
 bool prompt_tc_fits(const PromptArgs& a) {
-  if (a.dtype == NYS_F32 || a.d > 128 || a.dv > 128 || a.d % 8 || a.dv % 8) return false;
+  const int elem = a.dtype == NYS_F32 ? 4 : 2, unit = 16 / elem;
+  if (a.d > 128 || a.dv > 128 || a.d % unit || a.dv % unit) return false;
   if (a.k_rows == 0 || a.k_rows > (1 << 30) || a.q_rows > (1 << 30)) return false;
   // K and V share the choice between a KV head's own rows and one head's rows.
   const bool kb = a.kv_heads > 1 && a.k.head == 0, vb = a.kv_heads > 1 && a.v.head == 0;
-  return kb == vb && tileable(a.q, a.q_rows, a.heads, 2, false) &&
-         tileable(a.k, a.k_rows, a.kv_heads, 2, true) &&
-         tileable(a.v, a.k_rows, a.kv_heads, 2, true) &&
-         tileable(a.out, a.q_rows, a.heads, 2, false);
+  return kb == vb && tileable(a.q, a.q_rows, a.heads, elem, false) &&
+         tileable(a.k, a.k_rows, a.kv_heads, elem, true) &&
+         tileable(a.v, a.k_rows, a.kv_heads, elem, true) &&
+         tileable(a.out, a.q_rows, a.heads, elem, false);
 }
 
 cudaError_t launch_prompt_tc(const PromptArgs& p, cudaStream_t stream) {
@@ -209,6 +217,12 @@ cudaError_t launch_prompt_tc(const PromptArgs& p, cudaStream_t stream) {
   a.v_head = p.v.head;
   a.kv_y = !(p.kv_heads > 1 && p.k.head == 0);
   a.status = p.status;
+  a.q = p.q;
+  a.per = p.dtype == NYS_F32 ? 1 : 2;
+  // At most this many units: a partial one a sequence on top of the full ones.
+  const int64_t most = (p.q_rows / (a.per * a.tp) + p.n) * p.kv_heads;
+  const unsigned grid = (unsigned)(most < kSms ? most : kSms);
+  if (p.dtype == NYS_F32) return launch_attn_tc32(a, grid, stream);
   TileMaps m;
   const bool bf16 = p.dtype == NYS_BF16;
   const int64_t kvh = a.kv_y ? p.kv_heads : 1;
@@ -216,9 +230,7 @@ cudaError_t launch_prompt_tc(const PromptArgs& p, cudaStream_t stream) {
       !make_map(&m.k, bf16, p.k.p, p.k_rows, kvh, p.d, p.k.row, p.k.head, 1, kTileN) ||
       !make_map(&m.v, bf16, p.v.p, p.k_rows, kvh, p.dv, p.v.row, p.v.head, 1, kTileN))
     return cudaErrorInvalidValue;
-  // At most this many units: a partial pair a sequence on top of the full ones.
-  const int64_t most = (p.q_rows / (2 * a.tp) + p.n) * p.kv_heads;
-  return launch_attn_tc(a, m, p.dtype, (unsigned)(most < kSms ? most : kSms), stream);
+  return launch_attn_tc(a, m, p.dtype, grid, stream);
 }
 
 }  // namespace nys

@@ -20,8 +20,10 @@ struct TileArgs {
   int32_t n, causal;
   int32_t heads, kv_heads, group, tp;  // tp: positions of a query tile, 128 / group
   int32_t d, dv;
+  int32_t per;     // query tiles of a unit: 2, or 1 (f32)
   int32_t splits;  // pieces that each unit's keys are cut into
   float scale;
+  Rows q;               // (f32; the 16-bit kernel reads it by its map)
   Rows out;             // results, where splits == 0
   float* lse;           // [q_rows][heads] or null
   float *part, *part_lse;  // pieces' results [split][q_rows][heads][dv], [..]; splits > 0
@@ -82,11 +84,13 @@ cudaError_t launch_shared_tiled(const SharedArgs& a, void* workspace, cudaStream
 cudaError_t launch_own(const SharedArgs& a, const OwnArgs& o, cudaStream_t stream);
 cudaError_t launch_join(const JoinArgs& a, int dtype, cudaStream_t stream);
 
-// Whether the tiled kernels take a prompt batch (16-bit types), and its launch.
+// Whether the tiled kernels take a prompt batch, and its launch.
 bool prompt_tc_fits(const PromptArgs& a);
 cudaError_t launch_prompt_tc(const PromptArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_tc(const TileArgs& a, const TileMaps& m, int dtype, unsigned grid,
                            cudaStream_t stream);
+
+cudaError_t launch_attn_tc32(const TileArgs& a, unsigned grid, cudaStream_t stream);
 
 #ifdef __CUDACC__
 // Walks the launch's units in order; one warp.  Within a sequence the query
@@ -112,7 +116,7 @@ struct UnitWalk {
         nk = (int)a.k_rows;
       }
     }
-    pairs = (nq + 2 * a.tp - 1) / (2 * a.tp);
+    pairs = (nq + a.per * a.tp - 1) / (a.per * a.tp);
     count = (int64_t)pairs * a.kv_heads * (a.splits ? a.splits : 1);
     upto = count;
 #pragma unroll
@@ -145,10 +149,10 @@ struct UnitWalk {
     r /= ns;
     u.kvh = (int)(r % a.kv_heads);
     const int pair = spairs - 1 - (int)(r / a.kv_heads);
-    const int p0 = pair * 2 * a.tp;
+    const int p0 = pair * a.per * a.tp;
     const int left = snq - p0;
     u.np0 = min(left, a.tp);
-    u.np1 = min(max(left - a.tp, 0), a.tp);
+    u.np1 = a.per == 2 ? min(max(left - a.tp, 0), a.tp) : 0;
     u.q_row = sq0 + p0;
     u.k_row = sk0;
     // Keys that the first position sees, and the last of each tile.

@@ -44,7 +44,7 @@ __device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
 }
 // Waits for the completion of the barrier's phase `parity`; false after 2 s or
 // once another thread of the CTA gave up.
-static __device__ __noinline__ bool bar_wait_slow(uint64_t* b, uint32_t parity, volatile int* abort) {
+__device__ __forceinline__ bool bar_wait_slow(uint64_t* b, uint32_t parity, volatile int* abort) {
   uint64_t t0, t1;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
   for (uint32_t i = 0;; ++i) {
