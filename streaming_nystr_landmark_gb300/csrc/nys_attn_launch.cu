@@ -57,6 +57,11 @@ bool tileable(const Rows& r, int64_t rows, int heads, int elem, bool bcast) {
   return true;
 }
 
+// The f32 kernel's row offsets, 32 bits in units of 16 bytes, reach the tensor.
+bool within_64_gb(int64_t rows, int64_t row, int heads, int64_t head) {
+  return (rows * row + heads * head) / 4 <= (int64_t)UINT32_MAX;
+}
+
 constexpr int kSms = 152;
 constexpr int kMostPieces = 64;
 
@@ -112,6 +117,10 @@ bool shared_tiled_fits(const SharedArgs& a) {
   if (reinterpret_cast<uintptr_t>(a.k) % 16 || reinterpret_cast<uintptr_t>(a.v) % 16) return false;
   if (a.n_pages * a.page > (1 << 30)) return false;
   if (!tileable(a.q, a.n, a.heads, elem, false)) return false;
+  if (a.dtype == NYS_F32 && a.prefix_len > 0 &&
+      !(within_64_gb(a.n, a.q.row, a.heads, a.q.head) &&
+        within_64_gb(a.n_pages * a.page, (int64_t)a.kv_heads * (a.d > a.dv ? a.d : a.dv), 0, 0)))
+    return false;
   if (a.prefix_len > 0 && a.dtype != NYS_F32 && a.page % 8) return false;
   return true;
 }
@@ -184,6 +193,10 @@ bool prompt_tc_fits(const PromptArgs& a) {
   const int elem = a.dtype == NYS_F32 ? 4 : 2, unit = 16 / elem;
   if (a.d > 128 || a.dv > 128 || a.d % unit || a.dv % unit) return false;
   if (a.k_rows == 0 || a.k_rows > (1 << 30) || a.q_rows > (1 << 30)) return false;
+  if (a.dtype == NYS_F32 && !(within_64_gb(a.q_rows, a.q.row, a.heads, a.q.head) &&
+                              within_64_gb(a.k_rows, a.k.row, a.kv_heads, a.k.head) &&
+                              within_64_gb(a.k_rows, a.v.row, a.kv_heads, a.v.head)))
+    return false;
   // K and V share the choice between a KV head's own rows and one head's rows.
   const bool kb = a.kv_heads > 1 && a.k.head == 0, vb = a.kv_heads > 1 && a.v.head == 0;
   return kb == vb && tileable(a.q, a.q_rows, a.heads, elem, false) &&

@@ -91,32 +91,32 @@ __device__ __forceinline__ void job_of(int e, int nt, int& what, int& j) {
   }
 }
 
-// Offset (elements) of row r of a job's tile in its tensor, -1: zeros.
+// Where row r of a job's tile begins in its tensor, in units of 16 bytes.  Rows
+// past the sequence stand for its last one: their scores are masked, their
+// weights 0, their results not stored.  A page outside the pool: 0, and `bad`.
 template <bool PAGED>
-__device__ __forceinline__ int64_t job_row(const TileArgs& a, const Unit& u, int what, int j,
-                                           int r) {
+__device__ __forceinline__ uint32_t job_row(const TileArgs& a, const Unit& u, int what, int j,
+                                            int r, bool& bad) {
   if (what == kJobQ) {
     const int pos = r / a.group, hd = r - pos * a.group;
-    if (pos >= u.np0) return -1;
-    return (u.q_row + (int64_t)pos) * a.q.row + (int64_t)(u.kvh * a.group + hd) * a.q.head;
+    return (uint32_t)(((u.q_row + (int64_t)min(pos, u.np0 - 1)) * a.q.row +
+                       (int64_t)(u.kvh * a.group + hd) * a.q.head) >> 2);
   }
-  const int key = u.kb + j * kTileN + r;
-  if (key >= u.nkl) return -1;
+  const int key = min(u.kb + j * kTileN + r, u.nkl - 1);
   int64_t row = (int64_t)u.k_row + key;
   if (PAGED) {
     const int32_t pg = a.pages[key / a.page];
     if (pg < 0 || pg >= a.n_pages) {
       attn_report(a.status, NYS_ATTN_BAD_PAGE);
-      return -1;
+      bad = true;
+      return 0;
     }
     row = (int64_t)pg * a.page + key % a.page;
   }
-  return what == kJobK ? row * a.k_row + u.kvh * a.k_head : row * a.v_row + u.kvh * a.v_head;
+  return (uint32_t)((what == kJobK ? row * a.k_row + u.kvh * a.k_head
+                                   : row * a.v_row + u.kvh * a.v_head) >> 2);
 }
 
-__device__ __forceinline__ float4 load4(const float* p) {
-  return __ldg(reinterpret_cast<const float4*>(p));
-}
 __device__ __forceinline__ bool finite_bits(float x) {
   return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u;
 }
@@ -126,81 +126,84 @@ template <bool PAGED>
 __device__ void convert_role(const TileArgs& a, Shared& sh, unsigned char* sm, int cw, int lane) {
   volatile int* ab = &sh.abort;
   uint32_t nu = 0, nq = 0, tile0 = 0, done_k = 0, done_v = 0;
-  Unit u;
   // The next job: unit u, step e.  Skips units without keys.
   int e = 0;
-  uint32_t held = 0;  // ring place of u
+  uint32_t held = 0;  // the unit's place in the ring (it is read there: registers are short)
+  int nt = 0;
   auto next_unit = [&]() {
     for (;;) {
       if (!bar_wait_warp(&sh.u_full[nu % kUnitRing], (nu / kUnitRing) & 1, ab)) return false;
       held = nu % kUnitRing;
-      u = sh.unit[held];
       ++nu;
-      if (!u.valid) return false;
-      if (u.nt > 0) return true;
+      if (!sh.unit[held].valid) return false;
+      nt = sh.unit[held].nt;
+      if (nt > 0) return true;
       __syncwarp();
       if (lane == 0) bar_arrive(&sh.u_empty[held]);
     }
   };
   const bool kcol = lane * 4 < a.d, vcol = lane * 4 < a.dv;
   const int r0 = cw * kConvRows;
-  const float* base[3] = {(const float*)a.q.p + lane * 4, (const float*)a.k_raw + lane * 4,
-                          (const float*)a.v_raw + lane * 4};
   float4 x[kConvRows];
   bool have = next_unit();
   if (!have) return;
-  {
-    const int64_t off = lane < kConvRows ? job_row<PAGED>(a, u, kJobQ, 0, r0 + lane) : -1;
+  // Rows of the next job, its first column for this lane, and its bad rows.
+  uint32_t off;
+  const float4* src;
+  uint32_t bad_rows = 0;
+  auto aim = [&](int what, int j) {
+    bool bad = false;
+    off = job_row<PAGED>(a, sh.unit[held], what, j, r0 + (lane & (kConvRows - 1)), bad);
+    bad_rows = PAGED ? __ballot_sync(0xffffffffu, bad) & 0xffffu : 0;
+    const float* p = (const float*)(what == kJobQ ? a.q.p : what == kJobK ? a.k_raw : a.v_raw);
+    src = reinterpret_cast<const float4*>(p) + ((what == kJobV ? vcol : kcol) ? lane : 0);
+  };
+  aim(kJobQ, 0);
 #pragma unroll
-    for (int r = 0; r < kConvRows; ++r) {
-      const int64_t o = __shfl_sync(0xffffffffu, off, r);
-      x[r] = o >= 0 && kcol ? load4(base[0] + o) : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-  }
-  // Where this lane's four columns lie in row r of a tile: 64-column block,
+  for (int r = 0; r < kConvRows; ++r) x[r] = __ldg(src + __shfl_sync(0xffffffffu, off, r));
+  // Where this lane's four columns lie in a row of a tile: 64-column block,
   // then 16-byte units exchanged by the row's low bits (128-byte swizzle).
-  const uint32_t col_at = (uint32_t)(lane >> 4) * 16384u + (uint32_t)(lane & 1) * 8u;
-  const uint32_t unit16 = (uint32_t)(lane & 15) >> 1;
+  const uint32_t col_at = (uint32_t)(lane >> 4) * 16384u + (uint32_t)(lane & 1) * 8u +
+                          (uint32_t)r0 * 128u;
+  const uint32_t unit16 = ((uint32_t)(lane & 15) >> 1) << 4;
   while (have) {
     int what, j;
-    job_of(e, u.nt, what, j);
+    job_of(e, nt, what, j);
     const uint32_t tile = tile0 + (uint32_t)j;
-    const Unit cur = u;
+    const bool edge = what == kJobV && j >= sh.unit[held].edge;
     const uint32_t cur_held = held, cur_nq = nq;
+    const uint32_t cur_bad = bad_rows;
     // What comes after it.
     bool last = false;
-    if (++e > 2 * u.nt) {
+    if (++e > 2 * nt) {
       last = true;
-      tile0 += (uint32_t)u.nt;
+      tile0 += (uint32_t)nt;
       ++nq;
       e = 0;
       have = next_unit();
     }
-    int nwhat = kJobQ, nj = 0;
-    int64_t off = -1;
-    if (have) {
-      job_of(e, u.nt, nwhat, nj);
-      if (lane < kConvRows) off = job_row<PAGED>(a, u, nwhat, nj, r0 + lane);
+    if (have) {  // (otherwise the last rows are read once more)
+      int nwhat, nj;
+      job_of(e, nt, nwhat, nj);
+      aim(nwhat, nj);
     }
-    const float* nbase = base[nwhat];
-    const bool ncol = have && (nwhat == kJobV ? vcol : kcol);
+    const int cols = what == kJobV ? a.dv : a.d;
+    if (cur_bad || ((cols & 15) && lane * 4 >= cols)) {  // zeros
+#pragma unroll
+      for (int r = 0; r < kConvRows; ++r)
+        if (((cur_bad >> r) & 1) || lane * 4 >= cols) x[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
 
     // The rows' common exponent.
     float t0 = 0.f, t1 = 0.f;
 #pragma unroll
     for (int r = 0; r < kConvRows; ++r) {
-      t0 = max3(t0, fabsf(x[r].x), fabsf(x[r].y));
-      t1 = max3(t1, fabsf(x[r].z), fabsf(x[r].w));
+      t0 = max3_abs_nan(t0, x[r].x, x[r].y);
+      t1 = max3_abs_nan(t1, x[r].z, x[r].w);
     }
-    uint32_t top = __float_as_uint(fmaxf(t0, t1));
-    bool odd = false;  // (fmaxf passes NaN by: sums keep it)
-    {
-      float z = 0.f;
-#pragma unroll
-      for (int r = 0; r < kConvRows; ++r)
-        z += (x[r].x * 0.f + x[r].y * 0.f) + (x[r].z * 0.f + x[r].w * 0.f);
-      odd = __any_sync(0xffffffffu, z != 0.f);  // NaN: some value is not finite
-    }
+    uint32_t top = __reduce_max_sync(
+        0xffffffffu, max(__float_as_uint(t0) & 0x7FFFFFFFu, __float_as_uint(t1) & 0x7FFFFFFFu));
+    bool odd = top >= 0x7F800000u;  // some value is not finite
     if (odd) {
       float f = 0.f;
 #pragma unroll
@@ -210,9 +213,9 @@ __device__ void convert_role(const TileArgs& a, Shared& sh, unsigned char* sm, i
         for (int i = 0; i < 4; ++i)
           if (finite_bits(y[i])) f = fmaxf(f, fabsf(y[i]));
       }
-      top = __float_as_uint(f);
+      top = __reduce_max_sync(0xffffffffu, __float_as_uint(f));
       // Values that some row does not see: out, and added in the epilogue.
-      if (what == kJobV && j >= cur.edge) {
+      if (edge) {
 #pragma unroll
         for (int r = 0; r < kConvRows; ++r) {
           if (!finite_bits(x[r].x)) x[r].x = 0.f;
@@ -224,7 +227,6 @@ __device__ void convert_role(const TileArgs& a, Shared& sh, unsigned char* sm, i
         odd = false;
       }
     }
-    top = __reduce_max_sync(0xffffffffu, top);
     int ex = (int)(top >> 23);          // biased
     if (ex == 0) ex = 127;              // all zero: any scale
     if (ex < 40) ex = 40;
@@ -247,20 +249,20 @@ __device__ void convert_role(const TileArgs& a, Shared& sh, unsigned char* sm, i
     else ok = bar_wait_warp(&sh.v_empty, (done_v++ & 1) ^ 1, ab);
     if (!ok) return;
     unsigned char* t = sm + what * 2 * kPiece + col_at;
-    const int cols = what == kJobV ? a.dv : a.d;
     const bool put = lane * 4 < ((cols + 15) & ~15);
-#pragma unroll
-    for (int r = 0; r < kConvRows; ++r) {
-      const int row = r0 + r;
-      const uint32_t at = (uint32_t)row * 128u + ((unit16 ^ (uint32_t)(row & 7)) << 4);
-      float y[4] = {x[r].x * scale, x[r].y * scale, x[r].z * scale, x[r].w * scale};
+    const uint64_t scale2 = pair(scale, scale), minus2 = pair(-1.f, -1.f);
+    using H = Type16<__half>;
+    auto store_row = [&](int r, bool keep) {
+      float y[4];
+      const uint64_t ya = mul2(pair(x[r].x, x[r].y), scale2), yb = mul2(pair(x[r].z, x[r].w), scale2);
+      unpair(ya, y[0], y[1]);
+      unpair(yb, y[2], y[3]);
       float h[4], l[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        h[i] = __uint_as_float(__float_as_uint(y[i]) & 0xFFFFE000u);
-        l[i] = y[i] - h[i];
-      }
-      if (odd) {  // infinities and NaN stay what they are, alone in hi
+      for (int i = 0; i < 4; ++i) h[i] = cut11(y[i]);
+      unpair(fma2(pair(h[0], h[1]), minus2, ya), l[0], l[1]);
+      unpair(fma2(pair(h[2], h[3]), minus2, yb), l[2], l[3]);
+      if (keep) {  // infinities and NaN stay what they are, alone in hi
         const float z[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -269,15 +271,20 @@ __device__ void convert_role(const TileArgs& a, Shared& sh, unsigned char* sm, i
             l[i] = 0.f;
           }
       }
-      using H = Type16<__half>;
       if (put) {
-        *reinterpret_cast<uint2*>(t + at) = make_uint2(H::pack(h[0], h[1]), H::pack(h[2], h[3]));
-        *reinterpret_cast<uint2*>(t + kPiece + at) =
-            make_uint2(H::pack(l[0], l[1]), H::pack(l[2], l[3]));
+        unsigned char* to = t + r * 128 + (unit16 ^ (uint32_t)((r & 7) << 4));
+        *reinterpret_cast<uint2*>(to) = make_uint2(H::pack(h[0], h[1]), H::pack(h[2], h[3]));
+        *reinterpret_cast<uint2*>(to + kPiece) = make_uint2(H::pack(l[0], l[1]), H::pack(l[2], l[3]));
       }
       // The next job's row takes these registers.
-      const int64_t o = __shfl_sync(0xffffffffu, off, r);
-      x[r] = o >= 0 && ncol ? load4(nbase + o) : make_float4(0.f, 0.f, 0.f, 0.f);
+      x[r] = __ldg(src + __shfl_sync(0xffffffffu, off, r));
+    };
+    if (odd) {
+#pragma unroll
+      for (int r = 0; r < kConvRows; ++r) store_row(r, true);
+    } else {
+#pragma unroll
+      for (int r = 0; r < kConvRows; ++r) store_row(r, false);
     }
     proxy_fence();
     __syncwarp();
@@ -412,7 +419,10 @@ __device__ void row_role(const TileArgs& a, Shared& sh, uint32_t tmem, int row, 
           wait_ld();
           pin32(o);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) acc[c + i] += __uint_as_float(o[i]);
+          for (int i = 0; i < 32; i += 2)
+            unpair(add2(pair(acc[c + i], acc[c + i + 1]),
+                        pair(__uint_as_float(o[i]), __uint_as_float(o[i + 1]))),
+                   acc[c + i], acc[c + i + 1]);
         }
       fence_before();
       __syncwarp();
@@ -429,28 +439,38 @@ __device__ void row_role(const TileArgs& a, Shared& sh, uint32_t tmem, int row, 
       const float* km = sh.k_mul[n & 3];
       const float* ve = sh.v_exp[n & 3];
       const float* vi = sh.v_inv[n & 3];
-      const bool cut = lim0 < (j + 1) * kTileN;
-      const int vis = lim - j * kTileN;
-      float top = m;
+      if (lim0 < (j + 1) * kTileN) {  // some row does not see some key: mask S in place
+        const int vis = lim - j * kTileN;
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 32) {
+          uint32_t x[32];
+          ld32(s_at + c, x);
+          wait_ld();
+          pin32(x);
 #pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (c + i >= vis) x[i] = 0xff800000u;
+          st32(s_at + c, x);
+        }
+        wait_st();
+      }
+      float top = m;
+#pragma unroll 1
       for (int c = 0; c < 128; c += 32) {
         uint32_t x[32];
         ld32(s_at + c, x);
         wait_ld();
         pin32(x);
-        if (cut) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (c + i >= vis) x[i] = 0xff800000u;
-        }
 #pragma unroll
         for (int g = 0; g < 32; g += 16) {
-          float t0 = __uint_as_float(x[g]), t1 = __uint_as_float(x[g + 1]);
+          float t0 = max3(__uint_as_float(x[g]), __uint_as_float(x[g + 1]), __uint_as_float(x[g + 2]));
+          float t1 = max3(__uint_as_float(x[g + 3]), __uint_as_float(x[g + 4]), __uint_as_float(x[g + 5]));
 #pragma unroll
-          for (int i = 2; i < 16; i += 2) {
-            t0 = fmaxf(t0, __uint_as_float(x[g + i]));
-            t1 = fmaxf(t1, __uint_as_float(x[g + i + 1]));
+          for (int i = 6; i < 14; i += 4) {
+            t0 = max3(t0, __uint_as_float(x[g + i]), __uint_as_float(x[g + i + 1]));
+            t1 = max3(t1, __uint_as_float(x[g + i + 2]), __uint_as_float(x[g + i + 3]));
           }
+          t0 = max3(t0, __uint_as_float(x[g + 14]), __uint_as_float(x[g + 15]));
           const float f = fmaxf(km[(c + g) >> 4] * qm, 1e-36f);
           top = fmaxf(top, fmaf(fmaxf(t0, t1), f, ve[(c + g) >> 4]));
         }
@@ -465,34 +485,40 @@ __device__ void row_role(const TileArgs& a, Shared& sh, uint32_t tmem, int row, 
       const float ref = (m == -INFINITY ? 0.f : m) - kLift;
       // A group of 16 keys at a time, the next one's scores on their way: P's
       // pieces take the group's own 16 columns.
-      uint32_t x[2][16];
-      ld16(s_at, x[0]);
-#pragma unroll
-      for (int g = 0; g < 8; ++g) {
-        wait_ld();
-        pin16(x[g & 1]);
-        if (g < 7) ld16(s_at + (g + 1) * 16, x[(g + 1) & 1]);
+      uint32_t xa[16], xb[16];
+      auto weights = [&](uint32_t* x, int g) {
         const float f = fmaxf(km[g] * qm, 1e-36f), z = ve[g] - ref;
         uint32_t p[16];
-        float l0 = 0.f, l1 = 0.f;
+        const uint64_t f2 = pair(f, f), z2 = pair(z, z), minus2 = pair(-1.f, -1.f);
+        uint64_t sum = pair(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
-          float y0 = fmaf(__uint_as_float(x[g & 1][i]), f, z);
-          float y1 = fmaf(__uint_as_float(x[g & 1][i + 1]), f, z);
-          if (cut) {
-            if (g * 16 + i >= vis) y0 = -INFINITY;
-            if (g * 16 + i + 1 >= vis) y1 = -INFINITY;
-          }
+          float y0, y1, r0, r1;
+          unpair(fma2(pair(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), f2, z2), y0, y1);
           const float p0 = ex2(y0), p1 = ex2(y1);
-          l0 += p0;
-          l1 += p1;
-          const float h0 = __uint_as_float(__float_as_uint(p0) & 0xFFFFE000u);
-          const float h1 = __uint_as_float(__float_as_uint(p1) & 0xFFFFE000u);
+          const uint64_t w = pair(p0, p1);
+          sum = add2(sum, w);
+          const float h0 = cut11(p0), h1 = cut11(p1);
+          unpair(fma2(pair(h0, h1), minus2, w), r0, r1);
           p[i / 2] = Type16<__half>::pack(h0, h1);
-          p[8 + i / 2] = Type16<__half>::pack(p0 - h0, p1 - h1);
+          p[8 + i / 2] = Type16<__half>::pack(r0, r1);
         }
+        float l0, l1;
+        unpair(sum, l0, l1);
         l = fmaf(l0 + l1, vi[g], l);
         st16(s_at + g * 16, p);
+      };
+      ld16(s_at, xa);
+#pragma unroll 1
+      for (int g = 0; g < 8; g += 2) {
+        wait_ld();
+        pin16(xa);
+        ld16(s_at + g * 16 + 16, xb);
+        weights(xa, g);
+        wait_ld();
+        pin16(xb);
+        if (g < 6) ld16(s_at + g * 16 + 32, xa);
+        weights(xb, g + 1);
       }
       wait_st();
       fence_before();
@@ -526,7 +552,7 @@ __device__ void row_role(const TileArgs& a, Shared& sh, uint32_t tmem, int row, 
             for (int k = u.edge * kTileN; k < lim; ++k) {
               const float* v = value_row<PAGED>(a, u, u.kb + k);
               if (!v) continue;
-              const float4 z = load4(v + c);
+              const float4 z = *reinterpret_cast<const float4*>(v + c);
               if (!finite_bits(z.x)) acc[c] += z.x;
               if (!finite_bits(z.y)) acc[c + 1] += z.y;
               if (!finite_bits(z.z)) acc[c + 2] += z.z;
@@ -555,9 +581,9 @@ template <int N>
 __device__ __forceinline__ void fewer_regs() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
-// The launch holds 512 x 128 registers; the shares are 128 x 232 + 256 x 104 +
-// 128 x 72 = those 65,536.
-constexpr int kRegsRow = 232, kRegsConvert = 104, kRegsRest = 72;
+// The launch holds 512 x 128 registers; the shares are 128 x 208 + 256 x 120 +
+// 128 x 64 = those 65,536.
+constexpr int kRegsRow = 208, kRegsConvert = 120, kRegsRest = 64;
 static_assert(128 * kRegsRow + 256 * kRegsConvert + 128 * kRegsRest <= 512 * 128, "registers");
 
 template <bool PAGED>
