@@ -606,9 +606,9 @@ attn_tc_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CUten
   if (warp < 8) {
     row_role<T, PAGED>(a, sh, tmem, warp >> 2, tid & 127, lane);
   } else if (warp == 8) {
-    if (lane == 0) load_role<PAGED>(a, &mq, &mk, &mv, sh, sm);
+    if (elect_one()) load_role<PAGED>(a, &mq, &mk, &mv, sh, sm);
   } else if (warp == 9) {
-    if (lane == 0) mma_role<T>(a, sh, sm, tmem);
+    if (elect_one()) mma_role<T>(a, sh, sm, tmem);
   } else if (warp == 10) {
     unit_role(a, sh, lane);
   } else {

@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc32_kernel(const __grid_con
   } else {
     fewer_regs<kRegsRest>();
     if (warp == 12) {
-      if (lane == 0) mma_role(a, sh, sm, tmem);
+      if (elect_one()) mma_role(a, sh, sm, tmem);
     } else if (warp == 13) {
       unit_role(a, sh, lane);
     }

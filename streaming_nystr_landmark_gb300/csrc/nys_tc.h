@@ -15,6 +15,16 @@ namespace tc {
 constexpr uint64_t kWaitNs = 2000000000ull;  // every wait gives up after 2 s
 constexpr uint32_t kSuspendNs = 100000;      // a waiting thread sleeps up to 0.1 ms a try
 
+// One lane of the warp, the same one each time.  The products' operands live
+// in uniform registers; a branch on this (unlike one on the lane number) tells
+// the compiler that a single thread takes it, so it moves them there at once
+// (measured: 74 against 97 clocks a product of 128 x 128 x 16).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t y;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(y));
+  return y != 0;
+}
 __device__ __forceinline__ uint32_t sptr(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
