@@ -27,21 +27,28 @@ EncodeTiled encoder() {
   return fn;
 }
 
-// Map of a [rows][heads][dim] tensor of 16-bit elements; boxes of 64 columns,
-// `box_h` heads and `box_r` rows, 128-byte swizzle.  Strides in elements; those
-// of extents of one are not used and replaced by valid ones.
-bool make_map(CUtensorMap* m, bool bf16, const void* p, int64_t rows, int64_t heads, int64_t dim,
+// Map of a [rows][heads][dim] tensor; boxes of `box_h` heads and `box_r` rows
+// of 64 columns with the 128-byte swizzle (16-bit types), or of 128 columns as
+// they are (f32).  Strides in elements; those of extents of one are not used
+// and replaced by valid ones.
+bool make_map(CUtensorMap* m, int dtype, const void* p, int64_t rows, int64_t heads, int64_t dim,
               int64_t row, int64_t head, int box_h, int box_r) {
+  const bool f32 = dtype == NYS_F32;
+  const int64_t es = f32 ? 4 : 2;
   const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)rows};
-  const cuuint64_t line = (cuuint64_t)((dim * 2 + 15) & ~int64_t(15));
-  const cuuint64_t st[2] = {heads > 1 ? (cuuint64_t)head * 2 : line,
-                            rows > 1 ? (cuuint64_t)row * 2 : line * (cuuint64_t)heads};
-  const cuuint32_t box[3] = {64, (cuuint32_t)box_h, (cuuint32_t)box_r};
+  const cuuint64_t line = (cuuint64_t)((dim * es + 15) & ~int64_t(15));
+  const cuuint64_t st[2] = {heads > 1 ? (cuuint64_t)(head * es) : line,
+                            rows > 1 ? (cuuint64_t)(row * es) : line * (cuuint64_t)heads};
+  const cuuint32_t box[3] = {f32 ? 128u : 64u, (cuuint32_t)box_h, (cuuint32_t)box_r};
   const cuuint32_t one[3] = {1, 1, 1};
+  const CUtensorMapDataType type = f32                  ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : dtype == NYS_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const EncodeTiled enc = encoder();
-  return enc && enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                    3, const_cast<void*>(p), dims, st, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  return enc && enc(m, type, 3, const_cast<void*>(p), dims, st, box, one,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    f32 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -55,11 +62,6 @@ bool tileable(const Rows& r, int64_t rows, int heads, int elem, bool bcast) {
       (head <= 0 || head % 16 || head >= (int64_t(1) << 40)))
     return false;
   return true;
-}
-
-// The f32 kernel's row offsets, 32 bits in units of 16 bytes, reach the tensor.
-bool within_64_gb(int64_t rows, int64_t row, int heads, int64_t head) {
-  return (rows * row + heads * head) / 4 <= (int64_t)UINT32_MAX;
 }
 
 constexpr int kSms = 152;
@@ -117,10 +119,6 @@ bool shared_tiled_fits(const SharedArgs& a) {
   if (reinterpret_cast<uintptr_t>(a.k) % 16 || reinterpret_cast<uintptr_t>(a.v) % 16) return false;
   if (a.n_pages * a.page > (1 << 30)) return false;
   if (!tileable(a.q, a.n, a.heads, elem, false)) return false;
-  if (a.dtype == NYS_F32 && a.prefix_len > 0 &&
-      !(within_64_gb(a.n, a.q.row, a.heads, a.q.head) &&
-        within_64_gb(a.n_pages * a.page, (int64_t)a.kv_heads * (a.d > a.dv ? a.d : a.dv), 0, 0)))
-    return false;
   if (a.prefix_len > 0 && a.dtype != NYS_F32 && a.page % 8) return false;
   return true;
 }
@@ -154,7 +152,6 @@ cudaError_t launch_shared_tiled(const SharedArgs& s, void* workspace, cudaStream
     a.part_lse = o.part_lse;
     a.pages = s.prefix_pages;
     a.page = s.page;
-    a.box = gcd(s.page, kTileN);
     a.n_pages = s.n_pages;
     a.k_raw = s.k;
     a.v_raw = s.v;
@@ -168,19 +165,17 @@ cudaError_t launch_shared_tiled(const SharedArgs& s, void* workspace, cudaStream
     a.per = s.dtype == NYS_F32 ? 1 : 2;
     const int64_t all = units * o.prefix_pieces;
     const unsigned grid = (unsigned)(all < kSms ? all : kSms);
-    cudaError_t e;
-    if (s.dtype == NYS_F32) {
-      e = launch_attn_tc32(a, grid, stream);
-    } else {
-    const bool bf16 = s.dtype == NYS_BF16;
+    const bool f32 = s.dtype == NYS_F32;
+    a.box = gcd(s.page, f32 ? kTileN / 2 : kTileN);
     const int64_t slots = s.n_pages * s.page;
     TileMaps m;
-    if (!make_map(&m.q, bf16, s.q.p, s.n, s.heads, s.d, s.q.row, s.q.head, s.group, a.tp) ||
-        !make_map(&m.k, bf16, s.k, slots, s.kv_heads, s.d, a.k_row, a.k_head, 1, a.box) ||
-        !make_map(&m.v, bf16, s.v, slots, s.kv_heads, s.dv, a.v_row, a.v_head, 1, a.box))
+    if ((!f32 &&
+         !make_map(&m.q, s.dtype, s.q.p, s.n, s.heads, s.d, s.q.row, s.q.head, s.group, a.tp)) ||
+        !make_map(&m.k, s.dtype, s.k, slots, s.kv_heads, s.d, a.k_row, a.k_head, 1, a.box) ||
+        !make_map(&m.v, s.dtype, s.v, slots, s.kv_heads, s.dv, a.v_row, a.v_head, 1, a.box))
       return cudaErrorInvalidValue;
-    e = launch_attn_tc(a, m, s.dtype, grid, stream);
-    }
+    const cudaError_t e = f32 ? launch_attn_tc32(a, m, grid, stream)
+                              : launch_attn_tc(a, m, s.dtype, grid, stream);
     if (e != cudaSuccess) return e;
   }
   const cudaError_t e = launch_own(s, o, stream);
@@ -193,10 +188,6 @@ bool prompt_tc_fits(const PromptArgs& a) {
   const int elem = a.dtype == NYS_F32 ? 4 : 2, unit = 16 / elem;
   if (a.d > 128 || a.dv > 128 || a.d % unit || a.dv % unit) return false;
   if (a.k_rows == 0 || a.k_rows > (1 << 30) || a.q_rows > (1 << 30)) return false;
-  if (a.dtype == NYS_F32 && !(within_64_gb(a.q_rows, a.q.row, a.heads, a.q.head) &&
-                              within_64_gb(a.k_rows, a.k.row, a.kv_heads, a.k.head) &&
-                              within_64_gb(a.k_rows, a.v.row, a.kv_heads, a.v.head)))
-    return false;
   // K and V share the choice between a KV head's own rows and one head's rows.
   const bool kb = a.kv_heads > 1 && a.k.head == 0, vb = a.kv_heads > 1 && a.v.head == 0;
   return kb == vb && tileable(a.q, a.q_rows, a.heads, elem, false) &&
@@ -235,14 +226,16 @@ cudaError_t launch_prompt_tc(const PromptArgs& p, cudaStream_t stream) {
   // At most this many units: a partial one a sequence on top of the full ones.
   const int64_t most = (p.q_rows / (a.per * a.tp) + p.n) * p.kv_heads;
   const unsigned grid = (unsigned)(most < kSms ? most : kSms);
-  if (p.dtype == NYS_F32) return launch_attn_tc32(a, grid, stream);
   TileMaps m;
-  const bool bf16 = p.dtype == NYS_BF16;
+  const bool f32 = p.dtype == NYS_F32;
   const int64_t kvh = a.kv_y ? p.kv_heads : 1;
-  if (!make_map(&m.q, bf16, p.q.p, p.q_rows, p.heads, p.d, p.q.row, p.q.head, p.group, a.tp) ||
-      !make_map(&m.k, bf16, p.k.p, p.k_rows, kvh, p.d, p.k.row, p.k.head, 1, kTileN) ||
-      !make_map(&m.v, bf16, p.v.p, p.k_rows, kvh, p.dv, p.v.row, p.v.head, 1, kTileN))
+  const int box = f32 ? kTileN / 2 : kTileN;
+  if ((!f32 && !make_map(&m.q, p.dtype, p.q.p, p.q_rows, p.heads, p.d, p.q.row, p.q.head, p.group,
+                         a.tp)) ||
+      !make_map(&m.k, p.dtype, p.k.p, p.k_rows, kvh, p.d, p.k.row, p.k.head, 1, box) ||
+      !make_map(&m.v, p.dtype, p.v.p, p.k_rows, kvh, p.dv, p.v.row, p.v.head, 1, box))
     return cudaErrorInvalidValue;
+  if (f32) return launch_attn_tc32(a, m, grid, stream);
   return launch_attn_tc(a, m, p.dtype, grid, stream);
 }
 

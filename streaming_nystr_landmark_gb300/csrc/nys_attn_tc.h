@@ -90,7 +90,8 @@ cudaError_t launch_prompt_tc(const PromptArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_tc(const TileArgs& a, const TileMaps& m, int dtype, unsigned grid,
                            cudaStream_t stream);
 
-cudaError_t launch_attn_tc32(const TileArgs& a, unsigned grid, cudaStream_t stream);
+cudaError_t launch_attn_tc32(const TileArgs& a, const TileMaps& m, unsigned grid,
+                             cudaStream_t stream);  // (no q map)
 
 #ifdef __CUDACC__
 // Walks the launch's units in order; one warp.  Within a sequence the query

@@ -22,14 +22,16 @@
 //
 // One CTA of 512 threads a SM works on one query tile of 128 rows (positions x
 // heads of the group): warps 0-3 softmax and accumulation (thread = row, 128
-// accumulators), 4-11 load f32 rows and convert them into the swizzled tiles
-// (16 rows a warp, the next tile's loads in flight while this one is
-// converted), 12 products, 13 units of work.  Registers move from the others
-// to the softmax.  Shared memory: Q, K and V, each a hi and a lo tile of 32 KB.
-// Products of tile j + 1's scores run during tile j's softmax, and K (V) is
-// converted while the value (score) products run, so single buffers suffice.
-// Tensor memory: two S and two O of 128 columns; P hi and lo take S's place, 8
-// columns each for 16 keys.
+// accumulators), 4-11 convert, 12 products, 13 units of work, 14 TMA loads.
+// Registers move from the others to the softmax.  TMA brings f32 rows into a
+// ring of three 32 KB stages (64 rows each); converting warps turn 16 rows each
+// into the swizzled hi and lo tiles of K and V (32 KB a piece), and the query
+// tile, thread = row, straight into tensor memory, because a product with A
+// there takes 74 clocks and one with A in shared memory 107.  Products of tile
+// j + 1's scores run during tile j's softmax, and K (V) is converted while the
+// value (score) products run, so single buffers suffice.  Tensor memory: Q hi
+// and lo (64 columns each), two S and one O of 128 columns; P hi and lo take S's
+// place, 8 columns each for 16 keys.
 //
 // Rows that are not in the sequence are zeros and never read.  Values that are
 // not finite where some row of the tile does not see their key are replaced
@@ -49,7 +51,12 @@ constexpr int kThreads = 512;
 constexpr int kConv = 8;        // converting warps
 constexpr int kConvRows = 16;   // rows of one of them
 constexpr uint32_t kPiece = 32768;
-constexpr uint32_t kOffK = 2 * kPiece, kOffV = 4 * kPiece, kTiles = 6 * kPiece;
+constexpr int kStages = 3;
+constexpr int kStageRows = 64;
+constexpr uint32_t kStageBytes = kStageRows * 512;
+constexpr uint32_t kOffV = 2 * kPiece, kOffStage = 4 * kPiece;
+constexpr uint32_t kTiles = kOffStage + kStages * kStageBytes;
+constexpr uint32_t kColQ = 0, kColS = 128, kColO = 384;  // tensor memory
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.f;
@@ -58,11 +65,12 @@ constexpr int kTop = 13;        // the largest value's power of two after scalin
 
 struct Shared {
   uint64_t q_full, q_empty, k_full, k_empty, v_full, v_empty;
-  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], x_full[2];
+  uint64_t s_full[2], p_full[2], x_full[2], o_full, o_empty;
+  uint64_t st_full[kStages], st_empty[kStages];
   uint64_t u_full[kUnitRing], u_empty[kUnitRing];
   uint64_t drain;
   Unit unit[kUnitRing];
-  float q_mul[2][kConv];             // 2^eq, [unit & 1][16 rows]
+  float q_mul[2][kTileM];            // 2^eq, [unit & 1][row]
   float k_mul[4][kConv];             // 2^ek, [tile & 3][16 keys]
   float v_exp[4][kConv], v_inv[4][kConv];  // ev, 2^-ev
   uint32_t tmem;
@@ -72,6 +80,7 @@ constexpr uint32_t kSmem = kTiles + sizeof(Shared);
 static_assert(kSmem <= 227 * 1024, "one CTA's shared memory");
 
 enum { kJobQ = 0, kJobK = 1, kJobV = 2 };
+
 
 // Step e of a unit's conversions: Q K0 V0 K1 K2 V1 K3 V2 .. (K of the tile
 // after next, once its scores' predecessor is done, before the next V).
@@ -91,207 +100,293 @@ __device__ __forceinline__ void job_of(int e, int nt, int& what, int& j) {
   }
 }
 
-// Where row r of a job's tile begins in its tensor, in units of 16 bytes.  Rows
-// past the sequence stand for its last one: their scores are masked, their
-// weights 0, their results not stored.  A page outside the pool: 0, and `bad`.
-template <bool PAGED>
-__device__ __forceinline__ uint32_t job_row(const TileArgs& a, const Unit& u, int what, int j,
-                                            int r, bool& bad) {
-  if (what == kJobQ) {
-    const int pos = r / a.group, hd = r - pos * a.group;
-    return (uint32_t)(((u.q_row + (int64_t)min(pos, u.np0 - 1)) * a.q.row +
-                       (int64_t)(u.kvh * a.group + hd) * a.q.head) >> 2);
-  }
-  const int key = min(u.kb + j * kTileN + r, u.nkl - 1);
-  int64_t row = (int64_t)u.k_row + key;
-  if (PAGED) {
-    const int32_t pg = a.pages[key / a.page];
-    if (pg < 0 || pg >= a.n_pages) {
-      attn_report(a.status, NYS_ATTN_BAD_PAGE);
-      bad = true;
-      return 0;
-    }
-    row = (int64_t)pg * a.page + key % a.page;
-  }
-  return (uint32_t)((what == kJobK ? row * a.k_row + u.kvh * a.k_head
-                                   : row * a.v_row + u.kvh * a.v_head) >> 2);
-}
-
 __device__ __forceinline__ bool finite_bits(float x) {
   return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u;
 }
 
-// ---- conversion (eight warps; cw = 0 .. 7)
+// ---- TMA loads (one thread): every tile as two stages of 64 rows.  A stage
+// past the sequence's end is passed on empty.
 template <bool PAGED>
-__device__ void convert_role(const TileArgs& a, Shared& sh, unsigned char* sm, int cw, int lane) {
+__device__ void load_role(const TileArgs& a, const CUtensorMap* mk, const CUtensorMap* mv,
+                          Shared& sh, unsigned char* sm) {
   volatile int* ab = &sh.abort;
-  uint32_t nu = 0, nq = 0, tile0 = 0, done_k = 0, done_v = 0;
-  // The next job: unit u, step e.  Skips units without keys.
-  int e = 0;
-  uint32_t held = 0;  // the unit's place in the ring (it is read there: registers are short)
-  int nt = 0;
-  auto next_unit = [&]() {
-    for (;;) {
-      if (!bar_wait_warp(&sh.u_full[nu % kUnitRing], (nu / kUnitRing) & 1, ab)) return false;
-      held = nu % kUnitRing;
-      ++nu;
-      if (!sh.unit[held].valid) return false;
-      nt = sh.unit[held].nt;
-      if (nt > 0) return true;
-      __syncwarp();
-      if (lane == 0) bar_arrive(&sh.u_empty[held]);
+  uint32_t cnt = 0, filled = 0;
+  bool ok = true;
+  for (uint32_t nu = 0; ok; ++nu) {
+    if (!bar_wait(&sh.u_full[nu % kUnitRing], (nu / kUnitRing) & 1, ab)) break;
+    const Unit u = sh.unit[nu % kUnitRing];
+    bar_arrive(&sh.u_empty[nu % kUnitRing]);
+    if (!u.valid) break;
+    const int y = a.kv_y ? u.kvh : 0;
+    for (int e = 1; e <= 2 * u.nt && ok; ++e) {
+      int what, j;
+      job_of(e, u.nt, what, j);
+      const CUtensorMap* m = what == kJobK ? mk : mv;
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t slot = cnt % kStages;
+        ok = bar_wait(&sh.st_empty[slot], ((cnt / kStages) & 1) ^ 1, ab);
+        if (!ok) break;
+        ++cnt;
+        const int key = u.kb + j * kTileN + h * kStageRows;
+        if (key >= u.nkl) {
+          filled &= ~(1u << slot);
+          bar_arrive(&sh.st_full[slot]);
+          continue;
+        }
+        filled |= 1u << slot;
+        unsigned char* dst = sm + kOffStage + slot * kStageBytes;
+        bar_expect(&sh.st_full[slot], kStageBytes);
+        if (!PAGED) {
+          tma_load3(dst, m, 0, y, u.k_row + key, &sh.st_full[slot]);
+        } else {
+          for (int b = 0; b < kStageRows; b += a.box) {
+            // Past the prefix or outside the pool: a row past the tensor's
+            // end, which reads as zeros.
+            int64_t row = a.n_pages * a.page;
+            if (key + b < u.nkl) {
+              const int32_t pg = a.pages[(key + b) / a.page];
+              if (pg >= 0 && pg < a.n_pages) row = (int64_t)pg * a.page + (key + b) % a.page;
+              else attn_report(a.status, NYS_ATTN_BAD_PAGE);
+            }
+            tma_load3(dst + b * 512, m, 0, y, (int)row, &sh.st_full[slot]);
+          }
+        }
+      }
     }
-  };
-  const bool kcol = lane * 4 < a.d, vcol = lane * 4 < a.dv;
-  const int r0 = cw * kConvRows;
-  float4 x[kConvRows];
-  bool have = next_unit();
-  if (!have) return;
-  // Rows of the next job, its first column for this lane, and its bad rows.
-  uint32_t off;
-  const float4* src;
-  uint32_t bad_rows = 0;
-  auto aim = [&](int what, int j) {
-    bool bad = false;
-    off = job_row<PAGED>(a, sh.unit[held], what, j, r0 + (lane & (kConvRows - 1)), bad);
-    bad_rows = PAGED ? __ballot_sync(0xffffffffu, bad) & 0xffffu : 0;
-    const float* p = (const float*)(what == kJobQ ? a.q.p : what == kJobK ? a.k_raw : a.v_raw);
-    src = reinterpret_cast<const float4*>(p) + ((what == kJobV ? vcol : kcol) ? lane : 0);
-  };
-  aim(kJobQ, 0);
+  }
+  // Copies in flight land before the CTA may leave.
+  if (*ab) {
+    int none = 0;
+    for (uint32_t c = cnt > kStages ? cnt - kStages : 0; c < cnt; ++c)
+      if ((filled >> (c % kStages)) & 1)
+        bar_wait(&sh.st_full[c % kStages], (c / kStages) & 1, &none);
+  }
+}
+
+// ---- conversion (eight warps)
+// The power of two that puts a value with these upper bits at 2^13, and back.
+__device__ __forceinline__ int top_exponent(uint32_t top) {
+  const int ex = (int)(top >> 23);         // biased
+  return ex == 0 ? 127 : (ex < 40 ? 40 : ex);  // all zero: any scale
+}
+__device__ __forceinline__ float scale_of(int ex) {  // 2^(13 - (ex - 127))
+  return __uint_as_float((uint32_t)(254 + kTop - ex) << 23);
+}
+__device__ __forceinline__ float back_of(int ex) {
+  return __uint_as_float((uint32_t)(ex - kTop) << 23);
+}
+// Four scaled values as hi and lo words.  keep: infinities and NaN stay what
+// they are, alone in hi.
+__device__ __forceinline__ void split4(float4 x, uint64_t scale2, bool keep, uint32_t (&hi)[2],
+                                       uint32_t (&lo)[2]) {
+  const uint64_t ya = mul2(pair(x.x, x.y), scale2), yb = mul2(pair(x.z, x.w), scale2);
+  const uint64_t minus2 = pair(-1.f, -1.f);
+  float y[4], h[4], l[4];
+  unpair(ya, y[0], y[1]);
+  unpair(yb, y[2], y[3]);
 #pragma unroll
-  for (int r = 0; r < kConvRows; ++r) x[r] = __ldg(src + __shfl_sync(0xffffffffu, off, r));
+  for (int i = 0; i < 4; ++i) h[i] = cut11(y[i]);
+  unpair(fma2(pair(h[0], h[1]), minus2, ya), l[0], l[1]);
+  unpair(fma2(pair(h[2], h[3]), minus2, yb), l[2], l[3]);
+  if (keep) {
+    const float z[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (!finite_bits(z[i])) {
+        h[i] = z[i];
+        l[i] = 0.f;
+      }
+  }
+  using H = Type16<__half>;
+  hi[0] = H::pack(h[0], h[1]);
+  hi[1] = H::pack(h[2], h[3]);
+  lo[0] = H::pack(l[0], l[1]);
+  lo[1] = H::pack(l[2], l[3]);
+}
+__device__ __forceinline__ float finite_max(float4 x) {
+  float f = 0.f;
+  if (finite_bits(x.x)) f = fmaxf(f, fabsf(x.x));
+  if (finite_bits(x.y)) f = fmaxf(f, fabsf(x.y));
+  if (finite_bits(x.z)) f = fmaxf(f, fabsf(x.z));
+  if (finite_bits(x.w)) f = fmaxf(f, fabsf(x.w));
+  return f;
+}
+
+// The query tile into tensor memory: thread = row of the warp's 32, columns
+// 64 * half .. (the other half is read for the row's exponent alone).  Rows past
+// the tile's positions stand for its last one.
+__device__ __forceinline__ void convert_q(const TileArgs& a, const Unit& u, float* q_mul,
+                                          uint32_t tmem, int warp, int lane, bool& waited,
+                                          uint64_t* q_empty, uint32_t parity, volatile int* ab) {
+  const int row = (warp & 3) * 32 + lane, half = warp >= 8;
+  const int pos = row / a.group, hd = row - pos * a.group;
+  const float* src = (const float*)a.q.p + (u.q_row + (int64_t)min(pos, u.np0 - 1)) * a.q.row +
+                     (int64_t)(u.kvh * a.group + hd) * a.q.head;
+  float4 x[16];
+  float t = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int c = half * 64 + i * 4;
+    x[i] = c < a.d ? __ldg(reinterpret_cast<const float4*>(src + c)) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int c = (1 - half) * 64 + i * 4;
+    if (c < a.d) {
+      const float4 z = __ldg(reinterpret_cast<const float4*>(src + c));
+      t = max3_abs_nan(t, z.x, z.y);
+      t = max3_abs_nan(t, z.z, z.w);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    t = max3_abs_nan(t, x[i].x, x[i].y);
+    t = max3_abs_nan(t, x[i].z, x[i].w);
+  }
+  uint32_t top = __float_as_uint(t) & 0x7FFFFFFFu;
+  const bool odd = __any_sync(0xffffffffu, top >= 0x7F800000u);
+  if (odd && top >= 0x7F800000u) {
+    float f = 0.f;
+    for (int c = 0; c < a.d; c += 4) f = fmaxf(f, finite_max(*reinterpret_cast<const float4*>(src + c)));
+    top = __float_as_uint(f);
+  }
+  const int ex = top_exponent(top);
+  if (half == 0) q_mul[row] = back_of(ex);
+  const float scale = scale_of(ex);
+  const uint64_t scale2 = pair(scale, scale);
+  waited = bar_wait_warp(q_empty, parity, ab);
+  if (!waited) return;
+  fence_after();
+  const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kColQ + half * 32;
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    uint32_t hi[16], lo[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t h2[2], l2[2];
+      split4(x[b * 8 + i], scale2, odd, h2, l2);
+      hi[2 * i] = h2[0];
+      hi[2 * i + 1] = h2[1];
+      lo[2 * i] = l2[0];
+      lo[2 * i + 1] = l2[1];
+    }
+    st16(at + b * 16, hi);
+    st16(at + 64 + b * 16, lo);
+  }
+  wait_st();
+  fence_before();
+}
+
+__device__ void convert_role(const TileArgs& a, Shared& sh, unsigned char* sm, uint32_t tmem,
+                             int warp, int lane) {
+  volatile int* ab = &sh.abort;
+  const int cw = warp - 4, half = cw >> 2;
+  const int r0 = cw * kConvRows;  // first row in the tile
+  uint32_t tile0 = 0, n_q = 0, n_job = 0;
   // Where this lane's four columns lie in a row of a tile: 64-column block,
   // then 16-byte units exchanged by the row's low bits (128-byte swizzle).
   const uint32_t col_at = (uint32_t)(lane >> 4) * 16384u + (uint32_t)(lane & 1) * 8u +
                           (uint32_t)r0 * 128u;
   const uint32_t unit16 = ((uint32_t)(lane & 15) >> 1) << 4;
-  while (have) {
-    int what, j;
-    job_of(e, nt, what, j);
-    const uint32_t tile = tile0 + (uint32_t)j;
-    const bool edge = what == kJobV && j >= sh.unit[held].edge;
-    const uint32_t cur_held = held, cur_nq = nq;
-    const uint32_t cur_bad = bad_rows;
-    // What comes after it.
-    bool last = false;
-    if (++e > 2 * nt) {
-      last = true;
-      tile0 += (uint32_t)nt;
-      ++nq;
-      e = 0;
-      have = next_unit();
+  const uint32_t stage_at = kOffStage + (uint32_t)(cw & 3) * kConvRows * 512u + (uint32_t)lane * 16u;
+  for (uint32_t nu = 0;; ++nu) {
+    if (!bar_wait_warp(&sh.u_full[nu % kUnitRing], (nu / kUnitRing) & 1, ab)) return;
+    const Unit& u = sh.unit[nu % kUnitRing];  // (read in place: registers are short)
+    if (!u.valid) return;
+    const int nt = u.nt, keys = u.nkl - u.kb, edge = u.edge;
+    if (nt > 0) {
+      bool ok;
+      convert_q(a, u, sh.q_mul[n_q & 1], tmem, warp, lane, ok, &sh.q_empty, (n_q & 1) ^ 1, ab);
+      if (!ok) return;
+      ++n_q;
+      __syncwarp();
+      if (lane == 0) bar_arrive(&sh.q_full);
     }
-    if (have) {  // (otherwise the last rows are read once more)
-      int nwhat, nj;
-      job_of(e, nt, nwhat, nj);
-      aim(nwhat, nj);
-    }
-    const int cols = what == kJobV ? a.dv : a.d;
-    if (cur_bad || ((cols & 15) && lane * 4 >= cols)) {  // zeros
+    for (int e = 1; e <= 2 * nt; ++e, ++n_job) {
+      int what, j;
+      job_of(e, nt, what, j);
+      const uint32_t tile = tile0 + (uint32_t)j;
+      const uint32_t n_st = 2 * n_job + half, slot = n_st % kStages;
+      if (!bar_wait_warp(&sh.st_full[slot], (n_st / kStages) & 1, ab)) return;
+      float4 x[kConvRows];
+      const unsigned char* from = sm + stage_at + slot * kStageBytes;
 #pragma unroll
-      for (int r = 0; r < kConvRows; ++r)
-        if (((cur_bad >> r) & 1) || lane * 4 >= cols) x[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-
-    // The rows' common exponent.
-    float t0 = 0.f, t1 = 0.f;
+      for (int r = 0; r < kConvRows; ++r) x[r] = *reinterpret_cast<const float4*>(from + r * 512);
+      const int rows = keys - j * kTileN - r0;  // of them, those in the sequence
+      if (rows < kConvRows) {
 #pragma unroll
-    for (int r = 0; r < kConvRows; ++r) {
-      t0 = max3_abs_nan(t0, x[r].x, x[r].y);
-      t1 = max3_abs_nan(t1, x[r].z, x[r].w);
-    }
-    uint32_t top = __reduce_max_sync(
-        0xffffffffu, max(__float_as_uint(t0) & 0x7FFFFFFFu, __float_as_uint(t1) & 0x7FFFFFFFu));
-    bool odd = top >= 0x7F800000u;  // some value is not finite
-    if (odd) {
-      float f = 0.f;
+        for (int r = 0; r < kConvRows; ++r)
+          if (r >= rows) x[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      // The rows' common exponent.
+      float t0 = 0.f, t1 = 0.f;
 #pragma unroll
       for (int r = 0; r < kConvRows; ++r) {
-        const float y[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (finite_bits(y[i])) f = fmaxf(f, fabsf(y[i]));
+        t0 = max3_abs_nan(t0, x[r].x, x[r].y);
+        t1 = max3_abs_nan(t1, x[r].z, x[r].w);
       }
-      top = __reduce_max_sync(0xffffffffu, __float_as_uint(f));
-      // Values that some row does not see: out, and added in the epilogue.
-      if (edge) {
+      uint32_t top = __reduce_max_sync(
+          0xffffffffu, max(__float_as_uint(t0) & 0x7FFFFFFFu, __float_as_uint(t1) & 0x7FFFFFFFu));
+      __syncwarp();
+      if (lane == 0) bar_arrive(&sh.st_empty[slot]);
+      bool odd = top >= 0x7F800000u;  // some value is not finite
+      if (odd) {
+        float f = 0.f;
 #pragma unroll
-        for (int r = 0; r < kConvRows; ++r) {
-          if (!finite_bits(x[r].x)) x[r].x = 0.f;
-          if (!finite_bits(x[r].y)) x[r].y = 0.f;
-          if (!finite_bits(x[r].z)) x[r].z = 0.f;
-          if (!finite_bits(x[r].w)) x[r].w = 0.f;
-        }
-        if (lane == 0) *(volatile int*)&sh.unit[cur_held].patch = 1;
-        odd = false;
-      }
-    }
-    int ex = (int)(top >> 23);          // biased
-    if (ex == 0) ex = 127;              // all zero: any scale
-    if (ex < 40) ex = 40;
-    const float scale = __uint_as_float((uint32_t)(254 + kTop - ex) << 23);  // 2^(13 - (ex - 127))
-    const float back = __uint_as_float((uint32_t)(ex - kTop) << 23);
-    if (lane == 0) {
-      if (what == kJobQ) {
-        sh.q_mul[cur_nq & 1][cw] = back;
-      } else if (what == kJobK) {
-        sh.k_mul[tile & 3][cw] = back;
-      } else {
-        sh.v_exp[tile & 3][cw] = (float)(ex - 127 - kTop);
-        sh.v_inv[tile & 3][cw] = scale;
-        bar_arrive(&sh.x_full[tile & 1]);
-      }
-    }
-    bool ok;
-    if (what == kJobQ) ok = bar_wait_warp(&sh.q_empty, (cur_nq & 1) ^ 1, ab);
-    else if (what == kJobK) ok = bar_wait_warp(&sh.k_empty, (done_k++ & 1) ^ 1, ab);
-    else ok = bar_wait_warp(&sh.v_empty, (done_v++ & 1) ^ 1, ab);
-    if (!ok) return;
-    unsigned char* t = sm + what * 2 * kPiece + col_at;
-    const bool put = lane * 4 < ((cols + 15) & ~15);
-    const uint64_t scale2 = pair(scale, scale), minus2 = pair(-1.f, -1.f);
-    using H = Type16<__half>;
-    auto store_row = [&](int r, bool keep) {
-      float y[4];
-      const uint64_t ya = mul2(pair(x[r].x, x[r].y), scale2), yb = mul2(pair(x[r].z, x[r].w), scale2);
-      unpair(ya, y[0], y[1]);
-      unpair(yb, y[2], y[3]);
-      float h[4], l[4];
+        for (int r = 0; r < kConvRows; ++r) f = fmaxf(f, finite_max(x[r]));
+        top = __reduce_max_sync(0xffffffffu, __float_as_uint(f));
+        // Values that some row does not see: out, and added in the epilogue.
+        if (what == kJobV && j >= edge) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) h[i] = cut11(y[i]);
-      unpair(fma2(pair(h[0], h[1]), minus2, ya), l[0], l[1]);
-      unpair(fma2(pair(h[2], h[3]), minus2, yb), l[2], l[3]);
-      if (keep) {  // infinities and NaN stay what they are, alone in hi
-        const float z[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (!finite_bits(z[i])) {
-            h[i] = z[i];
-            l[i] = 0.f;
+          for (int r = 0; r < kConvRows; ++r) {
+            if (!finite_bits(x[r].x)) x[r].x = 0.f;
+            if (!finite_bits(x[r].y)) x[r].y = 0.f;
+            if (!finite_bits(x[r].z)) x[r].z = 0.f;
+            if (!finite_bits(x[r].w)) x[r].w = 0.f;
           }
+          if (lane == 0) *(volatile int*)&sh.unit[nu % kUnitRing].patch = 1;
+          odd = false;
+        }
       }
-      if (put) {
-        unsigned char* to = t + r * 128 + (unit16 ^ (uint32_t)((r & 7) << 4));
-        *reinterpret_cast<uint2*>(to) = make_uint2(H::pack(h[0], h[1]), H::pack(h[2], h[3]));
-        *reinterpret_cast<uint2*>(to + kPiece) = make_uint2(H::pack(l[0], l[1]), H::pack(l[2], l[3]));
+      const int ex = top_exponent(top);
+      const float scale = scale_of(ex);
+      if (lane == 0) {
+        if (what == kJobK) {
+          sh.k_mul[tile & 3][cw] = back_of(ex);
+        } else {
+          sh.v_exp[tile & 3][cw] = (float)(ex - 127 - kTop);
+          sh.v_inv[tile & 3][cw] = scale;
+          bar_arrive(&sh.x_full[tile & 1]);
+        }
       }
-      // The next job's row takes these registers.
-      x[r] = __ldg(src + __shfl_sync(0xffffffffu, off, r));
-    };
-    if (odd) {
+      uint64_t* empty = what == kJobK ? &sh.k_empty : &sh.v_empty;
+      if (!bar_wait_warp(empty, (tile & 1) ^ 1, ab)) return;
+      unsigned char* t = sm + (what == kJobK ? 0u : kOffV) + col_at;
+      const bool put = lane * 4 < (((what == kJobV ? a.dv : a.d) + 15) & ~15);
+      const uint64_t scale2 = pair(scale, scale);
+      auto store_row = [&](int r, bool keep) {
+        uint32_t hi[2], lo[2];
+        split4(x[r], scale2, keep, hi, lo);
+        if (put) {
+          unsigned char* to = t + r * 128 + (unit16 ^ (uint32_t)((r & 7) << 4));
+          *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2*>(to + kPiece) = make_uint2(lo[0], lo[1]);
+        }
+      };
+      if (odd) {
 #pragma unroll
-      for (int r = 0; r < kConvRows; ++r) store_row(r, true);
-    } else {
+        for (int r = 0; r < kConvRows; ++r) store_row(r, true);
+      } else {
 #pragma unroll
-      for (int r = 0; r < kConvRows; ++r) store_row(r, false);
+        for (int r = 0; r < kConvRows; ++r) store_row(r, false);
+      }
+      proxy_fence();
+      __syncwarp();
+      if (lane == 0) bar_arrive(what == kJobK ? &sh.k_full : &sh.v_full);
     }
-    proxy_fence();
+    tile0 += (uint32_t)nt;
     __syncwarp();
-    if (lane == 0) {
-      bar_arrive(what == kJobQ ? &sh.q_full : what == kJobK ? &sh.k_full : &sh.v_full);
-      if (last) bar_arrive(&sh.u_empty[cur_held]);
-    }
+    if (lane == 0) bar_arrive(&sh.u_empty[nu % kUnitRing]);
   }
 }
 
@@ -302,7 +397,8 @@ __device__ void mma_role(const TileArgs& a, Shared& sh, unsigned char* sm, uint3
   const int nv = (a.dv + 15) & ~15;
   const uint32_t id_s = idesc(kTileM, kTileN, false, false);
   const uint32_t id_o = idesc(kTileM, nv, false, true);
-  const uint32_t q0 = sptr(sm), k0 = sptr(sm + kOffK), v0 = sptr(sm + kOffV);
+  // Descriptors of the hi tiles; the lo tiles lie kPiece further.
+  const uint64_t k0 = desc128(sptr(sm), 16, 1024), v0 = desc128(sptr(sm + kOffV), 16384, 1024);
   uint32_t nu = 0, nq = 0, n_s = 0, n_o = 0;  // units, query tiles, score and value tiles begun
   bool ok = true;
   for (; ok; ++nu) {
@@ -316,14 +412,15 @@ __device__ void mma_role(const TileArgs& a, Shared& sh, unsigned char* sm, uint3
     auto scores = [&](bool last) {
       if (!bar_wait(&sh.k_full, n_s & 1, ab)) return false;
       fence_after();
-      const uint32_t d = tmem + (n_s & 1) * 128;
+      const uint32_t d = tmem + kColS + (n_s & 1) * 128;
 #pragma unroll 1
       for (int p = 0; p < 3; ++p) {  // lo hi, hi lo, hi hi
-        const uint32_t q = q0 + (p == 0 ? kPiece : 0), k = k0 + (p == 1 ? kPiece : 0);
-        for (int i = 0; i < ks; ++i) {
-          const uint32_t off = (i >> 2) * 16384 + (i & 3) * 32;
-          mma_ss(d, desc128(q + off, 16, 1024), desc128(k + off, 16, 1024), id_s, p + i > 0);
-        }
+        const uint32_t q = tmem + kColQ + (p == 0 ? 64 : 0);
+        const uint64_t k = k0 + (p == 1 ? kPiece >> 4 : 0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i < ks)
+            mma_ts(d, q + i * 8, k + (uint64_t)((i >> 2) * 1024 + (i & 3) * 2), id_s, p + i > 0);
       }
       commit(&sh.k_empty);
       commit(&sh.s_full[n_s & 1]);
@@ -336,19 +433,20 @@ __device__ void mma_role(const TileArgs& a, Shared& sh, unsigned char* sm, uint3
     for (int j = 0; j < nt && ok; ++j) {
       const uint32_t b = n_o & 1, ph = (n_o >> 1) & 1;
       ok = bar_wait(&sh.v_full, n_o & 1, ab) && bar_wait(&sh.p_full[b], ph, ab) &&
-           bar_wait(&sh.o_empty[b], ph ^ 1, ab);
+           bar_wait(&sh.o_empty, (n_o & 1) ^ 1, ab);
       if (!ok) break;
       fence_after();
-      const uint32_t s = tmem + b * 128, o = tmem + 256 + b * 128;
+      const uint32_t w0 = tmem + kColS + b * 128, o = tmem + kColO;
 #pragma unroll 1
       for (int p = 0; p < 3; ++p) {
-        const uint32_t v = v0 + (p == 1 ? kPiece : 0), w = s + (p == 0 ? 8 : 0);
+        const uint64_t v = v0 + (p == 1 ? kPiece >> 4 : 0);
+        const uint32_t w = w0 + (p == 0 ? 8 : 0);
+#pragma unroll
         for (int i = 0; i < kTileN / 16; ++i)
-          mma_ts(o, w + i * 16, desc128(v + i * 2048, 16384, 1024), id_o,
-                 p + i > 0);
+          mma_ts(o, w + i * 16, v + (uint64_t)(i * 128), id_o, p + i > 0);
       }
       commit(&sh.v_empty);
-      commit(&sh.o_full[b]);
+      commit(&sh.o_full);
       ++n_o;
       if (j + 2 < nt) ok = scores(j + 3 == nt);
     }
@@ -409,13 +507,13 @@ __device__ void row_role(const TileArgs& a, Shared& sh, uint32_t tmem, int row, 
     for (int c = 0; c < 128; ++c) acc[c] = 0.f;
     // acc += O of the last tile.
     auto fold = [&](uint32_t t) {
-      if (!bar_wait_warp(&sh.o_full[t & 1], (t >> 1) & 1, ab)) return false;
+      if (!bar_wait_warp(&sh.o_full, t & 1, ab)) return false;
       fence_after();
 #pragma unroll
       for (int c = 0; c < 128; c += 32)
         if (c < a.dv) {
           uint32_t o[32];
-          ld32(at + 256 + (t & 1) * 128 + c, o);
+          ld32(at + kColO + c, o);
           wait_ld();
           pin32(o);
 #pragma unroll
@@ -426,7 +524,7 @@ __device__ void row_role(const TileArgs& a, Shared& sh, uint32_t tmem, int row, 
         }
       fence_before();
       __syncwarp();
-      if (lane == 0) bar_arrive(&sh.o_empty[t & 1]);
+      if (lane == 0) bar_arrive(&sh.o_empty);
       return true;
     };
     for (int j = 0; j < nt; ++j, ++n) {
@@ -434,8 +532,8 @@ __device__ void row_role(const TileArgs& a, Shared& sh, uint32_t tmem, int row, 
       if (!bar_wait_warp(&sh.s_full[b], ph, ab)) return;
       if (!bar_wait_warp(&sh.x_full[b], ph, ab)) return;
       fence_after();
-      if (j == 0) qm = sh.q_mul[nq & 1][row >> 4] * sc;
-      const uint32_t s_at = at + b * 128;
+      if (j == 0) qm = sh.q_mul[nq & 1][row] * sc;
+      const uint32_t s_at = at + kColS + b * 128;
       const float* km = sh.k_mul[n & 3];
       const float* ve = sh.v_exp[n & 3];
       const float* vi = sh.v_inv[n & 3];
@@ -581,13 +679,15 @@ template <int N>
 __device__ __forceinline__ void fewer_regs() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
-// The launch holds 512 x 128 registers; the shares are 128 x 208 + 256 x 120 +
-// 128 x 64 = those 65,536.
-constexpr int kRegsRow = 208, kRegsConvert = 120, kRegsRest = 64;
+// The launch holds 512 x 128 registers; the shares are 128 x 208 + 256 x 112 +
+// 128 x 80 = those 65,536.
+constexpr int kRegsRow = 208, kRegsConvert = 112, kRegsRest = 80;
 static_assert(128 * kRegsRow + 256 * kRegsConvert + 128 * kRegsRest <= 512 * 128, "registers");
 
 template <bool PAGED>
-__global__ void __launch_bounds__(kThreads, 1) attn_tc32_kernel(const __grid_constant__ TileArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) 
+attn_tc32_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CUtensorMap mk,
+                 const __grid_constant__ CUtensorMap mv) {
   extern __shared__ __align__(1024) unsigned char sm[];
   Shared& sh = *reinterpret_cast<Shared*>(sm + kTiles);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -601,13 +701,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc32_kernel(const __grid_con
     for (int i = 0; i < 2; ++i) {
       bar_init(&sh.s_full[i], 1);
       bar_init(&sh.p_full[i], 4);
-      bar_init(&sh.o_full[i], 1);
-      bar_init(&sh.o_empty[i], 4);
       bar_init(&sh.x_full[i], kConv);
+    }
+    bar_init(&sh.o_full, 1);
+    bar_init(&sh.o_empty, 4);
+    for (int i = 0; i < kStages; ++i) {
+      bar_init(&sh.st_full[i], 1);
+      bar_init(&sh.st_empty[i], kConv / 2);
     }
     for (int i = 0; i < kUnitRing; ++i) {
       bar_init(&sh.u_full[i], 1);
-      bar_init(&sh.u_empty[i], 4 + kConv + 1);  // softmax, converting and product warps
+      bar_init(&sh.u_empty[i], 4 + kConv + 2);  // softmax, converting, product, load warps
     }
     bar_init(&sh.drain, 1);
     bar_init_fence();
@@ -623,13 +727,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc32_kernel(const __grid_con
     row_role<PAGED>(a, sh, tmem, tid, lane);
   } else if (warp < 12) {
     fewer_regs<kRegsConvert>();
-    convert_role<PAGED>(a, sh, sm, warp - 4, lane);
+    convert_role(a, sh, sm, tmem, warp, lane);
   } else {
     fewer_regs<kRegsRest>();
     if (warp == 12) {
       if (elect_one()) mma_role(a, sh, sm, tmem);
     } else if (warp == 13) {
       unit_role(a, sh, lane);
+    } else if (warp == 14) {
+      if (elect_one()) load_role<PAGED>(a, &mk, &mv, sh, sm);
     }
   }
   __syncwarp();
@@ -643,18 +749,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc32_kernel(const __grid_con
 }
 
 template <bool PAGED>
-cudaError_t launch_t(const TileArgs& a, unsigned grid, cudaStream_t stream) {
+cudaError_t launch_t(const TileArgs& a, const TileMaps& m, unsigned grid, cudaStream_t stream) {
   static const cudaError_t ready = cudaFuncSetAttribute(
       attn_tc32_kernel<PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (ready != cudaSuccess) return ready;
-  attn_tc32_kernel<PAGED><<<grid, kThreads, kSmem, stream>>>(a);
+  attn_tc32_kernel<PAGED><<<grid, kThreads, kSmem, stream>>>(a, m.k, m.v);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_attn_tc32(const TileArgs& a, unsigned grid, cudaStream_t stream) {
-  return a.pages ? launch_t<true>(a, grid, stream) : launch_t<false>(a, grid, stream);
+cudaError_t launch_attn_tc32(const TileArgs& a, const TileMaps& m, unsigned grid,
+                             cudaStream_t stream) {
+  return a.pages ? launch_t<true>(a, m, grid, stream) : launch_t<false>(a, m, grid, stream);
 }
 
 }  // namespace nys
