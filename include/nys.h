@@ -417,10 +417,13 @@ enum {
 };
 
 /* Bytes of device workspace that nys_attn_prompt (n sequences, `rows` query
- * rows in all) and nys_attn_shared (n requests, rows = n) use on this geometry
- * to split long key ranges over more CTAs.  Host arithmetic only.  0 is a
- * possible answer.  Errors: NYS_E_INVAL, NYS_E_UNSUPPORTED. */
-int nys_attn_workspace_bytes(const nys_attn_config* cfg, int64_t n, int64_t rows, size_t* bytes);
+ * rows and `keys` key rows in all) and nys_attn_shared (n requests, rows = n, a
+ * prefix of `keys`) use on this geometry: f32 keys and values as pieces for the
+ * tensor cores, and results of key ranges that are split over CTAs.  Host
+ * arithmetic only.  0 is a possible answer.  Errors: NYS_E_INVAL,
+ * NYS_E_UNSUPPORTED. */
+int nys_attn_workspace_bytes(const nys_attn_config* cfg, int64_t n, int64_t rows, int64_t keys,
+                             size_t* bytes);
 
 /* Causal attention over packed prompts.  Sequence i's queries are rows
  * q_off[i] .. q_off[i+1]-1 of q, its keys and values rows k_off[i] ..
@@ -433,8 +436,8 @@ int nys_attn_workspace_bytes(const nys_attn_config* cfg, int64_t n, int64_t rows
  * strides; lse, if not NULL, fp32 [q_rows][heads], receives the log of the
  * softmax's denominator.  Values of keys that a row does not see never reach
  * it, whatever they are.
- * workspace: nys_attn_workspace_bytes(cfg, n, q_rows) bytes, 256-byte aligned
- * (smaller or NULL is allowed and means no splitting).
+ * workspace: nys_attn_workspace_bytes(cfg, n, q_rows, k_rows) bytes, 256-byte
+ * aligned.  Less or NULL is allowed: f32 then takes the general kernel.
  * Errors: NYS_E_INVAL, NYS_E_UNSUPPORTED, NYS_E_ALIGN (workspace), NYS_E_CUDA. */
 int nys_attn_prompt(const nys_attn_config* cfg, int64_t n, int64_t q_rows, int64_t k_rows,
                     const int32_t* q_off, const int32_t* k_off, const nys_rows* q,
@@ -449,7 +452,7 @@ int nys_attn_prompt(const nys_attn_config* cfg, int64_t n, int64_t q_rows, int64
  * plain paged decode.  A request without keys gets 0 (lse -INF).  prefix_pages
  * (int32), lens (int32 [n]) and table (int32 [n][width]) are device arrays;
  * entries past a length are not read.  lse, if not NULL, fp32 [n][heads].
- * workspace: nys_attn_workspace_bytes(cfg, n, n) bytes, 256-byte aligned;
+ * workspace: nys_attn_workspace_bytes(cfg, n, n, prefix_len) bytes, 256-byte aligned;
  * less is NYS_E_BUF.
  * Errors: NYS_E_INVAL, NYS_E_UNSUPPORTED, NYS_E_BUF, NYS_E_ALIGN, NYS_E_CUDA. */
 int nys_attn_shared(const nys_attn_config* cfg, int64_t n, const nys_pool* pool,

@@ -55,11 +55,16 @@ bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(
 
 extern "C" {
 
-int nys_attn_workspace_bytes(const nys_attn_config* cfg, int64_t n, int64_t rows, size_t* bytes) {
+int nys_attn_workspace_bytes(const nys_attn_config* cfg, int64_t n, int64_t rows, int64_t keys,
+                             size_t* bytes) {
   const int rc = check_attn(cfg);
   if (rc) return rc;
-  if (!bytes || n < 0 || rows < 0 || n > INT32_MAX || rows > INT32_MAX) return NYS_E_INVAL;
-  *bytes = nys::attn_workspace(*cfg, n, rows);
+  if (!bytes || n < 0 || rows < 0 || keys < 0 || n > INT32_MAX || rows > INT32_MAX ||
+      keys > INT32_MAX)
+    return NYS_E_INVAL;
+  const size_t p = nys::prompt_workspace(*cfg, n, rows, keys);
+  const size_t s = rows == n ? nys::shared_workspace(*cfg, n, keys) : 0;
+  *bytes = p > s ? p : s;
   return NYS_OK;
 }
 
@@ -102,8 +107,10 @@ int nys_attn_prompt(const nys_attn_config* cfg, int64_t n, int64_t q_rows, int64
   a.scale = scale_of(*cfg);
   a.status = status;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e =
-      nys::prompt_tc_fits(a) ? nys::launch_prompt_tc(a, s) : nys::launch_prompt_general(a, s);
+  const bool room = workspace && workspace_bytes >= nys::prompt_workspace(*cfg, n, q_rows, k_rows);
+  const cudaError_t e = nys::prompt_tc_fits(a) && (room || cfg->dtype != NYS_F32)
+                            ? nys::launch_prompt_tc(a, workspace, s)
+                            : nys::launch_prompt_general(a, s);
   return e == cudaSuccess ? NYS_OK : NYS_E_CUDA;
 }
 
@@ -125,7 +132,7 @@ int nys_attn_shared(const nys_attn_config* cfg, int64_t n, const nys_pool* pool,
   if (!lens || (width > 0 && !table) || (prefix_len > 0 && !prefix_pages)) return NYS_E_INVAL;
   if ((int64_t)width * pool->page > INT32_MAX) return NYS_E_UNSUPPORTED;
   size_t need = 0;
-  if ((rc = nys_attn_workspace_bytes(cfg, n, n, &need))) return rc;
+  if ((rc = nys_attn_workspace_bytes(cfg, n, n, prefix_len, &need))) return rc;
   if (need > 0 && (!workspace || workspace_bytes < need)) return NYS_E_BUF;
   nys::SharedArgs a{};
   a.q = rows_of(q);

@@ -27,28 +27,23 @@ EncodeTiled encoder() {
   return fn;
 }
 
-// Map of a [rows][heads][dim] tensor; boxes of `box_h` heads and `box_r` rows
-// of 64 columns with the 128-byte swizzle (16-bit types), or of 128 columns as
-// they are (f32).  Strides in elements; those of extents of one are not used
-// and replaced by valid ones.
+// Map of a [rows][heads][dim] tensor of 16-bit elements; boxes of 64 columns,
+// `box_h` heads and `box_r` rows, 128-byte swizzle.  Strides in elements; those
+// of extents of one are not used and replaced by valid ones.
 bool make_map(CUtensorMap* m, int dtype, const void* p, int64_t rows, int64_t heads, int64_t dim,
               int64_t row, int64_t head, int box_h, int box_r) {
-  const bool f32 = dtype == NYS_F32;
-  const int64_t es = f32 ? 4 : 2;
   const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)rows};
-  const cuuint64_t line = (cuuint64_t)((dim * es + 15) & ~int64_t(15));
-  const cuuint64_t st[2] = {heads > 1 ? (cuuint64_t)(head * es) : line,
-                            rows > 1 ? (cuuint64_t)(row * es) : line * (cuuint64_t)heads};
-  const cuuint32_t box[3] = {f32 ? 128u : 64u, (cuuint32_t)box_h, (cuuint32_t)box_r};
+  const cuuint64_t line = (cuuint64_t)((dim * 2 + 15) & ~int64_t(15));
+  const cuuint64_t st[2] = {heads > 1 ? (cuuint64_t)head * 2 : line,
+                            rows > 1 ? (cuuint64_t)row * 2 : line * (cuuint64_t)heads};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_h, (cuuint32_t)box_r};
   const cuuint32_t one[3] = {1, 1, 1};
-  const CUtensorMapDataType type = f32                  ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                                   : dtype == NYS_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const EncodeTiled enc = encoder();
-  return enc && enc(m, type, 3, const_cast<void*>(p), dims, st, box, one,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    f32 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  return enc && enc(m,
+                    dtype == NYS_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                      : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                    3, const_cast<void*>(p), dims, st, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -103,14 +98,47 @@ int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
 }  // namespace
 
-size_t attn_workspace(const nys_attn_config& c, int64_t n, int64_t rows) {
+namespace {
+
+// The f32 images' part of a workspace: K, V, exponents, flags.
+struct Images {
+  size_t v, exps, odd, end;
+};
+Images images_of(int kv_heads, int d, int dv, int64_t n, int64_t keys) {
+  const size_t count = (size_t)key_tiles(keys, n) * kv_heads;
+  Images im;
+  im.v = count * 2 * (size_t)((d + 63) / 64) * 16384;
+  im.exps = im.v + count * 2 * (size_t)((dv + 63) / 64) * 16384;
+  im.odd = im.exps + count * sizeof(TileExps);
+  im.end = (im.odd + count * 8 * sizeof(int32_t) + 255) & ~size_t(255);
+  return im;
+}
+void place_images(TileArgs& a, void* workspace, int64_t n, int64_t keys) {
+  unsigned char* w = static_cast<unsigned char*>(workspace);
+  const Images im = images_of(a.kv_heads, a.d, a.dv, n, keys);
+  a.k_image = w;
+  a.v_image = w + im.v;
+  a.exps = reinterpret_cast<TileExps*>(w + im.exps);
+  a.odd = reinterpret_cast<int32_t*>(w + im.odd);
+}
+
+}  // namespace
+
+size_t prompt_workspace(const nys_attn_config& c, int64_t n, int64_t rows, int64_t keys) {
   (void)rows;
+  if (n == 0 || keys == 0 || c.d > 128 || c.dv > 128 || c.dtype != NYS_F32) return 0;
+  return images_of(c.kv_heads, c.d, c.dv, n, keys).end;
+}
+
+size_t shared_workspace(const nys_attn_config& c, int64_t n, int64_t keys) {
   if (n == 0 || c.d > 128 || c.dv > 128) return 0;
   const int group = c.heads / c.kv_heads;
   const int64_t pieces =
       most_prefix_pieces(n, c.kv_heads, group, c.dtype) + most_own_pieces(n, c.kv_heads);
-  const size_t row = (size_t)n * c.heads;
-  return (size_t)pieces * row * ((size_t)c.dv + 1) * 4 + 256;
+  const size_t parts = (size_t)pieces * n * c.heads * ((size_t)c.dv + 1) * 4;
+  const size_t images =
+      c.dtype == NYS_F32 && keys > 0 ? images_of(c.kv_heads, c.d, c.dv, 1, keys).end : 0;
+  return images + parts;
 }
 
 bool shared_tiled_fits(const SharedArgs& a) {
@@ -133,7 +161,10 @@ cudaError_t launch_shared_tiled(const SharedArgs& s, void* workspace, cudaStream
   const int64_t cap = (int64_t)s.width * s.page;
   o.pieces = clamp_int(div_up(cap, 256), 1, most_own_pieces(s.n, s.kv_heads));
   const int64_t pieces = o.prefix_pieces + (o.pieces > 1 ? o.pieces : 0);
-  o.part = static_cast<float*>(workspace);
+  const size_t images = s.dtype == NYS_F32 && s.prefix_len > 0
+                            ? images_of(s.kv_heads, s.d, s.dv, 1, s.prefix_len).end
+                            : 0;
+  o.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + images);
   o.part_lse = o.part + pieces * row * s.dv;
   if (o.prefix_pieces > 0) {
     TileArgs a{};
@@ -165,17 +196,20 @@ cudaError_t launch_shared_tiled(const SharedArgs& s, void* workspace, cudaStream
     a.per = s.dtype == NYS_F32 ? 1 : 2;
     const int64_t all = units * o.prefix_pieces;
     const unsigned grid = (unsigned)(all < kSms ? all : kSms);
-    const bool f32 = s.dtype == NYS_F32;
-    a.box = gcd(s.page, f32 ? kTileN / 2 : kTileN);
-    const int64_t slots = s.n_pages * s.page;
-    TileMaps m;
-    if ((!f32 &&
-         !make_map(&m.q, s.dtype, s.q.p, s.n, s.heads, s.d, s.q.row, s.q.head, s.group, a.tp)) ||
-        !make_map(&m.k, s.dtype, s.k, slots, s.kv_heads, s.d, a.k_row, a.k_head, 1, a.box) ||
-        !make_map(&m.v, s.dtype, s.v, slots, s.kv_heads, s.dv, a.v_row, a.v_head, 1, a.box))
-      return cudaErrorInvalidValue;
-    const cudaError_t e = f32 ? launch_attn_tc32(a, m, grid, stream)
-                              : launch_attn_tc(a, m, s.dtype, grid, stream);
+    cudaError_t e;
+    if (s.dtype == NYS_F32) {
+      place_images(a, workspace, 1, s.prefix_len);
+      e = launch_attn_tc32(a, grid, stream);
+    } else {
+      a.box = gcd(s.page, kTileN);
+      const int64_t slots = s.n_pages * s.page;
+      TileMaps m;
+      if (!make_map(&m.q, s.dtype, s.q.p, s.n, s.heads, s.d, s.q.row, s.q.head, s.group, a.tp) ||
+          !make_map(&m.k, s.dtype, s.k, slots, s.kv_heads, s.d, a.k_row, a.k_head, 1, a.box) ||
+          !make_map(&m.v, s.dtype, s.v, slots, s.kv_heads, s.dv, a.v_row, a.v_head, 1, a.box))
+        return cudaErrorInvalidValue;
+      e = launch_attn_tc(a, m, s.dtype, grid, stream);
+    }
     if (e != cudaSuccess) return e;
   }
   const cudaError_t e = launch_own(s, o, stream);
@@ -196,7 +230,7 @@ bool prompt_tc_fits(const PromptArgs& a) {
          tileable(a.out, a.q_rows, a.heads, elem, false);
 }
 
-cudaError_t launch_prompt_tc(const PromptArgs& p, cudaStream_t stream) {
+cudaError_t launch_prompt_tc(const PromptArgs& p, void* workspace, cudaStream_t stream) {
   TileArgs a{};
   a.q_off = p.q_off;
   a.k_off = p.k_off;
@@ -226,16 +260,16 @@ cudaError_t launch_prompt_tc(const PromptArgs& p, cudaStream_t stream) {
   // At most this many units: a partial one a sequence on top of the full ones.
   const int64_t most = (p.q_rows / (a.per * a.tp) + p.n) * p.kv_heads;
   const unsigned grid = (unsigned)(most < kSms ? most : kSms);
+  if (p.dtype == NYS_F32) {
+    place_images(a, workspace, p.n, p.k_rows);
+    return launch_attn_tc32(a, grid, stream);
+  }
   TileMaps m;
-  const bool f32 = p.dtype == NYS_F32;
   const int64_t kvh = a.kv_y ? p.kv_heads : 1;
-  const int box = f32 ? kTileN / 2 : kTileN;
-  if ((!f32 && !make_map(&m.q, p.dtype, p.q.p, p.q_rows, p.heads, p.d, p.q.row, p.q.head, p.group,
-                         a.tp)) ||
-      !make_map(&m.k, p.dtype, p.k.p, p.k_rows, kvh, p.d, p.k.row, p.k.head, 1, box) ||
-      !make_map(&m.v, p.dtype, p.v.p, p.k_rows, kvh, p.dv, p.v.row, p.v.head, 1, box))
+  if (!make_map(&m.q, p.dtype, p.q.p, p.q_rows, p.heads, p.d, p.q.row, p.q.head, p.group, a.tp) ||
+      !make_map(&m.k, p.dtype, p.k.p, p.k_rows, kvh, p.d, p.k.row, p.k.head, 1, kTileN) ||
+      !make_map(&m.v, p.dtype, p.v.p, p.k_rows, kvh, p.dv, p.v.row, p.v.head, 1, kTileN))
     return cudaErrorInvalidValue;
-  if (f32) return launch_attn_tc32(a, m, grid, stream);
   return launch_attn_tc(a, m, p.dtype, grid, stream);
 }
 

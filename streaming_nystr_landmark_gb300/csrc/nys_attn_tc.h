@@ -11,6 +11,20 @@ constexpr int kTileM = 128;  // rows of a query tile: (position, head of the gro
 constexpr int kTileN = 128;  // keys of a tile
 constexpr int kUnitRing = 4;
 
+// Exponents of one f32 tile of one KV head, for each group of 16 keys: keys are
+// stored as k 2^-ek (k_mul = 2^ek), values as v 2^-ev.
+struct TileExps {
+  float k_mul[8];
+  int32_t v_exp[8];
+};
+
+// Where the tiles of sequence i, whose first key row is k0, begin among all
+// tiles: no sequence's tiles reach the next one's, and no sum over the
+// sequences is needed.
+__host__ __device__ constexpr int seq_tile(int k0, int i) { return k0 / kTileN + i; }
+// Room for all tiles.
+constexpr int64_t key_tiles(int64_t k_rows, int64_t n) { return k_rows / kTileN + n; }
+
 // One batch of a tiled launch.  Causal prompts: q_off and k_off give the
 // sequences.  Prefix of a shared batch (q_off null): one sequence of n_rows
 // query positions, every one of which sees all n_keys keys.
@@ -31,6 +45,10 @@ struct TileArgs {
   const int32_t* pages;
   int32_t page, box;
   int64_t n_pages;
+  // f32: K and V as pieces, tile by tile (nys_attn_tc32.cu).
+  unsigned char *k_image, *v_image;
+  TileExps* exps;
+  int32_t* odd;  // [tile][KV head][group]: holds values that are not finite
   // Values and keys for the checks of unusual values, and the pages' own rows.
   const void *k_raw, *v_raw;
   int64_t k_row, k_head, v_row, v_head;
@@ -54,8 +72,8 @@ struct Unit {
   int32_t nkl;      // keys the piece ends before
   int32_t split;
   int32_t edge;     // first key tile in which some row does not see some key
-  int32_t patch;    // set where such a tile holds a value that is not finite
-  int32_t pad[2];
+  int32_t patch;    // set where the epilogue has to add values that are not finite
+  int32_t tile;     // number of the piece's first key tile among all (f32)
 };
 
 struct TileMaps {
@@ -77,8 +95,11 @@ struct JoinArgs {
   float* lse;
 };
 
-// Workspace of the tiled kernels for n requests or `rows` query rows.
-size_t attn_workspace(const nys_attn_config& c, int64_t n, int64_t rows);
+// Workspace of the tiled kernels: nys_attn_prompt with n sequences of `rows` query
+// rows and `keys` key rows in all; nys_attn_shared with n requests and a prefix of
+// `keys`.
+size_t prompt_workspace(const nys_attn_config& c, int64_t n, int64_t rows, int64_t keys);
+size_t shared_workspace(const nys_attn_config& c, int64_t n, int64_t keys);
 bool shared_tiled_fits(const SharedArgs& a);
 cudaError_t launch_shared_tiled(const SharedArgs& a, void* workspace, cudaStream_t stream);
 cudaError_t launch_own(const SharedArgs& a, const OwnArgs& o, cudaStream_t stream);
@@ -86,12 +107,12 @@ cudaError_t launch_join(const JoinArgs& a, int dtype, cudaStream_t stream);
 
 // Whether the tiled kernels take a prompt batch, and its launch.
 bool prompt_tc_fits(const PromptArgs& a);
-cudaError_t launch_prompt_tc(const PromptArgs& a, cudaStream_t stream);
+cudaError_t launch_prompt_tc(const PromptArgs& a, void* workspace, cudaStream_t stream);
 cudaError_t launch_attn_tc(const TileArgs& a, const TileMaps& m, int dtype, unsigned grid,
                            cudaStream_t stream);
 
-cudaError_t launch_attn_tc32(const TileArgs& a, const TileMaps& m, unsigned grid,
-                             cudaStream_t stream);  // (no q map)
+cudaError_t launch_attn_tc32(const TileArgs& a, unsigned grid, cudaStream_t stream);
+
 
 #ifdef __CUDACC__
 // Walks the launch's units in order; one warp.  Within a sequence the query
@@ -156,6 +177,7 @@ struct UnitWalk {
     u.np1 = a.per == 2 ? min(max(left - a.tp, 0), a.tp) : 0;
     u.q_row = sq0 + p0;
     u.k_row = sk0;
+    u.tile = seq_tile(sk0, s0 + src);
     // Keys that the first position sees, and the last of each tile.
     u.lim = a.causal ? p0 + 1 + snk - snq : snk;
     const int e0 = a.causal ? u.lim + u.np0 - 1 : snk;
@@ -164,6 +186,7 @@ struct UnitWalk {
     const int t1 = (min(max(e1, 0), snk) + kTileN - 1) / kTileN;  // t1 >= t0
     const int tb = (int)((int64_t)t1 * u.split / ns), te = (int)((int64_t)t1 * (u.split + 1) / ns);
     u.kb = tb * kTileN;
+    u.tile += tb;
     u.nt = te - tb;
     u.nt0 = min(max(t0 - tb, 0), u.nt);
     u.nkl = min(snk, te * kTileN);

@@ -122,7 +122,7 @@ def _load():
         "nys_o1_free": [VP],
         "nys_debug_stall_once": [VP, I32],
         "nys_debug_stall_replay_once": [VP],
-        "nys_attn_workspace_bytes": [P(NysAttnConfig), I64, I64, P(ctypes.c_size_t)],
+        "nys_attn_workspace_bytes": [P(NysAttnConfig), I64, I64, I64, P(ctypes.c_size_t)],
         "nys_attn_prompt": [P(NysAttnConfig), I64, I64, I64, VP, VP, P(NysRows), P(NysRows),
                             P(NysRows), P(NysRows), VP, VP, ctypes.c_size_t, VP, VP],
         "nys_attn_shared": [P(NysAttnConfig), I64, P(NysPool), VP, I32, VP, VP, I32,
@@ -242,9 +242,9 @@ def nys_config_of(handle):
     return cfg, n.value
 
 
-def nys_attn_workspace_bytes(cfg: NysAttnConfig, n: int, rows: int) -> int:
+def nys_attn_workspace_bytes(cfg: NysAttnConfig, n: int, rows: int, keys: int = 0) -> int:
     out = ctypes.c_size_t(0)
-    _check(_lib.nys_attn_workspace_bytes(ctypes.byref(cfg), n, rows, ctypes.byref(out)),
+    _check(_lib.nys_attn_workspace_bytes(ctypes.byref(cfg), n, rows, keys, ctypes.byref(out)),
            "nys_attn_workspace_bytes")
     return out.value
 
@@ -683,20 +683,17 @@ class ExactAttention(_Status):
         self.cfg = NysAttnConfig(heads, kv_heads, d, dv, _dtype_code(self.dtype),
                                  0.0 if scale is None else scale)
         self._init_status(torch, self.device)
-        self._sizes = {}
         self._work = None
         self._work_ptr = None
+        self._work_bytes = 0
         nys_attn_workspace_bytes(self.cfg, 0, 0)   # refuses a bad geometry here
 
-    def _workspace(self, n, rows):
-        """(address, bytes) of a workspace for n sequences of `rows` rows."""
-        need = self._sizes.get((n, rows))
-        if need is None:
-            need = self._sizes[(n, rows)] = nys_attn_workspace_bytes(self.cfg, n, rows)
-        if need > 0 and (self._work is None or self._work.numel() < need):
+    def _workspace(self, n, rows, keys):
+        """Makes the workspace large enough for a call of these sizes."""
+        need = nys_attn_workspace_bytes(self.cfg, n, rows, keys)
+        if need > self._work_bytes:
             self._work = self.torch.empty(need, dtype=self.torch.uint8, device=self.device)
-            self._work_ptr = self._work.data_ptr()
-        return self._work_ptr, need
+            self._work_ptr, self._work_bytes = self._work.data_ptr(), need
 
     def prompt(self, q, k, v, q_off, out, k_off=None, lse=None):
         """Packed causal attention (nys_attn_prompt): q [rows][heads][d], k and
@@ -706,7 +703,7 @@ class ExactAttention(_Status):
         n, rows, keys = q_off.shape[0] - 1, q.shape[0], k.shape[0]
         if v.shape[0] != keys or out.shape[0] != rows:
             raise ValueError("k and v, and q and out, must have as many rows as each other")
-        ws, ws_bytes = self._workspace(n, rows)
+        self._workspace(n, rows, keys)
         nys_attn_prompt(
             self.cfg, n, rows, keys, _ints(q_off, torch.int32, (None,), "q_off"),
             None if k_off is None else _ints(k_off, torch.int32, (n + 1,), "k_off"),
@@ -715,7 +712,7 @@ class ExactAttention(_Status):
             _rows(v, self.dtype, self.kv_heads, self.dv, "v"),
             _rows(out, self.dtype, self.heads, self.dv, "out"),
             None if lse is None else _ptr(lse, torch.float32, (rows, self.heads), "lse"),
-            ws, ws_bytes, self._status_ptr,
+            self._work_ptr, self._work_bytes, self._status_ptr,
             torch.cuda.current_stream(self.device).cuda_stream)
         return out
 
@@ -735,7 +732,7 @@ class ExactAttention(_Status):
             pages = _ints(prefix_pages, torch.int32, (None,), "prefix_pages")
             if prefix_pages.shape[0] * cache.page < prefix_len:
                 raise ValueError("prefix_pages: too few pages for prefix_len")
-        ws, ws_bytes = self._workspace(n, n)
+        self._workspace(n, n, prefix_len)
         nys_attn_shared(
             self.cfg, n, cache._pool, pages, prefix_len,
             _ints(lens, torch.int32, (n,), "lens"),
@@ -743,6 +740,6 @@ class ExactAttention(_Status):
             _rows(q, self.dtype, self.heads, self.d, "q"),
             _rows(out, self.dtype, self.heads, self.dv, "out"),
             None if lse is None else _ptr(lse, torch.float32, (n, self.heads), "lse"),
-            ws, ws_bytes, self._status_ptr,
+            self._work_ptr, self._work_bytes, self._status_ptr,
             torch.cuda.current_stream(self.device).cuda_stream)
         return out

@@ -44,11 +44,12 @@ def test_bad_geometry(kw, code):
 def test_workspace_sizes():
     c = cfg()
     assert nys.nys_attn_workspace_bytes(c, 0, 0) >= 0
-    for n, r in ((-1, 0), (0, -1), (1 << 31, 1), (1, 1 << 31)):
+    for n, r, k in ((-1, 0, 0), (0, -1, 0), (1 << 31, 1, 1), (1, 1 << 31, 1), (1, 1, -1),
+                    (1, 1, 1 << 31)):
         with pytest.raises(nys.NysError):
-            nys.nys_attn_workspace_bytes(c, n, r)
-    assert nys._lib.nys_attn_workspace_bytes(c, 1, 1, None) == nys.NYS_E_INVAL
-    assert nys._lib.nys_attn_workspace_bytes(None, 1, 1, None) == nys.NYS_E_INVAL
+            nys.nys_attn_workspace_bytes(c, n, r, k)
+    assert nys._lib.nys_attn_workspace_bytes(c, 1, 1, 1, None) == nys.NYS_E_INVAL
+    assert nys._lib.nys_attn_workspace_bytes(None, 1, 1, 1, None) == nys.NYS_E_INVAL
 
 
 def _prompt(**kw):
@@ -102,7 +103,7 @@ def test_shared_refusals(kw, code):
 
 
 def test_shared_workspace_too_small():
-    need = nys.nys_attn_workspace_bytes(cfg(), 2, 2)
+    need = nys.nys_attn_workspace_bytes(cfg(), 2, 2, 20)
     if need:
         assert _shared(ws=None, wb=0) == nys.NYS_E_BUF
         assert _shared(wb=need - 1) == nys.NYS_E_BUF
