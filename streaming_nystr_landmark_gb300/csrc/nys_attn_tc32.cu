@@ -57,7 +57,12 @@ constexpr int kGroups = kTileN / kGroup;
 constexpr int kSlots = 3;
 constexpr uint32_t kPiece = 32768;
 constexpr uint32_t kSlotBytes = 2 * kPiece;
-constexpr uint32_t kTiles = kSlots * kSlotBytes;
+// Each softmax and query warp moves its 32 rows between global memory (whole
+// sectors, 16 columns of 8 rows an instruction) and "thread = row" through a
+// buffer of its own: 16 columns, rows 80 bytes apart, free of bank conflicts.
+constexpr uint32_t kTurnRow = 80, kTurn = 32 * kTurnRow;
+constexpr uint32_t kOffTurn = kSlots * kSlotBytes;
+constexpr uint32_t kTiles = kOffTurn + 12 * kTurn;
 constexpr uint32_t kColQ = 0, kColS = 128, kColO = 384;  // tensor memory
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -194,60 +199,90 @@ __device__ __forceinline__ float finite_max(float4 x) {
   return f;
 }
 
-// The query tile into tensor memory (four warps, thread = row).  Rows past the
-// tile's positions stand for its last one: their results are not stored.
-__device__ void query_role(const TileArgs& a, Shared& sh, uint32_t tmem, int row, int lane) {
+// The query tile into tensor memory (four warps, 32 rows each; a lane loads 16
+// bytes of rows lane / 4 + 8 i, then takes row `lane` for the conversion).  Rows
+// past the tile's positions stand for its last one: their results are not
+// stored.
+__device__ void query_role(const TileArgs& a, Shared& sh, unsigned char* turn, uint32_t tmem,
+                           int warp, int lane) {
   volatile int* ab = &sh.abort;
-  const int pos = row / a.group, hd = row - pos * a.group;
-  const uint32_t at = tmem + ((uint32_t)(row & ~31) << 16) + kColQ;
+  const uint32_t at = tmem + ((uint32_t)(warp * 32) << 16) + kColQ;
+  const int sub = lane & 3;  // 4 columns of a chunk of 16
+  int pos[4], hd[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = warp * 32 + i * 8 + (lane >> 2);
+    pos[i] = r / a.group;
+    hd[i] = r - pos[i] * a.group;
+  }
   uint32_t n_q = 0;
   for (uint32_t nu = 0;; ++nu) {
     if (!bar_wait_warp(&sh.u_full[nu % kUnitRing], (nu / kUnitRing) & 1, ab)) return;
     const Unit& u = sh.unit[nu % kUnitRing];
     if (!u.valid) return;
     if (u.nt > 0) {
-      const float* src = (const float*)a.q.p + (u.q_row + (int64_t)min(pos, u.np0 - 1)) * a.q.row +
-                         (int64_t)(u.kvh * a.group + hd) * a.q.head;
-      float t = 0.f;
-#pragma unroll 16
-      for (int c = 0; c < 128; c += 4)
-        if (c < a.d) {
-          const float4 z = __ldg(reinterpret_cast<const float4*>(src + c));
-          t = max3_abs_nan(t, z.x, z.y);
-          t = max3_abs_nan(t, z.z, z.w);
-        }
-      uint32_t top = __float_as_uint(t) & 0x7FFFFFFFu;
-      const bool odd = __any_sync(0xffffffffu, top >= 0x7F800000u);
-      if (odd && top >= 0x7F800000u) {
-        float f = 0.f;
-        for (int c = 0; c < a.d; c += 4)
-          f = fmaxf(f, finite_max(*reinterpret_cast<const float4*>(src + c)));
-        top = __float_as_uint(f);
+      // The whole tile at once, 32 loads a lane.
+      float4 x[32];
+      const float* src[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        src[i] = (const float*)a.q.p + (u.q_row + (int64_t)min(pos[i], u.np0 - 1)) * a.q.row +
+                 (int64_t)(u.kvh * a.group + hd[i]) * a.q.head + sub * 4;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          x[c * 4 + i] = c * 16 + sub * 4 < a.d ? __ldg(reinterpret_cast<const float4*>(src[i] + c * 16))
+                                                : make_float4(0.f, 0.f, 0.f, 0.f);
       }
-      const int ex = top_exponent(top);
-      sh.q_exp[n_q & 1][row] = (int8_t)(ex - 127 - kTop);
-      const float scale = scale_of(ex);
+      // The rows' exponents.
+      bool odd = false;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float t = 0.f;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          t = max3_abs_nan(t, x[c * 4 + i].x, x[c * 4 + i].y);
+          t = max3_abs_nan(t, x[c * 4 + i].z, x[c * 4 + i].w);
+        }
+        uint32_t top = __float_as_uint(t) & 0x7FFFFFFFu;
+        if (top >= 0x7F800000u) {
+          odd = true;
+          float f = 0.f;
+          for (int c = 0; c + sub * 4 < a.d; c += 16)
+            f = fmaxf(f, finite_max(*reinterpret_cast<const float4*>(src[i] + c)));
+          top = __float_as_uint(f);
+        }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        if (sub == 0) sh.q_exp[n_q & 1][warp * 32 + i * 8 + (lane >> 2)] =
+            (int8_t)(top_exponent(top) - 127 - kTop);
+      }
+      odd = __any_sync(0xffffffffu, odd);
+      __syncwarp();
+      const float scale = exp_of(-sh.q_exp[n_q & 1][warp * 32 + lane]);
       const uint64_t scale2 = pair(scale, scale);
       if (!bar_wait_warp(&sh.q_empty, (n_q & 1) ^ 1, ab)) return;
       fence_after();
-#pragma unroll 1
-      for (int b = 0; b < 4; ++b) {  // 32 columns at a time (read again, from L1)
-        uint32_t hi[16], lo[16];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int c = b * 32 + i * 4;
-          const float4 x = c < a.d ? __ldg(reinterpret_cast<const float4*>(src + c))
-                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int b = 0; b < 8; ++b) {  // 16 columns
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<float4*>(turn + (i * 8 + (lane >> 2)) * kTurnRow + sub * 16) = x[b * 4 + i];
+        __syncwarp();
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 v = *reinterpret_cast<const float4*>(turn + lane * kTurnRow + i * 16);
           uint32_t h2[2], l2[2];
-          if (odd) split4<kKeep>(x, scale2, h2, l2);
-          else split4<kNone>(x, scale2, h2, l2);
-          hi[2 * i] = h2[0];
-          hi[2 * i + 1] = h2[1];
-          lo[2 * i] = l2[0];
-          lo[2 * i + 1] = l2[1];
+          if (odd) split4<kKeep>(v, scale2, h2, l2);
+          else split4<kNone>(v, scale2, h2, l2);
+          w[2 * i] = h2[0];
+          w[2 * i + 1] = h2[1];
+          w[8 + 2 * i] = l2[0];
+          w[9 + 2 * i] = l2[1];
         }
-        st16(at + b * 16, hi);
-        st16(at + 64 + b * 16, lo);
+        st8(at + b * 8, w);
+        st8(at + 64 + b * 8, w + 8);
       }
       wait_st();
       fence_before();
@@ -433,9 +468,10 @@ __device__ void unit_role(const TileArgs& a, Shared& sh, int lane) {
     Unit u;
     walk.get(a, w, lane, u);
     if (u.valid) {  // does a tile hold values that are not finite?
-      int odd = 0;
-      for (int i = lane; i < u.nt * kGroups; i += 32)
-        odd |= a.odd[((int64_t)(u.tile + i / kGroups) * a.kv_heads + u.kvh) * kGroups + i % kGroups];
+      uint64_t odd = 0;
+#pragma unroll 4
+      for (int i = lane; i < u.nt; i += 32)
+        odd |= reinterpret_cast<const uint64_t*>(a.odd)[(int64_t)(u.tile + i) * a.kv_heads + u.kvh];
       u.patch = __any_sync(0xffffffffu, odd != 0);
     }
     if (!bar_wait_warp(&sh.u_empty[nu % kUnitRing], ((nu / kUnitRing) & 1) ^ 1, ab)) return;
@@ -462,13 +498,20 @@ __device__ __forceinline__ const float* value_row(const TileArgs& a, const Unit&
 // ---- softmax, accumulation and results (two warpgroups, two threads a row:
 // `half` takes keys 64 * half .. of each tile and value columns 64 * half ..)
 template <bool PAGED>
-__device__ void row_role(const TileArgs& a, Shared& sh, uint32_t tmem, int row, int half,
-                         int lane) {
+__device__ void row_role(const TileArgs& a, Shared& sh, unsigned char* turn, uint32_t tmem,
+                         int row, int half, int lane) {
   volatile int* ab = &sh.abort;
   const float sc = a.scale * kLog2e;
   const int pos = row / a.group, hd = row - pos * a.group;
   const uint32_t at = tmem + ((uint32_t)(row & ~31) << 16);
   uint64_t* mx_full = &sh.mx_full[row >> 5];
+  int turn_pos[4], turn_hd[4];  // of the rows that this lane stores
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = (row & ~31) + i * 8 + (lane >> 2);
+    turn_pos[i] = r / a.group;
+    turn_hd[i] = r - turn_pos[i] * a.group;
+  }
   uint32_t n = 0, nq = 0, n_mx = 0;  // tiles, query tiles, exchanges
   // Both halves' values of this row, through shared memory.
   auto exchange = [&](float mine, float& other) {
@@ -627,45 +670,62 @@ __device__ void row_role(const TileArgs& a, Shared& sh, uint32_t tmem, int row, 
       if (!exchange(l, other)) return;
       l = half == 0 ? l + other : other + l;
     }
-    if (pos < u.np0) {
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      const int64_t orow = (int64_t)u.q_row + pos;
-      const int head = u.kvh * a.group + hd;
-      const int64_t prow = ((int64_t)u.split * a.q_rows + orow) * a.heads + head;
-      float* out = (a.splits ? a.part + prow * a.dv
-                             : (float*)a.out.p + orow * a.out.row + head * a.out.head) + half * 64;
-      const int cols = a.dv - half * 64;
-      if (u.patch) {
-#pragma unroll
-        for (int c = 0; c < 64; c += 4)
-          if (c < cols)
-#pragma unroll 1
-            for (int k = 0; k < lim; ++k) {
-              const int64_t im = (int64_t)(u.tile + k / kTileN) * a.kv_heads + u.kvh;
-              if (!a.odd[im * kGroups + k % kTileN / kGroup]) {
-                k |= kGroup - 1;  // on to the next group
-                continue;
-              }
-              const float* v = value_row<PAGED>(a, u, u.kb + k);
-              if (!v) continue;
-              const float4 z = *reinterpret_cast<const float4*>(v + half * 64 + c);
-              if (!finite_bits(z.x)) acc[c] += z.x;
-              if (!finite_bits(z.y)) acc[c + 1] += z.y;
-              if (!finite_bits(z.z)) acc[c + 2] += z.z;
-              if (!finite_bits(z.w)) acc[c + 3] += z.w;
-            }
-      }
+    const bool mine = pos < u.np0;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int cols = a.dv - half * 64;
+    if (u.patch && mine) {
 #pragma unroll
       for (int c = 0; c < 64; c += 4)
         if (c < cols)
-          *reinterpret_cast<float4*>(out + c) =
-              make_float4(acc[c] * inv, acc[c + 1] * inv, acc[c + 2] * inv, acc[c + 3] * inv);
-      if (half == 0) {
-        const float v = l == 0.f ? -INFINITY : fmaf(m - kLift, kLn2, logf(l));
-        if (a.splits) a.part_lse[prow] = v;
-        else if (a.lse) a.lse[orow * a.heads + head] = v;
-      }
+#pragma unroll 1
+          for (int k = 0; k < lim; ++k) {
+            const int64_t im = (int64_t)(u.tile + k / kTileN) * a.kv_heads + u.kvh;
+            if (!a.odd[im * kGroups + k % kTileN / kGroup]) {
+              k |= kGroup - 1;  // on to the next group
+              continue;
+            }
+            const float* v = value_row<PAGED>(a, u, u.kb + k);
+            if (!v) continue;
+            const float4 z = *reinterpret_cast<const float4*>(v + half * 64 + c);
+            if (!finite_bits(z.x)) acc[c] += z.x;
+            if (!finite_bits(z.y)) acc[c + 1] += z.y;
+            if (!finite_bits(z.z)) acc[c + 2] += z.z;
+            if (!finite_bits(z.w)) acc[c + 3] += z.w;
+          }
     }
+    if (half == 0 && mine) {
+      const int64_t orow = (int64_t)u.q_row + pos;
+      const int head = u.kvh * a.group + hd;
+      const float v = l == 0.f ? -INFINITY : fmaf(m - kLift, kLn2, logf(l));
+      if (a.splits) a.part_lse[((int64_t)u.split * a.q_rows + orow) * a.heads + head] = v;
+      else if (a.lse) a.lse[orow * a.heads + head] = v;
+    }
+    // 16 columns at a time: from "thread = row" to 64 bytes of 8 rows a store.
+    float* to[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int p = turn_pos[i], h = u.kvh * a.group + turn_hd[i];
+      const int64_t orow = (int64_t)u.q_row + p;
+      to[i] = p >= u.np0 ? nullptr
+                         : (a.splits ? a.part + (((int64_t)u.split * a.q_rows + orow) * a.heads + h) * a.dv
+                                     : (float*)a.out.p + orow * a.out.row + h * a.out.head) +
+                               half * 64 + (lane & 3) * 4;
+    }
+#pragma unroll
+    for (int c = 0; c < 64; c += 16)
+      if (c < cols) {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+          *reinterpret_cast<float4*>(turn + lane * kTurnRow + i * 4) =
+              make_float4(acc[c + i] * inv, acc[c + i + 1] * inv, acc[c + i + 2] * inv, acc[c + i + 3] * inv);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 v = *reinterpret_cast<const float4*>(turn + (i * 8 + (lane >> 2)) * kTurnRow + (lane & 3) * 16);
+          if (to[i] && c + (lane & 3) * 4 < cols) *reinterpret_cast<float4*>(to[i] + c) = v;
+        }
+      }
     __syncwarp();
     if (lane == 0) bar_arrive(&sh.u_empty[nu % kUnitRing]);
   }
@@ -679,10 +739,10 @@ template <int N>
 __device__ __forceinline__ void fewer_regs() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
-// The launch holds 512 x 128 registers = 65,536; the shares are 256 x 152 +
-// 128 x 104 + 128 x 104 of them.
-constexpr int kRegsRow = 152, kRegsRest = 104;
-static_assert(256 * kRegsRow + 256 * kRegsRest <= 512 * 128, "registers");
+// The launch holds 512 x 128 registers = 65,536; the shares are 256 x 136 +
+// 128 x 168 + 128 x 72 of them.
+constexpr int kRegsRow = 136, kRegsQuery = 168, kRegsRest = 72;
+static_assert(256 * kRegsRow + 128 * kRegsQuery + 128 * kRegsRest <= 512 * 128, "registers");
 
 template <bool PAGED>
 __global__ void __launch_bounds__(kThreads, 1) 
@@ -719,12 +779,13 @@ attn_tc32_kernel(const __grid_constant__ TileArgs a) {
   const uint32_t tmem = sh.tmem;
   if (warp < 8) {
     more_regs<kRegsRow>();
-    row_role<PAGED>(a, sh, tmem, tid & 127, warp >> 2, lane);
+    row_role<PAGED>(a, sh, sm + kOffTurn + warp * kTurn, tmem, tid & 127, warp >> 2, lane);
+  } else if (warp < 12) {
+    more_regs<kRegsQuery>();
+    query_role(a, sh, sm + kOffTurn + warp * kTurn, tmem, warp & 3, lane);
   } else {
     fewer_regs<kRegsRest>();
-    if (warp < 12) {
-      query_role(a, sh, tmem, tid & 127, lane);
-    } else if (warp == 12) {
+    if (warp == 12) {
       if (elect_one()) mma_role(a, sh, sm, tmem);
     } else if (warp == 13) {
       unit_role(a, sh, lane);
