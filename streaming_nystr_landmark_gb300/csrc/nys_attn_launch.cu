@@ -222,6 +222,7 @@ bool prompt_tc_fits(const PromptArgs& a) {
   const int elem = a.dtype == NYS_F32 ? 4 : 2, unit = 16 / elem;
   if (a.d > 128 || a.dv > 128 || a.d % unit || a.dv % unit) return false;
   if (a.k_rows == 0 || a.k_rows > (1 << 30) || a.q_rows > (1 << 30)) return false;
+  if ((a.q_rows / (kTileM / a.group) + a.n) * a.kv_heads > (1 << 30)) return false;  // units
   // K and V share the choice between a KV head's own rows and one head's rows.
   const bool kb = a.kv_heads > 1 && a.k.head == 0, vb = a.kv_heads > 1 && a.v.head == 0;
   return kb == vb && tileable(a.q, a.q_rows, a.heads, elem, false) &&

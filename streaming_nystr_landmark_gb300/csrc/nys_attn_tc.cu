@@ -198,11 +198,14 @@ __device__ void mma_role(const TileArgs& a, Shared& sh, unsigned char* sm, uint3
       const uint32_t at = base + k_at(j, pair), slot = at % kSlots;
       if (!bar_wait(&sh.kv_full[slot], (at / kSlots) & 1, ab)) return false;
       fence_after();
-      const uint32_t q = q0 + (pair ? s : 0) * 32768, k = kv0 + slot * kSlotBytes;
-      for (int i = 0; i < ks; ++i) {
-        const uint32_t off = (i >> 2) * 16384 + (i & 3) * 32;
-        mma_ss(tmem + s * 128, desc128(q + off, 16, 1024), desc128(k + off, 16, 1024), id_s, i > 0);
-      }
+      const uint64_t q = desc128(q0 + (pair ? s : 0) * 32768, 16, 1024);
+      const uint64_t k = desc128(kv0 + slot * kSlotBytes, 16, 1024);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < ks) {
+          const uint64_t off = (i >> 2) * 1024 + (i & 3) * 2;
+          mma_ss(tmem + s * 128, q + off, k + off, id_s, i > 0);
+        }
       commit(&sh.s_full[s]);
       if (j == u.nt - 1 && (!pair || s == 1)) commit(&sh.q_empty);  // the unit's last
       return true;
@@ -217,10 +220,11 @@ __device__ void mma_role(const TileArgs& a, Shared& sh, unsigned char* sm, uint3
         o_free[s] = true;
       }
       fence_after();
-      const uint32_t v = kv0 + slot * kSlotBytes;
+      const uint64_t v = desc128(kv0 + slot * kSlotBytes, 16384, 1024);
+#pragma unroll
       for (int i = 0; i < kTileN / 16; ++i)
-        mma_ts(tmem + 256 + s * 128, tmem + s * 128 + i * 8, desc128(v + i * 2048, 16384, 1024),
-               id_o, !(first && i == 0));
+        mma_ts(tmem + 256 + s * 128, tmem + s * 128 + i * 8, v + (uint64_t)(i * 128), id_o,
+               !(first && i == 0));
       return true;
     };
     auto free_slot = [&](uint32_t at) { commit(&sh.kv_empty[(base + at) % kSlots]); };
@@ -273,7 +277,7 @@ __device__ void unit_role(const TileArgs& a, Shared& sh, int lane) {
   for (uint32_t nu = 0;; ++nu) {
     // Every other round runs backwards, so that no CTA gets the longer unit of
     // every round.
-    const int64_t w = (int64_t)nu * gridDim.x +
+    const int32_t w = nu * gridDim.x +
                       ((nu & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
     Unit u;
     walk.get(a, w, lane, u);
@@ -499,7 +503,7 @@ __device__ void row_role(const TileArgs& a, Shared& sh, uint32_t tmem, int s, in
       a1 = s == 0 ? ao : am;
     }
     fence_after();
-    const float inv = total == 0.f ? 0.f : 1.f / total;
+    const float inv = total == 0.f ? 0.f : reciprocal(total);
     a0 *= inv;
     a1 *= inv;
     const bool mine = pos < (pair && s == 1 ? u.np1 : u.np0);
@@ -529,18 +533,6 @@ __device__ void row_role(const TileArgs& a, Shared& sh, uint32_t tmem, int s, in
         for (int i = 0; i < 16; ++i) y[i] = fmaf(__uint_as_float(o[i]), a1, y[i]);
       }
       if (!mine) continue;
-      if (patch) {
-        for (int k = u.edge * kTileN; k < lim; ++k) {
-          const T* v = value_row<T, PAGED>(a, u, u.kb + k);
-          if (!v) continue;
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (c + i < a.dv) {
-              const float z = (float)v[c + i];
-              if (!isfinite(z)) y[i] += z;
-            }
-        }
-      }
 #pragma unroll
       for (int i = 0; i < 16; i += 8)
         if (c + i < a.dv) {
@@ -548,8 +540,18 @@ __device__ void row_role(const TileArgs& a, Shared& sh, uint32_t tmem, int s, in
           else store8(out + c + i, y + i);
         }
     }
+    if (patch && mine) {
+      for (int k = u.edge * kTileN; k < lim; ++k) {
+        const T* v = value_row<T, PAGED>(a, u, u.kb + k);
+        if (!v) continue;
+        for (int c = pair ? 0 : 16 * s; c < a.dv; c += pair ? 16 : 32) {
+          if (a.splits) add_unusual(a.part + prow * a.dv, v, c, min(c + 16, a.dv));
+          else add_unusual(out, v, c, min(c + 16, a.dv));
+        }
+      }
+    }
     if (mine && (pair || s == 0)) {
-      const float v = total == 0.f ? -INFINITY : fmaf(top, a.scale, logf(total));
+      const float v = total == 0.f ? -INFINITY : fmaf(top, a.scale, lg2(total) * 0.6931471805599453f);
       if (a.splits) a.part_lse[prow] = v;
       else if (a.lse) a.lse[orow * a.heads + head] = v;
     }
@@ -567,6 +569,11 @@ __device__ void row_role(const TileArgs& a, Shared& sh, uint32_t tmem, int s, in
     }
   }
 }
+
+// The launch holds 384 x 168 registers = 64,512; the shares are 256 x 208 +
+// 128 x 88 of them.
+constexpr int kRegsRow = 208, kRegsRest = 88;
+static_assert(256 * kRegsRow + 128 * kRegsRest <= 384 * 168, "registers");
 
 template <typename T, bool PAGED>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -604,15 +611,19 @@ attn_tc_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CUten
   fence_after();
   const uint32_t tmem = sh.tmem;
   if (warp < 8) {
+    more_regs<kRegsRow>();
     row_role<T, PAGED>(a, sh, tmem, warp >> 2, tid & 127, lane);
-  } else if (warp == 8) {
-    if (elect_one()) load_role<PAGED>(a, &mq, &mk, &mv, sh, sm);
-  } else if (warp == 9) {
-    if (elect_one()) mma_role<T>(a, sh, sm, tmem);
-  } else if (warp == 10) {
-    unit_role(a, sh, lane);
   } else {
-    clean_role<T>(a, sh, sm, lane);
+    fewer_regs<kRegsRest>();
+    if (warp == 8) {
+      if (elect_one()) load_role<PAGED>(a, &mq, &mk, &mv, sh, sm);
+    } else if (warp == 9) {
+      if (elect_one()) mma_role<T>(a, sh, sm, tmem);
+    } else if (warp == 10) {
+      unit_role(a, sh, lane);
+    } else {
+      clean_role<T>(a, sh, sm, lane);
+    }
   }
   __syncwarp();
   fence_before();

@@ -115,14 +115,25 @@ cudaError_t launch_attn_tc32(const TileArgs& a, unsigned grid, cudaStream_t stre
 
 
 #ifdef __CUDACC__
+// Values that are not finite are 0 in what the products read; the rows that see
+// their keys get them here, after their results were written: `out` is this
+// thread's row, x += z (infinities stay, opposite ones and NaN give NaN).
+template <typename T, typename V>
+__device__ __forceinline__ void add_unusual(T* out, const V* v, int c0, int c1) {
+  for (int c = c0; c < c1; ++c) {
+    const float z = (float)v[c];
+    if (!isfinite(z)) out[c] = (T)((float)out[c] + z);
+  }
+}
+
 // Walks the launch's units in order; one warp.  Within a sequence the query
 // tiles come last position first, because under the causal mask those are the
 // longest; KV heads of one position lie next to each other.
 struct UnitWalk {
-  int64_t before = 0;  // units of the sequences before the window
+  int32_t before = 0;  // units of the sequences before the window
   int s0 = 0;          // the window's first sequence, 32 of them
   int q0, nq, k0, nk, pairs;
-  int64_t count, upto;  // this lane's sequence's units, and the inclusive sum
+  int32_t count, upto;  // this lane's sequence's units, and the inclusive sum
 
   __device__ __forceinline__ void load(const TileArgs& a, int lane) {
     const int i = s0 + lane;
@@ -139,22 +150,22 @@ struct UnitWalk {
       }
     }
     pairs = (nq + a.per * a.tp - 1) / (a.per * a.tp);
-    count = (int64_t)pairs * a.kv_heads * (a.splits ? a.splits : 1);
+    count = pairs * a.kv_heads * (a.splits ? a.splits : 1);
     upto = count;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+      const int32_t y = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += y;
     }
   }
 
   // Unit number w (ascending from call to call) into `u` in every lane;
   // u.valid == 0 past the last.
-  __device__ __forceinline__ void get(const TileArgs& a, int64_t w, int lane, Unit& u) {
+  __device__ __forceinline__ void get(const TileArgs& a, int32_t w, int lane, Unit& u) {
     u.valid = 0;
     u.patch = 0;
     for (;;) {
-      const int64_t all = __shfl_sync(0xffffffffu, upto, 31);
+      const int32_t all = __shfl_sync(0xffffffffu, upto, 31);
       if (w < before + all) break;
       before += all;
       s0 += 32;
@@ -165,12 +176,12 @@ struct UnitWalk {
     const int sq0 = __shfl_sync(0xffffffffu, q0, src), snq = __shfl_sync(0xffffffffu, nq, src);
     const int sk0 = __shfl_sync(0xffffffffu, k0, src), snk = __shfl_sync(0xffffffffu, nk, src);
     const int spairs = __shfl_sync(0xffffffffu, pairs, src);
-    int64_t r = w - before - __shfl_sync(0xffffffffu, upto - count, src);
+    int32_t r = w - before - __shfl_sync(0xffffffffu, upto - count, src);
     const int ns = a.splits ? a.splits : 1;
-    u.split = (int)(r % ns);
+    u.split = r % ns;
     r /= ns;
-    u.kvh = (int)(r % a.kv_heads);
-    const int pair = spairs - 1 - (int)(r / a.kv_heads);
+    u.kvh = r % a.kv_heads;
+    const int pair = spairs - 1 - r / a.kv_heads;
     const int p0 = pair * a.per * a.tp;
     const int left = snq - p0;
     u.np0 = min(left, a.tp);

@@ -79,7 +79,7 @@ struct Shared {
   uint64_t drain;
   Unit unit[kUnitRing];
   alignas(16) TileExps exps[4];      // of tile & 3
-  int8_t q_exp[2][kTileM];           // eq, [unit & 1][row]
+  int8_t q_exp[4][kTileM];           // eq, [unit & 3][row]: the query warps run up to three units ahead
   float mx[2][2][kTileM];            // halves' maxima [exchange & 1][half][row], also of l
   uint32_t tmem;
   int abort;
@@ -234,7 +234,6 @@ __device__ void query_role(const TileArgs& a, Shared& sh, unsigned char* turn, u
                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
       }
       // The rows' exponents.
-      bool odd = false;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float t = 0.f;
@@ -244,21 +243,15 @@ __device__ void query_role(const TileArgs& a, Shared& sh, unsigned char* turn, u
           t = max3_abs_nan(t, x[c * 4 + i].z, x[c * 4 + i].w);
         }
         uint32_t top = __float_as_uint(t) & 0x7FFFFFFFu;
-        if (top >= 0x7F800000u) {
-          odd = true;
-          float f = 0.f;
-          for (int c = 0; c + sub * 4 < a.d; c += 16)
-            f = fmaxf(f, finite_max(*reinterpret_cast<const float4*>(src[i] + c)));
-          top = __float_as_uint(f);
-        }
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        if (sub == 0) sh.q_exp[n_q & 1][warp * 32 + i * 8 + (lane >> 2)] =
-            (int8_t)(top_exponent(top) - 127 - kTop);
+        // (127 marks a query with a value that is not finite: its results are NaN)
+        if (sub == 0) sh.q_exp[n_q & 3][warp * 32 + i * 8 + (lane >> 2)] =
+            (int8_t)(top >= 0x7F800000u ? 127 : top_exponent(top) - 127 - kTop);
       }
-      odd = __any_sync(0xffffffffu, odd);
       __syncwarp();
-      const float scale = exp_of(-sh.q_exp[n_q & 1][warp * 32 + lane]);
+      const int qe = sh.q_exp[n_q & 3][warp * 32 + lane];
+      const float scale = qe == 127 ? NAN : exp_of(-qe);
       const uint64_t scale2 = pair(scale, scale);
       if (!bar_wait_warp(&sh.q_empty, (n_q & 1) ^ 1, ab)) return;
       fence_after();
@@ -274,8 +267,7 @@ __device__ void query_role(const TileArgs& a, Shared& sh, unsigned char* turn, u
         for (int i = 0; i < 4; ++i) {
           const float4 v = *reinterpret_cast<const float4*>(turn + lane * kTurnRow + i * 16);
           uint32_t h2[2], l2[2];
-          if (odd) split4<kKeep>(v, scale2, h2, l2);
-          else split4<kNone>(v, scale2, h2, l2);
+          split4<kNone>(v, scale2, h2, l2);
           w[2 * i] = h2[0];
           w[2 * i + 1] = h2[1];
           w[8 + 2 * i] = l2[0];
@@ -463,7 +455,7 @@ __device__ void unit_role(const TileArgs& a, Shared& sh, int lane) {
   UnitWalk walk;
   walk.load(a, lane);
   for (uint32_t nu = 0;; ++nu) {
-    const int64_t w = (int64_t)nu * gridDim.x +
+    const int32_t w = nu * gridDim.x +
                       ((nu & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
     Unit u;
     walk.get(a, w, lane, u);
@@ -560,25 +552,12 @@ __device__ void row_role(const TileArgs& a, Shared& sh, unsigned char* turn, uin
       const uint32_t b = n & 1, ph = (n >> 1) & 1;
       if (!bar_wait_warp(&sh.s_full[b], ph, ab)) return;
       fence_after();
-      if (j == 0) qm = exp_of(sh.q_exp[nq & 1][row]) * sc;
+      if (j == 0) qm = exp_of(sh.q_exp[nq & 3][row]) * sc;
       const uint32_t s_at = at + kColS + b * 128 + half * 64;
       const float* km = sh.exps[n & 3].k_mul + half * 4;
       const int32_t* ve = sh.exps[n & 3].v_exp + half * 4;
-      if (lim0 < (j + 1) * kTileN) {  // some row does not see some key: mask S in place
-        const int vis = lim - j * kTileN - half * 64;
-#pragma unroll 1
-        for (int c = 0; c < 64; c += 32) {
-          uint32_t x[32];
-          ld32(s_at + c, x);
-          wait_ld();
-          pin32(x);
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (c + i >= vis) x[i] = 0xff800000u;
-          st32(s_at + c, x);
-        }
-        wait_st();
-      }
+      const bool cut = lim0 < (j + 1) * kTileN;  // some row does not see some key
+      const int vis = lim - j * kTileN - half * 64;
       float top = m;
 #pragma unroll
       for (int c = 0; c < 64; c += 32) {
@@ -586,6 +565,12 @@ __device__ void row_role(const TileArgs& a, Shared& sh, unsigned char* turn, uin
         ld32(s_at + c, x);
         wait_ld();
         pin32(x);
+        if (cut) {  // mask S in place
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (c + i >= vis) x[i] = 0xff800000u;
+          st32(s_at + c, x);
+        }
 #pragma unroll
         for (int g = 0; g < 32; g += 16) {
           float t0 = max3(__uint_as_float(x[g]), __uint_as_float(x[g + 1]), __uint_as_float(x[g + 2]));
@@ -639,8 +624,9 @@ __device__ void row_role(const TileArgs& a, Shared& sh, unsigned char* turn, uin
         l = fmaf(l0 + l1, exp_of(-ev), l);
         st16(s_at + g * 16, p);
       };
+      if (cut) wait_st();
       ld16(s_at, xa);
-#pragma unroll
+#pragma unroll 1
       for (int g = 0; g < 4; g += 2) {
         wait_ld();
         pin16(xa);
@@ -671,32 +657,12 @@ __device__ void row_role(const TileArgs& a, Shared& sh, unsigned char* turn, uin
       l = half == 0 ? l + other : other + l;
     }
     const bool mine = pos < u.np0;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float inv = l == 0.f ? 0.f : reciprocal(l);
     const int cols = a.dv - half * 64;
-    if (u.patch && mine) {
-#pragma unroll
-      for (int c = 0; c < 64; c += 4)
-        if (c < cols)
-#pragma unroll 1
-          for (int k = 0; k < lim; ++k) {
-            const int64_t im = (int64_t)(u.tile + k / kTileN) * a.kv_heads + u.kvh;
-            if (!a.odd[im * kGroups + k % kTileN / kGroup]) {
-              k |= kGroup - 1;  // on to the next group
-              continue;
-            }
-            const float* v = value_row<PAGED>(a, u, u.kb + k);
-            if (!v) continue;
-            const float4 z = *reinterpret_cast<const float4*>(v + half * 64 + c);
-            if (!finite_bits(z.x)) acc[c] += z.x;
-            if (!finite_bits(z.y)) acc[c + 1] += z.y;
-            if (!finite_bits(z.z)) acc[c + 2] += z.z;
-            if (!finite_bits(z.w)) acc[c + 3] += z.w;
-          }
-    }
     if (half == 0 && mine) {
       const int64_t orow = (int64_t)u.q_row + pos;
       const int head = u.kvh * a.group + hd;
-      const float v = l == 0.f ? -INFINITY : fmaf(m - kLift, kLn2, logf(l));
+      const float v = l == 0.f ? -INFINITY : (m - kLift + lg2(l)) * kLn2;
       if (a.splits) a.part_lse[((int64_t)u.split * a.q_rows + orow) * a.heads + head] = v;
       else if (a.lse) a.lse[orow * a.heads + head] = v;
     }
@@ -726,19 +692,29 @@ __device__ void row_role(const TileArgs& a, Shared& sh, unsigned char* turn, uin
           if (to[i] && c + (lane & 3) * 4 < cols) *reinterpret_cast<float4*>(to[i] + c) = v;
         }
       }
+    if (u.patch) {
+      __syncwarp();  // the row's results are there
+      if (mine) {
+        const int64_t orow = (int64_t)u.q_row + pos;
+        const int head = u.kvh * a.group + hd;
+        float* out = a.splits ? a.part + (((int64_t)u.split * a.q_rows + orow) * a.heads + head) * a.dv
+                              : (float*)a.out.p + orow * a.out.row + head * a.out.head;
+        for (int k = 0; k < lim; ++k) {
+          const int64_t im = (int64_t)(u.tile + k / kTileN) * a.kv_heads + u.kvh;
+          if (!a.odd[im * kGroups + k % kTileN / kGroup]) {
+            k |= kGroup - 1;  // on to the next group
+            continue;
+          }
+          const float* v = value_row<PAGED>(a, u, u.kb + k);
+          if (v) add_unusual(out, v, half * 64, min(half * 64 + 64, a.dv));
+        }
+      }
+    }
     __syncwarp();
     if (lane == 0) bar_arrive(&sh.u_empty[nu % kUnitRing]);
   }
 }
 
-template <int N>
-__device__ __forceinline__ void more_regs() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void fewer_regs() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
 // The launch holds 512 x 128 registers = 65,536; the shares are 256 x 136 +
 // 128 x 168 + 128 x 72 of them.
 constexpr int kRegsRow = 136, kRegsQuery = 168, kRegsRest = 72;

@@ -25,6 +25,16 @@ __device__ __forceinline__ bool elect_one() {
                : "=r"(y));
   return y != 0;
 }
+// Registers a thread for this warpgroup from here on; what one takes, others of
+// the launch have to have given up.
+template <int N>
+__device__ __forceinline__ void more_regs() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_regs() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 __device__ __forceinline__ uint32_t sptr(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
@@ -53,21 +63,18 @@ __device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
   return ok != 0;
 }
 // Waits for the completion of the barrier's phase `parity`; false after 2 s or
-// once another thread of the CTA gave up.
+// once another thread of the CTA gave up.  (Small on purpose: it is inlined at
+// every wait, and the kernels' code competes for the instruction caches.)
 __device__ __forceinline__ bool bar_wait_slow(uint64_t* b, uint32_t parity, volatile int* abort) {
   uint64_t t0, t1;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
-  for (uint32_t i = 0;; ++i) {
-    if (bar_try(b, parity)) return true;
-    if ((i & 7u) == 7u) {
-      if (*abort) return false;
-      asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t1));
-      if (t1 - t0 > kWaitNs) {
-        *abort = 1;
-        return false;
-      }
-    }
+#pragma unroll 1
+  while (!bar_try(b, parity)) {
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t1));
+    if (t1 - t0 > kWaitNs) *abort = 1;
+    if (*abort) return false;
   }
+  return true;
 }
 __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, volatile int* abort) {
   if (bar_try(b, parity)) return true;
@@ -221,6 +228,17 @@ __device__ __forceinline__ void tmem_free(uint32_t base, uint32_t cols) {
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols));
 }
 
+// 1 / x to about half a step (approximation and one Newton step), and log2 x.
+__device__ __forceinline__ float reciprocal(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return fmaf(y, fmaf(-x, y, 1.f), y);
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
