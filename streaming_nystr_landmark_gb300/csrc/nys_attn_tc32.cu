@@ -30,7 +30,7 @@
 // attn_tc32_kernel: one CTA of 512 threads a SM works on one query tile of 128
 // rows (positions x heads of the group): warps 0-7 softmax and accumulation (two
 // threads a row: each takes half the tile's keys for the weights and half the
-// value columns for the sums), 8-11 the query tile's pieces, 12 products, 13
+// value columns for the sums), 8-11 the query tile's pieces and the results' stores, 12 products, 13
 // units of work, 14 copies.  Q goes straight into tensor memory, because a
 // product with A there takes 74 clocks and one with A in shared memory 107; K and
 // V images stream through three 64 KB slots as plain bulk copies.  Scores of
@@ -57,12 +57,16 @@ constexpr int kGroups = kTileN / kGroup;
 constexpr int kSlots = 3;
 constexpr uint32_t kPiece = 32768;
 constexpr uint32_t kSlotBytes = 2 * kPiece;
-// Each softmax and query warp moves its 32 rows between global memory (whole
-// sectors, 16 columns of 8 rows an instruction) and "thread = row" through a
-// buffer of its own: 16 columns, rows 80 bytes apart, free of bank conflicts.
-constexpr uint32_t kTurnRow = 80, kTurn = 32 * kTurnRow;
+// The query warps move their 32 rows between global memory (whole sectors, 16
+// columns of 8 rows an instruction) and "thread = row" through a buffer of 16
+// columns each; 16-byte units are exchanged by the row so that neither side
+// meets bank conflicts.
+constexpr uint32_t kTurn = 32 * 64;
 constexpr uint32_t kOffTurn = kSlots * kSlotBytes;
-constexpr uint32_t kTiles = kOffTurn + 12 * kTurn;
+constexpr uint32_t kTiles = kOffTurn + 4 * kTurn;
+__device__ __forceinline__ uint32_t turn_at(int row, int unit) {
+  return (uint32_t)(row * 64 + ((unit ^ ((row >> 1) & 3)) << 4));
+}
 constexpr uint32_t kColQ = 0, kColS = 128, kColO = 384;  // tensor memory
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -73,7 +77,7 @@ constexpr int kTop = 13;        // the largest value's power of two after scalin
 struct Shared {
   uint64_t q_full, q_empty;
   uint64_t kv_full[kSlots], kv_empty[kSlots];
-  uint64_t s_full[2], p_full[2], o_full, o_empty;
+  uint64_t s_full[2], p_full[2], o_full, o_empty, r_full;  // r: O holds the results
   uint64_t mx_full[4];               // both halves of a quarter's rows have their maxima
   uint64_t u_full[kUnitRing], u_empty[kUnitRing];
   uint64_t drain;
@@ -199,14 +203,27 @@ __device__ __forceinline__ float finite_max(float4 x) {
   return f;
 }
 
-// The query tile into tensor memory (four warps, 32 rows each; a lane loads 16
-// bytes of rows lane / 4 + 8 i, then takes row `lane` for the conversion).  Rows
-// past the tile's positions stand for its last one: their results are not
-// stored.
+template <bool PAGED>
+__device__ __forceinline__ const float* value_row(const TileArgs& a, const Unit& u, int j) {
+  int64_t row = (int64_t)u.k_row + j;
+  if (PAGED) {
+    const int32_t pg = a.pages[j / a.page];
+    if (pg < 0 || pg >= a.n_pages) return nullptr;
+    row = (int64_t)pg * a.page + j % a.page;
+  }
+  return (const float*)a.v_raw + row * a.v_row + u.kvh * a.v_head;
+}
+
+// The query tile into tensor memory, and the results out of it (four warps, 32
+// rows each; towards global memory a lane has 16 bytes of rows lane / 4 + 8 i,
+// towards tensor memory row `lane`).  Rows past the tile's positions stand for
+// its last one; their results are not stored.  While one unit is worked on, the
+// next one's query is fetched and the last one's results leave.
+template <bool PAGED>
 __device__ void query_role(const TileArgs& a, Shared& sh, unsigned char* turn, uint32_t tmem,
                            int warp, int lane) {
   volatile int* ab = &sh.abort;
-  const uint32_t at = tmem + ((uint32_t)(warp * 32) << 16) + kColQ;
+  const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
   const int sub = lane & 3;  // 4 columns of a chunk of 16
   int pos[4], hd[4];
 #pragma unroll
@@ -215,22 +232,93 @@ __device__ void query_role(const TileArgs& a, Shared& sh, unsigned char* turn, u
     pos[i] = r / a.group;
     hd[i] = r - pos[i] * a.group;
   }
-  uint32_t n_q = 0;
+  uint32_t n_q = 0, n_r = 0;
+
+  // Results of the unit in ring place `at`.
+  auto results = [&](uint32_t at) {
+    const Unit& u = sh.unit[at];
+    const int64_t split_row = (int64_t)u.split * a.q_rows + u.q_row;
+    if (u.nt > 0) {
+      if (!bar_wait_warp(&sh.r_full, n_r & 1, ab)) return false;
+      ++n_r;
+      fence_after();
+    }
+    float* to[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int h = u.kvh * a.group + hd[i];
+      to[i] = pos[i] >= u.np0 ? nullptr
+              : a.splits      ? a.part + ((split_row + pos[i]) * a.heads + h) * a.dv + sub * 4
+                              : (float*)a.out.p + (u.q_row + (int64_t)pos[i]) * a.out.row +
+                                    h * a.out.head + sub * 4;
+    }
+#pragma unroll 1
+    for (int c = 0; c < a.dv; c += 32) {
+      uint32_t o[32];
+      if (u.nt > 0) {
+        ld32(lanes + kColO + c, o);
+        wait_ld();
+        pin32(o);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = 0;
+      }
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4*>(turn + turn_at(lane, i)) =
+              make_uint4(o[g * 16 + i * 4], o[g * 16 + i * 4 + 1], o[g * 16 + i * 4 + 2], o[g * 16 + i * 4 + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 v = *reinterpret_cast<const float4*>(turn + turn_at(i * 8 + (lane >> 2), sub));
+          if (to[i] && c + g * 16 + sub * 4 < a.dv) *reinterpret_cast<float4*>(to[i] + c + g * 16) = v;
+        }
+      }
+    }
+    fence_before();
+    if (u.patch) {
+      __syncwarp();  // the row's results are there
+      const int row = warp * 32 + lane, p = row / a.group, h = row - p * a.group + u.kvh * a.group;
+      const int lim = min(a.causal ? u.lim + p : u.lim, u.nkl) - u.kb;
+      if (p < u.np0) {
+        float* out = a.splits ? a.part + ((split_row + p) * a.heads + h) * a.dv
+                              : (float*)a.out.p + (u.q_row + (int64_t)p) * a.out.row + h * a.out.head;
+        for (int k = 0; k < lim; ++k) {
+          const int64_t im = (int64_t)(u.tile + k / kTileN) * a.kv_heads + u.kvh;
+          if (!a.odd[im * kGroups + k % kTileN / kGroup]) {
+            k |= kGroup - 1;  // on to the next group
+            continue;
+          }
+          const float* v = value_row<PAGED>(a, u, u.kb + k);
+          if (v) add_unusual(out, v, 0, a.dv);
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) {
+      if (u.nt > 0) bar_arrive(&sh.o_empty, 2);  // eight arrivals free O
+      bar_arrive(&sh.u_empty[at]);
+    }
+    return true;
+  };
+
   for (uint32_t nu = 0;; ++nu) {
     if (!bar_wait_warp(&sh.u_full[nu % kUnitRing], (nu / kUnitRing) & 1, ab)) return;
     const Unit& u = sh.unit[nu % kUnitRing];
-    if (!u.valid) return;
-    if (u.nt > 0) {
+    const bool valid = u.valid;
+    if (valid && u.nt > 0) {
       // The whole tile at once, 32 loads a lane.
       float4 x[32];
-      const float* src[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        src[i] = (const float*)a.q.p + (u.q_row + (int64_t)min(pos[i], u.np0 - 1)) * a.q.row +
-                 (int64_t)(u.kvh * a.group + hd[i]) * a.q.head + sub * 4;
+        const float* src = (const float*)a.q.p + (u.q_row + (int64_t)min(pos[i], u.np0 - 1)) * a.q.row +
+                           (int64_t)(u.kvh * a.group + hd[i]) * a.q.head + sub * 4;
 #pragma unroll
         for (int c = 0; c < 8; ++c)
-          x[c * 4 + i] = c * 16 + sub * 4 < a.d ? __ldg(reinterpret_cast<const float4*>(src[i] + c * 16))
+          x[c * 4 + i] = c * 16 + sub * 4 < a.d ? __ldg(reinterpret_cast<const float4*>(src + c * 16))
                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
       }
       // The rows' exponents.
@@ -260,12 +348,12 @@ __device__ void query_role(const TileArgs& a, Shared& sh, unsigned char* turn, u
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<float4*>(turn + (i * 8 + (lane >> 2)) * kTurnRow + sub * 16) = x[b * 4 + i];
+          *reinterpret_cast<float4*>(turn + turn_at(i * 8 + (lane >> 2), sub)) = x[b * 4 + i];
         __syncwarp();
         uint32_t w[16];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float4 v = *reinterpret_cast<const float4*>(turn + lane * kTurnRow + i * 16);
+          const float4 v = *reinterpret_cast<const float4*>(turn + turn_at(lane, i));
           uint32_t h2[2], l2[2];
           split4<kNone>(v, scale2, h2, l2);
           w[2 * i] = h2[0];
@@ -273,18 +361,17 @@ __device__ void query_role(const TileArgs& a, Shared& sh, unsigned char* turn, u
           w[8 + 2 * i] = l2[0];
           w[9 + 2 * i] = l2[1];
         }
-        st8(at + b * 8, w);
-        st8(at + 64 + b * 8, w + 8);
+        st8(lanes + kColQ + b * 8, w);
+        st8(lanes + kColQ + 64 + b * 8, w + 8);
       }
       wait_st();
       fence_before();
       ++n_q;
+      __syncwarp();
+      if (lane == 0) bar_arrive(&sh.q_full);
     }
-    __syncwarp();
-    if (lane == 0) {
-      if (u.nt > 0) bar_arrive(&sh.q_full);
-      bar_arrive(&sh.u_empty[nu % kUnitRing]);
-    }
+    if (nu > 0 && !results((nu - 1) % kUnitRing)) return;
+    if (!valid) return;
   }
 }
 
@@ -476,34 +563,15 @@ __device__ void unit_role(const TileArgs& a, Shared& sh, int lane) {
   }
 }
 
-template <bool PAGED>
-__device__ __forceinline__ const float* value_row(const TileArgs& a, const Unit& u, int j) {
-  int64_t row = (int64_t)u.k_row + j;
-  if (PAGED) {
-    const int32_t pg = a.pages[j / a.page];
-    if (pg < 0 || pg >= a.n_pages) return nullptr;
-    row = (int64_t)pg * a.page + j % a.page;
-  }
-  return (const float*)a.v_raw + row * a.v_row + u.kvh * a.v_head;
-}
-
-// ---- softmax, accumulation and results (two warpgroups, two threads a row:
+// ---- softmax and accumulation (two warpgroups, two threads a row:
 // `half` takes keys 64 * half .. of each tile and value columns 64 * half ..)
-template <bool PAGED>
-__device__ void row_role(const TileArgs& a, Shared& sh, unsigned char* turn, uint32_t tmem,
-                         int row, int half, int lane) {
+__device__ void row_role(const TileArgs& a, Shared& sh, uint32_t tmem, int row, int half,
+                         int lane) {
   volatile int* ab = &sh.abort;
   const float sc = a.scale * kLog2e;
   const int pos = row / a.group, hd = row - pos * a.group;
   const uint32_t at = tmem + ((uint32_t)(row & ~31) << 16);
   uint64_t* mx_full = &sh.mx_full[row >> 5];
-  int turn_pos[4], turn_hd[4];  // of the rows that this lane stores
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = (row & ~31) + i * 8 + (lane >> 2);
-    turn_pos[i] = r / a.group;
-    turn_hd[i] = r - turn_pos[i] * a.group;
-  }
   uint32_t n = 0, nq = 0, n_mx = 0;  // tiles, query tiles, exchanges
   // Both halves' values of this row, through shared memory.
   auto exchange = [&](float mine, float& other) {
@@ -527,7 +595,7 @@ __device__ void row_role(const TileArgs& a, Shared& sh, unsigned char* turn, uin
 #pragma unroll
     for (int c = 0; c < 64; ++c) acc[c] = 0.f;
     // acc += O of the last tile.
-    auto fold = [&](uint32_t t) {
+    auto fold = [&](uint32_t t, bool last) {
       if (!bar_wait_warp(&sh.o_full, t & 1, ab)) return false;
       fence_after();
 #pragma unroll
@@ -543,6 +611,7 @@ __device__ void row_role(const TileArgs& a, Shared& sh, unsigned char* turn, uin
                         pair(__uint_as_float(o[i]), __uint_as_float(o[i + 1]))),
                    acc[c + i], acc[c + i + 1]);
         }
+      if (last) return true;  // (the results take O's place)
       fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive(&sh.o_empty);
@@ -642,7 +711,7 @@ __device__ void row_role(const TileArgs& a, Shared& sh, unsigned char* turn, uin
       __syncwarp();
       if (lane == 0) bar_arrive(&sh.p_full[b]);
       if (j > 0) {
-        if (!fold(n - 1)) return;
+        if (!fold(n - 1, false)) return;
         if (__any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll
           for (int c = 0; c < 64; ++c) acc[c] *= alpha;
@@ -651,64 +720,31 @@ __device__ void row_role(const TileArgs& a, Shared& sh, unsigned char* turn, uin
     }
     if (nt > 0) {
       ++nq;
-      if (!fold(n - 1)) return;
       float other;
       if (!exchange(l, other)) return;
       l = half == 0 ? l + other : other + l;
+      const float inv = l == 0.f ? 0.f : reciprocal(l);
+      if (!fold(n - 1, true)) return;
+      // Results to tensor memory, for the query warps to store.
+#pragma unroll
+      for (int c = 0; c < 64; c += 16)
+        if (half * 64 + c < a.dv) {
+          uint32_t o[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(acc[c + i] * inv);
+          st16(at + kColO + half * 64 + c, o);
+        }
+      wait_st();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(&sh.r_full);
     }
-    const bool mine = pos < u.np0;
-    const float inv = l == 0.f ? 0.f : reciprocal(l);
-    const int cols = a.dv - half * 64;
-    if (half == 0 && mine) {
+    if (half == 0 && pos < u.np0) {
       const int64_t orow = (int64_t)u.q_row + pos;
       const int head = u.kvh * a.group + hd;
       const float v = l == 0.f ? -INFINITY : (m - kLift + lg2(l)) * kLn2;
       if (a.splits) a.part_lse[((int64_t)u.split * a.q_rows + orow) * a.heads + head] = v;
       else if (a.lse) a.lse[orow * a.heads + head] = v;
-    }
-    // 16 columns at a time: from "thread = row" to 64 bytes of 8 rows a store.
-    float* to[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int p = turn_pos[i], h = u.kvh * a.group + turn_hd[i];
-      const int64_t orow = (int64_t)u.q_row + p;
-      to[i] = p >= u.np0 ? nullptr
-                         : (a.splits ? a.part + (((int64_t)u.split * a.q_rows + orow) * a.heads + h) * a.dv
-                                     : (float*)a.out.p + orow * a.out.row + h * a.out.head) +
-                               half * 64 + (lane & 3) * 4;
-    }
-#pragma unroll
-    for (int c = 0; c < 64; c += 16)
-      if (c < cols) {
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 16; i += 4)
-          *reinterpret_cast<float4*>(turn + lane * kTurnRow + i * 4) =
-              make_float4(acc[c + i] * inv, acc[c + i + 1] * inv, acc[c + i + 2] * inv, acc[c + i + 3] * inv);
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 v = *reinterpret_cast<const float4*>(turn + (i * 8 + (lane >> 2)) * kTurnRow + (lane & 3) * 16);
-          if (to[i] && c + (lane & 3) * 4 < cols) *reinterpret_cast<float4*>(to[i] + c) = v;
-        }
-      }
-    if (u.patch) {
-      __syncwarp();  // the row's results are there
-      if (mine) {
-        const int64_t orow = (int64_t)u.q_row + pos;
-        const int head = u.kvh * a.group + hd;
-        float* out = a.splits ? a.part + (((int64_t)u.split * a.q_rows + orow) * a.heads + head) * a.dv
-                              : (float*)a.out.p + orow * a.out.row + head * a.out.head;
-        for (int k = 0; k < lim; ++k) {
-          const int64_t im = (int64_t)(u.tile + k / kTileN) * a.kv_heads + u.kvh;
-          if (!a.odd[im * kGroups + k % kTileN / kGroup]) {
-            k |= kGroup - 1;  // on to the next group
-            continue;
-          }
-          const float* v = value_row<PAGED>(a, u, u.kb + k);
-          if (v) add_unusual(out, v, half * 64, min(half * 64 + 64, a.dv));
-        }
-      }
     }
     __syncwarp();
     if (lane == 0) bar_arrive(&sh.u_empty[nu % kUnitRing]);
@@ -739,6 +775,7 @@ attn_tc32_kernel(const __grid_constant__ TileArgs a) {
     }
     bar_init(&sh.o_full, 1);
     bar_init(&sh.o_empty, 8);
+    bar_init(&sh.r_full, 8);
     for (int i = 0; i < 4; ++i) bar_init(&sh.mx_full[i], 2);
     for (int i = 0; i < kUnitRing; ++i) {
       bar_init(&sh.u_full[i], 1);
@@ -755,10 +792,10 @@ attn_tc32_kernel(const __grid_constant__ TileArgs a) {
   const uint32_t tmem = sh.tmem;
   if (warp < 8) {
     more_regs<kRegsRow>();
-    row_role<PAGED>(a, sh, sm + kOffTurn + warp * kTurn, tmem, tid & 127, warp >> 2, lane);
+    row_role(a, sh, tmem, tid & 127, warp >> 2, lane);
   } else if (warp < 12) {
     more_regs<kRegsQuery>();
-    query_role(a, sh, sm + kOffTurn + warp * kTurn, tmem, warp & 3, lane);
+    query_role<PAGED>(a, sh, sm + kOffTurn + (warp & 3) * kTurn, tmem, warp & 3, lane);
   } else {
     fewer_regs<kRegsRest>();
     if (warp == 12) {
