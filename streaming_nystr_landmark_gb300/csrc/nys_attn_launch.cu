@@ -65,33 +65,25 @@ constexpr int kMostPieces = 64;
 int64_t div_up(int64_t x, int64_t y) { return (x + y - 1) / y; }
 int clamp_int(int64_t x, int lo, int hi) { return (int)(x < lo ? lo : (x > hi ? hi : x)); }
 
-// Units of the prefix launch before its keys are cut.
-int64_t prefix_units(int64_t n, int kv_heads, int group, int dtype) {
-  return div_up(n, (dtype == NYS_F32 ? 1 : 2) * (kTileM / group)) * kv_heads;
-}
-// Pieces at most: enough for four rounds of CTAs.  Bounds the workspace, so it
-// depends on the batch alone.
-int most_prefix_pieces(int64_t n, int kv_heads, int group, int dtype) {
-  return clamp_int(div_up(4 * kSms, prefix_units(n, kv_heads, group, dtype)), 1, kMostPieces);
+// How a prefix of `tiles` key tiles is dealt out: an even share for each SM, but
+// at least two tiles a CTA (a CTA's start costs about three tiles' time) and no
+// more pieces of a unit than the join takes.  tiles == 0: the most pieces that
+// any prefix can have (bounds the workspace by the batch alone).
+Shares shares_of(int64_t n, int kv_heads, int group, int dtype, int64_t tiles) {
+  Shares s{};
+  s.rows = (dtype == NYS_F32 ? 1 : 2) * (kTileM / group);
+  s.units = (int32_t)(div_up(n, s.rows) * kv_heads);
+  s.nt = (int32_t)(tiles > 0 ? tiles : INT32_MAX / 2);
+  const int64_t all = (int64_t)s.units * s.nt;
+  int64_t ctas = kSms;
+  if (ctas > (int64_t)s.units * (kMostPieces - 2)) ctas = (int64_t)s.units * (kMostPieces - 2);
+  if (ctas > div_up(all, 2)) ctas = div_up(all, 2);
+  s.ctas = (int32_t)ctas;
+  s.most = (int32_t)div_up(ctas, s.units) + 1;
+  return s;
 }
 int most_own_pieces(int64_t n, int kv_heads) {
   return clamp_int(div_up(4 * kSms, n * kv_heads), 1, kMostPieces);
-}
-
-// How many pieces to cut `tiles` key tiles of `units` units into: the least of
-// rounds of CTAs x (tiles of a piece + what a unit costs besides, about three
-// tiles' time), with a little for writing and joining each piece.
-int pick_pieces(int64_t units, int64_t tiles, int most) {
-  int best = 1;
-  double cost = 1e300;
-  for (int p = 1; p <= most && p <= tiles; ++p) {
-    const double c = (double)div_up(units * p, kSms) * (double)(div_up(tiles, p) + 3) + 0.5 * p;
-    if (c < cost) {
-      cost = c;
-      best = p;
-    }
-  }
-  return best;
 }
 
 int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
@@ -134,7 +126,7 @@ size_t shared_workspace(const nys_attn_config& c, int64_t n, int64_t keys) {
   if (n == 0 || c.d > 128 || c.dv > 128) return 0;
   const int group = c.heads / c.kv_heads;
   const int64_t pieces =
-      most_prefix_pieces(n, c.kv_heads, group, c.dtype) + most_own_pieces(n, c.kv_heads);
+      shares_of(n, c.kv_heads, group, c.dtype, 0).most + most_own_pieces(n, c.kv_heads);
   const size_t parts = (size_t)pieces * n * c.heads * ((size_t)c.dv + 1) * 4;
   const size_t images =
       c.dtype == NYS_F32 && keys > 0 ? images_of(c.kv_heads, c.d, c.dv, 1, keys).end : 0;
@@ -145,7 +137,7 @@ bool shared_tiled_fits(const SharedArgs& a) {
   const int elem = a.dtype == NYS_F32 ? 4 : 2, unit = 16 / elem;
   if (a.d > 128 || a.dv > 128 || a.d % unit || a.dv % unit || a.n_pages == 0) return false;
   if (reinterpret_cast<uintptr_t>(a.k) % 16 || reinterpret_cast<uintptr_t>(a.v) % 16) return false;
-  if (a.n_pages * a.page > (1 << 30)) return false;
+  if (a.n_pages * a.page > (1 << 30) || a.n_pages * a.page * a.kv_heads > INT32_MAX) return false;
   if (!tileable(a.q, a.n, a.heads, elem, false)) return false;
   if (a.prefix_len > 0 && a.dtype != NYS_F32 && a.page % 8) return false;
   return true;
@@ -154,19 +146,17 @@ bool shared_tiled_fits(const SharedArgs& a) {
 cudaError_t launch_shared_tiled(const SharedArgs& s, void* workspace, cudaStream_t stream) {
   const int64_t row = (int64_t)s.n * s.heads;
   OwnArgs o{};
-  const int64_t units = prefix_units(s.n, s.kv_heads, s.group, s.dtype);
-  const int64_t tiles = div_up(s.prefix_len, kTileN);
   if (s.prefix_len > 0)
-    o.prefix_pieces = pick_pieces(units, tiles, most_prefix_pieces(s.n, s.kv_heads, s.group, s.dtype));
+    o.shares = shares_of(s.n, s.kv_heads, s.group, s.dtype, div_up(s.prefix_len, kTileN));
   const int64_t cap = (int64_t)s.width * s.page;
   o.pieces = clamp_int(div_up(cap, 256), 1, most_own_pieces(s.n, s.kv_heads));
-  const int64_t pieces = o.prefix_pieces + (o.pieces > 1 ? o.pieces : 0);
+  const int64_t pieces = o.shares.most + (o.pieces > 1 ? o.pieces : 0);
   const size_t images = s.dtype == NYS_F32 && s.prefix_len > 0
                             ? images_of(s.kv_heads, s.d, s.dv, 1, s.prefix_len).end
                             : 0;
   o.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + images);
   o.part_lse = o.part + pieces * row * s.dv;
-  if (o.prefix_pieces > 0) {
+  if (o.shares.units > 0) {
     TileArgs a{};
     a.q_rows = s.n;
     a.k_rows = s.prefix_len;
@@ -177,7 +167,8 @@ cudaError_t launch_shared_tiled(const SharedArgs& s, void* workspace, cudaStream
     a.tp = kTileM / s.group;
     a.d = s.d;
     a.dv = s.dv;
-    a.splits = o.prefix_pieces;
+    a.splits = 1;
+    a.shares = o.shares;
     a.scale = s.scale;
     a.part = o.part;
     a.part_lse = o.part_lse;
@@ -194,8 +185,7 @@ cudaError_t launch_shared_tiled(const SharedArgs& s, void* workspace, cudaStream
     a.status = s.status;
     a.q = s.q;
     a.per = s.dtype == NYS_F32 ? 1 : 2;
-    const int64_t all = units * o.prefix_pieces;
-    const unsigned grid = (unsigned)(all < kSms ? all : kSms);
+    const unsigned grid = (unsigned)o.shares.ctas;
     cudaError_t e;
     if (s.dtype == NYS_F32) {
       place_images(a, workspace, 1, s.prefix_len);
@@ -214,8 +204,7 @@ cudaError_t launch_shared_tiled(const SharedArgs& s, void* workspace, cudaStream
   }
   const cudaError_t e = launch_own(s, o, stream);
   if (e != cudaSuccess || o.pieces == 1) return e;
-  JoinArgs j{o.part, o.part_lse, (int32_t)pieces, s.heads, s.dv, s.n, s.out, s.lse};
-  return launch_join(j, s.dtype, stream);
+  return launch_join(s, o, stream);
 }
 
 bool prompt_tc_fits(const PromptArgs& a) {

@@ -58,17 +58,27 @@ __device__ __forceinline__ void own_range(const SharedArgs& a, const OwnArgs& o,
   hi = (int)(h < len ? h : len);
 }
 
-// Row number (times KV heads) of key j of request b in the pool, -1 where its
-// page is not in it.
-__device__ __forceinline__ int64_t own_row(const SharedArgs& a, const int32_t* pages, int j) {
+constexpr uint32_t kNoRow = 0xffffffffu;
+
+// Row (slot x KV heads + KV head) of key j < hi of a request in the pool, kNoRow
+// past the end or where its page is not in the pool.
+__device__ __forceinline__ uint32_t own_row(const SharedArgs& a, const int32_t* pages, int j,
+                                            int hi, int kvh) {
+  if (j >= hi) return kNoRow;
   const int pi = j / a.page;
   const int32_t pg = pages[pi];
   if (pg < 0 || pg >= a.n_pages) {
     attn_report(a.status, NYS_ATTN_BAD_PAGE);
-    return -1;
+    return kNoRow;
   }
-  return (int64_t)pg * a.page + (j - pi * a.page);
+  return ((uint32_t)pg * a.page + (j - pi * a.page)) * a.kv_heads + kvh;
 }
+
+// A warp's keys come in blocks of 32 (block i of warp w: 32 (4 i + w) ..), whose
+// rows the lanes look up one block ahead.
+struct RowAhead {
+  uint32_t now = kNoRow, next = kNoRow;
+};
 
 template <typename T>
 __device__ __forceinline__ T narrow(float x);
@@ -85,6 +95,11 @@ __device__ __forceinline__ __half narrow<__half>(float x) {
   return __float2half_rn(x);
 }
 
+// Pieces of the prefix that request b's rows of a KV head have.
+__device__ __forceinline__ int prefix_pieces(const SharedArgs& a, const OwnArgs& o, int b, int kvh) {
+  return o.shares.units > 0 ? o.shares.pieces(b / o.shares.rows * a.kv_heads + kvh) : 0;
+}
+
 // Joins the warps' results (log2 maxima m and sums l [warp][head], O
 // [warp][head][dv]) and, where this CTA has all of the request's own keys, the
 // prefix's pieces; thread = column.  heads: of this CTA, from h0.
@@ -99,7 +114,7 @@ __device__ void join(const SharedArgs& a, const OwnArgs& o, const float* m, cons
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) top = fmaxf(top, m[w * HB + h]);
     // The prefix's pieces: lane = piece, log2 of their sums.
-    const int np = o.pieces == 1 ? o.prefix_pieces : 0;
+    const int np = o.pieces == 1 ? prefix_pieces(a, o, b, (h0 + h) / a.group) : 0;
     float pl[2] = {-INFINITY, -INFINITY};
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -158,7 +173,7 @@ __device__ void join(const SharedArgs& a, const OwnArgs& o, const float* m, cons
       }
       if (lane == 0 && a.lse) a.lse[row] = lse;
     } else {
-      const int64_t at = (int64_t)(o.prefix_pieces + piece) * rows + row;
+      const int64_t at = (int64_t)(o.shares.most + piece) * rows + row;
       if (col) *reinterpret_cast<float4*>(o.part + at * a.dv + lane * 4) = make_float4(y[0], y[1], y[2], y[3]);
       if (lane == 0) o.part_lse[at] = lse;
     }
@@ -224,25 +239,29 @@ __global__ void __launch_bounds__(kThreads, 2) own16_kernel(SharedArgs a, OwnArg
       *reinterpret_cast<uint4*>(sm + i) = make_uint4(0, 0, 0, 0);
     __syncthreads();
   }
-  // Tile t of this warp: keys lo + (t * kWarps + warp) * 16 ...
-  const int tiles = (hi - lo + kKeys16 - 1) / kKeys16;
-  const int mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
+  // Two tiles a block of 32 keys.
+  const int blocks32 = (hi - lo + 31) / 32;
+  const int mine = 2 * (blocks32 > warp ? (blocks32 - warp + kWarps - 1) / kWarps : 0);
+  auto key_of = [&](int t) { return lo + ((t >> 1) * kWarps + warp) * 32 + (t & 1) * kKeys16; };
+  RowAhead row;
+  row.next = own_row(a, pages, key_of(0) + lane, hi, kvh);
+  const unsigned char* kb = (const unsigned char*)a.k + (lane & 15) * 16;
+  const unsigned char* vb = (const unsigned char*)a.v + (lane & 15) * 16;
+  const bool kcol = (lane & 15) < dc, vcol = (lane & 15) < vc;
   auto fetch = [&](int t) {
     if (t < mine) {
-      unsigned char* st = ring + (t % kStages16) * kStage16;
-      const int j0 = lo + (t * kWarps + warp) * kKeys16;
-      // Lane l < 16 looks key l up; two lanes' worth of chunks a row follow.
-      int64_t row = -1;
-      if (lane < kKeys16 && j0 + lane < hi) row = own_row(a, pages, j0 + lane);
-      const int r0 = lane >> 4, c = lane & 15;
+      if (!(t & 1)) {
+        row.now = row.next;
+        row.next = own_row(a, pages, key_of(t + 2) + lane, hi, kvh);
+      }
+      const uint32_t st = sptr(ring + (t % kStages16) * kStage16) + (lane >> 4) * kRow16 + (lane & 15) * 16;
 #pragma unroll
       for (int i = 0; i < kKeys16; i += 2) {
-        const int64_t at = __shfl_sync(0xffffffffu, row, i + r0) * a.kv_heads + kvh;
-        const bool have = at >= 0;
-        const uint32_t d0 = sptr(st + (i + r0) * kRow16 + c * 16);
-        if (c < dc) cp16(d0, (const T*)a.k + (have ? at : 0) * a.d + c * 8, have);
-        if (c < vc)
-          cp16(d0 + kKeys16 * kRow16, (const T*)a.v + (have ? at : 0) * a.dv + c * 8, have);
+        const uint32_t at = __shfl_sync(0xffffffffu, row.now, (t & 1) * kKeys16 + i + (lane >> 4));
+        const bool have = at != kNoRow;
+        const uint64_t r = have ? at : 0;
+        if (kcol) cp16(st + i * kRow16, kb + r * (uint32_t)(a.d * 2), have);
+        if (vcol) cp16(st + (kKeys16 + i) * kRow16, vb + r * (uint32_t)(a.dv * 2), have);
       }
     }
     cp_commit();
@@ -277,17 +296,17 @@ __global__ void __launch_bounds__(kThreads, 2) own16_kernel(SharedArgs a, OwnArg
     cp_wait<kStages16 - 2>();
     __syncwarp();
     fetch(t + kStages16 - 1);
-    const uint32_t kb = sptr(ring + (t % kStages16) * kStage16), vb = kb + kKeys16 * kRow16;
+    const uint32_t ks_at = sptr(ring + (t % kStages16) * kStage16), vs_at = ks_at + kKeys16 * kRow16;
     float s[2][4] = {};
 #pragma unroll
     for (int k = 0; k < 8; ++k)
       if (k < ks) {
         uint32_t r[4];
-        ldsm4(r, kb + ((lane & 7) + (lane >> 4) * 8) * kRow16 + k * 32 + ((lane >> 3) & 1) * 16);
+        ldsm4(r, ks_at + ((lane & 7) + (lane >> 4) * 8) * kRow16 + k * 32 + ((lane >> 3) & 1) * 16);
         mma16<T>(s[0], q[k], r[0], r[1]);
         mma16<T>(s[1], q[k], r[2], r[3]);
       }
-    const int left = hi - (lo + (t * kWarps + warp) * kKeys16);  // keys of this tile
+    const int left = hi - key_of(t);  // keys of this tile
     uint32_t p[4];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {  // rows lane / 4 and lane / 4 + 8
@@ -327,13 +346,14 @@ __global__ void __launch_bounds__(kThreads, 2) own16_kernel(SharedArgs a, OwnArg
     for (int n = 0; n < 8; ++n)
       if (n < ns) {
         uint32_t r[4];
-        ldsm4t(r, vb + ((lane & 7) + ((lane >> 3) & 1) * 8) * kRow16 + n * 32 + (lane >> 4) * 16);
+        ldsm4t(r, vs_at + ((lane & 7) + ((lane >> 3) & 1) * 8) * kRow16 + n * 32 + (lane >> 4) * 16);
         mma16<T>(acc[2 * n], p, r[0], r[1]);
         mma16<T>(acc[2 * n + 1], p, r[2], r[3]);
       }
   }
   cp_wait<0>();
-  __syncthreads();  // the ring becomes the warps' results
+  wait_for_previous();  // the prefix's pieces, which this kernel ran beside
+  __syncthreads();      // the ring becomes the warps' results
   float* jm = reinterpret_cast<float*>(sm);
   float* jl = jm + kWarps * kHeads16;
   float* ja = jl + kWarps * kHeads16;
@@ -407,23 +427,28 @@ __global__ void __launch_bounds__(kThreads, 2) own32_kernel(SharedArgs a, OwnArg
   const int32_t* pages = a.table + (int64_t)b * a.width;
   const bool kcol = lane * 4 < a.d, vcol = lane * 4 < a.dv;
   unsigned char* ring = sm + warp * kStages32 * kStage32 + lane * 16;  // this lane's columns
-  const int tiles = (hi - lo + kKeys32 - 1) / kKeys32;
-  const int mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
+  // Four tiles a block of 32 keys.
+  const int blocks32 = (hi - lo + 31) / 32;
+  const int mine = 4 * (blocks32 > warp ? (blocks32 - warp + kWarps - 1) / kWarps : 0);
+  auto key_of = [&](int t) { return lo + ((t >> 2) * kWarps + warp) * 32 + (t & 3) * kKeys32; };
+  RowAhead row;
+  row.next = own_row(a, pages, key_of(0) + lane, hi, kvh);
+  const float4* kb = (const float4*)a.k + (kcol ? lane : 0);
+  const float4* vb = (const float4*)a.v + (vcol ? lane : 0);
   auto fetch = [&](int t) {
     if (t < mine) {
-      unsigned char* st = ring + (t % kStages32) * kStage32;
-      const int j0 = lo + (t * kWarps + warp) * kKeys32;
-      int64_t row = -1;
-      if (lane < kKeys32 && j0 + lane < hi) row = own_row(a, pages, j0 + lane);
+      if (!(t & 3)) {
+        row.now = row.next;
+        row.next = own_row(a, pages, key_of(t + 4) + lane, hi, kvh);
+      }
+      const uint32_t st = sptr(ring + (t % kStages32) * kStage32);
 #pragma unroll
       for (int i = 0; i < kKeys32; ++i) {
-        const int64_t at = __shfl_sync(0xffffffffu, row, i) * a.kv_heads + kvh;
-        const bool have = at >= 0;
-        if (kcol)
-          cp16(sptr(st + i * 512), (const float*)a.k + (have ? at : 0) * a.d + lane * 4, have);
-        if (vcol)
-          cp16(sptr(st + (kKeys32 + i) * 512), (const float*)a.v + (have ? at : 0) * a.dv + lane * 4,
-               have);
+        const uint32_t at = __shfl_sync(0xffffffffu, row.now, (t & 3) * kKeys32 + i);
+        const bool have = at != kNoRow;
+        const uint64_t r = have ? at : 0;
+        if (kcol) cp16(st + i * 512, kb + r * (uint32_t)(a.d >> 2), have);
+        if (vcol) cp16(st + (kKeys32 + i) * 512, vb + r * (uint32_t)(a.dv >> 2), have);
       }
     }
     cp_commit();
@@ -432,16 +457,17 @@ __global__ void __launch_bounds__(kThreads, 2) own32_kernel(SharedArgs a, OwnArg
   for (int t = 0; t < kStages32 - 1; ++t) fetch(t);
 
   const float sc = a.scale * kLog2e;
-  float4 q[HT], acc[HT];
+  uint64_t q[HT][2], acc[HT][2];  // four columns as two pairs
 #pragma unroll
   for (int h = 0; h < HT; ++h) {
-    q[h] = acc[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+    q[h][0] = q[h][1] = acc[h][0] = acc[h][1] = pair(0.f, 0.f);
     if (h < heads && kcol) {
       const float* p = (const float*)a.q.p + b * a.q.row + (h0 + h) * a.q.head + lane * 4;
-      q[h] = make_float4(p[0] * sc, p[1] * sc, p[2] * sc, p[3] * sc);
+      q[h][0] = pair(p[0] * sc, p[1] * sc);
+      q[h][1] = pair(p[2] * sc, p[3] * sc);
     }
   }
-  const int val = lane / kRep, key_of = val % KB;  // this lane's (head, key)
+  const int my_key = lane / kRep % KB;  // of this lane's (head, key) pair
   float m = -INFINITY, l = 0.f;                    // of this lane's head
   for (int t = 0; t < mine; ++t) {
     cp_wait<kStages32 - 2>();  // (each lane reads back what it copied itself)
@@ -449,18 +475,21 @@ __global__ void __launch_bounds__(kThreads, 2) own32_kernel(SharedArgs a, OwnArg
     const unsigned char* st = ring + (t % kStages32) * kStage32;
 #pragma unroll
     for (int g = 0; g < kKeys32; g += KB) {
-      const int left = hi - (lo + (t * kWarps + warp) * kKeys32) - g;
+      const int left = hi - key_of(t) - g;
       float x[V];
 #pragma unroll
       for (int i = 0; i < KB; ++i) {
         const float4 k = kcol ? *reinterpret_cast<const float4*>(st + (g + i) * 512)
                               : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int h = 0; h < HT; ++h)
-          x[h * KB + i] = fmaf(q[h].x, k.x, fmaf(q[h].y, k.y, fmaf(q[h].z, k.z, q[h].w * k.w)));
+        for (int h = 0; h < HT; ++h) {
+          float x0, x1;
+          unpair(fma2(q[h][0], pair(k.x, k.y), mul2(q[h][1], pair(k.z, k.w))), x0, x1);
+          x[h * KB + i] = x0 + x1;
+        }
       }
       float s = sum_multi<V>(x, lane);
-      if (key_of >= left) s = -INFINITY;
+      if (my_key >= left) s = -INFINITY;
       float top = s;
 #pragma unroll
       for (int off = kRep * KB / 2; off >= kRep; off >>= 1)
@@ -474,10 +503,8 @@ __global__ void __launch_bounds__(kThreads, 2) own32_kernel(SharedArgs a, OwnArg
 #pragma unroll
         for (int h = 0; h < HT; ++h) {
           const float fh = __shfl_sync(0xffffffffu, f, h * KB * kRep);
-          acc[h].x *= fh;
-          acc[h].y *= fh;
-          acc[h].z *= fh;
-          acc[h].w *= fh;
+          acc[h][0] = mul2(acc[h][0], pair(fh, fh));
+          acc[h][1] = mul2(acc[h][1], pair(fh, fh));
         }
       }
       const float p = ex2(s - (m == -INFINITY ? 0.f : m));
@@ -489,10 +516,8 @@ __global__ void __launch_bounds__(kThreads, 2) own32_kernel(SharedArgs a, OwnArg
 #pragma unroll
         for (int h = 0; h < HT; ++h) {
           const float w = __shfl_sync(0xffffffffu, p, (h * KB + i) * kRep);
-          acc[h].x = fmaf(w, v.x, acc[h].x);
-          acc[h].y = fmaf(w, v.y, acc[h].y);
-          acc[h].z = fmaf(w, v.z, acc[h].z);
-          acc[h].w = fmaf(w, v.w, acc[h].w);
+          acc[h][0] = fma2(pair(w, w), pair(v.x, v.y), acc[h][0]);
+          acc[h][1] = fma2(pair(w, w), pair(v.z, v.w), acc[h][1]);
         }
       }
     }
@@ -501,6 +526,7 @@ __global__ void __launch_bounds__(kThreads, 2) own32_kernel(SharedArgs a, OwnArg
 #pragma unroll
   for (int off = kRep * KB / 2; off >= kRep; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
   cp_wait<0>();
+  wait_for_previous();
   __syncthreads();
   float* jm = reinterpret_cast<float*>(sm);
   float* jl = jm + kWarps * HT;
@@ -511,32 +537,49 @@ __global__ void __launch_bounds__(kThreads, 2) own32_kernel(SharedArgs a, OwnArg
       jm[warp * HT + h] = m;
       jl[warp * HT + h] = l;
     }
-    if (vcol) *reinterpret_cast<float4*>(ja + (warp * HT + h) * a.dv + lane * 4) = acc[h];
+    if (vcol)
+      *reinterpret_cast<ulonglong2*>(ja + (warp * HT + h) * a.dv + lane * 4) =
+          make_ulonglong2(acc[h][0], acc[h][1]);
   }
   __syncthreads();
   join<float, HT>(a, o, jm, jl, ja, b, h0, heads, piece);
 }
 
-// Joins `pieces` partial results of each row; one warp a row.
+// Joins the prefix's and the own pieces of each row; one warp a row.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) join_kernel(JoinArgs a) {
+__global__ void __launch_bounds__(kThreads) join_kernel(SharedArgs a, OwnArgs o) {
   const int lane = threadIdx.x & 31;
-  const int64_t rows = a.rows * a.heads;
+  const int64_t rows = (int64_t)a.n * a.heads;
   for (int64_t r = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); r < rows;
        r += (int64_t)gridDim.x * kWarps) {
-    float top = -INFINITY;
-    for (int p = lane; p < a.pieces; p += 32) top = fmaxf(top, a.part_lse[p * rows + r]);
+    const int b = (int)(r / a.heads), h = (int)(r - (int64_t)b * a.heads);
+    const int np = prefix_pieces(a, o, b, h / a.group), all = np + o.pieces;
+    auto place = [&](int p) { return (int64_t)(p < np ? p : o.shares.most + p - np) * rows + r; };
+    // Lane = piece (at most 128): its weight against the largest.
+    float w[4], top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[i] = lane + 32 * i < all ? o.part_lse[place(lane + 32 * i)] * kLog2e : -INFINITY;
+      top = fmaxf(top, w[i]);
+    }
 #pragma unroll
     for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
     const float ref = top == -INFINITY ? 0.f : top;
     float total = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[i] = ex2(w[i] - ref);
+      total += w[i];
+    }
+#pragma unroll
+    for (int s = 16; s; s >>= 1) total += __shfl_xor_sync(0xffffffffu, total, s);
     float y[4] = {0.f, 0.f, 0.f, 0.f};
     const bool col = lane * 4 < a.dv;
-    for (int p = 0; p < a.pieces; ++p) {
-      const float f = ex2((a.part_lse[p * rows + r] - ref) * kLog2e);
-      total += f;
+#pragma unroll 4
+    for (int p = 0; p < all; ++p) {
+      const float f = __shfl_sync(0xffffffffu, p < 32 ? w[0] : p < 64 ? w[1] : p < 96 ? w[2] : w[3], p & 31);
       if (col && f != 0.f) {
-        const float4 x = *reinterpret_cast<const float4*>(a.part + (p * rows + r) * a.dv + lane * 4);
+        const float4 x = *reinterpret_cast<const float4*>(o.part + place(p) * a.dv + lane * 4);
         y[0] = fmaf(x.x, f, y[0]);
         y[1] = fmaf(x.y, f, y[1]);
         y[2] = fmaf(x.z, f, y[2]);
@@ -544,14 +587,13 @@ __global__ void __launch_bounds__(kThreads) join_kernel(JoinArgs a) {
       }
     }
     const float inv = total == 0.f ? 0.f : 1.f / total;
-    const int64_t row = r / a.heads;
-    const int h = (int)(r - row * a.heads);
     if (col) {
-      T* out = (T*)a.out.p + row * a.out.row + h * a.out.head + lane * 4;
+      T* out = (T*)a.out.p + b * a.out.row + h * a.out.head + lane * 4;
 #pragma unroll
       for (int i = 0; i < 4; ++i) out[i] = narrow<T>(y[i] * inv);
     }
-    if (lane == 0 && a.lse) a.lse[r] = total == 0.f ? -INFINITY : top + logf(total);
+    if (lane == 0 && a.lse)
+      a.lse[r] = total == 0.f ? -INFINITY : fmaf(top, 0.6931471805599453f, logf(total));
   }
 }
 
@@ -560,13 +602,20 @@ cudaError_t allow(K kernel, int bytes) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
+// Beside the prefix's launch where there is one.
+cudaError_t launch_own_kernel(void (*kernel)(SharedArgs, OwnArgs), dim3 grid, size_t smem,
+                              cudaStream_t stream, const SharedArgs& a, const OwnArgs& o) {
+  if (o.shares.units > 0) return launch_dependent(kernel, grid, kThreads, smem, stream, a, o);
+  kernel<<<grid, kThreads, smem, stream>>>(a, o);
+  return cudaGetLastError();
+}
+
 template <int HT>
 cudaError_t launch32(const SharedArgs& a, const OwnArgs& o, cudaStream_t stream) {
   static const cudaError_t ready = allow(own32_kernel<HT>, kSmem32);
   if (ready != cudaSuccess) return ready;
   const dim3 grid((unsigned)(a.n * o.pieces), (unsigned)(a.kv_heads * ((a.group + HT - 1) / HT)));
-  own32_kernel<HT><<<grid, kThreads, kSmem32, stream>>>(a, o);
-  return cudaGetLastError();
+  return launch_own_kernel(own32_kernel<HT>, grid, kSmem32, stream, a, o);
 }
 template <typename T>
 cudaError_t launch16(const SharedArgs& a, const OwnArgs& o, cudaStream_t stream) {
@@ -574,8 +623,7 @@ cudaError_t launch16(const SharedArgs& a, const OwnArgs& o, cudaStream_t stream)
   if (ready != cudaSuccess) return ready;
   const dim3 grid((unsigned)(a.n * o.pieces),
                   (unsigned)(a.kv_heads * ((a.group + kHeads16 - 1) / kHeads16)));
-  own16_kernel<T><<<grid, kThreads, kSmem16, stream>>>(a, o);
-  return cudaGetLastError();
+  return launch_own_kernel(own16_kernel<T>, grid, kSmem16, stream, a, o);
 }
 
 }  // namespace
@@ -589,14 +637,12 @@ cudaError_t launch_own(const SharedArgs& a, const OwnArgs& o, cudaStream_t strea
                         : launch32<8>(a, o, stream);
 }
 
-cudaError_t launch_join(const JoinArgs& a, int dtype, cudaStream_t stream) {
-  const int64_t warps = a.rows * a.heads;
-  if (warps == 0) return cudaSuccess;
-  const int64_t want = (warps + kWarps - 1) / kWarps;
+cudaError_t launch_join(const SharedArgs& a, const OwnArgs& o, cudaStream_t stream) {
+  const int64_t want = ((int64_t)a.n * a.heads + kWarps - 1) / kWarps;
   const unsigned grid = (unsigned)(want < 152 * 16 ? want : 152 * 16);
-  if (dtype == NYS_F32) join_kernel<float><<<grid, kThreads, 0, stream>>>(a);
-  else if (dtype == NYS_BF16) join_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(a);
-  else join_kernel<__half><<<grid, kThreads, 0, stream>>>(a);
+  if (a.dtype == NYS_F32) join_kernel<float><<<grid, kThreads, 0, stream>>>(a, o);
+  else if (a.dtype == NYS_BF16) join_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(a, o);
+  else join_kernel<__half><<<grid, kThreads, 0, stream>>>(a, o);
   return cudaGetLastError();
 }
 

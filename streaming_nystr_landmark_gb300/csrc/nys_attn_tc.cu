@@ -273,14 +273,16 @@ __device__ void mma_role(const TileArgs& a, Shared& sh, unsigned char* sm, uint3
 __device__ void unit_role(const TileArgs& a, Shared& sh, int lane) {
   volatile int* ab = &sh.abort;
   UnitWalk walk;
-  walk.load(a, lane);
+  if (a.q_off) walk.load(a, lane);
   for (uint32_t nu = 0;; ++nu) {
-    // Every other round runs backwards, so that no CTA gets the longer unit of
-    // every round.
-    const int32_t w = nu * gridDim.x +
-                      ((nu & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
     Unit u;
-    walk.get(a, w, lane, u);
+    if (a.q_off) {
+      // Every other round runs backwards, so that no CTA gets the longer unit
+      // of every round.
+      walk.get(a, nu * gridDim.x + ((nu & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x), lane, u);
+    } else {
+      prefix_unit(a, blockIdx.x, nu, u);
+    }
     if (!bar_wait_warp(&sh.u_empty[nu % kUnitRing], ((nu / kUnitRing) & 1) ^ 1, ab)) return;
     if (lane == 0) {
       sh.unit[nu % kUnitRing] = u;
@@ -610,6 +612,7 @@ attn_tc_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CUten
   __syncthreads();
   fence_after();
   const uint32_t tmem = sh.tmem;
+  let_next_start();
   if (warp < 8) {
     more_regs<kRegsRow>();
     row_role<T, PAGED>(a, sh, tmem, warp >> 2, tid & 127, lane);

@@ -11,6 +11,25 @@ constexpr int kTileM = 128;  // rows of a query tile: (position, head of the gro
 constexpr int kTileN = 128;  // keys of a tile
 constexpr int kUnitRing = 4;
 
+// How a prefix's key tiles are dealt out.  A unit (query tiles of one KV head)
+// has nt tiles; the units' tiles, one after another, are cut into `ctas` equal
+// shares, so that every CTA has the same work whatever the numbers; a unit's
+// share with a CTA is a piece.
+struct Shares {
+  int32_t nt, ctas, units, rows;  // rows: requests of a unit
+  int32_t most;                   // pieces of a unit, at most
+  // The CTA that has tile t of all.
+  __host__ __device__ int cta_of(int64_t t) const {
+    return (int)(((t + 1) * ctas - 1) / ((int64_t)units * nt));
+  }
+  __host__ __device__ int64_t begin(int cta) const {
+    return (int64_t)cta * units * nt / ctas;
+  }
+  __host__ __device__ int pieces(int unit) const {
+    return cta_of((int64_t)(unit + 1) * nt - 1) - cta_of((int64_t)unit * nt) + 1;
+  }
+};
+
 // Exponents of one f32 tile of one KV head, for each group of 16 keys: keys are
 // stored as k 2^-ek (k_mul = 2^ek), values as v 2^-ev.
 struct TileExps {
@@ -35,7 +54,8 @@ struct TileArgs {
   int32_t heads, kv_heads, group, tp;  // tp: positions of a query tile, 128 / group
   int32_t d, dv;
   int32_t per;     // query tiles of a unit: 2, or 1 (f32)
-  int32_t splits;  // pieces that each unit's keys are cut into
+  int32_t splits;  // 1: results go to `part` as pieces (prefix)
+  Shares shares;   // prefix
   float scale;
   Rows q;               // (f32; the 16-bit kernel reads it by its map)
   Rows out;             // results, where splits == 0
@@ -80,19 +100,12 @@ struct TileMaps {
   CUtensorMap q, k, v;
 };
 
-// A request's own keys: how many pieces they are cut into, how many the
-// prefix was, and the pieces' results (the prefix's first).
+// A request's own keys: how many pieces they are cut into, and all pieces'
+// results: the prefix's in places 0 .. shares.most - 1, then the own ones.
 struct OwnArgs {
-  int32_t pieces, prefix_pieces;
+  Shares shares;  // units == 0: no prefix
+  int32_t pieces;
   float *part, *part_lse;
-};
-
-struct JoinArgs {
-  const float *part, *part_lse;
-  int32_t pieces, heads, dv;
-  int64_t rows;
-  Rows out;
-  float* lse;
 };
 
 // Workspace of the tiled kernels: nys_attn_prompt with n sequences of `rows` query
@@ -103,7 +116,7 @@ size_t shared_workspace(const nys_attn_config& c, int64_t n, int64_t keys);
 bool shared_tiled_fits(const SharedArgs& a);
 cudaError_t launch_shared_tiled(const SharedArgs& a, void* workspace, cudaStream_t stream);
 cudaError_t launch_own(const SharedArgs& a, const OwnArgs& o, cudaStream_t stream);
-cudaError_t launch_join(const JoinArgs& a, int dtype, cudaStream_t stream);
+cudaError_t launch_join(const SharedArgs& a, const OwnArgs& o, cudaStream_t stream);
 
 // Whether the tiled kernels take a prompt batch, and its launch.
 bool prompt_tc_fits(const PromptArgs& a);
@@ -115,6 +128,24 @@ cudaError_t launch_attn_tc32(const TileArgs& a, unsigned grid, cudaStream_t stre
 
 
 #ifdef __CUDACC__
+// Launches `kernel` as a programmatic dependent of the launch before it: its
+// CTAs may start while that one's last ones run, and wait for it themselves.
+template <typename... P, typename... Q>
+inline cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem,
+                                    cudaStream_t stream, Q... args) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, args...);
+}
+
 // Values that are not finite are 0 in what the products read; the rows that see
 // their keys get them here, after their results were written: `out` is this
 // thread's row, x += z (infinities stay, opposite ones and NaN give NaN).
@@ -139,18 +170,13 @@ struct UnitWalk {
     const int i = s0 + lane;
     q0 = nq = k0 = nk = 0;
     if (i < a.n) {
-      if (a.q_off) {
-        bool bad = false;
-        seq_range(a.q_off, i, a.q_rows, q0, nq, bad);
-        seq_range(a.k_off, i, a.k_rows, k0, nk, bad);
-        if (bad) attn_report(a.status, NYS_ATTN_BAD_OFFSETS);
-      } else {
-        nq = (int)a.q_rows;
-        nk = (int)a.k_rows;
-      }
+      bool bad = false;
+      seq_range(a.q_off, i, a.q_rows, q0, nq, bad);
+      seq_range(a.k_off, i, a.k_rows, k0, nk, bad);
+      if (bad) attn_report(a.status, NYS_ATTN_BAD_OFFSETS);
     }
     pairs = (nq + a.per * a.tp - 1) / (a.per * a.tp);
-    count = pairs * a.kv_heads * (a.splits ? a.splits : 1);
+    count = pairs * a.kv_heads;
     upto = count;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -176,10 +202,8 @@ struct UnitWalk {
     const int sq0 = __shfl_sync(0xffffffffu, q0, src), snq = __shfl_sync(0xffffffffu, nq, src);
     const int sk0 = __shfl_sync(0xffffffffu, k0, src), snk = __shfl_sync(0xffffffffu, nk, src);
     const int spairs = __shfl_sync(0xffffffffu, pairs, src);
-    int32_t r = w - before - __shfl_sync(0xffffffffu, upto - count, src);
-    const int ns = a.splits ? a.splits : 1;
-    u.split = r % ns;
-    r /= ns;
+    const int32_t r = w - before - __shfl_sync(0xffffffffu, upto - count, src);
+    u.split = 0;
     u.kvh = r % a.kv_heads;
     const int pair = spairs - 1 - r / a.kv_heads;
     const int p0 = pair * a.per * a.tp;
@@ -190,21 +214,54 @@ struct UnitWalk {
     u.k_row = sk0;
     u.tile = seq_tile(sk0, s0 + src);
     // Keys that the first position sees, and the last of each tile.
-    u.lim = a.causal ? p0 + 1 + snk - snq : snk;
-    const int e0 = a.causal ? u.lim + u.np0 - 1 : snk;
-    const int e1 = a.causal ? e0 + u.np1 : snk;
+    u.lim = p0 + 1 + snk - snq;
+    const int e0 = u.lim + u.np0 - 1, e1 = e0 + u.np1;
     const int t0 = (min(max(e0, 0), snk) + kTileN - 1) / kTileN;
     const int t1 = (min(max(e1, 0), snk) + kTileN - 1) / kTileN;  // t1 >= t0
-    const int tb = (int)((int64_t)t1 * u.split / ns), te = (int)((int64_t)t1 * (u.split + 1) / ns);
-    u.kb = tb * kTileN;
-    u.tile += tb;
-    u.nt = te - tb;
-    u.nt0 = min(max(t0 - tb, 0), u.nt);
-    u.nkl = min(snk, te * kTileN);
+    u.kb = 0;
+    u.nt = t1;
+    u.nt0 = t0;
+    u.nkl = snk;
     u.edge = max(min(u.lim, u.nkl) - u.kb, 0) / kTileN;
     u.valid = 1;
   }
 };
+
+// Piece k of CTA `cta`'s share of a prefix; u.valid == 0 past the last.
+__device__ __forceinline__ void prefix_unit(const TileArgs& a, int cta, int k, Unit& u) {
+  u.valid = 0;
+  u.patch = 0;
+  const Shares& s = a.shares;
+  const int64_t t0 = s.begin(cta), t1 = s.begin(cta + 1);
+  const int unit = (int)(t0 / s.nt) + k;
+  const int64_t first = (int64_t)unit * s.nt;
+  if (first >= t1) return;
+  const int tb = (int)(t0 > first ? t0 - first : 0);
+  const int te = (int)(t1 - first < s.nt ? t1 - first : s.nt);
+  const int p0 = unit / a.kv_heads * s.rows, left = (int)a.q_rows - p0;
+  u.kvh = unit % a.kv_heads;
+  u.np0 = min(left, a.tp);
+  u.np1 = a.per == 2 ? min(max(left - a.tp, 0), a.tp) : 0;
+  u.q_row = p0;
+  u.k_row = 0;
+  u.lim = (int)a.k_rows;
+  u.kb = tb * kTileN;
+  u.tile = tb;
+  u.nt = u.nt0 = te - tb;
+  u.nkl = min((int)a.k_rows, te * kTileN);
+  u.edge = (u.nkl - u.kb) / kTileN;
+  u.split = cta - s.cta_of(first);
+  u.valid = 1;
+}
+
+// The kernel launched next (a programmatic dependent) may start; and: all that
+// kernels before this one wrote is visible.
+__device__ __forceinline__ void let_next_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
 #endif
 
 }  // namespace nys

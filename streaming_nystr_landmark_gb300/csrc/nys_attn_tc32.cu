@@ -378,6 +378,7 @@ __device__ void query_role(const TileArgs& a, Shared& sh, unsigned char* turn, u
 // K and V as tile images.  Grid: tiles x KV heads, K and V; a warp takes 16 rows.
 template <bool PAGED>
 __global__ void __launch_bounds__(256) split_kernel(const __grid_constant__ TileArgs a) {
+  let_next_start();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool is_v = blockIdx.y != 0;
   const int64_t at = blockIdx.x;  // tile * kv_heads + KV head
@@ -540,12 +541,16 @@ __device__ void mma_role(const TileArgs& a, Shared& sh, unsigned char* sm, uint3
 __device__ void unit_role(const TileArgs& a, Shared& sh, int lane) {
   volatile int* ab = &sh.abort;
   UnitWalk walk;
-  walk.load(a, lane);
+  if (a.q_off) walk.load(a, lane);
   for (uint32_t nu = 0;; ++nu) {
-    const int32_t w = nu * gridDim.x +
-                      ((nu & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
     Unit u;
-    walk.get(a, w, lane, u);
+    if (a.q_off) {
+      // Every other round runs backwards, so that no CTA gets the longer unit
+      // of every round.
+      walk.get(a, nu * gridDim.x + ((nu & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x), lane, u);
+    } else {
+      prefix_unit(a, blockIdx.x, nu, u);
+    }
     if (u.valid) {  // does a tile hold values that are not finite?
       uint64_t odd = 0;
 #pragma unroll 4
@@ -790,6 +795,8 @@ attn_tc32_kernel(const __grid_constant__ TileArgs a) {
   __syncthreads();
   fence_after();
   const uint32_t tmem = sh.tmem;
+  let_next_start();
+  wait_for_previous();  // the images
   if (warp < 8) {
     more_regs<kRegsRow>();
     row_role(a, sh, tmem, tid & 127, warp >> 2, lane);
@@ -823,8 +830,7 @@ cudaError_t launch_t(const TileArgs& a, unsigned grid, cudaStream_t stream) {
   if (ready != cudaSuccess) return ready;
   const dim3 images((unsigned)(key_tiles(a.k_rows, a.k_off ? a.n : 1) * a.kv_heads), 2);
   split_kernel<PAGED><<<images, 256, 0, stream>>>(a);
-  attn_tc32_kernel<PAGED><<<grid, kThreads, kSmem, stream>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(attn_tc32_kernel<PAGED>, grid, kThreads, kSmem, stream, a);
 }
 
 }  // namespace
