@@ -42,20 +42,19 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// The piece of request b's keys that this CTA reads: [lo, hi).
-__device__ __forceinline__ void own_range(const SharedArgs& a, const OwnArgs& o, int b, int piece,
+// Request b's length, held inside its table.
+__device__ __forceinline__ int own_len(const SharedArgs& a, int b, bool report) {
+  const int len = a.lens[b], cap = a.width * a.page;
+  if (report && (len < 0 || len > cap)) attn_report(a.status, NYS_ATTN_BAD_LENGTH);
+  return len < 0 ? 0 : (len > cap ? cap : len);
+}
+// The piece of its keys that this CTA reads, [lo, hi); false: there is none.
+__device__ __forceinline__ bool own_range(const SharedArgs& a, const OwnArgs& o, int b, int piece,
                                           int& lo, int& hi) {
-  int64_t len = a.lens[b];
-  const int64_t cap = (int64_t)a.width * a.page;
-  if (len < 0 || len > cap) {
-    attn_report(a.status, NYS_ATTN_BAD_LENGTH);
-    len = len < 0 ? 0 : cap;
-  }
-  // Whole 64-key steps, so that the four warps share a piece evenly.
-  const int64_t steps = (len + 63) / 64;
-  lo = (int)(steps * piece / o.pieces * 64);
-  const int64_t h = steps * (piece + 1) / o.pieces * 64;
-  hi = (int)(h < len ? h : len);
+  const int len = own_len(a, b, true);
+  lo = piece * o.keys;
+  hi = min(len, lo + o.keys);
+  return o.pieces == 1 || lo < hi;
 }
 
 constexpr uint32_t kNoRow = 0xffffffffu;
@@ -152,6 +151,7 @@ __device__ void join(const SharedArgs& a, const OwnArgs& o, const float* m, cons
         y[3] = fmaf(x.w, wf[w], y[3]);
       }
     }
+#pragma unroll 4
     for (int p = 0; p < np; ++p) {
       const float f = __shfl_sync(0xffffffffu, p < 32 ? pf[0] : pf[1], p & 31);
       if (col && f != 0.f) {
@@ -183,7 +183,7 @@ __device__ void join(const SharedArgs& a, const OwnArgs& o, const float* m, cons
 // ------------------------------------------------------------ bf16 and fp16
 constexpr int kHeads16 = 16;      // MMA rows: heads of a CTA
 constexpr int kKeys16 = 16;       // keys of a warp's tile
-constexpr int kStages16 = 3;
+constexpr int kStages16 = 2;
 constexpr int kRow16 = 272;       // bytes of a row in shared memory: 256 + 16, conflict-free
 constexpr int kStage16 = 2 * kKeys16 * kRow16;
 constexpr int kSmem16 = kWarps * kStages16 * kStage16;
@@ -219,7 +219,7 @@ __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uin
 
 // Grid: x = pieces, y = KV heads x blocks of 16 heads, z-major requests in x.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) own16_kernel(SharedArgs a, OwnArgs o) {
+__global__ void __launch_bounds__(kThreads, 3) own16_kernel(SharedArgs a, OwnArgs o) {
   extern __shared__ __align__(128) unsigned char sm[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int piece = blockIdx.x % o.pieces, b = blockIdx.x / o.pieces;
@@ -228,7 +228,11 @@ __global__ void __launch_bounds__(kThreads, 2) own16_kernel(SharedArgs a, OwnArg
   const int h0 = kvh * a.group + hb * kHeads16;
   const int heads = min(kHeads16, a.group - hb * kHeads16);
   int lo, hi;
-  own_range(a, o, b, piece, lo, hi);
+  let_next_start();
+  if (!own_range(a, o, b, piece, lo, hi)) {
+    wait_for_previous();
+    return;
+  }
   const int32_t* pages = a.table + (int64_t)b * a.width;
   const int dc = a.d >> 3, vc = a.dv >> 3;  // 16-byte chunks of a row
   const int ks = (a.d + 15) >> 4, ns = (a.dv + 15) >> 4;
@@ -382,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 2) own16_kernel(SharedArgs a, OwnArg
 
 // --------------------------------------------------------------------- f32
 constexpr int kKeys32 = 8;
-constexpr int kStages32 = 3;
+constexpr int kStages32 = 2;
 constexpr int kStage32 = 2 * kKeys32 * 512;
 constexpr int kSmem32 = kWarps * kStages32 * kStage32;
 
@@ -411,7 +415,7 @@ __device__ __forceinline__ float sum_multi(float (&x)[V], int lane) {
 // HT heads at a time.  A value is (head, key) = head * KB + key: its lanes
 // are the top bits of the lane number, so a head's keys are neighbours.
 template <int HT>
-__global__ void __launch_bounds__(kThreads, 2) own32_kernel(SharedArgs a, OwnArgs o) {
+__global__ void __launch_bounds__(kThreads, 3) own32_kernel(SharedArgs a, OwnArgs o) {
   extern __shared__ __align__(128) unsigned char sm[];
   constexpr int KB = HT == 8 ? 4 : 8;  // keys of one butterfly
   constexpr int V = HT * KB;
@@ -423,7 +427,11 @@ __global__ void __launch_bounds__(kThreads, 2) own32_kernel(SharedArgs a, OwnArg
   const int h0 = kvh * a.group + hb * HT;
   const int heads = min(HT, a.group - hb * HT);
   int lo, hi;
-  own_range(a, o, b, piece, lo, hi);
+  let_next_start();
+  if (!own_range(a, o, b, piece, lo, hi)) {
+    wait_for_previous();
+    return;
+  }
   const int32_t* pages = a.table + (int64_t)b * a.width;
   const bool kcol = lane * 4 < a.d, vcol = lane * 4 < a.dv;
   unsigned char* ring = sm + warp * kStages32 * kStage32 + lane * 16;  // this lane's columns
@@ -548,12 +556,13 @@ __global__ void __launch_bounds__(kThreads, 2) own32_kernel(SharedArgs a, OwnArg
 // Joins the prefix's and the own pieces of each row; one warp a row.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) join_kernel(SharedArgs a, OwnArgs o) {
+  wait_for_previous();
   const int lane = threadIdx.x & 31;
   const int64_t rows = (int64_t)a.n * a.heads;
   for (int64_t r = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); r < rows;
        r += (int64_t)gridDim.x * kWarps) {
     const int b = (int)(r / a.heads), h = (int)(r - (int64_t)b * a.heads);
-    const int np = prefix_pieces(a, o, b, h / a.group), all = np + o.pieces;
+    const int np = prefix_pieces(a, o, b, h / a.group), own = (own_len(a, b, false) + o.keys - 1) / o.keys, all = np + own;
     auto place = [&](int p) { return (int64_t)(p < np ? p : o.shares.most + p - np) * rows + r; };
     // Lane = piece (at most 128): its weight against the largest.
     float w[4], top = -INFINITY;
@@ -575,7 +584,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(SharedArgs a, OwnArgs o)
     for (int s = 16; s; s >>= 1) total += __shfl_xor_sync(0xffffffffu, total, s);
     float y[4] = {0.f, 0.f, 0.f, 0.f};
     const bool col = lane * 4 < a.dv;
-#pragma unroll 4
+#pragma unroll 8
     for (int p = 0; p < all; ++p) {
       const float f = __shfl_sync(0xffffffffu, p < 32 ? w[0] : p < 64 ? w[1] : p < 96 ? w[2] : w[3], p & 31);
       if (col && f != 0.f) {
@@ -640,10 +649,10 @@ cudaError_t launch_own(const SharedArgs& a, const OwnArgs& o, cudaStream_t strea
 cudaError_t launch_join(const SharedArgs& a, const OwnArgs& o, cudaStream_t stream) {
   const int64_t want = ((int64_t)a.n * a.heads + kWarps - 1) / kWarps;
   const unsigned grid = (unsigned)(want < 152 * 16 ? want : 152 * 16);
-  if (a.dtype == NYS_F32) join_kernel<float><<<grid, kThreads, 0, stream>>>(a, o);
-  else if (a.dtype == NYS_BF16) join_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(a, o);
-  else join_kernel<__half><<<grid, kThreads, 0, stream>>>(a, o);
-  return cudaGetLastError();
+  void (*kernel)(SharedArgs, OwnArgs) = a.dtype == NYS_F32    ? join_kernel<float>
+                                        : a.dtype == NYS_BF16 ? join_kernel<__nv_bfloat16>
+                                                              : join_kernel<__half>;
+  return launch_dependent(kernel, grid, kThreads, 0, stream, a, o);
 }
 
 }  // namespace nys

@@ -100,11 +100,12 @@ struct TileMaps {
   CUtensorMap q, k, v;
 };
 
-// A request's own keys: how many pieces they are cut into, and all pieces'
-// results: the prefix's in places 0 .. shares.most - 1, then the own ones.
+// A request's own keys: pieces of `keys` keys each, at most `pieces` (1: all of
+// them, and the result is final), and all pieces' results: the prefix's in
+// places 0 .. shares.most - 1, then the own ones.
 struct OwnArgs {
   Shares shares;  // units == 0: no prefix
-  int32_t pieces;
+  int32_t pieces, keys;
   float *part, *part_lse;
 };
 
