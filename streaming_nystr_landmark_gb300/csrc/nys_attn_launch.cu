@@ -66,7 +66,8 @@ int64_t div_up(int64_t x, int64_t y) { return (x + y - 1) / y; }
 int clamp_int(int64_t x, int lo, int hi) { return (int)(x < lo ? lo : (x > hi ? hi : x)); }
 
 // How a prefix of `tiles` key tiles is dealt out: an even share for each SM, but
-// at least two tiles a CTA (a CTA's start costs about three tiles' time) and no
+// at least two tiles a CTA (a CTA's start costs about three tiles' time; four in
+// f32, where the own pages are read beside it on the SMs that it leaves) and no
 // more pieces of a unit than the join takes.  tiles == 0: the most pieces that
 // any prefix can have (bounds the workspace by the batch alone).
 Shares shares_of(int64_t n, int kv_heads, int group, int dtype, int64_t tiles) {
@@ -77,7 +78,8 @@ Shares shares_of(int64_t n, int kv_heads, int group, int dtype, int64_t tiles) {
   const int64_t all = (int64_t)s.units * s.nt;
   int64_t ctas = kSms;
   if (ctas > (int64_t)s.units * (kMostPieces - 2)) ctas = (int64_t)s.units * (kMostPieces - 2);
-  if (ctas > div_up(all, 2)) ctas = div_up(all, 2);
+  const int least = dtype == NYS_F32 ? 4 : 2;
+  if (ctas > div_up(all, least)) ctas = div_up(all, least);
   s.ctas = (int32_t)ctas;
   s.most = (int32_t)div_up(ctas, s.units) + 1;
   return s;

@@ -81,91 +81,120 @@ __device__ __forceinline__ uint32_t v_at(int j, int nt, bool pair) {
   return pair ? 2 * j + 1 : min(2 * j + 2, 2 * nt - 1);
 }
 
-// ---- TMA loads (one thread)
+// Which tile has place e in the order that k_at and v_at give.
+__device__ __forceinline__ void tile_at(int e, int nt, bool pair, bool& is_k, int& j) {
+  if (pair) {
+    is_k = !(e & 1);
+    j = e >> 1;
+  } else if (e < 2 && e < nt) {
+    is_k = true;
+    j = e;
+  } else if (e == 2 * nt - 1) {
+    is_k = false;
+    j = nt - 1;
+  } else {
+    is_k = e & 1;
+    j = is_k ? (e + 1) >> 1 : (e - 2) >> 1;
+  }
+}
+
+// ---- TMA loads (one warp; one lane issues, and with pages every lane looks up
+// a box of the next tile, so that no load waits for its page's number)
 template <bool PAGED>
 __device__ void load_role(const TileArgs& a, const CUtensorMap* mq, const CUtensorMap* mk,
-                          const CUtensorMap* mv, Shared& sh, unsigned char* sm) {
+                          const CUtensorMap* mv, Shared& sh, unsigned char* sm, int lane) {
   volatile int* ab = &sh.abort;
   uint32_t cnt = 0, nu = 0, nq = 0;
   uint32_t raw_phase = 0, raw_last = 0;  // per slot: v_raw's phase; whether its last tile went there
   const int chunks_d = (a.d + 63) / 64, chunks_v = (a.dv + 63) / 64;
   const uint32_t q_tile = (uint32_t)(chunks_d * 128 * a.group * a.tp);
+  const int boxes = PAGED ? kTileN / a.box : 1;
+  const int none = PAGED ? (int)(a.n_pages * a.page) : 0;  // past the tensor's end: reads as zeros
+  // Row of this lane's box of the tile at `key`: outside the prefix or the pool
+  // the one past the end.
+  auto look = [&](int key) {
+    int row = none;
+    key += lane * a.box;
+    if (lane < boxes && key < a.k_rows) {
+      const int pi = key / a.page;
+      const int32_t pg = a.pages[pi];
+      if (pg >= 0 && pg < a.n_pages) row = pg * a.page + (key - pi * a.page);
+      else attn_report(a.status, NYS_ATTN_BAD_PAGE);
+    }
+    return row;
+  };
   for (;; ++nu) {
-    if (!bar_wait(&sh.u_full[nu % kUnitRing], (nu / kUnitRing) & 1, ab)) break;
+    if (!bar_wait_warp(&sh.u_full[nu % kUnitRing], (nu / kUnitRing) & 1, ab)) break;
     const Unit u = sh.unit[nu % kUnitRing];
-    bar_arrive(&sh.u_empty[nu % kUnitRing]);
+    __syncwarp();
+    if (lane == 0) bar_arrive(&sh.u_empty[nu % kUnitRing]);
     if (!u.valid) break;
     if (u.nt == 0) continue;
     const bool pair = u.np1 > 0;
-    if (!bar_wait(&sh.q_empty, (nq & 1) ^ 1, ab)) break;
+    if (!bar_wait_warp(&sh.q_empty, (nq & 1) ^ 1, ab)) break;
     ++nq;
-    bar_expect(&sh.q_full, q_tile * (pair ? 2 : 1));
-    for (int s = 0; s <= (pair ? 1 : 0); ++s)
-      for (int c = 0; c < chunks_d; ++c)
-        tma_load3(sm + s * 32768 + c * 16384, mq, c * 64, u.kvh * a.group, u.q_row + s * a.tp,
-                  &sh.q_full);
+    if (elect_one()) {
+      bar_expect(&sh.q_full, q_tile * (pair ? 2 : 1));
+      for (int s = 0; s <= (pair ? 1 : 0); ++s)
+        for (int c = 0; c < chunks_d; ++c)
+          tma_load3(sm + s * 32768 + c * 16384, mq, c * 64, u.kvh * a.group, u.q_row + s * a.tp,
+                    &sh.q_full);
+    }
     const int y = a.kv_y ? u.kvh : 0;
+    int next_row = PAGED ? look(u.kb) : 0;
     bool ok = true;
-    for (int e = 0; e < 2 * u.nt && ok; ++e) {
-      // Which tile has place e.
+    for (int e = 0; e < 2 * u.nt; ++e) {
       bool is_k;
       int j;
-      if (pair) {
-        is_k = !(e & 1);
-        j = e >> 1;
-      } else if (e < 2 && e < u.nt) {
-        is_k = true;
-        j = e;
-      } else if (e == 2 * u.nt - 1) {
-        is_k = false;
-        j = u.nt - 1;
-      } else {
-        is_k = e & 1;
-        j = is_k ? (e + 1) >> 1 : (e - 2) >> 1;
+      tile_at(e, u.nt, pair, is_k, j);
+      const int my_row = next_row;
+      if (PAGED && e + 1 < 2 * u.nt) {
+        bool k1;
+        int j1;
+        tile_at(e + 1, u.nt, pair, k1, j1);
+        next_row = look(u.kb + j1 * kTileN);
       }
       const uint32_t slot = cnt % kSlots;
-      ok = bar_wait(&sh.kv_empty[slot], ((cnt / kSlots) & 1) ^ 1, ab);
+      ok = bar_wait_warp(&sh.kv_empty[slot], ((cnt / kSlots) & 1) ^ 1, ab);
       if (!ok) break;
       ++cnt;
       unsigned char* dst = sm + kQBytes + slot * kSlotBytes;
       const CUtensorMap* m = is_k ? mk : mv;
       const int chunks = is_k ? chunks_d : chunks_v;
-      const int key = u.kb + j * kTileN;
       // Tiles to be cleaned land on v_raw; the cleaner then completes kv_full.
       const bool edge = !is_k && j >= u.edge;
       uint64_t* full = edge ? &sh.v_raw[slot] : &sh.kv_full[slot];
       raw_last = (raw_last & ~(1u << slot)) | ((uint32_t)edge << slot);
       raw_phase ^= (uint32_t)edge << slot;
-      bar_expect(full, (uint32_t)chunks * 16384u);
       if (!PAGED) {
-        for (int c = 0; c < chunks; ++c)
-          tma_load3(dst + c * 16384, m, c * 64, y, u.k_row + key, full);
-      } else {
-        for (int b = 0; b < kTileN; b += a.box) {
-          // Past the prefix or outside the pool: a row past the tensor's end,
-          // which reads as zeros.
-          int64_t row = a.n_pages * a.page;
-          if (key + b < a.k_rows) {
-            const int32_t pg = a.pages[(key + b) / a.page];
-            if (pg >= 0 && pg < a.n_pages) row = (int64_t)pg * a.page + (key + b) % a.page;
-            else attn_report(a.status, NYS_ATTN_BAD_PAGE);
-          }
+        if (elect_one()) {
+          bar_expect(full, (uint32_t)chunks * 16384u);
           for (int c = 0; c < chunks; ++c)
-            tma_load3(dst + c * 16384 + b * 128, m, c * 64, y, (int)row, full);
+            tma_load3(dst + c * 16384, m, c * 64, y, u.k_row + u.kb + j * kTileN, full);
+        }
+      } else {
+        if (elect_one()) bar_expect(full, (uint32_t)chunks * 16384u);
+        __syncwarp();
+        for (int b = 0; b < boxes; ++b) {
+          const int row = __shfl_sync(0xffffffffu, my_row, b);
+          if (elect_one())
+            for (int c = 0; c < chunks; ++c)
+              tma_load3(dst + c * 16384 + b * a.box * 128, m, c * 64, y, row, full);
         }
       }
+      __syncwarp();
     }
     if (!ok) break;
   }
   // Copies in flight land before the CTA may leave.
   if (*ab) {
-    int none = 0;
+    int never = 0;
     for (uint32_t c = cnt > kSlots ? cnt - kSlots : 0; c < cnt; ++c) {
       const uint32_t slot = c % kSlots;
-      if ((raw_last >> slot) & 1) bar_wait(&sh.v_raw[slot], ((raw_phase >> slot) & 1) ^ 1, &none);
-      else bar_wait(&sh.kv_full[slot], (c / kSlots) & 1, &none);
+      if ((raw_last >> slot) & 1) bar_wait(&sh.v_raw[slot], ((raw_phase >> slot) & 1) ^ 1, &never);
+      else bar_wait(&sh.kv_full[slot], (c / kSlots) & 1, &never);
     }
-    if (nq) bar_wait(&sh.q_full, (nq - 1) & 1, &none);
+    if (nq) bar_wait(&sh.q_full, (nq - 1) & 1, &never);
   }
 }
 
@@ -619,7 +648,7 @@ attn_tc_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CUten
   } else {
     fewer_regs<kRegsRest>();
     if (warp == 8) {
-      if (elect_one()) load_role<PAGED>(a, &mq, &mk, &mv, sh, sm);
+      load_role<PAGED>(a, &mq, &mk, &mv, sh, sm, lane);
     } else if (warp == 9) {
       if (elect_one()) mma_role<T>(a, sh, sm, tmem);
     } else if (warp == 10) {
