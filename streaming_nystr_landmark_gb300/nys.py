@@ -562,7 +562,7 @@ def _dtype_code(dtype):
 def _rows(t, dtype, heads, dim, where):
     """A [rows][heads][dim] CUDA tensor as NysRows: any row and head strides,
     the last dimension contiguous."""
-    if t.dtype != dtype or not t.is_cuda:
+    if t.dtype is not dtype or not t.is_cuda:
         raise ValueError(f"{where}: need a CUDA {dtype} tensor")
     shape, st = t.shape, t.stride()
     if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
@@ -573,13 +573,22 @@ def _rows(t, dtype, heads, dim, where):
 
 
 def _ints(t, dtype, shape, where):
-    """Address of a contiguous CUDA integer tensor of `shape` (None: any length)."""
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+    """Address of a contiguous CUDA tensor of this type and shape."""
+    if t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{where}: need a contiguous CUDA {dtype} tensor")
-    if len(t.shape) != len(shape) or any(w is not None and w != g
-                                         for w, g in zip(shape, t.shape)):
-        raise ValueError(f"{where}: shape {tuple(t.shape)} != {tuple(shape)}")
-    return t.data_ptr()
+    raise ValueError(f"{where}: shape {tuple(t.shape)} != {tuple(shape)}")
+
+
+def _current_stream(device):
+    """The device's current torch stream as an address (what
+    torch.cuda.current_stream(device).cuda_stream gives, without making an
+    object: 0.1 us against 3.5)."""
+    import torch
+    index = device.index
+    return torch._C._cuda_getCurrentRawStream(
+        torch.cuda.current_device() if index is None else index)
 
 
 class _Status:
@@ -630,7 +639,7 @@ class PagedKV:
         nys_kv_write(self._cfg, self._pool, n, _rows(k, self.dtype, self.kv_heads, self.d, "k"),
                      _rows(v, self.dtype, self.kv_heads, self.dv, "v"),
                      _ints(slots, torch.int64, (n,), "slots"),
-                     torch.cuda.current_stream(self.device).cuda_stream)
+                     _current_stream(self.device))
 
 
 class PagePlan(_Status):
@@ -661,10 +670,10 @@ class PagePlan(_Status):
         i32 = self.torch.int32
         nys_kv_plan(self.n, self.page, _ints(cached, i32, (self.n,), "cached"),
                     _ints(fresh, i32, (self.n,), "fresh"),
-                    _ints(free_pages, i32, (None,), "free_pages"), free_pages.shape[0],
+                    _ints(free_pages, i32, free_pages.shape[:1], "free_pages"), free_pages.shape[0],
                     _ints(table, i32, (self.n, self.width), "table"), self.width, self.total,
                     *self._out, self._status_ptr,
-                    self.torch.cuda.current_stream(self.device).cuda_stream)
+                    _current_stream(self.device))
         return self
 
 
@@ -686,11 +695,15 @@ class ExactAttention(_Status):
         self._work = None
         self._work_ptr = None
         self._work_bytes = 0
+        self._sizes = None
         nys_attn_workspace_bytes(self.cfg, 0, 0)   # refuses a bad geometry here
 
     def _workspace(self, n, rows, keys):
         """Makes the workspace large enough for a call of these sizes."""
+        if (n, rows, keys) == self._sizes:
+            return
         need = nys_attn_workspace_bytes(self.cfg, n, rows, keys)
+        self._sizes = (n, rows, keys)
         if need > self._work_bytes:
             self._work = self.torch.empty(need, dtype=self.torch.uint8, device=self.device)
             self._work_ptr, self._work_bytes = self._work.data_ptr(), need
@@ -705,15 +718,15 @@ class ExactAttention(_Status):
             raise ValueError("k and v, and q and out, must have as many rows as each other")
         self._workspace(n, rows, keys)
         nys_attn_prompt(
-            self.cfg, n, rows, keys, _ints(q_off, torch.int32, (None,), "q_off"),
+            self.cfg, n, rows, keys, _ints(q_off, torch.int32, (n + 1,), "q_off"),
             None if k_off is None else _ints(k_off, torch.int32, (n + 1,), "k_off"),
             _rows(q, self.dtype, self.heads, self.d, "q"),
             _rows(k, self.dtype, self.kv_heads, self.d, "k"),
             _rows(v, self.dtype, self.kv_heads, self.dv, "v"),
             _rows(out, self.dtype, self.heads, self.dv, "out"),
-            None if lse is None else _ptr(lse, torch.float32, (rows, self.heads), "lse"),
+            None if lse is None else _ints(lse, torch.float32, (rows, self.heads), "lse"),
             self._work_ptr, self._work_bytes, self._status_ptr,
-            torch.cuda.current_stream(self.device).cuda_stream)
+            _current_stream(self.device))
         return out
 
     def shared(self, q, cache, lens, table, out, prefix_pages=None, prefix_len=0, lse=None):
@@ -729,17 +742,17 @@ class ExactAttention(_Status):
             raise ValueError("out must have q's rows, and table be [n][width]")
         pages = None
         if prefix_len > 0:
-            pages = _ints(prefix_pages, torch.int32, (None,), "prefix_pages")
+            pages = _ints(prefix_pages, torch.int32, prefix_pages.shape[:1], "prefix_pages")
             if prefix_pages.shape[0] * cache.page < prefix_len:
                 raise ValueError("prefix_pages: too few pages for prefix_len")
         self._workspace(n, n, prefix_len)
         nys_attn_shared(
             self.cfg, n, cache._pool, pages, prefix_len,
             _ints(lens, torch.int32, (n,), "lens"),
-            _ints(table, torch.int32, (n, None), "table"), table.shape[1],
+            _ints(table, torch.int32, (n, table.shape[1]), "table"), table.shape[1],
             _rows(q, self.dtype, self.heads, self.d, "q"),
             _rows(out, self.dtype, self.heads, self.dv, "out"),
-            None if lse is None else _ptr(lse, torch.float32, (n, self.heads), "lse"),
+            None if lse is None else _ints(lse, torch.float32, (n, self.heads), "lse"),
             self._work_ptr, self._work_bytes, self._status_ptr,
-            torch.cuda.current_stream(self.device).cuda_stream)
+            _current_stream(self.device))
         return out
