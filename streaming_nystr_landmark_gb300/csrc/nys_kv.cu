@@ -149,25 +149,32 @@ __global__ void __launch_bounds__(kWriteThreads) write_kernel(WriteArgs a) {
   const int64_t stride = (int64_t)gridDim.x * kWriteThreads;
   for (int64_t u0 = (int64_t)blockIdx.x * kWriteThreads + threadIdx.x; u0 < total;
        u0 += stride * kWriteEach) {
+    // All slots, then all rows, then the stores: no load waits for another
+    // unit's.
+    int64_t token[kWriteEach], slot[kWriteEach];
+    uint32_t in[kWriteEach];
+#pragma unroll
+    for (int e = 0; e < kWriteEach; ++e) {
+      const int64_t u = u0 + e * stride;
+      const bool here = u < total;
+      token[e] = total <= INT32_MAX ? (int64_t)((uint32_t)(here ? u : 0) / per) : (here ? u : 0) / per;
+      in[e] = (uint32_t)((here ? u : 0) - token[e] * per);
+      slot[e] = here ? a.slots[token[e]] : -1;
+    }
     U x[kWriteEach];
     U* dst[kWriteEach];
 #pragma unroll
     for (int e = 0; e < kWriteEach; ++e) {
-      const int64_t u = u0 + e * stride;
-      dst[e] = nullptr;
-      if (u >= total) continue;
-      const int64_t t = total <= INT32_MAX ? (int64_t)((uint32_t)u / per) : u / per;
-      uint32_t in = (uint32_t)(u - t * per);
-      const int64_t slot = a.slots[t];
-      if (slot < 0 || slot >= a.n_slots) continue;
-      const bool is_k = in < ku;
-      if (!is_k) in -= ku;
+      const bool is_k = in[e] < ku;
+      const uint32_t at = is_k ? in[e] : in[e] - ku;
       const uint32_t hu = is_k ? a.k_head_units : a.v_head_units;
-      const uint32_t h = in / hu;
-      const U* src = is_k ? (const U*)a.k + t * a.k_row + h * a.k_head + (in - h * hu)
-                          : (const U*)a.v + t * a.v_row + h * a.v_head + (in - h * hu);
-      x[e] = *src;
-      dst[e] = is_k ? (U*)a.pool_k + slot * ku + in : (U*)a.pool_v + slot * a.v_units + in;
+      const uint32_t h = at / hu;
+      const U* src = is_k ? (const U*)a.k + token[e] * a.k_row + h * a.k_head + (at - h * hu)
+                          : (const U*)a.v + token[e] * a.v_row + h * a.v_head + (at - h * hu);
+      x[e] = *src;  // (a token without a slot is read too: its row exists)
+      dst[e] = slot[e] < 0 || slot[e] >= a.n_slots ? nullptr
+               : is_k ? (U*)a.pool_k + slot[e] * ku + at
+                      : (U*)a.pool_v + slot[e] * a.v_units + at;
     }
 #pragma unroll
     for (int e = 0; e < kWriteEach; ++e)
