@@ -437,7 +437,8 @@ int nys_attn_workspace_bytes(const nys_attn_config* cfg, int64_t n, int64_t rows
  * softmax's denominator.  Values of keys that a row does not see never reach
  * it, whatever they are.
  * workspace: nys_attn_workspace_bytes(cfg, n, q_rows, k_rows) bytes, 256-byte
- * aligned.  Less or NULL is allowed: f32 then takes the general kernel.
+ * aligned.  Less or NULL is allowed: f32 then takes the general kernel, and
+ * work is spread over the CTAs beforehand.
  * Errors: NYS_E_INVAL, NYS_E_UNSUPPORTED, NYS_E_ALIGN (workspace), NYS_E_CUDA. */
 int nys_attn_prompt(const nys_attn_config* cfg, int64_t n, int64_t q_rows, int64_t k_rows,
                     const int32_t* q_off, const int32_t* k_off, const nys_rows* q,

@@ -109,7 +109,7 @@ int nys_attn_prompt(const nys_attn_config* cfg, int64_t n, int64_t q_rows, int64
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool room = workspace && workspace_bytes >= nys::prompt_workspace(*cfg, n, q_rows, k_rows);
   const cudaError_t e = nys::prompt_tc_fits(a) && (room || cfg->dtype != NYS_F32)
-                            ? nys::launch_prompt_tc(a, workspace, s)
+                            ? nys::launch_prompt_tc(a, room ? workspace : nullptr, s)
                             : nys::launch_prompt_general(a, s);
   return e == cudaSuccess ? NYS_OK : NYS_E_CUDA;
 }

@@ -94,10 +94,22 @@ __device__ __forceinline__ __half narrow<__half>(float x) {
   return __float2half_rn(x);
 }
 
-// Pieces of the prefix that request b's rows of a KV head have.
-__device__ __forceinline__ int prefix_pieces(const SharedArgs& a, const OwnArgs& o, int b, int kvh) {
-  return o.shares.units > 0 ? o.shares.pieces(b / o.shares.rows * a.kv_heads + kvh) : 0;
-}
+// The prefix's pieces of one row: how many, and the row of the first in `part`
+// (those of the others follow `step` rows apart).
+struct PrefixRow {
+  int pieces = 0;
+  int64_t first = 0, step = 0;
+  __device__ __forceinline__ PrefixRow(const SharedArgs& a, const OwnArgs& o, int b, int h) {
+    const Shares& s = o.shares;
+    if (s.units == 0) return;
+    const int kvh = h / a.group, unit = b / s.rows * a.kv_heads + kvh;
+    const int pos = b % s.rows, tile = pos / s.tp;
+    pieces = s.pieces(unit);
+    step = (int64_t)o.per * kTileM;
+    first = (unit + s.cta_of((int64_t)unit * s.nt)) * step + tile * kTileM +
+            (pos - tile * s.tp) * a.group + (h - kvh * a.group);
+  }
+};
 
 // Joins the warps' results (log2 maxima m and sums l [warp][head], O
 // [warp][head][dv]) and, where this CTA has all of the request's own keys, the
@@ -113,11 +125,12 @@ __device__ void join(const SharedArgs& a, const OwnArgs& o, const float* m, cons
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) top = fmaxf(top, m[w * HB + h]);
     // The prefix's pieces: lane = piece, log2 of their sums.
-    const int np = o.pieces == 1 ? prefix_pieces(a, o, b, (h0 + h) / a.group) : 0;
+    const PrefixRow pre(a, o, b, h0 + h);
+    const int np = o.pieces == 1 ? pre.pieces : 0;
     float pl[2] = {-INFINITY, -INFINITY};
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      if (lane + 32 * i < np) pl[i] = o.part_lse[(lane + 32 * i) * rows + row] * kLog2e;
+      if (lane + 32 * i < np) pl[i] = o.part_lse[pre.first + (lane + 32 * i) * pre.step] * kLog2e;
     float pt = fmaxf(pl[0], pl[1]);
 #pragma unroll
     for (int s = 16; s; s >>= 1) pt = fmaxf(pt, __shfl_xor_sync(0xffffffffu, pt, s));
@@ -155,7 +168,7 @@ __device__ void join(const SharedArgs& a, const OwnArgs& o, const float* m, cons
     for (int p = 0; p < np; ++p) {
       const float f = __shfl_sync(0xffffffffu, p < 32 ? pf[0] : pf[1], p & 31);
       if (col && f != 0.f) {
-        const float4 x = *reinterpret_cast<const float4*>(o.part + (p * rows + row) * a.dv + lane * 4);
+        const float4 x = *reinterpret_cast<const float4*>(o.part + (pre.first + p * pre.step) * a.dv + lane * 4);
         y[0] = fmaf(x.x, f, y[0]);
         y[1] = fmaf(x.y, f, y[1]);
         y[2] = fmaf(x.z, f, y[2]);
@@ -173,9 +186,9 @@ __device__ void join(const SharedArgs& a, const OwnArgs& o, const float* m, cons
       }
       if (lane == 0 && a.lse) a.lse[row] = lse;
     } else {
-      const int64_t at = (int64_t)(o.shares.most + piece) * rows + row;
-      if (col) *reinterpret_cast<float4*>(o.part + at * a.dv + lane * 4) = make_float4(y[0], y[1], y[2], y[3]);
-      if (lane == 0) o.part_lse[at] = lse;
+      const int64_t at = (int64_t)piece * rows + row;
+      if (col) *reinterpret_cast<float4*>(o.own + at * a.dv + lane * 4) = make_float4(y[0], y[1], y[2], y[3]);
+      if (lane == 0) o.own_lse[at] = lse;
     }
   }
 }
@@ -562,13 +575,20 @@ __global__ void __launch_bounds__(kThreads) join_kernel(SharedArgs a, OwnArgs o)
   for (int64_t r = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); r < rows;
        r += (int64_t)gridDim.x * kWarps) {
     const int b = (int)(r / a.heads), h = (int)(r - (int64_t)b * a.heads);
-    const int np = prefix_pieces(a, o, b, h / a.group), own = (own_len(a, b, false) + o.keys - 1) / o.keys, all = np + own;
-    auto place = [&](int p) { return (int64_t)(p < np ? p : o.shares.most + p - np) * rows + r; };
+    const PrefixRow pre(a, o, b, h);
+    const int np = pre.pieces, own = (own_len(a, b, false) + o.keys - 1) / o.keys, all = np + own;
+    auto lse_of = [&](int p) {
+      return p < np ? o.part_lse[pre.first + p * pre.step] : o.own_lse[(p - np) * rows + r];
+    };
+    auto row_of = [&](int p) {
+      return (p < np ? o.part + (pre.first + p * pre.step) * a.dv : o.own + ((p - np) * rows + r) * a.dv) +
+             lane * 4;
+    };
     // Lane = piece (at most 128): its weight against the largest.
     float w[4], top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      w[i] = lane + 32 * i < all ? o.part_lse[place(lane + 32 * i)] * kLog2e : -INFINITY;
+      w[i] = lane + 32 * i < all ? lse_of(lane + 32 * i) * kLog2e : -INFINITY;
       top = fmaxf(top, w[i]);
     }
 #pragma unroll
@@ -588,7 +608,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(SharedArgs a, OwnArgs o)
     for (int p = 0; p < all; ++p) {
       const float f = __shfl_sync(0xffffffffu, p < 32 ? w[0] : p < 64 ? w[1] : p < 96 ? w[2] : w[3], p & 31);
       if (col && f != 0.f) {
-        const float4 x = *reinterpret_cast<const float4*>(o.part + place(p) * a.dv + lane * 4);
+        const float4 x = *reinterpret_cast<const float4*>(row_of(p));
         y[0] = fmaf(x.x, f, y[0]);
         y[1] = fmaf(x.y, f, y[1]);
         y[2] = fmaf(x.z, f, y[2]);
@@ -603,6 +623,80 @@ __global__ void __launch_bounds__(kThreads) join_kernel(SharedArgs a, OwnArgs o)
     }
     if (lane == 0 && a.lse)
       a.lse[r] = total == 0.f ? -INFINITY : fmaf(top, 0.6931471805599453f, logf(total));
+  }
+}
+
+// Joins the pieces of a prompt's cut units: blockIdx.x is the unit, a warp takes a
+// row (16 CTAs a unit: a row is a chain of a few dependent reads, so rows have to
+// be many at once).
+template <typename T>
+__global__ void __launch_bounds__(256) tail_join_kernel(const __grid_constant__ TileArgs a, int ctas) {
+  __shared__ Unit su;
+  __shared__ Tail st;
+  wait_for_previous();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (warp == 0) {
+    Tail t;
+    t.find(a, ctas, lane);
+    Unit u;
+    u.valid = 0;
+    if ((int)blockIdx.x < t.units) {
+      UnitWalk w;
+      w.load(a, lane);
+      w.get(a, t.full + blockIdx.x, lane, u);
+    }
+    if (lane == 0) {
+      su = u;
+      st = t;
+    }
+  }
+  __syncthreads();
+  if (!su.valid) return;
+  const int64_t step = (int64_t)a.per * kTileM;
+  for (int row = blockIdx.y * 8 + warp; row < (su.np1 > 0 ? 2 : 1) * kTileM; row += 8 * gridDim.y) {
+    const int tile = row / kTileM, r = row - tile * kTileM, pos = r / a.group;
+    if (pos >= (tile ? su.np1 : su.np0)) continue;
+    const int h = su.kvh * a.group + (r - pos * a.group);
+    const int64_t orow = (int64_t)su.q_row + tile * a.tp + pos;
+    const int64_t first = blockIdx.x * (int64_t)st.cut * step + row;
+    float top = -INFINITY, w[5];  // lane = piece (at most 152)
+#pragma unroll
+    for (int i = 0; i < 5; ++i) {
+      w[i] = lane + 32 * i < st.cut ? a.part_lse[first + (lane + 32 * i) * step] * kLog2e : -INFINITY;
+      top = fmaxf(top, w[i]);
+    }
+#pragma unroll
+    for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+    const float ref = top == -INFINITY ? 0.f : top;
+    float total = 0.f;
+#pragma unroll
+    for (int i = 0; i < 5; ++i) {
+      w[i] = ex2(w[i] - ref);
+      total += w[i];
+    }
+#pragma unroll
+    for (int s = 16; s; s >>= 1) total += __shfl_xor_sync(0xffffffffu, total, s);
+    float y[4] = {0.f, 0.f, 0.f, 0.f};
+    const bool col = lane * 4 < a.dv;
+#pragma unroll 8
+    for (int p = 0; p < st.cut; ++p) {
+      const float f = __shfl_sync(0xffffffffu, p < 32 ? w[0] : p < 64 ? w[1] : p < 96 ? w[2] : p < 128 ? w[3] : w[4], p & 31);
+      if (col && f != 0.f) {
+        const float4 x = *reinterpret_cast<const float4*>(a.part + (first + p * step) * a.dv + lane * 4);
+        y[0] = fmaf(x.x, f, y[0]);
+        y[1] = fmaf(x.y, f, y[1]);
+        y[2] = fmaf(x.z, f, y[2]);
+        y[3] = fmaf(x.w, f, y[3]);
+      }
+    }
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+    if (col) {
+      T* out = (T*)a.out.p + orow * a.out.row + h * a.out.head + lane * 4;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) out[i] = narrow<T>(y[i] * inv);
+    }
+    if (lane == 0 && a.lse)
+      a.lse[orow * a.heads + h] = total == 0.f ? -INFINITY : fmaf(top, 0.6931471805599453f, logf(total));
   }
 }
 
@@ -653,6 +747,13 @@ cudaError_t launch_join(const SharedArgs& a, const OwnArgs& o, cudaStream_t stre
                                         : a.dtype == NYS_BF16 ? join_kernel<__nv_bfloat16>
                                                               : join_kernel<__half>;
   return launch_dependent(kernel, grid, kThreads, 0, stream, a, o);
+}
+
+cudaError_t launch_tail_join(const TileArgs& a, int dtype, unsigned ctas, cudaStream_t stream) {
+  void (*kernel)(TileArgs, int) = dtype == NYS_F32    ? tail_join_kernel<float>
+                                  : dtype == NYS_BF16 ? tail_join_kernel<__nv_bfloat16>
+                                                      : tail_join_kernel<__half>;
+  return launch_dependent(kernel, dim3(ctas / 2, 16), 256, 0, stream, a, (int)ctas);
 }
 
 }  // namespace nys

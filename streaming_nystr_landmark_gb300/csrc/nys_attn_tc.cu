@@ -50,6 +50,7 @@ namespace {
 using namespace tc;
 
 constexpr int kThreads = 384;
+constexpr int kUnitRing = 2;  // units that a CTA has taken: the current one and the next
 constexpr int kSlots = 5;
 constexpr uint32_t kSlotBytes = 32768;
 constexpr uint32_t kQBytes = 65536;
@@ -301,18 +302,12 @@ __device__ void mma_role(const TileArgs& a, Shared& sh, unsigned char* sm, uint3
 // ---- units of work (one warp)
 __device__ void unit_role(const TileArgs& a, Shared& sh, int lane) {
   volatile int* ab = &sh.abort;
-  UnitWalk walk;
-  if (a.q_off) walk.load(a, lane);
+  UnitSource source;
+  source.begin(a, lane);
   for (uint32_t nu = 0;; ++nu) {
-    Unit u;
-    if (a.q_off) {
-      // Every other round runs backwards, so that no CTA gets the longer unit
-      // of every round.
-      walk.get(a, nu * gridDim.x + ((nu & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x), lane, u);
-    } else {
-      prefix_unit(a, blockIdx.x, nu, u);
-    }
     if (!bar_wait_warp(&sh.u_empty[nu % kUnitRing], ((nu / kUnitRing) & 1) ^ 1, ab)) return;
+    Unit u;
+    source.next(a, nu, lane, u);
     if (lane == 0) {
       sh.unit[nu % kUnitRing] = u;
       bar_arrive(&sh.u_full[nu % kUnitRing]);
@@ -541,7 +536,7 @@ __device__ void row_role(const TileArgs& a, Shared& sh, uint32_t tmem, int s, in
     const int64_t orow = (int64_t)u.q_row + shift + pos;
     const int head = u.kvh * a.group + hd;
     const bool patch = *(volatile int*)&sh.unit[nu % kUnitRing].patch != 0;
-    const int64_t prow = ((int64_t)u.split * a.q_rows + orow) * a.heads + head;
+    const int64_t prow = ((int64_t)u.slot * a.per + (pair ? s : 0)) * kTileM + row;
     T* out = (T*)a.out.p + orow * a.out.row + head * a.out.head;
     for (int c = pair ? 0 : 16 * s; c < a.dv; c += pair ? 16 : 32) {
       float y[16];
@@ -567,7 +562,7 @@ __device__ void row_role(const TileArgs& a, Shared& sh, uint32_t tmem, int s, in
 #pragma unroll
       for (int i = 0; i < 16; i += 8)
         if (c + i < a.dv) {
-          if (a.splits) store8(a.part + prow * a.dv + c + i, y + i);
+          if (u.slot >= 0) store8(a.part + prow * a.dv + c + i, y + i);
           else store8(out + c + i, y + i);
         }
     }
@@ -576,14 +571,14 @@ __device__ void row_role(const TileArgs& a, Shared& sh, uint32_t tmem, int s, in
         const T* v = value_row<T, PAGED>(a, u, u.kb + k);
         if (!v) continue;
         for (int c = pair ? 0 : 16 * s; c < a.dv; c += pair ? 16 : 32) {
-          if (a.splits) add_unusual(a.part + prow * a.dv, v, c, min(c + 16, a.dv));
+          if (u.slot >= 0) add_unusual(a.part + prow * a.dv, v, c, min(c + 16, a.dv));
           else add_unusual(out, v, c, min(c + 16, a.dv));
         }
       }
     }
     if (mine && (pair || s == 0)) {
       const float v = total == 0.f ? -INFINITY : fmaf(top, a.scale, lg2(total) * 0.6931471805599453f);
-      if (a.splits) a.part_lse[prow] = v;
+      if (u.slot >= 0) a.part_lse[prow] = v;
       else if (a.lse) a.lse[orow * a.heads + head] = v;
     }
     fence_before();

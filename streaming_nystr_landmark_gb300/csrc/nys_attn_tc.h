@@ -9,7 +9,6 @@ namespace nys {
 
 constexpr int kTileM = 128;  // rows of a query tile: (position, head of the group) pairs
 constexpr int kTileN = 128;  // keys of a tile
-constexpr int kUnitRing = 4;
 
 // How a prefix's key tiles are dealt out.  A unit (query tiles of one KV head)
 // has nt tiles; the units' tiles, one after another, are cut into `ctas` equal
@@ -17,7 +16,10 @@ constexpr int kUnitRing = 4;
 // share with a CTA is a piece.
 struct Shares {
   int32_t nt, ctas, units, rows;  // rows: requests of a unit
-  int32_t most;                   // pieces of a unit, at most
+  int32_t tp;                     // of them in one query tile
+  // Piece i of a unit lies in slot unit + cta_of(its first tile) + i: pieces and
+  // CTAs ascend together, so no two pieces share a slot.
+  __host__ __device__ int slots() const { return units + ctas; }
   // The CTA that has tile t of all.
   __host__ __device__ int cta_of(int64_t t) const {
     return (int)(((t + 1) * ctas - 1) / ((int64_t)units * nt));
@@ -54,13 +56,15 @@ struct TileArgs {
   int32_t heads, kv_heads, group, tp;  // tp: positions of a query tile, 128 / group
   int32_t d, dv;
   int32_t per;     // query tiles of a unit: 2, or 1 (f32)
-  int32_t splits;  // 1: results go to `part` as pieces (prefix)
   Shares shares;   // prefix
+  uint32_t* counter;  // prompts: units begun beyond the first of each CTA; null:
+                      // every CTA takes every gridDim.x-th
+  int32_t tail;    // prompts: cut the units of the last, partial round
   float scale;
   Rows q;               // (f32; the 16-bit kernel reads it by its map)
-  Rows out;             // results, where splits == 0
+  Rows out;             // results of whole units
   float* lse;           // [q_rows][heads] or null
-  float *part, *part_lse;  // pieces' results [split][q_rows][heads][dv], [..]; splits > 0
+  float *part, *part_lse;  // pieces' results [slot][per * 128 rows][dv], [..]
   // Keys in pages (prefix): their numbers, tokens a page, pages in the pool.
   const int32_t* pages;
   int32_t page, box;
@@ -90,7 +94,7 @@ struct Unit {
   int32_t nt0;      // of them, those the first tile reads (pair)
   int32_t lim;      // keys that position 0 sees (may be <= 0)
   int32_t nkl;      // keys the piece ends before
-  int32_t split;
+  int32_t slot;     // where a piece's results go; -1: a whole unit, to `out`
   int32_t edge;     // first key tile in which some row does not see some key
   int32_t patch;    // set where the epilogue has to add values that are not finite
   int32_t tile;     // number of the piece's first key tile among all (f32)
@@ -100,13 +104,15 @@ struct TileMaps {
   CUtensorMap q, k, v;
 };
 
-// A request's own keys: pieces of `keys` keys each, at most `pieces` (1: all of
-// them, and the result is final), and all pieces' results: the prefix's in
-// places 0 .. shares.most - 1, then the own ones.
+// The prefix's pieces and a request's own keys: pieces of `keys` keys each, at
+// most `pieces` (1: all of them, and the result is final) with their results
+// [piece][n * heads][dv].
 struct OwnArgs {
   Shares shares;  // units == 0: no prefix
+  const float *part, *part_lse;  // the prefix's
+  int32_t per;
   int32_t pieces, keys;
-  float *part, *part_lse;
+  float *own, *own_lse;
 };
 
 // Workspace of the tiled kernels: nys_attn_prompt with n sequences of `rows` query
@@ -126,7 +132,8 @@ cudaError_t launch_attn_tc(const TileArgs& a, const TileMaps& m, int dtype, unsi
                            cudaStream_t stream);
 
 cudaError_t launch_attn_tc32(const TileArgs& a, unsigned grid, cudaStream_t stream);
-
+// Joins the pieces of a prompt's cut units (after a launch of `ctas` CTAs).
+cudaError_t launch_tail_join(const TileArgs& a, int dtype, unsigned ctas, cudaStream_t stream);
 
 #ifdef __CUDACC__
 // Launches `kernel` as a programmatic dependent of the launch before it: its
@@ -186,7 +193,18 @@ struct UnitWalk {
     }
   }
 
-  // Unit number w (ascending from call to call) into `u` in every lane;
+  // All units of the launch.
+  static __device__ __forceinline__ int32_t total(const TileArgs& a, int lane) {
+    UnitWalk w;
+    int32_t sum = 0;
+    for (w.s0 = 0; w.s0 < a.n; w.s0 += 32) {
+      w.load(a, lane);
+      sum += __shfl_sync(0xffffffffu, w.upto, 31);
+    }
+    return sum;
+  }
+
+  // Unit number w (not descending from call to call) into `u` in every lane;
   // u.valid == 0 past the last.
   __device__ __forceinline__ void get(const TileArgs& a, int32_t w, int lane, Unit& u) {
     u.valid = 0;
@@ -204,7 +222,7 @@ struct UnitWalk {
     const int sk0 = __shfl_sync(0xffffffffu, k0, src), snk = __shfl_sync(0xffffffffu, nk, src);
     const int spairs = __shfl_sync(0xffffffffu, pairs, src);
     const int32_t r = w - before - __shfl_sync(0xffffffffu, upto - count, src);
-    u.split = 0;
+    u.slot = -1;
     u.kvh = r % a.kv_heads;
     const int pair = spairs - 1 - r / a.kv_heads;
     const int p0 = pair * a.per * a.tp;
@@ -251,9 +269,72 @@ __device__ __forceinline__ void prefix_unit(const TileArgs& a, int cta, int k, U
   u.nt = u.nt0 = te - tb;
   u.nkl = min((int)a.k_rows, te * kTileN);
   u.edge = (u.nkl - u.kb) / kTileN;
-  u.split = cta - s.cta_of(first);
+  u.slot = unit + cta;
   u.valid = 1;
 }
+
+// Where a launch of `ctas` CTAs has units for some whole rounds and a rest, the
+// rest's units are cut into as many pieces as there are CTAs for each.
+struct Tail {
+  int32_t full = INT32_MAX, cut = 1, units = 0;  // units before the rest; pieces; units of the rest
+  __device__ __forceinline__ void find(const TileArgs& a, int ctas, int lane) {
+    const int32_t all = UnitWalk::total(a, lane), rest = all % ctas;
+    if (rest > 0 && ctas / rest >= 2) {
+      full = all - rest;
+      cut = ctas / rest;
+      units = rest;
+    }
+  }
+};
+// Piece p of `cut` of a whole unit (empty where it has too few tiles).
+__device__ __forceinline__ void cut_unit(Unit& u, int p, int cut, int slot) {
+  const int c = min(cut, max(u.nt / 2, 1));
+  const int tb = p < c ? u.nt * p / c : u.nt, te = p < c ? u.nt * (p + 1) / c : u.nt;
+  u.slot = slot;
+  u.kb = tb * kTileN;
+  u.tile += tb;
+  u.nt0 = min(max(u.nt0 - tb, 0), te - tb);
+  u.nt = te - tb;
+  u.nkl = min(u.nkl, te * kTileN);
+  u.edge = max(min(u.lim, u.nkl) - u.kb, 0) / kTileN;
+}
+
+// The next unit of this CTA, one warp's work.  Calls give k = 0, 1, ..
+struct UnitSource {
+  UnitWalk walk;
+  Tail tail;
+  __device__ __forceinline__ void begin(const TileArgs& a, int lane) {
+    if (!a.q_off) return;
+    walk.load(a, lane);
+    if (a.tail) tail.find(a, gridDim.x, lane);
+  }
+  __device__ __forceinline__ void next(const TileArgs& a, int k, int lane, Unit& u) {
+    if (!a.q_off) {
+      prefix_unit(a, blockIdx.x, k, u);
+      return;
+    }
+    // Without a counter every other round runs backwards, so that no CTA gets
+    // the longer unit of every round.
+    int32_t w = k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    if (a.counter) {
+      w = blockIdx.x;
+      if (k > 0) {
+        uint32_t c = 0;
+        if (lane == 0) c = atomicAdd(a.counter, 1u);
+        w = gridDim.x + __shfl_sync(0xffffffffu, c, 0);
+      }
+    }
+    if (w < tail.full) {
+      walk.get(a, w, lane, u);
+    } else {
+      const int32_t v = w - tail.full, r = v / tail.cut;
+      u.valid = 0;
+      if (r >= tail.units) return;
+      walk.get(a, tail.full + r, lane, u);
+      if (u.valid) cut_unit(u, v - r * tail.cut, tail.cut, v);
+    }
+  }
+};
 
 // The kernel launched next (a programmatic dependent) may start; and: all that
 // kernels before this one wrote is visible.

@@ -52,6 +52,7 @@ namespace {
 using namespace tc;
 
 constexpr int kThreads = 512;
+constexpr int kUnitRing = 3;  // units that a CTA has taken: the last, the current and the next one
 constexpr int kGroup = 16;      // keys of one exponent
 constexpr int kGroups = kTileN / kGroup;
 constexpr int kSlots = 3;
@@ -237,7 +238,7 @@ __device__ void query_role(const TileArgs& a, Shared& sh, unsigned char* turn, u
   // Results of the unit in ring place `at`.
   auto results = [&](uint32_t at) {
     const Unit& u = sh.unit[at];
-    const int64_t split_row = (int64_t)u.split * a.q_rows + u.q_row;
+    const int64_t part_row = (int64_t)u.slot * kTileM + warp * 32;
     if (u.nt > 0) {
       if (!bar_wait_warp(&sh.r_full, n_r & 1, ab)) return false;
       ++n_r;
@@ -248,7 +249,7 @@ __device__ void query_role(const TileArgs& a, Shared& sh, unsigned char* turn, u
     for (int i = 0; i < 4; ++i) {
       const int h = u.kvh * a.group + hd[i];
       to[i] = pos[i] >= u.np0 ? nullptr
-              : a.splits      ? a.part + ((split_row + pos[i]) * a.heads + h) * a.dv + sub * 4
+              : u.slot >= 0   ? a.part + (part_row + i * 8 + (lane >> 2)) * a.dv + sub * 4
                               : (float*)a.out.p + (u.q_row + (int64_t)pos[i]) * a.out.row +
                                     h * a.out.head + sub * 4;
     }
@@ -284,7 +285,7 @@ __device__ void query_role(const TileArgs& a, Shared& sh, unsigned char* turn, u
       const int row = warp * 32 + lane, p = row / a.group, h = row - p * a.group + u.kvh * a.group;
       const int lim = min(a.causal ? u.lim + p : u.lim, u.nkl) - u.kb;
       if (p < u.np0) {
-        float* out = a.splits ? a.part + ((split_row + p) * a.heads + h) * a.dv
+        float* out = u.slot >= 0 ? a.part + (part_row + lane) * a.dv
                               : (float*)a.out.p + (u.q_row + (int64_t)p) * a.out.row + h * a.out.head;
         for (int k = 0; k < lim; ++k) {
           const int64_t im = (int64_t)(u.tile + k / kTileN) * a.kv_heads + u.kvh;
@@ -379,6 +380,7 @@ __device__ void query_role(const TileArgs& a, Shared& sh, unsigned char* turn, u
 template <bool PAGED>
 __global__ void __launch_bounds__(256) split_kernel(const __grid_constant__ TileArgs a) {
   let_next_start();
+  if (a.counter && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.counter = 0;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool is_v = blockIdx.y != 0;
   const int64_t at = blockIdx.x;  // tile * kv_heads + KV head
@@ -540,17 +542,12 @@ __device__ void mma_role(const TileArgs& a, Shared& sh, unsigned char* sm, uint3
 
 __device__ void unit_role(const TileArgs& a, Shared& sh, int lane) {
   volatile int* ab = &sh.abort;
-  UnitWalk walk;
-  if (a.q_off) walk.load(a, lane);
+  UnitSource source;
+  source.begin(a, lane);
   for (uint32_t nu = 0;; ++nu) {
+    if (!bar_wait_warp(&sh.u_empty[nu % kUnitRing], ((nu / kUnitRing) & 1) ^ 1, ab)) return;
     Unit u;
-    if (a.q_off) {
-      // Every other round runs backwards, so that no CTA gets the longer unit
-      // of every round.
-      walk.get(a, nu * gridDim.x + ((nu & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x), lane, u);
-    } else {
-      prefix_unit(a, blockIdx.x, nu, u);
-    }
+    source.next(a, nu, lane, u);
     if (u.valid) {  // does a tile hold values that are not finite?
       uint64_t odd = 0;
 #pragma unroll 4
@@ -558,7 +555,6 @@ __device__ void unit_role(const TileArgs& a, Shared& sh, int lane) {
         odd |= reinterpret_cast<const uint64_t*>(a.odd)[(int64_t)(u.tile + i) * a.kv_heads + u.kvh];
       u.patch = __any_sync(0xffffffffu, odd != 0);
     }
-    if (!bar_wait_warp(&sh.u_empty[nu % kUnitRing], ((nu / kUnitRing) & 1) ^ 1, ab)) return;
     if (lane == 0) {
       sh.unit[nu % kUnitRing] = u;
       bar_arrive(&sh.u_full[nu % kUnitRing]);
@@ -748,7 +744,7 @@ __device__ void row_role(const TileArgs& a, Shared& sh, uint32_t tmem, int row, 
       const int64_t orow = (int64_t)u.q_row + pos;
       const int head = u.kvh * a.group + hd;
       const float v = l == 0.f ? -INFINITY : (m - kLift + lg2(l)) * kLn2;
-      if (a.splits) a.part_lse[((int64_t)u.split * a.q_rows + orow) * a.heads + head] = v;
+      if (u.slot >= 0) a.part_lse[(int64_t)u.slot * kTileM + row] = v;
       else if (a.lse) a.lse[orow * a.heads + head] = v;
     }
     __syncwarp();
