@@ -1,0 +1,145 @@
+"""The exact side of one attention layer in a serving loop.
+
+A landmark state (nys.NystromStates) replaces a request's KV cache once its
+prompt is sealed; until then, and for layers and requests that stay exact, a
+server needs what this module puts together from the exact operators of
+nys.py: a pool of KV pages with a prefix that all requests share, the admission
+of prompts of any lengths, and one-token decode.
+
+    layer = ExactLayer(heads=16, kv_heads=8, d=128, dv=128, requests=64, ...)
+    layer.set_prefix(k, v)                    # a system prompt, once
+    out = layer.admit(q, k, v, lengths)       # packed prompts of all requests
+    out = layer.decode(q, k, v)               # one token for each of them
+    seal_prompts(states, q, k, v, lengths)    # landmark states of the same prompts
+
+Everything is enqueued on the current torch stream; the host only counts
+pages, so nothing waits for the GPU.
+"""
+from __future__ import annotations
+
+from . import nys
+
+
+def merge(out_a, lse_a, out_b, lse_b, out):
+    """Attention over two disjoint sets of keys from the results over each and
+    their log-sums: sum_x e^{lse_x} out_x / sum_x e^{lse_x}, in f32; rows that
+    saw neither set stay 0."""
+    import torch
+    top = torch.maximum(lse_a, lse_b)
+    top = torch.where(torch.isinf(top), torch.zeros_like(top), top)
+    wa, wb = torch.exp(lse_a - top), torch.exp(lse_b - top)
+    total = wa + wb
+    total = torch.where(total == 0, torch.ones_like(total), total)
+    a = (wa / total).unsqueeze(-1) * out_a.float()
+    out.copy_(a.addcmul_((wb / total).unsqueeze(-1), out_b.float()))
+    return out
+
+
+class ExactLayer:
+    """One layer's exact attention for `requests` requests of up to max_len
+    tokens each (besides the shared prefix), in pages of `page` tokens."""
+
+    def __init__(self, heads, kv_heads, d, dv, requests, n_pages, page, max_len, dtype=None,
+                 scale=None, device="cuda"):
+        import torch
+        self.torch = torch
+        self.device = torch.device(device)
+        self.attention = nys.ExactAttention(heads, kv_heads, d, dv, dtype=dtype, scale=scale,
+                                            device=device)
+        self.cache = nys.PagedKV(n_pages, page, kv_heads, d, dv, dtype=dtype, device=device)
+        self.requests, self.page = requests, page
+        self.width = -(-max_len // page)
+        i32 = dict(dtype=torch.int32, device=self.device)
+        self.table = torch.full((requests, self.width), -1, **i32)
+        self.free = torch.arange(n_pages, **i32)
+        self.used = 0                       # pages taken from the front of `free`
+        self.lengths = [0] * requests       # tokens of each request, as the host counts them
+        self.lens = torch.zeros(requests, **i32)
+        self.prefix_len = 0
+        self.prefix_pages = None
+        self._plans = {}
+
+    def _plan(self, fresh):
+        """Pages and slots for fresh[i] more tokens of request i."""
+        torch, total = self.torch, sum(fresh)
+        if total not in self._plans:
+            self._plans = {total: nys.PagePlan(self.requests, self.width, total, self.page,
+                                               device=self.device)}
+        plan = self._plans[total]
+        pages = lambda n: -(-n // self.page)
+        need = sum(pages(a + b) - pages(a) for a, b in zip(self.lengths, fresh))
+        if self.used + need > self.free.shape[0]:
+            raise ValueError(f"{need} more pages wanted, {self.free.shape[0] - self.used} left")
+        if max(a + b for a, b in zip(self.lengths, fresh)) > self.width * self.page:
+            raise ValueError("a request would outgrow max_len")
+        grow = torch.tensor(fresh, dtype=torch.int32, device=self.device)
+        plan.update(self.lens, grow, self.free[self.used:], self.table)
+        self.used += need
+        self.lengths = [a + b for a, b in zip(self.lengths, fresh)]
+        self.lens.copy_(plan.lens)
+        return plan
+
+    def set_prefix(self, k, v):
+        """Keys and values [rows][kv_heads][d|dv] that every request sees first;
+        before any request is admitted."""
+        if self.used:
+            raise ValueError("the prefix comes before the first request")
+        torch, n = self.torch, k.shape[0]
+        self.used = -(-n // self.page)
+        self.prefix_pages = self.free[:self.used].clone()
+        self.prefix_len = n
+        at = torch.arange(n, device=self.device)
+        self.cache.write(k, v, self.prefix_pages.long()[at // self.page] * self.page
+                         + at % self.page)
+
+    def admit(self, q, k, v, lengths):
+        """The requests' prompts, packed back to back (q [sum][heads][d], k and v
+        [sum][kv_heads][d|dv]): into their pages, and attended causally after the
+        prefix.  Returns [sum][heads][dv]."""
+        torch, att = self.torch, self.attention
+        if any(self.lengths):
+            raise ValueError("admit() takes requests from their first token")
+        plan = self._plan(list(lengths))
+        self.cache.write(k, v, plan.slots)
+        rows = q.shape[0]
+        out = torch.empty((rows, att.heads, att.dv), dtype=att.dtype, device=self.device)
+        if self.prefix_len == 0:
+            return att.prompt(q, k, v, plan.q_off, out)
+        # Over the prompt's own keys and, as rows without own keys, over the prefix.
+        lse, over = torch.empty((2, rows, att.heads), device=self.device).unbind(0)
+        att.prompt(q, k, v, plan.q_off, out, lse=lse)
+        first = torch.empty_like(out)
+        none = torch.zeros(rows, dtype=torch.int32, device=self.device)
+        att.shared(q, self.cache, none, none.view(rows, 1), first,
+                   prefix_pages=self.prefix_pages, prefix_len=self.prefix_len, lse=over)
+        return merge(out, lse, first, over, out)
+
+    def decode(self, q, k, v):
+        """One new token for every request: q [requests][heads][d], k and v
+        [requests][kv_heads][d|dv].  Returns [requests][heads][dv]."""
+        att = self.attention
+        plan = self._plan([1] * self.requests)
+        self.cache.write(k, v, plan.slots)
+        out = self.torch.empty((self.requests, att.heads, att.dv), dtype=att.dtype,
+                               device=self.device)
+        return att.shared(q, self.cache, self.lens, self.table, out,
+                          prefix_pages=self.prefix_pages, prefix_len=self.prefix_len)
+
+
+def seal_prompts(states, q, k, v, lengths, g0=0):
+    """Seals landmark states on packed prompts (the tensors of
+    ExactLayer.admit, f32): request i's KV head j becomes group
+    g0 + i * kv_heads + j of `states`."""
+    import torch
+    rows, heads, d = q.shape
+    kv, group = k.shape[1], heads // k.shape[1]
+    qs, ks, vs = [], [], []
+    at = 0
+    for t in lengths:
+        cut = slice(at, at + t)
+        qs.append(q[cut].view(t, kv, group, d).permute(1, 2, 0, 3).reshape(-1, d))
+        ks.append(k[cut].transpose(0, 1).reshape(-1, d))
+        vs.append(v[cut].transpose(0, 1).reshape(-1, v.shape[2]))
+        at += t
+    states.seal_ragged([t for t in lengths for _ in range(kv)], torch.cat(qs), torch.cat(ks),
+                       torch.cat(vs), g0=g0)

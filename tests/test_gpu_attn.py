@@ -436,3 +436,139 @@ def test_write(cuda_device, dtype, tokens, kv, d, dv, odd):
     cache = nys.PagedKV(n_pages, page, kv, d, dv, dtype=dt, device=cuda_device, k=pk, v=pv)
     cache.write(k, v, slots)
     assert torch.equal(pk.view(-1, kv, d), wk) and torch.equal(pv.view(-1, kv, dv), wv)
+
+
+# ------------------------------------------------- the tiled kernels' own corners
+@pytest.mark.parametrize("dtype,q_lens,k_lens", [
+    ("float32", [1300], [2350]), ("float32", [70, 1250], [1100, 1400]),
+    ("bfloat16", [2500], [2500]), ("float16", [1, 2440], [1200, 2900])])
+def test_prompt_last_round_is_cut(cuda_device, dtype, q_lens, k_lens):
+    """Slightly more units than SMs: the rest's keys are cut into pieces and
+    joined; values that are not finite still reach the rows that see them, and
+    only those."""
+    torch, ref, nys = _mods()
+    _run_prompt(cuda_device, dtype, (16, 8, 128, 128), q_lens, k_lens)
+    dt = getattr(torch, dtype)
+    q, k, v, qo, ko = _inputs(torch, cuda_device, q_lens, k_lens, 16, 8, 128, 128, dt)
+    want, wl, b, lb = ref.prompt(q, k, v, q_lens, k_lens, 2, 1 / math.sqrt(128), dt)
+    at = sum(k_lens) - 40          # in the last sequence, seen by its last 40 queries
+    v[at, 3, 9] = math.inf
+    v[sum(k_lens[:-1]) + 5, 6, 1] = math.nan
+    att = nys.ExactAttention(16, 8, 128, 128, dtype=dt, device=cuda_device)
+    out = torch.empty_like(q)
+    att.prompt(q, k, v, qo, out, k_off=ko)
+    hit = torch.zeros(out.shape, dtype=torch.bool)
+    hit[-40:, 6:8, 9] = True
+    # Key 5 is seen from query 5 - (nk - nq) of its sequence on.
+    hit[sum(q_lens[:-1]) + max(0, 5 - (k_lens[-1] - q_lens[-1])):, 12:14, 1] = True
+    got = out.float().cpu()
+    assert not torch.isfinite(got[hit]).any()
+    ref.check(got[~hit], want[~hit], b[~hit], "out")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_prompt_without_workspace(cuda_device, dtype):
+    torch, ref, nys = _mods()
+    dt = getattr(torch, dtype)
+    lens = [200, 65] * 12
+    q, k, v, qo, ko = _inputs(torch, cuda_device, lens, lens, 16, 8, 64, 64, dt)
+    out = torch.empty_like(q)
+    cfg = nys.NysAttnConfig(16, 8, 64, 64, nys._dtype_code(dt), 0.0)
+    r = lambda t, h: nys._rows(t, dt, h, 64, "t")
+    nys.nys_attn_prompt(cfg, len(lens), sum(lens), sum(lens), qo.data_ptr(), None, r(q, 16), r(k, 8),
+                        r(v, 8), r(out, 16), stream=torch.cuda.current_stream().cuda_stream)
+    want, _, b, _ = ref.prompt(q, k, v, lens, lens, 2, 1 / 8.0, dt)
+    ref.check(out, want, b, "out")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_prompt_row_offsets_past_32_bits(cuda_device, dtype):
+    """Keys whose rows lie 2^24 elements apart: the last ones begin past 2^32."""
+    torch, ref, nys = _mods()
+    dt = getattr(torch, dtype)
+    n, d, gap = 300, 64, 1 << 24
+    q, k, v, qo, ko = _inputs(torch, cuda_device, [n], [n], 2, 1, d, d, dt)
+    big = torch.empty(n * gap // (1 if dt != torch.float32 else 2), dtype=dt, device=cuda_device)
+    step = big.numel() // n
+    kk = big.as_strided((n, 1, d), (step, d, 1))
+    vv = big.as_strided((n, 1, d), (step, d, 1), 4096)
+    kk.copy_(k), vv.copy_(v)
+    att = nys.ExactAttention(2, 1, d, d, dtype=dt, device=cuda_device)
+    out = torch.empty_like(q)
+    att.prompt(q, kk, vv, qo, out)
+    want, _, b, _ = ref.prompt(q, k, v, [n], [n], 2, 1 / 8.0, dt)
+    ref.check(out, want, b, "out")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_prompt_result_does_not_depend_on_the_batch(cuda_device, dtype):
+    """A sequence alone and in a large batch: within both results' bounds."""
+    torch, ref, nys = _mods()
+    dt = getattr(torch, dtype)
+    lens = [77] + [(i * 29) % 190 for i in range(300)]
+    q, k, v, qo, ko = _inputs(torch, cuda_device, lens, lens, 4, 2, 128, 128, dt)
+    att = nys.ExactAttention(4, 2, 128, 128, dtype=dt, device=cuda_device)
+    out = torch.empty_like(q)
+    att.prompt(q, k, v, qo, out)
+    alone = torch.empty_like(q[:77])
+    att.prompt(q[:77], k[:77], v[:77], qo[:2].contiguous(), alone)
+    want, _, b, _ = ref.prompt(q[:77], k[:77], v[:77], [77], [77], 2, 1 / math.sqrt(128), dt)
+    ref.check(out[:77], want, b, "in the batch")
+    ref.check(alone, want, b, "alone")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("geo", [(16, 8, 128, 128), (64, 1, 64, 64), (40, 1, 64, 128)])
+def test_shared_wide_groups_and_long_prefix(cuda_device, dtype, geo):
+    _run_shared(cuda_device, dtype, geo, [200, 3, 0, 66], 1500, 16)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_shared_bad_value_in_the_prefix(cuda_device, dtype):
+    """Infinities and NaN of the prefix and of own pages reach the requests that
+    see them, in their channel."""
+    torch, ref, nys = _mods()
+    dt = getattr(torch, dtype)
+    heads, kv, d, page, prefix, lens = 4, 2, 64, 16, 250, [20, 0, 33]
+    k, v, pp, table = _pool(torch, cuda_device, lens, prefix, page, kv, d, d, dt)
+    q = torch.randn((3, heads, d), device=cuda_device).to(dt)
+    want, _, b, _ = ref.shared(q, k, v, pp, prefix, lens, table, 2, 1 / 8.0, dt)
+    v[pp[1], 3, 0, 5] = math.inf       # the prefix, KV head 0
+    v[table[2][1], 2, 1, 7] = math.nan  # request 2, KV head 1
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)
+    cache = nys.PagedKV(k.shape[0], page, kv, d, d, dtype=dt, device=cuda_device, k=k, v=v)
+    att = nys.ExactAttention(heads, kv, d, d, dtype=dt, device=cuda_device)
+    out = torch.empty((3, heads, d), device=cuda_device, dtype=dt)
+    att.shared(q, cache, i32(lens), i32(table), out, prefix_pages=i32(pp), prefix_len=prefix)
+    hit = torch.zeros(out.shape, dtype=torch.bool)
+    hit[:, :2, 5] = True
+    hit[2, 2:, 7] = True
+    got = out.float().cpu()
+    assert not torch.isfinite(got[hit]).any()
+    ref.check(got[~hit], want[~hit], b[~hit], "out")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_shared_in_a_graph(cuda_device, dtype):
+    torch, ref, nys = _mods()
+    dt = getattr(torch, dtype)
+    heads, kv, d, page, prefix, lens = 8, 2, 128, 16, 300, [40, 500, 1]
+    k, v, pp, table = _pool(torch, cuda_device, lens, prefix, page, kv, d, d, dt, junk=0.0)
+    q = torch.randn((3, heads, d), device=cuda_device).to(dt)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)
+    tl, tt, tp = i32(lens), i32(table), i32(pp)
+    cache = nys.PagedKV(k.shape[0], page, kv, d, d, dtype=dt, device=cuda_device, k=k, v=v)
+    att = nys.ExactAttention(heads, kv, d, d, dtype=dt, device=cuda_device)
+    out = torch.empty_like(q)
+    run = lambda: att.shared(q, cache, tl, tt, out, prefix_pages=tp, prefix_len=prefix)
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    q.copy_(torch.randn_like(q))
+    tl.copy_(i32([33, 499, 0]))
+    out.zero_()
+    graph.replay()
+    want, _, b, _ = ref.shared(q, k, v, pp, prefix, [33, 499, 0], table, 4, 1 / math.sqrt(d), dt)
+    ref.check(out, want, b, "replayed")

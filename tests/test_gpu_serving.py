@@ -1,0 +1,87 @@
+"""The exact operators together, as a serving loop uses them: a shared prefix,
+prompts admitted in one packed batch, tokens decoded one by one, and landmark
+states sealed on the same prompts."""
+import math
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
+@pytest.mark.parametrize("prefix", [0, 37])
+def test_layer_serves_prompts_and_tokens(cuda_device, dtype, prefix):
+    import torch
+    import attn_reference as ref
+    from streaming_nystr_landmark_gb300 import serving
+    dt = getattr(torch, dtype)
+    heads, kv, d, dv, page, tokens = 8, 2, 64, 128, 16, 6
+    lens = [1, 40, 16, 0, 129]
+    g = torch.Generator(device=cuda_device).manual_seed(3)
+    rn = lambda *s: torch.randn(s, generator=g, device=cuda_device).to(dt)
+    layer = serving.ExactLayer(heads, kv, d, dv, len(lens), 64, page, 160, dtype=dt,
+                               device=cuda_device)
+    pk, pv = rn(prefix, kv, d), rn(prefix, kv, dv)
+    if prefix:
+        layer.set_prefix(pk, pv)
+    q, k, v = rn(sum(lens), heads, d), rn(sum(lens), kv, d), rn(sum(lens), kv, dv)
+    out = layer.admit(q, k, v, lens)
+    # Plain form: every request's keys are the prefix's and its own.
+    ks = [torch.cat([pk, x]) for x in k.split(lens)]
+    vs = [torch.cat([pv, x]) for x in v.split(lens)]
+    want, _, bound, _ = ref.prompt(q, torch.cat(ks), torch.cat(vs), lens,
+                                   [prefix + x for x in lens], heads // kv, 1 / math.sqrt(d), dt)
+    # Two results are rounded to their type and weighed before the last rounding.
+    extra = 0.0 if dt == torch.float32 else 2 * ref.EPS[dt] * float(torch.cat(vs).abs().max())
+    ref.check(out, want, 2 * bound + extra + 2.0 ** -22, "prompts")
+    for _ in range(tokens):
+        q1, k1, v1 = rn(len(lens), heads, d), rn(len(lens), kv, d), rn(len(lens), kv, dv)
+        out = layer.decode(q1, k1, v1)
+        ks = [torch.cat([a, b[None]]) for a, b in zip(ks, k1)]
+        vs = [torch.cat([a, b[None]]) for a, b in zip(vs, v1)]
+        want, _, bound, _ = ref.prompt(q1, torch.cat(ks), torch.cat(vs), [1] * len(lens),
+                                       [len(x) for x in ks], heads // kv, 1 / math.sqrt(d), dt)
+        ref.check(out, want, bound, "token")
+    assert layer.attention.status() == 0
+    assert layer.lens.tolist() == [x + tokens for x in lens]
+
+
+def test_layer_refuses_what_does_not_fit(cuda_device):
+    import torch
+    from streaming_nystr_landmark_gb300 import serving
+    layer = serving.ExactLayer(2, 2, 64, 64, 2, 4, 8, 16, dtype=torch.bfloat16, device=cuda_device)
+    z = lambda n, h: torch.zeros((n, h, 64), dtype=torch.bfloat16, device=cuda_device)
+    with pytest.raises(ValueError, match="outgrow"):
+        layer.admit(z(20, 2), z(20, 2), z(20, 2), [3, 17])
+    layer.admit(z(24, 2), z(24, 2), z(24, 2), [8, 16])
+    with pytest.raises(ValueError, match="pages"):
+        serving.ExactLayer(2, 2, 64, 64, 2, 2, 8, 16, dtype=torch.bfloat16,
+                           device=cuda_device).admit(z(24, 2), z(24, 2), z(24, 2), [8, 16])
+    with pytest.raises(ValueError, match="first token"):
+        layer.admit(z(2, 2), z(2, 2), z(2, 2), [1, 1])
+    with pytest.raises(ValueError, match="before"):
+        layer.set_prefix(z(2, 2), z(2, 2))
+
+
+def test_landmark_states_of_the_same_prompts(cuda_device):
+    """seal_prompts seals exactly what nys_seal seals group by group."""
+    import torch
+    from streaming_nystr_landmark_gb300 import nys, serving
+    heads, kv, d, lens = 4, 2, 64, [80, 131]
+    m, w, sink = 8, 16, 4
+    g = torch.Generator(device=cuda_device).manual_seed(1)
+    rn = lambda *s: torch.randn(s, generator=g, device=cuda_device)
+    q, k, v = rn(sum(lens), heads, d), rn(sum(lens), kv, d), rn(sum(lens), kv, d)
+    geo = (m, w, sink, heads // kv, d, d, len(lens) * kv)
+    both = nys.NystromStates(*geo, device=cuda_device)
+    serving.seal_prompts(both, q, k, v, lens)
+    each = nys.NystromStates(*geo, device=cuda_device)
+    at = 0
+    for i, t in enumerate(lens):
+        cut = slice(at, at + t)
+        qs = q[cut].view(t, kv, heads // kv, d).permute(1, 2, 0, 3).contiguous()
+        each.seal(qs, k[cut].transpose(0, 1).contiguous(), v[cut].transpose(0, 1).contiguous(),
+                  g0=i * kv, n=kv)
+        at += t
+    for name in ("win_k", "sink_v", "k_tilde", "q_tilde", "mu", "t_hat", "z_hat", "m_max", "far_len"):
+        assert torch.equal(both.region(name), each.region(name)), name
