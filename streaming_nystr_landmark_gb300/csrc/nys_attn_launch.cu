@@ -27,22 +27,32 @@ EncodeTiled encoder() {
   return fn;
 }
 
-// Map of a [rows][heads][dim] tensor of 16-bit elements; boxes of 64 columns,
-// `box_h` heads and `box_r` rows, 128-byte swizzle.  Strides in elements; those
-// of extents of one are not used and replaced by valid ones.
+// Map of a [rows][heads][dim] tensor of 16-bit elements for tiles in shared
+// memory of [64-column block][row][head][64 columns], 128-byte swizzle: its
+// dimensions are 64 columns, heads, rows, blocks, so that one copy of a full
+// tile's 128 rows brings all blocks (a copy costs its thread about 200 clocks to
+// issue); smaller boxes bring one block.  A dim that is no multiple of 64 has one
+// block of `dim` columns instead, of which a copy takes 64, with zeros past the
+// end.  Strides in elements; those of extents of one are not used and replaced
+// by valid ones.
 bool make_map(CUtensorMap* m, int dtype, const void* p, int64_t rows, int64_t heads, int64_t dim,
               int64_t row, int64_t head, int box_h, int box_r) {
-  const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)rows};
+  const bool whole = dim % 64 == 0;
+  const cuuint64_t blocks = whole ? (cuuint64_t)(dim / 64) : 1;
+  const cuuint64_t dims[4] = {(cuuint64_t)(whole ? 64 : dim), (cuuint64_t)heads, (cuuint64_t)rows,
+                              blocks};
   const cuuint64_t line = (cuuint64_t)((dim * 2 + 15) & ~int64_t(15));
-  const cuuint64_t st[2] = {heads > 1 ? (cuuint64_t)head * 2 : line,
-                            rows > 1 ? (cuuint64_t)row * 2 : line * (cuuint64_t)heads};
-  const cuuint32_t box[3] = {64, (cuuint32_t)box_h, (cuuint32_t)box_r};
-  const cuuint32_t one[3] = {1, 1, 1};
+  const cuuint64_t st[3] = {heads > 1 ? (cuuint64_t)head * 2 : line,
+                            rows > 1 ? (cuuint64_t)row * 2 : line * (cuuint64_t)heads,
+                            blocks > 1 ? 128 : line * (cuuint64_t)heads * (cuuint64_t)rows};
+  const cuuint32_t box[4] = {64, (cuuint32_t)box_h, (cuuint32_t)box_r,
+                             box_h * box_r == kTileM ? (cuuint32_t)blocks : 1u};
+  const cuuint32_t one[4] = {1, 1, 1, 1};
   const EncodeTiled enc = encoder();
   return enc && enc(m,
                     dtype == NYS_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                    3, const_cast<void*>(p), dims, st, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    4, const_cast<void*>(p), dims, st, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

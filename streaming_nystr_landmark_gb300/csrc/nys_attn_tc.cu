@@ -61,7 +61,10 @@ struct Shared {
   uint64_t q_full, q_empty;
   uint64_t kv_full[kSlots], kv_empty[kSlots];
   uint64_t v_raw[kSlots];  // a value tile landed that is to be cleaned first
-  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], ml_full[2];
+  // A barrier's phases have to be seen one by one by whoever waits on it, so O's
+  // completion has a pair of barriers for units whose streams are read each by
+  // its own warpgroup, and one for units that both read.
+  uint64_t s_full[2], p_full[2], o_full[2], both_full[2], o_empty[2], ml_full[2];
   uint64_t u_full[kUnitRing], u_empty[kUnitRing];
   uint64_t drain;
   Unit unit[kUnitRing];
@@ -109,20 +112,36 @@ __device__ void load_role(const TileArgs& a, const CUtensorMap* mq, const CUtens
   uint32_t raw_phase = 0, raw_last = 0;  // per slot: v_raw's phase; whether its last tile went there
   const int chunks_d = (a.d + 63) / 64, chunks_v = (a.dv + 63) / 64;
   const uint32_t q_tile = (uint32_t)(chunks_d * 128 * a.group * a.tp);
+  // One 64-column block of a box, or all of them where the box is a full tile
+  // (make_map's boxes).
+  auto copy = [&](unsigned char* dst, const CUtensorMap* m, int dim, int rows, int y, int z,
+                  uint64_t* bar) {
+    const bool whole = dim % 64 == 0;
+    const int n = whole && rows == kTileM ? 1 : (dim + 63) / 64;
+    for (int c = 0; c < n; ++c)
+      tma_load4(dst + c * 16384, m, whole ? 0 : c * 64, y, z, whole ? c : 0, bar);
+  };
   const int boxes = PAGED ? kTileN / a.box : 1;
   const int none = PAGED ? (int)(a.n_pages * a.page) : 0;  // past the tensor's end: reads as zeros
-  // Row of this lane's box of the tile at `key`: outside the prefix or the pool
-  // the one past the end.
+  // The page of this lane's box of the tile at `key` and the box's place in it;
+  // the number is not touched before the next tile's turn.
+  int next_page = -1, next_in = 0;
   auto look = [&](int key) {
-    int row = none;
     key += lane * a.box;
+    next_page = -1;
+    next_in = -1;
     if (lane < boxes && key < a.k_rows) {
       const int pi = key / a.page;
-      const int32_t pg = a.pages[pi];
-      if (pg >= 0 && pg < a.n_pages) row = pg * a.page + (key - pi * a.page);
-      else attn_report(a.status, NYS_ATTN_BAD_PAGE);
+      next_in = key - pi * a.page;
+      next_page = a.pages[pi];
     }
-    return row;
+  };
+  // Its row: outside the prefix or the pool the one past the end.
+  auto row_of = [&](int page, int in) {
+    if (in < 0) return none;
+    if (page >= 0 && page < a.n_pages) return page * a.page + in;
+    attn_report(a.status, NYS_ATTN_BAD_PAGE);
+    return none;
   };
   for (;; ++nu) {
     if (!bar_wait_warp(&sh.u_full[nu % kUnitRing], (nu / kUnitRing) & 1, ab)) break;
@@ -137,23 +156,21 @@ __device__ void load_role(const TileArgs& a, const CUtensorMap* mq, const CUtens
     if (elect_one()) {
       bar_expect(&sh.q_full, q_tile * (pair ? 2 : 1));
       for (int s = 0; s <= (pair ? 1 : 0); ++s)
-        for (int c = 0; c < chunks_d; ++c)
-          tma_load3(sm + s * 32768 + c * 16384, mq, c * 64, u.kvh * a.group, u.q_row + s * a.tp,
-                    &sh.q_full);
+        copy(sm + s * 32768, mq, a.d, a.group * a.tp, u.kvh * a.group, u.q_row + s * a.tp, &sh.q_full);
     }
     const int y = a.kv_y ? u.kvh : 0;
-    int next_row = PAGED ? look(u.kb) : 0;
+    if (PAGED) look(u.kb);
     bool ok = true;
     for (int e = 0; e < 2 * u.nt; ++e) {
       bool is_k;
       int j;
       tile_at(e, u.nt, pair, is_k, j);
-      const int my_row = next_row;
+      const int my_page = next_page, my_in = next_in;
       if (PAGED && e + 1 < 2 * u.nt) {
         bool k1;
         int j1;
         tile_at(e + 1, u.nt, pair, k1, j1);
-        next_row = look(u.kb + j1 * kTileN);
+        look(u.kb + j1 * kTileN);
       }
       const uint32_t slot = cnt % kSlots;
       ok = bar_wait_warp(&sh.kv_empty[slot], ((cnt / kSlots) & 1) ^ 1, ab);
@@ -170,17 +187,16 @@ __device__ void load_role(const TileArgs& a, const CUtensorMap* mq, const CUtens
       if (!PAGED) {
         if (elect_one()) {
           bar_expect(full, (uint32_t)chunks * 16384u);
-          for (int c = 0; c < chunks; ++c)
-            tma_load3(dst + c * 16384, m, c * 64, y, u.k_row + u.kb + j * kTileN, full);
+          copy(dst, m, is_k ? a.d : a.dv, kTileN, y, u.k_row + u.kb + j * kTileN, full);
         }
       } else {
+        const int my_row = row_of(my_page, my_in);
         if (elect_one()) bar_expect(full, (uint32_t)chunks * 16384u);
         __syncwarp();
         for (int b = 0; b < boxes; ++b) {
           const int row = __shfl_sync(0xffffffffu, my_row, b);
           if (elect_one())
-            for (int c = 0; c < chunks; ++c)
-              tma_load3(dst + c * 16384 + b * a.box * 128, m, c * 64, y, row, full);
+            copy(dst + b * a.box * 128, m, is_k ? a.d : a.dv, a.box, y, row, full);
         }
       }
       __syncwarp();
@@ -209,7 +225,7 @@ __device__ void mma_role(const TileArgs& a, Shared& sh, unsigned char* sm, uint3
   const uint32_t id_o = idesc(kTileM, nv, Type16<T>::kBf16, true);
   const uint32_t q0 = sptr(sm), kv0 = sptr(sm + kQBytes);
   uint32_t base = 0, nu = 0, nq = 0;
-  uint32_t n_p[2] = {0, 0};
+  uint32_t n_p[2] = {0, 0}, n_o[2] = {0, 0};  // P tiles of each stream; units that used its O
   bool ok = true;
   for (; ok; ++nu) {
     if (!bar_wait(&sh.u_full[nu % kUnitRing], (nu / kUnitRing) & 1, ab)) break;
@@ -218,7 +234,6 @@ __device__ void mma_role(const TileArgs& a, Shared& sh, unsigned char* sm, uint3
     if (!u.valid) break;
     const bool pair = u.np1 > 0;
     const int n_of[2] = {pair ? u.nt0 : (u.nt + 1) / 2, pair ? u.nt : u.nt / 2};
-    bool o_free[2] = {false, false};
     if (u.nt > 0) {
       if (!bar_wait(&sh.q_full, nq & 1, ab)) break;
       ++nq;
@@ -246,8 +261,8 @@ __device__ void mma_role(const TileArgs& a, Shared& sh, unsigned char* sm, uint3
       if (!bar_wait(&sh.p_full[s], n_p[s] & 1, ab)) return false;
       ++n_p[s];
       if (first) {
-        if (!bar_wait(&sh.o_empty[s], (nu & 1) ^ 1, ab)) return false;
-        o_free[s] = true;
+        if (!bar_wait(&sh.o_empty[s], (n_o[s] & 1) ^ 1, ab)) return false;
+        ++n_o[s];
       }
       fence_after();
       const uint64_t v = desc128(kv0 + slot * kSlotBytes, 16384, 1024);
@@ -281,7 +296,7 @@ __device__ void mma_role(const TileArgs& a, Shared& sh, unsigned char* sm, uint3
         ok = values(s, j, j < 2);
         if (!ok) break;
         free_slot(v_at(j, u.nt, false));
-        if (j + 2 >= u.nt) commit(&sh.o_full[s]);
+        if (j + 2 >= u.nt) commit(&sh.both_full[s]);
         if (j + 2 < u.nt) {
           ok = scores(s, j + 2);
           if (ok) free_slot(k_at(j + 2, false));
@@ -289,8 +304,6 @@ __device__ void mma_role(const TileArgs& a, Shared& sh, unsigned char* sm, uint3
       }
     }
     if (!ok) break;
-    for (int s = 0; s < 2; ++s)
-      if (!o_free[s] && !bar_wait(&sh.o_empty[s], (nu & 1) ^ 1, ab)) ok = false;
     base += 2 * (uint32_t)u.nt;
   }
   // Every product and arrival in flight ends before the CTA may leave.
@@ -403,7 +416,7 @@ __device__ void row_role(const TileArgs& a, Shared& sh, uint32_t tmem, int s, in
   const int pos = row / a.group, hd = row - pos * a.group;
   const uint32_t lane_at = (uint32_t)(row & ~31) << 16;
   const uint32_t s_at = tmem + lane_at + s * 128, o_at = tmem + lane_at + 256;
-  uint32_t n_s = 0, n_o0 = 0, n_o1 = 0, n_merge = 0;
+  uint32_t n_s = 0, n_own = 0, n_both[2] = {0, 0}, n_merge = 0;
   for (uint32_t nu = 0;; ++nu) {
     if (!bar_wait_warp(&sh.u_full[nu % kUnitRing], (nu / kUnitRing) & 1, ab)) return;
     const Unit u = sh.unit[nu % kUnitRing];
@@ -415,6 +428,7 @@ __device__ void row_role(const TileArgs& a, Shared& sh, uint32_t tmem, int s, in
     // Keys that this row sees, and that every row of the tile sees.
     const int lim0 = min(a.causal ? u.lim + shift : u.lim, u.nkl) - u.kb;
     const int lim = min(a.causal ? u.lim + shift + pos : u.lim, u.nkl) - u.kb;
+    const bool mine = pos < (pair && s == 1 ? u.np1 : u.np0);
     float m = -INFINITY, l = 0.f;
     for (int j = first; j < end; j += step) {
       if (!bar_wait_warp(&sh.s_full[s], n_s & 1, ab)) return;
@@ -445,7 +459,8 @@ __device__ void row_role(const TileArgs& a, Shared& sh, uint32_t tmem, int s, in
         t3 = max3(t3, __uint_as_float(x[c + 6]), __uint_as_float(x[c + 7]));
       }
       const float top = fmaxf(fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)), m);
-      const bool grow = m == -INFINITY ? top > m : (top - m) * sc > kLazy;
+      // (Rows that are not stored hold anything: they have no say in it.)
+      const bool grow = mine && (m == -INFINITY ? top > m : (top - m) * sc > kLazy);
       if (__any_sync(0xffffffffu, grow)) {
         const float alpha = top == m ? 1.f : ex2((m - top) * sc);
         m = top;
@@ -497,10 +512,21 @@ __device__ void row_role(const TileArgs& a, Shared& sh, uint32_t tmem, int s, in
     const int n0 = pair ? u.nt0 : (u.nt + 1) / 2, n1 = pair ? u.nt : u.nt / 2;
     const bool has0 = n0 > 0, has1 = n1 > 0;
     const bool use0 = has0 && (!pair || s == 0), use1 = has1 && (!pair || s == 1);
-    if (use0 && !bar_wait_warp(&sh.o_full[0], n_o0 & 1, ab)) return;
-    if (use1 && !bar_wait_warp(&sh.o_full[1], n_o1 & 1, ab)) return;
-    n_o0 += has0;
-    n_o1 += has1;
+    if (pair) {
+      if (use0 || use1) {
+        if (!bar_wait_warp(&sh.o_full[s], n_own & 1, ab)) return;
+        ++n_own;
+      }
+    } else {
+      if (has0) {
+        if (!bar_wait_warp(&sh.both_full[0], n_both[0] & 1, ab)) return;
+        ++n_both[0];
+      }
+      if (has1) {
+        if (!bar_wait_warp(&sh.both_full[1], n_both[1] & 1, ab)) return;
+        ++n_both[1];
+      }
+    }
     float a0, a1, total, top = m;
     if (pair) {
       total = l;
@@ -514,10 +540,14 @@ __device__ void row_role(const TileArgs& a, Shared& sh, uint32_t tmem, int s, in
         sh.ml[s][row][0] = m;
         sh.ml[s][row][1] = l;
       }
-      __syncwarp();
-      if (lane == 0) bar_arrive(&sh.ml_full[s]);
-      if (!bar_wait_warp(&sh.ml_full[1 - s], n_merge & 1, ab)) return;
-      ++n_merge;
+      // (A unit without tiles is left out: nothing would hold one warpgroup back
+      // from its next arrival until the other has seen this one.)
+      if (has0) {
+        __syncwarp();
+        if (lane == 0) bar_arrive(&sh.ml_full[s]);
+        if (!bar_wait_warp(&sh.ml_full[1 - s], n_merge & 1, ab)) return;
+        ++n_merge;
+      }
       const bool other = s == 0 ? has1 : has0;
       const float mo = other ? sh.ml[1 - s][row][0] : -INFINITY;
       const float lo = other ? sh.ml[1 - s][row][1] : 0.f;
@@ -532,7 +562,6 @@ __device__ void row_role(const TileArgs& a, Shared& sh, uint32_t tmem, int s, in
     const float inv = total == 0.f ? 0.f : reciprocal(total);
     a0 *= inv;
     a1 *= inv;
-    const bool mine = pos < (pair && s == 1 ? u.np1 : u.np0);
     const int64_t orow = (int64_t)u.q_row + shift + pos;
     const int head = u.kvh * a.group + hd;
     const bool patch = *(volatile int*)&sh.unit[nu % kUnitRing].patch != 0;
@@ -584,12 +613,14 @@ __device__ void row_role(const TileArgs& a, Shared& sh, uint32_t tmem, int s, in
     fence_before();
     __syncwarp();
     if (lane == 0) {
-      // Eight arrivals free an O: four warps twice, or eight warps once.
+      // Eight arrivals free an O that was used: four warps twice, or eight warps
+      // once.  An O that was not gets none, so that its barrier never runs ahead
+      // of the products' thread.
       if (pair) {
-        bar_arrive(&sh.o_empty[s], 2);
+        if (s == 0 ? has0 : has1) bar_arrive(&sh.o_empty[s], 2);
       } else {
-        bar_arrive(&sh.o_empty[0]);
-        bar_arrive(&sh.o_empty[1]);
+        if (has0) bar_arrive(&sh.o_empty[0]);
+        if (has1) bar_arrive(&sh.o_empty[1]);
       }
       bar_arrive(&sh.u_empty[nu % kUnitRing]);
     }
@@ -620,6 +651,7 @@ attn_tc_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CUten
       bar_init(&sh.s_full[i], 1);
       bar_init(&sh.p_full[i], 4);
       bar_init(&sh.o_full[i], 1);
+      bar_init(&sh.both_full[i], 1);
       bar_init(&sh.o_empty[i], 8);
       bar_init(&sh.ml_full[i], 4);
     }

@@ -85,12 +85,12 @@ __device__ __forceinline__ bool bar_wait_warp(uint64_t* b, uint32_t parity, vola
   return __all_sync(0xffffffffu, bar_wait(b, parity, abort));
 }
 
-__device__ __forceinline__ void tma_load3(void* dst, const CUtensorMap* map, int x, int y, int z,
-                                          uint64_t* bar) {
+__device__ __forceinline__ void tma_load4(void* dst, const CUtensorMap* map, int x, int y, int z,
+                                          int w, uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
-      "[%1, {%2, %3, %4}], [%5];" ::"r"(sptr(dst)),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(sptr(bar))
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%2, %3, %4, %5}], [%6];" ::"r"(sptr(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(sptr(bar))
       : "memory");
 }
 // A contiguous copy; both addresses and the size are multiples of 16 bytes.

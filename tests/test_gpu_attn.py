@@ -572,3 +572,28 @@ def test_shared_in_a_graph(cuda_device, dtype):
     graph.replay()
     want, _, b, _ = ref.shared(q, k, v, pp, prefix, [33, 499, 0], table, 4, 1 / math.sqrt(d), dt)
     ref.check(out, want, b, "replayed")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_prompt_units_of_every_kind_in_any_order(cuda_device, dtype):
+    """Units of one and two query tiles, with one, many and no key tiles, follow
+    each other in every order on a CTA: no barrier may run a phase ahead of who
+    waits on it.  Every launch gives the same bits and none gives up."""
+    torch, ref, nys = _mods()
+    dt = getattr(torch, dtype)
+    g = torch.Generator().manual_seed(11)
+    att = nys.ExactAttention(4, 2, 64, 64, dtype=dt, device=cuda_device)
+    for n, top, more in ((700, 28, 300), (400, 150, 0), (300, 70, 900), (64, 300, 0)):
+        q_lens = torch.randint(0, top, (n,), generator=g).tolist()
+        # Some sequences' first queries see no key at all, some see many.
+        k_lens = [max(0, x - 20) if i % 3 == 0 else x + (more if i % 5 == 0 else 0)
+                  for i, x in enumerate(q_lens)]
+        q, k, v, qo, ko = _inputs(torch, cuda_device, q_lens, k_lens, 4, 2, 64, 64, dt)
+        first = torch.empty_like(q)
+        att.prompt(q, k, v, qo, first, k_off=ko)
+        again = torch.empty_like(q)
+        for _ in range(150):
+            again.zero_()
+            att.prompt(q, k, v, qo, again, k_off=ko)
+            assert torch.equal(first, again)
+        assert att.status() == 0
