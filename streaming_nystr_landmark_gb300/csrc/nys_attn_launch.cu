@@ -100,6 +100,7 @@ Shares shares_of(int64_t n, int kv_heads, int group, int dtype, int64_t tiles) {
 // reads at a fraction of the memory's rate, so long ones are cut: measured on 64
 // requests of 97 to 1025 keys, 8 KV heads, f32: two pieces 45 us, five 36 us.
 int most_own_pieces(int64_t n, int kv_heads) {
+  if (n * kv_heads >= 6 * kSms) return 1;
   return clamp_int(div_up(16 * kSms, n * kv_heads), 1, kMostPieces);
 }
 
