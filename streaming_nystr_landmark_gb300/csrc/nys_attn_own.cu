@@ -242,8 +242,12 @@ __global__ void __launch_bounds__(kThreads, 3) own16_kernel(SharedArgs a, OwnArg
   const int heads = min(kHeads16, a.group - hb * kHeads16);
   int lo, hi;
   let_next_start();
+  // Pieces need nothing of the prefix's launch and leave at once, so that the
+  // rest of this grid gets their places while that one runs; one CTA waits for
+  // it, so that this grid does not end before it.
+  const bool waits = o.pieces == 1 || (blockIdx.x == 0 && blockIdx.y == 0);
   if (!own_range(a, o, b, piece, lo, hi)) {
-    wait_for_previous();
+    if (waits) wait_for_previous();
     return;
   }
   const int32_t* pages = a.table + (int64_t)b * a.width;
@@ -369,8 +373,8 @@ __global__ void __launch_bounds__(kThreads, 3) own16_kernel(SharedArgs a, OwnArg
       }
   }
   cp_wait<0>();
-  wait_for_previous();  // the prefix's pieces, which this kernel ran beside
-  __syncthreads();      // the ring becomes the warps' results
+  if (waits) wait_for_previous();  // the prefix's pieces, which this kernel ran beside
+  __syncthreads();                 // the ring becomes the warps' results
   float* jm = reinterpret_cast<float*>(sm);
   float* jl = jm + kWarps * kHeads16;
   float* ja = jl + kWarps * kHeads16;
@@ -441,8 +445,12 @@ __global__ void __launch_bounds__(kThreads, 3) own32_kernel(SharedArgs a, OwnArg
   const int heads = min(HT, a.group - hb * HT);
   int lo, hi;
   let_next_start();
+  // Pieces need nothing of the prefix's launch and leave at once, so that the
+  // rest of this grid gets their places while that one runs; one CTA waits for
+  // it, so that this grid does not end before it.
+  const bool waits = o.pieces == 1 || (blockIdx.x == 0 && blockIdx.y == 0);
   if (!own_range(a, o, b, piece, lo, hi)) {
-    wait_for_previous();
+    if (waits) wait_for_previous();
     return;
   }
   const int32_t* pages = a.table + (int64_t)b * a.width;
@@ -547,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 3) own32_kernel(SharedArgs a, OwnArg
 #pragma unroll
   for (int off = kRep * KB / 2; off >= kRep; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
   cp_wait<0>();
-  wait_for_previous();
+  if (waits) wait_for_previous();
   __syncthreads();
   float* jm = reinterpret_cast<float*>(sm);
   float* jl = jm + kWarps * HT;
