@@ -193,10 +193,15 @@ __device__ void load_role(const TileArgs& a, const CUtensorMap* mq, const CUtens
         const int my_row = row_of(my_page, my_in);
         if (elect_one()) bar_expect(full, (uint32_t)chunks * 16384u);
         __syncwarp();
-        for (int b = 0; b < boxes; ++b) {
-          const int row = __shfl_sync(0xffffffffu, my_row, b);
-          if (elect_one())
-            copy(dst + b * a.box * 128, m, is_k ? a.d : a.dv, a.box, y, row, full);
+        const int dim = is_k ? a.d : a.dv;
+        const bool whole = dim % 64 == 0;
+        const int each = whole && a.box == kTileM ? 1 : chunks;  // copies of a box
+        for (int x0 = 0; x0 < boxes * each; x0 += 32) {
+          const int x = x0 + lane, b = x / each, c = x - b * each;
+          const int row = __shfl_sync(0xffffffffu, my_row, b & 31);
+          if (x < boxes * each)
+            tma_load4(dst + c * 16384 + b * a.box * 128, m, whole ? 0 : c * 64, y, row, whole ? c : 0,
+                      full);
         }
       }
       __syncwarp();
