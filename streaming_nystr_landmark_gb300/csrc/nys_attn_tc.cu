@@ -318,10 +318,8 @@ __device__ void mma_role(const TileArgs& a, Shared& sh, unsigned char* sm, uint3
 }
 
 // ---- units of work (one warp)
-__device__ void unit_role(const TileArgs& a, Shared& sh, int lane) {
+__device__ void unit_role(const TileArgs& a, Shared& sh, UnitSource& source, int lane) {
   volatile int* ab = &sh.abort;
-  UnitSource source;
-  source.begin(a, lane);
   for (uint32_t nu = 0;; ++nu) {
     if (!bar_wait_warp(&sh.u_empty[nu % kUnitRing], ((nu / kUnitRing) & 1) ^ 1, ab)) return;
     Unit u;
@@ -351,17 +349,29 @@ __device__ void clean_role(const TileArgs& a, Shared& sh, unsigned char* sm, int
       if (!bar_wait_warp(&sh.v_raw[slot], (phase >> slot) & 1, ab)) return;
       phase ^= 1u << slot;
       const int rows = u.nkl - u.kb - j * kTileN;  // keys of the sequence in this tile
-      uint32_t seen = 0;
-      for (int c = 0; c < chunks; ++c) {
-        unsigned char* t = sm + kQBytes + slot * kSlotBytes + c * 16384;
-#pragma unroll 4
-        for (int i = 0; i < 32; ++i) {  // a warp covers four rows of 128 bytes
-          uint4* p = reinterpret_cast<uint4*>(t + i * 512 + lane * 16);
+      unsigned char* tile = sm + kQBytes + slot * kSlotBytes + lane * 16;
+      // Usually all are finite: one operation for two values finds out.
+      uint32_t m0 = 0, m1 = 0, m2 = 0, m3 = 0;
+      for (int c = 0; c < chunks; ++c)
+#pragma unroll 16
+        for (int i = 0; i < 32; ++i) {
+          const uint4 x = *reinterpret_cast<const uint4*>(tile + c * 16384 + i * 512);
+          m0 = Type16<T>::max_abs(m0, x.x);
+          m1 = Type16<T>::max_abs(m1, x.y);
+          m2 = Type16<T>::max_abs(m2, x.z);
+          m3 = Type16<T>::max_abs(m3, x.w);
+        }
+      const uint32_t found = not_finite<T>(m0) | not_finite<T>(m1) | not_finite<T>(m2) | not_finite<T>(m3);
+      if (__any_sync(0xffffffffu, found != 0)) {
+        uint32_t seen = 0;
+#pragma unroll 1
+        for (int i = 0; i < 32 * chunks; ++i) {  // a warp covers four rows of 128 bytes
+          uint4* p = reinterpret_cast<uint4*>(tile + i * 512);
           uint4 x = *p;
           const uint32_t b0 = not_finite<T>(x.x), b1 = not_finite<T>(x.y);
           const uint32_t b2 = not_finite<T>(x.z), b3 = not_finite<T>(x.w);
           if (b0 | b1 | b2 | b3) {
-            if (i * 4 + (lane >> 3) < rows) seen = 1;
+            if ((i & 31) * 4 + (lane >> 3) < rows) seen = 1;
             auto keep = [](uint32_t w, uint32_t b) {
               return w & ~(((b >> 15) & 1u) * 0xFFFFu | (b >> 31) * 0xFFFF0000u);
             };
@@ -372,9 +382,9 @@ __device__ void clean_role(const TileArgs& a, Shared& sh, unsigned char* sm, int
             *p = x;
           }
         }
+        if (__any_sync(0xffffffffu, seen) && lane == 0)
+          *(volatile int*)&sh.unit[nu % kUnitRing].patch = 1;
       }
-      if (__any_sync(0xffffffffu, seen) && lane == 0)
-        *(volatile int*)&sh.unit[nu % kUnitRing].patch = 1;
       proxy_fence();
       __syncwarp();
       if (lane == 0) bar_arrive(&sh.kv_full[slot]);
@@ -668,7 +678,18 @@ attn_tc_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CUten
     bar_init_fence();
     sh.abort = 0;
   }
-  if (warp == 8) tmem_alloc(&sh.tmem, 512);
+  UnitSource source;
+  if (warp == 8) {
+    if (lane == 0) {
+      prefetch_map(&mq);
+      prefetch_map(&mk);
+      prefetch_map(&mv);
+    }
+    __syncwarp();
+    tmem_alloc(&sh.tmem, 512);
+  } else if (warp == 10) {
+    source.begin(a, lane);
+  }
   fence_before();
   __syncthreads();
   fence_after();
@@ -684,7 +705,7 @@ attn_tc_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CUten
     } else if (warp == 9) {
       if (elect_one()) mma_role<T>(a, sh, sm, tmem);
     } else if (warp == 10) {
-      unit_role(a, sh, lane);
+      unit_role(a, sh, source, lane);
     } else {
       clean_role<T>(a, sh, sm, lane);
     }

@@ -80,9 +80,10 @@ struct Shared {
   uint64_t kv_full[kSlots], kv_empty[kSlots];
   uint64_t s_full[2], p_full[2], o_full, o_empty, r_full;  // r: O holds the results
   uint64_t mx_full[4];               // both halves of a quarter's rows have their maxima
-  uint64_t u_full[kUnitRing], u_empty[kUnitRing];
+  uint64_t u_full[kUnitRing], u_empty[kUnitRing], patch_full[kUnitRing];
   uint64_t drain;
   Unit unit[kUnitRing];
+  int patch[kUnitRing];  // results need values that are not finite added
   alignas(16) TileExps exps[4];      // of tile & 3
   int8_t q_exp[4][kTileM];           // eq, [unit & 3][row]: the query warps run up to three units ahead
   float mx[2][2][kTileM];            // halves' maxima [exchange & 1][half][row], also of l
@@ -113,6 +114,7 @@ __device__ void load_role(const TileArgs& a, Shared& sh, unsigned char* sm) {
     const int64_t im = (int64_t)sh.unit[nu % kUnitRing].tile * a.kv_heads + sh.unit[nu % kUnitRing].kvh;
     bar_arrive(&sh.u_empty[nu % kUnitRing]);
     if (!valid) break;
+    if (nu == 0) wait_for_previous();  // the images
     for (int e = 0; e < 2 * nt; ++e) {
       bool is_k;
       int j;
@@ -235,9 +237,11 @@ __device__ void query_role(const TileArgs& a, Shared& sh, unsigned char* turn, u
   }
   uint32_t n_q = 0, n_r = 0;
 
-  // Results of the unit in ring place `at`.
-  auto results = [&](uint32_t at) {
+  // Results of unit nu.
+  auto results = [&](uint32_t nu) {
+    const uint32_t at = nu % kUnitRing;
     const Unit& u = sh.unit[at];
+    if (!bar_wait_warp(&sh.patch_full[at], (nu / kUnitRing) & 1, ab)) return false;
     const int64_t part_row = (int64_t)u.slot * kTileM + warp * 32;
     if (u.nt > 0) {
       if (!bar_wait_warp(&sh.r_full, n_r & 1, ab)) return false;
@@ -280,7 +284,7 @@ __device__ void query_role(const TileArgs& a, Shared& sh, unsigned char* turn, u
       }
     }
     fence_before();
-    if (u.patch) {
+    if (sh.patch[at]) {
       __syncwarp();  // the row's results are there
       const int row = warp * 32 + lane, p = row / a.group, h = row - p * a.group + u.kvh * a.group;
       const int lim = min(a.causal ? u.lim + p : u.lim, u.nkl) - u.kb;
@@ -371,7 +375,7 @@ __device__ void query_role(const TileArgs& a, Shared& sh, unsigned char* turn, u
       __syncwarp();
       if (lane == 0) bar_arrive(&sh.q_full);
     }
-    if (nu > 0 && !results((nu - 1) % kUnitRing)) return;
+    if (nu > 0 && !results(nu - 1)) return;
     if (!valid) return;
   }
 }
@@ -540,27 +544,31 @@ __device__ void mma_role(const TileArgs& a, Shared& sh, unsigned char* sm, uint3
   bar_wait(&sh.drain, 0, &none);
 }
 
-__device__ void unit_role(const TileArgs& a, Shared& sh, int lane) {
+__device__ void unit_role(const TileArgs& a, Shared& sh, UnitSource& source, int lane) {
   volatile int* ab = &sh.abort;
-  UnitSource source;
-  source.begin(a, lane);
   for (uint32_t nu = 0;; ++nu) {
     if (!bar_wait_warp(&sh.u_empty[nu % kUnitRing], ((nu / kUnitRing) & 1) ^ 1, ab)) return;
     Unit u;
     source.next(a, nu, lane, u);
-    if (u.valid) {  // does a tile hold values that are not finite?
-      uint64_t odd = 0;
-#pragma unroll 4
-      for (int i = lane; i < u.nt; i += 32)
-        odd |= reinterpret_cast<const uint64_t*>(a.odd)[(int64_t)(u.tile + i) * a.kv_heads + u.kvh];
-      u.patch = __any_sync(0xffffffffu, odd != 0);
-    }
     if (lane == 0) {
       sh.unit[nu % kUnitRing] = u;
       bar_arrive(&sh.u_full[nu % kUnitRing]);
     }
     __syncwarp();
     if (!u.valid) return;
+    // (The flags, and the counter from here on, are the split's.)
+    if (nu == 0) wait_for_previous();
+    // Does a tile hold values that are not finite?  Nobody asks before the
+    // results, so nobody waits for the answer's way from memory.
+    uint64_t odd = 0;
+#pragma unroll 4
+    for (int i = lane; i < u.nt; i += 32)
+      odd |= reinterpret_cast<const uint64_t*>(a.odd)[(int64_t)(u.tile + i) * a.kv_heads + u.kvh];
+    odd = __any_sync(0xffffffffu, odd != 0);
+    if (lane == 0) {
+      sh.patch[nu % kUnitRing] = odd != 0;
+      bar_arrive(&sh.patch_full[nu % kUnitRing]);
+    }
   }
 }
 
@@ -780,19 +788,21 @@ attn_tc32_kernel(const __grid_constant__ TileArgs a) {
     for (int i = 0; i < 4; ++i) bar_init(&sh.mx_full[i], 2);
     for (int i = 0; i < kUnitRing; ++i) {
       bar_init(&sh.u_full[i], 1);
+      bar_init(&sh.patch_full[i], 1);
       bar_init(&sh.u_empty[i], 8 + 4 + 2);  // softmax, query, product, copying warps
     }
     bar_init(&sh.drain, 1);
     bar_init_fence();
     sh.abort = 0;
   }
+  UnitSource source;
   if (warp == 12) tmem_alloc(&sh.tmem, 512);
+  else if (warp == 13) source.begin(a, lane);
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = sh.tmem;
   let_next_start();
-  wait_for_previous();  // the images
   if (warp < 8) {
     more_regs<kRegsRow>();
     row_role(a, sh, tmem, tid & 127, warp >> 2, lane);
@@ -804,7 +814,7 @@ attn_tc32_kernel(const __grid_constant__ TileArgs a) {
     if (warp == 12) {
       if (elect_one()) mma_role(a, sh, sm, tmem);
     } else if (warp == 13) {
-      unit_role(a, sh, lane);
+      unit_role(a, sh, source, lane);
     } else if (warp == 14) {
       if (elect_one()) load_role(a, sh, sm);
     }
