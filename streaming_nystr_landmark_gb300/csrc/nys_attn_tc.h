@@ -165,14 +165,17 @@ __device__ __forceinline__ void add_unusual(T* out, const V* v, int c0, int c1) 
   }
 }
 
-// Walks the launch's units in order; one warp.  Within a sequence the query
-// tiles come last position first, because under the causal mask those are the
-// longest; KV heads of one position lie next to each other.
+// Walks the launch's units in order; one warp.  32 sequences at a time, one a
+// lane; among those the query tiles of the last positions of the longest prompts
+// come first, because under the causal mask those are the longest, and short work
+// fills the gaps that long work leaves.  Level l is the l-th unit of each
+// sequence that has one; a level's units lie next to each other, each sequence's
+// KV heads together.
 struct UnitWalk {
-  int32_t before = 0;  // units of the sequences before the window
+  int32_t before = 0;  // units of the windows and levels before
   int s0 = 0;          // the window's first sequence, 32 of them
+  int level = 0;
   int q0, nq, k0, nk, pairs;
-  int32_t count, upto;  // this lane's sequence's units, and the inclusive sum
 
   __device__ __forceinline__ void load(const TileArgs& a, int lane) {
     const int i = s0 + lane;
@@ -184,13 +187,7 @@ struct UnitWalk {
       if (bad) attn_report(a.status, NYS_ATTN_BAD_OFFSETS);
     }
     pairs = (nq + a.per * a.tp - 1) / (a.per * a.tp);
-    count = pairs * a.kv_heads;
-    upto = count;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int32_t y = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += y;
-    }
+    level = __reduce_max_sync(0xffffffffu, pairs) - 1;
   }
 
   // All units of the launch.
@@ -199,7 +196,7 @@ struct UnitWalk {
     int32_t sum = 0;
     for (w.s0 = 0; w.s0 < a.n; w.s0 += 32) {
       w.load(a, lane);
-      sum += __shfl_sync(0xffffffffu, w.upto, 31);
+      sum += __reduce_add_sync(0xffffffffu, w.pairs) * a.kv_heads;
     }
     return sum;
   }
@@ -209,23 +206,25 @@ struct UnitWalk {
   __device__ __forceinline__ void get(const TileArgs& a, int32_t w, int lane, Unit& u) {
     u.valid = 0;
     u.patch = 0;
+    uint32_t have;  // sequences of this level
     for (;;) {
-      const int32_t all = __shfl_sync(0xffffffffu, upto, 31);
+      have = __ballot_sync(0xffffffffu, pairs > level);
+      const int32_t all = level >= 0 ? __popc(have) * a.kv_heads : 0;
       if (w < before + all) break;
       before += all;
-      s0 += 32;
-      if (s0 >= a.n) return;
-      load(a, lane);
+      if (--level < 0) {
+        s0 += 32;
+        if (s0 >= a.n) return;
+        load(a, lane);
+      }
     }
-    const int src = __ffs(__ballot_sync(0xffffffffu, before + upto > w)) - 1;
+    const int32_t r = w - before;
+    const int src = __fns(have, 0, r / a.kv_heads + 1);
     const int sq0 = __shfl_sync(0xffffffffu, q0, src), snq = __shfl_sync(0xffffffffu, nq, src);
     const int sk0 = __shfl_sync(0xffffffffu, k0, src), snk = __shfl_sync(0xffffffffu, nk, src);
-    const int spairs = __shfl_sync(0xffffffffu, pairs, src);
-    const int32_t r = w - before - __shfl_sync(0xffffffffu, upto - count, src);
     u.slot = -1;
     u.kvh = r % a.kv_heads;
-    const int pair = spairs - 1 - r / a.kv_heads;
-    const int p0 = pair * a.per * a.tp;
+    const int p0 = level * a.per * a.tp;
     const int left = snq - p0;
     u.np0 = min(left, a.tp);
     u.np1 = a.per == 2 ? min(max(left - a.tp, 0), a.tp) : 0;
