@@ -1,10 +1,10 @@
 // Exact attention on the tensor cores, f32.
 //
 // The formulas are those of nys_attn_tc.cu.  An f32 operand x is taken as a
-// pair of fp16 pieces of x' = x 2^-e: hi = x' cut to 11 bits, lo = x' - hi
-// rounded to 11 bits, so that x' = hi + lo to 2^-22; a product takes three
-// tcgen05 products, lo hi + hi lo + hi hi (the dropped lo lo is below 2^-20 of
-// |x y| at worst, 2^-23 in the mean), summed in f32 in tensor memory, small
+// pair of fp16 pieces of x' = x 2^-e: hi = x' to 11 bits, lo = x' - hi rounded to
+// 11 bits, so that x' = hi + lo to 2^-22; a product takes three tcgen05 products,
+// lo hi + hi lo + hi hi (the dropped lo lo is below 2^-21 of |x y| at worst, about
+// 2^-24 in the mean and of either sign), summed in f32 in tensor memory, small
 // ones first.  The exponent e is common to 16 rows (those that one warp
 // converts) and puts their largest value at 2^13, where fp16 keeps 22 bits of
 // everything down to 2^-27 of it.
@@ -176,9 +176,14 @@ __device__ __forceinline__ void split4(float4 x, uint64_t scale2, uint32_t (&hi)
                                        uint32_t (&lo)[2]) {
   const uint64_t ya = mul2(pair(x.x, x.y), scale2), yb = mul2(pair(x.z, x.w), scale2);
   const uint64_t minus2 = pair(-1.f, -1.f);
+  // hi is the value with about half a step of hi added, then cut (4/3 2^-12 of the
+  // value is 0.33 to 0.67 steps): lo has either sign, so that the dropped lo lo
+  // does not add up.  Against plain cutting the error of 64 prompts of 256 falls
+  // from 4.6e-7 to 3.0e-7, for 1% of the time.
+  const uint64_t half = pair(3.2552083e-4f, 3.2552083e-4f);
   float y[4], h[4], l[4];
-  unpair(ya, y[0], y[1]);
-  unpair(yb, y[2], y[3]);
+  unpair(fma2(ya, half, ya), y[0], y[1]);
+  unpair(fma2(yb, half, yb), y[2], y[3]);
 #pragma unroll
   for (int i = 0; i < 4; ++i) h[i] = cut11(y[i]);
   unpair(fma2(pair(h[0], h[1]), minus2, ya), l[0], l[1]);
