@@ -167,7 +167,7 @@ int nys_kv_plan(int64_t n, int32_t page, const int32_t* cached, const int32_t* f
                 int64_t total, int32_t* q_off, int32_t* lens, int64_t* slots,
                 int32_t* positions, int32_t* taken, int32_t* status, void* stream) {
   if (n < 0 || n >= INT32_MAX || page < 1 || page > (1 << 20) || n_free < 0 ||
-      n_free > INT32_MAX || width < 0 || total < 0 || total > INT32_MAX)
+      n_free > INT32_MAX || width < 0 || total < 0 || total >= INT32_MAX)
     return NYS_E_INVAL;
   if (!q_off || !taken) return NYS_E_INVAL;
   if (n > 0 && (!cached || !fresh || !lens || (width > 0 && !table))) return NYS_E_INVAL;

@@ -681,7 +681,9 @@ class ExactAttention(_Status):
     """Exact grouped-query attention of one layer's geometry: packed causal
     prompts (``prompt``) and one token over a shared prefix and paged own keys
     (``shared``).  The workspace grows on demand and is kept, so calls on one
-    object must be ordered (one stream, or events)."""
+    object must be ordered (one stream, or events).  One that a CUDA graph has
+    captured is kept for the graph's replays, which count as calls, even when a
+    larger one takes its place."""
 
     def __init__(self, heads, kv_heads, d, dv, dtype=None, scale=None, device="cuda"):
         import torch
@@ -696,17 +698,28 @@ class ExactAttention(_Status):
         self._work_ptr = None
         self._work_bytes = 0
         self._sizes = None
+        self._captured = False   # a graph may hold the workspace's address
+        self._held = []          # workspaces that were outgrown and that one holds
         nys_attn_workspace_bytes(self.cfg, 0, 0)   # refuses a bad geometry here
 
     def _workspace(self, n, rows, keys):
         """Makes the workspace large enough for a call of these sizes."""
+        capturing = self.torch.cuda.is_current_stream_capturing()
         if (n, rows, keys) == self._sizes:
+            self._captured |= capturing
             return
         need = nys_attn_workspace_bytes(self.cfg, n, rows, keys)
         self._sizes = (n, rows, keys)
         if need > self._work_bytes:
+            if self._captured:
+                self._held.append(self._work)
+            elif self._work is not None:
+                # Work that uses it may be queued on a stream other than its own.
+                self._work.record_stream(self.torch.cuda.current_stream(self.device))
+            self._captured = False
             self._work = self.torch.empty(need, dtype=self.torch.uint8, device=self.device)
             self._work_ptr, self._work_bytes = self._work.data_ptr(), need
+        self._captured |= capturing
 
     def prompt(self, q, k, v, q_off, out, k_off=None, lse=None):
         """Packed causal attention (nys_attn_prompt): q [rows][heads][d], k and

@@ -415,6 +415,31 @@ def test_plan_without_pages_or_columns(cuda_device):
     assert p3.status() == nys.NYS_PLAN_BAD_LENGTH
 
 
+@pytest.mark.parametrize("fresh", [
+    [2**31 - 1, 1, 5],           # the sum passes 31 bits
+    [2**31 - 1, 2**31 - 1, 8],   # and 32 bits, to 6 = the slots there are
+    [3, 2**31 - 1, 2**31 - 1, 5],
+])
+def test_plan_lengths_that_sum_past_32_bits(cuda_device, fresh):
+    """Their sum is held, no other memory is reached, and the call is reported."""
+    torch, _, nys = _mods()
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)
+    n, width, total = len(fresh), 4, 6
+    plan = nys.PagePlan(n, width, total, 4, device=cuda_device)
+    whole = torch.full((n + 2, width), -1, dtype=torch.int32, device=cuda_device)
+    plan.update(i32([0] * n), i32(fresh), i32([9, 5, 7]), whole[1:n + 1])
+    cell, want, row = iter([9, 5, 7]), [[-1] * width for _ in range(n + 2)], []
+    for t in range(total):
+        i = max(x for x in range(n) if sum(fresh[:x]) <= t)
+        pos = t - sum(fresh[:i])
+        if pos % 4 == 0:
+            want[i + 1][pos // 4] = next(cell)
+        row.append(want[i + 1][pos // 4] * 4 + pos % 4)
+    assert whole.tolist() == want and plan.slots.tolist() == row
+    assert plan.q_off.tolist() == [min(sum(fresh[:x]), total + 1) for x in range(n + 1)]
+    assert plan.status() & nys.NYS_PLAN_BAD_LENGTH and plan.taken.item() == 3
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("tokens,kv,d,dv", [(1, 1, 64, 64), (64, 8, 128, 128), (333, 2, 20, 12),
                                             (50, 3, 4, 8), (5000, 4, 128, 64)])
@@ -572,6 +597,45 @@ def test_shared_in_a_graph(cuda_device, dtype):
     graph.replay()
     want, _, b, _ = ref.shared(q, k, v, pp, prefix, [33, 499, 0], table, 4, 1 / math.sqrt(d), dt)
     ref.check(out, want, b, "replayed")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_graph_keeps_its_workspace(cuda_device, dtype):
+    """A larger call after a capture takes a new workspace; the graph's stays."""
+    torch, _, nys = _mods()
+    dt = getattr(torch, dtype)
+    att = nys.ExactAttention(8, 2, 64, 64, dtype=dt, device=cuda_device)
+    torch.manual_seed(5)
+
+    def args(lens):
+        off = torch.tensor([sum(lens[:i]) for i in range(len(lens) + 1)], dtype=torch.int32,
+                           device=cuda_device)
+        rows = sum(lens)
+        make = lambda h: torch.randn((rows, h, 64), device=cuda_device).to(dt)
+        return make(8), make(2), make(2), off, torch.zeros((rows, 8, 64), device=cuda_device, dtype=dt)
+
+    # f32 holds its keys' pieces there; 16-bit types a counter, and for few long
+    # prompts pieces of results.
+    small, large = args([2000] if dtype == "float32" else [1000] * 20), args([6000, 100])
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        att.prompt(*small)
+        want = small[4].clone()
+        side.synchronize()
+        with torch.cuda.graph(graph, stream=side):
+            att.prompt(*small)
+        before = att._work_ptr
+        att.prompt(*large)
+        assert att._work_ptr != before
+        # Had the graph's workspace been freed, these would lie in it.
+        others = [torch.full((1 << 20,), 7, dtype=torch.uint8, device=cuda_device) for _ in range(64)]
+        small[4].zero_()
+        graph.replay()
+        side.synchronize()
+    assert torch.equal(small[4], want)
+    assert all(bool((x == 7).all()) for x in others)
+    assert att.status() == 0
 
 
 @pytest.mark.parametrize("dtype", TYPES)
