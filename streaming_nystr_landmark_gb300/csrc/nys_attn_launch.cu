@@ -13,7 +13,7 @@ using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, 
                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// The driver's encoder, looked up once (the library links no libcuda).
+// CUDA's encoder of tensor maps, looked up once (the library links no libcuda).
 EncodeTiled encoder() {
   static const EncodeTiled fn = [] {
     void* p = nullptr;
@@ -97,18 +97,17 @@ Shares shares_of(int64_t n, int kv_heads, int group, int dtype, int64_t tiles) {
   return s;
 }
 // Pieces of a request's own keys at most.  Requests differ in length and one CTA
-// reads at a fraction of the memory's rate, so long ones are cut: measured on 64
-// requests of 97 to 1025 keys, 8 KV heads, f32: two pieces 45 us, five 36 us.
+// reads at a fraction of the memory's rate, so long ones are cut: 64 requests of
+// 97 to 1025 keys, 8 KV heads, f32, whole call: two pieces 45 us, five 39 us.
+// With six CTAs a SM's worth of requests the lengths even out by themselves, and
+// whole requests need no join: 256 requests of 1 to 517 keys, 4 KV heads, over a
+// prefix of 32,768, bf16, 147 us whole and 155 us cut.
 int most_own_pieces(int64_t n, int kv_heads) {
   if (n * kv_heads >= 6 * kSms) return 1;
   return clamp_int(div_up(16 * kSms, n * kv_heads), 1, kMostPieces);
 }
 
 int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
-
-}  // namespace
-
-namespace {
 
 // The f32 images' part of a workspace: K, V, exponents, flags.
 struct Images {
@@ -132,10 +131,6 @@ void place_images(TileArgs& a, void* workspace, int64_t n, int64_t keys) {
   a.odd = w + im.odd;
 }
 
-}  // namespace
-
-namespace {
-
 constexpr size_t kCounterBytes = 256;
 size_t slot_bytes(int dtype, int dv) {
   return (size_t)query_tiles(dtype) * kTileM * ((size_t)dv + 1) * 4;
@@ -146,9 +141,9 @@ int64_t prompt_units(int64_t n, int64_t rows, int kv_heads, int group, int dtype
   return (rows / (query_tiles(dtype) * (kTileM / group)) + n) * kv_heads;
 }
 // Whether the last round's units are cut.  It pays where rounds are few and
-// long: measured on 2 prompts' last 1,021 and 1,500 tokens over 5,003 earlier
-// ones, f32, 320 units of 45 tiles on 152 CTAs, 303 us whole and 217 us cut;
-// the look through the sequences and the join cost about 6 us.
+// long: 2 prompts' last 1,021 and 1,500 tokens over 5,003 earlier ones, f32, 320
+// units of 45 tiles on 152 CTAs, take 303 us whole and 277 us cut (whole calls,
+// the join's 11 us among them).
 bool cut_tail(int64_t n, int64_t rows, int64_t keys, int kv_heads, int group, int dtype) {
   const int64_t units = prompt_units(n, rows, kv_heads, group, dtype);
   return n <= 128 && keys >= 1024 * n && units <= 8 * kSms;

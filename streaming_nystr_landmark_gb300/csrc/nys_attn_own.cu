@@ -8,8 +8,10 @@
 // the group, and there is little arithmetic a byte.  A CTA of four warps
 // takes one (request, KV head, piece of its keys); each warp streams tiles of
 // its own through a private ring in shared memory with cp.async, no barrier
-// between warps until their results are joined, so that two CTAs a SM keep
-// ~130 KB of reads in flight.  Keys past the length and pages outside the pool
+// between warps until their results are joined; three CTAs a SM keep the reads
+// in flight.  64 requests of 97 to 1025 keys over a prefix of 2,000 (8 KV heads of
+// 128, f32): 42 us for 208 MB from memory, 64% of its peak, and 60 us for the whole
+// call (floor 33 us).  Keys past the length and pages outside the pool
 // are filled with zeros and never read from memory.
 //
 // bf16 / fp16: tiles of 16 keys, mma.sync m16n8k16 with the group's heads as

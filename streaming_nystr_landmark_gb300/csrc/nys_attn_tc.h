@@ -96,7 +96,7 @@ struct Unit {
   int32_t nkl;      // keys the piece ends before
   int32_t slot;     // where a piece's results go; -1: a whole unit, to `out`
   int32_t edge;     // first key tile in which some row does not see some key
-  int32_t patch;    // set where the epilogue has to add values that are not finite
+  int32_t patch;    // (16-bit) set where the epilogue has to add values that are not finite
   int32_t tile;     // number of the piece's first key tile among all (f32)
 };
 
