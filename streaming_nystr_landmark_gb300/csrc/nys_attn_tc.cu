@@ -24,7 +24,7 @@
 // the measured dense rate in a burst and 88% of the sustained one), where S = Q K^T,
 // with A in shared memory, takes 107 clocks an instruction and P V, with A in
 // tensor memory, 74.  Short prompts are bound by each unit's chain of loads,
-// products and softmax (16 ragged prompts: 67 us).  Two query tiles at once, one
+// products and softmax (33 prompts of 1 to 2,047 tokens, 16 heads on 8: 67 us).  Two query tiles at once, one
 // softmax hidden behind the other's products, is why a tile is 128 rows and not
 // 256: tensor memory holds no third S.
 //

@@ -62,17 +62,21 @@ class ExactLayer:
     def _plan(self, fresh):
         """Pages and slots for fresh[i] more tokens of request i."""
         torch, total = self.torch, sum(fresh)
-        if total not in self._plans:
-            self._plans = {total: nys.PagePlan(self.requests, self.width, total, self.page,
-                                               device=self.device)}
-        plan = self._plans[total]
+        if len(fresh) != self.requests or min(fresh) < 0:
+            raise ValueError(f"need {self.requests} lengths, none negative")
         pages = lambda n: -(-n // self.page)
         need = sum(pages(a + b) - pages(a) for a, b in zip(self.lengths, fresh))
         if self.used + need > self.free.shape[0]:
             raise ValueError(f"{need} more pages wanted, {self.free.shape[0] - self.used} left")
         if max(a + b for a, b in zip(self.lengths, fresh)) > self.width * self.page:
             raise ValueError("a request would outgrow max_len")
-        grow = torch.tensor(fresh, dtype=torch.int32, device=self.device)
+        if total not in self._plans:
+            self._plans = {total: nys.PagePlan(self.requests, self.width, total, self.page,
+                                               device=self.device)}
+        plan = self._plans[total]
+        # From pinned memory: a copy that the host does not wait for.
+        grow = torch.tensor(fresh, dtype=torch.int32, pin_memory=True).to(self.device,
+                                                                         non_blocking=True)
         plan.update(self.lens, grow, self.free[self.used:], self.table)
         self.used += need
         self.lengths = [a + b for a, b in zip(self.lengths, fresh)]
@@ -85,7 +89,10 @@ class ExactLayer:
         if self.used:
             raise ValueError("the prefix comes before the first request")
         torch, n = self.torch, k.shape[0]
-        self.used = -(-n // self.page)
+        need = -(-n // self.page)
+        if need > self.free.shape[0]:
+            raise ValueError(f"{need} pages wanted, {self.free.shape[0]} there")
+        self.used = need
         self.prefix_pages = self.free[:self.used].clone()
         self.prefix_len = n
         at = torch.arange(n, device=self.device)
@@ -99,6 +106,8 @@ class ExactLayer:
         torch, att = self.torch, self.attention
         if any(self.lengths):
             raise ValueError("admit() takes requests from their first token")
+        if not q.shape[0] == k.shape[0] == v.shape[0] == sum(lengths):
+            raise ValueError("q, k and v must have as many rows as the lengths' sum")
         plan = self._plan(list(lengths))
         self.cache.write(k, v, plan.slots)
         rows = q.shape[0]
@@ -118,6 +127,8 @@ class ExactLayer:
         """One new token for every request: q [requests][heads][d], k and v
         [requests][kv_heads][d|dv].  Returns [requests][heads][dv]."""
         att = self.attention
+        if not q.shape[0] == k.shape[0] == v.shape[0] == self.requests:
+            raise ValueError("q, k and v must have one row a request")
         plan = self._plan([1] * self.requests)
         self.cache.write(k, v, plan.slots)
         out = self.torch.empty((self.requests, att.heads, att.dv), dtype=att.dtype,

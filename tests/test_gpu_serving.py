@@ -63,6 +63,27 @@ def test_layer_refuses_what_does_not_fit(cuda_device):
         layer.set_prefix(z(2, 2), z(2, 2))
 
 
+def test_layer_refuses_rows_and_lengths_that_differ(cuda_device):
+    import torch
+    from streaming_nystr_landmark_gb300 import serving
+    layer = serving.ExactLayer(4, 2, 64, 64, 2, 8, 16, 64, device=cuda_device)
+    z = lambda n, h: torch.zeros(n, h, 64, device=cuda_device)
+    with pytest.raises(ValueError, match="pages wanted"):
+        layer.set_prefix(z(130, 2), z(130, 2))      # 9 pages of a pool of 8
+    with pytest.raises(ValueError, match="lengths"):
+        layer.admit(z(5, 4), z(5, 2), z(5, 2), [5])
+    with pytest.raises(ValueError, match="lengths"):
+        layer.admit(z(5, 4), z(5, 2), z(5, 2), [6, -1])
+    with pytest.raises(ValueError, match="rows"):
+        layer.admit(z(5, 4), z(5, 2), z(5, 2), [5, 1])
+    with pytest.raises(ValueError, match="one row"):
+        layer.decode(z(1, 4), z(1, 2), z(1, 2))
+    # Nothing was taken or counted by any of them.
+    assert layer.used == 0 and layer.lengths == [0, 0] and layer.prefix_len == 0
+    layer.admit(z(6, 4), z(6, 2), z(6, 2), [5, 1])
+    assert layer.lengths == [5, 1] and layer.lens.tolist() == [5, 1]
+
+
 def test_landmark_states_of_the_same_prompts(cuda_device):
     """seal_prompts seals exactly what nys_seal seals group by group."""
     import torch
