@@ -96,15 +96,34 @@ Shares shares_of(int64_t n, int kv_heads, int group, int dtype, int64_t tiles) {
   s.ctas = (int32_t)ctas;
   return s;
 }
+// CTAs of the own keys' kernel for one piece a request: each has up to 8 (f32) or
+// 16 heads of a group.
+int64_t own_ctas(int64_t n, int kv_heads, int group, int dtype) {
+  return n * kv_heads * div_up(group, dtype == NYS_F32 ? 8 : 16);
+}
 // Pieces of a request's own keys at most.  Requests differ in length and one CTA
 // reads at a fraction of the memory's rate, so long ones are cut: 64 requests of
 // 97 to 1025 keys, 8 KV heads, f32, whole call: two pieces 45 us, five 39 us.
 // With six CTAs a SM's worth of requests the lengths even out by themselves, and
 // whole requests need no join: 256 requests of 1 to 517 keys, 4 KV heads, over a
 // prefix of 32,768, bf16, 147 us whole and 155 us cut.
-int most_own_pieces(int64_t n, int kv_heads) {
-  if (n * kv_heads >= 6 * kSms) return 1;
-  return clamp_int(div_up(16 * kSms, n * kv_heads), 1, kMostPieces);
+int most_own_pieces(int64_t ctas) {
+  if (ctas >= 6 * kSms) return 1;
+  return clamp_int(div_up(16 * kSms, ctas), 1, kMostPieces);
+}
+// Keys of a piece at least.  With few CTAs a piece's own length is the call's time
+// (one request of 346 keys, 8 KV heads, f32: 128 keys 8.6 us, 192 10.7 us; four of
+// 500 to 700: 10.7 and 11.6 us); with more, the pieces that are joined are (40
+// requests of 500 to 700: 256 keys 38 us, 192 43 us).
+int least_own_keys(int64_t ctas) { return ctas <= 48 ? 128 : 256; }
+// Whether each request reads the prefix's keys for itself, in front of its own: no
+// tile kernel, no split, one join less.  It pays until the rows read again weigh
+// more (few requests or a short prefix): 4 requests of 3 to 45 keys over 301, bf16,
+// 8 KV heads, 8.2 us against 14.4 us; f32 8.8 against 20.6 us; 64 over 301, 4 KV
+// heads (77,000 rows), bf16 20.6 against 26.8 us, f32 29.0 against 25.5 us; 16 over
+// 1,000, 8 KV heads (128,000 rows), bf16 21.5 against 14.0 us.
+bool read_with_own(int64_t ctas, int64_t prefix, int dtype) {
+  return prefix > 0 && ctas * prefix <= (dtype == NYS_F32 ? 60000 : 80000);
 }
 
 int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
@@ -171,7 +190,8 @@ size_t shared_workspace(const nys_attn_config& c, int64_t n, int64_t keys) {
   if (keys > 0)
     all += shares_of(n, c.kv_heads, c.heads / c.kv_heads, c.dtype, 0).slots() *
            slot_bytes(c.dtype, c.dv);
-  return all + (size_t)most_own_pieces(n, c.kv_heads) * n * c.heads * ((size_t)c.dv + 1) * 4;
+  const int64_t ctas = own_ctas(n, c.kv_heads, c.heads / c.kv_heads, c.dtype);
+  return all + (size_t)most_own_pieces(ctas) * n * c.heads * ((size_t)c.dv + 1) * 4;
 }
 
 bool shared_tiled_fits(const SharedArgs& a) {
@@ -179,21 +199,25 @@ bool shared_tiled_fits(const SharedArgs& a) {
   if (a.d > 128 || a.dv > 128 || a.d % unit || a.dv % unit || a.n_pages == 0) return false;
   if (reinterpret_cast<uintptr_t>(a.k) % 16 || reinterpret_cast<uintptr_t>(a.v) % 16) return false;
   if (a.n_pages * a.page > (1 << 30) || a.n_pages * a.page * a.kv_heads > INT32_MAX) return false;
+  if ((int64_t)a.width * a.page > (1 << 30)) return false;
   if (!tileable(a.q, a.n, a.heads, elem, false)) return false;
-  if (a.prefix_len > 0 && a.dtype != NYS_F32 && a.page % 8) return false;
+  if (a.prefix_len > 0 && a.dtype != NYS_F32 && a.page % 8 &&
+      !read_with_own(own_ctas(a.n, a.kv_heads, a.group, a.dtype), a.prefix_len, a.dtype))
+    return false;
   return true;
 }
 
 cudaError_t launch_shared_tiled(const SharedArgs& s, void* workspace, cudaStream_t stream) {
   const int64_t row = (int64_t)s.n * s.heads;
   OwnArgs o{};
-  if (s.prefix_len > 0)
+  const int64_t ctas = own_ctas(s.n, s.kv_heads, s.group, s.dtype);
+  if (read_with_own(ctas, s.prefix_len, s.dtype)) o.lead = s.prefix_len;
+  else if (s.prefix_len > 0)
     o.shares = shares_of(s.n, s.kv_heads, s.group, s.dtype, div_up(s.prefix_len, kTileN));
-  const int64_t cap = (int64_t)s.width * s.page;
-  o.pieces = clamp_int(div_up(cap, 192), 1, most_own_pieces(s.n, s.kv_heads));
-  o.keys = (int32_t)(div_up(div_up(cap, o.pieces), 64) * 64);
-  if (o.keys < 64) o.keys = 64;
-  const size_t images = s.dtype == NYS_F32 && s.prefix_len > 0
+  const int64_t cap = o.lead + (int64_t)s.width * s.page;
+  o.keys = least_own_keys(ctas);
+  o.pieces = clamp_int(div_up(cap, o.keys), 1, most_own_pieces(ctas));
+  const size_t images = s.dtype == NYS_F32 && o.shares.units > 0
                             ? images_of(s.kv_heads, s.d, s.dv, 1, s.prefix_len).end
                             : 0;
   // The prefix's pieces, the own pieces, then both's sums.

@@ -50,12 +50,20 @@ __device__ __forceinline__ int own_len(const SharedArgs& a, int b, bool report) 
   if (report && (len < 0 || len > cap)) attn_report(a.status, NYS_ATTN_BAD_LENGTH);
   return len < 0 ? 0 : (len > cap ? cap : len);
 }
-// The piece of its keys that this CTA reads, [lo, hi); false: there is none.
+// Keys of a piece of a request's `len`: even pieces, of short requests fewer, and
+// more than 16 only of 256 keys and more (the join's time).
+__device__ __forceinline__ int piece_keys(const OwnArgs& o, int len) {
+  const int some = min(256, len / 16), even = (len + o.pieces - 1) / o.pieces;
+  return (max(max(some, even), o.keys) + 31) & ~31;
+}
+// The piece of its keys (the prefix's first, where they are read with them) that
+// this CTA reads, [lo, hi); false: there is none.
 __device__ __forceinline__ bool own_range(const SharedArgs& a, const OwnArgs& o, int b, int piece,
                                           int& lo, int& hi) {
-  const int len = own_len(a, b, true);
-  lo = piece * o.keys;
-  hi = min(len, lo + o.keys);
+  const int len = o.lead + own_len(a, b, true);
+  const int keys = piece_keys(o, len);
+  lo = piece * keys;
+  hi = min(len, lo + keys);
   return o.pieces == 1 || lo < hi;
 }
 
@@ -63,9 +71,11 @@ constexpr uint32_t kNoRow = 0xffffffffu;
 
 // Row (slot x KV heads + KV head) of key j < hi of a request in the pool, kNoRow
 // past the end or where its page is not in the pool.
-__device__ __forceinline__ uint32_t own_row(const SharedArgs& a, const int32_t* pages, int j,
-                                            int hi, int kvh) {
+__device__ __forceinline__ uint32_t own_row(const SharedArgs& a, const OwnArgs& o,
+                                            const int32_t* pages, int j, int hi, int kvh) {
   if (j >= hi) return kNoRow;
+  if (j < o.lead) pages = a.prefix_pages;
+  else j -= o.lead;
   const int pi = j / a.page;
   const int32_t pg = pages[pi];
   if (pg < 0 || pg >= a.n_pages) {
@@ -267,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 3) own16_kernel(SharedArgs a, OwnArg
   const int mine = 2 * (blocks32 > warp ? (blocks32 - warp + kWarps - 1) / kWarps : 0);
   auto key_of = [&](int t) { return lo + ((t >> 1) * kWarps + warp) * 32 + (t & 1) * kKeys16; };
   RowAhead row;
-  row.next = own_row(a, pages, key_of(0) + lane, hi, kvh);
+  row.next = own_row(a, o, pages, key_of(0) + lane, hi, kvh);
   const unsigned char* kb = (const unsigned char*)a.k + (lane & 15) * 16;
   const unsigned char* vb = (const unsigned char*)a.v + (lane & 15) * 16;
   const bool kcol = (lane & 15) < dc, vcol = (lane & 15) < vc;
@@ -275,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 3) own16_kernel(SharedArgs a, OwnArg
     if (t < mine) {
       if (!(t & 1)) {
         row.now = row.next;
-        row.next = own_row(a, pages, key_of(t + 2) + lane, hi, kvh);
+        row.next = own_row(a, o, pages, key_of(t + 2) + lane, hi, kvh);
       }
       const uint32_t st = sptr(ring + (t % kStages16) * kStage16) + (lane >> 4) * kRow16 + (lane & 15) * 16;
 #pragma unroll
@@ -463,14 +473,14 @@ __global__ void __launch_bounds__(kThreads, 3) own32_kernel(SharedArgs a, OwnArg
   const int mine = 4 * (blocks32 > warp ? (blocks32 - warp + kWarps - 1) / kWarps : 0);
   auto key_of = [&](int t) { return lo + ((t >> 2) * kWarps + warp) * 32 + (t & 3) * kKeys32; };
   RowAhead row;
-  row.next = own_row(a, pages, key_of(0) + lane, hi, kvh);
+  row.next = own_row(a, o, pages, key_of(0) + lane, hi, kvh);
   const float4* kb = (const float4*)a.k + (kcol ? lane : 0);
   const float4* vb = (const float4*)a.v + (vcol ? lane : 0);
   auto fetch = [&](int t) {
     if (t < mine) {
       if (!(t & 3)) {
         row.now = row.next;
-        row.next = own_row(a, pages, key_of(t + 4) + lane, hi, kvh);
+        row.next = own_row(a, o, pages, key_of(t + 4) + lane, hi, kvh);
       }
       const uint32_t st = sptr(ring + (t % kStages32) * kStage32);
 #pragma unroll
@@ -586,7 +596,8 @@ __global__ void __launch_bounds__(kThreads) join_kernel(SharedArgs a, OwnArgs o)
        r += (int64_t)gridDim.x * kWarps) {
     const int b = (int)(r / a.heads), h = (int)(r - (int64_t)b * a.heads);
     const PrefixRow pre(a, o, b, h);
-    const int np = pre.pieces, own = (own_len(a, b, false) + o.keys - 1) / o.keys, all = np + own;
+    const int len = o.lead + own_len(a, b, false), keys = piece_keys(o, len);
+    const int np = pre.pieces, own = (len + keys - 1) / keys, all = np + own;
     auto lse_of = [&](int p) {
       return p < np ? o.part_lse[pre.first + p * pre.step] : o.own_lse[(p - np) * rows + r];
     };

@@ -104,14 +104,15 @@ struct TileMaps {
   CUtensorMap q, k, v;
 };
 
-// The prefix's pieces and a request's own keys: pieces of `keys` keys each, at
-// most `pieces` (1: all of them, and the result is final) with their results
+// The prefix's pieces and a request's own keys: at most `pieces` (1: all of them,
+// and the result is final) of at least `keys` keys, with their results
 // [piece][n * heads][dv].
 struct OwnArgs {
   Shares shares;  // units == 0: no prefix
   const float *part, *part_lse;  // the prefix's
   int32_t per;
   int32_t pieces, keys;
+  int32_t lead;  // the prefix's keys, read with each request's own
   float *own, *own_lse;
 };
 

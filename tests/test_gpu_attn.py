@@ -573,6 +573,100 @@ def test_shared_bad_value_in_the_prefix(cuda_device, dtype):
     ref.check(got[~hit], want[~hit], b[~hit], "out")
 
 
+# A prefix is read by each request for itself while that is little, and else once
+# by the tile kernel: the tests below have enough requests, or prefix, for that.
+MANY = [(i * 7) % 5 for i in range(300)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("geo", GEOMETRIES)
+def test_shared_prefix_read_once(cuda_device, dtype, geo):
+    _run_shared(cuda_device, dtype, geo, MANY, 333, 16)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("prefix,page", [(40, 16), (128, 64), (127, 24), (300, 8), (129, 128),
+                                         (1000, 7)])
+def test_shared_prefix_read_once_lengths(cuda_device, dtype, prefix, page):
+    _run_shared(cuda_device, dtype, (16, 8, 128, 128), MANY, prefix, page)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("geo,prefix", [((16, 8, 128, 128), 2600), ((64, 1, 64, 64), 5200),
+                                        ((40, 1, 64, 128), 6800)])
+def test_shared_prefix_read_once_by_few(cuda_device, dtype, geo, prefix):
+    """Its tiles are dealt out over all CTAs."""
+    _run_shared(cuda_device, dtype, geo, [200, 3, 0, 66], prefix, 16)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_shared_prefix_read_once_bad_values_and_pages(cuda_device, dtype):
+    torch, ref, nys = _mods()
+    dt = getattr(torch, dtype)
+    heads, kv, d, page, prefix = 16, 8, 64, 16, 250
+    k, v, pp, table = _pool(torch, cuda_device, MANY, prefix, page, kv, d, d, dt, junk=0.0)
+    q = torch.randn((len(MANY), heads, d), device=cuda_device).to(dt)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)
+    cache = nys.PagedKV(k.shape[0], page, kv, d, d, dtype=dt, device=cuda_device, k=k, v=v)
+    att = nys.ExactAttention(heads, kv, d, d, dtype=dt, device=cuda_device)
+    out = torch.empty((len(MANY), heads, d), device=cuda_device, dtype=dt)
+    run = lambda: att.shared(q, cache, i32(MANY), i32(table), out, prefix_pages=i32(pp),
+                             prefix_len=prefix)
+    want, _, b, _ = ref.shared(q, k, v, pp, prefix, MANY, table, 2, 1 / 8.0, dt)
+    for bad in (math.inf, math.nan):
+        kept = v[pp[1], 3, 0, 5].clone()
+        v[pp[1], 3, 0, 5] = bad            # KV head 0, every request
+        run()
+        hit = torch.zeros(out.shape, dtype=torch.bool)
+        hit[:, :2, 5] = True
+        got = out.float().cpu()
+        assert not torch.isfinite(got[hit]).any()
+        ref.check(got[~hit], want[~hit], b[~hit], "out")
+        v[pp[1], 3, 0, 5] = kept
+    assert att.status() == 0
+    pp[1], pp[4] = k.shape[0], -1
+    run()
+    want, _, b, _ = ref.shared(q, k, v, pp, prefix, MANY, table, 2, 1 / 8.0, dt)
+    ref.check(out, want, b, "bad pages")
+    assert att.status() == nys.NYS_ATTN_BAD_PAGE
+    att.clear_status()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_shared_pieces_of_uneven_requests(cuda_device, dtype):
+    """Few and many pieces a request in one call, with and without a prefix."""
+    for lens, prefix in (([4000, 1, 0, 129, 700], 0), ([2500, 0, 31], 77), ([600] * 40 + [0, 1], 0)):
+        _run_shared(cuda_device, dtype, (16, 8, 64, 64), lens, prefix, 32)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_shared_prefix_read_once_in_a_graph(cuda_device, dtype):
+    torch, ref, nys = _mods()
+    dt = getattr(torch, dtype)
+    heads, kv, d, page, prefix = 16, 8, 128, 16, 300
+    k, v, pp, table = _pool(torch, cuda_device, MANY, prefix, page, kv, d, d, dt, junk=0.0)
+    q = torch.randn((len(MANY), heads, d), device=cuda_device).to(dt)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)
+    tl, tt, tp = i32(MANY), i32(table), i32(pp)
+    cache = nys.PagedKV(k.shape[0], page, kv, d, d, dtype=dt, device=cuda_device, k=k, v=v)
+    att = nys.ExactAttention(heads, kv, d, d, dtype=dt, device=cuda_device)
+    out = torch.empty_like(q)
+    run = lambda: att.shared(q, cache, tl, tt, out, prefix_pages=tp, prefix_len=prefix)
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    q.copy_(torch.randn_like(q))
+    lens = [max(x - 1, 0) for x in MANY]
+    tl.copy_(i32(lens))
+    out.zero_()
+    graph.replay()
+    want, _, b, _ = ref.shared(q, k, v, pp, prefix, lens, table, 2, 1 / math.sqrt(d), dt)
+    ref.check(out, want, b, "replayed")
+    assert att.status() == 0
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_shared_in_a_graph(cuda_device, dtype):
     torch, ref, nys = _mods()
