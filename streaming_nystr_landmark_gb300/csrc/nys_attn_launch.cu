@@ -159,13 +159,15 @@ size_t slot_bytes(int dtype, int dv) {
 int64_t prompt_units(int64_t n, int64_t rows, int kv_heads, int group, int dtype) {
   return (rows / (query_tiles(dtype) * (kTileM / group)) + n) * kv_heads;
 }
-// Whether the last round's units are cut.  It pays where rounds are few and
-// long: 2 prompts' last 1,021 and 1,500 tokens over 5,003 earlier ones, f32, 320
-// units of 45 tiles on 152 CTAs, take 303 us whole and 277 us cut (whole calls,
-// the join's 11 us among them).
+// Whether the last round's units are cut; where units are fewer than CTAs, that
+// is all of them.  It pays where rounds are few and long: 2 prompts' last 1,021 and
+// 1,500 tokens over 5,003 earlier ones, f32, 320 units of 45 tiles on 152 CTAs,
+// take 303 us whole and 277 us cut (whole calls, the join's 11 us among them); one
+// new token over 4,000, 8 KV heads, 72 and 29 us, over 30,000 in bf16 183 and 38 us;
+// over 1,100, f32 28 and 25 us, but bf16 15.5 and 16.3 us.
 bool cut_tail(int64_t n, int64_t rows, int64_t keys, int kv_heads, int group, int dtype) {
   const int64_t units = prompt_units(n, rows, kv_heads, group, dtype);
-  return n <= 128 && keys >= 1024 * n && units <= 8 * kSms;
+  return n <= 128 && keys >= (dtype == NYS_F32 ? 1024 : 1536) * n && units <= 8 * kSms;
 }
 // Whether CTAs take their units from a counter: where each has some, and they
 // may differ.
@@ -320,7 +322,8 @@ cudaError_t launch_prompt_tc(const PromptArgs& p, void* workspace, cudaStream_t 
   a.q = p.q;
   a.per = query_tiles(p.dtype);
   const int64_t units = prompt_units(p.n, p.q_rows, p.kv_heads, p.group, p.dtype);
-  const unsigned grid = (unsigned)(units < kSms ? units : kSms);
+  a.tail = workspace && cut_tail(p.n, p.q_rows, p.k_rows, p.kv_heads, p.group, p.dtype);
+  const unsigned grid = (unsigned)(units < kSms && !a.tail ? units : kSms);
   if (workspace) {
     unsigned char* w = static_cast<unsigned char*>(workspace);
     if (p.dtype == NYS_F32) {
@@ -328,7 +331,6 @@ cudaError_t launch_prompt_tc(const PromptArgs& p, void* workspace, cudaStream_t 
       w += images_of(p.kv_heads, p.d, p.dv, p.n, p.k_rows).end;
     }
     if (count_units(units)) a.counter = reinterpret_cast<uint32_t*>(w);
-    a.tail = grid > 1 && cut_tail(p.n, p.q_rows, p.k_rows, p.kv_heads, p.group, p.dtype);
     a.part = reinterpret_cast<float*>(w + kCounterBytes);
     a.part_lse = a.part + (int64_t)kSms * a.per * kTileM * p.dv;
   }

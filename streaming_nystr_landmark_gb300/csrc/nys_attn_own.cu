@@ -674,6 +674,7 @@ __global__ void __launch_bounds__(256) tail_join_kernel(const __grid_constant__ 
   __syncthreads();
   if (!su.valid) return;
   const int64_t step = (int64_t)a.per * kTileM;
+  const int cut = cut_pieces(su, st.cut);
   for (int row = blockIdx.y * 8 + warp; row < (su.np1 > 0 ? 2 : 1) * kTileM; row += 8 * gridDim.y) {
     const int tile = row / kTileM, r = row - tile * kTileM, pos = r / a.group;
     if (pos >= (tile ? su.np1 : su.np0)) continue;
@@ -683,7 +684,7 @@ __global__ void __launch_bounds__(256) tail_join_kernel(const __grid_constant__ 
     float top = -INFINITY, w[5];  // lane = piece (at most 152)
 #pragma unroll
     for (int i = 0; i < 5; ++i) {
-      w[i] = lane + 32 * i < st.cut ? a.part_lse[first + (lane + 32 * i) * step] * kLog2e : -INFINITY;
+      w[i] = lane + 32 * i < cut ? a.part_lse[first + (lane + 32 * i) * step] * kLog2e : -INFINITY;
       top = fmaxf(top, w[i]);
     }
 #pragma unroll
@@ -700,7 +701,7 @@ __global__ void __launch_bounds__(256) tail_join_kernel(const __grid_constant__ 
     float y[4] = {0.f, 0.f, 0.f, 0.f};
     const bool col = lane * 4 < a.dv;
 #pragma unroll 8
-    for (int p = 0; p < st.cut; ++p) {
+    for (int p = 0; p < cut; ++p) {
       const float f = __shfl_sync(0xffffffffu, p < 32 ? w[0] : p < 64 ? w[1] : p < 96 ? w[2] : p < 128 ? w[3] : w[4], p & 31);
       if (col && f != 0.f) {
         const float4 x = *reinterpret_cast<const float4*>(a.part + (first + p * step) * a.dv + lane * 4);

@@ -286,9 +286,14 @@ struct Tail {
     }
   }
 };
-// Piece p of `cut` of a whole unit (empty where it has too few tiles).
+// Of `cut` pieces of a whole unit, those that are not empty: of two tiles at least,
+// and more than 32 only of 16 and more (the join reads a piece after the other).
+__device__ __forceinline__ int cut_pieces(const Unit& u, int cut) {
+  return min(min(cut, max(u.nt / 2, 1)), max(32, u.nt / 16));
+}
+// Piece p of `cut` of a whole unit.
 __device__ __forceinline__ void cut_unit(Unit& u, int p, int cut, int slot) {
-  const int c = min(cut, max(u.nt / 2, 1));
+  const int c = cut_pieces(u, cut);
   const int tb = p < c ? u.nt * p / c : u.nt, te = p < c ? u.nt * (p + 1) / c : u.nt;
   u.slot = slot;
   u.kb = tb * kTileN;

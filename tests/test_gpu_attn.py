@@ -492,6 +492,16 @@ def test_prompt_last_round_is_cut(cuda_device, dtype, q_lens, k_lens):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("geo,q_lens,k_lens", [
+    ((16, 8, 128, 128), [1], [4001]), ((1, 1, 64, 64), [1], [30000]), ((1, 1, 64, 64), [1], [1600]),
+    ((8, 1, 64, 128), [3, 1], [5000, 2]), ((16, 8, 128, 128), [16, 0, 2], [9000, 3000, 1]),
+    ((4, 2, 64, 64), [130], [4000])])
+def test_prompt_few_rows_of_many_keys(cuda_device, dtype, geo, q_lens, k_lens):
+    """Fewer units than CTAs: every unit is cut."""
+    _run_prompt(cuda_device, dtype, geo, q_lens, k_lens)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_prompt_without_workspace(cuda_device, dtype):
     torch, ref, nys = _mods()
     dt = getattr(torch, dtype)
