@@ -112,14 +112,27 @@ int most_own_pieces(int64_t ctas) {
   return clamp_int(div_up(16 * kSms, ctas), 1, kMostPieces);
 }
 // Keys of a piece at least.  With few CTAs a piece's own length is the call's time
-// (one request of 346 keys, 8 KV heads, f32: 128 keys 8.6 us, 192 10.7 us; four of
-// 500 to 700: 10.7 and 11.6 us); with more, the pieces that are joined are (40
+// (one request of 346 keys, 8 KV heads, f32, joined by a launch: 128 keys 8.6 us, 192
+// 10.7 us; four of 500 to 700: 10.7 and 11.6 us); with more, the pieces that are joined are (40
 // requests of 500 to 700: 256 keys 38 us, 192 43 us).
 int least_own_keys(int64_t ctas) { return ctas <= 48 ? 128 : 256; }
+// Pieces of a request where they are one cluster, which joins them in shared memory
+// instead of by another launch; 0: they are not.  Clusters hold their places until
+// their last piece is done, so they pay where all CTAs run at once, three a SM: 4
+// requests of 500 to 700 keys, 16 heads on 8, f32 10.7 -> 8.4 us, 16 of them (384
+// CTAs) 15.5 -> 13.7 us, 64 (1,536 CTAs) 57.9 -> 64.5 us.  More than 8 pieces, a
+// cluster's most, are worth giving up to 512 keys each (one request of up to 4,000,
+// bf16, 16.3 -> 13.6 us), but not in f32 with many heads on a key (22 -> 26 us).
+int cluster_pieces(int64_t ctas, int64_t cap, int pieces, int group, int dtype) {
+  constexpr int kMost = 8;
+  if (pieces > kMost && (cap > kMost * 512 || (dtype == NYS_F32 && group > 2))) return 0;
+  if (pieces > kMost) pieces = kMost;
+  return pieces > 1 && ctas * pieces <= 3 * kSms ? pieces : 0;
+}
 // Whether each request reads the prefix's keys for itself, in front of its own: no
 // tile kernel, no split, one join less.  It pays until the rows read again weigh
 // more (few requests or a short prefix): 4 requests of 3 to 45 keys over 301, bf16,
-// 8 KV heads, 8.2 us against 14.4 us; f32 8.8 against 20.6 us; 64 over 301, 4 KV
+// 8 KV heads, 6.6 us against 14.4 us; f32 7.1 against 20.6 us; 64 over 301, 4 KV
 // heads (77,000 rows), bf16 20.6 against 26.8 us, f32 29.0 against 25.5 us; 16 over
 // 1,000, 8 KV heads (128,000 rows), bf16 21.5 against 14.0 us.
 bool read_with_own(int64_t ctas, int64_t prefix, int dtype) {
@@ -219,6 +232,11 @@ cudaError_t launch_shared_tiled(const SharedArgs& s, void* workspace, cudaStream
   const int64_t cap = o.lead + (int64_t)s.width * s.page;
   o.keys = least_own_keys(ctas);
   o.pieces = clamp_int(div_up(cap, o.keys), 1, most_own_pieces(ctas));
+  if (o.shares.units == 0) {
+    const int pieces = cluster_pieces(ctas, cap, o.pieces, s.group, s.dtype);
+    o.cluster = pieces > 1;
+    if (o.cluster) o.pieces = pieces;
+  }
   const size_t images = s.dtype == NYS_F32 && o.shares.units > 0
                             ? images_of(s.kv_heads, s.d, s.dv, 1, s.prefix_len).end
                             : 0;
@@ -277,7 +295,7 @@ cudaError_t launch_shared_tiled(const SharedArgs& s, void* workspace, cudaStream
     if (e != cudaSuccess) return e;
   }
   const cudaError_t e = launch_own(s, o, stream);
-  if (e != cudaSuccess || o.pieces == 1) return e;
+  if (e != cudaSuccess || o.pieces == 1 || o.cluster) return e;
   return launch_join(s, o, stream);
 }
 

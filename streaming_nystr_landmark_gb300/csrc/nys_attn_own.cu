@@ -11,7 +11,10 @@
 // between warps until their results are joined; three CTAs a SM keep the reads
 // in flight.  64 requests of 97 to 1025 keys over a prefix of 2,000 (8 KV heads of
 // 128, f32): 42 us for 208 MB from memory, 64% of its peak, and 60 us for the whole
-// call (floor 33 us).  Keys past the length and pages outside the pool
+// call (floor 33 us).  Pieces of a request are joined by a second launch,
+// or, where all CTAs run at once, in shared memory as a cluster (4 requests of 3 to
+// 45 keys over a prefix of 301, bf16: 6.6 us, 8.3 us with the launch).
+// Keys past the length and pages outside the pool
 // are filled with zeros and never read from memory.
 //
 // bf16 / fp16: tiles of 16 keys, mma.sync m16n8k16 with the group's heads as
@@ -123,12 +126,79 @@ struct PrefixRow {
   }
 };
 
+// Shared memory of CTA `rank` of this cluster.
+__device__ __forceinline__ uint32_t cluster_at(uint32_t mine, int rank) {
+  uint32_t at;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(mine), "r"(rank));
+  return at;
+}
+__device__ __forceinline__ float cluster_read(uint32_t at) {
+  float x;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
+  return x;
+}
+__device__ __forceinline__ float4 cluster_read4(uint32_t at) {
+  float4 x;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+               : "r"(at)
+               : "memory");
+  return x;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::
+                   : "memory");
+}
+
+// Joins the pieces of a request where they are one cluster: each CTA's results
+// (log of the sum, and the row) are in its shared memory at `lse` and `y`; a warp
+// takes a head.
+template <typename T>
+__device__ void cluster_join(const SharedArgs& a, const OwnArgs& o, const float* lse,
+                             const float* y, int b, int h0, int heads, int piece) {
+  cluster_sync();
+  const int lane = threadIdx.x & 31;
+  const bool col = lane * 4 < a.dv;
+  for (int h = piece * kWarps + (threadIdx.x >> 5); h < heads; h += o.pieces * kWarps) {
+    float w = lane < o.pieces ? cluster_read(cluster_at(sptr(lse + h), lane)) * kLog2e : -INFINITY;
+    float top = w;
+#pragma unroll
+    for (int s = 4; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+    top = __shfl_sync(0xffffffffu, top, 0);
+    w = ex2(w - (top == -INFINITY ? 0.f : top));
+    float total = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int p = 0; p < o.pieces; ++p) {
+      const float f = __shfl_sync(0xffffffffu, w, p);
+      total += f;
+      if (col && f != 0.f) {
+        const float4 z = cluster_read4(cluster_at(sptr(y + h * a.dv + lane * 4), p));
+        x[0] = fmaf(z.x, f, x[0]);
+        x[1] = fmaf(z.y, f, x[1]);
+        x[2] = fmaf(z.z, f, x[2]);
+        x[3] = fmaf(z.w, f, x[3]);
+      }
+    }
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+    if (col) {
+      T* out = (T*)a.out.p + b * a.out.row + (h0 + h) * a.out.head + lane * 4;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) out[i] = narrow<T>(x[i] * inv);
+    }
+    if (lane == 0 && a.lse)
+      a.lse[(int64_t)b * a.heads + h0 + h] =
+          total == 0.f ? -INFINITY : fmaf(top, 0.6931471805599453f, logf(total));
+  }
+  cluster_sync();  // (no CTA leaves while its results are read)
+}
+
 // Joins the warps' results (log2 maxima m and sums l [warp][head], O
 // [warp][head][dv]) and, where this CTA has all of the request's own keys, the
 // prefix's pieces; thread = column.  heads: of this CTA, from h0.
 template <typename T, int HB>
 __device__ void join(const SharedArgs& a, const OwnArgs& o, const float* m, const float* l,
-                     const float* acc, int b, int h0, int heads, int piece) {
+                     float* acc, int b, int h0, int heads, int piece) {
+  float* cy = acc + kWarps * HB * a.dv;  // this CTA's results for its cluster
+  float* cl = cy + HB * a.dv;
   for (int h = threadIdx.x >> 5; h < heads; h += kWarps) {
     const int lane = threadIdx.x & 31;
     const int64_t row = (int64_t)b * a.heads + h0 + h;
@@ -197,12 +267,16 @@ __device__ void join(const SharedArgs& a, const OwnArgs& o, const float* m, cons
         for (int i = 0; i < 4; ++i) out[i] = narrow<T>(y[i]);
       }
       if (lane == 0 && a.lse) a.lse[row] = lse;
+    } else if (o.cluster) {
+      if (col) *reinterpret_cast<float4*>(cy + h * a.dv + lane * 4) = make_float4(y[0], y[1], y[2], y[3]);
+      if (lane == 0) cl[h] = lse;
     } else {
       const int64_t at = (int64_t)piece * rows + row;
       if (col) *reinterpret_cast<float4*>(o.own + at * a.dv + lane * 4) = make_float4(y[0], y[1], y[2], y[3]);
       if (lane == 0) o.own_lse[at] = lse;
     }
   }
+  if (o.cluster) cluster_join<T>(a, o, cl, cy, b, h0, heads, piece);
 }
 
 // ------------------------------------------------------------ bf16 and fp16
@@ -212,6 +286,7 @@ constexpr int kStages16 = 2;
 constexpr int kRow16 = 272;       // bytes of a row in shared memory: 256 + 16, conflict-free
 constexpr int kStage16 = 2 * kKeys16 * kRow16;
 constexpr int kSmem16 = kWarps * kStages16 * kStage16;
+static_assert(kSmem16 >= ((kWarps + 1) * kHeads16 * 129 + kWarps * kHeads16) * 4, "results to join");
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -260,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 3) own16_kernel(SharedArgs a, OwnArg
   const bool waits = o.pieces == 1 || (blockIdx.x == 0 && blockIdx.y == 0);
   if (!own_range(a, o, b, piece, lo, hi)) {
     if (waits) wait_for_previous();
-    return;
+    if (!o.cluster) return;
   }
   const int32_t* pages = a.table + (int64_t)b * a.width;
   const int dc = a.d >> 3, vc = a.dv >> 3;  // 16-byte chunks of a row
@@ -418,6 +493,7 @@ constexpr int kKeys32 = 8;
 constexpr int kStages32 = 2;
 constexpr int kStage32 = 2 * kKeys32 * 512;
 constexpr int kSmem32 = kWarps * kStages32 * kStage32;
+static_assert(kSmem32 >= ((kWarps + 1) * 8 * 129 + kWarps * 8) * 4, "results to join");
 
 // Sums each of V per-lane partials over the warp; lane gets the total of value
 // value_of<V>(lane).
@@ -463,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 3) own32_kernel(SharedArgs a, OwnArg
   const bool waits = o.pieces == 1 || (blockIdx.x == 0 && blockIdx.y == 0);
   if (!own_range(a, o, b, piece, lo, hi)) {
     if (waits) wait_for_previous();
-    return;
+    if (!o.cluster) return;
   }
   const int32_t* pages = a.table + (int64_t)b * a.width;
   const bool kcol = lane * 4 < a.d, vcol = lane * 4 < a.dv;
@@ -727,10 +803,25 @@ cudaError_t allow(K kernel, int bytes) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-// Beside the prefix's launch where there is one.
+// Beside the prefix's launch where there is one; with a request's pieces as
+// clusters where they join themselves.
 cudaError_t launch_own_kernel(void (*kernel)(SharedArgs, OwnArgs), dim3 grid, size_t smem,
                               cudaStream_t stream, const SharedArgs& a, const OwnArgs& o) {
   if (o.shares.units > 0) return launch_dependent(kernel, grid, kThreads, smem, stream, a, o);
+  if (o.cluster) {
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid;
+    c.blockDim = dim3(kThreads);
+    c.dynamicSmemBytes = smem;
+    c.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)o.pieces;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    c.attrs = at;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, kernel, a, o);
+  }
   kernel<<<grid, kThreads, smem, stream>>>(a, o);
   return cudaGetLastError();
 }

@@ -112,6 +112,7 @@ struct OwnArgs {
   const float *part, *part_lse;  // the prefix's
   int32_t per;
   int32_t pieces, keys;
+  int32_t cluster;  // a request's pieces are one cluster and join themselves
   int32_t lead;  // the prefix's keys, read with each request's own
   float *own, *own_lse;
 };

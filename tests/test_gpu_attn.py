@@ -650,6 +650,42 @@ def test_shared_pieces_of_uneven_requests(cuda_device, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("geo", [(16, 8, 128, 128), (1, 1, 64, 64), (20, 1, 64, 128), (6, 2, 96, 64)])
+@pytest.mark.parametrize("lens,prefix", [([257, 1, 0], 0), ([900, 0, 129], 100), ([0, 0], 300),
+                                         ([5000], 0), ([2000, 3], 0)])
+def test_shared_pieces_that_join_in_a_cluster(cuda_device, dtype, geo, lens, prefix):
+    """Two to eight pieces a request, some of them empty, and next to it more."""
+    _run_shared(cuda_device, dtype, geo, lens, prefix, 16)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_shared_cluster_bad_values(cuda_device, dtype):
+    """A NaN or infinity in one piece reaches its request and channel, no other."""
+    torch, ref, nys = _mods()
+    dt = getattr(torch, dtype)
+    heads, kv, d, page, lens = 4, 2, 64, 16, [700, 0, 300]
+    k, v, _, table = _pool(torch, cuda_device, lens, 0, page, kv, d, d, dt)
+    q = torch.randn((3, heads, d), device=cuda_device).to(dt)
+    want, _, b, _ = ref.shared(q, k, v, [], 0, lens, table, 2, 1 / 8.0, dt)
+    v[table[0][25], 3, 0, 5] = math.inf
+    v[table[2][1], 2, 1, 7] = math.nan
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)
+    cache = nys.PagedKV(k.shape[0], page, kv, d, d, dtype=dt, device=cuda_device, k=k, v=v)
+    att = nys.ExactAttention(heads, kv, d, d, dtype=dt, device=cuda_device)
+    out = torch.empty((3, heads, d), device=cuda_device, dtype=dt)
+    att.shared(q, cache, i32(lens), i32(table), out)
+    hit = torch.zeros(out.shape, dtype=torch.bool)
+    hit[0, :2, 5] = True
+    hit[2, 2:, 7] = True
+    got = out.float().cpu()
+    assert not torch.isfinite(got[hit]).any()
+    ref.check(got[~hit], want[~hit], b[~hit], "out")
+    again = torch.empty_like(out)
+    att.shared(q, cache, i32(lens), i32(table), again)
+    assert torch.equal(out.view(torch.uint8), again.view(torch.uint8))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_shared_prefix_read_once_in_a_graph(cuda_device, dtype):
     torch, ref, nys = _mods()
     dt = getattr(torch, dtype)
