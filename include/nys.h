@@ -471,7 +471,9 @@ int nys_attn_shared(const nys_attn_config* cfg, int64_t n, const nys_pool* pool,
  * for each of the `total` new tokens in request order its slot (int64,
  * page * page_size + offset; -1 without a page) and its position in the
  * request (int32).  taken[0] is how many pages left the free list.  All
- * pointers are device pointers.  Errors: NYS_E_INVAL, NYS_E_CUDA. */
+ * pointers are device pointers.  lens may be cached itself, which then holds
+ * the new lengths; apart from that no array that is written may overlap
+ * another one (NYS_E_INVAL).  Errors: NYS_E_INVAL, NYS_E_ALIGN, NYS_E_CUDA. */
 int nys_kv_plan(int64_t n, int32_t page, const int32_t* cached, const int32_t* fresh,
                 const int32_t* free_pages, int64_t n_free, int32_t* table, int32_t width,
                 int64_t total, int32_t* q_off, int32_t* lens, int64_t* slots,

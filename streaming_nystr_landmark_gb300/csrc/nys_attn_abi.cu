@@ -51,6 +51,16 @@ int check_pool(const nys_pool* p, int elem) {
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) % to) == 0; }
 
+struct Range {
+  const void* p;
+  int64_t bytes;
+};
+bool overlap(const Range& a, const Range& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x && y && a.bytes > 0 && b.bytes > 0 && x < y + (uintptr_t)b.bytes &&
+         y < x + (uintptr_t)a.bytes;
+}
+
 }  // namespace
 
 extern "C" {
@@ -177,6 +187,18 @@ int nys_kv_plan(int64_t n, int32_t page, const int32_t* cached, const int32_t* f
       !aligned(table, 4) || !aligned(q_off, 4) || !aligned(lens, 4) || !aligned(slots, 8) ||
       !aligned(positions, 4) || !aligned(taken, 4) || !aligned(status, 4))
     return NYS_E_ALIGN;
+  // Every CTA reads all lengths while others write: what is written overlaps nothing
+  // else (lens may be cached itself).
+  const Range in[] = {{cached, 4 * n}, {fresh, 4 * n}, {free_pages, 4 * n_free}};
+  const Range out[] = {{lens, 4 * n},      {q_off, 4 * (n + 1)},   {table, 4 * n * width},
+                       {slots, 8 * total}, {positions, 4 * total}, {taken, 4},
+                       {status, 4}};
+  for (const Range& o : out) {
+    for (const Range& i : in)
+      if (overlap(o, i) && !(i.p == cached && o.p == lens && cached == lens)) return NYS_E_INVAL;
+    for (const Range& x : out)
+      if (&x < &o && overlap(o, x)) return NYS_E_INVAL;
+  }
   nys::PlanArgs a{cached,    fresh, free_pages, table,  q_off,  lens,
                   slots,     positions, taken,  status, total,  n_free,
                   (int32_t)n, width, page};

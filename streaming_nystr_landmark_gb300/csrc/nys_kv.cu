@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a, int64_t 
       const int i = c0 + x;
       if (i < a.n && blockIdx.x == (unsigned)(c0 / kPlanChunk) % gridDim.x) {
         a.q_off[i] = (int)(uint32_t)at;
-        a.lens[i] = cached[e] + fresh[e];
+        if (a.lens) a.lens[i] = cached[e] + fresh[e];
       }
     }
     if (tid == 0) s_off[kPlanChunk] = (int)(uint32_t)all;
@@ -145,6 +145,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a, int64_t 
     a.slots[t] = -1;
     a.positions[t] = -1;
   }
+}
+
+// New lengths in place of the old ones (lens is cached), after the plan's CTAs have
+// all read them; bad lengths as plan_kernel takes them.
+__global__ void __launch_bounds__(256) grow_kernel(int32_t* lens, const int32_t* fresh, int32_t n) {
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;
+  const int c = lens[i], f = fresh[i];
+  lens[i] = c < 0 || f < 0 || (int64_t)c + f > INT32_MAX ? max(c, 0) : c + f;
 }
 
 // Rows into pages: token t's K and V rows go to slot slots[t] of the pools; a
@@ -204,7 +213,15 @@ cudaError_t launch_plan(const PlanArgs& a, cudaStream_t stream) {
   if (ctas < 1) ctas = 1;
   if (ctas > 2 * 152) ctas = 2 * 152;
   const int64_t per = (a.total + ctas - 1) / ctas;
-  plan_kernel<<<(unsigned)ctas, kPlanThreads, 0, stream>>>(a, per < 1 ? 1 : per);
+  // A single CTA's threads read a length before they write it; more CTAs leave the
+  // writing of lengths that they all read to a launch of its own.
+  PlanArgs p = a;
+  const bool later = a.n > 0 && a.lens == a.cached && ctas > 1;
+  if (later) p.lens = nullptr;
+  plan_kernel<<<(unsigned)ctas, kPlanThreads, 0, stream>>>(p, per < 1 ? 1 : per);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || !later) return e;
+  grow_kernel<<<(unsigned)((a.n + 255) / 256), 256, 0, stream>>>(a.lens, a.fresh, a.n);
   return cudaGetLastError();
 }
 

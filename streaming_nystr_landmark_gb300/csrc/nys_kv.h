@@ -12,7 +12,7 @@ struct PlanArgs {
   const int32_t* free_pages;      // [n_free]
   int32_t* table;                 // [n][width]
   int32_t* q_off;                 // [n + 1]
-  int32_t* lens;                  // [n]
+  int32_t* lens;                  // [n]; may be `cached`
   int64_t* slots;                 // [total]
   int32_t* positions;             // [total]
   int32_t* taken;                 // [1]

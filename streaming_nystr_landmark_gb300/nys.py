@@ -666,7 +666,8 @@ class PagePlan(_Status):
 
     def update(self, cached, fresh, free_pages, table):
         """cached, fresh int32 [n]; free_pages int32 [any]; table int32
-        [n][width], whose new columns are filled in place."""
+        [n][width], whose new columns are filled in place.  cached may be this
+        plan's lens, which then grows in place."""
         i32 = self.torch.int32
         nys_kv_plan(self.n, self.page, _ints(cached, i32, (self.n,), "cached"),
                     _ints(fresh, i32, (self.n,), "fresh"),

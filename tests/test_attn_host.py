@@ -132,6 +132,24 @@ def test_plan_refusals(kw, code):
     assert _plan(**kw) == code
 
 
+def _apart(**kw):
+    """Plan arguments that do not overlap, a megabyte apart, but for those given."""
+    names = ("cached", "fresh", "free", "table", "qo", "lens", "slots", "pos", "taken", "st")
+    a = {x: A + (i << 20) for i, x in enumerate(names)}
+    return dict(a, **kw)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(fresh=A + (5 << 20)),              # fresh = lens
+    dict(lens=A + 4),                       # lens one request into cached
+    dict(qo=A), dict(free=A + (3 << 20) + 28), dict(table=A + (1 << 20) - 28),
+    dict(slots=A + (7 << 20) - 8), dict(taken=A + (4 << 20) + 8), dict(st=A + (2 << 20)),
+])
+def test_plan_refuses_outputs_that_overlap(kw):
+    """Every CTA reads all lengths while others write."""
+    assert _plan(**_apart(**kw)) == nys.NYS_E_INVAL
+
+
 @pytest.mark.parametrize("kw,code", [
     (dict(pool=None), nys.NYS_E_INVAL), (dict(tokens=-1), nys.NYS_E_INVAL),
     (dict(k=None), nys.NYS_E_INVAL), (dict(v=rows(p=None)), nys.NYS_E_INVAL),

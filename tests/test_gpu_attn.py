@@ -389,6 +389,30 @@ def test_plan(cuda_device, page, n, most_cached, most_fresh):
     assert p.status() == 0
 
 
+@pytest.mark.parametrize("n,most", [(1, 5), (70, 900), (2500, 40)])
+def test_plan_grows_its_lengths_in_place(cuda_device, n, most):
+    """lens passed as cached, by one CTA and by many: the same plan, step by step."""
+    torch, ref, nys = _mods()
+    g = torch.Generator().manual_seed(n)
+    page, steps = 16, 3
+    fresh = [torch.randint(0, most + 1, (n,), generator=g).tolist() for _ in range(steps)]
+    total = [sum(f) for f in fresh]
+    width = max(sum(f) for f in zip(*fresh)) // page + 1
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)
+    free = list(range(n * width))
+    cached, table = [0] * n, [[-1] * width for _ in range(n)]
+    t, lens = i32(table), i32(cached)
+    for f, k in zip(fresh, total):
+        p = nys.PagePlan(n, width, k, page, device=cuda_device)
+        p.lens.copy_(lens)
+        p.update(p.lens, i32(f), i32(free), t)
+        table, off, cached, slots, positions, taken = ref.plan(cached, f, free, table, page)
+        free, lens = free[taken:], p.lens
+        got = [x.tolist() for x in (t, p.q_off, p.lens, p.slots, p.positions)]
+        assert got == [table, off, cached, slots, positions]
+        assert p.taken.item() == taken and p.status() == 0
+
+
 def test_plan_without_pages_or_columns(cuda_device):
     torch, ref, nys = _mods()
     i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)
