@@ -710,16 +710,18 @@ class ExactAttention(_Status):
             self._captured |= capturing
             return
         need = nys_attn_workspace_bytes(self.cfg, n, rows, keys)
-        self._sizes = (n, rows, keys)
         if need > self._work_bytes:
+            # May raise: nothing is noted before it is there.
+            work = self.torch.empty(need, dtype=self.torch.uint8, device=self.device)
             if self._captured:
                 self._held.append(self._work)
             elif self._work is not None:
                 # Work that uses it may be queued on a stream other than its own.
                 self._work.record_stream(self.torch.cuda.current_stream(self.device))
             self._captured = False
-            self._work = self.torch.empty(need, dtype=self.torch.uint8, device=self.device)
-            self._work_ptr, self._work_bytes = self._work.data_ptr(), need
+            self._work = work
+            self._work_ptr, self._work_bytes = work.data_ptr(), need
+        self._sizes = (n, rows, keys)
         self._captured |= capturing
 
     def prompt(self, q, k, v, q_off, out, k_off=None, lse=None):

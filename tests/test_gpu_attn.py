@@ -802,6 +802,26 @@ def test_graph_keeps_its_workspace(cuda_device, dtype):
     assert att.status() == 0
 
 
+def test_workspace_is_asked_for_again_after_it_was_refused(cuda_device, monkeypatch):
+    """An allocation that failed leaves no note of its size behind: the same call
+    made again takes the workspace then, and the tiled kernel."""
+    torch, ref, nys = _mods()
+    q, k, v, qo, ko = _inputs(torch, cuda_device, [300], [300], 4, 2, 64, 64, torch.float32)
+    att = nys.ExactAttention(4, 2, 64, 64, device=cuda_device)
+    out = torch.empty_like(q)
+
+    def refuse(*a, **kw):
+        raise torch.cuda.OutOfMemoryError("out of memory")
+    with monkeypatch.context() as m:
+        m.setattr(torch, "empty", refuse)
+        with pytest.raises(torch.cuda.OutOfMemoryError):
+            att.prompt(q, k, v, qo, out)
+    att.prompt(q, k, v, qo, out)
+    assert att._work_bytes >= nys.nys_attn_workspace_bytes(att.cfg, 1, 300, 300) > 0
+    want, _, b, _ = ref.prompt(q, k, v, [300], [300], 2, 1 / 8.0, torch.float32)
+    ref.check(out, want, b, "out")
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_prompt_units_of_every_kind_in_any_order(cuda_device, dtype):
     """Units of one and two query tiles, with one, many and no key tiles, follow
