@@ -59,6 +59,17 @@ class ExactLayer:
         self.prefix_pages = None
         self._plans = {}
 
+    def _check(self, q, k, v):
+        """Refuses tensors that a call below would refuse, before anything is taken
+        or counted."""
+        att = self.attention
+        if q is not None:
+            nys._rows(q, att.dtype, att.heads, att.d, "q")
+        nys._rows(k, att.dtype, att.kv_heads, att.d, "k")
+        nys._rows(v, att.dtype, att.kv_heads, att.dv, "v")
+        if v.shape[0] != k.shape[0]:
+            raise ValueError(f"v: {v.shape[0]} rows, k has {k.shape[0]}")
+
     def _plan(self, fresh):
         """Pages and slots for fresh[i] more tokens of request i."""
         torch, total = self.torch, sum(fresh)
@@ -88,16 +99,15 @@ class ExactLayer:
         before any request is admitted."""
         if self.used:
             raise ValueError("the prefix comes before the first request")
+        self._check(None, k, v)
         torch, n = self.torch, k.shape[0]
         need = -(-n // self.page)
         if need > self.free.shape[0]:
             raise ValueError(f"{need} pages wanted, {self.free.shape[0]} there")
-        self.used = need
-        self.prefix_pages = self.free[:self.used].clone()
-        self.prefix_len = n
+        pages = self.free[:need].clone()
         at = torch.arange(n, device=self.device)
-        self.cache.write(k, v, self.prefix_pages.long()[at // self.page] * self.page
-                         + at % self.page)
+        self.cache.write(k, v, pages.long()[at // self.page] * self.page + at % self.page)
+        self.used, self.prefix_pages, self.prefix_len = need, pages, n
 
     def admit(self, q, k, v, lengths):
         """The requests' prompts, packed back to back (q [sum][heads][d], k and v
@@ -108,17 +118,22 @@ class ExactLayer:
             raise ValueError("admit() takes requests from their first token")
         if not q.shape[0] == k.shape[0] == v.shape[0] == sum(lengths):
             raise ValueError("q, k and v must have as many rows as the lengths' sum")
-        plan = self._plan(list(lengths))
-        self.cache.write(k, v, plan.slots)
+        self._check(q, k, v)
+        # Memory first: an allocation that fails leaves the requests as they were.
         rows = q.shape[0]
         out = torch.empty((rows, att.heads, att.dv), dtype=att.dtype, device=self.device)
+        att._workspace(self.requests, rows, rows)
+        if self.prefix_len > 0:
+            lse, over = torch.empty((2, rows, att.heads), device=self.device).unbind(0)
+            first = torch.empty_like(out)
+            none = torch.zeros(rows, dtype=torch.int32, device=self.device)
+            att._workspace(rows, rows, self.prefix_len)
+        plan = self._plan(list(lengths))
+        self.cache.write(k, v, plan.slots)
         if self.prefix_len == 0:
             return att.prompt(q, k, v, plan.q_off, out)
         # Over the prompt's own keys and, as rows without own keys, over the prefix.
-        lse, over = torch.empty((2, rows, att.heads), device=self.device).unbind(0)
         att.prompt(q, k, v, plan.q_off, out, lse=lse)
-        first = torch.empty_like(out)
-        none = torch.zeros(rows, dtype=torch.int32, device=self.device)
         att.shared(q, self.cache, none, none.view(rows, 1), first,
                    prefix_pages=self.prefix_pages, prefix_len=self.prefix_len, lse=over)
         return merge(out, lse, first, over, out)
@@ -129,10 +144,12 @@ class ExactLayer:
         att = self.attention
         if not q.shape[0] == k.shape[0] == v.shape[0] == self.requests:
             raise ValueError("q, k and v must have one row a request")
-        plan = self._plan([1] * self.requests)
-        self.cache.write(k, v, plan.slots)
+        self._check(q, k, v)
         out = self.torch.empty((self.requests, att.heads, att.dv), dtype=att.dtype,
                                device=self.device)
+        att._workspace(self.requests, self.requests, self.prefix_len)
+        plan = self._plan([1] * self.requests)
+        self.cache.write(k, v, plan.slots)
         return att.shared(q, self.cache, self.lens, self.table, out,
                           prefix_pages=self.prefix_pages, prefix_len=self.prefix_len)
 

@@ -84,6 +84,68 @@ def test_layer_refuses_rows_and_lengths_that_differ(cuda_device):
     assert layer.lengths == [5, 1] and layer.lens.tolist() == [5, 1]
 
 
+def _state(layer):
+    return (layer.used, list(layer.lengths), layer.lens.tolist(), layer.prefix_len,
+            layer.prefix_pages is None, layer.table.tolist())
+
+
+def test_layer_refuses_tensors_before_anything_is_counted(cuda_device, monkeypatch):
+    """Tensors of another type, geometry or layout, and memory that is not there,
+    leave the layer as it was: the right call made next succeeds."""
+    import torch
+    import attn_reference as ref
+    from streaming_nystr_landmark_gb300 import serving
+    heads, kv, d, dv = 4, 2, 64, 32
+    layer = serving.ExactLayer(heads, kv, d, dv, 2, 16, 16, 64, device=cuda_device)
+    g = torch.Generator(device=cuda_device).manual_seed(0)
+    rn = lambda *s: torch.randn(s, generator=g, device=cuda_device)
+
+    def refused(call, q, k, v, *more):
+        """Every tensor wrong in every way, one at a time."""
+        good, names = [q, k, v], ("q", "k", "v")
+        bad = {"type": lambda t: t.bfloat16(), "host": lambda t: t.cpu(),
+               "heads": lambda t: torch.cat([t, t], 1), "dim": lambda t: torch.cat([t, t], 2),
+               "layout": lambda t: t.transpose(1, 2).contiguous().transpose(1, 2),
+               "rows": lambda t: t[:-1]}
+        for i, name in enumerate(names):
+            if good[i] is None:
+                continue
+            for why, change in bad.items():
+                args = list(good)
+                args[i] = change(good[i])
+                before = _state(layer)
+                with pytest.raises(ValueError):
+                    call(*[a for a in args if a is not None], *more)
+                assert _state(layer) == before, (name, why)
+
+        def no_memory(*a, **kw):
+            raise torch.cuda.OutOfMemoryError("out of memory")
+        if q is not None:
+            before = _state(layer)
+            with monkeypatch.context() as m:
+                m.setattr(torch, "empty", no_memory)
+                with pytest.raises(torch.cuda.OutOfMemoryError):
+                    call(q, k, v, *more)
+            assert _state(layer) == before
+
+    pk, pv = rn(20, kv, d), rn(20, kv, dv)
+    refused(layer.set_prefix, None, pk, pv)
+    layer.set_prefix(pk, pv)
+    lens = [5, 30]
+    q, k, v = rn(35, heads, d), rn(35, kv, d), rn(35, kv, dv)
+    refused(layer.admit, q, k, v, lens)
+    layer.admit(q, k, v, lens)
+    q1, k1, v1 = rn(2, heads, d), rn(2, kv, d), rn(2, kv, dv)
+    refused(layer.decode, q1, k1, v1)
+    out = layer.decode(q1, k1, v1)
+    ks = [torch.cat([pk, a, b[None]]) for a, b in zip(k.split(lens), k1)]
+    vs = [torch.cat([pv, a, b[None]]) for a, b in zip(v.split(lens), v1)]
+    want, _, bound, _ = ref.prompt(q1, torch.cat(ks), torch.cat(vs), [1, 1],
+                                   [len(x) for x in ks], heads // kv, 1 / math.sqrt(d), torch.float32)
+    ref.check(out, want, bound, "token")
+    assert layer.lengths == [6, 31] and layer.lens.tolist() == [6, 31]
+
+
 def test_landmark_states_of_the_same_prompts(cuda_device):
     """seal_prompts seals exactly what nys_seal seals group by group."""
     import torch
