@@ -598,6 +598,10 @@ class _Status:
         self._status = torch.zeros(1, dtype=torch.int32, device=device)
         self._status_ptr = self._status.data_ptr()
 
+    def share_status(self, other):
+        """Reports into other's status word from here on."""
+        self._status, self._status_ptr = other._status, other._status_ptr
+
     def status(self):
         """The status bits since the last clear (synchronises)."""
         return int(self._status.item())

@@ -13,7 +13,8 @@ of prompts of any lengths, and one-token decode.
     seal_prompts(states, q, k, v, lengths)    # landmark states of the same prompts
 
 Everything is enqueued on the current torch stream; the host only counts
-pages, so nothing waits for the GPU.
+pages, so nothing waits for the GPU.  What only the GPU can see (a wait that ran
+out, a page outside the pool) is in layer.status().
 """
 from __future__ import annotations
 
@@ -59,6 +60,15 @@ class ExactLayer:
         self.prefix_pages = None
         self._plans = {}
 
+    def status(self):
+        """The status bits (NYS_ATTN_*, NYS_PLAN_*) of all calls since the last clear;
+        synchronises.  Anything but 0 means that results are not to be used; a
+        server looks at it where it reads results anyway."""
+        return self.attention.status()
+
+    def clear_status(self):
+        self.attention.clear_status()
+
     def _check(self, q, k, v):
         """Refuses tensors that a call below would refuse, before anything is taken
         or counted."""
@@ -82,8 +92,9 @@ class ExactLayer:
         if max(a + b for a, b in zip(self.lengths, fresh)) > self.width * self.page:
             raise ValueError("a request would outgrow max_len")
         if total not in self._plans:
-            self._plans = {total: nys.PagePlan(self.requests, self.width, total, self.page,
-                                               device=self.device)}
+            plan = nys.PagePlan(self.requests, self.width, total, self.page, device=self.device)
+            plan.share_status(self.attention)
+            self._plans = {total: plan}
         plan = self._plans[total]
         # From pinned memory: a copy that the host does not wait for.
         grow = torch.tensor(fresh, dtype=torch.int32, pin_memory=True).to(self.device,

@@ -146,6 +146,26 @@ def test_layer_refuses_tensors_before_anything_is_counted(cuda_device, monkeypat
     assert layer.lengths == [6, 31] and layer.lens.tolist() == [6, 31]
 
 
+def test_layer_reports_what_its_calls_met(cuda_device):
+    """Bits of the attention's calls and of every plan, also of one that was
+    replaced since."""
+    import torch
+    from streaming_nystr_landmark_gb300 import nys, serving
+    layer = serving.ExactLayer(4, 2, 64, 64, 2, 16, 16, 64, device=cuda_device)
+    z = lambda n, h: torch.zeros(n, h, 64, device=cuda_device)
+    layer.admit(z(9, 4), z(9, 2), z(9, 2), [5, 4])
+    assert layer.status() == 0
+    layer.table[1, 0] = -1
+    layer._plan([0, 1])                 # the token's page is gone
+    layer._plan([1, 1])                 # another size of plan
+    assert layer.status() & nys.NYS_PLAN_NO_PAGES
+    layer.clear_status()
+    assert layer.status() == 0
+    layer.table[1, 0] = 1 << 20
+    layer.decode(z(2, 4), z(2, 2), z(2, 2))
+    assert layer.status() & nys.NYS_ATTN_BAD_PAGE
+
+
 def test_landmark_states_of_the_same_prompts(cuda_device):
     """seal_prompts seals exactly what nys_seal seals group by group."""
     import torch
