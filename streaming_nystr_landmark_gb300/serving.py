@@ -171,6 +171,8 @@ def seal_prompts(states, q, k, v, lengths, g0=0):
     g0 + i * kv_heads + j of `states`."""
     import torch
     rows, heads, d = q.shape
+    if not rows == k.shape[0] == v.shape[0] == sum(lengths):
+        raise ValueError("q, k and v must have as many rows as the lengths' sum")
     kv, group = k.shape[1], heads // k.shape[1]
     qs, ks, vs = [], [], []
     at = 0

@@ -188,3 +188,16 @@ def test_landmark_states_of_the_same_prompts(cuda_device):
         at += t
     for name in ("win_k", "sink_v", "k_tilde", "q_tilde", "mu", "t_hat", "z_hat", "m_max", "far_len"):
         assert torch.equal(both.region(name), each.region(name)), name
+
+
+def test_landmark_states_refuse_rows_without_a_length(cuda_device):
+    """Rows past the lengths' sum would be left out of every state in silence."""
+    import torch
+    from streaming_nystr_landmark_gb300 import nys, serving
+    q, k, v = (torch.zeros(200, h, 64, device=cuda_device) for h in (4, 2, 2))
+    states = nys.NystromStates(8, 16, 4, 2, 64, 64, 4, device=cuda_device)
+    for lens in ([80, 100], [80, 131]):
+        with pytest.raises(ValueError, match="rows"):
+            serving.seal_prompts(states, q, k, v, lens)
+    with pytest.raises(ValueError, match="rows"):
+        serving.seal_prompts(states, q, k, v[:-1], [80, 120])
