@@ -167,8 +167,8 @@ class ExactLayer:
 
 def seal_prompts(states, q, k, v, lengths, g0=0):
     """Seals landmark states on packed prompts (the tensors of
-    ExactLayer.admit, f32): request i's KV head j becomes group
-    g0 + i * kv_heads + j of `states`."""
+    ExactLayer.admit; 16-bit ones as the f32 values they hold, which the states
+    keep): request i's KV head j becomes group g0 + i * kv_heads + j of `states`."""
     import torch
     rows, heads, d = q.shape
     if not rows == k.shape[0] == v.shape[0] == sum(lengths):
@@ -182,5 +182,5 @@ def seal_prompts(states, q, k, v, lengths, g0=0):
         ks.append(k[cut].transpose(0, 1).reshape(-1, d))
         vs.append(v[cut].transpose(0, 1).reshape(-1, v.shape[2]))
         at += t
-    states.seal_ragged([t for t in lengths for _ in range(kv)], torch.cat(qs), torch.cat(ks),
-                       torch.cat(vs), g0=g0)
+    states.seal_ragged([t for t in lengths for _ in range(kv)], torch.cat(qs).float(),
+                       torch.cat(ks).float(), torch.cat(vs).float(), g0=g0)

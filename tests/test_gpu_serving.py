@@ -201,3 +201,20 @@ def test_landmark_states_refuse_rows_without_a_length(cuda_device):
             serving.seal_prompts(states, q, k, v, lens)
     with pytest.raises(ValueError, match="rows"):
         serving.seal_prompts(states, q, k, v[:-1], [80, 120])
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+def test_landmark_states_of_16_bit_prompts(cuda_device, dtype):
+    """The same states as of the values in f32."""
+    import torch
+    from streaming_nystr_landmark_gb300 import nys, serving
+    lens = [80, 131]
+    g = torch.Generator(device=cuda_device).manual_seed(2)
+    q, k, v = (torch.randn((sum(lens), h, 64), generator=g, device=cuda_device)
+               .to(getattr(torch, dtype)) for h in (4, 2, 2))
+    geo = (8, 16, 4, 2, 64, 64, 4)
+    a, b = (nys.NystromStates(*geo, device=cuda_device) for _ in range(2))
+    serving.seal_prompts(a, q, k, v, lens)
+    serving.seal_prompts(b, q.float(), k.float(), v.float(), lens)
+    for name in ("win_k", "sink_v", "k_tilde", "q_tilde", "t_hat", "z_hat"):
+        assert torch.equal(a.region(name), b.region(name)), name
