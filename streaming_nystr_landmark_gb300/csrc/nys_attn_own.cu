@@ -798,11 +798,6 @@ __global__ void __launch_bounds__(256) tail_join_kernel(const __grid_constant__ 
   }
 }
 
-template <typename K>
-cudaError_t allow(K kernel, int bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-}
-
 // Beside the prefix's launch where there is one; with a request's pieces as
 // clusters where they join themselves.
 cudaError_t launch_own_kernel(void (*kernel)(SharedArgs, OwnArgs), dim3 grid, size_t smem,
@@ -828,14 +823,14 @@ cudaError_t launch_own_kernel(void (*kernel)(SharedArgs, OwnArgs), dim3 grid, si
 
 template <int HT>
 cudaError_t launch32(const SharedArgs& a, const OwnArgs& o, cudaStream_t stream) {
-  static const cudaError_t ready = allow(own32_kernel<HT>, kSmem32);
+  const cudaError_t ready = ensure_smem<own32_kernel<HT>>(kSmem32);
   if (ready != cudaSuccess) return ready;
   const dim3 grid((unsigned)(a.n * o.pieces), (unsigned)(a.kv_heads * ((a.group + HT - 1) / HT)));
   return launch_own_kernel(own32_kernel<HT>, grid, kSmem32, stream, a, o);
 }
 template <typename T>
 cudaError_t launch16(const SharedArgs& a, const OwnArgs& o, cudaStream_t stream) {
-  static const cudaError_t ready = allow(own16_kernel<T>, kSmem16);
+  const cudaError_t ready = ensure_smem<own16_kernel<T>>(kSmem16);
   if (ready != cudaSuccess) return ready;
   const dim3 grid((unsigned)(a.n * o.pieces),
                   (unsigned)(a.kv_heads * ((a.group + kHeads16 - 1) / kHeads16)));

@@ -731,13 +731,8 @@ attn_tc_kernel(const __grid_constant__ TileArgs a, const __grid_constant__ CUten
 
 template <typename T, bool PAGED>
 cudaError_t launch_t(const TileArgs& a, const TileMaps& m, unsigned grid, cudaStream_t stream) {
-  static bool ready = false;
-  if (!ready) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        attn_tc_kernel<T, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-    if (e != cudaSuccess) return e;
-    ready = true;
-  }
+  const cudaError_t ready = ensure_smem<attn_tc_kernel<T, PAGED>>(kSmem);
+  if (ready != cudaSuccess) return ready;
   attn_tc_kernel<T, PAGED><<<grid, kThreads, kSmem, stream>>>(a, m.q, m.k, m.v);
   return cudaGetLastError();
 }

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "nys_attn.h"
+#include "nys_device.h"
 #include "nys_tc.h"
 
 namespace nys {

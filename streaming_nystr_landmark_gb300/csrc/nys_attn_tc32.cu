@@ -851,8 +851,7 @@ attn_tc32_kernel(const __grid_constant__ TileArgs a) {
 
 template <bool PAGED>
 cudaError_t launch_t(const TileArgs& a, unsigned grid, cudaStream_t stream) {
-  static const cudaError_t ready = cudaFuncSetAttribute(
-      attn_tc32_kernel<PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  const cudaError_t ready = ensure_smem<attn_tc32_kernel<PAGED>>(kSmem);
   if (ready != cudaSuccess) return ready;
   const dim3 images((unsigned)(key_tiles(a.k_rows, a.k_off ? a.n : 1) * a.kv_heads), 2);
   split_kernel<PAGED><<<images, 256, 0, stream>>>(a);
