@@ -559,11 +559,17 @@ def _dtype_code(dtype):
     return codes[dtype]
 
 
-def _rows(t, dtype, heads, dim, where):
+def _wrong_place(t, dtype, where, index):
+    if t.dtype is dtype and t.is_cuda:
+        raise ValueError(f"{where}: on cuda:{t.get_device()}, need cuda:{index}")
+    raise ValueError(f"{where}: need a CUDA {dtype} tensor")
+
+
+def _rows(t, dtype, heads, dim, where, index=None):
     """A [rows][heads][dim] CUDA tensor as NysRows: any row and head strides,
-    the last dimension contiguous."""
-    if t.dtype is not dtype or not t.is_cuda:
-        raise ValueError(f"{where}: need a CUDA {dtype} tensor")
+    the last dimension contiguous; on device `index`, if given."""
+    if t.dtype is not dtype or (not t.is_cuda if index is None else t.get_device() != index):
+        _wrong_place(t, dtype, where, index)
     shape, st = t.shape, t.stride()
     if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
         raise ValueError(f"{where}: shape {tuple(shape)} != (rows, {heads}, {dim})")
@@ -572,26 +578,40 @@ def _rows(t, dtype, heads, dim, where):
     return NysRows(t.data_ptr(), st[0], st[1])
 
 
-def _ints(t, dtype, shape, where):
-    """Address of a contiguous CUDA tensor of this type and shape."""
-    if t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous():
-        return t.data_ptr()
-    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+def _ints(t, dtype, shape, where, index=None):
+    """Address of a contiguous CUDA tensor of this type and shape, on device
+    `index`, if given."""
+    if t.dtype is not dtype or (not t.is_cuda if index is None else t.get_device() != index):
+        _wrong_place(t, dtype, where, index)
+    if t.shape != shape:
+        raise ValueError(f"{where}: shape {tuple(t.shape)} != {tuple(shape)}")
+    if not t.is_contiguous():
         raise ValueError(f"{where}: need a contiguous CUDA {dtype} tensor")
-    raise ValueError(f"{where}: shape {tuple(t.shape)} != {tuple(shape)}")
+    return t.data_ptr()
 
 
-def _current_stream(device):
-    """The device's current torch stream as an address (what
-    torch.cuda.current_stream(device).cuda_stream gives, without making an
-    object: 0.1 us against 3.5)."""
+def _cuda_device(device):
+    """A torch.device with its index: "cuda" is the device current now."""
     import torch
-    index = device.index
-    return torch._C._cuda_getCurrentRawStream(
-        torch.cuda.current_device() if index is None else index)
+    device = torch.device(device)
+    if device.type == "cuda" and device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    return device
 
 
-class _Status:
+class _OnDevice:
+    """Calls are made with the object's device current (a legacy default stream is
+    the current device's, whatever the tensors are), on its current torch stream,
+    whose address _stream() gives without making an object: 0.1 us against 3.5."""
+
+    def _elsewhere(self):
+        return self.torch._C._cuda_getDevice() != self.device.index
+
+    def _stream(self):
+        return self.torch._C._cuda_getCurrentRawStream(self.device.index)
+
+
+class _Status(_OnDevice):
     """A device status word that kernels set bits of (NYS_ATTN_*, NYS_PLAN_*)."""
 
     def _init_status(self, torch, device):
@@ -610,7 +630,7 @@ class _Status:
         self._status.zero_()
 
 
-class PagedKV:
+class PagedKV(_OnDevice):
     """A pool of KV pages of one layer: k [n_pages][page][kv_heads][d],
     v [..][dv], allocated here or given.  Page numbers come from a PagePlan."""
 
@@ -618,7 +638,7 @@ class PagedKV:
         import torch
         self.torch = torch
         self.dtype = torch.float32 if dtype is None else dtype
-        self.device = torch.device(device)
+        self.device = _cuda_device(device)
         self.n_pages, self.page = n_pages, page
         self.kv_heads, self.d, self.dv = kv_heads, d, dv
         make = lambda c: torch.empty((n_pages, page, kv_heads, c), dtype=self.dtype,
@@ -627,23 +647,27 @@ class PagedKV:
         self.v = make(dv) if v is None else v
         for name, t, c in (("k", self.k, d), ("v", self.v, dv)):
             if (t.dtype != self.dtype or not t.is_cuda or not t.is_contiguous()
-                    or tuple(t.shape) != (n_pages, page, kv_heads, c)):
-                raise ValueError(f"{name}: need a contiguous CUDA {self.dtype} tensor of shape "
-                                 f"{(n_pages, page, kv_heads, c)}")
+                    or tuple(t.shape) != (n_pages, page, kv_heads, c)
+                    or t.get_device() != self.device.index):
+                raise ValueError(f"{name}: need a contiguous {self.dtype} tensor of shape "
+                                 f"{(n_pages, page, kv_heads, c)} on {self.device}")
         self._cfg = NysAttnConfig(kv_heads, kv_heads, d, dv, _dtype_code(self.dtype), 0.0)
         self._pool = NysPool(self.k.data_ptr(), self.v.data_ptr(), n_pages, page)
 
     def write(self, k, v, slots):
         """Rows k [tokens][kv_heads][d], v [..][dv] into slots int64 [tokens];
         a slot of -1 is skipped."""
-        torch = self.torch
+        torch, index = self.torch, self.device.index
+        if self._elsewhere():
+            with torch.cuda.device(index):
+                return self.write(k, v, slots)
         n = k.shape[0]
         if v.shape[0] != n:
             raise ValueError(f"v: {v.shape[0]} rows, k has {n}")
-        nys_kv_write(self._cfg, self._pool, n, _rows(k, self.dtype, self.kv_heads, self.d, "k"),
-                     _rows(v, self.dtype, self.kv_heads, self.dv, "v"),
-                     _ints(slots, torch.int64, (n,), "slots"),
-                     _current_stream(self.device))
+        nys_kv_write(self._cfg, self._pool, n,
+                     _rows(k, self.dtype, self.kv_heads, self.d, "k", index),
+                     _rows(v, self.dtype, self.kv_heads, self.dv, "v", index),
+                     _ints(slots, torch.int64, (n,), "slots", index), self._stream())
 
 
 class PagePlan(_Status):
@@ -656,7 +680,7 @@ class PagePlan(_Status):
     def __init__(self, n, width, total, page, device="cuda"):
         import torch
         self.torch = torch
-        self.device = torch.device(device)
+        self.device = _cuda_device(device)
         self.n, self.width, self.total, self.page = n, width, total, page
         make = lambda size, dt: torch.empty(size, dtype=dt, device=self.device)
         self.q_off = make(n + 1, torch.int32)
@@ -672,13 +696,15 @@ class PagePlan(_Status):
         """cached, fresh int32 [n]; free_pages int32 [any]; table int32
         [n][width], whose new columns are filled in place.  cached may be this
         plan's lens, which then grows in place."""
-        i32 = self.torch.int32
-        nys_kv_plan(self.n, self.page, _ints(cached, i32, (self.n,), "cached"),
-                    _ints(fresh, i32, (self.n,), "fresh"),
-                    _ints(free_pages, i32, free_pages.shape[:1], "free_pages"), free_pages.shape[0],
-                    _ints(table, i32, (self.n, self.width), "table"), self.width, self.total,
-                    *self._out, self._status_ptr,
-                    _current_stream(self.device))
+        i32, index = self.torch.int32, self.device.index
+        if self._elsewhere():
+            with self.torch.cuda.device(index):
+                return self.update(cached, fresh, free_pages, table)
+        nys_kv_plan(self.n, self.page, _ints(cached, i32, (self.n,), "cached", index),
+                    _ints(fresh, i32, (self.n,), "fresh", index),
+                    _ints(free_pages, i32, free_pages.shape[:1], "free_pages", index),
+                    free_pages.shape[0], _ints(table, i32, (self.n, self.width), "table", index),
+                    self.width, self.total, *self._out, self._status_ptr, self._stream())
         return self
 
 
@@ -694,7 +720,7 @@ class ExactAttention(_Status):
         import torch
         self.torch = torch
         self.dtype = torch.float32 if dtype is None else dtype
-        self.device = torch.device(device)
+        self.device = _cuda_device(device)
         self.heads, self.kv_heads, self.d, self.dv = heads, kv_heads, d, dv
         self.cfg = NysAttnConfig(heads, kv_heads, d, dv, _dtype_code(self.dtype),
                                  0.0 if scale is None else scale)
@@ -732,47 +758,53 @@ class ExactAttention(_Status):
         """Packed causal attention (nys_attn_prompt): q [rows][heads][d], k and
         v [keys][kv_heads][d|dv], q_off and k_off int32 [n+1]; writes out
         [rows][heads][dv] and, if given, lse fp32 [rows][heads]."""
-        torch = self.torch
+        torch, index = self.torch, self.device.index
+        if self._elsewhere():
+            with torch.cuda.device(index):
+                return self.prompt(q, k, v, q_off, out, k_off, lse)
         n, rows, keys = q_off.shape[0] - 1, q.shape[0], k.shape[0]
         if v.shape[0] != keys or out.shape[0] != rows:
             raise ValueError("k and v, and q and out, must have as many rows as each other")
         self._workspace(n, rows, keys)
         nys_attn_prompt(
-            self.cfg, n, rows, keys, _ints(q_off, torch.int32, (n + 1,), "q_off"),
-            None if k_off is None else _ints(k_off, torch.int32, (n + 1,), "k_off"),
-            _rows(q, self.dtype, self.heads, self.d, "q"),
-            _rows(k, self.dtype, self.kv_heads, self.d, "k"),
-            _rows(v, self.dtype, self.kv_heads, self.dv, "v"),
-            _rows(out, self.dtype, self.heads, self.dv, "out"),
-            None if lse is None else _ints(lse, torch.float32, (rows, self.heads), "lse"),
-            self._work_ptr, self._work_bytes, self._status_ptr,
-            _current_stream(self.device))
+            self.cfg, n, rows, keys, _ints(q_off, torch.int32, (n + 1,), "q_off", index),
+            None if k_off is None else _ints(k_off, torch.int32, (n + 1,), "k_off", index),
+            _rows(q, self.dtype, self.heads, self.d, "q", index),
+            _rows(k, self.dtype, self.kv_heads, self.d, "k", index),
+            _rows(v, self.dtype, self.kv_heads, self.dv, "v", index),
+            _rows(out, self.dtype, self.heads, self.dv, "out", index),
+            None if lse is None else _ints(lse, torch.float32, (rows, self.heads), "lse", index),
+            self._work_ptr, self._work_bytes, self._status_ptr, self._stream())
         return out
 
     def shared(self, q, cache, lens, table, out, prefix_pages=None, prefix_len=0, lse=None):
         """One token for each of n requests (nys_attn_shared): q [n][heads][d]
         over the prefix's keys and lens[b] own keys in cache's pages table[b]
         (lens int32 [n], table int32 [n][width]); writes out [n][heads][dv]."""
-        torch = self.torch
+        torch, index = self.torch, self.device.index
+        if self._elsewhere():
+            with torch.cuda.device(index):
+                return self.shared(q, cache, lens, table, out, prefix_pages, prefix_len, lse)
         n = q.shape[0]
         if (cache.dtype != self.dtype or cache.kv_heads != self.kv_heads or cache.d != self.d
                 or cache.dv != self.dv):
             raise ValueError("the cache's geometry is not this attention's")
+        if cache.device.index != index:
+            raise ValueError(f"the cache is on {cache.device}, this attention on {self.device}")
         if out.shape[0] != n or len(table.shape) != 2:
             raise ValueError("out must have q's rows, and table be [n][width]")
         pages = None
         if prefix_len > 0:
-            pages = _ints(prefix_pages, torch.int32, prefix_pages.shape[:1], "prefix_pages")
+            pages = _ints(prefix_pages, torch.int32, prefix_pages.shape[:1], "prefix_pages", index)
             if prefix_pages.shape[0] * cache.page < prefix_len:
                 raise ValueError("prefix_pages: too few pages for prefix_len")
         self._workspace(n, n, prefix_len)
         nys_attn_shared(
             self.cfg, n, cache._pool, pages, prefix_len,
-            _ints(lens, torch.int32, (n,), "lens"),
-            _ints(table, torch.int32, (n, table.shape[1]), "table"), table.shape[1],
-            _rows(q, self.dtype, self.heads, self.d, "q"),
-            _rows(out, self.dtype, self.heads, self.dv, "out"),
-            None if lse is None else _ints(lse, torch.float32, (n, self.heads), "lse"),
-            self._work_ptr, self._work_bytes, self._status_ptr,
-            _current_stream(self.device))
+            _ints(lens, torch.int32, (n,), "lens", index),
+            _ints(table, torch.int32, (n, table.shape[1]), "table", index), table.shape[1],
+            _rows(q, self.dtype, self.heads, self.d, "q", index),
+            _rows(out, self.dtype, self.heads, self.dv, "out", index),
+            None if lse is None else _ints(lse, torch.float32, (n, self.heads), "lse", index),
+            self._work_ptr, self._work_bytes, self._status_ptr, self._stream())
         return out

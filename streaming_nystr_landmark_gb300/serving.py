@@ -44,10 +44,10 @@ class ExactLayer:
                  scale=None, device="cuda"):
         import torch
         self.torch = torch
-        self.device = torch.device(device)
+        self.device = nys._cuda_device(device)
         self.attention = nys.ExactAttention(heads, kv_heads, d, dv, dtype=dtype, scale=scale,
-                                            device=device)
-        self.cache = nys.PagedKV(n_pages, page, kv_heads, d, dv, dtype=dtype, device=device)
+                                            device=self.device)
+        self.cache = nys.PagedKV(n_pages, page, kv_heads, d, dv, dtype=dtype, device=self.device)
         self.requests, self.page = requests, page
         self.width = -(-max_len // page)
         i32 = dict(dtype=torch.int32, device=self.device)
@@ -72,11 +72,11 @@ class ExactLayer:
     def _check(self, q, k, v):
         """Refuses tensors that a call below would refuse, before anything is taken
         or counted."""
-        att = self.attention
+        att, index = self.attention, self.device.index
         if q is not None:
-            nys._rows(q, att.dtype, att.heads, att.d, "q")
-        nys._rows(k, att.dtype, att.kv_heads, att.d, "k")
-        nys._rows(v, att.dtype, att.kv_heads, att.dv, "v")
+            nys._rows(q, att.dtype, att.heads, att.d, "q", index)
+        nys._rows(k, att.dtype, att.kv_heads, att.d, "k", index)
+        nys._rows(v, att.dtype, att.kv_heads, att.dv, "v", index)
         if v.shape[0] != k.shape[0]:
             raise ValueError(f"v: {v.shape[0]} rows, k has {k.shape[0]}")
 

@@ -177,3 +177,120 @@ def test_tensor_checks_of_the_wrapper():
 def test_error_names_the_call():
     with pytest.raises(nys.NysError, match="nys_kv_plan"):
         nys.nys_kv_plan(-1, 16, A, A, A, 1, A, 1, 1, A, A, A, A, A)
+
+
+class _Tensor:
+    """Stands for a CUDA tensor on a device that need not be there."""
+
+    def __init__(self, shape, dtype, index):
+        self.shape, self.dtype, self.index, self.is_cuda = shape, dtype, index, True
+
+    def stride(self):
+        out, step = [], 1
+        for n in reversed(self.shape):
+            out.insert(0, step)
+            step *= n
+        return out
+
+    def get_device(self):
+        return self.index
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return A
+
+
+class _Device:
+    """Stands for torch on a machine with two GPUs: notes which one is current."""
+
+    def __init__(self, monkeypatch):
+        import torch
+        self.now, self.calls = 0, []
+        outer = self
+
+        class device:
+            def __init__(self, index):
+                self.index = index
+
+            def __enter__(self):
+                self.was, outer.now = outer.now, self.index
+
+            def __exit__(self, *a):
+                outer.now = self.was
+
+        class cuda:
+            @staticmethod
+            def is_current_stream_capturing():
+                return False
+        cuda.device = device
+        self.cuda = cuda
+        for name in ("int32", "int64", "float32", "uint8"):
+            setattr(self, name, getattr(torch, name))
+        self.empty = lambda n, dtype, device: _Tensor((n,), dtype, device.index)
+        self._C = type("_C", (), dict(_cuda_getDevice=lambda: self.now,
+                                      _cuda_getCurrentRawStream=lambda index: 1000 + index))
+        for name in ("nys_attn_prompt", "nys_attn_shared", "nys_kv_plan", "nys_kv_write"):
+            monkeypatch.setattr(nys, name, lambda *a, name=name: self.calls.append(
+                (name, self.now, a[-1])))
+
+
+def _objects(monkeypatch, index):
+    torch = pytest.importorskip("torch")
+    fake, dev = _Device(monkeypatch), torch.device("cuda", index)
+    att = nys.ExactAttention.__new__(nys.ExactAttention)
+    vars(att).update(torch=fake, device=dev, dtype=torch.float32, heads=2, kv_heads=2, d=8, dv=8,
+                     cfg=nys.NysAttnConfig(2, 2, 8, 8, nys.NYS_F32, 0.0), _work=None,
+                     _work_ptr=None, _work_bytes=0, _sizes=None, _captured=False, _held=[],
+                     _status_ptr=A)
+    cache = nys.PagedKV.__new__(nys.PagedKV)
+    vars(cache).update(torch=fake, device=dev, dtype=torch.float32, kv_heads=2, d=8, dv=8, page=4,
+                       n_pages=2, _cfg=att.cfg, _pool=nys.NysPool(A, A, 2, 4))
+    plan = nys.PagePlan.__new__(nys.PagePlan)
+    vars(plan).update(torch=fake, device=dev, n=3, width=2, total=3, page=4, _out=[A] * 5,
+                      _status_ptr=A)
+    f = lambda *s, i=index: _Tensor(s, torch.float32, i)
+    i32 = lambda *s, i=index: _Tensor(s, torch.int32, i)
+    i64 = lambda *s, i=index: _Tensor(s, torch.int64, i)
+    calls = {
+        "nys_attn_prompt": (att.prompt, [f(3, 2, 8), f(3, 2, 8), f(3, 2, 8), i32(2), f(3, 2, 8),
+                                         i32(2), f(3, 2)]),
+        "nys_attn_shared": (att.shared, [f(3, 2, 8), cache, i32(3), i32(3, 2), f(3, 2, 8), i32(2),
+                                         5, f(3, 2)]),
+        "nys_kv_plan": (plan.update, [i32(3), i32(3), i32(4), i32(3, 2)]),
+        "nys_kv_write": (cache.write, [f(3, 2, 8), f(3, 2, 8), i64(3)]),
+    }
+    return fake, calls
+
+
+@pytest.mark.parametrize("name", ["nys_attn_prompt", "nys_attn_shared", "nys_kv_plan",
+                                  "nys_kv_write"])
+def test_calls_run_on_their_objects_device(monkeypatch, name):
+    """Whichever device is current: a legacy default stream is the current device's,
+    whatever the tensors are."""
+    for index in (0, 1):
+        fake, calls = _objects(monkeypatch, index)
+        fn, args = calls[name]
+        fn(*args)
+        assert fake.calls == [(name, index, 1000 + index)] and fake.now == 0
+
+
+@pytest.mark.parametrize("name", ["nys_attn_prompt", "nys_attn_shared", "nys_kv_plan",
+                                  "nys_kv_write"])
+def test_tensors_of_another_device_are_refused(monkeypatch, name):
+    fake, calls = _objects(monkeypatch, 1)
+    fn, args = calls[name]
+    for i, a in enumerate(args):
+        if not isinstance(a, _Tensor):
+            continue
+        a.index = 0
+        with pytest.raises(ValueError, match="cuda:0"):
+            fn(*args)
+        a.index = 1
+    if name == "nys_attn_shared":
+        import torch
+        args[1].device = torch.device("cuda", 0)
+        with pytest.raises(ValueError, match="cuda:0"):
+            fn(*args)
+    assert fake.calls == []
