@@ -43,8 +43,9 @@
 // each), two S and one O of 128 columns; P hi and lo take S's place, 8 columns
 // each for 16 keys.
 //
-// Values that are not finite are 0 in the images and flagged by tile: the
-// epilogue adds them to the rows that see their keys, and no others.
+// Values that are not finite are 0 in the images and flagged by group: units that
+// read a flagged tile leave their results to the query warps, which compute them in
+// f32 from the tensors (exact_rows).
 //
 // Every wait is bounded (2 s), as in nys_attn_tc.cu.
 #include <cmath>
@@ -89,12 +90,12 @@ struct Shared {
   uint64_t u_full[kUnitRing], u_empty[kUnitRing], patch_full[kUnitRing];
   uint64_t drain;
   Unit unit[kUnitRing];
-  int patch[kUnitRing];  // results need values that are not finite added
+  int patch[kUnitRing];  // results are computed in f32 by the query warps (exact_rows)
   alignas(16) TileExps exps[4];      // of tile & 3
   int8_t q_exp[4][kTileM];           // eq, [unit & 3][row]: the query warps run up to three units ahead
   float mx[2][2][kTileM];            // halves' maxima [exchange & 1][half][row], also of l
   uint32_t tmem;
-  int abort;
+  Beats beats;
 };
 constexpr uint32_t kSmem = kTiles + sizeof(Shared);
 static_assert(kSmem <= 227 * 1024, "one CTA's shared memory");
@@ -110,7 +111,7 @@ __device__ __forceinline__ bool finite_bits(float x) {
 
 // ---- copies (one thread)
 __device__ void load_role(const TileArgs& a, Shared& sh, unsigned char* sm) {
-  volatile int* ab = &sh.abort;
+  volatile Beats* ab = &sh.beats;
   uint32_t cnt = 0, tile = 0;
   const uint32_t kb = (uint32_t)((a.d + 63) / 64) * 16384u, vb = (uint32_t)((a.dv + 63) / 64) * 16384u;
   bool ok = true;
@@ -151,8 +152,8 @@ __device__ void load_role(const TileArgs& a, Shared& sh, unsigned char* sm) {
     tile += (uint32_t)nt;
   }
   // Copies in flight land before the CTA may leave.
-  if (*ab) {
-    int none = 0;
+  if (ab->abort) {
+    Beats none{};
     for (uint32_t c = cnt > kSlots ? cnt - kSlots : 0; c < cnt; ++c)
       bar_wait(&sh.kv_full[c % kSlots], (c / kSlots) & 1, &none);
   }
@@ -217,15 +218,138 @@ __device__ __forceinline__ float finite_max(float4 x) {
   return f;
 }
 
+// Results of this warp's 32 rows of a unit in f32 throughout, from the tensors
+// themselves: for units that hold what the fp16 pieces do not.  Every row reads the
+// keys that it sees and no others.  Eight rows at a time, two keys a step, which come
+// through shared memory (`turn`) and are asked for a step ahead: four lanes have a
+// row, each a quarter of its columns.  Right for everything and fast for nothing: 64
+// prompts of 256 with a flag each take 3.3 ms (159 us without), 4 of 4,096 61 ms (0.56
+// ms).  Its beats tell the waiting warps that it goes on.  (A call: inlined, its code costs the
+// tiles 1%, 64 prompts of 256 158.8 -> 160.5 us.)
 template <bool PAGED>
-__device__ __forceinline__ const float* value_row(const TileArgs& a, const Unit& u, int j) {
-  int64_t row = (int64_t)u.k_row + j;
-  if (PAGED) {
-    const int32_t pg = a.pages[j / a.page];
-    if (pg < 0 || pg >= a.n_pages) return nullptr;
-    row = (int64_t)pg * a.page + j % a.page;
+__device__ __noinline__ void exact_rows(const TileArgs& a, const Unit& u, unsigned char* turn,
+                                        int warp, int lane, volatile Beats* beats) {
+  constexpr int kKeys = 2, kCols = 8;  // keys of a step; pieces of four columns of a lane
+  static_assert(kTurn == kKeys * 2 * 512, "the keys and values of a step");
+  const float sc = a.scale * kLog2e;
+  const int d = a.d, dv = a.dv, page = a.page, kb = u.kb, c0 = (lane & 3) * 4;
+  const int64_t k_step = a.k_row, v_step = a.v_row, first = u.k_row, n_pages = a.n_pages;
+  const int32_t* pages = a.pages;
+  const float* k_lane = (const float*)a.k_raw + u.kvh * a.k_head + lane * 4;
+  const float* v_lane = (const float*)a.v_raw + u.kvh * a.v_head + lane * 4;
+  const bool k_col = lane * 4 < d, v_col = lane * 4 < dv;
+  float4* mine = reinterpret_cast<float4*>(turn) + lane;           // [key or value][512 bytes]
+  const float4* quarter = reinterpret_cast<const float4*>(turn) + (lane & 3);
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  // Row of key j of the piece; -1 where its page is not in the pool.
+  auto key_row = [&](int j) {
+    j += kb;
+    if (!PAGED) return first + j;
+    const int32_t pg = pages[j / page];
+    return pg < 0 || pg >= n_pages ? (int64_t)-1 : (int64_t)pg * page + j % page;
+  };
+#pragma unroll 1
+  for (int r0 = warp * 32; r0 < warp * 32 + 32; r0 += 8) {
+    if (r0 / a.group >= u.np0) return;
+    const int row = r0 + (lane >> 2), pos = row / a.group, h = u.kvh * a.group + (row - pos * a.group);
+    const bool here = pos < u.np0;
+    const int lim = here ? min(a.causal ? u.lim + pos : u.lim, u.nkl) - kb : 0;
+    const int most = __reduce_max_sync(0xffffffffu, lim);
+    uint64_t q[2 * kCols], acc[2 * kCols];
+    const float* src = (const float*)a.q.p + (u.q_row + (int64_t)pos) * a.q.row + h * a.q.head + c0;
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) {
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (here && c * 16 + c0 < d) x = __ldg(reinterpret_cast<const float4*>(src + c * 16));
+      q[2 * c] = pair(x.x * sc, x.y * sc);
+      q[2 * c + 1] = pair(x.z * sc, x.w * sc);
+      acc[2 * c] = acc[2 * c + 1] = pair(0.f, 0.f);
+    }
+    float m = -INFINITY, l = 0.f;
+    float4 kx[kKeys], vx[kKeys];
+    auto ask = [&](int k0) {
+#pragma unroll
+      for (int j = 0; j < kKeys; ++j) {
+        const int64_t o = k0 + j < most ? key_row(k0 + j) : -1;
+        kx[j] = o >= 0 && k_col ? __ldg(reinterpret_cast<const float4*>(k_lane + o * k_step)) : zero;
+        vx[j] = o >= 0 && v_col ? __ldg(reinterpret_cast<const float4*>(v_lane + o * v_step)) : zero;
+      }
+    };
+    ask(0);
+#pragma unroll 1
+    for (int k0 = 0; k0 < most; k0 += kKeys) {
+      if (lane == 0 && !(k0 & 2047)) beats->beat = now_ns();
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < kKeys; ++j) {
+        mine[j * 32] = kx[j];
+        mine[(kKeys + j) * 32] = vx[j];
+      }
+      __syncwarp();
+      ask(k0 + kKeys);
+      uint64_t sum[kKeys];
+#pragma unroll
+      for (int j = 0; j < kKeys; ++j) sum[j] = pair(0.f, 0.f);
+#pragma unroll
+      for (int c = 0; c < kCols; ++c)
+#pragma unroll
+        for (int j = 0; j < kKeys; ++j) {
+          const float4 x = quarter[j * 32 + c * 4];
+          sum[j] = fma2(q[2 * c], pair(x.x, x.y), sum[j]);
+          sum[j] = fma2(q[2 * c + 1], pair(x.z, x.w), sum[j]);
+        }
+      float y[kKeys], top = m;
+#pragma unroll
+      for (int j = 0; j < kKeys; ++j) {
+        float y0, y1;
+        unpair(sum[j], y0, y1);
+        y0 += y1;
+        y0 += __shfl_xor_sync(0xffffffffu, y0, 1);
+        y0 += __shfl_xor_sync(0xffffffffu, y0, 2);
+        y[j] = k0 + j < lim ? y0 : -INFINITY;
+        top = fmaxf(top, y[j]);
+      }
+      const float f = top == m ? 1.f : ex2(m - top);
+      m = top;
+      l *= f;
+#pragma unroll
+      for (int j = 0; j < kKeys; ++j) {
+        y[j] = ex2(y[j] - (m == -INFINITY ? 0.f : m));
+        l += y[j];
+      }
+      if (__any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll
+        for (int c = 0; c < 2 * kCols; ++c) acc[c] = mul2(acc[c], pair(f, f));
+      }
+#pragma unroll
+      for (int j = 0; j < kKeys; ++j)
+        if (k0 + j < lim) {  // (0 x NaN is NaN)
+#pragma unroll
+          for (int c = 0; c < kCols; ++c) {
+            const float4 x = quarter[(kKeys + j) * 32 + c * 4];
+            acc[2 * c] = fma2(pair(y[j], y[j]), pair(x.x, x.y), acc[2 * c]);
+            acc[2 * c + 1] = fma2(pair(y[j], y[j]), pair(x.z, x.w), acc[2 * c + 1]);
+          }
+        }
+    }
+    if (!here) continue;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int64_t part_row = (int64_t)u.slot * kTileM + row, orow = u.q_row + (int64_t)pos;
+    float* out = (u.slot >= 0 ? a.part + part_row * dv : (float*)a.out.p + orow * a.out.row + h * a.out.head) + c0;
+#pragma unroll
+    for (int c = 0; c < kCols; ++c)
+      if (c * 16 + c0 < dv) {
+        float4 y;
+        unpair(acc[2 * c], y.x, y.y);
+        unpair(acc[2 * c + 1], y.z, y.w);
+        *reinterpret_cast<float4*>(out + c * 16) = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+      }
+    const float lse = l == 0.f ? -INFINITY : fmaf(m, kLn2, logf(l));
+    if ((lane & 3) == 0) {
+      if (u.slot >= 0) a.part_lse[part_row] = lse;
+      else if (a.lse) a.lse[orow * a.heads + h] = lse;
+    }
   }
-  return (const float*)a.v_raw + row * a.v_row + u.kvh * a.v_head;
 }
 
 // The query tile into tensor memory, and the results out of it (four warps, 32
@@ -236,7 +360,7 @@ __device__ __forceinline__ const float* value_row(const TileArgs& a, const Unit&
 template <bool PAGED>
 __device__ void query_role(const TileArgs& a, Shared& sh, unsigned char* turn, uint32_t tmem,
                            int warp, int lane) {
-  volatile int* ab = &sh.abort;
+  volatile Beats* ab = &sh.beats;
   const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
   const int sub = lane & 3;  // 4 columns of a chunk of 16
   int pos[4], hd[4];
@@ -258,6 +382,15 @@ __device__ void query_role(const TileArgs& a, Shared& sh, unsigned char* turn, u
       if (!bar_wait_warp(&sh.r_full, n_r & 1, ab)) return false;
       ++n_r;
       fence_after();
+    }
+    if (sh.patch[at]) {  // (a unit with tiles: nobody reads its O, whose next use may begin)
+      fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(&sh.o_empty, 2);
+      exact_rows<PAGED>(a, u, turn, warp, lane, ab);
+      __syncwarp();
+      if (lane == 0) bar_arrive(&sh.u_empty[at]);
+      return true;
     }
     float* to[4];
 #pragma unroll
@@ -295,24 +428,6 @@ __device__ void query_role(const TileArgs& a, Shared& sh, unsigned char* turn, u
       }
     }
     fence_before();
-    if (sh.patch[at]) {
-      __syncwarp();  // the row's results are there
-      const int row = warp * 32 + lane, p = row / a.group, h = row - p * a.group + u.kvh * a.group;
-      const int lim = min(a.causal ? u.lim + p : u.lim, u.nkl) - u.kb;
-      if (p < u.np0) {
-        float* out = u.slot >= 0 ? a.part + (part_row + lane) * a.dv
-                              : (float*)a.out.p + (u.q_row + (int64_t)p) * a.out.row + h * a.out.head;
-        for (int k = 0; k < lim; ++k) {
-          const int64_t im = (int64_t)(u.tile + k / kTileN) * a.kv_heads + u.kvh;
-          if (!a.odd[im * kGroups + k % kTileN / kGroup]) {
-            k |= kGroup - 1;  // on to the next group
-            continue;
-          }
-          const float* v = value_row<PAGED>(a, u, u.kb + k);
-          if (v) add_unusual(out, v, 0, a.dv);
-        }
-      }
-    }
     __syncwarp();
     if (lane == 0) {
       if (u.nt > 0) bar_arrive(&sh.o_empty, 2);  // eight arrivals free O
@@ -488,7 +603,7 @@ __global__ void __launch_bounds__(256) split_kernel(const __grid_constant__ Tile
 
 // ---- products (one thread)
 __device__ void mma_role(const TileArgs& a, Shared& sh, unsigned char* sm, uint32_t tmem) {
-  volatile int* ab = &sh.abort;
+  volatile Beats* ab = &sh.beats;
   const int ks = (a.d + 15) / 16;
   const int nv = (a.dv + 15) & ~15;
   const uint32_t id_s = idesc(kTileM, kTileN, false, false);
@@ -550,13 +665,13 @@ __device__ void mma_role(const TileArgs& a, Shared& sh, unsigned char* sm, uint3
     }
     base += 2 * (uint32_t)nt;
   }
-  int none = 0;
+  Beats none{};
   commit(&sh.drain);
   bar_wait(&sh.drain, 0, &none);
 }
 
 __device__ void unit_role(const TileArgs& a, Shared& sh, UnitSource& source, int lane) {
-  volatile int* ab = &sh.abort;
+  volatile Beats* ab = &sh.beats;
   int last_nt = 0;
   for (uint32_t nu = 0;; ++nu) {
     if (!bar_wait_warp(&sh.u_empty[nu % kUnitRing], ((nu / kUnitRing) & 1) ^ 1, ab)) return;
@@ -596,7 +711,7 @@ __device__ void unit_role(const TileArgs& a, Shared& sh, UnitSource& source, int
 // `half` takes keys 64 * half .. of each tile and value columns 64 * half ..)
 __device__ void row_role(const TileArgs& a, Shared& sh, uint32_t tmem, int row, int half,
                          int lane) {
-  volatile int* ab = &sh.abort;
+  volatile Beats* ab = &sh.beats;
   const float sc = a.scale * kLog2e;
   const int pos = row / a.group, hd = row - pos * a.group;
   const uint32_t at = tmem + ((uint32_t)(row & ~31) << 16);
@@ -768,7 +883,8 @@ __device__ void row_role(const TileArgs& a, Shared& sh, uint32_t tmem, int row, 
       __syncwarp();
       if (lane == 0) bar_arrive(&sh.r_full);
     }
-    if (half == 0 && pos < u.np0) {
+    if (half == 0 && !bar_wait_warp(&sh.patch_full[nu % kUnitRing], (nu / kUnitRing) & 1, ab)) return;
+    if (half == 0 && pos < u.np0 && !sh.patch[nu % kUnitRing]) {
       const int64_t orow = (int64_t)u.q_row + pos;
       const int head = u.kvh * a.group + hd;
       const float v = l == 0.f ? -INFINITY : (m - kLift + lg2(l)) * kLn2;
@@ -813,7 +929,7 @@ attn_tc32_kernel(const __grid_constant__ TileArgs a) {
     }
     bar_init(&sh.drain, 1);
     bar_init_fence();
-    sh.abort = 0;
+    sh.beats = Beats{};
   }
   UnitSource source;
   if (warp == 12) tmem_alloc(&sh.tmem, 512);
@@ -842,7 +958,7 @@ attn_tc32_kernel(const __grid_constant__ TileArgs a) {
   __syncwarp();
   fence_before();
   __syncthreads();
-  if (tid == 0 && sh.abort) attn_report(a.status, NYS_ATTN_GAVE_UP);
+  if (tid == 0 && sh.beats.abort) attn_report(a.status, NYS_ATTN_GAVE_UP);
   if (warp == 12) {
     fence_after();
     tmem_free(tmem, 512);

@@ -1,0 +1,74 @@
+"""Exact attention on unusual values: what a row does not see never reaches it,
+whatever it is, and what it sees reaches it as the formula says, against plain
+64-bit forms (tests/attn_reference.py, where the bounds are derived)."""
+import math
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+
+def _mods():
+    import torch
+    import attn_reference as ref
+    from streaming_nystr_landmark_gb300 import nys
+    return torch, ref, nys
+
+
+def _rand(torch, dev, rows, heads, kv, d, seed=0):
+    g = torch.Generator(device=dev).manual_seed(seed)
+    rn = lambda h: torch.randn((rows, h, d), generator=g, device=dev)
+    return rn(heads), rn(kv), rn(kv)
+
+
+def _prompt(torch, nys, q, k, v, q_lens, k_lens, scale=None):
+    dev = q.device
+    off = lambda x: torch.tensor([0] + x, device=dev).cumsum(0).int()
+    att = nys.ExactAttention(q.shape[1], k.shape[1], q.shape[2], v.shape[2], dtype=q.dtype,
+                             scale=scale, device=dev)
+    out = torch.full((q.shape[0], q.shape[1], v.shape[2]), 7.0, device=dev, dtype=q.dtype)
+    lse = torch.full(out.shape[:2], 7.0, device=dev)
+    att.prompt(q, k, v, off(q_lens), out, k_off=off(k_lens), lse=lse)
+    assert att.status() == 0
+    return out, lse
+
+
+def test_long_row_of_nan_beside_healthy_ones(cuda_device):
+    """400,000 values that are not finite in a unit that is not cut (129 sequences
+    and more): it is slow, and nothing gives up waiting for it."""
+    torch, ref, nys = _mods()
+    n, long, d = 130, 400000, 64
+    q_lens, k_lens = [1] + [3] * (n - 1), [long] + [3] * (n - 1)
+    q, _, _ = _rand(torch, cuda_device, sum(q_lens), 1, 1, d)
+    _, k, v = _rand(torch, cuda_device, sum(k_lens), 1, 1, d, seed=1)
+    v[:long] = math.nan
+    out, lse = _prompt(torch, nys, q, k, v, q_lens, k_lens)
+    assert bool(torch.isnan(out[0]).all())
+    want = torch.logsumexp(k[:long, 0].double() @ q[0, 0].double() / 8.0, 0)
+    assert abs(float(lse[0, 0]) - float(want)) < 1e-4
+    want, wl, b, lb = ref.prompt(q[1:], k[long:], v[long:], [3] * (n - 1), [3] * (n - 1), 1, 1 / 8.0,
+                                 torch.float32)
+    ref.check(out[1:], want, b, "out")
+    ref.check(lse[1:], wl, lb, "lse")
+
+
+@pytest.mark.parametrize("geo", [(4, 2, 128), (3, 1, 20), (40, 1, 64)])
+@pytest.mark.parametrize("q_len,k_len", [(150, 150), (40, 333), (1, 2000), (200, 90)])
+def test_f32_units_with_bad_values(cuda_device, geo, q_len, k_len):
+    """One infinity far from most rows: its own channel of the rows that see it,
+    and everything else, log-sums among it, as without it."""
+    torch, ref, nys = _mods()
+    heads, kv, d = geo
+    q, _, _ = _rand(torch, cuda_device, q_len, heads, kv, d)
+    _, k, v = _rand(torch, cuda_device, k_len, heads, kv, d, seed=1)
+    want, wl, b, lb = ref.prompt(q, k, v, [q_len], [k_len], heads // kv, 1 / math.sqrt(d),
+                                 torch.float32)
+    at = k_len - 17
+    v[at, kv - 1, 5] = math.inf
+    out, lse = _prompt(torch, nys, q, k, v, [q_len], [k_len])
+    hit = torch.zeros(out.shape, dtype=torch.bool)
+    hit[max(0, at + q_len - k_len):, heads - heads // kv:, 5] = True
+    got = out.cpu()
+    assert not bool(torch.isfinite(got[hit]).any())
+    ref.check(got[~hit], want[~hit], b[~hit], "out")
+    ref.check(lse, wl, lb, "lse")
