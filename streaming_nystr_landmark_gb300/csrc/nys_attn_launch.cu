@@ -151,7 +151,7 @@ Images images_of(int kv_heads, int d, int dv, int64_t n, int64_t keys) {
   im.v = count * 2 * (size_t)((d + 63) / 64) * 16384;
   im.exps = im.v + count * 2 * (size_t)((dv + 63) / 64) * 16384;
   im.odd = im.exps + count * sizeof(TileExps);
-  im.end = (im.odd + count * 8 + 255) & ~size_t(255);
+  im.end = (im.odd + count * 16 + 255) & ~size_t(255);
   return im;
 }
 void place_images(TileArgs& a, void* workspace, int64_t n, int64_t keys) {

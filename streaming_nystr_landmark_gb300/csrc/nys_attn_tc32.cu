@@ -43,9 +43,10 @@
 // each), two S and one O of 128 columns; P hi and lo take S's place, 8 columns
 // each for 16 keys.
 //
-// Values that are not finite are 0 in the images and flagged by group: units that
-// read a flagged tile leave their results to the query warps, which compute them in
-// f32 from the tensors (exact_rows).
+// Keys and values that are not finite are 0 in the images and flagged by group: units
+// that read a flagged tile leave their results to the query warps, which compute them
+// in f32 from the tensors (exact_rows).  (A product of pieces with an infinity has
+// the sign of either piece: lo x inf + hi x inf would be NaN for a key of weight 0.)
 //
 // Every wait is bounded (2 s), as in nys_attn_tc.cu.
 #include <cmath>
@@ -174,10 +175,9 @@ __device__ __forceinline__ float exp_of(int e) {  // 2^e, -126 <= e <= 127
 __device__ __forceinline__ float back_of(int ex) {
   return __uint_as_float((uint32_t)(ex - kTop) << 23);
 }
-// Four scaled values as hi and lo words.  Infinities and NaN: kKeep leaves them
-// what they are, alone in hi; kDrop puts 0; kNone expects none.
-enum { kNone, kKeep, kDrop };
-template <int MODE>
+// Four scaled values as hi and lo words; DROP: 0 for infinities and NaN, which
+// else do not occur.
+template <bool DROP>
 __device__ __forceinline__ void split4(float4 x, uint64_t scale2, uint32_t (&hi)[2],
                                        uint32_t (&lo)[2]) {
   const uint64_t ya = mul2(pair(x.x, x.y), scale2), yb = mul2(pair(x.z, x.w), scale2);
@@ -194,14 +194,11 @@ __device__ __forceinline__ void split4(float4 x, uint64_t scale2, uint32_t (&hi)
   for (int i = 0; i < 4; ++i) h[i] = cut11(y[i]);
   unpair(fma2(pair(h[0], h[1]), minus2, ya), l[0], l[1]);
   unpair(fma2(pair(h[2], h[3]), minus2, yb), l[2], l[3]);
-  if (MODE != kNone) {
+  if (DROP) {
     const float z[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (!finite_bits(z[i])) {
-        h[i] = MODE == kKeep ? z[i] : 0.f;
-        l[i] = 0.f;
-      }
+      if (!finite_bits(z[i])) h[i] = l[i] = 0.f;
   }
   using H = Type16<__half>;
   hi[0] = H::pack(h[0], h[1]);
@@ -486,7 +483,7 @@ __device__ void query_role(const TileArgs& a, Shared& sh, unsigned char* turn, u
         for (int i = 0; i < 4; ++i) {
           const float4 v = *reinterpret_cast<const float4*>(turn + turn_at(lane, i));
           uint32_t h2[2], l2[2];
-          split4<kNone>(v, scale2, h2, l2);
+          split4<false>(v, scale2, h2, l2);
           w[2 * i] = h2[0];
           w[2 * i + 1] = h2[1];
           w[8 + 2 * i] = l2[0];
@@ -573,12 +570,9 @@ __global__ void __launch_bounds__(256) split_kernel(const __grid_constant__ Tile
   }
   const int ex = top_exponent(top);
   if (lane == 0) {
-    if (is_v) {
-      a.exps[at].v_exp[warp] = ex - 127 - kTop;
-      a.odd[at * kGroups + warp] = odd;
-    } else {
-      a.exps[at].k_mul[warp] = back_of(ex);
-    }
+    if (is_v) a.exps[at].v_exp[warp] = ex - 127 - kTop;
+    else a.exps[at].k_mul[warp] = back_of(ex);
+    a.odd[(at * 2 + is_v) * kGroups + warp] = odd;
   }
   const float scale = scale_of(ex);
   const uint64_t scale2 = pair(scale, scale);
@@ -592,9 +586,8 @@ __global__ void __launch_bounds__(256) split_kernel(const __grid_constant__ Tile
 #pragma unroll
   for (int r = 0; r < kGroup; ++r) {
     uint32_t hi[2], lo[2];
-    if (!odd) split4<kNone>(x[r], scale2, hi, lo);
-    else if (is_v) split4<kDrop>(x[r], scale2, hi, lo);
-    else split4<kKeep>(x[r], scale2, hi, lo);
+    if (!odd) split4<false>(x[r], scale2, hi, lo);
+    else split4<true>(x[r], scale2, hi, lo);
     unsigned char* to = t + r * 128 + (unit16 ^ (uint32_t)((r & 7) << 4));
     *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
     *reinterpret_cast<uint2*>(to + piece) = make_uint2(lo[0], lo[1]);
@@ -693,12 +686,14 @@ __device__ void unit_role(const TileArgs& a, Shared& sh, UnitSource& source, int
     last_nt = u.nt;
     // (The flags, and the counter from here on, are the split's.)
     if (nu == 0) wait_for_previous();
-    // Does a tile hold values that are not finite?  Nobody asks before the
-    // results, so nobody waits for the answer's way from memory.
-    uint64_t odd = 0;
+    // Is a tile flagged?  Nobody asks before the results, so nobody waits for the
+    // answer's way from memory.
+    uint32_t odd = 0;
 #pragma unroll 4
-    for (int i = lane; i < u.nt; i += 32)
-      odd |= reinterpret_cast<const uint64_t*>(a.odd)[(int64_t)(u.tile + i) * a.kv_heads + u.kvh];
+    for (int i = lane; i < u.nt; i += 32) {
+      const uint4 x = reinterpret_cast<const uint4*>(a.odd)[(int64_t)(u.tile + i) * a.kv_heads + u.kvh];
+      odd |= x.x | x.y | x.z | x.w;
+    }
     odd = __any_sync(0xffffffffu, odd != 0);
     if (lane == 0) {
       sh.patch[nu % kUnitRing] = odd != 0;

@@ -72,3 +72,57 @@ def test_f32_units_with_bad_values(cuda_device, geo, q_len, k_len):
     assert not bool(torch.isfinite(got[hit]).any())
     ref.check(got[~hit], want[~hit], b[~hit], "out")
     ref.check(lse, wl, lb, "lse")
+
+
+def _without(torch, ref, q, k, v, q_lens, gone, group):
+    """The plain form of one sequence in which no row gives key `gone` any weight."""
+    n = k.shape[0]
+    d = q.shape[2]
+    i, j = torch.arange(q_lens)[:, None], torch.arange(n)[None, :]
+    seen = (j <= i + n - q_lens) & (j != gone)
+    res = [ref.attend(q[:, h].double().cpu(), k[:, h // group].double().cpu(),
+                      v[:, h // group].double().cpu(), seen, 1 / math.sqrt(d), q.dtype)
+           for h in range(q.shape[1])]
+    return [torch.stack([r[x] for r in res], 1) for x in range(4)]
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
+@pytest.mark.parametrize("q_len,k_len", [(64, 64), (1, 300), (150, 400), (1, 3000)])
+def test_key_of_minus_infinity_has_no_weight(cuda_device, dtype, q_len, k_len):
+    """An infinite element against queries that give the score -inf."""
+    torch, ref, nys = _mods()
+    dt = getattr(torch, dtype)
+    heads, kv, d, at = 4, 2, 64, 10
+    q, _, _ = _rand(torch, cuda_device, q_len, heads, kv, d)
+    _, k, v = _rand(torch, cuda_device, k_len, heads, kv, d, seed=1)
+    q[..., 5] = q[..., 5].abs() + 0.1
+    q[..., 9] = -q[..., 9].abs() - 0.1
+    q, k, v = q.to(dt), k.to(dt), v.to(dt)
+    want, wl, b, lb = _without(torch, ref, q, k, v, q_len, at, heads // kv)
+    k[at, 0, 5], k[at, 1, 9] = -math.inf, math.inf
+    out, lse = _prompt(torch, nys, q, k, v, [q_len], [k_len])
+    ref.check(out, want, b, "out")
+    ref.check(lse, wl, lb, "lse")
+
+
+def test_prefix_key_of_minus_infinity_has_no_weight(cuda_device):
+    """The same for keys of a prefix that is read once for all requests (f32)."""
+    torch, ref, nys = _mods()
+    n, heads, kv, d, page, prefix = 300, 4, 2, 64, 16, 512
+    q, _, _ = _rand(torch, cuda_device, n, heads, kv, d)
+    _, k, v = _rand(torch, cuda_device, prefix, heads, kv, d, seed=1)
+    q[..., 5] = q[..., 5].abs() + 0.1
+    rest = [x for x in range(prefix) if x != 200]
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)
+    want = [ref.attend(q[:, h].double().cpu(), k[rest, h // 2].double().cpu(),
+                       v[rest, h // 2].double().cpu(), torch.ones(n, prefix - 1, dtype=torch.bool),
+                       1 / 8.0, torch.float32) for h in range(heads)]
+    k[200, :, 5] = -math.inf
+    cache = nys.PagedKV(prefix // page, page, kv, d, d, device=cuda_device,
+                        k=k.view(-1, page, kv, d), v=v.view(-1, page, kv, d))
+    att = nys.ExactAttention(heads, kv, d, d, device=cuda_device)
+    out = torch.empty((n, heads, d), device=cuda_device)
+    att.shared(q, cache, i32([0] * n), i32([[0]] * n), out,
+               prefix_pages=i32(list(range(prefix // page))), prefix_len=prefix)
+    ref.check(out, torch.stack([w[0] for w in want], 1), torch.stack([w[2] for w in want], 1), "out")
+    assert att.status() == 0
