@@ -73,8 +73,8 @@ struct TileArgs {
   // f32: K and V as pieces, tile by tile (nys_attn_tc32.cu).
   unsigned char *k_image, *v_image;
   TileExps* exps;
-  uint8_t* odd;  // [tile][KV head][keys, values][group]: holds some that are not finite;
-                 // units that read it are computed in f32
+  uint8_t* odd;  // [tile][KV head][keys, values][group]: what the group says of the range
+                 // of its numbers (nys_attn_tc32.cu)
   // Values and keys for the checks of unusual values, and the pages' own rows.
   const void *k_raw, *v_raw;
   int64_t k_row, k_head, v_row, v_head;

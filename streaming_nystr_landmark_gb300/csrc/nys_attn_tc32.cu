@@ -82,6 +82,14 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.f;
 constexpr float kLift = 6.f;
 constexpr int kTop = 13;        // the largest value's power of two after scaling
+// A group of values that are all 0 has no exponent of its own.  It takes one that is
+// below those of values above 2^-47, so that its keys do not raise the reference above
+// other keys' weights, and high enough that their weights, which l still counts, stay
+// f32 numbers beside values up to 2^43; units with values outside that are flagged.
+constexpr int kZeroExp = -60, kZeroLow = kZeroExp, kZeroHigh = 30;
+// What a group of values says to its units: 0, all are 0; kOdd, computed in f32; else
+// the biased exponent of the largest.
+constexpr uint32_t kOdd = 255;
 
 struct Shared {
   uint64_t q_full, q_empty;
@@ -570,9 +578,10 @@ __global__ void __launch_bounds__(256) split_kernel(const __grid_constant__ Tile
   }
   const int ex = top_exponent(top);
   if (lane == 0) {
-    if (is_v) a.exps[at].v_exp[warp] = ex - 127 - kTop;
+    const bool none = top >> 23 == 0;
+    if (is_v) a.exps[at].v_exp[warp] = none ? kZeroExp : ex - 127 - kTop;
     else a.exps[at].k_mul[warp] = back_of(ex);
-    a.odd[(at * 2 + is_v) * kGroups + warp] = odd;
+    a.odd[(at * 2 + is_v) * kGroups + warp] = (uint8_t)(odd ? kOdd : is_v && !none ? (uint32_t)ex : 0u);
   }
   const float scale = scale_of(ex);
   const uint64_t scale2 = pair(scale, scale);
@@ -688,15 +697,25 @@ __device__ void unit_role(const TileArgs& a, Shared& sh, UnitSource& source, int
     if (nu == 0) wait_for_previous();
     // Is a tile flagged?  Nobody asks before the results, so nobody waits for the
     // answer's way from memory.
-    uint32_t odd = 0;
+    uint32_t keys = 0, low = ~0u, high = 0, zero = 0;  // of values: four groups at a time
 #pragma unroll 4
     for (int i = lane; i < u.nt; i += 32) {
       const uint4 x = reinterpret_cast<const uint4*>(a.odd)[(int64_t)(u.tile + i) * a.kv_heads + u.kvh];
-      odd |= x.x | x.y | x.z | x.w;
+      keys |= x.x | x.y;
+      high = __vmaxu4(high, __vmaxu4(x.z, x.w));
+      low = __vminu4(low, __vminu4(__vsub4(x.z, 0x01010101u), __vsub4(x.w, 0x01010101u)));  // (0: 255)
+      zero |= __vcmpeq4(x.z, 0u) | __vcmpeq4(x.w, 0u);
     }
-    odd = __any_sync(0xffffffffu, odd != 0);
+    auto most = [](uint32_t x) {  // of a word's bytes and the warp
+      x = __vmaxu4(x, x >> 16);
+      return __reduce_max_sync(0xffffffffu, max(x & 255u, x >> 8 & 255u));
+    };
+    const int top = (int)most(high), bottom = 256 - (int)most(~low);  // 256: all are zero
+    const bool mixed = zero != 0 && bottom < 256 &&
+                       (bottom - 127 - kTop < kZeroLow || top - 127 - kTop > kZeroHigh);
+    const bool odd = __any_sync(0xffffffffu, keys != 0 || mixed) || top == (int)kOdd;
     if (lane == 0) {
-      sh.patch[nu % kUnitRing] = odd != 0;
+      sh.patch[nu % kUnitRing] = odd;
       bar_arrive(&sh.patch_full[nu % kUnitRing]);
     }
   }

@@ -126,3 +126,45 @@ def test_prefix_key_of_minus_infinity_has_no_weight(cuda_device):
                prefix_pages=i32(list(range(prefix // page))), prefix_len=prefix)
     ref.check(out, torch.stack([w[0] for w in want], 1), torch.stack([w[2] for w in want], 1), "out")
     assert att.status() == 0
+
+
+@pytest.mark.parametrize("size", [1e10, 1.0, 1e-2, 1e-4, 1e-6, 1e-8, 1e-12, 1e-20])
+@pytest.mark.parametrize("q_len,k_len", [(64, 64), (1, 200), (100, 700)])
+def test_zero_values_beside_small_ones(cuda_device, size, q_len, k_len):
+    """16 zero value rows: they take their share of the weight and nothing else."""
+    torch, ref, nys = _mods()
+    heads, kv, d = 2, 1, 64
+    q, _, _ = _rand(torch, cuda_device, q_len, heads, kv, d)
+    _, k, v = _rand(torch, cuda_device, k_len, heads, kv, d, seed=1)
+    v *= size
+    v[16:32] = 0
+    want, wl, b, lb = ref.prompt(q, k, v, [q_len], [k_len], heads, 1 / math.sqrt(d), torch.float32)
+    out, lse = _prompt(torch, nys, q, k, v, [q_len], [k_len])
+    ref.check(out, want, b, "out")
+    ref.check(lse, wl, lb, "lse")
+
+
+@pytest.mark.parametrize("size", [1.0, 1e-6, 1e-20])
+def test_zero_pages_of_a_prefix_of_small_values(cuda_device, size):
+    """The same for a prefix read once for all requests (f32); a page outside the
+    pool counts as zeros."""
+    torch, ref, nys = _mods()
+    n, heads, kv, d, page, prefix = 300, 4, 2, 64, 16, 512
+    q, _, _ = _rand(torch, cuda_device, n, heads, kv, d)
+    _, k, v = _rand(torch, cuda_device, prefix, heads, kv, d, seed=1)
+    v *= size
+    v[64:80] = 0
+    pages = list(range(prefix // page))
+    pages[7] = 1 << 20
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)
+    pk, pv = k.view(-1, page, kv, d), v.view(-1, page, kv, d)
+    want, wl, b, lb = ref.shared(q, pk, pv, pages, prefix, [0] * n, [[0]] * n, heads // kv, 1 / 8.0,
+                                 torch.float32)
+    cache = nys.PagedKV(prefix // page, page, kv, d, d, device=cuda_device, k=pk, v=pv)
+    att = nys.ExactAttention(heads, kv, d, d, device=cuda_device)
+    out, lse = torch.empty((n, heads, d), device=cuda_device), torch.empty((n, heads), device=cuda_device)
+    att.shared(q, cache, i32([0] * n), i32([[0]] * n), out, prefix_pages=i32(pages),
+               prefix_len=prefix, lse=lse)
+    ref.check(out, want, b, "out")
+    ref.check(lse, wl, lb, "lse")
+    assert att.status() == nys.NYS_ATTN_BAD_PAGE
