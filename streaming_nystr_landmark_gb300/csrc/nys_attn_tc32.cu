@@ -6,8 +6,9 @@
 // lo hi + hi lo + hi hi (the dropped lo lo is below 2^-21 of |x y| at worst, about
 // 2^-24 in the mean and of either sign), summed in f32 in tensor memory, small
 // ones first.  The exponent e is common to 16 rows (those that one warp
-// converts) and puts their largest value at 2^13, where fp16 keeps 22 bits of
-// everything down to 2^-27 of it.
+// converts) and puts their largest value at 2^13.  fp16's smallest step is 2^-24, so
+// 22 bits are kept down to 2^-15 of the largest, and 2^-38 of it below.  Groups and
+// units with a wider range than that takes are computed in f32 (below).
 //
 //   S' = Q' K'^T gives s_ij = S' 2^(eq + ek) scale log2(e), one multiplier a
 //   group of 16 keys.  The value's exponent goes into the weight:
@@ -43,10 +44,13 @@
 // each), two S and one O of 128 columns; P hi and lo take S's place, 8 columns
 // each for 16 keys.
 //
-// Keys and values that are not finite are 0 in the images and flagged by group: units
-// that read a flagged tile leave their results to the query warps, which compute them
-// in f32 from the tensors (exact_rows).  (A product of pieces with an infinity has
-// the sign of either piece: lo x inf + hi x inf would be NaN for a key of weight 0.)
+// Keys and values that are not finite are 0 in the images, and their group is flagged
+// (odd), as are groups whose numbers are too far apart for a common exponent: units
+// that read a flagged tile, and warps with such a query row, leave their results to the
+// query warps, which compute them in f32 from the tensors (exact_rows).  So a key
+// that a row does not see costs the row no more than roundings at f32's level, and one
+// that it sees none but its own.  (A product of pieces with an infinity has the sign
+// of either piece: lo x inf + hi x inf would be NaN for a key of weight 0.)
 //
 // Every wait is bounded (2 s), as in nys_attn_tc.cu.
 #include <cmath>
@@ -90,6 +94,15 @@ constexpr int kZeroExp = -60, kZeroLow = kZeroExp, kZeroHigh = 30;
 // What a group of values says to its units: 0, all are 0; kOdd, computed in f32; else
 // the biased exponent of the largest.
 constexpr uint32_t kOdd = 255;
+// fp16 holds a piece lo of a number at 2^-38 of its group's largest at best, so a key
+// beside a far larger one, and a column beside a far larger one, would be rounded to what
+// the larger one leaves: a group is odd where numbers lie more than kSpan powers of
+// two below its largest.  Single numbers do in any group; what counts is four columns
+// of a row (small_cells) and a column of 16 rows.  Weights are rounded at 2^-31 of the
+// largest contribution (weight and value), so a unit is odd where its groups' largest
+// values are more than kSpanUnit apart.  Products of exponents stay below f32's range.
+constexpr int kSpan = 13, kSpanUnit = 10;
+constexpr int kLeastK = 40, kMostK = 187, kLeastV = 60;  // biased exponents
 
 struct Shared {
   uint64_t q_full, q_empty;
@@ -102,6 +115,7 @@ struct Shared {
   int patch[kUnitRing];  // results are computed in f32 by the query warps (exact_rows)
   alignas(16) TileExps exps[4];      // of tile & 3
   int8_t q_exp[4][kTileM];           // eq, [unit & 3][row]: the query warps run up to three units ahead
+  uint8_t q_odd[4][4];               // [unit & 3][query warp]: computes its rows in f32
   float mx[2][2][kTileM];            // halves' maxima [exchange & 1][half][row], also of l
   uint32_t tmem;
   Beats beats;
@@ -183,6 +197,20 @@ __device__ __forceinline__ float exp_of(int e) {  // 2^e, -126 <= e <= 127
 __device__ __forceinline__ float back_of(int ex) {
   return __uint_as_float((uint32_t)(ex - kTop) << 23);
 }
+// The largest magnitude of four columns, NaN if one is.
+__device__ __forceinline__ float cell_of(float4 x) {
+  return max3_abs_nan(max3_abs_nan(0.f, x.x, x.y), x.z, x.w);
+}
+// Magnitudes below this are small against a largest one of biased exponent ex; 0 is
+// none.
+__device__ __forceinline__ float small_below(int ex) {
+  return __uint_as_float(ex > kSpan ? (uint32_t)(ex - kSpan) << 23 : 0u);
+}
+__device__ __forceinline__ bool is_small(float x, float below) { return x != 0.f && fabsf(x) < below; }
+// How many cells of `rows` rows' numbers are few enough to be chance (in numbers drawn
+// from one distribution a cell is small once in 10^14, or in some 10^4 where zeros
+// leave it one number).
+__device__ __forceinline__ int small_cells(int dim) { return (dim + 31) / 32; }
 // Four scaled values as hi and lo words; DROP: 0 for infinities and NaN, which
 // else do not occur.
 template <bool DROP>
@@ -376,6 +404,7 @@ __device__ void query_role(const TileArgs& a, Shared& sh, unsigned char* turn, u
     hd[i] = r - pos[i] * a.group;
   }
   uint32_t n_q = 0, n_r = 0;
+  bool odd_now = false, odd_last = false;  // the warp's rows of this unit and the last
 
   // Results of unit nu.
   auto results = [&](uint32_t nu) {
@@ -388,7 +417,7 @@ __device__ void query_role(const TileArgs& a, Shared& sh, unsigned char* turn, u
       ++n_r;
       fence_after();
     }
-    if (sh.patch[at]) {  // (a unit with tiles: nobody reads its O, whose next use may begin)
+    if (sh.patch[at] || odd_last) {  // (a unit with tiles: nobody reads its O, whose next use may begin)
       fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive(&sh.o_empty, 2);
@@ -445,6 +474,7 @@ __device__ void query_role(const TileArgs& a, Shared& sh, unsigned char* turn, u
     if (!bar_wait_warp(&sh.u_full[nu % kUnitRing], (nu / kUnitRing) & 1, ab)) return;
     const Unit& u = sh.unit[nu % kUnitRing];
     const bool valid = u.valid;
+    odd_now = false;
     if (valid && u.nt > 0) {
       // The whole tile at once, 32 loads a lane.
       float4 x[32];
@@ -458,21 +488,37 @@ __device__ void query_role(const TileArgs& a, Shared& sh, unsigned char* turn, u
                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
       }
       // The rows' exponents.
+      bool odd = false;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        float t = 0.f;
+        float t = 0.f, least = INFINITY;  // (zeros count: the check itself is rare enough)
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          t = max3_abs_nan(t, x[c * 4 + i].x, x[c * 4 + i].y);
-          t = max3_abs_nan(t, x[c * 4 + i].z, x[c * 4 + i].w);
+        for (int c = 0; c < 8; c += 2) {
+          const float y = cell_of(x[c * 4 + i]), z = cell_of(x[c * 4 + 4 + i]);
+          t = max3_abs_nan(t, y, z);
+          least = min3(least, y, z);
         }
         uint32_t top = __float_as_uint(t) & 0x7FFFFFFFu;
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // (127 marks a query with a value that is not finite: its results are NaN)
+        const int e = (int)(top >> 23);
+        const float below = small_below(e);
+        if (__any_sync(0xffffffffu, least < below)) {
+          int small = 0;  // a row's cells are on four lanes
+#pragma unroll
+          for (int c = 0; c < 8; ++c) small += is_small(cell_of(x[c * 4 + i]), below);
+          small += __shfl_xor_sync(0xffffffffu, small, 1);
+          small += __shfl_xor_sync(0xffffffffu, small, 2);
+          odd |= small >= small_cells(a.d);
+        }
+        odd |= (top != 0 && e < kLeastK) || e > kMostK;  // (infinities, NaN too)
+        // (127 marks a query with a value that is not finite, whatever S then holds)
         if (sub == 0) sh.q_exp[n_q & 3][warp * 32 + i * 8 + (lane >> 2)] =
             (int8_t)(top >= 0x7F800000u ? 127 : top_exponent(top) - 127 - kTop);
       }
+      odd = __any_sync(0xffffffffu, odd);
+      odd_now = odd;
+      if (lane == 0) sh.q_odd[n_q & 3][warp] = odd;
       __syncwarp();
       const int qe = sh.q_exp[n_q & 3][warp * 32 + lane];
       const float scale = qe == 127 ? NAN : exp_of(-qe);
@@ -508,12 +554,15 @@ __device__ void query_role(const TileArgs& a, Shared& sh, unsigned char* turn, u
     }
     if (nu > 0 && !results(nu - 1)) return;
     if (!valid) return;
+    odd_last = odd_now;
   }
 }
 
-// K and V as tile images.  Grid: tiles x KV heads, K and V; a warp takes 16 rows.
+// K and V as tile images.  Grid: tiles x KV heads, K and V; a warp takes 16 rows.  Three
+// CTAs a SM: with the two that 105 registers would leave 64 prompts of 256 take 1.8 us
+// longer.
 template <bool PAGED>
-__global__ void __launch_bounds__(256) split_kernel(const __grid_constant__ TileArgs a) {
+__global__ void __launch_bounds__(256, 3) split_kernel(const __grid_constant__ TileArgs a) {
   let_next_start();
   if (a.counter && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.counter = 0;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -561,20 +610,42 @@ __global__ void __launch_bounds__(256) split_kernel(const __grid_constant__ Tile
     x[r] = o >= 0 && col ? __ldcs(reinterpret_cast<const float4*>(src + o * stride))
                          : make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  float t0 = 0.f, t1 = 0.f;
+  float column[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int r = 0; r < kGroup; ++r) {
-    t0 = max3_abs_nan(t0, x[r].x, x[r].y);
-    t1 = max3_abs_nan(t1, x[r].z, x[r].w);
+  for (int r = 0; r < kGroup; r += 2) {
+    column[0] = max3_abs_nan(column[0], x[r].x, x[r + 1].x);
+    column[1] = max3_abs_nan(column[1], x[r].y, x[r + 1].y);
+    column[2] = max3_abs_nan(column[2], x[r].z, x[r + 1].z);
+    column[3] = max3_abs_nan(column[3], x[r].w, x[r + 1].w);
   }
   uint32_t top = __reduce_max_sync(
-      0xffffffffu, max(__float_as_uint(t0) & 0x7FFFFFFFu, __float_as_uint(t1) & 0x7FFFFFFFu));
-  const bool odd = top >= 0x7F800000u;
-  if (odd) {
+      0xffffffffu,
+      __float_as_uint(cell_of(make_float4(column[0], column[1], column[2], column[3]))) & 0x7FFFFFFFu);
+  const bool bad = top >= 0x7F800000u;
+  bool odd = bad;
+  if (bad) {
     float f = 0.f;
 #pragma unroll
     for (int r = 0; r < kGroup; ++r) f = fmaxf(f, finite_max(x[r]));
     top = __reduce_max_sync(0xffffffffu, __float_as_uint(f));
+  } else {
+    const int e = (int)(top >> 23);
+    const float below = small_below(e);
+    float least = INFINITY;  // (zeros count here: the check itself is rare enough)
+#pragma unroll
+    for (int r = 0; r < kGroup; r += 2) least = min3(least, cell_of(x[r]), cell_of(x[r + 1]));
+    if (__any_sync(0xffffffffu, col && least < below)) {
+      int small = 0;
+#pragma unroll
+      for (int r = 0; r < kGroup; ++r) small += is_small(cell_of(x[r]), below);
+      odd = __reduce_add_sync(0xffffffffu, small) >= small_cells(dim);
+    }
+    // (In fewer rows than 16 a column may be small by chance.)
+    const float narrow = min3(min3(INFINITY, column[0], column[1]), column[2], column[3]);
+    if (rows == kGroup && __any_sync(0xffffffffu, col && narrow < below))
+      odd |= __any_sync(0xffffffffu, is_small(column[0], below) || is_small(column[1], below) ||
+                                         is_small(column[2], below) || is_small(column[3], below));
+    odd |= is_v ? top != 0 && e < kLeastV : (top != 0 && e < kLeastK) || e > kMostK;
   }
   const int ex = top_exponent(top);
   if (lane == 0) {
@@ -595,7 +666,7 @@ __global__ void __launch_bounds__(256) split_kernel(const __grid_constant__ Tile
 #pragma unroll
   for (int r = 0; r < kGroup; ++r) {
     uint32_t hi[2], lo[2];
-    if (!odd) split4<false>(x[r], scale2, hi, lo);
+    if (!bad) split4<false>(x[r], scale2, hi, lo);
     else split4<true>(x[r], scale2, hi, lo);
     unsigned char* to = t + r * 128 + (unit16 ^ (uint32_t)((r & 7) << 4));
     *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
@@ -713,7 +784,8 @@ __device__ void unit_role(const TileArgs& a, Shared& sh, UnitSource& source, int
     const int top = (int)most(high), bottom = 256 - (int)most(~low);  // 256: all are zero
     const bool mixed = zero != 0 && bottom < 256 &&
                        (bottom - 127 - kTop < kZeroLow || top - 127 - kTop > kZeroHigh);
-    const bool odd = __any_sync(0xffffffffu, keys != 0 || mixed) || top == (int)kOdd;
+    const bool apart = bottom < 256 && top - bottom > kSpanUnit;
+    const bool odd = __any_sync(0xffffffffu, keys != 0 || mixed) || apart || top == (int)kOdd;
     if (lane == 0) {
       sh.patch[nu % kUnitRing] = odd;
       bar_arrive(&sh.patch_full[nu % kUnitRing]);
@@ -898,7 +970,9 @@ __device__ void row_role(const TileArgs& a, Shared& sh, uint32_t tmem, int row, 
       if (lane == 0) bar_arrive(&sh.r_full);
     }
     if (half == 0 && !bar_wait_warp(&sh.patch_full[nu % kUnitRing], (nu / kUnitRing) & 1, ab)) return;
-    if (half == 0 && pos < u.np0 && !sh.patch[nu % kUnitRing]) {
+    // (Unless the query warps compute the row.)
+    if (half == 0 && pos < u.np0 && !sh.patch[nu % kUnitRing] &&
+        !(nt > 0 && sh.q_odd[(nq - 1) & 3][row >> 5])) {
       const int64_t orow = (int64_t)u.q_row + pos;
       const int head = u.kvh * a.group + hd;
       const float v = l == 0.f ? -INFINITY : (m - kLift + lg2(l)) * kLn2;

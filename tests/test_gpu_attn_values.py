@@ -168,3 +168,115 @@ def test_zero_pages_of_a_prefix_of_small_values(cuda_device, size):
     ref.check(out, want, b, "out")
     ref.check(lse, wl, lb, "lse")
     assert att.status() == nys.NYS_ATTN_BAD_PAGE
+
+
+SIZES = [2.0 ** e for e in (4, 8, 10, 12, 13, 14, 16, 20, 40)] + [1e6, 1e12, 1e30]
+
+
+@pytest.mark.parametrize("what", ["k", "v"])
+@pytest.mark.parametrize("size", SIZES)
+@pytest.mark.parametrize("n,at", [(48, 10), (300, 290), (500, 127)])
+def test_f32_large_values_that_rows_do_not_see(cuda_device, what, size, n, at):
+    """A key's finite row, far larger than those before it: rows that do not see
+    it come out as if it were ordinary, in its group of keys, its tile and beyond."""
+    torch, ref, nys = _mods()
+    heads, kv, d = 2, 1, 64
+    q, k, v = _rand(torch, cuda_device, n, heads, kv, d)
+    want, wl, b, lb = ref.prompt(q, k, v, [n], [n], heads, 1 / math.sqrt(d), torch.float32)
+    (k if what == "k" else v)[at] *= size
+    out, lse = _prompt(torch, nys, q, k, v, [n], [n])
+    ref.check(out[:at], want[:at], b[:at], "out")
+    ref.check(lse[:at], wl[:at], lb[:at], "lse")
+    if what == "v":   # and the others as the formula says
+        want, wl, b, lb = ref.prompt(q, k, v, [n], [n], heads, 1 / math.sqrt(d), torch.float32)
+        ref.check(out, want, b, "out")
+        ref.check(lse, wl, lb, "lse")
+
+
+@pytest.mark.parametrize("size", SIZES)
+@pytest.mark.parametrize("rows", [slice(10, 11), slice(32, 48), slice(128, 300), slice(3, 300, 2)])
+def test_f32_large_values_that_rows_see(cuda_device, size, rows):
+    """Large value rows among ordinary ones, with weights of their own: one, a
+    group of keys, whole tiles, every other one."""
+    torch, ref, nys = _mods()
+    n, heads, kv, d = 300, 2, 1, 64
+    q, k, v = _rand(torch, cuda_device, n, heads, kv, d)
+    v[rows] *= size
+    want, wl, b, lb = ref.prompt(q, k, v, [n], [n], heads, 1 / math.sqrt(d), torch.float32)
+    out, lse = _prompt(torch, nys, q, k, v, [n], [n])
+    ref.check(out, want, b, "out")
+    ref.check(lse, wl, lb, "lse")
+
+
+@pytest.mark.parametrize("size", SIZES)
+@pytest.mark.parametrize("score", [-4.0, -12.0, -30.0, -60.0])
+def test_f32_large_value_of_small_weight(cuda_device, size, score):
+    """One large value row whose key's score is far below the others'."""
+    torch, ref, nys = _mods()
+    n, heads, kv, d = 200, 1, 1, 64
+    q, _, _ = _rand(torch, cuda_device, 1, heads, kv, d)
+    _, k, v = _rand(torch, cuda_device, n, heads, kv, d, seed=1)
+    k[77, 0] = q[0, 0] * (score * math.sqrt(d)) / float(q[0, 0] @ q[0, 0])
+    v[77] *= size
+    want, wl, b, lb = ref.prompt(q, k, v, [1], [n], 1, 1 / math.sqrt(d), torch.float32)
+    out, lse = _prompt(torch, nys, q, k, v, [1], [n])
+    ref.check(out, want, b, "out")
+    ref.check(lse, wl, lb, "lse")
+
+
+@pytest.mark.parametrize("size", SIZES + [1 / x for x in SIZES])
+@pytest.mark.parametrize("where", ["v one", "v column", "k column", "k one", "q column", "q one"])
+def test_f32_columns_of_other_sizes(cuda_device, size, where):
+    """One element, or one column, far from the rest; where it is the keys' or the
+    queries' the other side's column makes up for it, so that scores stay ordinary."""
+    torch, ref, nys = _mods()
+    n, heads, kv, d, c = 200, 2, 1, 64, 13
+    q, k, v = _rand(torch, cuda_device, n, heads, kv, d)
+    if where == "v one":
+        v[20, 0, c] *= size
+    elif where == "v column":
+        v[..., c] *= size
+    elif where in ("k column", "q column"):
+        x = size if where[0] == "k" else 1 / size
+        k[..., c] *= x
+        q[..., c] /= x
+    elif where == "k one":
+        k[20, 0, c] *= size
+        q[..., c] *= 1 / size if size > 1 else 1.0
+    else:
+        q[20, :, c] *= size
+        k[..., c] *= 1 / size if size > 1 else 1.0
+    want, wl, b, lb = ref.prompt(q, k, v, [n], [n], heads, 1 / math.sqrt(d), torch.float32)
+    out, lse = _prompt(torch, nys, q, k, v, [n], [n])
+    ref.check(out, want, b, "out")
+    ref.check(lse, wl, lb, "lse")
+
+
+@pytest.mark.parametrize("size", [1e6, 1e12, 1e30])
+@pytest.mark.parametrize("where", ["row", "column", "own pages"])
+def test_f32_shared_prefix_of_other_sizes(cuda_device, size, where):
+    """A prefix read once for all requests, and own pages beside it."""
+    torch, ref, nys = _mods()
+    n, heads, kv, d, page, prefix = 300, 4, 2, 64, 16, 512
+    q, _, _ = _rand(torch, cuda_device, n, heads, kv, d)
+    _, k, v = _rand(torch, cuda_device, prefix + n * page, heads, kv, d, seed=1)
+    if where == "row":
+        v[100] *= size
+    elif where == "column":
+        v[:prefix, :, 3] *= size
+    else:
+        v[prefix::2] *= size
+    pk, pv = k.view(-1, page, kv, d), v.view(-1, page, kv, d)
+    pages = list(range(prefix // page))
+    table, lens = [[prefix // page + i] for i in range(n)], [i % 17 for i in range(n)]
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)
+    want, wl, b, lb = ref.shared(q, pk, pv, pages, prefix, lens, table, heads // kv, 1 / 8.0,
+                                 torch.float32)
+    cache = nys.PagedKV(pk.shape[0], page, kv, d, d, device=cuda_device, k=pk, v=pv)
+    att = nys.ExactAttention(heads, kv, d, d, device=cuda_device)
+    out, lse = torch.empty((n, heads, d), device=cuda_device), torch.empty((n, heads), device=cuda_device)
+    att.shared(q, cache, i32(lens), i32(table), out, prefix_pages=i32(pages), prefix_len=prefix,
+               lse=lse)
+    ref.check(out, want, b, "out")
+    ref.check(lse, wl, lb, "lse")
+    assert att.status() == 0
