@@ -762,7 +762,12 @@ __device__ void unit_role(const TileArgs& a, Shared& sh, UnitSource& source, int
       bar_arrive(&sh.u_full[nu % kUnitRing]);
     }
     __syncwarp();
-    if (!u.valid) return;
+    if (!u.valid) {
+      // (A launch without units does not end before the split, which the next launch
+      // on this workspace would then overtake.)
+      if (nu == 0) wait_for_previous();
+      return;
+    }
     last_nt = u.nt;
     // (The flags, and the counter from here on, are the split's.)
     if (nu == 0) wait_for_previous();

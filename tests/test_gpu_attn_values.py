@@ -280,3 +280,25 @@ def test_f32_shared_prefix_of_other_sizes(cuda_device, size, where):
     ref.check(out, want, b, "out")
     ref.check(lse, wl, lb, "lse")
     assert att.status() == 0
+
+
+def test_f32_call_without_units_before_another(cuda_device):
+    """Rows that no sequence covers: the attention launch has nothing to do but is
+    not done before its keys' split is, whose workspace the next call takes."""
+    torch, ref, nys = _mods()
+    heads, kv, d, n = 4, 2, 64, 3000
+    q, k, v = _rand(torch, cuda_device, n, heads, kv, d)
+    q2, k2, v2 = _rand(torch, cuda_device, 200, heads, kv, d, seed=1)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=cuda_device)
+    want, _, b, _ = ref.prompt(q2, k2, v2, [200], [200], 2, 1 / 8.0, torch.float32)
+    att = nys.ExactAttention(heads, kv, d, d, device=cuda_device)
+    none, koff, off, out = i32(0, 0), i32(0, n), i32(0, 200), torch.full_like(q, 7.0)
+    got = [torch.empty_like(q2) for _ in range(20)]
+    for x in got:
+        att.prompt(q, k, v, none, out, k_off=koff)
+        att.prompt(q2, k2, v2, off, x)
+    assert bool((out == 7.0).all())
+    for x in got:
+        assert torch.equal(x, got[0])
+    ref.check(got[0], want, b, "out")
+    assert att.status() == 0
