@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 3) own16_kernel(SharedArgs a, OwnArg
           acc[n][x * 2 + 1] *= f;
         }
       }
-      const float ref = m[x] == -INFINITY ? 0.f : m[x];
+      const float ref = (m[x] == -INFINITY ? 0.f : m[x]) - Type16<T>::kLift;
       float w[4];
 #pragma unroll
       for (int n = 0; n < 2; ++n)
@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 3) own16_kernel(SharedArgs a, OwnArg
     const int h = (lane >> 2) + x * 8;
     if (h < heads) {
       if ((lane & 3) == 0) {
-        jm[warp * kHeads16 + h] = m[x];
+        jm[warp * kHeads16 + h] = m[x] - Type16<T>::kLift;  // (what the weights refer to)
         jl[warp * kHeads16 + h] = l[x];
       }
 #pragma unroll

@@ -3,7 +3,8 @@
 // For each query row i (one position and head) over the keys j that it sees,
 // in one pass:   s_ij = q_i . k_j,  m_i = running maximum,
 //   P_ij = 2^{c (s_ij - m_i)},  c = scale log2(e),   l_i += sum_j P_ij,
-//   O_i += sum_j P_ij v_j,   result O_i / l_i,   lse_i = scale m_i + ln l_i.
+//   O_i += sum_j P_ij v_j,   result O_i / l_i,   lse_i = scale m_i + ln l_i
+// (fp16: P 2^7 times that, Type16::kLift).
 // A tile of 128 keys is one step: S = Q K^T and O += P V are tcgen05 products
 // with f32 accumulators in tensor memory.  Both maxima and sums are f32; P is
 // rounded once to the inputs' type, which the second product needs (half a
@@ -504,7 +505,7 @@ __device__ void row_role(const TileArgs& a, Shared& sh, uint32_t tmem, int s, in
           wait_st();
         }
       }
-      const float ref = m == -INFINITY ? 0.f : m * sc;
+      const float ref = (m == -INFINITY ? 0.f : m * sc) - Type16<T>::kLift;
       float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
 #pragma unroll
       for (int c = 0; c < 128; c += 32) {
@@ -630,7 +631,7 @@ __device__ void row_role(const TileArgs& a, Shared& sh, uint32_t tmem, int s, in
       }
     }
     if (mine && (pair || s == 0)) {
-      const float v = total == 0.f ? -INFINITY : fmaf(top, a.scale, lg2(total) * 0.6931471805599453f);
+      const float v = total == 0.f ? -INFINITY : fmaf(top, a.scale, (lg2(total) - Type16<T>::kLift) * 0.6931471805599453f);
       if (u.slot >= 0) a.part_lse[prow] = v;
       else if (a.lse) a.lse[orow * a.heads + head] = v;
     }

@@ -314,11 +314,17 @@ __device__ __forceinline__ float cut11(float x) {
   return __uint_as_float(__float_as_uint(x) & 0xFFFFE000u);
 }
 
+// kLift: powers of two that the softmax's weights are raised by before they are rounded
+// to the type.  fp16's smallest step is 2^-24: unraised, weights below 2^-25 of the
+// largest would be 0, and keys by the thousand with such weights lost; raised, and
+// with a reference that a row may outgrow by 2^8, they stay below 2^15 and are held
+// down to 2^-32.
 template <typename T>
 struct Type16;
 template <>
 struct Type16<__nv_bfloat16> {
   static constexpr bool kBf16 = true;
+  static constexpr float kLift = 0.f;
   static constexpr uint32_t kExp = 0x7F807F80u, kOne = 0x00800080u;
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     uint32_t r;
@@ -335,6 +341,7 @@ struct Type16<__nv_bfloat16> {
 template <>
 struct Type16<__half> {
   static constexpr bool kBf16 = false;
+  static constexpr float kLift = 7.f;
   static constexpr uint32_t kExp = 0x7C007C00u, kOne = 0x04000400u;
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     uint32_t r;

@@ -302,3 +302,46 @@ def test_f32_call_without_units_before_another(cuda_device):
         assert torch.equal(x, got[0])
     ref.check(got[0], want, b, "out")
     assert att.status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("gap", [10.0, 14.0, 17.4, 20.0])
+@pytest.mark.parametrize("how", ["prompt", "prompt cut", "pages", "prefix"])
+def test_many_keys_of_small_weight(cuda_device, dtype, gap, how):
+    """One key far above all others, with value 0: the result is the others' share.
+    A weight is off by half a step, or by half of fp16's smallest step at 2^7
+    (2^-32 of the largest); sums and the exponential as in attn_reference."""
+    torch, ref, nys = _mods()
+    dt = getattr(torch, dtype)
+    n, d, page = 4096 if how == "prompt cut" else 1472, 64, 16
+    q = torch.zeros(1, 1, d, device=cuda_device, dtype=dt)
+    k = torch.zeros(n, 1, d, device=cuda_device, dtype=dt)
+    v = torch.ones(n, 1, d, device=cuda_device, dtype=dt)
+    q[..., 0], k[0, 0, 0], v[0] = 1, gap, 0
+    att = nys.ExactAttention(1, 1, d, d, dtype=dt, scale=1.0, device=cuda_device)
+    requests = 300 if how == "prefix" else 1
+    out = torch.empty(requests, 1, d, device=cuda_device, dtype=dt)
+    lse = torch.empty(requests, 1, device=cuda_device)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)
+    if how.startswith("prompt"):
+        att.prompt(q, k, v, i32([0, 1]), out, k_off=i32([0, n]), lse=lse)
+    else:
+        cache = nys.PagedKV(n // page, page, 1, d, d, dtype=dt, device=cuda_device,
+                            k=k.view(-1, page, 1, d), v=v.view(-1, page, 1, d))
+        pages = list(range(n // page))
+        if how == "pages":
+            att.shared(q, cache, i32([n]), i32([pages]), out, lse=lse)
+        else:
+            att.shared(q.expand(requests, 1, d).contiguous(), cache, i32([0] * requests),
+                       i32([[0]] * requests), out, prefix_pages=i32(pages), prefix_len=n, lse=lse)
+    w = math.exp(-float(k[0, 0, 0]))
+    total = 1 + (n - 1) * w
+    want = (n - 1) * w / total
+    half = 0.0 if dtype == "float32" else ref.EPS[dt]
+    weight = max(w * half, 2.0 ** -32 if dtype == "float16" else 0.0)
+    bound = ((n - 1) * weight / total + want * (ref.EPS[dt] + 2.0 ** -18 + n * 2.0 ** -23)
+             + (2.0 ** -25 if dtype == "float16" else 0.0))
+    err = float((out.double() - want).abs().max())
+    assert err <= bound, (err, bound, want)
+    assert float((lse.double() - float(k[0, 0, 0]) - math.log(total)).abs().max()) < 2.0 ** -17
+    assert att.status() == 0
