@@ -12,10 +12,13 @@
 //
 //   S' = Q' K'^T gives s_ij = S' 2^(eq + ek) scale log2(e), one multiplier a
 //   group of 16 keys.  The value's exponent goes into the weight:
-//   P_ij = 2^(s_ij + ev_j - m_i + 6), m_i the running maximum of s + ev, so
-//   that P V' is the plain sum at scale 2^(6 - m_i); l_i += P_ij 2^-ev_j.
-//   P is split into two pieces as the operands are; the 6 keeps small weights
-//   above fp16's smallest numbers (P stays below 2^14).
+//   P_ij = 2^(s_ij + ev_j - m_i + 15), m_i the running maximum of s + ev, so
+//   that P V' is the plain sum at scale 2^(15 - m_i); l_i += P_ij 2^-ev_j.
+//   P is split into two pieces as the operands are; 15 is the most that fp16 takes,
+//   so that keys by the thousand far below the largest still count (they are held
+//   down to 2^-40 of it, in 22 bits to 2^-18).  That takes the maximum itself: one that
+//   was followed only after a growth by 2^8 cost 8 of those bits and saved nothing
+//   here, where a new one rescales registers.
 //
 // The tensor cores cut sums towards zero, so O is taken out after each tile of
 // 128 keys (24 sums) and added to f32 accumulators in registers; a long row
@@ -83,8 +86,7 @@ __device__ __forceinline__ uint32_t turn_at(int row, int unit) {
 constexpr uint32_t kColQ = 0, kColS = 128, kColO = 384;  // tensor memory
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kLazy = 8.f;
-constexpr float kLift = 6.f;
+constexpr float kLift = 15.f;
 constexpr int kTop = 13;        // the largest value's power of two after scaling
 // A group of values that are all 0 has no exponent of its own.  It takes one that is
 // below those of values above 2^-47, so that its keys do not raise the reference above
@@ -895,9 +897,8 @@ __device__ void row_role(const TileArgs& a, Shared& sh, uint32_t tmem, int row, 
         top = fmaxf(top, other);
       }
       float alpha = 1.f;
-      const bool grow = m == -INFINITY ? top > m : top - m > kLazy;
-      if (__any_sync(0xffffffffu, grow)) {
-        alpha = top == m ? 1.f : ex2(m - top);
+      if (top > m) {
+        alpha = ex2(m - top);
         m = top;
         l *= alpha;
       }

@@ -304,7 +304,7 @@ def test_f32_call_without_units_before_another(cuda_device):
     assert att.status() == 0
 
 
-@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
 @pytest.mark.parametrize("gap", [10.0, 14.0, 17.4, 20.0])
 @pytest.mark.parametrize("how", ["prompt", "prompt cut", "pages", "prefix"])
 def test_many_keys_of_small_weight(cuda_device, dtype, gap, how):
