@@ -486,6 +486,14 @@ int nys_kv_plan(int64_t n, int32_t page, const int32_t* cached, const int32_t* f
 int nys_kv_write(const nys_attn_config* cfg, const nys_pool* pool, int64_t tokens,
                  const nys_rows* k, const nys_rows* v, const int64_t* slots, void* stream);
 
+/* Test hook, no counterpart on the pages: the first CTA of this process's next
+ * tiled attention launch (nys_attn_prompt, or the shared prefix of
+ * nys_attn_shared) issues no copies (role 1) or no products (role 2), so that its
+ * bounded waits run out after 2 s, it sets NYS_ATTN_GAVE_UP and leaves its
+ * units' rows unwritten.  Exercises the timeout path without faulting or hanging
+ * the GPU; the context stays usable.  Errors: NYS_E_INVAL. */
+int nys_debug_stall_attn_once(int32_t role);
+
 /* Static description of a status code.  Never NULL. */
 const char* nys_strerror(int status);
 

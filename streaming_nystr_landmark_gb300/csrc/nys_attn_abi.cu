@@ -172,6 +172,12 @@ int nys_attn_shared(const nys_attn_config* cfg, int64_t n, const nys_pool* pool,
   return e == cudaSuccess ? NYS_OK : NYS_E_CUDA;
 }
 
+int nys_debug_stall_attn_once(int32_t role) {
+  if (role != nys::kStallCopies && role != nys::kStallProducts) return NYS_E_INVAL;
+  nys::stall_next(role);
+  return NYS_OK;
+}
+
 int nys_kv_plan(int64_t n, int32_t page, const int32_t* cached, const int32_t* fresh,
                 const int32_t* free_pages, int64_t n_free, int32_t* table, int32_t width,
                 int64_t total, int32_t* q_off, int32_t* lens, int64_t* slots,

@@ -1,5 +1,6 @@
 // Host side of the tiled attention kernels: which calls they take, tensor maps
 // and launch shapes.
+#include <atomic>
 #include <cstdint>
 #include <cstring>
 
@@ -186,7 +187,15 @@ bool cut_tail(int64_t n, int64_t rows, int64_t keys, int kv_heads, int group, in
 // may differ.
 bool count_units(int64_t units) { return units > kSms; }
 
+std::atomic<int32_t> stalled{kStallNone};
+int32_t take_stall() {
+  return stalled.load(std::memory_order_relaxed) == kStallNone ? kStallNone
+                                                               : stalled.exchange(kStallNone);
+}
+
 }  // namespace
+
+void stall_next(int32_t what) { stalled.store(what); }
 
 // Images (f32), a counter, pieces of cut units.
 size_t prompt_workspace(const nys_attn_config& c, int64_t n, int64_t rows, int64_t keys) {
@@ -275,6 +284,7 @@ cudaError_t launch_shared_tiled(const SharedArgs& s, void* workspace, cudaStream
     a.v_head = s.dv;
     a.kv_y = 1;
     a.status = s.status;
+    a.stall = take_stall();
     a.q = s.q;
     a.per = query_tiles(s.dtype);
     const unsigned grid = (unsigned)o.shares.ctas;
@@ -337,6 +347,7 @@ cudaError_t launch_prompt_tc(const PromptArgs& p, void* workspace, cudaStream_t 
   a.v_head = p.v.head;
   a.kv_y = !(p.kv_heads > 1 && p.k.head == 0);
   a.status = p.status;
+  a.stall = take_stall();
   a.q = p.q;
   a.per = query_tiles(p.dtype);
   const int64_t units = prompt_units(p.n, p.q_rows, p.kv_heads, p.group, p.dtype);

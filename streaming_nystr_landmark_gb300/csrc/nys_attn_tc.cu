@@ -168,6 +168,7 @@ __device__ void load_role(const TileArgs& a, const CUtensorMap* mq, const CUtens
       for (int s = 0; s <= (pair ? 1 : 0); ++s)
         copy(sm + s * 32768, mq, a.d, a.group * a.tp, u.kvh * a.group, u.q_row + s * a.tp, &sh.q_full);
     }
+    if (a.stall == kStallCopies && blockIdx.x == 0) break;
     const int y = a.kv_y ? u.kvh : 0;
     if (PAGED) look(u.kb);
     bool ok = true;
@@ -246,7 +247,7 @@ __device__ void mma_role(const TileArgs& a, Shared& sh, unsigned char* sm, uint3
     if (!bar_wait(&sh.u_full[nu % kUnitRing], (nu / kUnitRing) & 1, ab)) break;
     const Unit u = sh.unit[nu % kUnitRing];
     bar_arrive(&sh.u_empty[nu % kUnitRing]);
-    if (!u.valid) break;
+    if (!u.valid || (a.stall == kStallProducts && blockIdx.x == 0)) break;
     const bool pair = u.np1 > 0;
     const int n_of[2] = {pair ? u.nt0 : (u.nt + 1) / 2, pair ? u.nt : u.nt / 2};
     if (u.nt > 0) {

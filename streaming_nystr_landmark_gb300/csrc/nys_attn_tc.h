@@ -80,7 +80,11 @@ struct TileArgs {
   int64_t k_row, k_head, v_row, v_head;
   int32_t kv_y;  // 0 where all KV heads share one head's rows (head stride 0)
   int32_t* status;
+  int32_t stall;  // test hook: what the first CTA withholds (kStall..)
 };
+enum : int32_t { kStallNone = 0, kStallCopies = 1, kStallProducts = 2 };
+// The next tiled launch's `stall`, once (any thread).
+void stall_next(int32_t what);
 
 // One unit: two query tiles of one KV head that read the same keys ("pair"),
 // or, where the second tile would be empty, one tile whose key tiles two

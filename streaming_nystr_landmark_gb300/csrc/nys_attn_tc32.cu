@@ -145,7 +145,7 @@ __device__ void load_role(const TileArgs& a, Shared& sh, unsigned char* sm) {
     const int valid = sh.unit[nu % kUnitRing].valid, nt = sh.unit[nu % kUnitRing].nt;
     const int64_t im = (int64_t)sh.unit[nu % kUnitRing].tile * a.kv_heads + sh.unit[nu % kUnitRing].kvh;
     bar_arrive(&sh.u_empty[nu % kUnitRing]);
-    if (!valid) break;
+    if (!valid || (a.stall == kStallCopies && blockIdx.x == 0)) break;
     if (nu == 0) wait_for_previous();  // the images
     for (int e = 0; e < 2 * nt; ++e) {
       bool is_k;
@@ -689,7 +689,7 @@ __device__ void mma_role(const TileArgs& a, Shared& sh, unsigned char* sm, uint3
     if (!bar_wait(&sh.u_full[nu % kUnitRing], (nu / kUnitRing) & 1, ab)) break;
     const int valid = sh.unit[nu % kUnitRing].valid, nt = sh.unit[nu % kUnitRing].nt;
     bar_arrive(&sh.u_empty[nu % kUnitRing]);
-    if (!valid) break;
+    if (!valid || (a.stall == kStallProducts && blockIdx.x == 0)) break;
     if (nt == 0) continue;
     if (!bar_wait(&sh.q_full, nq & 1, ab)) break;
     ++nq;

@@ -47,7 +47,8 @@ EXPORTED = ("nys_memory_bytes", "nys_alloc_states", "nys_free_states",
             "nys_o1_seal", "nys_o1_sealed", "nys_o1_step", "nys_o1_memory_bytes",
             "nys_o1_states", "nys_o1_free", "nys_debug_stall_once",
             "nys_debug_stall_replay_once", "nys_attn_workspace_bytes",
-            "nys_attn_prompt", "nys_attn_shared", "nys_kv_plan", "nys_kv_write")
+            "nys_attn_prompt", "nys_attn_shared", "nys_kv_plan", "nys_kv_write",
+            "nys_debug_stall_attn_once")
 
 
 class NysConfig(ctypes.Structure):
@@ -129,6 +130,7 @@ def _load():
                             P(NysRows), P(NysRows), VP, VP, ctypes.c_size_t, VP, VP],
         "nys_kv_plan": [I64, I32, VP, VP, VP, I64, VP, I32, I64, VP, VP, VP, VP, VP, VP, VP],
         "nys_kv_write": [P(NysAttnConfig), P(NysPool), I64, P(NysRows), P(NysRows), VP, VP],
+        "nys_debug_stall_attn_once": [I32],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -270,6 +272,10 @@ def nys_kv_plan(n, page, cached, fresh, free_pages, n_free, table, width, total,
     _check(_lib.nys_kv_plan(n, page, cached, fresh, free_pages, n_free, table, width, total,
                             q_off, lens, slots, positions, taken, status, stream or None),
            "nys_kv_plan")
+
+
+def nys_debug_stall_attn_once(role):
+    _check(_lib.nys_debug_stall_attn_once(role), "nys_debug_stall_attn_once")
 
 
 def nys_kv_write(cfg, pool, tokens, k, v, slots, stream=0):

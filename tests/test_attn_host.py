@@ -294,3 +294,8 @@ def test_tensors_of_another_device_are_refused(monkeypatch, name):
         with pytest.raises(ValueError, match="cuda:0"):
             fn(*args)
     assert fake.calls == []
+
+
+@pytest.mark.parametrize("role", [0, 3, -1])
+def test_stall_hook_refuses_unknown_roles(role):
+    assert nys._lib.nys_debug_stall_attn_once(role) == nys.NYS_E_INVAL
