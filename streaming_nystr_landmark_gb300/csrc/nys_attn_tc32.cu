@@ -100,10 +100,13 @@ constexpr uint32_t kOdd = 255;
 // beside a far larger one, and a column beside a far larger one, would be rounded to what
 // the larger one leaves: a group is odd where numbers lie more than kSpan powers of
 // two below its largest.  Single numbers do in any group; what counts is four columns
-// of a row (small_cells) and a column of 16 rows.  Weights are rounded at 2^-31 of the
-// largest contribution (weight and value), so a unit is odd where its groups' largest
-// values are more than kSpanUnit apart.  Products of exponents stay below f32's range.
-constexpr int kSpan = 13, kSpanUnit = 10;
+// of a row (small_cells) and a column of 16 rows.  (Without that, one value row or
+// column 2^10 above the rest leaves the other columns where they were, 2^12 five times,
+// 2^14 forty times, 2^16 a hundred times further off.)  Weights are rounded at 2^-40 of
+// the largest contribution (weight and value), so a unit is odd where its groups' largest
+// values are more than kSpanUnit apart and f32's last bits would go.  Products of
+// exponents stay below f32's range.
+constexpr int kSpan = 13, kSpanUnit = 16;
 constexpr int kLeastK = 40, kMostK = 187, kLeastV = 60;  // biased exponents
 
 struct Shared {

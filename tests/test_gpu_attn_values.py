@@ -345,3 +345,19 @@ def test_many_keys_of_small_weight(cuda_device, dtype, gap, how):
     assert err <= bound, (err, bound, want)
     assert float((lse.double() - float(k[0, 0, 0]) - math.log(total)).abs().max()) < 2.0 ** -17
     assert att.status() == 0
+
+
+@pytest.mark.parametrize("size", SIZES)
+@pytest.mark.parametrize("rows", [slice(16, 32), slice(128, 256)])
+def test_f32_large_values_without_a_column(cuda_device, size, rows):
+    """A group of keys, or a tile, of large values that has nothing in one column:
+    there the other keys' values are all there is."""
+    torch, ref, nys = _mods()
+    n, heads, kv, d = 300, 2, 1, 64
+    q, k, v = _rand(torch, cuda_device, n, heads, kv, d)
+    v[rows] *= size
+    v[rows, :, 3] = 0
+    want, wl, b, lb = ref.prompt(q, k, v, [n], [n], heads, 1 / math.sqrt(d), torch.float32)
+    out, lse = _prompt(torch, nys, q, k, v, [n], [n])
+    ref.check(out, want, b, "out")
+    ref.check(lse, wl, lb, "lse")
