@@ -133,6 +133,17 @@ static_assert(kSmem <= 227 * 1024, "one CTA's shared memory");
 __device__ __forceinline__ uint32_t k_at(int j) { return j < 2 ? j : 2 * j - 1; }
 __device__ __forceinline__ uint32_t v_at(int j, int nt) { return min(2 * j + 2, 2 * nt - 1); }
 
+__device__ __forceinline__ float4 shared_load4(uint32_t at) {
+  float4 x;
+  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+               : "r"(at));
+  return x;
+}
+__device__ __forceinline__ void shared_store4(uint32_t at, float4 x) {
+  asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(at), "f"(x.x), "f"(x.y), "f"(x.z), "f"(x.w)
+               : "memory");
+}
 __device__ __forceinline__ bool finite_bits(float x) {
   return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u;
 }
@@ -261,7 +272,7 @@ __device__ __forceinline__ float finite_max(float4 x) {
 // keys that it sees and no others.  Eight rows at a time, two keys a step, which come
 // through shared memory (`turn`) and are asked for a step ahead: four lanes have a
 // row, each a quarter of its columns.  Right for everything and fast for nothing: 64
-// prompts of 256 with a flag each take 3.3 ms (159 us without), 4 of 4,096 61 ms (0.56
+// prompts of 256 with a flag each take 2.9 ms (162 us without), 4 of 4,096 49 ms (0.56
 // ms).  Its beats tell the waiting warps that it goes on.  (A call: inlined, its code costs the
 // tiles 1%, 64 prompts of 256 158.8 -> 160.5 us.)
 template <bool PAGED>
@@ -276,8 +287,8 @@ __device__ __noinline__ void exact_rows(const TileArgs& a, const Unit& u, unsign
   const float* k_lane = (const float*)a.k_raw + u.kvh * a.k_head + lane * 4;
   const float* v_lane = (const float*)a.v_raw + u.kvh * a.v_head + lane * 4;
   const bool k_col = lane * 4 < d, v_col = lane * 4 < dv;
-  float4* mine = reinterpret_cast<float4*>(turn) + lane;           // [key or value][512 bytes]
-  const float4* quarter = reinterpret_cast<const float4*>(turn) + (lane & 3);
+  const uint32_t mine = sptr(turn) + lane * 16;  // [key or value][512 bytes]
+  const uint32_t quarter = sptr(turn) + (lane & 3) * 16;
   const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
   // Row of key j of the piece; -1 where its page is not in the pool.
   auto key_row = [&](int j) {
@@ -320,8 +331,8 @@ __device__ __noinline__ void exact_rows(const TileArgs& a, const Unit& u, unsign
       __syncwarp();
 #pragma unroll
       for (int j = 0; j < kKeys; ++j) {
-        mine[j * 32] = kx[j];
-        mine[(kKeys + j) * 32] = vx[j];
+        shared_store4(mine + j * 512, kx[j]);
+        shared_store4(mine + (kKeys + j) * 512, vx[j]);
       }
       __syncwarp();
       ask(k0 + kKeys);
@@ -329,13 +340,16 @@ __device__ __noinline__ void exact_rows(const TileArgs& a, const Unit& u, unsign
 #pragma unroll
       for (int j = 0; j < kKeys; ++j) sum[j] = pair(0.f, 0.f);
 #pragma unroll
-      for (int c = 0; c < kCols; ++c)
+      for (int c = 0; c < kCols; c += 2) {
+        float4 x[2 * kKeys];
 #pragma unroll
-        for (int j = 0; j < kKeys; ++j) {
-          const float4 x = quarter[j * 32 + c * 4];
-          sum[j] = fma2(q[2 * c], pair(x.x, x.y), sum[j]);
-          sum[j] = fma2(q[2 * c + 1], pair(x.z, x.w), sum[j]);
+        for (int j = 0; j < 2 * kKeys; ++j) x[j] = shared_load4(quarter + (j >> 1) * 512 + (c + (j & 1)) * 64);
+#pragma unroll
+        for (int j = 0; j < 2 * kKeys; ++j) {
+          sum[j >> 1] = fma2(q[2 * (c + (j & 1))], pair(x[j].x, x[j].y), sum[j >> 1]);
+          sum[j >> 1] = fma2(q[2 * (c + (j & 1)) + 1], pair(x[j].z, x[j].w), sum[j >> 1]);
         }
+      }
       float y[kKeys], top = m;
 #pragma unroll
       for (int j = 0; j < kKeys; ++j) {
@@ -363,10 +377,15 @@ __device__ __noinline__ void exact_rows(const TileArgs& a, const Unit& u, unsign
       for (int j = 0; j < kKeys; ++j)
         if (k0 + j < lim) {  // (0 x NaN is NaN)
 #pragma unroll
-          for (int c = 0; c < kCols; ++c) {
-            const float4 x = quarter[(kKeys + j) * 32 + c * 4];
-            acc[2 * c] = fma2(pair(y[j], y[j]), pair(x.x, x.y), acc[2 * c]);
-            acc[2 * c + 1] = fma2(pair(y[j], y[j]), pair(x.z, x.w), acc[2 * c + 1]);
+          for (int c = 0; c < kCols; c += 4) {
+            float4 x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = shared_load4(quarter + (kKeys + j) * 512 + (c + i) * 64);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              acc[2 * (c + i)] = fma2(pair(y[j], y[j]), pair(x[i].x, x[i].y), acc[2 * (c + i)]);
+              acc[2 * (c + i) + 1] = fma2(pair(y[j], y[j]), pair(x[i].z, x[i].w), acc[2 * (c + i) + 1]);
+            }
           }
         }
     }
