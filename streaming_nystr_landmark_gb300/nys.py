@@ -724,6 +724,8 @@ class ExactAttention(_Status):
 
     def __init__(self, heads, kv_heads, d, dv, dtype=None, scale=None, device="cuda"):
         import torch
+        if scale is not None and not 0 < scale < float("inf"):
+            raise ValueError(f"scale {scale}: need a positive number, or None for 1/sqrt(d)")
         self.torch = torch
         self.dtype = torch.float32 if dtype is None else dtype
         self.device = _cuda_device(device)

@@ -299,3 +299,11 @@ def test_tensors_of_another_device_are_refused(monkeypatch, name):
 @pytest.mark.parametrize("role", [0, 3, -1])
 def test_stall_hook_refuses_unknown_roles(role):
     assert nys._lib.nys_debug_stall_attn_once(role) == nys.NYS_E_INVAL
+
+
+@pytest.mark.parametrize("scale", [0.0, -1.0, float("nan"), float("inf")])
+def test_scale_has_to_be_positive(scale):
+    """0 stands for 1/sqrt(d) in the C call: given here it was taken for that."""
+    pytest.importorskip("torch")
+    with pytest.raises(ValueError, match="scale"):
+        nys.ExactAttention(2, 2, 8, 8, scale=scale)
