@@ -803,6 +803,8 @@ class ExactAttention(_Status):
             raise ValueError("out must have q's rows, and table be [n][width]")
         pages = None
         if prefix_len > 0:
+            if prefix_pages is None:
+                raise ValueError("prefix_pages: needed for a prefix")
             pages = _ints(prefix_pages, torch.int32, prefix_pages.shape[:1], "prefix_pages", index)
             if prefix_pages.shape[0] * cache.page < prefix_len:
                 raise ValueError("prefix_pages: too few pages for prefix_len")

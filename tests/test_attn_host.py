@@ -307,3 +307,12 @@ def test_scale_has_to_be_positive(scale):
     pytest.importorskip("torch")
     with pytest.raises(ValueError, match="scale"):
         nys.ExactAttention(2, 2, 8, 8, scale=scale)
+
+
+def test_prefix_without_pages_is_refused(monkeypatch):
+    fake, calls = _objects(monkeypatch, 0)
+    fn, args = calls["nys_attn_shared"]
+    args[5] = None
+    with pytest.raises(ValueError, match="prefix_pages"):
+        fn(*args)
+    assert fake.calls == []
