@@ -12,13 +12,14 @@
 //
 //   S' = Q' K'^T gives s_ij = S' 2^(eq + ek) scale log2(e), one multiplier a
 //   group of 16 keys.  The value's exponent goes into the weight:
-//   P_ij = 2^(s_ij + ev_j - m_i + 15), m_i the running maximum of s + ev, so
-//   that P V' is the plain sum at scale 2^(15 - m_i); l_i += P_ij 2^-ev_j.
-//   P is split into two pieces as the operands are; 15 is the most that fp16 takes,
-//   so that keys by the thousand far below the largest still count (they are held
-//   down to 2^-40 of it, in 22 bits to 2^-18).  That takes the maximum itself: one that
-//   was followed only after a growth by 2^8 cost 8 of those bits and saved nothing
-//   here, where a new one rescales registers.
+//   P_ij = 2^15 2^(s_ij + ev_j - m_i), m_i the running maximum of s + ev, so that P V'
+//   is the plain sum at scale 2^(15 - m_i); l_i += P_ij 2^-ev_j.
+//   P is split into two pieces as the operands are; 2^15 is the most that fp16
+//   takes, so that keys by the thousand far below the largest still count (they are
+//   held down to 2^-40 of it, in 22 bits to 2^-18).  That takes the maximum itself: one
+//   that was followed only after a growth by 2^8 cost 8 of those bits and saved nothing
+//   here, where a new one rescales registers.  (Added to the exponent instead, the 15
+//   would round it: error of 64 prompts of 256 3.0e-7 -> 3.5e-7.)
 //
 // The tensor cores cut sums towards zero, so O is taken out after each tile of
 // 128 keys (24 sums) and added to f32 accumulators in registers; a long row
@@ -86,7 +87,7 @@ __device__ __forceinline__ uint32_t turn_at(int row, int unit) {
 constexpr uint32_t kColQ = 0, kColS = 128, kColO = 384;  // tensor memory
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kLift = 15.f;
+constexpr int kLift = 15;
 constexpr int kTop = 13;        // the largest value's power of two after scaling
 // A group of values that are all 0 has no exponent of its own.  It takes one that is
 // below those of values above 2^-47, so that its keys do not raise the reference above
@@ -822,6 +823,18 @@ __device__ void unit_role(const TileArgs& a, Shared& sh, UnitSource& source, int
   }
 }
 
+// Log of a row's sum l 2^(m - kLift).  m and l each hold the values' exponents, one up
+// and one down: whole powers of two meet m first, so that what is left has the size of the
+// result and is rounded there.  (This is what pieces are joined by: error of 100 requests
+// over a prefix of 8,000 8.7e-7 -> 5.4e-7.)
+__device__ __forceinline__ float log_sum(float m, float l) {
+  const uint32_t bits = __float_as_uint(l);
+  const int e = (int)(bits >> 23) - 127;
+  if (l == 0.f) return -INFINITY;
+  if (!finite_bits(l)) return l;
+  return ((m + (float)(e - kLift)) + lg2(__uint_as_float((bits & 0x7FFFFFu) | 0x3F800000u))) * kLn2;
+}
+
 // ---- softmax and accumulation (two warpgroups, two threads a row:
 // `half` takes keys 64 * half .. of each tile and value columns 64 * half ..)
 __device__ void row_role(const TileArgs& a, Shared& sh, uint32_t tmem, int row, int half,
@@ -924,7 +937,7 @@ __device__ void row_role(const TileArgs& a, Shared& sh, uint32_t tmem, int row, 
         m = top;
         l *= alpha;
       }
-      const float ref = (m == -INFINITY ? 0.f : m) - kLift;
+      const float ref = m == -INFINITY ? 0.f : m;
       // A group of 16 keys at a time, the next one's scores on their way: P's
       // pieces take the group's own 16 columns.
       uint32_t xa[16], xb[16];
@@ -933,14 +946,16 @@ __device__ void row_role(const TileArgs& a, Shared& sh, uint32_t tmem, int row, 
         const float f = fmaxf(km[g] * qm, 1e-36f), z = (float)ev - ref;
         uint32_t p[16];
         const uint64_t f2 = pair(f, f), z2 = pair(z, z), minus2 = pair(-1.f, -1.f);
+        const uint64_t lift2 = pair((float)(1 << kLift), (float)(1 << kLift));
         uint64_t sum = pair(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
           float y0, y1, r0, r1;
           unpair(fma2(pair(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), f2, z2), y0, y1);
-          const float p0 = ex2(y0), p1 = ex2(y1);
-          const uint64_t w = pair(p0, p1);
+          const uint64_t w = mul2(pair(ex2(y0), ex2(y1)), lift2);
           sum = add2(sum, w);
+          float p0, p1;
+          unpair(w, p0, p1);
           const float h0 = cut11(p0), h1 = cut11(p1);
           unpair(fma2(pair(h0, h1), minus2, w), r0, r1);
           p[i / 2] = Type16<__half>::pack(h0, h1);
@@ -1003,7 +1018,7 @@ __device__ void row_role(const TileArgs& a, Shared& sh, uint32_t tmem, int row, 
         !(nt > 0 && sh.q_odd[(nq - 1) & 3][row >> 5])) {
       const int64_t orow = (int64_t)u.q_row + pos;
       const int head = u.kvh * a.group + hd;
-      const float v = l == 0.f ? -INFINITY : (m - kLift + lg2(l)) * kLn2;
+      const float v = log_sum(m, l);
       if (u.slot >= 0) a.part_lse[(int64_t)u.slot * kTileM + row] = v;
       else if (a.lse) a.lse[orow * a.heads + head] = v;
     }
