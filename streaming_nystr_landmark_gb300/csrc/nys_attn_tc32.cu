@@ -99,15 +99,15 @@ constexpr int kZeroExp = -60, kZeroLow = kZeroExp, kZeroHigh = 30;
 constexpr uint32_t kOdd = 255;
 // fp16 holds a piece lo of a number at 2^-38 of its group's largest at best, so a key
 // beside a far larger one, and a column beside a far larger one, would be rounded to what
-// the larger one leaves: a group is odd where numbers lie more than kSpan powers of
-// two below its largest.  Single numbers do in any group; what counts is four columns
-// of a row (small_cells) and a column of 16 rows.  (Without that, one value row or
-// column 2^10 above the rest leaves the other columns where they were, 2^12 five times,
-// 2^14 forty times, 2^16 a hundred times further off.)  Weights are rounded at 2^-40 of
-// the largest contribution (weight and value), so a unit is odd where its groups' largest
-// values are more than kSpanUnit apart and f32's last bits would go.  Products of
-// exponents stay below f32's range.
-constexpr int kSpan = 13, kSpanUnit = 16;
+// the larger one leaves: a group of values is odd where more numbers than chance puts
+// there (chance_of) lie over kSpanV powers of two below its largest.  (Without that, one
+// value row or column 2^10 above the rest leaves the other columns where they were, 2^12
+// five times, 2^14 forty times, 2^16 a hundred times further off.)  Groups of keys, and
+// query rows, are sums' operands and take kSpanK: 2^18 there leaves results where they
+// were.  Weights are rounded at 2^-40 of the largest contribution (weight and value), so
+// a unit is odd where its groups' largest values are more than kSpanUnit apart and f32's
+// last bits would go.  Products of exponents stay below f32's range.
+constexpr int kSpanV = 13, kSpanK = 17, kSpanUnit = 16;
 constexpr int kLeastK = 40, kMostK = 187, kLeastV = 60;  // biased exponents
 
 struct Shared {
@@ -214,20 +214,22 @@ __device__ __forceinline__ float exp_of(int e) {  // 2^e, -126 <= e <= 127
 __device__ __forceinline__ float back_of(int ex) {
   return __uint_as_float((uint32_t)(ex - kTop) << 23);
 }
-// The largest magnitude of four columns, NaN if one is.
-__device__ __forceinline__ float cell_of(float4 x) {
-  return max3_abs_nan(max3_abs_nan(0.f, x.x, x.y), x.z, x.w);
+// Magnitudes below this are small against a largest one of biased exponent ex.
+__device__ __forceinline__ float small_below(int ex, int span) {
+  return __uint_as_float(ex > span ? (uint32_t)(ex - span) << 23 : 0u);
 }
-// Magnitudes below this are small against a largest one of biased exponent ex; 0 is
-// none.
-__device__ __forceinline__ float small_below(int ex) {
-  return __uint_as_float(ex > kSpan ? (uint32_t)(ex - kSpan) << 23 : 0u);
+// How many of four are; zeros, which any scale holds, among them or not.
+template <bool ZEROS>
+__device__ __forceinline__ int count_small(float4 x, float below) {
+  auto is = [&](float y) { return (int)((ZEROS || y != 0.f) && fabsf(y) < below); };
+  return is(x.x) + is(x.y) + is(x.z) + is(x.w);
 }
-__device__ __forceinline__ bool is_small(float x, float below) { return x != 0.f && fabsf(x) < below; }
-// How many cells of `rows` rows' numbers are few enough to be chance (in numbers drawn
-// from one distribution a cell is small once in 10^14, or in some 10^4 where zeros
-// leave it one number).
-__device__ __forceinline__ int small_cells(int dim) { return (dim + 31) / 32; }
+// From how many small ones of `numbers` on it is no chance.  Normal numbers of one size
+// are below 2^-13 of the largest of 2,048 once in 3,000: more than 11 of 2,048, or 3 of
+// 128, come once in some 10^7 groups; below 2^-17, 4 of 2,048, or 2 of 128.
+__device__ __forceinline__ int chance_of(int numbers, bool values) {
+  return values ? 3 + (numbers > 32) + numbers / 256 : 3 + numbers / 1024;
+}
 // Four scaled values as hi and lo words; DROP: 0 for infinities and NaN, which
 // else do not occur.
 template <bool DROP>
@@ -518,23 +520,25 @@ __device__ void query_role(const TileArgs& a, Shared& sh, unsigned char* turn, u
       for (int i = 0; i < 4; ++i) {
         float t = 0.f, least = INFINITY;  // (zeros count: the check itself is rare enough)
 #pragma unroll
-        for (int c = 0; c < 8; c += 2) {
-          const float y = cell_of(x[c * 4 + i]), z = cell_of(x[c * 4 + 4 + i]);
-          t = max3_abs_nan(t, y, z);
-          least = min3(least, y, z);
+        for (int c = 0; c < 8; ++c) {
+          const float4 y = x[c * 4 + i];
+          t = max3_abs_nan(t, y.x, y.y);
+          t = max3_abs_nan(t, y.z, y.w);
+          least = min3_abs(least, y.x, y.y);
+          least = min3_abs(least, y.z, y.w);
         }
         uint32_t top = __float_as_uint(t) & 0x7FFFFFFFu;
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int e = (int)(top >> 23);
-        const float below = small_below(e);
+        const float below = small_below(e, kSpanK);
         if (__any_sync(0xffffffffu, least < below)) {
-          int small = 0;  // a row's cells are on four lanes
+          int small = 0;  // a row's columns are on four lanes
 #pragma unroll
-          for (int c = 0; c < 8; ++c) small += is_small(cell_of(x[c * 4 + i]), below);
+          for (int c = 0; c < 8; ++c) small += count_small<false>(x[c * 4 + i], below);
           small += __shfl_xor_sync(0xffffffffu, small, 1);
           small += __shfl_xor_sync(0xffffffffu, small, 2);
-          odd |= small >= small_cells(a.d);
+          odd |= small >= chance_of(a.d, false);
         }
         odd |= (top != 0 && e < kLeastK) || e > kMostK;  // (infinities, NaN too)
         // (127 marks a query with a value that is not finite, whatever S then holds)
@@ -635,17 +639,13 @@ __global__ void __launch_bounds__(256, 3) split_kernel(const __grid_constant__ T
     x[r] = o >= 0 && col ? __ldcs(reinterpret_cast<const float4*>(src + o * stride))
                          : make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  float column[4] = {0.f, 0.f, 0.f, 0.f};
+  float largest = 0.f;
 #pragma unroll
-  for (int r = 0; r < kGroup; r += 2) {
-    column[0] = max3_abs_nan(column[0], x[r].x, x[r + 1].x);
-    column[1] = max3_abs_nan(column[1], x[r].y, x[r + 1].y);
-    column[2] = max3_abs_nan(column[2], x[r].z, x[r + 1].z);
-    column[3] = max3_abs_nan(column[3], x[r].w, x[r + 1].w);
+  for (int r = 0; r < kGroup; ++r) {
+    largest = max3_abs_nan(largest, x[r].x, x[r].y);
+    largest = max3_abs_nan(largest, x[r].z, x[r].w);
   }
-  uint32_t top = __reduce_max_sync(
-      0xffffffffu,
-      __float_as_uint(cell_of(make_float4(column[0], column[1], column[2], column[3]))) & 0x7FFFFFFFu);
+  uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(largest) & 0x7FFFFFFFu);
   const bool bad = top >= 0x7F800000u;
   bool odd = bad;
   if (bad) {
@@ -655,21 +655,17 @@ __global__ void __launch_bounds__(256, 3) split_kernel(const __grid_constant__ T
     top = __reduce_max_sync(0xffffffffu, __float_as_uint(f));
   } else {
     const int e = (int)(top >> 23);
-    const float below = small_below(e);
-    float least = INFINITY;  // (zeros count here: the check itself is rare enough)
+    const float below = small_below(e, is_v ? kSpanV : kSpanK);
+    const int chance = chance_of(max(min(rows, kGroup), 0) * dim, is_v);
+    int small = 0;  // with zeros first: few groups have any
 #pragma unroll
-    for (int r = 0; r < kGroup; r += 2) least = min3(least, cell_of(x[r]), cell_of(x[r + 1]));
-    if (__any_sync(0xffffffffu, col && least < below)) {
-      int small = 0;
+    for (int r = 0; r < kGroup; ++r) small += count_small<true>(x[r], below);
+    if (__reduce_add_sync(0xffffffffu, col ? small : 0) >= chance) {
+      small = 0;
 #pragma unroll
-      for (int r = 0; r < kGroup; ++r) small += is_small(cell_of(x[r]), below);
-      odd = __reduce_add_sync(0xffffffffu, small) >= small_cells(dim);
+      for (int r = 0; r < kGroup; ++r) small += count_small<false>(x[r], below);
+      odd = __reduce_add_sync(0xffffffffu, small) >= chance;
     }
-    // (In fewer rows than 16 a column may be small by chance.)
-    const float narrow = min3(min3(INFINITY, column[0], column[1]), column[2], column[3]);
-    if (rows == kGroup && __any_sync(0xffffffffu, col && narrow < below))
-      odd |= __any_sync(0xffffffffu, is_small(column[0], below) || is_small(column[1], below) ||
-                                         is_small(column[2], below) || is_small(column[3], below));
     odd |= is_v ? top != 0 && e < kLeastV : (top != 0 && e < kLeastK) || e > kMostK;
   }
   const int ex = top_exponent(top);

@@ -361,3 +361,25 @@ def test_f32_large_values_without_a_column(cuda_device, size, rows):
     out, lse = _prompt(torch, nys, q, k, v, [n], [n])
     ref.check(out, want, b, "out")
     ref.check(lse, wl, lb, "lse")
+
+
+@pytest.mark.parametrize("d", [4, 8, 20])
+@pytest.mark.parametrize("n", [1, 2, 7, 30])
+@pytest.mark.parametrize("size", [1e6, 1e12, 1e18])
+@pytest.mark.parametrize("where", ["one column", "every fourth", "a diagonal"])
+def test_f32_few_numbers_of_other_sizes(cuda_device, d, n, size, where):
+    """Narrow and short: every row, every column and every four numbers may hold a
+    large one."""
+    torch, ref, nys = _mods()
+    q, k, v = _rand(torch, cuda_device, n, 2, 1, d)
+    if where == "one column":
+        v[..., 1] *= size
+    elif where == "every fourth":
+        v[..., ::4] *= size
+    else:
+        for i in range(n):
+            v[i, :, i % 4::4] *= size
+    want, wl, b, lb = ref.prompt(q, k, v, [n], [n], 2, 1 / math.sqrt(d), torch.float32)
+    out, lse = _prompt(torch, nys, q, k, v, [n], [n])
+    ref.check(out, want, b, "out")
+    ref.check(lse, wl, lb, "lse")
