@@ -121,7 +121,6 @@ struct Shared {
   int patch[kUnitRing];  // results are computed in f32 by the query warps (exact_rows)
   alignas(16) TileExps exps[4];      // of tile & 3
   int8_t q_exp[4][kTileM];           // eq, [unit & 3][row]: the query warps run up to three units ahead
-  uint8_t q_odd[4][4];               // [unit & 3][query warp]: computes its rows in f32
   float mx[2][2][kTileM];            // halves' maxima [exchange & 1][half][row], also of l
   uint32_t tmem;
   Beats beats;
@@ -547,7 +546,6 @@ __device__ void query_role(const TileArgs& a, Shared& sh, unsigned char* turn, u
       }
       odd = __any_sync(0xffffffffu, odd);
       odd_now = odd;
-      if (lane == 0) sh.q_odd[n_q & 3][warp] = odd;
       __syncwarp();
       const int qe = sh.q_exp[n_q & 3][warp * 32 + lane];
       const float scale = qe == 127 ? NAN : exp_of(-qe);
@@ -987,6 +985,15 @@ __device__ void row_role(const TileArgs& a, Shared& sh, uint32_t tmem, int row, 
         }
       }
     }
+    // The log-sum, before r_full: where the query warps compute the row themselves they
+    // put theirs in its place afterwards.
+    auto write_lse = [&](float v) {
+      if (half != 0 || pos >= u.np0) return;
+      const int64_t orow = (int64_t)u.q_row + pos;
+      if (u.slot >= 0) a.part_lse[(int64_t)u.slot * kTileM + row] = v;
+      else if (a.lse) a.lse[orow * a.heads + u.kvh * a.group + hd] = v;
+    };
+    if (nt == 0) write_lse(-INFINITY);
     if (nt > 0) {
       ++nq;
       float other;
@@ -1003,20 +1010,11 @@ __device__ void row_role(const TileArgs& a, Shared& sh, uint32_t tmem, int row, 
           for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(acc[c + i] * inv);
           st16(at + kColO + half * 64 + c, o);
         }
+      write_lse(log_sum(m, l));
       wait_st();
       fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive(&sh.r_full);
-    }
-    if (half == 0 && !bar_wait_warp(&sh.patch_full[nu % kUnitRing], (nu / kUnitRing) & 1, ab)) return;
-    // (Unless the query warps compute the row.)
-    if (half == 0 && pos < u.np0 && !sh.patch[nu % kUnitRing] &&
-        !(nt > 0 && sh.q_odd[(nq - 1) & 3][row >> 5])) {
-      const int64_t orow = (int64_t)u.q_row + pos;
-      const int head = u.kvh * a.group + hd;
-      const float v = log_sum(m, l);
-      if (u.slot >= 0) a.part_lse[(int64_t)u.slot * kTileM + row] = v;
-      else if (a.lse) a.lse[orow * a.heads + head] = v;
     }
     __syncwarp();
     if (lane == 0) bar_arrive(&sh.u_empty[nu % kUnitRing]);
