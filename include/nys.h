@@ -365,12 +365,22 @@ int nys_o1_free(nys_o1* o);
  * calls.
  *
  * Tensors are fp32, bf16 or fp16 (nys_dtype), all tensors of one call alike;
- * query head h reads KV head h / (heads / kv_heads).  Products are taken of
- * the stored values and summed in fp32; the softmax runs in fp32 (16-bit
- * types round its weights once, to the same type, for the second product).
+ * query head h reads KV head h / (heads / kv_heads).  Sums and the softmax run
+ * in fp32.  16-bit types: products of the stored values; the softmax's weights
+ * are rounded once, to the same type, for the second product (off by half a step
+ * of it, in fp16 by 2^-32 of the row's largest where that is more).  fp32: the
+ * tiled kernels take numbers as pairs of 11-bit pieces, so that a product is good
+ * to 2^-21 at worst and 2^-24 in the mean, and a number to 2^-38 of the largest of
+ * its 16 rows (keys, values) or its row (queries); weights are held to 2^-40 of the
+ * row's largest contribution.  Rows where that would show (numbers further apart
+ * than chance puts them, infinities, NaN) are computed in plain fp32 instead,
+ * which takes 20 to 90 times as long for the rows concerned.
  * The conventions at the top hold, except that pointers need only their
- * element type's alignment: rows that are 16-byte aligned and head dims up to
- * 128 take the tiled kernels, everything else a general one. */
+ * element type's alignment.  Rows that are 16-byte aligned and head dims up to
+ * 128 (multiples of 8 in 16-bit types) take the tiled kernels, and so does a
+ * prefix in 16-bit pages of a multiple of 8 tokens, or one that is short for its
+ * requests; everything else takes a general one, which is slow (8 prompts of 512
+ * tokens, 16 heads of 256: 15 ms).  Outputs overlap no input. */
 typedef enum { NYS_F32 = 0, NYS_BF16 = 1, NYS_F16 = 2 } nys_dtype;
 
 typedef struct {
@@ -434,12 +444,13 @@ int nys_attn_workspace_bytes(const nys_attn_config* cfg, int64_t n, int64_t rows
  * n + 1 int32, ascending within [0, q_rows] and [0, k_rows]; rows that no
  * sequence covers are not written.  out [q_rows][heads][dv] as given by its
  * strides; lse, if not NULL, fp32 [q_rows][heads], receives the log of the
- * softmax's denominator.  Values of keys that a row does not see never reach
- * it, whatever they are.
+ * softmax's denominator.  Keys and values that a row does not see never reach
+ * it, whatever they are (in fp32 they may decide which way it is computed, a
+ * matter of its last bits).
  * workspace: nys_attn_workspace_bytes(cfg, n, q_rows, k_rows) bytes, 256-byte
  * aligned.  Less or NULL is allowed: f32 then takes the general kernel, and
  * work is spread over the CTAs beforehand.
- * Errors: NYS_E_INVAL, NYS_E_UNSUPPORTED, NYS_E_ALIGN (workspace), NYS_E_CUDA. */
+ * Errors: NYS_E_INVAL, NYS_E_UNSUPPORTED, NYS_E_ALIGN, NYS_E_CUDA. */
 int nys_attn_prompt(const nys_attn_config* cfg, int64_t n, int64_t q_rows, int64_t k_rows,
                     const int32_t* q_off, const int32_t* k_off, const nys_rows* q,
                     const nys_rows* k, const nys_rows* v, const nys_rows* out, float* lse,
@@ -482,7 +493,7 @@ int nys_kv_plan(int64_t n, int32_t page, const int32_t* cached, const int32_t* f
 /* Write `tokens` new rows k and v into the pool's slots (slot s is row s mod
  * page of page s / page); tokens whose slot lies outside the pool (-1) are
  * skipped.  Of two tokens with one slot either may stay.  Errors: NYS_E_INVAL,
- * NYS_E_UNSUPPORTED, NYS_E_CUDA. */
+ * NYS_E_UNSUPPORTED, NYS_E_ALIGN, NYS_E_CUDA. */
 int nys_kv_write(const nys_attn_config* cfg, const nys_pool* pool, int64_t tokens,
                  const nys_rows* k, const nys_rows* v, const int64_t* slots, void* stream);
 

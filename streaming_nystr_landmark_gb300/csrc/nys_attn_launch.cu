@@ -177,7 +177,7 @@ int64_t prompt_units(int64_t n, int64_t rows, int kv_heads, int group, int dtype
 // is all of them.  It pays where rounds are few and long: 2 prompts' last 1,021 and
 // 1,500 tokens over 5,003 earlier ones, f32, 320 units of 45 tiles on 152 CTAs,
 // take 303 us whole and 277 us cut (whole calls, the join's 11 us among them); one
-// new token over 4,000, 8 KV heads, 72 and 29 us, over 30,000 in bf16 183 and 38 us;
+// new token over 4,000, 8 KV heads, 72 and 32 us, over 30,000 in bf16 183 and 38 us;
 // over 1,100, f32 28 and 25 us, but bf16 15.5 and 16.3 us.
 bool cut_tail(int64_t n, int64_t rows, int64_t keys, int kv_heads, int group, int dtype) {
   const int64_t units = prompt_units(n, rows, kv_heads, group, dtype);

@@ -4,13 +4,14 @@
 //   for pieces x with maxima m_x, sums l_x and O_x = sum_j 2^{s_j - m_x} v_j:
 //   out = sum_x 2^{m_x - m} O_x / sum_x 2^{m_x - m} l_x,  m = max_x m_x.
 //
-// Bound by HBM: a request's keys and values are read once for all heads of
-// the group, and there is little arithmetic a byte.  A CTA of four warps
+// Bound by HBM: a request's keys and values are read once for the heads of a
+// group (8 of them in f32, 16 in 16-bit types; wider groups read them again), and there
+// is little arithmetic a byte.  A CTA of four warps
 // takes one (request, KV head, piece of its keys); each warp streams tiles of
 // its own through a private ring in shared memory with cp.async, no barrier
 // between warps until their results are joined; three CTAs a SM keep the reads
 // in flight.  64 requests of 97 to 1025 keys over a prefix of 2,000 (8 KV heads of
-// 128, f32): 42 us for 208 MB from memory, 64% of its peak, and 60 us for the whole
+// 128, f32): 43 us for 208 MB from memory, 62% of its peak, and 60 us for the whole
 // call (floor 33 us).  Pieces of a request are joined by a second launch,
 // or, where all CTAs run at once, in shared memory as a cluster (4 requests of 3 to
 // 45 keys over a prefix of 301, bf16: 6.6 us, 8.3 us with the launch).

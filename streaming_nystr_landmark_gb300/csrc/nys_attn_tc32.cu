@@ -31,16 +31,16 @@
 // zero), with its eight groups' exponents beside it.  Done inside the attention
 // kernel instead, each query tile converting what it reads, the conversion took
 // longer than the products (a tile of keys 6,400 clocks against 3,600).  It runs
-// at the memory's rate: 64 prompts of 256 tokens, 8 KV heads of 128: 40 us, 134 MB
-// read and as much written (77 MB of it during the kernel, the rest stays in L2).
+// at the memory's rate: 64 prompts of 256 tokens, 8 KV heads of 128: 42 us, 134 MB
+// read and as much written (76 MB of it during the kernel, the rest stays in L2).
 //
 // attn_tc32_kernel: one CTA of 512 threads a SM works on one query tile of 128
 // rows (positions x heads of the group): warps 0-7 softmax and accumulation (two
 // threads a row: each takes half the tile's keys for the weights and half the
 // value columns for the sums), 8-11 the query tile's pieces and the results'
 // stores, 12 products, 13 units of work, 14 copies.  The products bound it where
-// prompts are long (2 prompts continued over 5,003 tokens: 218 us, tensor pipe 82%
-// busy), each unit's chain of steps where they are short (64 prompts of 256: 156 us
+// prompts are long (2 prompts continued over 5,003 tokens: 224 us, tensor pipe 80%
+// busy), each unit's chain of steps where they are short (64 prompts of 256: 162 us
 // with the split).  Q goes straight into tensor memory, because a
 // product with A there takes 74 clocks and one with A in shared memory 107; K and
 // V images stream through three 64 KB slots as plain bulk copies.  Scores of

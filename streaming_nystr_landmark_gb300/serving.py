@@ -24,7 +24,10 @@ from . import nys
 def merge(out_a, lse_a, out_b, lse_b, out):
     """Attention over two disjoint sets of keys from the results over each and
     their log-sums: sum_x e^{lse_x} out_x / sum_x e^{lse_x}, in f32; rows that
-    saw neither set stay 0."""
+    saw neither set stay 0.  Results of 16-bit types come rounded to their type,
+    so the sum of two is off by up to half a step more than one pass over all keys
+    would be: that pass would have to read the prefix from its pages for every
+    prompt row, which the operators do for single tokens."""
     import torch
     top = torch.maximum(lse_a, lse_b)
     top = torch.where(torch.isinf(top), torch.zeros_like(top), top)
@@ -38,7 +41,9 @@ def merge(out_a, lse_a, out_b, lse_b, out):
 
 class ExactLayer:
     """One layer's exact attention for `requests` requests of up to max_len
-    tokens each (besides the shared prefix), in pages of `page` tokens."""
+    tokens each (besides the shared prefix), in pages of `page` tokens.  It serves
+    one batch: requests are admitted together, each gets a token in every decode,
+    and pages are given back with the object."""
 
     def __init__(self, heads, kv_heads, d, dv, requests, n_pages, page, max_len, dtype=None,
                  scale=None, device="cuda"):
