@@ -99,15 +99,16 @@ constexpr int kZeroExp = -60, kZeroLow = kZeroExp, kZeroHigh = 30;
 constexpr uint32_t kOdd = 255;
 // fp16 holds a piece lo of a number at 2^-38 of its group's largest at best, so a key
 // beside a far larger one, and a column beside a far larger one, would be rounded to what
-// the larger one leaves: a group of values is odd where more numbers than chance puts
-// there (chance_of) lie over kSpanV powers of two below its largest.  (Without that, one
-// value row or column 2^10 above the rest leaves the other columns where they were, 2^12
-// five times, 2^14 forty times, 2^16 a hundred times further off.)  Groups of keys, and
-// query rows, are sums' operands and take kSpanK: 2^18 there leaves results where they
-// were.  Weights are rounded at 2^-40 of the largest contribution (weight and value), so
-// a unit is odd where its groups' largest values are more than kSpanUnit apart and f32's
-// last bits would go.  Products of exponents stay below f32's range.
-constexpr int kSpanV = 13, kSpanK = 17, kSpanUnit = 16;
+// the larger one leaves.  A group is odd where rows, columns or most numbers lie that
+// far below its largest, kSpan powers of two (is_odd); single numbers do in any group,
+// and in some the half of them, and do no harm among others of their row and column.
+// (Without that, one value row or column 2^10 above the rest leaves the other columns
+// where they were, 2^12 five times, 2^14 forty times, 2^16 a hundred times further off.
+// Keys and queries are a sum's operands: 2^18 there leaves results where they were.)
+// Weights are rounded at 2^-40 of the largest contribution (weight and value), so a unit
+// is odd where its groups' largest values are more than kSpanUnit apart and f32's last
+// bits would go.  Products of exponents stay below f32's range.
+constexpr int kSpanV = 13, kSpanMostV = 16, kSpanK = 17, kSpanUnit = 16;
 constexpr int kLeastK = 40, kMostK = 187, kLeastV = 60;  // biased exponents
 
 struct Shared {
@@ -213,22 +214,21 @@ __device__ __forceinline__ float exp_of(int e) {  // 2^e, -126 <= e <= 127
 __device__ __forceinline__ float back_of(int ex) {
   return __uint_as_float((uint32_t)(ex - kTop) << 23);
 }
-// Magnitudes below this are small against a largest one of biased exponent ex.
+// The largest magnitude of four columns, NaN if one is.
+__device__ __forceinline__ float cell_of(float4 x) {
+  return max3_abs_nan(max3_abs_nan(0.f, x.x, x.y), x.z, x.w);
+}
+// Magnitudes below this are small against a largest one of biased exponent ex; zeros,
+// which any scale holds, are not.
 __device__ __forceinline__ float small_below(int ex, int span) {
   return __uint_as_float(ex > span ? (uint32_t)(ex - span) << 23 : 0u);
 }
-// How many of four are; zeros, which any scale holds, among them or not.
-template <bool ZEROS>
+__device__ __forceinline__ int is_small(float x, float below) { return x != 0.f && fabsf(x) < below; }
 __device__ __forceinline__ int count_small(float4 x, float below) {
-  auto is = [&](float y) { return (int)((ZEROS || y != 0.f) && fabsf(y) < below); };
-  return is(x.x) + is(x.y) + is(x.z) + is(x.w);
+  return is_small(x.x, below) + is_small(x.y, below) + is_small(x.z, below) + is_small(x.w, below);
 }
-// From how many small ones of `numbers` on it is no chance.  Normal numbers of one size
-// are below 2^-13 of the largest of 2,048 once in 3,000: more than 11 of 2,048, or 3 of
-// 128, come once in some 10^7 groups; below 2^-17, 4 of 2,048, or 2 of 128.
-__device__ __forceinline__ int chance_of(int numbers, bool values) {
-  return values ? 3 + (numbers > 32) + numbers / 256 : 3 + numbers / 1024;
-}
+// From how many small ones of `numbers` on they are most.
+__device__ __forceinline__ int most_of(int numbers) { return max(3, numbers / 8); }
 // Four scaled values as hi and lo words; DROP: 0 for infinities and NaN, which
 // else do not occur.
 template <bool DROP>
@@ -534,10 +534,10 @@ __device__ void query_role(const TileArgs& a, Shared& sh, unsigned char* turn, u
         if (__any_sync(0xffffffffu, least < below)) {
           int small = 0;  // a row's columns are on four lanes
 #pragma unroll
-          for (int c = 0; c < 8; ++c) small += count_small<false>(x[c * 4 + i], below);
+          for (int c = 0; c < 8; ++c) small += count_small(x[c * 4 + i], below);
           small += __shfl_xor_sync(0xffffffffu, small, 1);
           small += __shfl_xor_sync(0xffffffffu, small, 2);
-          odd |= small >= chance_of(a.d, false);
+          odd |= small >= most_of(a.d);
         }
         odd |= (top != 0 && e < kLeastK) || e > kMostK;  // (infinities, NaN too)
         // (127 marks a query with a value that is not finite, whatever S then holds)
@@ -583,6 +583,39 @@ __device__ void query_role(const TileArgs& a, Shared& sh, unsigned char* turn, u
     if (!valid) return;
     odd_last = odd_now;
   }
+}
+
+// Whether rows, columns or most numbers of a group are small (a warp; x: four columns of
+// each row, `columns` their largest).  A row is small where half of it is, four columns
+// at a time, below `below`: of normal numbers four are once in 10^13, in a group with
+// columns 2^10 above the rest once in 100.  In fewer rows than 16 a column may be small
+// by chance.  Most: an eighth, below `far`; what the others miss, large numbers in every
+// row and every column, and short and narrow groups.  Zeros let the first checks through
+// to the counting, which leaves them out.
+__device__ __forceinline__ bool is_odd(const float4 (&x)[kGroup], float4 columns, int rows, int dim,
+                                       float below, float far, bool col) {
+  float cell = INFINITY, number = INFINITY;
+#pragma unroll
+  for (int r = 0; r < kGroup; r += 2) cell = min3_abs(cell, cell_of(x[r]), cell_of(x[r + 1]));
+#pragma unroll
+  for (int r = 0; r < kGroup; ++r) {
+    number = min3_abs(number, x[r].x, x[r].y);
+    number = min3_abs(number, x[r].z, x[r].w);
+  }
+  bool odd = rows == kGroup && __any_sync(0xffffffffu, count_small(columns, below) > 0);
+  if (__any_sync(0xffffffffu, col && cell < below)) {
+    int small = 0;
+#pragma unroll
+    for (int r = 0; r < kGroup; ++r) small += is_small(cell_of(x[r]), below);
+    odd |= (int)__reduce_add_sync(0xffffffffu, small) >= max(1, dim / 8);
+  }
+  if (__any_sync(0xffffffffu, col && number < far)) {
+    int small = 0;
+#pragma unroll
+    for (int r = 0; r < kGroup; ++r) small += count_small(x[r], far);
+    odd |= (int)__reduce_add_sync(0xffffffffu, small) >= most_of(max(min(rows, kGroup), 0) * dim);
+  }
+  return odd;
 }
 
 // K and V as tile images.  Grid: tiles x KV heads, K and V; a warp takes 16 rows.  Three
@@ -637,13 +670,16 @@ __global__ void __launch_bounds__(256, 3) split_kernel(const __grid_constant__ T
     x[r] = o >= 0 && col ? __ldcs(reinterpret_cast<const float4*>(src + o * stride))
                          : make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  float largest = 0.f;
+  float column[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int r = 0; r < kGroup; ++r) {
-    largest = max3_abs_nan(largest, x[r].x, x[r].y);
-    largest = max3_abs_nan(largest, x[r].z, x[r].w);
+  for (int r = 0; r < kGroup; r += 2) {
+    column[0] = max3_abs_nan(column[0], x[r].x, x[r + 1].x);
+    column[1] = max3_abs_nan(column[1], x[r].y, x[r + 1].y);
+    column[2] = max3_abs_nan(column[2], x[r].z, x[r + 1].z);
+    column[3] = max3_abs_nan(column[3], x[r].w, x[r + 1].w);
   }
-  uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(largest) & 0x7FFFFFFFu);
+  const float4 columns = make_float4(column[0], column[1], column[2], column[3]);
+  uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(cell_of(columns)) & 0x7FFFFFFFu);
   const bool bad = top >= 0x7F800000u;
   bool odd = bad;
   if (bad) {
@@ -653,17 +689,8 @@ __global__ void __launch_bounds__(256, 3) split_kernel(const __grid_constant__ T
     top = __reduce_max_sync(0xffffffffu, __float_as_uint(f));
   } else {
     const int e = (int)(top >> 23);
-    const float below = small_below(e, is_v ? kSpanV : kSpanK);
-    const int chance = chance_of(max(min(rows, kGroup), 0) * dim, is_v);
-    int small = 0;  // with zeros first: few groups have any
-#pragma unroll
-    for (int r = 0; r < kGroup; ++r) small += count_small<true>(x[r], below);
-    if (__reduce_add_sync(0xffffffffu, col ? small : 0) >= chance) {
-      small = 0;
-#pragma unroll
-      for (int r = 0; r < kGroup; ++r) small += count_small<false>(x[r], below);
-      odd = __reduce_add_sync(0xffffffffu, small) >= chance;
-    }
+    odd = is_odd(x, columns, rows, dim, small_below(e, is_v ? kSpanV : kSpanK),
+                 small_below(e, is_v ? kSpanMostV : kSpanK), col);
     odd |= is_v ? top != 0 && e < kLeastV : (top != 0 && e < kLeastK) || e > kMostK;
   }
   const int ex = top_exponent(top);
