@@ -372,9 +372,9 @@ int nys_o1_free(nys_o1* o);
  * tiled kernels take numbers as pairs of 11-bit pieces, so that a product is good
  * to 2^-21 at worst and 2^-24 in the mean, and a number to 2^-38 of the largest of
  * its 16 rows (keys, values) or its row (queries); weights are held to 2^-40 of the
- * row's largest contribution.  Rows where that would show (numbers further apart
- * than chance puts them, infinities, NaN) are computed in plain fp32 instead,
- * which takes 20 to 90 times as long for the rows concerned.
+ * row's largest contribution.  Rows where that would show (keys, values or columns
+ * that lie far below others of their 16 rows, infinities, NaN) are computed in
+ * plain fp32 instead, which takes 20 to 90 times as long for the rows concerned.
  * The conventions at the top hold, except that pointers need only their
  * element type's alignment.  Rows that are 16-byte aligned and head dims up to
  * 128 (multiples of 8 in 16-bit types) take the tiled kernels, and so does a

@@ -40,7 +40,7 @@
 // value columns for the sums), 8-11 the query tile's pieces and the results'
 // stores, 12 products, 13 units of work, 14 copies.  The products bound it where
 // prompts are long (2 prompts continued over 5,003 tokens: 224 us, tensor pipe 80%
-// busy), each unit's chain of steps where they are short (64 prompts of 256: 162 us
+// busy), each unit's chain of steps where they are short (64 prompts of 256: 163 us
 // with the split).  Q goes straight into tensor memory, because a
 // product with A there takes 74 clocks and one with A in shared memory 107; K and
 // V images stream through three 64 KB slots as plain bulk copies.  Scores of
