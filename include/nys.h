@@ -505,6 +505,127 @@ int nys_kv_write(const nys_attn_config* cfg, const nys_pool* pool, int64_t token
  * the GPU; the context stays usable.  Errors: NYS_E_INVAL. */
 int nys_debug_stall_attn_once(int32_t role);
 
+/* ---- Between the projections and attention ---------------------------------
+ * The conventions of the section above hold.
+ *
+ * Queries and keys are normalised for each head and rotated by their positions
+ * in one pass over their rows:
+ *
+ *   y = x / sqrt(mean_i x_i^2 + eps) * weight      (weight NULL: y = x)
+ *   (a, b) -> (a cos t - b sin t, a sin t + b cos t),
+ *   t = (position + shift) * frequency_i,
+ *
+ * the pairs being numbers i and i + rot/2 of a head, or 2i and 2i + 1
+ * (interleaved), i < rot/2; numbers from rot on are not rotated.  All in fp32,
+ * rounded once.  turns[i] is frequency_i / (2 pi) * 2^64, rounded, modulo 2^64:
+ * the angle is then exact to 2^-31 of half a turn at every position. */
+typedef struct {
+  const float* q_weight; /* device fp32 [d], or NULL: queries are not normalised */
+  const float* k_weight; /* the same for keys                                    */
+  float eps;             /* >= 0                                                 */
+  const uint64_t* turns; /* device [rot/2]; NULL only if rot is 0                */
+  int32_t rot;           /* even, 0 .. d                                         */
+  int32_t interleaved;   /* 0 or 1                                               */
+  int32_t shift;         /* added to every position (a shared prefix's length)   */
+} nys_qk_prepare;
+
+/* Normalises and rotates q [tokens][heads][d] into q_out and k
+ * [tokens][kv_heads][d] into k_out.  Either pair may be NULL.  q_out may be q
+ * itself (the same address and strides), and k_out k; apart from that outputs
+ * overlap no input.  positions: device int32 [tokens], any sign; NULL if rot is
+ * 0.  Errors: NYS_E_INVAL, NYS_E_UNSUPPORTED, NYS_E_ALIGN, NYS_E_CUDA. */
+int nys_qk_rows(const nys_attn_config* cfg, const nys_qk_prepare* prep, int64_t tokens,
+                const nys_rows* q, const nys_rows* k, const int32_t* positions,
+                const nys_rows* q_out, const nys_rows* k_out, void* stream);
+
+/* The same, with the prepared keys and the values v [tokens][kv_heads][dv] (as
+ * they are) going into the pool's slots as in nys_kv_write, in the same launch.
+ * q and q_out may be NULL (both), k_out too: keys then go to the pool alone.
+ * A token whose slot lies outside the pool gets its q_out and k_out rows all the
+ * same.  Errors: NYS_E_INVAL, NYS_E_UNSUPPORTED, NYS_E_ALIGN, NYS_E_CUDA. */
+int nys_kv_append(const nys_attn_config* cfg, const nys_qk_prepare* prep, const nys_pool* pool,
+                  int64_t tokens, const nys_rows* q, const nys_rows* k, const nys_rows* v,
+                  const int32_t* positions, const int64_t* slots, const nys_rows* q_out,
+                  const nys_rows* k_out, void* stream);
+
+/* ---- A paged cache in 4 bits ------------------------------------------------
+ * A row of a head is held as groups of 64 numbers (the last may be short), each
+ * with a middle and a step in bf16 and a code c of 4 bits a number, which stands
+ * for mid + step * (c - 8).  With lo and hi the group's least and largest number,
+ *   mid  = bf16(lo + (hi - lo) * 8 / 15),
+ *   step = max((hi - mid) / 7, (mid - lo) / 8), up to the next bf16,
+ *   c    = round((x - mid) / step) + 8, ties to even,
+ * in fp32: a number is off by half a step at most, and a group of equal numbers
+ * that bf16 can hold, not at all.  A step below 2^-100 counts as 0.  A group with
+ * a number that is not finite, or of a spread of 2^125 and more, reads back as NaN.
+ * 4.5 bits a number where d and dv are multiples of 64; keys and values both take
+ * the groups of the wider of the two.
+ *
+ * data: [n_pages][kv_heads][page / 16] blocks of 1152 * groups bytes (16 tokens'
+ * keys and values of a head), groups = ceil(max(d, dv) / 64); 16-byte aligned.
+ * In 32-bit words, a block is
+ *   keys' codes    [group][token % 8][c][token / 8][h]      8 codes, lowest first, of the
+ *                                                            numbers from 64 group + 32 h + 8 c
+ *   values' codes  [group][r][token % 8 / 2][token / 8][token % 2]   from 64 group + 8 r
+ *   keys' scales, then values' scales
+ *                  [group][token % 8 / 2][token / 8][token % 2]      step << 16 | mid */
+typedef struct {
+  void* data;
+  int64_t n_pages;
+  int32_t page; /* tokens a page, a positive multiple of 16 */
+} nys_pool4;
+
+/* Bytes of a page of this geometry.  Host arithmetic only.  Errors: NYS_E_INVAL,
+ * NYS_E_UNSUPPORTED. */
+int nys_kv4_page_bytes(const nys_attn_config* cfg, int32_t page, size_t* bytes);
+
+/* Rows k and v into the cache's slots (nys_kv_write's rules; two tokens with one
+ * slot leave a mixture of the two, still codes and scales of the right form).  The
+ * rows' type is cfg's.  Errors: NYS_E_INVAL, NYS_E_UNSUPPORTED, NYS_E_ALIGN,
+ * NYS_E_CUDA. */
+int nys_kv4_write(const nys_attn_config* cfg, const nys_pool4* pool, int64_t tokens,
+                  const nys_rows* k, const nys_rows* v, const int64_t* slots, void* stream);
+
+/* nys_kv_append into a 4-bit cache: the codes are those of the prepared keys in
+ * fp32, before any rounding to cfg's type.  Errors: the same. */
+int nys_kv4_append(const nys_attn_config* cfg, const nys_qk_prepare* prep, const nys_pool4* pool,
+                   int64_t tokens, const nys_rows* q, const nys_rows* k, const nys_rows* v,
+                   const int32_t* positions, const int64_t* slots, const nys_rows* q_out,
+                   const nys_rows* k_out, void* stream);
+
+/* The rows in slots[0 .. tokens-1] as the values they stand for, rounded to cfg's
+ * type, into k_out [tokens][kv_heads][d] and v_out [..][dv]; a slot outside the
+ * pool gives zeros.  What needs rows takes them from here: a prompt that goes on
+ * (nys_attn_prompt), a request whose states are sealed.  Errors: the same. */
+int nys_kv4_read(const nys_attn_config* cfg, const nys_pool4* pool, int64_t tokens,
+                 const int64_t* slots, const nys_rows* k_out, const nys_rows* v_out,
+                 void* stream);
+
+/* Bytes of device workspace that nys_attn4 uses for n requests of up to `keys`
+ * tokens (width * page).  Host arithmetic only; 0 is a possible answer.  Errors:
+ * NYS_E_INVAL, NYS_E_UNSUPPORTED. */
+int nys_attn4_workspace_bytes(const nys_attn_config* cfg, int64_t n, int64_t keys, size_t* bytes);
+
+/* One token of attention for n requests over their keys in a 4-bit cache: query
+ * row b of q sees the lens[b] tokens in pages table[b * width + 0 ..], taken as
+ * exactly the values they stand for.  Scores take queries to 22 bits, weights are
+ * held to 16 bits (fp32 calls: 24) for the second product; sums run in fp32.  A
+ * request without keys gets 0 (lse -INF).  Pages outside the pool count as keys
+ * and values of 0 (NYS_ATTN_BAD_PAGE), lengths are taken clamped into their table
+ * (NYS_ATTN_BAD_LENGTH); entries past a length are not read.  A query row that is
+ * not finite gives NaN.
+ * first, first_lse (both or neither): the result [n][heads][dv] and log-sums
+ * [n][heads] of the same queries over other keys (a shared prefix,
+ * nys_attn_shared), which are joined in; first may be out itself, and first_lse
+ * lse.  lse, if not NULL, fp32 [n][heads], is that of all keys.
+ * workspace: nys_attn4_workspace_bytes(cfg, n, width * page) bytes, 256-byte
+ * aligned; less is NYS_E_BUF.
+ * Errors: NYS_E_INVAL, NYS_E_UNSUPPORTED, NYS_E_BUF, NYS_E_ALIGN, NYS_E_CUDA. */
+int nys_attn4(const nys_attn_config* cfg, int64_t n, const nys_pool4* pool, const int32_t* lens,
+              const int32_t* table, int32_t width, const nys_rows* q, const nys_rows* first,
+              const float* first_lse, const nys_rows* out, float* lse, void* workspace,
+              size_t workspace_bytes, int32_t* status, void* stream);
+
 /* Static description of a status code.  Never NULL. */
 const char* nys_strerror(int status);
 

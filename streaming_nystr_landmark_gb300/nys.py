@@ -11,7 +11,9 @@ stream to the C calls.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
+from fractions import Fraction
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnys.so")
 
@@ -48,7 +50,9 @@ EXPORTED = ("nys_memory_bytes", "nys_alloc_states", "nys_free_states",
             "nys_o1_states", "nys_o1_free", "nys_debug_stall_once",
             "nys_debug_stall_replay_once", "nys_attn_workspace_bytes",
             "nys_attn_prompt", "nys_attn_shared", "nys_kv_plan", "nys_kv_write",
-            "nys_debug_stall_attn_once")
+            "nys_debug_stall_attn_once", "nys_qk_rows", "nys_kv_append",
+            "nys_kv4_page_bytes", "nys_kv4_write", "nys_kv4_append", "nys_kv4_read",
+            "nys_attn4_workspace_bytes", "nys_attn4")
 
 
 class NysConfig(ctypes.Structure):
@@ -93,6 +97,16 @@ class NysPool(ctypes.Structure):
                 ("n_pages", ctypes.c_int64), ("page", ctypes.c_int32)]
 
 
+class NysPool4(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("page", ctypes.c_int32)]
+
+
+class NysQkPrepare(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("turns", ctypes.c_void_p), ("rot", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("shift", ctypes.c_int32)]
+
+
 def _load():
     if not os.path.exists(_LIB_PATH):
         raise ImportError(
@@ -131,6 +145,18 @@ def _load():
         "nys_kv_plan": [I64, I32, VP, VP, VP, I64, VP, I32, I64, VP, VP, VP, VP, VP, VP, VP],
         "nys_kv_write": [P(NysAttnConfig), P(NysPool), I64, P(NysRows), P(NysRows), VP, VP],
         "nys_debug_stall_attn_once": [I32],
+        "nys_qk_rows": [P(NysAttnConfig), P(NysQkPrepare), I64, P(NysRows), P(NysRows), VP,
+                        P(NysRows), P(NysRows), VP],
+        "nys_kv_append": [P(NysAttnConfig), P(NysQkPrepare), P(NysPool), I64, P(NysRows),
+                          P(NysRows), P(NysRows), VP, VP, P(NysRows), P(NysRows), VP],
+        "nys_kv4_page_bytes": [P(NysAttnConfig), I32, P(ctypes.c_size_t)],
+        "nys_kv4_write": [P(NysAttnConfig), P(NysPool4), I64, P(NysRows), P(NysRows), VP, VP],
+        "nys_kv4_append": [P(NysAttnConfig), P(NysQkPrepare), P(NysPool4), I64, P(NysRows),
+                           P(NysRows), P(NysRows), VP, VP, P(NysRows), P(NysRows), VP],
+        "nys_kv4_read": [P(NysAttnConfig), P(NysPool4), I64, VP, P(NysRows), P(NysRows), VP],
+        "nys_attn4_workspace_bytes": [P(NysAttnConfig), I64, I64, P(ctypes.c_size_t)],
+        "nys_attn4": [P(NysAttnConfig), I64, P(NysPool4), VP, VP, I32, P(NysRows), P(NysRows),
+                      VP, P(NysRows), VP, VP, ctypes.c_size_t, VP, VP],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -280,6 +306,54 @@ def nys_debug_stall_attn_once(role):
 
 def nys_kv_write(cfg, pool, tokens, k, v, slots, stream=0):
     _check(_lib.nys_kv_write(cfg, pool, tokens, k, v, slots, stream or None), "nys_kv_write")
+
+
+def nys_qk_rows(cfg, prep, tokens, q, k, positions, q_out, k_out, stream=0):
+    """q, k, q_out, k_out: NysRows or None; positions: a device address."""
+    _check(_lib.nys_qk_rows(cfg, prep, tokens, q, k, positions, q_out, k_out, stream or None),
+           "nys_qk_rows")
+
+
+def nys_kv_append(cfg, prep, pool, tokens, q, k, v, positions, slots, q_out=None, k_out=None,
+                  stream=0):
+    _check(_lib.nys_kv_append(cfg, prep, pool, tokens, q, k, v, positions, slots, q_out, k_out,
+                              stream or None), "nys_kv_append")
+
+
+def nys_kv4_page_bytes(cfg: NysAttnConfig, page: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(_lib.nys_kv4_page_bytes(ctypes.byref(cfg), page, ctypes.byref(out)),
+           "nys_kv4_page_bytes")
+    return out.value
+
+
+def nys_kv4_write(cfg, pool, tokens, k, v, slots, stream=0):
+    _check(_lib.nys_kv4_write(cfg, pool, tokens, k, v, slots, stream or None), "nys_kv4_write")
+
+
+def nys_kv4_append(cfg, prep, pool, tokens, q, k, v, positions, slots, q_out=None, k_out=None,
+                   stream=0):
+    _check(_lib.nys_kv4_append(cfg, prep, pool, tokens, q, k, v, positions, slots, q_out, k_out,
+                               stream or None), "nys_kv4_append")
+
+
+def nys_kv4_read(cfg, pool, tokens, slots, k_out, v_out, stream=0):
+    _check(_lib.nys_kv4_read(cfg, pool, tokens, slots, k_out, v_out, stream or None),
+           "nys_kv4_read")
+
+
+def nys_attn4_workspace_bytes(cfg: NysAttnConfig, n: int, keys: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(_lib.nys_attn4_workspace_bytes(ctypes.byref(cfg), n, keys, ctypes.byref(out)),
+           "nys_attn4_workspace_bytes")
+    return out.value
+
+
+def nys_attn4(cfg, n, pool, lens, table, width, q, out, first=None, first_lse=None, lse=None,
+              workspace=None, workspace_bytes=0, status=None, stream=0):
+    """q, out, first: NysRows; pool: NysPool4; the rest: device addresses."""
+    _check(_lib.nys_attn4(cfg, n, pool, lens, table, width, q, first, first_lse, out, lse,
+                          workspace, workspace_bytes, status, stream or None), "nys_attn4")
 
 
 # ---------------------------------------------------------------- torch wrapper
@@ -676,6 +750,194 @@ class PagedKV(_OnDevice):
                      _ints(slots, torch.int64, (n,), "slots", index), self._stream())
 
 
+class PagedKV4(_OnDevice):
+    """A pool of KV pages of one layer in 4 bits (4.5 with their scales; nys.h says what
+    a row is held as): `page` a multiple of 16.  Rows come and go in `dtype`.  data,
+    uint8 [n_pages][kv_heads][bytes], is allocated here or given; pages that were
+    never written hold whatever was there."""
+
+    def __init__(self, n_pages, page, kv_heads, d, dv, dtype=None, device="cuda", data=None):
+        import torch
+        self.torch = torch
+        self.dtype = torch.float32 if dtype is None else dtype
+        self.device = _cuda_device(device)
+        self.n_pages, self.page = n_pages, page
+        self.kv_heads, self.d, self.dv = kv_heads, d, dv
+        self._cfg = NysAttnConfig(kv_heads, kv_heads, d, dv, _dtype_code(self.dtype), 0.0)
+        if page < 16 or page % 16:
+            raise ValueError(f"page {page}: need a multiple of 16 tokens")
+        shape = (n_pages, kv_heads, nys_kv4_page_bytes(self._cfg, page) // kv_heads)
+        self.data = (torch.empty(shape, dtype=torch.uint8, device=self.device) if data is None
+                     else data)
+        if (self.data.dtype != torch.uint8 or not self.data.is_cuda
+                or not self.data.is_contiguous() or tuple(self.data.shape) != shape
+                or self.data.get_device() != self.device.index):
+            raise ValueError(f"data: need a contiguous uint8 tensor of shape {shape} on "
+                             f"{self.device}")
+        self._pool = NysPool4(self.data.data_ptr(), n_pages, page)
+
+    def write(self, k, v, slots):
+        """Rows k [tokens][kv_heads][d], v [..][dv] into slots int64 [tokens] (no slot
+        twice); a slot of -1 is skipped."""
+        torch, index = self.torch, self.device.index
+        if self._elsewhere():
+            with torch.cuda.device(index):
+                return self.write(k, v, slots)
+        n = k.shape[0]
+        if v.shape[0] != n:
+            raise ValueError(f"v: {v.shape[0]} rows, k has {n}")
+        nys_kv4_write(self._cfg, self._pool, n,
+                      _rows(k, self.dtype, self.kv_heads, self.d, "k", index),
+                      _rows(v, self.dtype, self.kv_heads, self.dv, "v", index),
+                      _ints(slots, torch.int64, (n,), "slots", index), self._stream())
+
+    def read(self, slots, k, v):
+        """The rows in slots int64 [tokens] as the values they stand for, into k
+        [tokens][kv_heads][d] and v [..][dv] of the cache's type; zeros for a slot of -1."""
+        torch, index = self.torch, self.device.index
+        if self._elsewhere():
+            with torch.cuda.device(index):
+                return self.read(slots, k, v)
+        n = slots.shape[0]
+        if k.shape[0] != n or v.shape[0] != n:
+            raise ValueError(f"k and v must have a row for each of the {n} slots")
+        nys_kv4_read(self._cfg, self._pool, n, _ints(slots, torch.int64, (n,), "slots", index),
+                     _rows(k, self.dtype, self.kv_heads, self.d, "k", index),
+                     _rows(v, self.dtype, self.kv_heads, self.dv, "v", index), self._stream())
+
+
+class Rotation:
+    """The rotation of the first `rot` (all, if not given) of a head's d numbers by their
+    position: pair i turns by base^(-2i / rot), or by freqs[i], radians a position.  Pairs
+    are numbers i and i + rot/2, or 2i and 2i + 1 (interleaved)."""
+
+    # 2 pi to 50 digits.
+    _TURN = Fraction(62831853071795864769252867665590057683943387987502, 10 ** 49)
+
+    def __init__(self, d, base=10000.0, rot=None, interleaved=False, freqs=None, device="cuda"):
+        import torch
+        rot = d if rot is None else rot
+        if rot < 0 or rot % 2 or rot > d:
+            raise ValueError(f"rot {rot}: need an even number of at most {d}")
+        if freqs is None:
+            freqs = [float(base) ** (-2.0 * i / rot) for i in range(rot // 2)]
+        freqs = [float(f) for f in freqs]
+        if len(freqs) != rot // 2 or not all(math.isfinite(f) for f in freqs):
+            raise ValueError(f"freqs: need {rot // 2} finite numbers")
+        self.d, self.rot, self.interleaved = d, rot, bool(interleaved)
+        self.device = _cuda_device(device)
+        # Fractions of a turn in 64 bits; torch holds them as int64.
+        turns = [round(Fraction(f) / self._TURN * 2 ** 64) % 2 ** 64 for f in freqs]
+        self.turns = torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns],
+                                  dtype=torch.int64).to(self.device)
+
+
+class QKPrepare(_OnDevice):
+    """What stands between a layer's projections and its attention: RMS norms of queries
+    and keys for each head (weights [d] or None) and their rotation (a Rotation or None),
+    in one pass (``rows``), or in one with the write into the cache's pages (``append``)."""
+
+    def __init__(self, heads, kv_heads, d, dtype=None, q_weight=None, k_weight=None, eps=1e-6,
+                 rotation=None, device="cuda"):
+        import torch
+        self.torch = torch
+        self.dtype = torch.float32 if dtype is None else dtype
+        self.device = _cuda_device(device)
+        self.heads, self.kv_heads, self.d = heads, kv_heads, d
+        if not 0 <= eps < float("inf"):
+            raise ValueError(f"eps {eps}: need a finite number that is not negative")
+        if rotation is not None and (rotation.d != d or rotation.device != self.device):
+            raise ValueError(f"rotation: made for {rotation.d} numbers on {rotation.device}, "
+                             f"need {d} on {self.device}")
+        self.rotation = rotation
+        # Copies in f32 of this object's own: a weight that changes later needs a new one.
+        self._weights = []
+        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+            if w is not None:
+                if tuple(w.shape) != (d,):
+                    raise ValueError(f"{name}: shape {tuple(w.shape)} != ({d},)")
+                w = w.detach().to(device=self.device, dtype=torch.float32, copy=True).contiguous()
+            self._weights.append(w)
+        self.cfg = NysAttnConfig(heads, kv_heads, d, d, _dtype_code(self.dtype), 0.0)
+        at = [None if w is None else w.data_ptr() for w in self._weights]
+        rot = 0 if rotation is None else rotation.rot
+        self._prep = NysQkPrepare(*at, eps, rotation.turns.data_ptr() if rot else None, rot,
+                                  int(rot > 0 and rotation.interleaved), 0)
+        nys_qk_rows(self.cfg, self._prep, 0, NysRows(), None, None, NysRows(), None)
+
+    def _turned(self, positions, n, shift):
+        """The arguments of the C call for this shift, and the positions' address."""
+        prep = self._prep
+        if shift:
+            if not -2 ** 31 <= shift < 2 ** 31:
+                raise ValueError(f"shift {shift}: past 32 bits")
+            prep = NysQkPrepare(prep.q_weight, prep.k_weight, prep.eps, prep.turns, prep.rot,
+                                prep.interleaved, shift)
+        if positions is None:
+            if prep.rot:
+                raise ValueError("positions: needed for a rotation")
+            return prep, None
+        return prep, _ints(positions, self.torch.int32, (n,), "positions", self.device.index)
+
+    def _in_out(self, x, out, heads, where):
+        index = self.device.index
+        if out is not None and out.shape[0] != x.shape[0]:
+            raise ValueError(f"{where}_out: {out.shape[0]} rows, {where} has {x.shape[0]}")
+        return (_rows(x, self.dtype, heads, self.d, where, index),
+                None if out is None else _rows(out, self.dtype, heads, self.d, where + "_out",
+                                               index))
+
+    def rows(self, q, k, positions, q_out=None, k_out=None, shift=0):
+        """q [tokens][heads][d] and k [tokens][kv_heads][d] (either may be None), normalised
+        and rotated by positions (int32 [tokens], plus shift), into q_out and k_out, or in
+        place where those are not given.  Returns them."""
+        if self._elsewhere():
+            with self.torch.cuda.device(self.device.index):
+                return self.rows(q, k, positions, q_out, k_out, shift)
+        if q is None and k is None or q is None and q_out is not None or k is None and k_out is not None:
+            raise ValueError("q and k: need one of them, and none for an output without it")
+        if q is not None and k is not None and q.shape[0] != k.shape[0]:
+            raise ValueError(f"k: {k.shape[0]} rows, q has {q.shape[0]}")
+        n = (k if q is None else q).shape[0]
+        q_out, k_out = q if q_out is None else q_out, k if k_out is None else k_out
+        prep, at = self._turned(positions, n, shift)
+        qs = (None, None) if q is None else self._in_out(q, q_out, self.heads, "q")
+        ks = (None, None) if k is None else self._in_out(k, k_out, self.kv_heads, "k")
+        nys_qk_rows(self.cfg, prep, n, qs[0], ks[0], at, qs[1], ks[1], self._stream())
+        return q_out, k_out
+
+    def append(self, q, k, v, positions, slots, cache, q_out=None, k_out=None, shift=0):
+        """The same with the prepared keys and the values v [tokens][kv_heads][dv] going into
+        slots int64 [tokens] of cache (a PagedKV or PagedKV4 of this type; no slot twice, a
+        slot of -1 is skipped).  q may be None; its rows go to q_out, or stay in place.  Keys
+        go to k_out as well, if given.  Returns q_out."""
+        torch, index = self.torch, self.device.index
+        if self._elsewhere():
+            with torch.cuda.device(index):
+                return self.append(q, k, v, positions, slots, cache, q_out, k_out, shift)
+        if cache.dtype != self.dtype or cache.kv_heads != self.kv_heads or cache.d != self.d:
+            raise ValueError("the cache's geometry is not this object's")
+        if cache.device.index != index:
+            raise ValueError(f"the cache is on {cache.device}, this object on {self.device}")
+        n = k.shape[0]
+        if v.shape[0] != n or (q is not None and q.shape[0] != n):
+            raise ValueError("q, k and v must have as many rows as each other")
+        if q is None and q_out is not None:
+            raise ValueError("q_out: there is no q")
+        q_out = q if q_out is None else q_out
+        prep, at = self._turned(positions, n, shift)
+        qs = (None, None) if q is None else self._in_out(q, q_out, self.heads, "q")
+        ks = self._in_out(k, k_out, self.kv_heads, "k")
+        cfg = self.cfg
+        if cache.dv != self.d:
+            cfg = NysAttnConfig(self.heads, self.kv_heads, self.d, cache.dv, cfg.dtype, 0.0)
+        (nys_kv4_append if isinstance(cache, PagedKV4) else nys_kv_append)(
+            cfg, prep, cache._pool, n, qs[0], ks[0],
+            _rows(v, self.dtype, self.kv_heads, cache.dv, "v", index), at,
+            _ints(slots, torch.int64, (n,), "slots", index), qs[1], ks[1], self._stream())
+        return q_out
+
+
 class PagePlan(_Status):
     """Block tables, slots and positions of a batch's next tokens, built on
     the GPU from its lengths (nys_kv_plan): up to n requests, `width` pages a
@@ -747,7 +1009,10 @@ class ExactAttention(_Status):
         if (n, rows, keys) == self._sizes:
             self._captured |= capturing
             return
-        need = nys_attn_workspace_bytes(self.cfg, n, rows, keys)
+        if keys is None:      # paged4: n requests of up to `rows` tokens
+            need = nys_attn4_workspace_bytes(self.cfg, n, rows)
+        else:
+            need = nys_attn_workspace_bytes(self.cfg, n, rows, keys)
         if need > self._work_bytes:
             # May raise: nothing is noted before it is there.
             work = self.torch.empty(need, dtype=self.torch.uint8, device=self.device)
@@ -794,6 +1059,8 @@ class ExactAttention(_Status):
             with torch.cuda.device(index):
                 return self.shared(q, cache, lens, table, out, prefix_pages, prefix_len, lse)
         n = q.shape[0]
+        if isinstance(cache, PagedKV4):
+            raise ValueError("cache: need a PagedKV (paged4 takes one in 4 bits)")
         if (cache.dtype != self.dtype or cache.kv_heads != self.kv_heads or cache.d != self.d
                 or cache.dv != self.dv):
             raise ValueError("the cache's geometry is not this attention's")
@@ -815,6 +1082,43 @@ class ExactAttention(_Status):
             _ints(table, torch.int32, (n, table.shape[1]), "table", index), table.shape[1],
             _rows(q, self.dtype, self.heads, self.d, "q", index),
             _rows(out, self.dtype, self.heads, self.dv, "out", index),
+            None if lse is None else _ints(lse, torch.float32, (n, self.heads), "lse", index),
+            self._work_ptr, self._work_bytes, self._status_ptr, self._stream())
+        return out
+
+    def paged4(self, q, cache, lens, table, out, first=None, first_lse=None, lse=None):
+        """One token for each of n requests over a 4-bit cache (nys_attn4): q [n][heads][d]
+        over lens[b] keys in the pages table[b] of cache, a PagedKV4 (lens int32 [n], table
+        int32 [n][width]); writes out [n][heads][dv] and, if given, lse fp32 [n][heads].
+        first [n][heads][dv] and first_lse: the same queries' result over other keys, joined
+        in (shared() over a prefix); they may be out and lse themselves."""
+        torch, index = self.torch, self.device.index
+        if self._elsewhere():
+            with torch.cuda.device(index):
+                return self.paged4(q, cache, lens, table, out, first, first_lse, lse)
+        n = q.shape[0]
+        if not isinstance(cache, PagedKV4):
+            raise ValueError("cache: need a PagedKV4")
+        if (cache.dtype != self.dtype or cache.kv_heads != self.kv_heads or cache.d != self.d
+                or cache.dv != self.dv):
+            raise ValueError("the cache's geometry is not this attention's")
+        if cache.device.index != index:
+            raise ValueError(f"the cache is on {cache.device}, this attention on {self.device}")
+        if out.shape[0] != n or len(table.shape) != 2:
+            raise ValueError("out must have q's rows, and table be [n][width]")
+        if (first is None) != (first_lse is None) or (first is not None and first.shape[0] != n):
+            raise ValueError("first and first_lse go together, and have q's rows")
+        width = table.shape[1]
+        self._workspace(n, width * cache.page, None)
+        nys_attn4(
+            self.cfg, n, cache._pool, _ints(lens, torch.int32, (n,), "lens", index),
+            _ints(table, torch.int32, (n, width), "table", index), width,
+            _rows(q, self.dtype, self.heads, self.d, "q", index),
+            _rows(out, self.dtype, self.heads, self.dv, "out", index),
+            None if first is None else _rows(first, self.dtype, self.heads, self.dv, "first",
+                                             index),
+            None if first is None else _ints(first_lse, torch.float32, (n, self.heads),
+                                             "first_lse", index),
             None if lse is None else _ints(lse, torch.float32, (n, self.heads), "lse", index),
             self._work_ptr, self._work_bytes, self._status_ptr, self._stream())
         return out

@@ -12,6 +12,11 @@ of prompts of any lengths, and one-token decode.
     out = layer.decode(q, k, v)               # one token for each of them
     seal_prompts(states, q, k, v, lengths)    # landmark states of the same prompts
 
+With prepare=QKPrepare(...) the layer takes the projections' rows: queries and keys
+are normalised and rotated on their way, keys straight into the pages.  With
+bits=4 the requests' keys and values are held in 4 bits; the prefix, one for all,
+stays as it is.
+
 Everything is enqueued on the current torch stream; the host only counts
 pages, so nothing waits for the GPU.  What only the GPU can see (a wait that ran
 out, a page outside the pool) is in layer.status().
@@ -43,16 +48,28 @@ class ExactLayer:
     """One layer's exact attention for `requests` requests of up to max_len
     tokens each (besides the shared prefix), in pages of `page` tokens.  It serves
     one batch: requests are admitted together, each gets a token in every decode,
-    and pages are given back with the object."""
+    and pages are given back with the object.  prepare: a nys.QKPrepare that rows go
+    through, their positions counted from the prefix's first token; None: they come
+    ready.  bits: None, or 4 for a cache in 4 bits (pages a multiple of 16), where
+    the prefix has pages of its own besides the n_pages."""
 
     def __init__(self, heads, kv_heads, d, dv, requests, n_pages, page, max_len, dtype=None,
-                 scale=None, device="cuda"):
+                 scale=None, device="cuda", prepare=None, bits=None):
         import torch
         self.torch = torch
         self.device = nys._cuda_device(device)
         self.attention = nys.ExactAttention(heads, kv_heads, d, dv, dtype=dtype, scale=scale,
                                             device=self.device)
-        self.cache = nys.PagedKV(n_pages, page, kv_heads, d, dv, dtype=dtype, device=self.device)
+        if bits not in (None, 4):
+            raise ValueError(f"bits {bits}: need 4, or None for the rows' own type")
+        if prepare is not None and (
+                (prepare.heads, prepare.kv_heads, prepare.d) != (heads, kv_heads, d)
+                or prepare.dtype != self.attention.dtype or prepare.device != self.device):
+            raise ValueError("prepare: made for another geometry, type or device")
+        self.prepare, self.bits = prepare, bits
+        self.cache = (nys.PagedKV if bits is None else nys.PagedKV4)(
+            n_pages, page, kv_heads, d, dv, dtype=dtype, device=self.device)
+        self.prefix_cache = self.cache if bits is None else None
         self.requests, self.page = requests, page
         self.width = -(-max_len // page)
         i32 = dict(dtype=torch.int32, device=self.device)
@@ -113,17 +130,27 @@ class ExactLayer:
     def set_prefix(self, k, v):
         """Keys and values [rows][kv_heads][d|dv] that every request sees first;
         before any request is admitted."""
-        if self.used:
+        if self.used or self.prefix_len:
             raise ValueError("the prefix comes before the first request")
         self._check(None, k, v)
-        torch, n = self.torch, k.shape[0]
+        torch, att, n = self.torch, self.attention, k.shape[0]
         need = -(-n // self.page)
-        if need > self.free.shape[0]:
-            raise ValueError(f"{need} pages wanted, {self.free.shape[0]} there")
-        pages = self.free[:need].clone()
         at = torch.arange(n, device=self.device)
-        self.cache.write(k, v, pages.long()[at // self.page] * self.page + at % self.page)
-        self.used, self.prefix_pages, self.prefix_len = need, pages, n
+        if self.bits is None:
+            if need > self.free.shape[0]:
+                raise ValueError(f"{need} pages wanted, {self.free.shape[0]} there")
+            cache, pages = self.cache, self.free[:need].clone()
+        else:
+            cache = nys.PagedKV(need, self.page, att.kv_heads, att.d, att.dv, dtype=att.dtype,
+                                device=self.device)
+            pages = torch.arange(need, dtype=torch.int32, device=self.device)
+        slots = pages.long()[at // self.page] * self.page + at % self.page
+        if self.prepare is None:
+            cache.write(k, v, slots)
+        else:
+            self.prepare.append(None, k, v, at.int(), slots, cache)
+        self.used = need if self.bits is None else 0
+        self.prefix_cache, self.prefix_pages, self.prefix_len = cache, pages, n
 
     def admit(self, q, k, v, lengths):
         """The requests' prompts, packed back to back (q [sum][heads][d], k and v
@@ -144,13 +171,14 @@ class ExactLayer:
             first = torch.empty_like(out)
             none = torch.zeros(rows, dtype=torch.int32, device=self.device)
             att._workspace(rows, rows, self.prefix_len)
+        ready = self._ready_rows(q, k, True)
         plan = self._plan(list(lengths))
-        self.cache.write(k, v, plan.slots)
+        q, k = self._write(q, k, v, plan, *ready)
         if self.prefix_len == 0:
             return att.prompt(q, k, v, plan.q_off, out)
         # Over the prompt's own keys and, as rows without own keys, over the prefix.
         att.prompt(q, k, v, plan.q_off, out, lse=lse)
-        att.shared(q, self.cache, none, none.view(rows, 1), first,
+        att.shared(q, self.prefix_cache, none, none.view(rows, 1), first,
                    prefix_pages=self.prefix_pages, prefix_len=self.prefix_len, lse=over)
         return merge(out, lse, first, over, out)
 
@@ -163,11 +191,57 @@ class ExactLayer:
         self._check(q, k, v)
         out = self.torch.empty((self.requests, att.heads, att.dv), dtype=att.dtype,
                                device=self.device)
+        lse = None
         att._workspace(self.requests, self.requests, self.prefix_len)
+        if self.bits is not None:
+            att._workspace(self.requests, self.width * self.page, None)
+            if self.prefix_len > 0:
+                lse = self.torch.empty((self.requests, att.heads), device=self.device)
+                none = self.torch.zeros((self.requests, 1), dtype=self.torch.int32,
+                                        device=self.device)
+        ready = self._ready_rows(q, k, False)
         plan = self._plan([1] * self.requests)
-        self.cache.write(k, v, plan.slots)
-        return att.shared(q, self.cache, self.lens, self.table, out,
-                          prefix_pages=self.prefix_pages, prefix_len=self.prefix_len)
+        q, _ = self._write(q, k, v, plan, *ready)
+        if self.bits is None:
+            return att.shared(q, self.cache, self.lens, self.table, out,
+                              prefix_pages=self.prefix_pages, prefix_len=self.prefix_len)
+        if lse is None:
+            return att.paged4(q, self.cache, self.lens, self.table, out)
+        # Over the prefix, then over the request's own keys, joined in place.
+        att.shared(q, self.prefix_cache, none.view(-1), none, out, prefix_pages=self.prefix_pages,
+                   prefix_len=self.prefix_len, lse=lse)
+        return att.paged4(q, self.cache, self.lens, self.table, out, first=out, first_lse=lse)
+
+    def _ready_rows(self, q, k, keys):
+        """Room for prepared queries and, for a prompt, keys; None where rows come ready."""
+        if self.prepare is None:
+            return None, None
+        make = lambda x: self.torch.empty(x.shape, dtype=x.dtype, device=self.device)
+        return make(q), make(k) if keys else None
+
+    def _write(self, q, k, v, plan, q_out, k_out):
+        """New rows into their pages; returns the queries and keys that attention takes."""
+        if self.prepare is None:
+            self.cache.write(k, v, plan.slots)
+            return q, k
+        self.prepare.append(q, k, v, plan.positions, plan.slots, self.cache, q_out=q_out,
+                            k_out=k_out, shift=self.prefix_len)
+        return q_out, k_out
+
+    def cached(self, i):
+        """Keys and values [tokens][kv_heads][d|dv] of request i as its pages hold them, the
+        prefix's not among them: for a prompt that goes on (ExactAttention.prompt with
+        k_off) or for states that are sealed later (seal_prompts)."""
+        torch, att, n = self.torch, self.attention, self.lengths[i]
+        at = torch.arange(n, device=self.device)
+        slots = self.table[i].long()[at // self.page] * self.page + at % self.page
+        if self.bits is None:
+            take = lambda x: x.view(-1, *x.shape[2:])[slots]
+            return take(self.cache.k), take(self.cache.v)
+        k, v = (torch.empty((n, att.kv_heads, c), dtype=att.dtype, device=self.device)
+                for c in (att.d, att.dv))
+        self.cache.read(slots, k, v)
+        return k, v
 
 
 def seal_prompts(states, q, k, v, lengths, g0=0):
