@@ -45,7 +45,7 @@ __device__ __forceinline__ int value_word4(int g, int t, int x) {
 }
 #endif
 
-// Rows of queries, keys and values on their way to attention (nys_qk.cu).
+// Rows of queries, keys and values on their way to attention (nys_qk.cuh).
 struct QkArgs {
   Rows q, k, v, q_out, k_out;  // p null: not there
   const float *q_weight, *k_weight;
@@ -86,6 +86,12 @@ struct Attn4Args {
   int32_t* status;
 };
 
+cudaError_t launch_qk_f32(const QkArgs& a, cudaStream_t stream);
+cudaError_t launch_qk_bf16(const QkArgs& a, cudaStream_t stream);
+cudaError_t launch_qk_f16(const QkArgs& a, cudaStream_t stream);
+cudaError_t launch_read4_f32(const Read4Args& a, cudaStream_t stream);
+cudaError_t launch_read4_bf16(const Read4Args& a, cudaStream_t stream);
+cudaError_t launch_read4_f16(const Read4Args& a, cudaStream_t stream);
 cudaError_t launch_qk(const QkArgs& a, cudaStream_t stream);
 cudaError_t launch_read4(const Read4Args& a, cudaStream_t stream);
 cudaError_t launch_attn4(const Attn4Args& a, void* workspace, cudaStream_t stream);

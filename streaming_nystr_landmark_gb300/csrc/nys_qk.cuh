@@ -1,0 +1,574 @@
+// Queries, keys and values on their way from a layer's projections to attention:
+//
+//   y = x / sqrt(mean_i x_i^2 + eps) * w          per head (queries and keys)
+//   (a, b) -> (a cos t - b sin t, a sin t + b cos t),  t = (position + shift) f_i,
+//
+// for the pairs (i, i + half) or (2i, 2i + 1) of the first 2 half numbers, written to
+// q_out and k_out, or with the values into the pages of their slots, as they are or in
+// 4 bits.  f32 throughout, rounded once where a row is stored.
+//
+// Angles: f_i comes as turns a position, a 64-bit binary fraction F_i.  The product with
+// the position modulo 2^64 is the exact fraction of a turn for any 32-bit position, off
+// by position * 2^-65 turns for the rounding of F_i; its upper 32 bits go to sinpi and
+// cospi.  (In f32 the angle of position 10^6 would be off by 0.06.)
+//
+// 4 bits: for a group of 64 numbers with least lo and largest hi
+//   mid  = bf16(lo + (hi - lo) 8/15),  step = bf16 up(max((hi - mid) / 7, (mid - lo) / 8)),
+//   code = round((x - mid) / step) + 8, ties to even, held in 0 .. 15,
+// each operation rounded to f32, quotients correctly (for the codes by Markstein's
+// correction of a product with the reciprocal: 2 FMAs instead of a division).  Every
+// number is held to half a step; a group with a number that is not finite, or of a
+// spread past f32, has a step of NaN.
+//
+// Bound by HBM: a row is read and written once.  A warp takes a token (a part of its rows
+// where there are few tokens): it makes the token's sines once, turns them and the weights into two
+// factors a number, y_i = (x_i A_i + x_pair B_i) / rms, and runs over the heads.  A row
+// lies over 8, 16 or 32 lanes, two chunks of 4 numbers a lane: where half is a multiple
+// of 4 those are the two sides of 4 pairs, so that no number leaves its lane; for 4 bits a
+// row goes through shared memory once more, to 8 numbers in a row a lane, a code word.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "nys_attn_tc.h"
+#include "nys_kv4.h"
+
+namespace nys {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxHalf = kAttnMaxDim / 2;
+// Pairs: none; numbers i and i + half, half a multiple of 4; 2i and 2i + 1, half even; the rest.
+enum Turn { kNone, kSides, kNext, kOdd };
+// Rows: 16-byte aligned and 8 numbers for each lane; every 4 numbers an aligned word; any.
+enum Form { kWhole, kWords, kAny };
+constexpr float kLeastStep = 0x1p-100f;
+
+template <typename T>
+struct alignas(4 * sizeof(T)) Four {
+  T x[4];
+};
+
+// Four numbers widened, and back.
+__device__ __forceinline__ void widen(const Four<float>& r, float* x) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = r.x[i];
+}
+__device__ __forceinline__ void widen(const Four<__nv_bfloat16>& r, float* x) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(&r);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void widen(const Four<__half>& r, float* x) {
+  const __half2* w = reinterpret_cast<const __half2*>(&r);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float2 y = __half22float2(w[i]);
+    x[2 * i] = y.x;
+    x[2 * i + 1] = y.y;
+  }
+}
+__device__ __forceinline__ Four<float> narrow(const float* x, float) { return {x[0], x[1], x[2], x[3]}; }
+__device__ __forceinline__ Four<__nv_bfloat16> narrow(const float* x, __nv_bfloat16) {
+  Four<__nv_bfloat16> r;
+  __nv_bfloat162* w = reinterpret_cast<__nv_bfloat162*>(&r);
+  w[0] = __floats2bfloat162_rn(x[0], x[1]);
+  w[1] = __floats2bfloat162_rn(x[2], x[3]);
+  return r;
+}
+__device__ __forceinline__ Four<__half> narrow(const float* x, __half) {
+  Four<__half> r;
+  __half2* w = reinterpret_cast<__half2*>(&r);
+  w[0] = __floats2half2_rn(x[0], x[1]);
+  w[1] = __floats2half2_rn(x[2], x[3]);
+  return r;
+}
+
+// A lane's two chunks of 4 numbers: at p + c0 and p + c1 (in0, in1: of the row; others are 0).
+template <typename T, Form F, bool InARow>
+__device__ __forceinline__ void get8(Four<T> (&r)[2], const T* p, int c0, int c1, bool in0, bool in1) {
+  if (F == kWhole && InARow && sizeof(T) == 2) {
+    uint4 y = make_uint4(0, 0, 0, 0);
+    if (in0) y = *reinterpret_cast<const uint4*>(p + c0);
+    *reinterpret_cast<uint2*>(&r[0]) = make_uint2(y.x, y.y);
+    *reinterpret_cast<uint2*>(&r[1]) = make_uint2(y.z, y.w);
+    return;
+  }
+  r[0] = r[1] = Four<T>{};
+  if (F != kAny) {
+    if (in0) r[0] = *reinterpret_cast<const Four<T>*>(p + c0);
+    if (in1) r[1] = *reinterpret_cast<const Four<T>*>(p + c1);
+  } else {
+    if (in0) r[0] = {p[c0], p[c0 + 1], p[c0 + 2], p[c0 + 3]};
+    if (in1) r[1] = {p[c1], p[c1 + 1], p[c1 + 2], p[c1 + 3]};
+  }
+}
+template <typename T, Form F, bool InARow>
+__device__ __forceinline__ void put8(const Four<T> (&r)[2], T* p, int c0, int c1, bool in0, bool in1) {
+  if (F == kWhole && InARow && sizeof(T) == 2) {
+    const uint2 x = *reinterpret_cast<const uint2*>(&r[0]), y = *reinterpret_cast<const uint2*>(&r[1]);
+    if (in0) *reinterpret_cast<uint4*>(p + c0) = make_uint4(x.x, x.y, y.x, y.y);
+    return;
+  }
+  if (F != kAny) {
+    if (in0) *reinterpret_cast<Four<T>*>(p + c0) = r[0];
+    if (in1) *reinterpret_cast<Four<T>*>(p + c1) = r[1];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (in0) p[c0 + i] = r[0].x[i];
+      if (in1) p[c1 + i] = r[1].x[i];
+    }
+  }
+}
+// The form that rows have which start at p.
+template <typename T>
+Form form_of(const void* p, int64_t row, int64_t head, int dim, int lanes) {
+  const uintptr_t all = reinterpret_cast<uintptr_t>(p) | (uintptr_t)(row * sizeof(T)) | (uintptr_t)(head * sizeof(T));
+  return all % 16 == 0 && dim == 8 * lanes ? kWhole : all % sizeof(Four<T>) == 0 ? kWords : kAny;
+}
+
+// x / by, rounded correctly, for inv = 1 / by rounded (Markstein), of a quotient that is
+// no subnormal number.
+__device__ __forceinline__ float quotient(float x, float by, float inv) {
+  const float q = __fmul_rn(x, inv);
+  return __fmaf_rn(__fmaf_rn(-q, by, x), inv, q);
+}
+
+// A group of 64 numbers over 8 lanes, the first n of 8 a lane, to its scale word and this
+// lane's 8 codes.
+__device__ __forceinline__ uint32_t quantize(const float (&y)[8], int n, uint32_t& scale) {
+  float lo = INFINITY, hi = -INFINITY, odd = 0.f;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    if (n >= 4 * h + 4) {
+#pragma unroll
+      for (int i = 4 * h; i < 4 * h + 4; ++i) {
+        lo = fminf(lo, y[i]);
+        hi = fmaxf(hi, y[i]);
+        odd += y[i];  // fminf and fmaxf pass over NaN, a sum does not
+      }
+    }
+  // Bit 0: a NaN, bit 1: a number at all.  (Opposite infinities count as NaN, rightly.)
+  uint32_t flags = (odd != odd ? 1u : 0u) | (n >= 4 ? 2u : 0u);
+#pragma unroll
+  for (int o = 4; o; o >>= 1) {
+    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o, 8));
+    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o, 8));
+    flags |= __shfl_xor_sync(0xffffffffu, flags, o, 8);
+  }
+  if (flags == 0) {
+    scale = 0;
+    return 0x88888888u;
+  }
+  const float span = __fmul_rn(__fsub_rn(hi, lo), 8.f);
+  const bool plain = span > 0x1p-90f && span < 0x1p125f;  // (the quotients' precondition)
+  const float part = plain ? quotient(span, 15.f, 1.f / 15.f) : __fdiv_rn(span, 15.f);
+  const float mid = __bfloat162float(__float2bfloat16_rn(__fadd_rn(lo, part)));
+  const float up = __fsub_rn(hi, mid);
+  float step = fmaxf(plain ? quotient(up, 7.f, 1.f / 7.f) : __fdiv_rn(up, 7.f),
+                     __fmul_rn(__fsub_rn(mid, lo), 0.125f));
+  step = __uint_as_float((__float_as_uint(step) + 0xffffu) & 0xffff0000u);
+  if ((flags & 1) || !(fabsf(mid) < INFINITY) || !(step < INFINITY)) {
+    scale = 0x7fc07fc0u;
+    return 0x88888888u;
+  }
+  if (step < kLeastStep) step = 0.f;
+  scale = __float_as_uint(step) | __float_as_uint(mid) >> 16;
+  if (step == 0.f) return 0x88888888u;
+  const float inv = __frcp_rn(step);
+  // t is in -8 .. 7 but for its rounding: t + 1.5 * 2^23 + 8 rounds it to a whole number, ties to
+  // even, and has the code in its last bits; the bits above them add up to a constant.
+  uint32_t codes = 0;
+#pragma unroll
+  for (int i = 7; i >= 0; --i) {
+    const float x = n >= (i / 4 + 1) * 4 ? __fsub_rn(y[i], mid) : 0.f;
+    codes = codes * 16 + __float_as_uint(__fadd_rn(quotient(x, step, inv), 12582920.f));
+  }
+  return codes - 0x3f400000u;  // 0x4b400000 * (1 + 16 + .. + 16^7), modulo 2^32
+}
+
+enum Kind { kQueries, kKeys, kValues };
+
+// What a warp knows of its token.
+struct Token {
+  int64_t at;       // its row
+  int64_t slot;     // < 0: none
+  uint32_t* block;  // of KV head 0, 4-bit caches
+  int in;           // place in the block
+};
+
+// Where a lane's two chunks of a row start.
+struct Chunks {
+  int at[2];
+  bool pair;  // they are two sides
+};
+template <Turn R>
+__device__ __forceinline__ Chunks chunks_of(int l, int half) {
+  if (R == kSides) {
+    const int over = l - half / 4;
+    if (over < 0) return {{4 * l, half + 4 * l}, true};
+    return {{2 * half + 8 * over, 2 * half + 8 * over + 4}, false};
+  }
+  return {{8 * l, 8 * l + 4}, false};
+}
+// The other number of number x's pair, and whether x is the pair's second.
+__device__ __forceinline__ int pair_of(int x, int half, bool interleaved) {
+  return interleaved ? x ^ 1 : x < half ? x + half : x - half;
+}
+__device__ __forceinline__ bool is_second(int x, int half, bool interleaved) {
+  return interleaved ? x & 1 : x >= half;
+}
+
+// Heads first + sub, first + sub + 32 / L, .. below end of one kind of rows.
+template <typename T, int L, bool Q4, Turn R, Form F, Kind K>
+__device__ __forceinline__ void run_rows(const QkArgs& a, const Token& t, int first, int end,
+                                         const float2* turns, float* stage) {
+  constexpr int kPer = 32 / L;
+  constexpr int kAhead = sizeof(T) == 4 ? 2 : R == kOdd ? 3 : 4;  // steps whose loads are in flight
+  constexpr Turn S = K == kValues ? kNone : R;
+  constexpr bool kInARow = S != kSides;
+  const int lane = threadIdx.x & 31, l = lane & (L - 1), sub = lane / L;
+  const Rows& from = K == kQueries ? a.q : K == kKeys ? a.k : a.v;
+  const Rows& to = K == kQueries ? a.q_out : a.k_out;
+  const int dim = F == kWhole ? 8 * L : K == kValues ? a.dv : a.d;
+  const int half = a.half;
+  const Chunks c = chunks_of<S>(l, half);
+  const bool in0 = F == kWhole || c.at[0] < dim, in1 = F == kWhole || c.at[1] < dim;
+  const T* src = static_cast<const T*>(from.p) + t.at * from.row + (first + sub) * from.head;
+  Four<T> raw[kAhead][2];
+  auto load = [&](Four<T> (&r)[2], int h) {
+    get8<T, F, kInARow>(r, src, c.at[0], c.at[1], h < end && in0, h < end && in1);
+    src += kPer * from.head;
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) load(raw[i], first + i * kPer + sub);
+
+  // y_i = (x_i A_i + x_pair B_i) * inv.
+  float fa[8], fb[8];
+  const float* weight = K == kQueries ? a.q_weight : a.k_weight;
+  const bool turned[2] = {S == kSides ? c.pair : c.at[0] < 2 * half, S == kSides ? c.pair : c.at[1] < 2 * half};
+  if (K != kValues) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int x = c.at[i / 4] + i % 4;
+      fa[i] = weight && (i < 4 ? in0 : in1) ? weight[x] : 1.f;
+      fb[i] = 0.f;
+    }
+    if (S == kSides && c.pair) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 z = turns[4 * l + i];
+        const float wa = fa[i], wb = fa[4 + i];
+        fa[i] = wa * z.x;
+        fb[i] = -(wb * z.y);
+        fa[4 + i] = wb * z.x;
+        fb[4 + i] = wa * z.y;
+      }
+    }
+    if (S == kNext) {
+#pragma unroll
+      for (int i = 0; i < 8; i += 2)
+        if (turned[i / 4]) {
+          const float2 z = turns[(c.at[i / 4] + i % 4) / 2];
+          const float wa = fa[i], wb = fa[i + 1];
+          fa[i] = wa * z.x;
+          fb[i] = -(wb * z.y);
+          fa[i + 1] = wb * z.x;
+          fb[i + 1] = wa * z.y;
+        }
+    }
+    if (S == kOdd) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int x = c.at[i / 4] + i % 4;
+        if (x < 2 * half) {
+          const int pair = pair_of(x, half, a.interleaved);
+          const bool second = is_second(x, half, a.interleaved);
+          const float2 z = turns[a.interleaved ? x / 2 : second ? pair : x];
+          const float wp = weight ? weight[pair] : 1.f;
+          fa[i] *= z.x;
+          fb[i] = second ? wp * z.y : -(wp * z.y);
+        }
+      }
+    }
+  }
+  const float inv_d = 1.f / (float)a.d;
+  T* dst = to.p && K != kValues ? static_cast<T*>(to.p) + t.at * to.row + (first + sub) * to.head : nullptr;
+  T* page = nullptr;
+  if (!Q4 && K != kQueries && t.slot >= 0)
+    page = static_cast<T*>(K == kValues ? a.pool_v : a.pool_k) + (t.slot * a.kv_heads + first + sub) * dim;
+
+  for (int base = first; base < end; base += kAhead * kPer) {
+#pragma unroll
+    for (int b = 0; b < kAhead; ++b) {
+      const int h = base + b * kPer + sub;
+      if (h - sub >= end) break;
+      const bool row = kPer == 1 || h < end;
+      if (K == kValues && !Q4) {
+        put8<T, F, true>(raw[b], page, c.at[0], c.at[1], row && in0, row && in1);
+        page += kPer * dim;
+      } else {
+        float y[8];
+        widen(raw[b][0], y);
+        widen(raw[b][1], y + 4);
+        if (K != kValues) {
+          float inv = 1.f;
+          if (weight) {
+            float ss = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss = fmaf(y[i], y[i], ss);
+#pragma unroll
+            for (int o = L / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o, L);
+            inv = rsqrtf(fmaf(ss, inv_d, a.eps));
+          }
+          float p[8];  // the other numbers of the pairs
+          if (S == kSides || S == kNext) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p[i] = y[S == kSides ? i ^ 4 : i ^ 1];
+          } else if (S == kOdd) {
+            // Number x at x + x / 8: the lanes' numbers i, 9 words apart, are in banks of their own.
+            float* mine = stage + sub * 9 * L;
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) mine[9 * l + i] = y[i];
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int x = pair_of(8 * l + i, half, a.interleaved);
+              p[i] = 8 * l + i < 2 * half ? mine[x + x / 8] : 0.f;
+            }
+          }
+          // (Beyond 2 half there is no pair: what lies in its place may be infinite.)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            if (S == kOdd || (S != kNone && turned[e])) {
+#pragma unroll
+              for (int i = 4 * e; i < 4 * e + 4; ++i) y[i] = fmaf(y[i], fa[i], p[i] * fb[i]) * inv;
+            } else {
+#pragma unroll
+              for (int i = 4 * e; i < 4 * e + 4; ++i) y[i] = y[i] * fa[i] * inv;
+            }
+          }
+          const Four<T> z[2] = {narrow(y, T{}), narrow(y + 4, T{})};
+          if (dst) {
+            put8<T, F, kInARow>(z, dst, c.at[0], c.at[1], row && in0, row && in1);
+            dst += kPer * to.head;
+          }
+          if (page) {
+            put8<T, F, kInARow>(z, page, c.at[0], c.at[1], row && in0, row && in1);
+            page += kPer * dim;
+          }
+        }
+        if (Q4 && K != kQueries && t.slot >= 0) {
+          const int n = dim - 8 * l;
+          if (!kInARow) {  // from two sides to 8 numbers in a row
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if (i == 0 ? in0 : in1)
+                *reinterpret_cast<float4*>(stage + sub * 8 * L + c.at[i]) =
+                    make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float4 z = *reinterpret_cast<const float4*>(stage + sub * 8 * L + 8 * l + 4 * i);
+              y[4 * i] = z.x, y[4 * i + 1] = z.y, y[4 * i + 2] = z.z, y[4 * i + 3] = z.w;
+            }
+          }
+          uint32_t scale;
+          const uint32_t codes = quantize(y, n, scale);
+          const int g = l / 8, x = l & 7;
+          if (row && g < a.groups) {
+            uint32_t* at = t.block + (int64_t)h * a.page_blocks * (block4_bytes(a.groups) / 4);
+            at[K == kValues ? values4(a.groups) / 4 + value_word4(g, t.in, x) : key_word4(g, t.in, x)] = codes;
+            if (x == 0)
+              at[(K == kValues ? value_scales4(a.groups) : key_scales4(a.groups)) / 4 + g * 16 + place4(t.in)] =
+                  scale;
+          }
+        }
+      }
+      load(raw[b], h + kAhead * kPer);
+    }
+  }
+}
+
+// Block of a slot's token, of KV head 0.
+__device__ __forceinline__ int64_t block_of(int64_t slot, int kv_heads, int page_blocks) {
+  const int64_t block = slot >> 4;
+  if (block <= INT32_MAX) {
+    const uint32_t page = (uint32_t)block / (uint32_t)page_blocks;
+    return (int64_t)page * kv_heads * page_blocks + ((uint32_t)block - page * (uint32_t)page_blocks);
+  }
+  const int64_t page = block / page_blocks;
+  return page * kv_heads * page_blocks + (block - page * page_blocks);
+}
+
+// A warp takes part `w % parts` of token w / parts's steps of 32 / L rows.
+template <typename T, int L, bool Q4, Turn R, Form F>
+__global__ void __launch_bounds__(kThreads, R == kOdd ? 3 : 4) qk_kernel(QkArgs a, int parts) {
+  constexpr int kPer = 32 / L;
+  __shared__ __align__(16) float2 s_turn[kWarps][kMaxHalf];
+  __shared__ __align__(16) float s_stage[kWarps][288];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t w = (int64_t)blockIdx.x * kWarps + warp;
+  Token t;
+  t.at = parts == 1 ? w : w / parts;
+  if (t.at >= a.tokens) return;
+  const int part = (int)(w - t.at * parts);
+  const int sq = (a.heads + kPer - 1) / kPer, sk = (a.kv_heads + kPer - 1) / kPer;
+  const int all = sq + sk + (a.v.p ? sk : 0);
+  const int s0 = (int)((int64_t)all * part / parts), s1 = (int)((int64_t)all * (part + 1) / parts);
+  t.slot = a.slots ? a.slots[t.at] : -1;
+  if (t.slot >= a.n_slots) t.slot = -1;
+  if (Q4 && t.slot >= 0) {
+    t.block = reinterpret_cast<uint32_t*>(a.blocks + block_of(t.slot, a.kv_heads, a.page_blocks) *
+                                                         block4_bytes(a.groups));
+    t.in = (int)(t.slot & 15);
+  }
+  if (R != kNone && s0 < sq + sk) {
+    const uint64_t at = (uint64_t)((int64_t)a.positions[t.at] + a.shift);
+    for (int i = lane; i < a.half; i += 32) {
+      float2 z;  // cos, sin of the turn in [-1/2, 1/2)
+      const float x = (float)(int32_t)(uint32_t)((at * a.turns[i]) >> 32) * 0x1p-31f;
+      sincospif(x, &z.y, &z.x);
+      s_turn[warp][i] = z;
+    }
+    __syncwarp();
+  }
+  float* stage = s_stage[warp];
+  if (s0 < sq)
+    run_rows<T, L, Q4, R, F, kQueries>(a, t, s0 * kPer, min(a.heads, s1 * kPer), s_turn[warp], stage);
+  if (s1 > sq && s0 < sq + sk)
+    run_rows<T, L, Q4, R, F, kKeys>(a, t, max(s0 - sq, 0) * kPer, min(a.kv_heads, (s1 - sq) * kPer), s_turn[warp],
+                                 stage);
+  if (s1 > sq + sk && t.slot >= 0)
+    run_rows<T, L, Q4, R, F, kValues>(a, t, max(s0 - sq - sk, 0) * kPer, min(a.kv_heads, (s1 - sq - sk) * kPer),
+                                   s_turn[warp], stage);
+}
+
+// How many warps a token's `steps` go over: one where the tokens fill the SMs (more would make
+// each token's factors more than once: 4,099 tokens of 18 rows of 80, fp16, 21 -> 23 us with
+// two, 16,576 rows of 2,048 numbers read from 4 bits 24 -> 30 us).
+int64_t parts_of(int64_t tokens, int64_t steps) {
+  const int64_t parts = 152 * 32 / tokens;
+  return parts < 1 ? 1 : parts > steps ? steps : parts;
+}
+
+template <typename T, int L, bool Q4, Form F>
+cudaError_t launch(const QkArgs& a, cudaStream_t stream) {
+  constexpr int kPer = 32 / L;
+  const int sk = (a.kv_heads + kPer - 1) / kPer;
+  const int parts = (int)parts_of(a.tokens, (a.heads + kPer - 1) / kPer + sk + (a.v.p ? sk : 0));
+  const unsigned ctas = (unsigned)((a.tokens * parts + kWarps - 1) / kWarps);
+  if (a.half == 0) qk_kernel<T, L, Q4, kNone, F><<<ctas, kThreads, 0, stream>>>(a, parts);
+  else if (a.interleaved && a.half % 2 == 0) qk_kernel<T, L, Q4, kNext, F><<<ctas, kThreads, 0, stream>>>(a, parts);
+  else if (!a.interleaved && a.half % 4 == 0) qk_kernel<T, L, Q4, kSides, F><<<ctas, kThreads, 0, stream>>>(a, parts);
+  else qk_kernel<T, L, Q4, kOdd, F == kWhole ? kWords : F><<<ctas, kThreads, 0, stream>>>(a, parts);
+  return cudaGetLastError();
+}
+
+template <typename T, bool Q4>
+cudaError_t launch_of(const QkArgs& a, cudaStream_t stream) {
+  const int most = a.d > a.dv ? a.d : a.dv;
+  const int lanes = most <= 64 ? 8 : most <= 128 ? 16 : 32;
+  Form form = a.v.p && a.dv != a.d ? kWords : kWhole;
+  const auto take = [&](const Rows& r, int dim) {
+    if (!r.p) return;
+    const Form f = form_of<T>(r.p, r.row, r.head, dim, lanes);
+    form = form > f ? form : f;
+  };
+  take(a.q, a.d);
+  take(a.k, a.d);
+  take(a.v, a.dv);
+  take(a.q_out, a.d);
+  take(a.k_out, a.d);
+  take({a.pool_k, a.d, a.d}, a.d);
+  take({a.pool_v, a.dv, a.dv}, a.dv);
+  // (Rows of no alignment take 32 lanes, whatever their length.)
+  if (form == kAny) return launch<T, 32, Q4, kAny>(a, stream);
+  if (lanes == 8) return form == kWhole ? launch<T, 8, Q4, kWhole>(a, stream) : launch<T, 8, Q4, kWords>(a, stream);
+  if (lanes == 16) return form == kWhole ? launch<T, 16, Q4, kWhole>(a, stream) : launch<T, 16, Q4, kWords>(a, stream);
+  return form == kWhole ? launch<T, 32, Q4, kWhole>(a, stream) : launch<T, 32, Q4, kWords>(a, stream);
+}
+
+// Rows of a 4-bit cache as the values they stand for; a slot outside it gives zeros.  Warps
+// and lanes as above: a lane takes a code word.
+template <typename T, int L, Form F>
+__device__ __forceinline__ void read_rows(const Read4Args& a, const Token& t, bool values, int first, int end) {
+  constexpr int kPer = 32 / L;
+  const int lane = threadIdx.x & 31, l = lane & (L - 1), sub = lane / L;
+  const Rows& to = values ? a.v : a.k;
+  const int n = (values ? a.dv : a.d) - 8 * l;
+  if (n <= 0) return;
+  T* dst = static_cast<T*>(to.p) + t.at * to.row + 8 * l;
+  const int g = l / 8, x = l & 7;
+  const int code_at = values ? values4(a.groups) / 4 + value_word4(g, t.in, x) : key_word4(g, t.in, x);
+  const int scale_at = (values ? value_scales4(a.groups) : key_scales4(a.groups)) / 4 + g * 16 + place4(t.in);
+  const int64_t stride = (int64_t)a.page_blocks * (block4_bytes(a.groups) / 4);
+#pragma unroll 4
+  for (int h = first + sub; h < end; h += kPer) {
+    uint32_t codes = 0, scale = 0;
+    if (t.block) {
+      codes = t.block[h * stride + code_at];
+      scale = t.block[h * stride + scale_at];
+    }
+    const float step = __uint_as_float(scale & 0xffff0000u), mid = __uint_as_float(scale << 16);
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)  // the product is exact: 8 + 4 bits
+      y[i] = mid + step * (float)((int)(codes >> (4 * i) & 15) - 8);
+    const Four<T> z[2] = {narrow(y, T{}), narrow(y + 4, T{})};
+    put8<T, F, true>(z, dst + h * to.head, 0, 4, true, n > 4);
+  }
+}
+
+template <typename T, int L, Form F>
+__global__ void __launch_bounds__(kThreads) read4_kernel(Read4Args a, int parts) {
+  constexpr int kPer = 32 / L;
+  const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  Token t;
+  t.at = parts == 1 ? w : w / parts;
+  if (t.at >= a.tokens) return;
+  const int part = (int)(w - t.at * parts), sk = (a.kv_heads + kPer - 1) / kPer;
+  const int s0 = (int)((int64_t)2 * sk * part / parts), s1 = (int)((int64_t)2 * sk * (part + 1) / parts);
+  t.slot = a.slots[t.at];
+  t.block = nullptr;
+  t.in = (int)(t.slot & 15);
+  if (t.slot >= 0 && t.slot < a.n_slots)
+    t.block = const_cast<uint32_t*>(reinterpret_cast<const uint32_t*>(
+        a.blocks + block_of(t.slot, a.kv_heads, a.page_blocks) * block4_bytes(a.groups)));
+  if (s0 < sk) read_rows<T, L, F>(a, t, false, s0 * kPer, min(a.kv_heads, s1 * kPer));
+  if (s1 > sk) read_rows<T, L, F>(a, t, true, max(s0 - sk, 0) * kPer, min(a.kv_heads, (s1 - sk) * kPer));
+}
+
+template <typename T, int L, Form F>
+cudaError_t launch_read(const Read4Args& a, cudaStream_t stream) {
+  const int64_t parts = parts_of(a.tokens, 2 * ((a.kv_heads + 32 / L - 1) / (32 / L)));
+  const int64_t ctas = (a.tokens * parts + kWarps - 1) / kWarps;
+  read4_kernel<T, L, F><<<(unsigned)ctas, kThreads, 0, stream>>>(a, (int)parts);
+  return cudaGetLastError();
+}
+template <typename T>
+cudaError_t launch_read_of(const Read4Args& a, cudaStream_t stream) {
+  const int most = a.d > a.dv ? a.d : a.dv;
+  const int lanes = most <= 64 ? 8 : most <= 128 ? 16 : 32;
+  const Form k = form_of<T>(a.k.p, a.k.row, a.k.head, a.d, lanes);
+  const Form v = form_of<T>(a.v.p, a.v.row, a.v.head, a.dv, lanes);
+  const Form form = k > v ? k : v;
+  if (form == kAny) return launch_read<T, 32, kAny>(a, stream);
+  if (lanes == 8) return form == kWhole ? launch_read<T, 8, kWhole>(a, stream) : launch_read<T, 8, kWords>(a, stream);
+  if (lanes == 16)
+    return form == kWhole ? launch_read<T, 16, kWhole>(a, stream) : launch_read<T, 16, kWords>(a, stream);
+  return form == kWhole ? launch_read<T, 32, kWhole>(a, stream) : launch_read<T, 32, kWords>(a, stream);
+}
+
+}  // namespace
+}  // namespace nys
