@@ -42,7 +42,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxHalf = kAttnMaxDim / 2;
-// Pairs: none; numbers i and i + half, half a multiple of 4; 2i and 2i + 1, half even; the rest.
+// Pairs: none; numbers i and i + half, half a multiple of 4; 2i and 2i + 1; i and i + half, any half.
 enum Turn { kNone, kSides, kNext, kOdd };
 // Rows: 16-byte aligned and 8 numbers for each lane; every 4 numbers an aligned word; any.
 enum Form { kWhole, kWords, kAny };
@@ -135,6 +135,52 @@ Form form_of(const void* p, int64_t row, int64_t head, int dim, int lanes) {
   return all % 16 == 0 && dim == 8 * lanes ? kWhole : all % sizeof(Four<T>) == 0 ? kWords : kAny;
 }
 
+// Two f32 operations an instruction, each rounded as its own.
+struct Two {
+  uint64_t w;
+  __device__ __forceinline__ Two() {}
+  __device__ __forceinline__ Two(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(w) : "f"(a), "f"(b)); }
+  __device__ __forceinline__ void get(float& a, float& b) const {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(w));
+  }
+};
+__device__ __forceinline__ Two add(Two a, Two b) {
+  Two c;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(c.w) : "l"(a.w), "l"(b.w));
+  return c;
+}
+__device__ __forceinline__ Two mul(Two a, Two b) {
+  Two c;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(c.w) : "l"(a.w), "l"(b.w));
+  return c;
+}
+__device__ __forceinline__ Two fma(Two a, Two b, Two c) {
+  Two d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.w) : "l"(a.w), "l"(b.w), "l"(c.w));
+  return d;
+}
+// The least and largest of numbers; NaN if one is NaN.
+__device__ __forceinline__ float least(float a, float b) {
+  float c;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(c) : "f"(a), "f"(b));
+  return c;
+}
+__device__ __forceinline__ float largest(float a, float b) {
+  float c;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(c) : "f"(a), "f"(b));
+  return c;
+}
+__device__ __forceinline__ float least(float a, float b, float c) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float largest(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // x / by, rounded correctly, for inv = 1 / by rounded (Markstein), of a quotient that is
 // no subnormal number.
 __device__ __forceinline__ float quotient(float x, float by, float inv) {
@@ -142,41 +188,35 @@ __device__ __forceinline__ float quotient(float x, float by, float inv) {
   return __fmaf_rn(__fmaf_rn(-q, by, x), inv, q);
 }
 
-// A group of 64 numbers over 8 lanes, the first n of 8 a lane, to its scale word and this
-// lane's 8 codes.
+// A group of 64 numbers over 8 lanes, the first n of 8 a lane (All: 8), to its scale word and
+// this lane's 8 codes.
+template <bool All>
 __device__ __forceinline__ uint32_t quantize(const float (&y)[8], int n, uint32_t& scale) {
-  float lo = INFINITY, hi = -INFINITY, odd = 0.f;
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-    if (n >= 4 * h + 4) {
-#pragma unroll
-      for (int i = 4 * h; i < 4 * h + 4; ++i) {
-        lo = fminf(lo, y[i]);
-        hi = fmaxf(hi, y[i]);
-        odd += y[i];  // fminf and fmaxf pass over NaN, a sum does not
-      }
-    }
-  // Bit 0: a NaN, bit 1: a number at all.  (Opposite infinities count as NaN, rightly.)
-  uint32_t flags = (odd != odd ? 1u : 0u) | (n >= 4 ? 2u : 0u);
+  float lo = INFINITY, hi = -INFINITY;
+  if (All || n >= 8) {
+    lo = least(least(y[0], y[1], y[2]), least(y[3], y[4], y[5]), least(y[6], y[7]));
+    hi = largest(largest(y[0], y[1], y[2]), largest(y[3], y[4], y[5]), largest(y[6], y[7]));
+  } else if (n >= 4) {
+    lo = least(least(y[0], y[1]), y[2], y[3]);
+    hi = largest(largest(y[0], y[1]), y[2], y[3]);
+  }
 #pragma unroll
   for (int o = 4; o; o >>= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o, 8));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o, 8));
-    flags |= __shfl_xor_sync(0xffffffffu, flags, o, 8);
+    lo = least(lo, __shfl_xor_sync(0xffffffffu, lo, o, 8));
+    hi = largest(hi, __shfl_xor_sync(0xffffffffu, hi, o, 8));
   }
-  if (flags == 0) {
-    scale = 0;
-    return 0x88888888u;
-  }
+  scale = 0;
+  if (!All && lo > hi) return 0x88888888u;  // no numbers of the row
   const float span = __fmul_rn(__fsub_rn(hi, lo), 8.f);
-  const bool plain = span > 0x1p-90f && span < 0x1p125f;  // (the quotients' precondition)
-  const float part = plain ? quotient(span, 15.f, 1.f / 15.f) : __fdiv_rn(span, 15.f);
+  float part = quotient(span, 15.f, 1.f / 15.f);
+  if (span < 0x1p-90f) part = __fdiv_rn(span, 15.f);
   const float mid = __bfloat162float(__float2bfloat16_rn(__fadd_rn(lo, part)));
   const float up = __fsub_rn(hi, mid);
-  float step = fmaxf(plain ? quotient(up, 7.f, 1.f / 7.f) : __fdiv_rn(up, 7.f),
-                     __fmul_rn(__fsub_rn(mid, lo), 0.125f));
+  float seventh = quotient(up, 7.f, 1.f / 7.f);
+  if (span < 0x1p-90f) seventh = __fdiv_rn(up, 7.f);
+  float step = largest(seventh, __fmul_rn(__fsub_rn(mid, lo), 0.125f));
   step = __uint_as_float((__float_as_uint(step) + 0xffffu) & 0xffff0000u);
-  if ((flags & 1) || !(fabsf(mid) < INFINITY) || !(step < INFINITY)) {
+  if (!(fabsf(mid) < INFINITY) || !(step < INFINITY)) {
     scale = 0x7fc07fc0u;
     return 0x88888888u;
   }
@@ -188,9 +228,16 @@ __device__ __forceinline__ uint32_t quantize(const float (&y)[8], int n, uint32_
   // even, and has the code in its last bits; the bits above them add up to a constant.
   uint32_t codes = 0;
 #pragma unroll
-  for (int i = 7; i >= 0; --i) {
-    const float x = n >= (i / 4 + 1) * 4 ? __fsub_rn(y[i], mid) : 0.f;
-    codes = codes * 16 + __float_as_uint(__fadd_rn(quotient(x, step, inv), 12582920.f));
+  for (int i = 6; i >= 0; i -= 2) {
+    float a = 0.f, b = 0.f;
+    if (All || n >= (i / 4 + 1) * 4) {
+      const Two x = add({y[i], y[i + 1]}, {-mid, -mid}), q = mul(x, {inv, inv});
+      const Two t = fma(fma(q, {-step, -step}, x), {inv, inv}, q);
+      t.get(a, b);
+    }
+    float c, d;
+    add({a, b}, {12582920.f, 12582920.f}).get(c, d);
+    codes = (codes * 16 + __float_as_uint(d)) * 16 + __float_as_uint(c);
   }
   return codes - 0x3f400000u;  // 0x4b400000 * (1 + 16 + .. + 16^7), modulo 2^32
 }
@@ -219,12 +266,11 @@ __device__ __forceinline__ Chunks chunks_of(int l, int half) {
   }
   return {{8 * l, 8 * l + 4}, false};
 }
-// The other number of number x's pair, and whether x is the pair's second.
-__device__ __forceinline__ int pair_of(int x, int half, bool interleaved) {
-  return interleaved ? x ^ 1 : x < half ? x + half : x - half;
-}
-__device__ __forceinline__ bool is_second(int x, int half, bool interleaved) {
-  return interleaved ? x & 1 : x >= half;
+// Where the other number of the pair of number x = 8 l + i is, x / 8 further on for each
+// number x so that a warp's numbers i are in banks of their own; less 9 l.
+__device__ __forceinline__ int pair_at(int i, int half, bool is_first) {
+  const int a = half / 8, b = half % 8;
+  return is_first ? 9 * a + i + b + (i + b >= 8) : i - b - 9 * a - (i < b);
 }
 
 // Heads first + sub, first + sub + 32 / L, .. below end of one kind of rows.
@@ -232,7 +278,7 @@ template <typename T, int L, bool Q4, Turn R, Form F, Kind K>
 __device__ __forceinline__ void run_rows(const QkArgs& a, const Token& t, int first, int end,
                                          const float2* turns, float* stage) {
   constexpr int kPer = 32 / L;
-  constexpr int kAhead = sizeof(T) == 4 ? 2 : R == kOdd ? 3 : 4;  // steps whose loads are in flight
+  constexpr int kAhead = sizeof(T) == 4 || Q4 ? 2 : R == kOdd ? 3 : 4;  // steps whose loads are in flight
   constexpr Turn S = K == kValues ? kNone : R;
   constexpr bool kInARow = S != kSides;
   const int lane = threadIdx.x & 31, l = lane & (L - 1), sub = lane / L;
@@ -253,15 +299,22 @@ __device__ __forceinline__ void run_rows(const QkArgs& a, const Token& t, int fi
 
   // y_i = (x_i A_i + x_pair B_i) * inv.
   float fa[8], fb[8];
+  float* mine = stage + sub * 9 * L;  // this row's numbers, x at x + x / 8 (kOdd)
   const float* weight = K == kQueries ? a.q_weight : a.k_weight;
   const bool turned[2] = {S == kSides ? c.pair : c.at[0] < 2 * half, S == kSides ? c.pair : c.at[1] < 2 * half};
   if (K != kValues) {
+    const bool word = reinterpret_cast<uintptr_t>(weight) % 16 == 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int x = c.at[i / 4] + i % 4;
-      fa[i] = weight && (i < 4 ? in0 : in1) ? weight[x] : 1.f;
-      fb[i] = 0.f;
+    for (int e = 0; e < 2; ++e) {
+      float4 w = make_float4(1.f, 1.f, 1.f, 1.f);
+      if (weight && (e == 0 ? in0 : in1)) {
+        const float* p = weight + c.at[e];
+        w = word ? *reinterpret_cast<const float4*>(p) : make_float4(p[0], p[1], p[2], p[3]);
+      }
+      fa[4 * e] = w.x, fa[4 * e + 1] = w.y, fa[4 * e + 2] = w.z, fa[4 * e + 3] = w.w;
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) fb[i] = 0.f;
     if (S == kSides && c.pair) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -276,7 +329,7 @@ __device__ __forceinline__ void run_rows(const QkArgs& a, const Token& t, int fi
     if (S == kNext) {
 #pragma unroll
       for (int i = 0; i < 8; i += 2)
-        if (turned[i / 4]) {
+        if (c.at[i / 4] + i % 4 < 2 * half) {
           const float2 z = turns[(c.at[i / 4] + i % 4) / 2];
           const float wa = fa[i], wb = fa[i + 1];
           fa[i] = wa * z.x;
@@ -286,16 +339,18 @@ __device__ __forceinline__ void run_rows(const QkArgs& a, const Token& t, int fi
         }
     }
     if (S == kOdd) {
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mine[9 * l + i] = fa[i];
+      __syncwarp();
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int x = c.at[i / 4] + i % 4;
+        const int x = 8 * l + i;
         if (x < 2 * half) {
-          const int pair = pair_of(x, half, a.interleaved);
-          const bool second = is_second(x, half, a.interleaved);
-          const float2 z = turns[a.interleaved ? x / 2 : second ? pair : x];
-          const float wp = weight ? weight[pair] : 1.f;
+          const float2 z = turns[x < half ? x : x - half];
+          const float wp = mine[9 * l + pair_at(i, half, x < half)];
           fa[i] *= z.x;
-          fb[i] = second ? wp * z.y : -(wp * z.y);
+          fb[i] = x < half ? -(wp * z.y) : wp * z.y;
         }
       }
     }
@@ -322,9 +377,12 @@ __device__ __forceinline__ void run_rows(const QkArgs& a, const Token& t, int fi
         if (K != kValues) {
           float inv = 1.f;
           if (weight) {
-            float ss = 0.f;
+            Two sums = mul({y[0], y[1]}, {y[0], y[1]});
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(y[i], y[i], ss);
+            for (int i = 2; i < 8; i += 2) sums = fma({y[i], y[i + 1]}, {y[i], y[i + 1]}, sums);
+            float ss, other;
+            sums.get(ss, other);
+            ss += other;
 #pragma unroll
             for (int o = L / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o, L);
             inv = rsqrtf(fmaf(ss, inv_d, a.eps));
@@ -334,27 +392,28 @@ __device__ __forceinline__ void run_rows(const QkArgs& a, const Token& t, int fi
 #pragma unroll
             for (int i = 0; i < 8; ++i) p[i] = y[S == kSides ? i ^ 4 : i ^ 1];
           } else if (S == kOdd) {
-            // Number x at x + x / 8: the lanes' numbers i, 9 words apart, are in banks of their own.
-            float* mine = stage + sub * 9 * L;
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < 8; ++i) mine[9 * l + i] = y[i];
             __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int x = pair_of(8 * l + i, half, a.interleaved);
-              p[i] = 8 * l + i < 2 * half ? mine[x + x / 8] : 0.f;
-            }
+            for (int i = 0; i < 8; ++i)
+              p[i] = 8 * l + i < 2 * half ? mine[9 * l + pair_at(i, half, 8 * l + i < half)] : 0.f;
           }
           // (Beyond 2 half there is no pair: what lies in its place may be infinite.)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             if (S == kOdd || (S != kNone && turned[e])) {
+              if (S == kNext && !(c.at[e] + 2 < 2 * half)) p[4 * e + 2] = p[4 * e + 3] = 0.f;
 #pragma unroll
-              for (int i = 4 * e; i < 4 * e + 4; ++i) y[i] = fmaf(y[i], fa[i], p[i] * fb[i]) * inv;
+              for (int i = 4 * e; i < 4 * e + 4; i += 2) {
+                const Two z = mul({p[i], p[i + 1]}, {fb[i], fb[i + 1]});
+                mul(fma({y[i], y[i + 1]}, {fa[i], fa[i + 1]}, z), {inv, inv}).get(y[i], y[i + 1]);
+              }
             } else {
 #pragma unroll
-              for (int i = 4 * e; i < 4 * e + 4; ++i) y[i] = y[i] * fa[i] * inv;
+              for (int i = 4 * e; i < 4 * e + 4; i += 2)
+                mul(mul({y[i], y[i + 1]}, {fa[i], fa[i + 1]}), {inv, inv}).get(y[i], y[i + 1]);
             }
           }
           const Four<T> z[2] = {narrow(y, T{}), narrow(y + 4, T{})};
@@ -384,7 +443,7 @@ __device__ __forceinline__ void run_rows(const QkArgs& a, const Token& t, int fi
             }
           }
           uint32_t scale;
-          const uint32_t codes = quantize(y, n, scale);
+          const uint32_t codes = quantize<F == kWhole>(y, n, scale);
           const int g = l / 8, x = l & 7;
           if (row && g < a.groups) {
             uint32_t* at = t.block + (int64_t)h * a.page_blocks * (block4_bytes(a.groups) / 4);
@@ -469,8 +528,8 @@ cudaError_t launch(const QkArgs& a, cudaStream_t stream) {
   const int parts = (int)parts_of(a.tokens, (a.heads + kPer - 1) / kPer + sk + (a.v.p ? sk : 0));
   const unsigned ctas = (unsigned)((a.tokens * parts + kWarps - 1) / kWarps);
   if (a.half == 0) qk_kernel<T, L, Q4, kNone, F><<<ctas, kThreads, 0, stream>>>(a, parts);
-  else if (a.interleaved && a.half % 2 == 0) qk_kernel<T, L, Q4, kNext, F><<<ctas, kThreads, 0, stream>>>(a, parts);
-  else if (!a.interleaved && a.half % 4 == 0) qk_kernel<T, L, Q4, kSides, F><<<ctas, kThreads, 0, stream>>>(a, parts);
+  else if (a.interleaved) qk_kernel<T, L, Q4, kNext, F><<<ctas, kThreads, 0, stream>>>(a, parts);
+  else if (a.half % 4 == 0) qk_kernel<T, L, Q4, kSides, F><<<ctas, kThreads, 0, stream>>>(a, parts);
   else qk_kernel<T, L, Q4, kOdd, F == kWhole ? kWords : F><<<ctas, kThreads, 0, stream>>>(a, parts);
   return cudaGetLastError();
 }
