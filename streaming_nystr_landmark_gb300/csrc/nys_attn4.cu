@@ -5,20 +5,23 @@
 //   step * (q . code) + mid * sum(q), and its part of the output
 //   sum_j (p_j step_j) code_j + sum_j p_j mid_j.
 //
-// The products take codes (whole numbers from -8 to 7, exact in 16 bits) and never see a
-// scale: keys' scales multiply a group's product, values' scales the weights.  q goes in
-// as two fp16 pieces (22 bits, after a power of two that fits its row), which are rows
-// 0-7 and 8-15 of mma.sync m16n8k16; weights go in as two bf16 pieces (16 bits), in f32
-// calls three.  Sums, maxima and the middles' part are f32.  A group of up to 8 heads
-// fills the products' 8 columns at best, and memory sets the time: the 128-row
-// tensor-memory form would be empty for the most part.
+// The products (mma.sync m16n8k16 in f16: memory is to set the time, and the 128-row
+// tensor-memory form would be empty for the most part) take codes less 8, whole numbers from -8
+// to 7, and never see a scale: keys' scales multiply a group's product, values' scales the
+// weights.  A code becomes a number by a mask into the mantissa of 1024 or, 4 bits higher, of 64,
+// and one subtraction.  Queries go in as two f16 pieces (22 bits, after a power of two that fits
+// the row) in rows r and r + 8, which the lane that needs their sum holds both; weights p_j step_j as two
+// f16 pieces too, after a power of two that follows the largest step so far (so that a weight is held to
+// 2^-38 of the largest).  The product's 8 rows and columns hold up to 8 heads; where there are at most 4, or
+// 2, the free ones hold the weights' second pieces, and the other half of the groups, so that a lane scales half
+// of them.  Sums, maxima and the middles' part are f32.
 //
-// A warp works by itself: it streams blocks of 16 tokens (1,152 bytes a group of 64) through
-// a ring of its own in shared memory with cp.async, and takes a range of one or more
-// requests' blocks.  Ranges come from the lengths, on the GPU, by either of two rules:
-// few (request, KV head) units are cut evenly into as many pieces as there are warps for;
-// many units are laid end to end and every warp takes an even share.  What cuts leave is
-// joined by a second launch.
+// A warp works by itself: it streams pairs of blocks of 16 tokens (1,152 bytes a group of 64
+// each) through a ring of its own in shared memory with cp.async, and takes a range of one or
+// more requests' blocks.  Ranges come from the lengths, on the GPU, by either of two rules:
+// few (request, KV head) units are cut into pieces of up to 32 blocks for a CTA, whose warps join their
+// results in shared memory; else the units are laid end to end and every warp takes an even share
+// (joined in the CTA where all four are of one unit).  What cuts leave is joined by a second launch.
 //
 // Blocks outside the pool are zeros, tokens past the length have weight 0 whatever their
 // bytes are.
@@ -37,17 +40,26 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kHeads = 8;       // heads of a unit
-constexpr int kLeast = 8;       // blocks of a piece of a cut unit, at least
+constexpr int kPiece = 32;      // blocks of a CTA's piece, at most
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kLazy = 8.f;
+constexpr float kLazy = 2.f;    // weights stay below 2^kLazy of the followed maximum's
 constexpr int kSms = 152;
+constexpr float kLeastStep4 = 0x1p-100f;  // but for 0
+constexpr uint32_t kUnits = 13;           // steps times up_g stay below 2^kUnits, weights below 2^15
 
+constexpr int kBoth = 2;        // blocks that are multiplied together: 32 tokens
+
+#ifndef NC
+#define NC 3
+#define NS 3
+#endif
 template <int G>
 struct Shape {
-  static constexpr int kStages = G <= 2 ? 4 : 3;
-  static constexpr int kCtas = G <= 2 ? 4 : G == 3 ? 3 : 2;  // of an SM
-  static constexpr int kSmem = kWarps * kStages * block4_bytes(G);
+  static constexpr int kStages = G <= 3 ? NS : 2;
+  static constexpr int kCtas = G <= 2 ? NC : 2;  // of an SM
+  static constexpr int kStage = kBoth * block4_bytes(G);
+  static constexpr int kSmem = kWarps * kStages * kStage;  // (two stages hold what a warp leaves)
 };
 
 // Pieces of cut units: in the workspace, first the units' records, then each piece's
@@ -85,19 +97,19 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                        uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// c = a b (First) or c + a b.
+template <bool First>
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (First)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // (x & mask) | bits: a code into the mantissa of a power of two.
 __device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
@@ -105,36 +117,25 @@ __device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t b
   asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "r"(mask), "r"(bits));
   return y;
 }
-// The two codes at bits 0-3 of the halves as fp16 code - 8: 1024 + code, less 1032.
-__device__ __forceinline__ uint32_t low_f16(uint32_t x) {
+// The two codes at bits 0-3 of the halves as code - 8: 1024 + code, less 1032.
+__device__ __forceinline__ uint32_t low_codes(uint32_t x) {
   const uint32_t y = and_or(x, 0x000f000fu, 0x64006400u);
   const __half2 z = __hsub2(*reinterpret_cast<const __half2*>(&y), __half2half2(__ushort_as_half(0x6408)));
   return *reinterpret_cast<const uint32_t*>(&z);
 }
 // The two at bits 4-7: 64 + code, less 72.
-__device__ __forceinline__ uint32_t high_f16(uint32_t x) {
+__device__ __forceinline__ uint32_t high_codes(uint32_t x) {
   const uint32_t y = and_or(x, 0x00f000f0u, 0x54005400u);
   const __half2 z = __hsub2(*reinterpret_cast<const __half2*>(&y), __half2half2(__ushort_as_half(0x5480)));
-  return *reinterpret_cast<const uint32_t*>(&z);
-}
-// The two at bits 0-3 as bf16: 128 + code, less 136.
-__device__ __forceinline__ uint32_t low_bf16(uint32_t x) {
-  const uint32_t y = and_or(x, 0x000f000fu, 0x43004300u);
-  const __nv_bfloat162 z = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&y),
-                                   __bfloat162bfloat162(__ushort_as_bfloat16(0x4308)));
   return *reinterpret_cast<const uint32_t*>(&z);
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 z = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&z);
 }
-// Two numbers as bf16, which are taken off them.
-__device__ __forceinline__ uint32_t take_bf16(float& lo, float& hi) {
-  const __nv_bfloat162 z = __floats2bfloat162_rn(lo, hi);
-  const uint32_t y = *reinterpret_cast<const uint32_t*>(&z);
-  lo -= __uint_as_float(y << 16);
-  hi -= __uint_as_float(y & 0xffff0000u);
-  return y;
+__device__ __forceinline__ Two unpack_f16(uint32_t x) {
+  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&x));
+  return {y.x, y.y};
 }
 __device__ __forceinline__ float step_of(uint32_t scale) { return __uint_as_float(scale & 0xffff0000u); }
 __device__ __forceinline__ float mid_of(uint32_t scale) { return __uint_as_float(scale << 16); }
@@ -229,269 +230,435 @@ __device__ __forceinline__ void put_result(const Attn4Args& a, int b, int h, int
   write4_as(a.out.p, b * a.out.row + h * a.out.head + c, a.dtype, y);
 }
 
-// Blocks [t0, t1) of unit (b, kvh, heads h0 ..) -> the final result, or piece `piece`.
-template <int G, bool F32>
-__device__ __forceinline__ void run_range(const Attn4Args& a, const Work4& w, uint32_t ring, int b,
-                                          int kvh, int h0, int t0, int t1, int piece) {
-  constexpr int kStages = Shape<G>::kStages, kBytes = block4_bytes(G);
-  constexpr int kWords = kBytes / 16;
-  const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-  const int len = len_of(a, b, false);
-  const int32_t* pages = a.table + (int64_t)b * a.width;
-  const int n_heads = min(kHeads, a.group - h0);
-  const int head0 = kvh * a.group + h0;
+// What row r of the products is: a head; second pieces of weights from row 4 on (not of 5 to 8 heads);
+// and, of up to 2 heads with more groups than one, groups g = slot + 2 x only.
+enum Rows4 { kEight, kFour, kTwo };
+template <int G, Rows4 R>
+struct Lane {
+  static constexpr int kHeadRows = R == kEight ? 8 : R == kFour ? 4 : 2;
+  static constexpr int kSlots = R == kTwo ? 2 : 1;
+  static constexpr int kOwn = (G + kSlots - 1) / kSlots;  // groups of a lane
+  static __device__ __forceinline__ int head(int r) { return r & (kHeadRows - 1); }
+  static __device__ __forceinline__ int slot(int r) { return R == kTwo ? r >> 1 & 1 : 0; }
+};
 
-  // Block t's place; the page's number is looked up one block ahead.
-  auto page_of = [&](int t) {
-    if (t >= t1 || t * kBlock4 >= len) return -1;
-    const int32_t pg = pages[t / a.page_blocks];
+// A query row in pieces: this lane's A operands of the products, and what goes with them.
+template <int G, Rows4 R>
+struct Query {
+  uint32_t a[G][2][2][4];
+  float sum[Lane<G, R>::kOwn];  // of the own groups' numbers
+  float scale;                  // of the scores, to base 2
+};
+// By way of `room` in shared memory (8 heads of 64 G numbers).
+template <int G, Rows4 R>
+__device__ __forceinline__ void make_query(Query<G, R>& q, const Attn4Args& a, int b, int head0, int n_heads,
+                                           float* room) {
+  const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+  const int h = Lane<G, R>::head(r), slot = Lane<G, R>::slot(r);
+#pragma unroll 1
+  for (int i = lane; i < n_heads * 16 * G; i += 32) {
+    const int head = i / (16 * G), d = 4 * (i - head * 16 * G);
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (d < a.d) y = read4_as(a.q.p, b * a.q.row + (head0 + head) * a.q.head + d, a.dtype);
+    *reinterpret_cast<float4*>(room + 4 * i) = y;
+  }
+  __syncwarp();
+  float x[G][2][8];
+  float most = 0.f;
+#pragma unroll
+  for (int g = 0; g < G; ++g)
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (h < n_heads) y = *reinterpret_cast<const float4*>(room + h * 64 * G + 64 * g + 32 * e + 8 * c + 4 * s);
+        x[g][e][4 * s] = y.x, x[g][e][4 * s + 1] = y.y, x[g][e][4 * s + 2] = y.z, x[g][e][4 * s + 3] = y.w;
+        most = largest(most, largest(fabsf(y.x), fabsf(y.y)), largest(fabsf(y.z), fabsf(y.w)));
+      }
+  most = largest(most, __shfl_xor_sync(0xffffffffu, most, 1));
+  most = largest(most, __shfl_xor_sync(0xffffffffu, most, 2));
+  // Numbers below 2^15; a row that is not finite has no scores.
+  const int exp = (int)(__float_as_uint(most) >> 23 & 255);
+  const float up = __uint_as_float((uint32_t)(min(14 - (exp - 127), 126) + 127) << 23);
+  q.scale = exp == 255 ? __uint_as_float(0x7fc00000u) : a.scale * kLog2e / up;
+#pragma unroll
+  for (int o = 0; o < Lane<G, R>::kOwn; ++o) q.sum[o] = 0.f;
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const bool own = g % Lane<G, R>::kSlots == slot;
+    float sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float y[8], low[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        y[i] = own ? x[g][e][i] * up : 0.f;
+        sum += y[i];
+        low[i] = (y[i] - __half2float(__float2half_rn(y[i]))) * 2048.f;
+      }
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          q.a[g][e][s][2 * i] = pack_f16(y[2 * s + i], y[2 * s + i + 4]);
+          q.a[g][e][s][2 * i + 1] = pack_f16(low[2 * s + i], low[2 * s + i + 4]);
+        }
+    }
+    q.sum[g / Lane<G, R>::kSlots] += sum;
+  }
+#pragma unroll
+  for (int o = 0; o < Lane<G, R>::kOwn; ++o) {
+    q.sum[o] += __shfl_xor_sync(0xffffffffu, q.sum[o], 1);
+    q.sum[o] += __shfl_xor_sync(0xffffffffu, q.sum[o], 2);
+  }
+}
+
+// Scores of this lane's head for the tokens 2c, 2c + 1, 2c + 8, 2c + 9 of a block, unscaled.  The
+// own groups' scales are `own` 64-byte steps apart from key_scales on.
+template <int G, Rows4 R>
+__device__ __forceinline__ void scores(const Query<G, R>& q, uint32_t at, int lane, float (&s)[4]) {
+  constexpr int kSlots = Lane<G, R>::kSlots;
+  const int c = lane & 3, slot = Lane<G, R>::slot(lane >> 2);
+  Two s2[2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+  for (int o = 0; o < Lane<G, R>::kOwn; ++o) {
+    float acc[2][4];
+#pragma unroll
+    for (int x = 0; x < kSlots; ++x) {
+      const int g = o * kSlots + x;
+      if (g >= G) continue;
+      const uint4 k = lds128(at + g * 512 + lane * 16);
+      const uint32_t words[2][2] = {{k.x, k.y}, {k.z, k.w}};
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t y = words[j][e], z = y >> 8;
+          if (x == 0 && e == 0) mma_f16<true>(acc[j], q.a[g][e][0], low_codes(y), high_codes(y));
+          else mma_f16<false>(acc[j], q.a[g][e][0], low_codes(y), high_codes(y));
+          mma_f16<false>(acc[j], q.a[g][e][1], low_codes(z), high_codes(z));
+        }
+    }
+    // (A last group that there is not: the row is 0, any scales do.)
+    const int g = o * kSlots + (G % kSlots && o == Lane<G, R>::kOwn - 1 ? 0 : slot);
+    const uint4 sc = lds128(at + key_scales4(G) + g * 64 + c * 16);
+    const uint32_t scales[2][2] = {{sc.x, sc.y}, {sc.z, sc.w}};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const Two dot = fma({acc[j][2], acc[j][3]}, {0x1p-11f, 0x1p-11f}, {acc[j][0], acc[j][1]});
+      const uint32_t a0 = scales[j][0], a1 = scales[j][1];
+      s2[j] = fma({step_of(a0), step_of(a1)}, dot, fma({mid_of(a0), mid_of(a1)}, {q.sum[o], q.sum[o]}, s2[j]));
+    }
+  }
+  s2[0].get(s[0], s[1]);
+  s2[1].get(s[2], s[3]);
+  if (R == kTwo) {  // the other groups' lanes
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], 8);
+  }
+}
+
+// What a warp leaves in shared memory of its range: results [heads][64 G] without the middles' part,
+// that part [heads][G], and each head's maximum and sum.  (And a log-sum that was read before any
+// is written, which may be in its place.)
+template <int G>
+struct Left {
+  float result[kHeads][64 * G];
+  float mid[kHeads][G];
+  float2 sum[kHeads];
+  float first[kHeads];  // the log-sum of what is joined in
+};
+
+// Blocks [t0, t1) of unit (b, kvh, heads h0 ..) -> `left`, which is the ring's place.
+template <int G, Rows4 R>
+__device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* room, int b, int kvh, int h0,
+                                          int t0, int t1) {
+  constexpr int kStages = Shape<G>::kStages, kBytes = block4_bytes(G), kStage = Shape<G>::kStage;
+  constexpr int kWords = kBytes / 16, kSlots = Lane<G, R>::kSlots, kOwn = Lane<G, R>::kOwn;
+  constexpr bool kColumns = R != kEight;  // second pieces are columns of their own
+  const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+  const int slot = Lane<G, R>::slot(r);
+  const uint32_t ring = tc::sptr(room);
+  const int len = len_of(a, b, false);
+  const int n_heads = min(kHeads, a.group - h0);
+
+  // The next block's page is looked up one block ahead.
+  int next = t0, in_page = t0 % a.page_blocks;
+  const int32_t* page_at = a.table + (int64_t)b * a.width + t0 / a.page_blocks;
+  const auto look_up = [&]() {
+    if (next >= t1 || next * kBlock4 >= len) return -1;
+    const int32_t pg = *page_at;
     if (pg < 0 || pg >= a.n_pages) {
       if (lane == 0) attn_report(a.status, NYS_ATTN_BAD_PAGE);
       return -1;
     }
     return pg;
   };
-  int ahead = page_of(t0);
-  auto fetch = [&](int t, int stage) {
-    const int pg = ahead;
-    ahead = page_of(t + 1);
-    if (t < t1) {
-      const uint8_t* src = a.blocks;
-      if (pg >= 0)
-        src += (((int64_t)pg * a.kv_heads + kvh) * a.page_blocks + t % a.page_blocks) * kBytes;
-      const uint32_t dst = ring + stage * kBytes;
+  int ahead = look_up();
+  const auto fetch = [&](uint32_t dst) {
 #pragma unroll
-      for (int i = 0; i < kWords; i += 32)
-        if (i + 32 <= kWords || i + lane < kWords)
-          cp16(dst + (i + lane) * 16, src + (i + lane) * 16, pg >= 0);
+    for (int e = 0; e < kBoth; ++e) {
+      if (next < t1) {
+        const int pg = ahead;
+        const uint8_t* src = a.blocks + lane * 16;
+        if (pg >= 0) src += (((int64_t)pg * a.kv_heads + kvh) * a.page_blocks + in_page) * kBytes;
+        ++next;
+        if (++in_page == a.page_blocks) {
+          in_page = 0;
+          ++page_at;
+        }
+        ahead = look_up();
+#pragma unroll
+        for (int i = 0; i < kWords; i += 32)
+          if (i + 32 <= kWords || i + lane < kWords) cp16(dst + e * kBytes + (i + lane) * 16, src + i * 16, pg >= 0);
+      }
     }
     cp_commit();
   };
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) fetch(t0 + i, i);
+  for (int i = 0; i < kStages - 1; ++i) fetch(ring + i * kStage);
 
-  // The query: pieces of its row's numbers times a power of two, and their sums.
-  uint32_t qa[G][2][2][4];
-  float q_sum[G];
-  float scale;
-  {
-    float4 x[G][2][2];
-    float most = 0.f;
-    const bool mine = r < n_heads;
-    const int64_t at = b * a.q.row + (head0 + r) * a.q.head;
+  Query<G, R> q;
+  make_query(q, a, b, kvh * a.group + h0, n_heads, reinterpret_cast<float*>(room + (kStages - 1) * kStage));
+
+  // Results: numbers 64 g + 8 r + 2 x (elements 2, 3: and one more) by columns 2c, 2c + 1 of the
+  // product, which are what the rows are.
+  float o[G][4][4] = {};
+  Two o_mid[kOwn], l = {0.f, 0.f};
+  float m = -INFINITY, m_next = -INFINITY;  // the maximum, and from where on it is followed
+  float up[kOwn];                           // weights are p step up,
+  uint32_t limit[kOwn];                     // where steps are below this (their bits)
 #pragma unroll
-    for (int g = 0; g < G; ++g)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const int d = 64 * g + 32 * h + 8 * c + 4 * s;
-          float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (mine && d < a.d) y = read4_as(a.q.p, at + d, a.dtype);
-          x[g][h][s] = y;
-          most = fmaxf(most, fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w))));
-        }
-    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-    // 2^14 <= most * up < 2^15; a row that is not finite stays as it is.
-    const int e = (int)(__float_as_uint(most) >> 23);
-    const int raise = e == 255 ? 0 : min(14 - (e - 127), 126);
-    const float up = e == 0 && most == 0.f ? 1.f : __uint_as_float((uint32_t)(raise + 127) << 23);
-    scale = a.scale * kLog2e / up;
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      q_sum[g] = 0.f;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float y[8] = {x[g][h][0].x, x[g][h][0].y, x[g][h][0].z, x[g][h][0].w,
-                      x[g][h][1].x, x[g][h][1].y, x[g][h][1].z, x[g][h][1].w};
-        float low[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          y[i] *= up;
-          q_sum[g] += y[i];
-          low[i] = (y[i] - __half2float(__float2half_rn(y[i]))) * 2048.f;
-        }
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          qa[g][h][s][0] = pack_f16(y[2 * s], y[2 * s + 4]);
-          qa[g][h][s][1] = pack_f16(low[2 * s], low[2 * s + 4]);
-          qa[g][h][s][2] = pack_f16(y[2 * s + 1], y[2 * s + 5]);
-          qa[g][h][s][3] = pack_f16(low[2 * s + 1], low[2 * s + 5]);
-        }
-      }
-      q_sum[g] += __shfl_xor_sync(0xffffffffu, q_sum[g], 1);
-      q_sum[g] += __shfl_xor_sync(0xffffffffu, q_sum[g], 2);
-    }
+  for (int x = 0; x < kOwn; ++x) {
+    o_mid[x] = {0.f, 0.f};
+    limit[x] = __float_as_uint(kLeastStep4);
+    up[x] = 1.f;
   }
-
-  float o[G][4][4] = {}, o_mid[G] = {};
-  float m = -INFINITY, l = 0.f;
   int stage = 0;
-  for (int t = t0; t < t1; ++t) {
+  for (int t = t0; t < t1; t += kBoth) {
     cp_wait<kStages - 2>();
     __syncwarp();
-    const uint32_t at = ring + stage * kBytes;
-    // Scores of head r for the tokens 2c, 2c + 1, 2c + 8, 2c + 9.
-    float s[4] = {};
+    const uint32_t at = ring + stage * kStage;
+    float s[kBoth][4];
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      const uint4 k = lds128(at + g * 512 + lane * 16);
-      const uint4 sc = lds128(at + key_scales4(G) + g * 64 + c * 16);
-      const uint32_t words[2][2] = {{k.x, k.y}, {k.z, k.w}};
-      const uint32_t scales[4] = {sc.x, sc.y, sc.z, sc.w};
+    for (int e = 0; e < kBoth; ++e) scores(q, at + e * kBytes, lane, s[e]);
+    uint32_t v_scales[kBoth][kOwn][4];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float acc[4] = {};
+    for (int e = 0; e < kBoth; ++e)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t x = words[j][h], y = x >> 8;
-          mma_f16(acc, qa[g][h][0][0], qa[g][h][0][1], qa[g][h][0][2], qa[g][h][0][3], low_f16(x),
-                  high_f16(x));
-          mma_f16(acc, qa[g][h][1][0], qa[g][h][1][1], qa[g][h][1][2], qa[g][h][1][3], low_f16(y),
-                  high_f16(y));
-        }
+      for (int x = 0; x < kOwn; ++x) {
+        const int g = x * kSlots + slot;
+        uint4 sc = make_uint4(0, 0, 0, 0);
+        if (G % kSlots == 0 || g < G) sc = lds128(at + e * kBytes + value_scales4(G) + g * 64 + c * 16);
+        v_scales[e][x][0] = sc.x, v_scales[e][x][1] = sc.y, v_scales[e][x][2] = sc.z, v_scales[e][x][3] = sc.w;
+      }
+    // Tokens past the length, and blocks that are another warp's.
+    if (t + kBoth > t1 || len - t * kBlock4 < kBoth * kBlock4) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t z = scales[2 * j + i];
-          const float dot = fmaf(acc[2 + i], 0x1p-11f, acc[i]);
-          s[2 * j + i] = fmaf(step_of(z), dot, fmaf(mid_of(z), q_sum[g], s[2 * j + i]));
-        }
+      for (int e = 0; e < kBoth; ++e) {
+        const int left = t + e < t1 ? len - (t + e) * kBlock4 : 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (2 * c + (i & 1) + (i >> 1) * 8 >= left) {
+            s[e][i] = -INFINITY;
+#pragma unroll
+            for (int x = 0; x < kOwn; ++x) v_scales[e][x][i] = 0;
+          }
       }
     }
-    uint32_t v_scales[G][4];
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      const uint4 sc = lds128(at + value_scales4(G) + g * 64 + c * 16);
-      v_scales[g][0] = sc.x, v_scales[g][1] = sc.y, v_scales[g][2] = sc.z, v_scales[g][3] = sc.w;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s[i] *= scale;
-    const int left = len - t * kBlock4;  // tokens of this block that count
-    if (left < kBlock4) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (2 * c + (i & 1) + (i >> 1) * 8 >= left) {
-          s[i] = -INFINITY;
-#pragma unroll
-          for (int g = 0; g < G; ++g) v_scales[g][i] = 0;
-        }
-    }
-    float top = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+    float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
+                      fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    if (__any_sync(0xffffffffu, top > m + kLazy || (m == -INFINITY && top > m))) {
-      const float now = fmaxf(m, top);
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2)) * q.scale;
+    bool follow = top > m_next;
+    uint32_t steps[kOwn];
+#pragma unroll
+    for (int x = 0; x < kOwn; ++x) {
+      steps[x] = 0;
+#pragma unroll
+      for (int e = 0; e < kBoth; ++e)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) steps[x] = max(steps[x], v_scales[e][x][i]);
+      follow |= steps[x] >= limit[x];
+    }
+    if (__any_sync(0xffffffffu, follow)) {
+      const float now = top > m_next ? fmaxf(m, top) : m;
       const float by = m == -INFINITY ? 0.f : exp2_fast(m - now);
       m = now;
-      l *= by;
+      m_next = m == -INFINITY ? m : m + kLazy;
+      l = mul(l, {by, by});
 #pragma unroll
-      for (int g = 0; g < G; ++g) o_mid[g] *= by;
-      const float by0 = __shfl_sync(0xffffffffu, by, 8 * c), by1 = __shfl_sync(0xffffffffu, by, 8 * c + 4);
-#pragma unroll
-      for (int g = 0; g < G; ++g)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          o[g][x][0] *= by0, o[g][x][2] *= by0;
-          o[g][x][1] *= by1, o[g][x][3] *= by1;
+      for (int x = 0; x < kOwn; ++x) {
+        o_mid[x] = mul(o_mid[x], {by, by});
+        float f = by;
+        uint32_t most = max(steps[x], __shfl_xor_sync(0xffffffffu, steps[x], 1));
+        most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        // The next power of two; a step of NaN has a middle of NaN, which decides.
+        if (most >= limit[x] && most < 0x7f800000u) {
+          const uint32_t exp = (most >> 23) + 1;
+          limit[x] = exp << 23;
+          const float was = up[x];
+          up[x] = __uint_as_float((127u + 127u + kUnits - exp) << 23);
+          f *= up[x] / was;
         }
-    }
-    const float from = m == -INFINITY ? 0.f : m;
-    float p[4];
+        // Factors of this lane's columns.
+        const float f0 = __shfl_sync(0xffffffffu, f, 8 * c), f1 = __shfl_sync(0xffffffffu, f, 8 * c + 4);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      p[i] = exp2_fast(s[i] - from);
-      l += p[i];
-    }
+        for (int g = x * kSlots; g < x * kSlots + kSlots && g < G; ++g)
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      float x[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[i] = p[i] * step_of(v_scales[g][i]);
-        o_mid[g] = fmaf(p[i], mid_of(v_scales[g][i]), o_mid[g]);
-      }
-      uint32_t pb[3][2];
-#pragma unroll
-      for (int i = 0; i < (F32 ? 3 : 2); ++i) {
-        pb[i][0] = take_bf16(x[0], x[1]);
-        pb[i][1] = take_bf16(x[2], x[3]);
-      }
-      const uint4 v = lds128(at + values4(G) + g * 512 + lane * 16);
-      const uint32_t va[2] = {__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632)};
-      const uint32_t vb[2] = {__byte_perm(v.z, v.w, 0x5410), __byte_perm(v.z, v.w, 0x7632)};
-#pragma unroll
-      for (int x4 = 0; x4 < 4; ++x4) {
-        const int half = x4 / 2, sh = (x4 & 1) * 8;
-        const uint32_t a0 = low_bf16(va[half] >> sh), a1 = low_bf16(va[half] >> (sh + 4));
-        const uint32_t a2 = low_bf16(vb[half] >> sh), a3 = low_bf16(vb[half] >> (sh + 4));
-#pragma unroll
-        for (int i = 0; i < (F32 ? 3 : 2); ++i) mma_bf16(o[g][x4], a0, a1, a2, a3, pb[i][0], pb[i][1]);
+          for (int z = 0; z < 4; ++z) {
+            o[g][z][0] *= f0, o[g][z][2] *= f0;
+            o[g][z][1] *= f1, o[g][z][3] *= f1;
+          }
       }
     }
+    const float from = m == -INFINITY ? 0.f : -m;
+    float p[kBoth][4];
+#pragma unroll
+    for (int e = 0; e < kBoth; ++e)
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {
+        fma({s[e][j], s[e][j + 1]}, {q.scale, q.scale}, {from, from}).get(p[e][j], p[e][j + 1]);
+        p[e][j] = exp2_fast(p[e][j]);
+        p[e][j + 1] = exp2_fast(p[e][j + 1]);
+        l = add(l, {p[e][j], p[e][j + 1]});
+      }
+#pragma unroll
+    for (int e = 0; e < kBoth; ++e)
+#pragma unroll
+      for (int x = 0; x < kOwn; ++x) {
+        uint32_t pb[2][2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t a0 = v_scales[e][x][2 * j], a1 = v_scales[e][x][2 * j + 1];
+          const Two y = {p[e][2 * j], p[e][2 * j + 1]};
+          o_mid[x] = fma(y, {mid_of(a0), mid_of(a1)}, o_mid[x]);
+          const Two z = mul(mul(y, {step_of(a0), step_of(a1)}), {up[x], up[x]});
+          float x0, x1, y0, y1;
+          z.get(x0, x1);
+          pb[0][j] = pack_f16(x0, x1);
+          // The second piece: less what was taken (exact).
+          add(z, mul(unpack_f16(pb[0][j]), {-1.f, -1.f})).get(y0, y1);
+          pb[1][j] = pack_f16(y0, y1);
+          if (kColumns && r >= 4) pb[0][j] = pb[1][j];
+        }
+#pragma unroll
+        for (int g = x * kSlots; g < x * kSlots + kSlots && g < G; ++g) {
+          const uint4 v = lds128(at + e * kBytes + values4(G) + g * 512 + lane * 16);
+          const uint32_t va[2] = {__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632)};
+          const uint32_t vb[2] = {__byte_perm(v.z, v.w, 0x5410), __byte_perm(v.z, v.w, 0x7632)};
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            const uint32_t wa = z & 1 ? va[z / 2] >> 8 : va[z / 2], wb = z & 1 ? vb[z / 2] >> 8 : vb[z / 2];
+            const uint32_t av[4] = {low_codes(wa), high_codes(wa), low_codes(wb), high_codes(wb)};
+            mma_f16<false>(o[g][z], av, pb[0][0], pb[0][1]);
+            if (!kColumns) mma_f16<false>(o[g][z], av, pb[1][0], pb[1][1]);
+          }
+        }
+      }
     __syncwarp();
-    fetch(t + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
+    fetch(ring + (stage == 0 ? kStages - 1 : stage - 1) * kStage);
     stage = stage == kStages - 1 ? 0 : stage + 1;
   }
   cp_wait<0>();
   __syncwarp();
 
-  l += __shfl_xor_sync(0xffffffffu, l, 1);
-  l += __shfl_xor_sync(0xffffffffu, l, 2);
+  // The ring is done with.
+  Left<G>& left = *reinterpret_cast<Left<G>*>(room);
+  const auto sum_of = [](const Two& x) {
+    float y, z;
+    x.get(y, z);
+    y += z;
+    y += __shfl_xor_sync(0xffffffffu, y, 1);
+    return y + __shfl_xor_sync(0xffffffffu, y, 2);
+  };
+  const float l_sum = sum_of(l);
+  const int head = Lane<G, R>::head(r);
+  const bool mine = head < n_heads && c == 0 && (!kColumns || r < 4);
+  if (mine && slot == 0) {
+    left.sum[head] = make_float2(m, l_sum);
+    left.first[head] = first_sum(a, b, kvh * a.group + h0 + head);
+  }
+#pragma unroll
+  for (int x = 0; x < kOwn; ++x) {
+    const float y = sum_of(o_mid[x]);
+    const int g = x * kSlots + slot;
+    if (mine && g < G) left.mid[head][g] = y;
+  }
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    o_mid[g] += __shfl_xor_sync(0xffffffffu, o_mid[g], 1);
-    o_mid[g] += __shfl_xor_sync(0xffffffffu, o_mid[g], 2);
-  }
-  // This lane's results are heads 2c and 2c + 1, numbers 64 g + 8 r ...
-  float wide[2];
+    const float down = 1.f / __shfl_sync(0xffffffffu, up[g / kSlots], 4 * Lane<G, R>::kHeadRows * (g % kSlots));
 #pragma unroll
-  for (int i = 0; i < 2; ++i) wide[i] = 2 * c + i < n_heads ? first_sum(a, b, head0 + 2 * c + i) : 0.f;
-  __syncwarp();
+    for (int i = 0; i < 2; ++i) {
+      float y[8];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int h = 2 * c + i, from = 4 * h;
-    const float hm = __shfl_sync(0xffffffffu, m, from), hl = __shfl_sync(0xffffffffu, l, from);
-    float mids[G];
-#pragma unroll
-    for (int g = 0; g < G; ++g) mids[g] = __shfl_sync(0xffffffffu, o_mid[g], from);
-    if (h >= n_heads) continue;
-    Joint z{};
-    if (piece < 0) {
-      z = join_first(wide[i], hm, hl);
-      if (a.lse && r == 0) a.lse[(int64_t)b * a.heads + head0 + h] = z.lse;
-    } else if (r == 0) {
-      w.sums[(int64_t)piece * w.heads + h] = make_float2(hm, hl);
-    }
-#pragma unroll
-    for (int g = 0; g < G; ++g)
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const int d = 64 * g + 8 * r + 4 * s;
-        const float4 y = make_float4(o[g][2 * s][i] + mids[g], o[g][2 * s][2 + i] + mids[g],
-                                     o[g][2 * s + 1][i] + mids[g], o[g][2 * s + 1][2 + i] + mids[g]);
-        if (piece >= 0)
-          *reinterpret_cast<float4*>(w.results + ((int64_t)piece * w.heads + h) * (64 * G) + d) = y;
-        else if (d < a.dv)
-          put_result(a, b, head0 + h, d, y, z);
+      for (int z = 0; z < 8; ++z) {
+        y[z] = o[g][z / 2][i + 2 * (z & 1)] * down;
+        if (kColumns) y[z] += __shfl_xor_sync(0xffffffffu, y[z], 2);  // the second pieces' columns
       }
+      const int column = 2 * c + i, h = Lane<G, R>::head(column);
+      if (h < n_heads && (!kColumns || column < 4) && Lane<G, R>::slot(column) == g % kSlots) {
+#pragma unroll
+        for (int z = 0; z < 8; z += 4)
+          *reinterpret_cast<float4*>(&left.result[h][64 * g + 8 * r + z]) =
+              make_float4(y[z], y[z + 1], y[z + 2], y[z + 3]);
+      }
+    }
   }
 }
 
-template <int G, bool F32>
+// What `warps` warps left (Left, `apart` bytes apart) of one unit, joined by threads `thread` of
+// `threads`: the final result (piece < 0) or piece `piece`.
+template <int G>
+__device__ __forceinline__ void emit(const Attn4Args& a, const Work4& w, const unsigned char* room, int apart, int warps,
+                                     int b, int head0, int n_heads, int64_t piece, int thread, int threads) {
+#pragma unroll 1
+  for (int i = thread; i < n_heads * 16 * G; i += threads) {
+    const int h = i / (16 * G), d = 4 * (i - h * 16 * G);
+    float top = -INFINITY, l = 0.f;
+#pragma unroll 1
+    for (int x = 0; x < warps; ++x) top = fmaxf(top, reinterpret_cast<const Left<G>*>(room + x * apart)->sum[h].x);
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int x = 0; x < warps; ++x) {
+      const Left<G>& left = *reinterpret_cast<const Left<G>*>(room + x * apart);
+      const float2 s = left.sum[h];
+      // (A sum of NaN has any maximum, and has to arrive.)
+      const float by = s.x == top ? 1.f : s.x == -INFINITY ? (s.y == 0.f ? 0.f : s.y) : exp2_fast(s.x - top);
+      const float4 z = *reinterpret_cast<const float4*>(&left.result[h][d]);
+      const float mid = left.mid[h][d / 64];
+      l = fmaf(s.y, by, l);
+      y.x = fmaf(z.x + mid, by, y.x), y.y = fmaf(z.y + mid, by, y.y);
+      y.z = fmaf(z.z + mid, by, y.z), y.w = fmaf(z.w + mid, by, y.w);
+    }
+    if (piece >= 0) {
+      if (d == 0) w.sums[piece * w.heads + h] = make_float2(top, l);
+      *reinterpret_cast<float4*>(w.results + (piece * w.heads + h) * (64 * G) + d) = y;
+      continue;
+    }
+    const Joint z = join_first(reinterpret_cast<const Left<G>*>(room)->first[h], top, l);
+    if (d < a.dv) put_result(a, b, head0 + h, d, y, z);
+    if (a.lse && d == 0) a.lse[(int64_t)b * a.heads + head0 + h] = z.lse;
+  }
+}
+
+template <int G, Rows4 R>
 __global__ void __launch_bounds__(kThreads, Shape<G>::kCtas) attn4_kernel(Attn4Args a, Work4 w) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int64_t s_sum[kWarps];
   __shared__ int s_request[kWarps];
   __shared__ int64_t s_before[kWarps];
+  constexpr int kRoom = Shape<G>::kStages * Shape<G>::kStage;  // of a warp
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int tiles = (a.group + kHeads - 1) / kHeads, per_request = a.kv_heads * tiles;
   const int64_t units = (int64_t)a.n * per_request;
   let_next_start();
 
   // All blocks.
-  int64_t sum = 0;
-  for (int b = tid; b < a.n; b += kThreads) sum += blocks_of(len_of(a, b, blockIdx.x == 0));
+  const int first_blocks = tid < a.n ? blocks_of(len_of(a, tid, blockIdx.x == 0)) : 0;
+  int64_t sum = first_blocks;
+  for (int b = tid + kThreads; b < a.n; b += kThreads) sum += blocks_of(len_of(a, b, blockIdx.x == 0));
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (lane == 0) s_sum[warp] = sum;
@@ -502,23 +669,20 @@ __global__ void __launch_bounds__(kThreads, Shape<G>::kCtas) attn4_kernel(Attn4A
   for (int i = 0; i < kWarps; ++i) sum += s_sum[i];
   const int64_t total = sum * per_request;
   const int64_t warps = (int64_t)gridDim.x * kWarps;
-  // The first rule: pieces of at most `most` blocks; the second: even shares.
-  const bool pieces = units <= warps / 2;
-  int64_t most = (total + warps - units - 1) / (warps - units);
-  most = most < kLeast ? kLeast : most;
-  const int64_t shares = total < warps ? total : warps;
-  const int64_t id = (int64_t)blockIdx.x * kWarps + warp;
-  // Where each warp of the CTA begins, in pieces or in blocks.
-  auto begin_of = [&](int64_t i) { return pieces ? i : i < shares ? i * total / shares : total; };
+  // The first rule: pieces of a CTA; the second: even shares of the warps, `share` blocks and one more in
+  // the first `more` warps.
+  const bool pieces = total / kPiece + units <= gridDim.x;
+  const int64_t share = total > UINT32_MAX ? total / warps : (uint32_t)total / (uint32_t)warps;
+  const int64_t more = total - share * warps;
+  const int64_t first_warp = (int64_t)blockIdx.x * kWarps;
+  // Where a warp begins, in pieces or in blocks.
+  const auto begin_of = [&](int64_t i) { return pieces ? i / kWarps : i * share + (i < more ? i : more); };
   int64_t carry = 0;
-  const int64_t last = begin_of((int64_t)blockIdx.x * kWarps + kWarps - 1);
+  const int64_t last = begin_of(first_warp + kWarps - 1);
   for (int c0 = 0; c0 < a.n; c0 += kThreads) {
     const int b = c0 + tid;
-    int64_t mine = 0;
-    if (b < a.n) {
-      const int t = blocks_of(len_of(a, b, false));
-      mine = (int64_t)per_request * (pieces ? (t + most - 1) / most : t);
-    }
+    const int t = c0 == 0 ? first_blocks : b < a.n ? blocks_of(len_of(a, b, false)) : 0;
+    const int64_t mine = (int64_t)per_request * (pieces ? (t + kPiece - 1) / kPiece : t);
     int64_t scan = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -535,9 +699,9 @@ __global__ void __launch_bounds__(kThreads, Shape<G>::kCtas) attn4_kernel(Attn4A
       carry += s_sum[i];
     }
     before += scan - mine;
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < kWarps; ++i) {
-      const int64_t x = begin_of((int64_t)blockIdx.x * kWarps + i);
+      const int64_t x = begin_of(first_warp + i);
       if (x >= before && x < before + mine) {
         s_request[i] = b;
         s_before[i] = before;
@@ -547,38 +711,74 @@ __global__ void __launch_bounds__(kThreads, Shape<G>::kCtas) attn4_kernel(Attn4A
   }
   __syncthreads();
   int b = s_request[warp];
-  if (b < 0) return;
-  const int64_t before = s_before[warp];
-  const uint32_t ring = tc::sptr(smem) + warp * Shape<G>::kStages * block4_bytes(G);
+  unsigned char* room = smem + warp * kRoom;
 
-  if (pieces) {
-    const int t = blocks_of(len_of(a, b, false)), np = (int)((t + most - 1) / most);
-    const int in = (int)(id - before), u = in / np, i = in - u * np;
-    const int kvh = u / tiles, h0 = (u - kvh * tiles) * kHeads;
-    if (w.units && i == 0 && lane == 0)
-      w.units[(int64_t)b * per_request + u] = {(int32_t)id, np};
-    run_range<G, F32>(a, w, ring, b, kvh, h0, (int)((int64_t)t * i / np),
-                      (int)((int64_t)t * (i + 1) / np), np == 1 ? -1 : (int)id);
+  // The second rule's warps of one unit join here too: what the CTA has is inside a unit.
+  bool together = pieces;
+  int t = b < 0 ? 1 : blocks_of(len_of(a, b, false));
+  int64_t x = begin_of(first_warp + warp), end = begin_of(first_warp + warp + 1);
+  int64_t at = x - s_before[warp];  // in request b
+  if (!pieces && s_request[0] >= 0) {
+    const int t0 = blocks_of(len_of(a, s_request[0], false));
+    const int64_t at0 = begin_of(first_warp) - s_before[0];
+    together = share > 0 && begin_of(first_warp + kWarps) - begin_of(first_warp) <= t0 - at0 % t0;
+  }
+  if (together) {
+    b = s_request[0];
+    if (b < 0) return;
+    t = blocks_of(len_of(a, b, false));
+    x = begin_of(first_warp);
+    at = x - s_before[0];
+    end = pieces ? x + 1 : begin_of(first_warp + kWarps);
+  } else if (b < 0) {
     return;
   }
-  int64_t x = begin_of(id);
-  const int64_t end = begin_of(id + 1);
-  int t = blocks_of(len_of(a, b, false));
-  int64_t at = x - before;  // in request b
+  const int np = pieces ? (t + kPiece - 1) / kPiece : 1;
   while (x < end) {
-    const int u = (int)(at / t), lo = (int)(at - (int64_t)u * t);
-    const int hi = (int)(end - x < t - lo ? lo + (end - x) : t);
+    // Unit u's blocks [lo, hi), this warp's of them [mine, mine_end).
+    const int per = pieces ? np : t;
+    const int u = (int)(at / per), i = (int)(at - (int64_t)u * per);
+    int lo = i, hi = (int)(end - x < t - lo ? lo + (end - x) : t);
+    if (pieces) {
+      lo = (int)((int64_t)t * i / np);
+      hi = (int)((int64_t)t * (i + 1) / np);
+    }
+    int mine = lo, mine_end = hi;
+    if (together) {
+      const int pairs = (hi - lo + 1) / 2;
+      mine = lo + 2 * (pairs * warp / kWarps);
+      mine_end = min(hi, lo + 2 * (pairs * (warp + 1) / kWarps));
+    }
     const int kvh = u / tiles, h0 = (u - kvh * tiles) * kHeads;
     const bool whole = lo == 0 && hi == t;
-    // The unit's piece in its first warp is that one's 2 id + 1, in later ones 2 id.
-    if (w.units && lo == 0 && lane == 0) {
-      const int64_t stop = x + t;  // the last warp that has some of it
-      const int64_t last_id = (stop * shares + total - 1) / total - 1;
-      w.units[(int64_t)b * per_request + u] = {(int32_t)(2 * id + 1),
-                                               whole ? 1 : -(int32_t)(last_id - id + 1)};
+    const int64_t id = together ? first_warp : first_warp + warp;
+    // Where the unit's pieces are: x .. of the first rule; of the second 2 id + 1 in the first
+    // warp that has some of it, 2 id in later ones.
+    const int64_t piece = whole ? -1 : pieces ? x : lo == 0 ? 2 * id + 1 : 2 * id;
+    if (w.units && lo == 0 && lane == 0 && (!together || warp == 0)) {
+      int32_t count = np;
+      if (!pieces && !whole) {
+        const int64_t end_at = x + t, fat = more * (share + 1);  // the warp that has the unit's last block
+        const int64_t last_id = end_at <= fat ? (end_at - 1) / (share + 1) : more + (end_at - 1 - fat) / share;
+        count = -(int32_t)(last_id - id + 1);
+      }
+      w.units[(int64_t)b * per_request + u] = {(int32_t)(pieces ? x : 2 * id + 1), count};
     }
-    run_range<G, F32>(a, w, ring, b, kvh, h0, lo, hi,
-                      whole ? -1 : (int)(lo == 0 ? 2 * id + 1 : 2 * id));
+    run_range<G, R>(a, room, b, kvh, h0, mine, mine_end);
+    const int n_heads = min(kHeads, a.group - h0);
+    if (together) __syncthreads();
+    else __syncwarp();
+    emit<G>(a, w, together ? smem : room, kRoom, together ? kWarps : 1, b, kvh * a.group + h0, n_heads, piece,
+            together ? tid : lane, together ? kThreads : 32);
+    if (together) {
+      // The other warps' places among the unit's pieces hold nothing.
+      if (!pieces && tid < (kWarps - 1) * n_heads) {
+        const int64_t other = first_warp + 1 + tid / n_heads;
+        w.sums[2 * other * w.heads + tid % n_heads] = make_float2(-INFINITY, 0.f);
+      }
+      return;
+    }
+    __syncwarp();
     x += hi - lo;
     at += hi - lo;
     if (at == (int64_t)t * per_request && x < end) {
@@ -628,7 +828,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join4_kernel(Attn4Args a, Wor
     for (int i = warp; i < n; i += kJoinWarps) {
       const int64_t p = piece(i);
       const float2 s = w.sums[p];
-      const float by = s.x == -INFINITY ? 0.f : exp2_fast(s.x - top);
+      if (s.x == -INFINITY && s.y == 0.f) continue;
+      const float by = s.x == -INFINITY ? s.y : exp2_fast(s.x - top);  // (of a sum of NaN: NaN)
       l += s.y * by;
 #pragma unroll
       for (int e = 0; e < kEach; ++e)
@@ -675,12 +876,11 @@ Plan4 plan(int64_t n, int kv_heads, int group, int64_t keys) {
   const int64_t blocks = keys > kBlock4 ? (keys + kBlock4 - 1) / kBlock4 : 1;
   // CTAs that run at once; fewer only where the pieces of the longest requests need fewer.
   const int64_t most = kSms * Shape<G>::kCtas;
-  const int64_t cut = (blocks + kLeast - 1) / kLeast;
-  int64_t ctas = cut > most * kWarps ? most : (p.units * (cut + 2) * 2 + kWarps - 1) / kWarps;
-  ctas = ctas < 1 ? 1 : ctas < most ? ctas : most;
-  p.ctas = (unsigned)ctas;
-  const bool never = cut == 1 && p.units <= ctas * kWarps / 2;
-  p.pieces = never ? 0 : 2 * ctas * kWarps;
+  const int64_t cut = (blocks + kPiece - 1) / kPiece;
+  const int64_t ctas = cut > most ? most : p.units * (cut + 1);
+  p.ctas = (unsigned)(ctas < most ? ctas : most);
+  const bool never = cut == 1 && p.units * 2 <= p.ctas;
+  p.pieces = never ? 0 : 2 * (int64_t)p.ctas * kWarps;
   return p;
 }
 Plan4 plan_of(int G, int64_t n, int kv_heads, int group, int64_t keys) {
@@ -694,7 +894,7 @@ Plan4 plan_of(int G, int64_t n, int kv_heads, int group, int64_t keys) {
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-template <int G, bool F32>
+template <int G, Rows4 R>
 cudaError_t launch(const Attn4Args& a, void* workspace, cudaStream_t stream) {
   const Plan4 p = plan<G>(a.n, a.kv_heads, a.group, (int64_t)a.width * a.page_blocks * kBlock4);
   Work4 w{};
@@ -707,23 +907,20 @@ cudaError_t launch(const Attn4Args& a, void* workspace, cudaStream_t stream) {
     at += up256(p.pieces * p.heads * sizeof(float2));
     w.results = reinterpret_cast<float*>(at);
   }
-  cudaError_t e = ensure_smem<attn4_kernel<G, F32>>(Shape<G>::kSmem);
+  cudaError_t e = ensure_smem<attn4_kernel<G, R>>(Shape<G>::kSmem);
   if (e != cudaSuccess) return e;
-  attn4_kernel<G, F32><<<p.ctas, kThreads, Shape<G>::kSmem, stream>>>(a, w);
+  attn4_kernel<G, R><<<p.ctas, kThreads, Shape<G>::kSmem, stream>>>(a, w);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.pieces == 0) return e;
   const int64_t rows = p.units * p.heads, ctas = rows < kSms * 8 ? rows : kSms * 8;
   return launch_dependent(join4_kernel<G>, dim3((unsigned)ctas), kJoinWarps * 32, 0, stream, a, w);
 }
 
-template <bool F32>
+template <int G>
 cudaError_t launch_of(const Attn4Args& a, void* workspace, cudaStream_t stream) {
-  switch (groups4(a.d, a.dv)) {
-    case 1: return launch<1, F32>(a, workspace, stream);
-    case 2: return launch<2, F32>(a, workspace, stream);
-    case 3: return launch<3, F32>(a, workspace, stream);
-    default: return launch<4, F32>(a, workspace, stream);
-  }
+  if (a.group > 4) return launch<G, kEight>(a, workspace, stream);
+  if (a.group > 2 || G == 1) return launch<G, kFour>(a, workspace, stream);
+  return launch<G, G == 1 ? kFour : kTwo>(a, workspace, stream);
 }
 
 }  // namespace
@@ -738,8 +935,12 @@ size_t attn4_workspace(const nys_attn_config& c, int64_t n, int64_t keys) {
 }
 
 cudaError_t launch_attn4(const Attn4Args& a, void* workspace, cudaStream_t stream) {
-  return a.dtype == NYS_F32 ? launch_of<true>(a, workspace, stream)
-                            : launch_of<false>(a, workspace, stream);
+  switch (groups4(a.d, a.dv)) {
+    case 1: return launch_of<1>(a, workspace, stream);
+    case 2: return launch_of<2>(a, workspace, stream);
+    case 3: return launch_of<3>(a, workspace, stream);
+    default: return launch_of<4>(a, workspace, stream);
+  }
 }
 
 }  // namespace nys

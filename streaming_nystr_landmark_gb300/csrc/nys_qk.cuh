@@ -135,52 +135,6 @@ Form form_of(const void* p, int64_t row, int64_t head, int dim, int lanes) {
   return all % 16 == 0 && dim == 8 * lanes ? kWhole : all % sizeof(Four<T>) == 0 ? kWords : kAny;
 }
 
-// Two f32 operations an instruction, each rounded as its own.
-struct Two {
-  uint64_t w;
-  __device__ __forceinline__ Two() {}
-  __device__ __forceinline__ Two(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(w) : "f"(a), "f"(b)); }
-  __device__ __forceinline__ void get(float& a, float& b) const {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(w));
-  }
-};
-__device__ __forceinline__ Two add(Two a, Two b) {
-  Two c;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(c.w) : "l"(a.w), "l"(b.w));
-  return c;
-}
-__device__ __forceinline__ Two mul(Two a, Two b) {
-  Two c;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(c.w) : "l"(a.w), "l"(b.w));
-  return c;
-}
-__device__ __forceinline__ Two fma(Two a, Two b, Two c) {
-  Two d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.w) : "l"(a.w), "l"(b.w), "l"(c.w));
-  return d;
-}
-// The least and largest of numbers; NaN if one is NaN.
-__device__ __forceinline__ float least(float a, float b) {
-  float c;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(c) : "f"(a), "f"(b));
-  return c;
-}
-__device__ __forceinline__ float largest(float a, float b) {
-  float c;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(c) : "f"(a), "f"(b));
-  return c;
-}
-__device__ __forceinline__ float least(float a, float b, float c) {
-  float d;
-  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-__device__ __forceinline__ float largest(float a, float b, float c) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
 // x / by, rounded correctly, for inv = 1 / by rounded (Markstein), of a quotient that is
 // no subnormal number.
 __device__ __forceinline__ float quotient(float x, float by, float inv) {
