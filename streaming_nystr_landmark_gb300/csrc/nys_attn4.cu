@@ -50,16 +50,14 @@ constexpr uint32_t kUnits = 13;           // steps times up_g stay below 2^kUnit
 
 constexpr int kBoth = 2;        // blocks that are multiplied together: 32 tokens
 
-#ifndef NC
-#define NC 3
-#define NS 3
-#endif
 template <int G>
 struct Shape {
-  static constexpr int kStages = G <= 3 ? NS : 2;
-  static constexpr int kCtas = G <= 2 ? NC : 2;  // of an SM
+  static constexpr int kStages = G <= 3 ? 3 : 2;
+  static constexpr int kCtas = G <= 2 ? 3 : 2;  // of an SM
   static constexpr int kStage = kBoth * block4_bytes(G);
-  static constexpr int kSmem = kWarps * kStages * kStage;  // (two stages hold what a warp leaves)
+  static constexpr int kSmem = kWarps * kStages * kStage;
+  // The query's rows go through one stage, and what a warp leaves (Left) takes the ring's place.
+  static_assert(kStage >= kHeads * 64 * G * 4 && kStages >= 2, "a stage holds 8 rows of 64 G floats");
 };
 
 // Pieces of cut units: in the workspace, first the units' records, then each piece's
@@ -369,6 +367,9 @@ struct Left {
   float2 sum[kHeads];
   float first[kHeads];  // the log-sum of what is joined in
 };
+template <int G>
+constexpr bool left_fits = sizeof(Left<G>) <= Shape<G>::kStages * Shape<G>::kStage;
+static_assert(left_fits<1> && left_fits<2> && left_fits<3> && left_fits<4>, "Left has a warp's ring");
 
 // Blocks [t0, t1) of unit (b, kvh, heads h0 ..) -> `left`, which is the ring's place.
 template <int G, Rows4 R>
@@ -383,36 +384,28 @@ __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* roo
   const int len = len_of(a, b, false);
   const int n_heads = min(kHeads, a.group - h0);
 
-  // The next block's page is looked up one block ahead.
+  // The next block's page is looked up one block ahead; blocks that there are none of are zeros.  (A
+  // request without keys has no table to look into.)
+  const int end = min(t1, (len + kBlock4 - 1) / kBlock4);
   int next = t0, in_page = t0 % a.page_blocks;
-  const int32_t* page_at = a.table + (int64_t)b * a.width + t0 / a.page_blocks;
-  const auto look_up = [&]() {
-    if (next >= t1 || next * kBlock4 >= len) return -1;
-    const int32_t pg = *page_at;
-    if (pg < 0 || pg >= a.n_pages) {
-      if (lane == 0) attn_report(a.status, NYS_ATTN_BAD_PAGE);
-      return -1;
-    }
-    return pg;
-  };
-  int ahead = look_up();
+  const int32_t* page_at = next < end ? a.table + (int64_t)b * a.width + t0 / a.page_blocks : a.lens;
+  int ahead = *page_at;
   const auto fetch = [&](uint32_t dst) {
 #pragma unroll
     for (int e = 0; e < kBoth; ++e) {
-      if (next < t1) {
-        const int pg = ahead;
-        const uint8_t* src = a.blocks + lane * 16;
-        if (pg >= 0) src += (((int64_t)pg * a.kv_heads + kvh) * a.page_blocks + in_page) * kBytes;
-        ++next;
-        if (++in_page == a.page_blocks) {
-          in_page = 0;
-          ++page_at;
-        }
-        ahead = look_up();
-#pragma unroll
-        for (int i = 0; i < kWords; i += 32)
-          if (i + 32 <= kWords || i + lane < kWords) cp16(dst + e * kBytes + (i + lane) * 16, src + i * 16, pg >= 0);
+      const bool wanted = next < end, there = wanted && (uint32_t)ahead < (uint32_t)a.n_pages;
+      if (wanted && !there && lane == 0) attn_report(a.status, NYS_ATTN_BAD_PAGE);
+      const int64_t block = there ? ((int64_t)ahead * a.kv_heads + kvh) * a.page_blocks + in_page : 0;
+      const uint8_t* src = a.blocks + block * kBytes + lane * 16;
+      ++next;
+      if (++in_page == a.page_blocks) {
+        in_page = 0;
+        if (next < end) ++page_at;
       }
+      ahead = *page_at;
+#pragma unroll
+      for (int i = 0; i < kWords; i += 32)
+        if (i + 32 <= kWords || i + lane < kWords) cp16(dst + e * kBytes + (i + lane) * 16, src + i * 16, there);
     }
     cp_commit();
   };
@@ -467,10 +460,11 @@ __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* roo
           }
       }
     }
-    float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
-                      fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2)) * q.scale;
+    // Whether a lane's scores pass what is followed; the row's maximum is looked for only then.
+    float top = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < kBoth; ++e) top = fmaxf(top, fmaxf(fmaxf(s[e][0], s[e][1]), fmaxf(s[e][2], s[e][3])));
+    top *= q.scale;
     bool follow = top > m_next;
     uint32_t steps[kOwn];
 #pragma unroll
@@ -483,6 +477,8 @@ __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* roo
       follow |= steps[x] >= limit[x];
     }
     if (__any_sync(0xffffffffu, follow)) {
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const float now = top > m_next ? fmaxf(m, top) : m;
       const float by = m == -INFINITY ? 0.f : exp2_fast(m - now);
       m = now;
@@ -539,7 +535,7 @@ __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* roo
           z.get(x0, x1);
           pb[0][j] = pack_f16(x0, x1);
           // The second piece: less what was taken (exact).
-          add(z, mul(unpack_f16(pb[0][j]), {-1.f, -1.f})).get(y0, y1);
+          fma(unpack_f16(pb[0][j]), {-1.f, -1.f}, z).get(y0, y1);
           pb[1][j] = pack_f16(y0, y1);
           if (kColumns && r >= 4) pb[0][j] = pb[1][j];
         }
@@ -788,44 +784,49 @@ __global__ void __launch_bounds__(kThreads, Shape<G>::kCtas) attn4_kernel(Attn4A
   }
 }
 
-// Joins the pieces of a cut unit: a CTA a unit, its warps over the pieces, a lane's numbers
-// 4 lane .. of each head.
+// Joins the pieces of cut units: a CTA's warps over one head's pieces, or (Alone: many heads, of few
+// pieces each) a warp each.  A lane has numbers 4 lane .. of the head.
 constexpr int kJoinWarps = 8;
 
-template <int G>
+template <int G, bool Alone>
 __global__ void __launch_bounds__(kJoinWarps * 32) join4_kernel(Attn4Args a, Work4 w) {
-  __shared__ float s_o[kJoinWarps][64 * G];
+  __shared__ float s_o[Alone ? 1 : kJoinWarps][64 * G];
   __shared__ float2 s_sum[kJoinWarps];
-  wait_for_previous();
+  constexpr int kEach = (G + 1) / 2;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int tiles = (a.group + kHeads - 1) / kHeads, per_request = a.kv_heads * tiles;
-  const int64_t units = (int64_t)a.n * per_request;
-  for (int64_t x = blockIdx.x; x < units * w.heads; x += gridDim.x) {
-    const int64_t u = x / w.heads;
+  const int64_t rows = (int64_t)a.n * per_request * w.heads;
+  const int64_t stride = Alone ? (int64_t)gridDim.x * kJoinWarps : gridDim.x;
+  wait_for_previous();
+  for (int64_t x = Alone ? (int64_t)blockIdx.x * kJoinWarps + warp : blockIdx.x; x < rows; x += stride) {
+    const int64_t u = rows <= INT32_MAX ? (uint32_t)x / (uint32_t)w.heads : x / w.heads;
     const int h = (int)(x - u * w.heads);
     const Cut4 unit = w.units[u];
-    const int b = (int)(u / per_request), in = (int)(u - (int64_t)b * per_request);
+    if (unit.pieces == 1) continue;
+    const int b = (int)(rows <= INT32_MAX ? (uint32_t)u / (uint32_t)per_request : u / per_request);
+    const int in = (int)(u - (int64_t)b * per_request);
     const int kvh = in / tiles, h0 = (in - kvh * tiles) * kHeads;
-    if (unit.pieces == 1 || h0 + h >= a.group) continue;
+    if (h0 + h >= a.group) continue;
     const int n = unit.pieces < 0 ? -unit.pieces : unit.pieces;
-    auto piece = [&](int i) {
+    const auto piece = [&](int i) {
       return (int64_t)(unit.pieces > 0 || i == 0 ? unit.first + i : unit.first + 2 * i - 1) * w.heads + h;
     };
     float top = -INFINITY;
-    for (int i = tid; i < n; i += kJoinWarps * 32) top = fmaxf(top, w.sums[piece(i)].x);
+    for (int i = Alone ? lane : tid; i < n; i += Alone ? 32 : kJoinWarps * 32) top = fmaxf(top, w.sums[piece(i)].x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    __syncthreads();
-    if (lane == 0) s_sum[warp].x = top;
-    __syncthreads();
+    if (!Alone) {
+      __syncthreads();
+      if (lane == 0) s_sum[warp].x = top;
+      __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kJoinWarps; ++i) top = fmaxf(top, s_sum[i].x);
-    __syncthreads();
-    constexpr int kEach = (G + 1) / 2;
+      for (int i = 0; i < kJoinWarps; ++i) top = fmaxf(top, s_sum[i].x);
+    }
+    const int head = kvh * a.group + h0 + h;
     float4 o[kEach] = {};
     float l = 0.f;
 #pragma unroll 4
-    for (int i = warp; i < n; i += kJoinWarps) {
+    for (int i = Alone ? 0 : warp; i < n; i += Alone ? 1 : kJoinWarps) {
       const int64_t p = piece(i);
       const float2 s = w.sums[p];
       if (s.x == -INFINITY && s.y == 0.f) continue;
@@ -839,19 +840,28 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join4_kernel(Attn4Args a, Wor
           o[e].z = fmaf(y.z, by, o[e].z), o[e].w = fmaf(y.w, by, o[e].w);
         }
     }
+    const float wide = first_sum(a, b, head);  // before any log-sum is written
+    if (Alone) {
+      __syncwarp();
+      const Joint z = join_first(wide, top, l);
+      if (a.lse && lane == 0) a.lse[(int64_t)b * a.heads + head] = z.lse;
+#pragma unroll
+      for (int e = 0; e < kEach; ++e)
+        if (128 * e + 4 * lane < a.dv) put_result(a, b, head, 128 * e + 4 * lane, o[e], z);
+      continue;
+    }
     if (lane == 0) s_sum[warp].y = l;
-    const int head = kvh * a.group + h0 + h;
-    const float wide = first_sum(a, b, head);
 #pragma unroll
     for (int e = 0; e < kEach; ++e)
-      if (128 * e + 4 * lane < 64 * G) *reinterpret_cast<float4*>(&s_o[warp][128 * e + 4 * lane]) = o[e];
+      if (128 * e + 4 * lane < 64 * G)
+        *reinterpret_cast<float4*>(&s_o[Alone ? 0 : warp][128 * e + 4 * lane]) = o[e];
     __syncthreads();
     if (tid * 4 < 64 * G) {
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
       l = 0.f;
 #pragma unroll
       for (int i = 0; i < kJoinWarps; ++i) {
-        const float4 z = *reinterpret_cast<const float4*>(&s_o[i][4 * tid]);
+        const float4 z = *reinterpret_cast<const float4*>(&s_o[Alone ? 0 : i][4 * tid]);
         y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
         l += s_sum[i].y;
       }
@@ -912,8 +922,12 @@ cudaError_t launch(const Attn4Args& a, void* workspace, cudaStream_t stream) {
   attn4_kernel<G, R><<<p.ctas, kThreads, Shape<G>::kSmem, stream>>>(a, w);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.pieces == 0) return e;
-  const int64_t rows = p.units * p.heads, ctas = rows < kSms * 8 ? rows : kSms * 8;
-  return launch_dependent(join4_kernel<G>, dim3((unsigned)ctas), kJoinWarps * 32, 0, stream, a, w);
+  const int64_t rows = p.units * p.heads;
+  if (rows <= kSms * 4)
+    return launch_dependent(join4_kernel<G, false>, dim3((unsigned)rows), kJoinWarps * 32, 0, stream, a, w);
+  const int64_t ctas = (rows + kJoinWarps - 1) / kJoinWarps;
+  return launch_dependent(join4_kernel<G, true>, dim3((unsigned)(ctas < kSms * 8 ? ctas : kSms * 8)), kJoinWarps * 32, 0,
+                          stream, a, w);
 }
 
 template <int G>
