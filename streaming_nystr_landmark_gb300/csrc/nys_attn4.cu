@@ -12,7 +12,7 @@
 // and one subtraction.  Queries go in as two f16 pieces (22 bits, after a power of two that fits
 // the row) in rows r and r + 8, which the lane that needs their sum holds both; weights p_j step_j as two
 // f16 pieces too, after a power of two that follows the largest step so far (so that a weight is held to
-// 2^-38 of the largest).  The product's 8 rows and columns hold up to 8 heads; where there are at most 4, or
+// 2^-35 of the largest).  The product's 8 rows and columns hold up to 8 heads; where there are at most 4, or
 // 2, the free ones hold the weights' second pieces, and the other half of the groups, so that a lane scales half
 // of them.  Sums, maxima and the middles' part are f32.
 //
@@ -37,27 +37,34 @@
 namespace nys {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
 constexpr int kHeads = 8;       // heads of a unit
-constexpr int kPiece = 32;      // blocks of a CTA's piece, at most
+constexpr int kPiece = 8;       // blocks of a warp's part of a CTA's piece, at most
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kLazy = 2.f;    // weights stay below 2^kLazy of the followed maximum's
+constexpr float kLazy = 5.f;    // weights stay below 2^kLazy of the followed maximum's
 constexpr int kSms = 152;
 constexpr float kLeastStep4 = 0x1p-100f;  // but for 0
-constexpr uint32_t kUnits = 13;           // steps times up_g stay below 2^kUnits, weights below 2^15
+constexpr uint32_t kUnits = 10;           // steps times up stay below 2^kUnits, weights below 2^15
 
 constexpr int kBoth = 2;        // blocks that are multiplied together: 32 tokens
 
 template <int G>
 struct Shape {
   static constexpr int kStages = G <= 3 ? 3 : 2;
-  static constexpr int kCtas = G <= 2 ? 3 : 2;  // of an SM
   static constexpr int kStage = kBoth * block4_bytes(G);
-  static constexpr int kSmem = kWarps * kStages * kStage;
+  static constexpr int kRoom = kStages * kStage;  // of a warp
   // The query's rows go through one stage, and what a warp leaves (Left) takes the ring's place.
   static_assert(kStage >= kHeads * 64 * G * 4 && kStages >= 2, "a stage holds 8 rows of 64 G floats");
+};
+// CTAs: of 4 warps, several on an SM; or, where there are fewer units than SMs, one of as many
+// warps as an SM's registers take (4 requests of 3 to 345 tokens: 9.6 us with 4 warps, WIDE_US with 12).
+template <int G, bool Large>
+struct Cta {
+  static constexpr int kWarps = !Large ? 4 : G <= 2 ? 12 : 8;
+  static constexpr int kOfSm = Large ? 1 : G <= 2 ? 3 : 2;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kSmem = kWarps * Shape<G>::kRoom;
+  static constexpr int kPieces = kWarps * kPiece;
 };
 
 // Pieces of cut units: in the workspace, first the units' records, then each piece's
@@ -72,10 +79,12 @@ struct Work4 {
   int32_t heads;  // of a piece
 };
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool fill) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(fill ? 16 : 0)
-               : "memory");
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool fill, bool here) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %3, 0;\n\t@p cp.async.cg.shared.global [%0], [%1], 16, %2;\n\t}" ::"r"(
+          dst),
+      "l"(src), "r"(fill ? 16 : 0), "r"((uint32_t)here)
+      : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -247,18 +256,65 @@ struct Query {
   float sum[Lane<G, R>::kOwn];  // of the own groups' numbers
   float scale;                  // of the scores, to base 2
 };
+// A unit's query rows on their way to shared memory: 4 numbers a lane and chunk, as they are or, where rows
+// are not aligned to them, as f32.
+template <int G, Rows4 R>
+struct RawQuery {
+  static constexpr int kChunks = Lane<G, R>::kHeadRows * G / 2 + (Lane<G, R>::kHeadRows * G % 2);
+  uint4 w[kChunks];
+  bool f32;
+};
+template <int G, Rows4 R>
+__device__ __forceinline__ void load_query(RawQuery<G, R>& q, const Attn4Args& a, int b, int head0, int n_heads) {
+  const int lane = threadIdx.x & 31, size = a.dtype == NYS_F32 ? 4 : 2;
+  const char* row = static_cast<const char*>(a.q.p) + (b * a.q.row + head0 * a.q.head) * size;
+  const bool word = ((reinterpret_cast<uintptr_t>(a.q.p) | (uintptr_t)(a.q.row * size) | (uintptr_t)(a.q.head * size)) &
+                     (uintptr_t)(4 * size - 1)) == 0;
+  q.f32 = a.dtype == NYS_F32 || !word;
+#pragma unroll
+  for (int k = 0; k < RawQuery<G, R>::kChunks; ++k) {
+    const int i = lane + 32 * k, head = i / (16 * G), d = 4 * (i - head * 16 * G);
+    q.w[k] = make_uint4(0, 0, 0, 0);
+    if (head < n_heads && d < a.d) {
+      const char* p = row + (head * a.q.head + d) * size;
+      if (word && size == 4) {
+        q.w[k] = *reinterpret_cast<const uint4*>(p);
+      } else if (word) {
+        const uint2 y = *reinterpret_cast<const uint2*>(p);
+        q.w[k].x = y.x, q.w[k].y = y.y;
+      }
+    }
+  }
+  if (word) return;
+#pragma unroll
+  for (int k = 0; k < RawQuery<G, R>::kChunks; ++k) {
+    const int i = lane + 32 * k, head = i / (16 * G), d = 4 * (i - head * 16 * G);
+    if (head < n_heads && d < a.d) {
+      const char* p = row + (head * a.q.head + d) * size;
+      q.w[k] = make_uint4(__float_as_uint(read_as(p, 0, a.dtype)), __float_as_uint(read_as(p, 1, a.dtype)),
+                          __float_as_uint(read_as(p, 2, a.dtype)), __float_as_uint(read_as(p, 3, a.dtype)));
+    }
+  }
+}
 // By way of `room` in shared memory (8 heads of 64 G numbers).
 template <int G, Rows4 R>
-__device__ __forceinline__ void make_query(Query<G, R>& q, const Attn4Args& a, int b, int head0, int n_heads,
+__device__ __forceinline__ void make_query(Query<G, R>& q, const RawQuery<G, R>& raw, const Attn4Args& a, int n_heads,
                                            float* room) {
   const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
   const int h = Lane<G, R>::head(r), slot = Lane<G, R>::slot(r);
-#pragma unroll 1
-  for (int i = lane; i < n_heads * 16 * G; i += 32) {
-    const int head = i / (16 * G), d = 4 * (i - head * 16 * G);
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (d < a.d) y = read4_as(a.q.p, b * a.q.row + (head0 + head) * a.q.head + d, a.dtype);
-    *reinterpret_cast<float4*>(room + 4 * i) = y;
+#pragma unroll
+  for (int k = 0; k < RawQuery<G, R>::kChunks; ++k) {
+    uint4 y = raw.w[k];
+    if (!raw.f32) {
+      if (a.dtype == NYS_BF16) {
+        y = make_uint4(y.x << 16, y.x & 0xffff0000u, y.y << 16, y.y & 0xffff0000u);
+      } else {
+        const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&y.x));
+        const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&y.y));
+        y = make_uint4(__float_as_uint(lo.x), __float_as_uint(lo.y), __float_as_uint(hi.x), __float_as_uint(hi.y));
+      }
+    }
+    if (lane + 32 * k < Lane<G, R>::kHeadRows * 16 * G) *reinterpret_cast<uint4*>(room + 4 * (lane + 32 * k)) = y;
   }
   __syncwarp();
   float x[G][2][8];
@@ -368,7 +424,7 @@ struct Left {
   float first[kHeads];  // the log-sum of what is joined in
 };
 template <int G>
-constexpr bool left_fits = sizeof(Left<G>) <= Shape<G>::kStages * Shape<G>::kStage;
+constexpr bool left_fits = sizeof(Left<G>) <= Shape<G>::kRoom;
 static_assert(left_fits<1> && left_fits<2> && left_fits<3> && left_fits<4>, "Left has a warp's ring");
 
 // Blocks [t0, t1) of unit (b, kvh, heads h0 ..) -> `left`, which is the ring's place.
@@ -384,28 +440,32 @@ __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* roo
   const int len = len_of(a, b, false);
   const int n_heads = min(kHeads, a.group - h0);
 
+  RawQuery<G, R> raw;
+  load_query(raw, a, b, kvh * a.group + h0, n_heads);
+
   // The next block's page is looked up one block ahead; blocks that there are none of are zeros.  (A
   // request without keys has no table to look into.)
   const int end = min(t1, (len + kBlock4 - 1) / kBlock4);
   int next = t0, in_page = t0 % a.page_blocks;
   const int32_t* page_at = next < end ? a.table + (int64_t)b * a.width + t0 / a.page_blocks : a.lens;
   int ahead = *page_at;
+  bool bad = false;
+  const int64_t head_bytes = (int64_t)a.page_blocks * kBytes, page_bytes = a.kv_heads * head_bytes;
+  const uint8_t* head_at = a.blocks + kvh * head_bytes + lane * 16;
   const auto fetch = [&](uint32_t dst) {
 #pragma unroll
     for (int e = 0; e < kBoth; ++e) {
       const bool wanted = next < end, there = wanted && (uint32_t)ahead < (uint32_t)a.n_pages;
-      if (wanted && !there && lane == 0) attn_report(a.status, NYS_ATTN_BAD_PAGE);
-      const int64_t block = there ? ((int64_t)ahead * a.kv_heads + kvh) * a.page_blocks + in_page : 0;
-      const uint8_t* src = a.blocks + block * kBytes + lane * 16;
+      bad |= wanted && !there;
+      const uint8_t* src = head_at + (there ? ahead * page_bytes + in_page * kBytes : 0);
       ++next;
-      if (++in_page == a.page_blocks) {
-        in_page = 0;
-        if (next < end) ++page_at;
-      }
+      const bool turn = ++in_page == a.page_blocks;
+      in_page = turn ? 0 : in_page;
+      page_at += turn && next < end ? 1 : 0;
       ahead = *page_at;
 #pragma unroll
       for (int i = 0; i < kWords; i += 32)
-        if (i + 32 <= kWords || i + lane < kWords) cp16(dst + e * kBytes + (i + lane) * 16, src + i * 16, there);
+        cp16(dst + e * kBytes + (i + lane) * 16, src + i * 16, there, i + 32 <= kWords || i + lane < kWords);
     }
     cp_commit();
   };
@@ -413,7 +473,7 @@ __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* roo
   for (int i = 0; i < kStages - 1; ++i) fetch(ring + i * kStage);
 
   Query<G, R> q;
-  make_query(q, a, b, kvh * a.group + h0, n_heads, reinterpret_cast<float*>(room + (kStages - 1) * kStage));
+  make_query(q, raw, a, n_heads, reinterpret_cast<float*>(room + (kStages - 1) * kStage));
 
   // Results: numbers 64 g + 8 r + 2 x (elements 2, 3: and one more) by columns 2c, 2c + 1 of the
   // product, which are what the rows are.
@@ -559,6 +619,7 @@ __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* roo
   }
   cp_wait<0>();
   __syncwarp();
+  if (bad && lane == 0) attn_report(a.status, NYS_ATTN_BAD_PAGE);
 
   // The ring is done with.
   Left<G>& left = *reinterpret_cast<Left<G>*>(room);
@@ -613,15 +674,17 @@ __device__ __forceinline__ void emit(const Attn4Args& a, const Work4& w, const u
   for (int i = thread; i < n_heads * 16 * G; i += threads) {
     const int h = i / (16 * G), d = 4 * (i - h * 16 * G);
     float top = -INFINITY, l = 0.f;
-#pragma unroll 1
-    for (int x = 0; x < warps; ++x) top = fmaxf(top, reinterpret_cast<const Left<G>*>(room + x * apart)->sum[h].x);
+    const float2* sums = &reinterpret_cast<const Left<G>*>(room)->sum[h];
+#pragma unroll 4
+    for (int x = 0; x < warps; ++x)
+      top = fmaxf(top, reinterpret_cast<const float2*>(reinterpret_cast<const char*>(sums) + x * apart)->x);
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
+#pragma unroll 4
     for (int x = 0; x < warps; ++x) {
       const Left<G>& left = *reinterpret_cast<const Left<G>*>(room + x * apart);
       const float2 s = left.sum[h];
       // (A sum of NaN has any maximum, and has to arrive.)
-      const float by = s.x == top ? 1.f : s.x == -INFINITY ? (s.y == 0.f ? 0.f : s.y) : exp2_fast(s.x - top);
+      const float by = s.x == top ? 1.f : s.x == -INFINITY ? s.y : exp2_fast(s.x - top);
       const float4 z = *reinterpret_cast<const float4*>(&left.result[h][d]);
       const float mid = left.mid[h][d / 64];
       l = fmaf(s.y, by, l);
@@ -639,30 +702,30 @@ __device__ __forceinline__ void emit(const Attn4Args& a, const Work4& w, const u
   }
 }
 
-template <int G, Rows4 R>
-__global__ void __launch_bounds__(kThreads, Shape<G>::kCtas) attn4_kernel(Attn4Args a, Work4 w) {
+template <int G, Rows4 R, bool Large>
+__global__ void __launch_bounds__(Cta<G, Large>::kThreads, Cta<G, Large>::kOfSm)
+attn4_kernel(Attn4Args a, Work4 w) {
+  constexpr int kWarps = Cta<G, Large>::kWarps, kThreads = Cta<G, Large>::kThreads;
+  constexpr int kPiece = Cta<G, Large>::kPieces;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ int64_t s_sum[kWarps];
-  __shared__ int s_request[kWarps];
-  __shared__ int64_t s_before[kWarps];
-  constexpr int kRoom = Shape<G>::kStages * Shape<G>::kStage;  // of a warp
+  constexpr int kRoom = Shape<G>::kRoom;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int tiles = (a.group + kHeads - 1) / kHeads, per_request = a.kv_heads * tiles;
   const int64_t units = (int64_t)a.n * per_request;
   let_next_start();
 
-  // All blocks.
-  const int first_blocks = tid < a.n ? blocks_of(len_of(a, tid, blockIdx.x == 0)) : 0;
-  int64_t sum = first_blocks;
-  for (int b = tid + kThreads; b < a.n; b += kThreads) sum += blocks_of(len_of(a, b, blockIdx.x == 0));
+  // All blocks, which every warp counts for itself (no step of the CTA's: 128 lengths a round), and where
+  // the prefix sum of `weight` passes x: the request, and the sum before it.
+  const auto blocks_at = [&](int b, bool report) { return b < a.n ? blocks_of(len_of(a, b, report)) : 0; };
+  int first[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) first[i] = blocks_at(4 * lane + i, blockIdx.x == 0 && warp == 0);
+  int64_t sum = (int64_t)first[0] + first[1] + first[2] + first[3];
+  for (int c0 = 128; c0 < a.n; c0 += 128)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum += blocks_at(c0 + 4 * lane + i, blockIdx.x == 0 && warp == 0);
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) s_sum[warp] = sum;
-  if (tid < kWarps) s_request[tid] = -1;
-  __syncthreads();
-  sum = 0;
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i) sum += s_sum[i];
   const int64_t total = sum * per_request;
   const int64_t warps = (int64_t)gridDim.x * kWarps;
   // The first rule: pieces of a CTA; the second: even shares of the warps, `share` blocks and one more in
@@ -672,68 +735,63 @@ __global__ void __launch_bounds__(kThreads, Shape<G>::kCtas) attn4_kernel(Attn4A
   const int64_t more = total - share * warps;
   const int64_t first_warp = (int64_t)blockIdx.x * kWarps;
   // Where a warp begins, in pieces or in blocks.
-  const auto begin_of = [&](int64_t i) { return pieces ? i / kWarps : i * share + (i < more ? i : more); };
-  int64_t carry = 0;
-  const int64_t last = begin_of(first_warp + kWarps - 1);
-  for (int c0 = 0; c0 < a.n; c0 += kThreads) {
-    const int b = c0 + tid;
-    const int t = c0 == 0 ? first_blocks : b < a.n ? blocks_of(len_of(a, b, false)) : 0;
-    const int64_t mine = (int64_t)per_request * (pieces ? (t + kPiece - 1) / kPiece : t);
-    int64_t scan = mine;
+  const auto begin_of = [&](int64_t i) { return i * share + (i < more ? i : more); };
+  const auto find = [&](int64_t x, int64_t& before) {
+    int64_t carry = 0;
+    for (int c0 = 0; c0 < a.n; c0 += 128) {
+      int64_t mine[4], all = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, scan, o);
-      if (lane >= o) scan += y;
-    }
-    __syncthreads();
-    if (lane == 31) s_sum[warp] = scan;
-    __syncthreads();
-    int64_t before = carry;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      if (i < warp) before += s_sum[i];
-      carry += s_sum[i];
-    }
-    before += scan - mine;
-#pragma unroll 1
-    for (int i = 0; i < kWarps; ++i) {
-      const int64_t x = begin_of(first_warp + i);
-      if (x >= before && x < before + mine) {
-        s_request[i] = b;
-        s_before[i] = before;
+      for (int i = 0; i < 4; ++i) {
+        const int t = c0 == 0 ? first[i] : blocks_at(c0 + 4 * lane + i, false);
+        mine[i] = all;
+        all += (int64_t)per_request * (pieces ? (t + kPiece - 1) / kPiece : t);
       }
+      int64_t scan = all;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, scan, o);
+        if (lane >= o) scan += y;
+      }
+      const int64_t from = carry + scan - all;
+      const uint32_t here = __ballot_sync(0xffffffffu, x >= from && x < from + all);
+      if (here) {
+        int in = 0;
+        int64_t to = from;
+#pragma unroll
+        for (int i = 1; i < 4; ++i)
+          if (x >= from + mine[i] && 4 * lane + i + c0 < a.n) in = i, to = from + mine[i];
+        const int who = __ffs(here) - 1;
+        before = __shfl_sync(0xffffffffu, to, who);
+        return c0 + 4 * who + __shfl_sync(0xffffffffu, in, who);
+      }
+      carry += __shfl_sync(0xffffffffu, scan, 31);
     }
-    if (carry > last) break;
-  }
-  __syncthreads();
-  int b = s_request[warp];
-  unsigned char* room = smem + warp * kRoom;
+    return -1;
+  };
+  // 64-bit numbers that are small, mostly.
+  const auto div = [](int64_t x, int y) { return (int)(x <= UINT32_MAX ? (uint32_t)x / (uint32_t)y : x / y); };
 
-  // The second rule's warps of one unit join here too: what the CTA has is inside a unit.
-  bool together = pieces;
-  int t = b < 0 ? 1 : blocks_of(len_of(a, b, false));
-  int64_t x = begin_of(first_warp + warp), end = begin_of(first_warp + warp + 1);
-  int64_t at = x - s_before[warp];  // in request b
-  if (!pieces && s_request[0] >= 0) {
-    const int t0 = blocks_of(len_of(a, s_request[0], false));
-    const int64_t at0 = begin_of(first_warp) - s_before[0];
-    together = share > 0 && begin_of(first_warp + kWarps) - begin_of(first_warp) <= t0 - at0 % t0;
-  }
-  if (together) {
-    b = s_request[0];
-    if (b < 0) return;
-    t = blocks_of(len_of(a, b, false));
-    x = begin_of(first_warp);
-    at = x - s_before[0];
-    end = pieces ? x + 1 : begin_of(first_warp + kWarps);
-  } else if (b < 0) {
-    return;
+  unsigned char* room = smem + warp * kRoom;
+  int64_t x = pieces ? blockIdx.x : begin_of(first_warp), end = pieces ? x + 1 : begin_of(first_warp + kWarps), before = 0;
+  if (x >= end) return;
+  int b = find(x, before);
+  if (b < 0) return;  // (the CTA's all, as what is left of a piece's CTA)
+  int t = blocks_at(b, false);
+  int64_t at = x - before;  // in request b
+  // The second rule's warps of one unit join too: what the CTA has is inside a unit.
+  const bool together = pieces || (share > 0 && end - x <= t - (at - (int64_t)div(at, t) * t));
+  if (!together) {
+    x = begin_of(first_warp + warp), end = begin_of(first_warp + warp + 1);
+    if (x >= end) return;
+    b = find(x, before);
+    t = blocks_at(b, false);
+    at = x - before;
   }
   const int np = pieces ? (t + kPiece - 1) / kPiece : 1;
   while (x < end) {
     // Unit u's blocks [lo, hi), this warp's of them [mine, mine_end).
     const int per = pieces ? np : t;
-    const int u = (int)(at / per), i = (int)(at - (int64_t)u * per);
+    const int u = div(at, per), i = (int)(at - (int64_t)u * per);
     int lo = i, hi = (int)(end - x < t - lo ? lo + (end - x) : t);
     if (pieces) {
       lo = (int)((int64_t)t * i / np);
@@ -823,23 +881,47 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join4_kernel(Attn4Args a, Wor
       for (int i = 0; i < kJoinWarps; ++i) top = fmaxf(top, s_sum[i].x);
     }
     const int head = kvh * a.group + h0 + h;
+    // This warp's pieces [lo, hi): their weights a lane each, and then those that there are (a CTA's
+    // warps that joined left one of four) four at a time.
     float4 o[kEach] = {};
     float l = 0.f;
-#pragma unroll 4
-    for (int i = Alone ? 0 : warp; i < n; i += Alone ? 1 : kJoinWarps) {
-      const int64_t p = piece(i);
-      const float2 s = w.sums[p];
-      if (s.x == -INFINITY && s.y == 0.f) continue;
-      const float by = s.x == -INFINITY ? s.y : exp2_fast(s.x - top);  // (of a sum of NaN: NaN)
-      l += s.y * by;
+    const int lo = Alone ? 0 : (int)((int64_t)n * warp / kJoinWarps);
+    const int hi = Alone ? n : (int)((int64_t)n * (warp + 1) / kJoinWarps);
+    for (int base = lo; base < hi; base += 32) {
+      float by = 0.f;
+      if (base + lane < hi) {
+        const float2 s = w.sums[piece(base + lane)];
+        by = s.x == -INFINITY ? s.y : exp2_fast(s.x - top);  // (of a sum of NaN: NaN)
+        l += s.y * by;
+      }
+      uint32_t left = __ballot_sync(0xffffffffu, by != 0.f);
+      while (left) {
+        float4 y[4][kEach];
+        float f[4];
 #pragma unroll
-      for (int e = 0; e < kEach; ++e)
-        if (128 * e + 4 * lane < 64 * G) {
-          const float4 y = *reinterpret_cast<const float4*>(w.results + p * (64 * G) + 128 * e + 4 * lane);
-          o[e].x = fmaf(y.x, by, o[e].x), o[e].y = fmaf(y.y, by, o[e].y);
-          o[e].z = fmaf(y.z, by, o[e].z), o[e].w = fmaf(y.w, by, o[e].w);
+        for (int k = 0; k < 4; ++k) {
+          const int i = left ? __ffs(left) - 1 : -1;
+          left &= left - 1;
+          f[k] = __shfl_sync(0xffffffffu, by, i < 0 ? 0 : i);
+#pragma unroll
+          for (int e = 0; e < kEach; ++e) {
+            y[k][e] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i >= 0 && 128 * e + 4 * lane < 64 * G)
+              y[k][e] = *reinterpret_cast<const float4*>(w.results + piece(base + i) * (64 * G) + 128 * e + 4 * lane);
+          }
+          if (i < 0) f[k] = 0.f;
         }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int e = 0; e < kEach; ++e) {
+            o[e].x = fmaf(y[k][e].x, f[k], o[e].x), o[e].y = fmaf(y[k][e].y, f[k], o[e].y);
+            o[e].z = fmaf(y[k][e].z, f[k], o[e].z), o[e].w = fmaf(y[k][e].w, f[k], o[e].w);
+          }
+      }
     }
+#pragma unroll
+    for (int i = 16; i; i >>= 1) l += __shfl_xor_sync(0xffffffffu, l, i);
     const float wide = first_sum(a, b, head);  // before any log-sum is written
     if (Alone) {
       __syncwarp();
@@ -876,21 +958,30 @@ struct Plan4 {
   unsigned ctas;
   int64_t units, pieces;  // pieces: 0 where no unit can be cut
   int heads;
+  bool large;
 };
+template <int G, bool Large>
+void plan_ctas(Plan4& p, int64_t blocks) {
+  using C = Cta<G, Large>;
+  // CTAs that run at once; fewer only where the pieces of the longest requests need fewer.
+  const int64_t most = kSms * C::kOfSm;
+  const int64_t cut = (blocks + C::kPieces - 1) / C::kPieces;
+  const int64_t ctas = cut > most ? most : p.units * (cut + 1);
+  p.ctas = (unsigned)(ctas < most ? ctas : most);
+  // (blocks / kPieces <= 1 piece a unit and one more for each: the first rule, and no cut.)
+  const bool never = cut == 1 && p.units * 2 <= p.ctas;
+  p.pieces = never ? 0 : 2 * (int64_t)p.ctas * C::kWarps;
+}
 template <int G>
 Plan4 plan(int64_t n, int kv_heads, int group, int64_t keys) {
-  Plan4 p;
+  Plan4 p{};
   const int tiles = (group + kHeads - 1) / kHeads;
   p.units = n * kv_heads * tiles;
   p.heads = group < kHeads ? group : kHeads;
   const int64_t blocks = keys > kBlock4 ? (keys + kBlock4 - 1) / kBlock4 : 1;
-  // CTAs that run at once; fewer only where the pieces of the longest requests need fewer.
-  const int64_t most = kSms * Shape<G>::kCtas;
-  const int64_t cut = (blocks + kPiece - 1) / kPiece;
-  const int64_t ctas = cut > most ? most : p.units * (cut + 1);
-  p.ctas = (unsigned)(ctas < most ? ctas : most);
-  const bool never = cut == 1 && p.units * 2 <= p.ctas;
-  p.pieces = never ? 0 : 2 * (int64_t)p.ctas * kWarps;
+  p.large = p.units * 2 <= kSms && blocks <= Cta<G, true>::kPieces;
+  if (p.large) plan_ctas<G, true>(p, blocks);
+  else plan_ctas<G, false>(p, blocks);
   return p;
 }
 Plan4 plan_of(int G, int64_t n, int kv_heads, int group, int64_t keys) {
@@ -904,6 +995,14 @@ Plan4 plan_of(int G, int64_t n, int kv_heads, int group, int64_t keys) {
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+template <int G, Rows4 R, bool Large>
+cudaError_t launch_main(const Attn4Args& a, const Work4& w, unsigned ctas, cudaStream_t stream) {
+  using C = Cta<G, Large>;
+  const cudaError_t e = ensure_smem<attn4_kernel<G, R, Large>>(C::kSmem);
+  if (e != cudaSuccess) return e;
+  attn4_kernel<G, R, Large><<<ctas, C::kThreads, C::kSmem, stream>>>(a, w);
+  return cudaGetLastError();
+}
 template <int G, Rows4 R>
 cudaError_t launch(const Attn4Args& a, void* workspace, cudaStream_t stream) {
   const Plan4 p = plan<G>(a.n, a.kv_heads, a.group, (int64_t)a.width * a.page_blocks * kBlock4);
@@ -917,10 +1016,8 @@ cudaError_t launch(const Attn4Args& a, void* workspace, cudaStream_t stream) {
     at += up256(p.pieces * p.heads * sizeof(float2));
     w.results = reinterpret_cast<float*>(at);
   }
-  cudaError_t e = ensure_smem<attn4_kernel<G, R>>(Shape<G>::kSmem);
-  if (e != cudaSuccess) return e;
-  attn4_kernel<G, R><<<p.ctas, kThreads, Shape<G>::kSmem, stream>>>(a, w);
-  e = cudaGetLastError();
+  const cudaError_t e = p.large ? launch_main<G, R, true>(a, w, p.ctas, stream)
+                                : launch_main<G, R, false>(a, w, p.ctas, stream);
   if (e != cudaSuccess || p.pieces == 0) return e;
   const int64_t rows = p.units * p.heads;
   if (rows <= kSms * 4)
