@@ -164,19 +164,16 @@ __device__ __forceinline__ uint32_t quantize(const float (&y)[8], int n, uint32_
   const float span = __fmul_rn(__fsub_rn(hi, lo), 8.f);
   float part = quotient(span, 15.f, 1.f / 15.f);
   if (span < 0x1p-90f) part = __fdiv_rn(span, 15.f);
-  const float mid = __bfloat162float(__float2bfloat16_rn(__fadd_rn(lo, part)));
-  const float up = __fsub_rn(hi, mid);
-  float seventh = quotient(up, 7.f, 1.f / 7.f);
-  if (span < 0x1p-90f) seventh = __fdiv_rn(up, 7.f);
-  float step = largest(seventh, __fmul_rn(__fsub_rn(mid, lo), 0.125f));
+  const float sum = __fadd_rn(lo, part);
+  const __nv_bfloat162 middle = __floats2bfloat162_rn(sum, sum);
+  const uint32_t mid_bits = *reinterpret_cast<const uint32_t*>(&middle) & 0xffff0000u;
+  const float mid = __uint_as_float(mid_bits);
+  // (Quotients below 2^-102 make no step, whatever their last bits; above, Markstein's holds.)
+  float step = largest(quotient(__fsub_rn(hi, mid), 7.f, 1.f / 7.f), __fmul_rn(__fsub_rn(mid, lo), 0.125f));
   step = __uint_as_float((__float_as_uint(step) + 0xffffu) & 0xffff0000u);
-  if (!(fabsf(mid) < INFINITY) || !(step < INFINITY)) {
-    scale = 0x7fc07fc0u;
-    return 0x88888888u;
-  }
-  if (step < kLeastStep) step = 0.f;
-  scale = __float_as_uint(step) | __float_as_uint(mid) >> 16;
-  if (step == 0.f) return 0x88888888u;
+  const bool odd = !(fabsf(mid) < INFINITY) || !(step < INFINITY), none = step < kLeastStep;
+  scale = odd ? 0x7fc07fc0u : (none ? 0u : __float_as_uint(step)) | mid_bits >> 16;
+  if (odd || none) return 0x88888888u;
   const float inv = __frcp_rn(step);
   // t is in -8 .. 7 but for its rounding: t + 1.5 * 2^23 + 8 rounds it to a whole number, ties to
   // even, and has the code in its last bits; the bits above them add up to a constant.
@@ -253,7 +250,8 @@ __device__ __forceinline__ void run_rows(const QkArgs& a, const Token& t, int fi
 
   // y_i = (x_i A_i + x_pair B_i) * inv.
   float fa[8], fb[8];
-  float* mine = stage + sub * 9 * L;  // this row's numbers, x at x + x / 8 (kOdd)
+  float* mine = stage + sub * (9 * L + 1);  // this row's numbers, x at x + x / 8, and a 0 (kOdd)
+  int pair[8];  // where the pairs' other numbers are there
   const float* weight = K == kQueries ? a.q_weight : a.k_weight;
   const bool turned[2] = {S == kSides ? c.pair : c.at[0] < 2 * half, S == kSides ? c.pair : c.at[1] < 2 * half};
   if (K != kValues) {
@@ -296,13 +294,16 @@ __device__ __forceinline__ void run_rows(const QkArgs& a, const Token& t, int fi
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < 8; ++i) mine[9 * l + i] = fa[i];
+      if (l == 0) mine[9 * L] = 0.f;
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int x = 8 * l + i;
+        pair[i] = x < 2 * half ? 9 * l + pair_at(i, half, x < half) : 9 * L;
+        asm volatile("" : "+r"(pair[i]));  // (is kept, not made again for every row)
         if (x < 2 * half) {
           const float2 z = turns[x < half ? x : x - half];
-          const float wp = mine[9 * l + pair_at(i, half, x < half)];
+          const float wp = mine[pair[i]];
           fa[i] *= z.x;
           fb[i] = x < half ? -(wp * z.y) : wp * z.y;
         }
@@ -311,6 +312,11 @@ __device__ __forceinline__ void run_rows(const QkArgs& a, const Token& t, int fi
   }
   const float inv_d = 1.f / (float)a.d;
   T* dst = to.p && K != kValues ? static_cast<T*>(to.p) + t.at * to.row + (first + sub) * to.head : nullptr;
+  uint32_t* block = t.block + (int64_t)(first + sub) * a.page_blocks * (block4_bytes(a.groups) / 4);
+  const int block_step = kPer * a.page_blocks * (block4_bytes(a.groups) / 4);
+  const int code_at = K == kValues ? values4(a.groups) / 4 + value_word4(l / 8, t.in, l & 7) : key_word4(l / 8, t.in, l & 7);
+  const int scale_at =
+      (K == kValues ? value_scales4(a.groups) : key_scales4(a.groups)) / 4 + l / 8 * 16 + place4(t.in);
   T* page = nullptr;
   if (!Q4 && K != kQueries && t.slot >= 0)
     page = static_cast<T*>(K == kValues ? a.pool_v : a.pool_k) + (t.slot * a.kv_heads + first + sub) * dim;
@@ -351,8 +357,7 @@ __device__ __forceinline__ void run_rows(const QkArgs& a, const Token& t, int fi
             for (int i = 0; i < 8; ++i) mine[9 * l + i] = y[i];
             __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              p[i] = 8 * l + i < 2 * half ? mine[9 * l + pair_at(i, half, 8 * l + i < half)] : 0.f;
+            for (int i = 0; i < 8; ++i) p[i] = mine[pair[i]];
           }
           // (Beyond 2 half there is no pair: what lies in its place may be infinite.)
 #pragma unroll
@@ -398,14 +403,11 @@ __device__ __forceinline__ void run_rows(const QkArgs& a, const Token& t, int fi
           }
           uint32_t scale;
           const uint32_t codes = quantize<F == kWhole>(y, n, scale);
-          const int g = l / 8, x = l & 7;
-          if (row && g < a.groups) {
-            uint32_t* at = t.block + (int64_t)h * a.page_blocks * (block4_bytes(a.groups) / 4);
-            at[K == kValues ? values4(a.groups) / 4 + value_word4(g, t.in, x) : key_word4(g, t.in, x)] = codes;
-            if (x == 0)
-              at[(K == kValues ? value_scales4(a.groups) : key_scales4(a.groups)) / 4 + g * 16 + place4(t.in)] =
-                  scale;
+          if (row && l / 8 < a.groups) {
+            block[code_at] = codes;
+            if ((l & 7) == 0) block[scale_at] = scale;
           }
+          block += block_step;
         }
       }
       load(raw[b], h + kAhead * kPer);
@@ -426,10 +428,10 @@ __device__ __forceinline__ int64_t block_of(int64_t slot, int kv_heads, int page
 
 // A warp takes part `w % parts` of token w / parts's steps of 32 / L rows.
 template <typename T, int L, bool Q4, Turn R, Form F>
-__global__ void __launch_bounds__(kThreads, R == kOdd ? 3 : 4) qk_kernel(QkArgs a, int parts) {
+__global__ void __launch_bounds__(kThreads, 4) qk_kernel(QkArgs a, int parts) {
   constexpr int kPer = 32 / L;
   __shared__ __align__(16) float2 s_turn[kWarps][kMaxHalf];
-  __shared__ __align__(16) float s_stage[kWarps][288];
+  __shared__ __align__(16) float s_stage[kWarps][292];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t w = (int64_t)blockIdx.x * kWarps + warp;
   Token t;
@@ -513,58 +515,68 @@ cudaError_t launch_of(const QkArgs& a, cudaStream_t stream) {
 }
 
 // Rows of a 4-bit cache as the values they stand for; a slot outside it gives zeros.  Warps
-// and lanes as above: a lane takes a code word.
+// and lanes as above: a lane takes a code word of keys and one of values, four heads at a time, all their loads
+// before the first is used (scattered words of 4 bytes: a token's lie 16 or 64 bytes apart).
 template <typename T, int L, Form F>
-__device__ __forceinline__ void read_rows(const Read4Args& a, const Token& t, bool values, int first, int end) {
-  constexpr int kPer = 32 / L;
+__global__ void __launch_bounds__(kThreads) read4_kernel(Read4Args a, int parts) {
+  constexpr int kPer = 32 / L, kHeads = 4;
   const int lane = threadIdx.x & 31, l = lane & (L - 1), sub = lane / L;
-  const Rows& to = values ? a.v : a.k;
-  const int n = (values ? a.dv : a.d) - 8 * l;
-  if (n <= 0) return;
-  T* dst = static_cast<T*>(to.p) + t.at * to.row + 8 * l;
-  const int g = l / 8, x = l & 7;
-  const int code_at = values ? values4(a.groups) / 4 + value_word4(g, t.in, x) : key_word4(g, t.in, x);
-  const int scale_at = (values ? value_scales4(a.groups) : key_scales4(a.groups)) / 4 + g * 16 + place4(t.in);
+  const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int64_t at = parts == 1 ? w : w / parts;
+  if (at >= a.tokens) return;
+  const int part = (int)(w - at * parts), steps = (a.kv_heads + kPer - 1) / kPer;
+  const int first = steps * part / parts * kPer, end = min(a.kv_heads, steps * (part + 1) / parts * kPer);
+  const int64_t slot = a.slots[at];
+  const bool there = slot >= 0 && slot < a.n_slots;
+  const uint32_t* block = reinterpret_cast<const uint32_t*>(
+      a.blocks + (there ? block_of(slot, a.kv_heads, a.page_blocks) * block4_bytes(a.groups) : 0));
+  const int in = (int)(slot & 15), g = l / 8, x = l & 7;
   const int64_t stride = (int64_t)a.page_blocks * (block4_bytes(a.groups) / 4);
-#pragma unroll 4
-  for (int h = first + sub; h < end; h += kPer) {
-    uint32_t codes = 0, scale = 0;
-    if (t.block) {
-      codes = t.block[h * stride + code_at];
-      scale = t.block[h * stride + scale_at];
-    }
-    const float step = __uint_as_float(scale & 0xffff0000u), mid = __uint_as_float(scale << 16);
-    float y[8];
+  const int n[2] = {a.d - 8 * l, a.dv - 8 * l};
+  const int code_at[2] = {key_word4(g, in, x), values4(a.groups) / 4 + value_word4(g, in, x)};
+  const int scale_at[2] = {key_scales4(a.groups) / 4 + g * 16 + place4(in),
+                           value_scales4(a.groups) / 4 + g * 16 + place4(in)};
+  T* dst[2] = {static_cast<T*>(a.k.p) + at * a.k.row + 8 * l, static_cast<T*>(a.v.p) + at * a.v.row + 8 * l};
+#pragma unroll 1
+  for (int base = first; base < end; base += kHeads * kPer) {
+    uint32_t codes[kHeads][2], scale[kHeads][2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)  // the product is exact: 8 + 4 bits
-      y[i] = mid + step * (float)((int)(codes >> (4 * i) & 15) - 8);
-    const Four<T> z[2] = {narrow(y, T{}), narrow(y + 4, T{})};
-    put8<T, F, true>(z, dst + h * to.head, 0, 4, true, n > 4);
+    for (int i = 0; i < kHeads; ++i)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int h = base + i * kPer + sub;
+        codes[i][k] = scale[i][k] = 0;
+        if (there && h < end && n[k] > 0) {
+          codes[i][k] = block[h * stride + code_at[k]];
+          scale[i][k] = block[h * stride + scale_at[k]];
+        }
+      }
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int h = base + i * kPer + sub;
+        if (h - sub >= end) continue;
+        const float step = __uint_as_float(scale[i][k] & 0xffff0000u), mid = __uint_as_float(scale[i][k] << 16);
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          // 2^23 + code, less 2^23 + 8; the product is exact: 8 + 4 bits.
+          const uint32_t c = e == 0 ? codes[i][k] : codes[i][k] >> (4 * e);
+          const Two z = add({__uint_as_float((c & 15u) | 0x4b000000u), __uint_as_float((c >> 4 & 15u) | 0x4b000000u)},
+                            {-8388616.f, -8388616.f});
+          fma({step, step}, z, {mid, mid}).get(y[e], y[e + 1]);
+        }
+        const Four<T> z[2] = {narrow(y, T{}), narrow(y + 4, T{})};
+        if (h < end && n[k] > 0)
+          put8<T, F, true>(z, dst[k] + h * (k ? a.v.head : a.k.head), 0, 4, true, n[k] > 4);
+      }
   }
 }
 
 template <typename T, int L, Form F>
-__global__ void __launch_bounds__(kThreads) read4_kernel(Read4Args a, int parts) {
-  constexpr int kPer = 32 / L;
-  const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  Token t;
-  t.at = parts == 1 ? w : w / parts;
-  if (t.at >= a.tokens) return;
-  const int part = (int)(w - t.at * parts), sk = (a.kv_heads + kPer - 1) / kPer;
-  const int s0 = (int)((int64_t)2 * sk * part / parts), s1 = (int)((int64_t)2 * sk * (part + 1) / parts);
-  t.slot = a.slots[t.at];
-  t.block = nullptr;
-  t.in = (int)(t.slot & 15);
-  if (t.slot >= 0 && t.slot < a.n_slots)
-    t.block = const_cast<uint32_t*>(reinterpret_cast<const uint32_t*>(
-        a.blocks + block_of(t.slot, a.kv_heads, a.page_blocks) * block4_bytes(a.groups)));
-  if (s0 < sk) read_rows<T, L, F>(a, t, false, s0 * kPer, min(a.kv_heads, s1 * kPer));
-  if (s1 > sk) read_rows<T, L, F>(a, t, true, max(s0 - sk, 0) * kPer, min(a.kv_heads, (s1 - sk) * kPer));
-}
-
-template <typename T, int L, Form F>
 cudaError_t launch_read(const Read4Args& a, cudaStream_t stream) {
-  const int64_t parts = parts_of(a.tokens, 2 * ((a.kv_heads + 32 / L - 1) / (32 / L)));
+  const int64_t parts = parts_of(a.tokens, (a.kv_heads + 32 / L - 1) / (32 / L));
   const int64_t ctas = (a.tokens * parts + kWarps - 1) / kWarps;
   read4_kernel<T, L, F><<<(unsigned)ctas, kThreads, 0, stream>>>(a, (int)parts);
   return cudaGetLastError();

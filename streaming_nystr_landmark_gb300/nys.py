@@ -858,6 +858,7 @@ class QKPrepare(_OnDevice):
                     raise ValueError(f"{name}: shape {tuple(w.shape)} != ({d},)")
                 w = w.detach().to(device=self.device, dtype=torch.float32, copy=True).contiguous()
             self._weights.append(w)
+        self._int32 = torch.int32
         self.cfg = NysAttnConfig(heads, kv_heads, d, d, _dtype_code(self.dtype), 0.0)
         at = [None if w is None else w.data_ptr() for w in self._weights]
         rot = 0 if rotation is None else rotation.rot
@@ -865,27 +866,24 @@ class QKPrepare(_OnDevice):
                                   int(rot > 0 and rotation.interleaved), 0)
         nys_qk_rows(self.cfg, self._prep, 0, NysRows(), None, None, NysRows(), None)
 
-    def _turned(self, positions, n, shift):
-        """The arguments of the C call for this shift, and the positions' address."""
-        prep = self._prep
-        if shift:
-            if not -2 ** 31 <= shift < 2 ** 31:
-                raise ValueError(f"shift {shift}: past 32 bits")
-            prep = NysQkPrepare(prep.q_weight, prep.k_weight, prep.eps, prep.turns, prep.rot,
-                                prep.interleaved, shift)
-        if positions is None:
-            if prep.rot:
-                raise ValueError("positions: needed for a rotation")
-            return prep, None
-        return prep, _ints(positions, self.torch.int32, (n,), "positions", self.device.index)
+    def _shifted(self, shift):
+        """The arguments of the C calls for this shift."""
+        if not -2 ** 31 <= shift < 2 ** 31:
+            raise ValueError(f"shift {shift}: past 32 bits")
+        p = self._prep
+        return NysQkPrepare(p.q_weight, p.k_weight, p.eps, p.turns, p.rot, p.interleaved, shift)
 
-    def _in_out(self, x, out, heads, where):
-        index = self.device.index
-        if out is not None and out.shape[0] != x.shape[0]:
-            raise ValueError(f"{where}_out: {out.shape[0]} rows, {where} has {x.shape[0]}")
-        return (_rows(x, self.dtype, heads, self.d, where, index),
-                None if out is None else _rows(out, self.dtype, heads, self.d, where + "_out",
-                                               index))
+    def _at(self, positions, n):
+        if positions is None:
+            if self._prep.rot:
+                raise ValueError("positions: needed for a rotation")
+            return None
+        return _ints(positions, self._int32, (n,), "positions", self.device.index)
+
+    def _out(self, out, n, heads, where):
+        if out.shape[0] != n:
+            raise ValueError(f"{where}: {out.shape[0]} rows, need {n}")
+        return _rows(out, self.dtype, heads, self.d, where, self.device.index)
 
     def rows(self, q, k, positions, q_out=None, k_out=None, shift=0):
         """q [tokens][heads][d] and k [tokens][kv_heads][d] (either may be None), normalised
@@ -894,16 +892,31 @@ class QKPrepare(_OnDevice):
         if self._elsewhere():
             with self.torch.cuda.device(self.device.index):
                 return self.rows(q, k, positions, q_out, k_out, shift)
-        if q is None and k is None or q is None and q_out is not None or k is None and k_out is not None:
+        index, dtype = self.device.index, self.dtype
+        qs = qo = ks = ko = None
+        if q is not None:
+            n = q.shape[0]
+            qs = qo = _rows(q, dtype, self.heads, self.d, "q", index)
+            if q_out is None:
+                q_out = q
+            else:
+                qo = self._out(q_out, n, self.heads, "q_out")
+        elif k is None or q_out is not None:
             raise ValueError("q and k: need one of them, and none for an output without it")
-        if q is not None and k is not None and q.shape[0] != k.shape[0]:
-            raise ValueError(f"k: {k.shape[0]} rows, q has {q.shape[0]}")
-        n = (k if q is None else q).shape[0]
-        q_out, k_out = q if q_out is None else q_out, k if k_out is None else k_out
-        prep, at = self._turned(positions, n, shift)
-        qs = (None, None) if q is None else self._in_out(q, q_out, self.heads, "q")
-        ks = (None, None) if k is None else self._in_out(k, k_out, self.kv_heads, "k")
-        nys_qk_rows(self.cfg, prep, n, qs[0], ks[0], at, qs[1], ks[1], self._stream())
+        if k is not None:
+            if q is None:
+                n = k.shape[0]
+            elif k.shape[0] != n:
+                raise ValueError(f"k: {k.shape[0]} rows, q has {n}")
+            ks = ko = _rows(k, dtype, self.kv_heads, self.d, "k", index)
+            if k_out is None:
+                k_out = k
+            else:
+                ko = self._out(k_out, n, self.kv_heads, "k_out")
+        elif k_out is not None:
+            raise ValueError("k_out: there is no k")
+        nys_qk_rows(self.cfg, self._shifted(shift) if shift else self._prep, n, qs, ks,
+                    self._at(positions, n), qo, ko, self._stream())
         return q_out, k_out
 
     def append(self, q, k, v, positions, slots, cache, q_out=None, k_out=None, shift=0):
@@ -915,26 +928,30 @@ class QKPrepare(_OnDevice):
         if self._elsewhere():
             with torch.cuda.device(index):
                 return self.append(q, k, v, positions, slots, cache, q_out, k_out, shift)
-        if cache.dtype != self.dtype or cache.kv_heads != self.kv_heads or cache.d != self.d:
+        dtype, kv_heads, d = self.dtype, self.kv_heads, self.d
+        if cache.dtype != dtype or cache.kv_heads != kv_heads or cache.d != d:
             raise ValueError("the cache's geometry is not this object's")
         if cache.device.index != index:
             raise ValueError(f"the cache is on {cache.device}, this object on {self.device}")
-        n = k.shape[0]
+        n, dv, cfg = k.shape[0], cache.dv, self.cfg
         if v.shape[0] != n or (q is not None and q.shape[0] != n):
             raise ValueError("q, k and v must have as many rows as each other")
-        if q is None and q_out is not None:
+        if dv != d:
+            cfg = NysAttnConfig(self.heads, kv_heads, d, dv, cfg.dtype, 0.0)
+        qs = qo = None
+        if q is not None:
+            qs = qo = _rows(q, dtype, self.heads, d, "q", index)
+            if q_out is None:
+                q_out = q
+            else:
+                qo = self._out(q_out, n, self.heads, "q_out")
+        elif q_out is not None:
             raise ValueError("q_out: there is no q")
-        q_out = q if q_out is None else q_out
-        prep, at = self._turned(positions, n, shift)
-        qs = (None, None) if q is None else self._in_out(q, q_out, self.heads, "q")
-        ks = self._in_out(k, k_out, self.kv_heads, "k")
-        cfg = self.cfg
-        if cache.dv != self.d:
-            cfg = NysAttnConfig(self.heads, self.kv_heads, self.d, cache.dv, cfg.dtype, 0.0)
         (nys_kv4_append if isinstance(cache, PagedKV4) else nys_kv_append)(
-            cfg, prep, cache._pool, n, qs[0], ks[0],
-            _rows(v, self.dtype, self.kv_heads, cache.dv, "v", index), at,
-            _ints(slots, torch.int64, (n,), "slots", index), qs[1], ks[1], self._stream())
+            cfg, self._shifted(shift) if shift else self._prep, cache._pool, n, qs,
+            _rows(k, dtype, kv_heads, d, "k", index), _rows(v, dtype, kv_heads, dv, "v", index),
+            self._at(positions, n), _ints(slots, torch.int64, (n,), "slots", index), qo,
+            None if k_out is None else self._out(k_out, n, kv_heads, "k_out"), self._stream())
         return q_out
 
 

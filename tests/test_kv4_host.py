@@ -60,7 +60,7 @@ def _read(**kw):
 
 
 def _attn(**kw):
-    a = dict(cfg=cfg(), n=2, pool=nys.NysPool4(A, 4, 16), lens=A, table=A, w=20, q=rows(), f=None, fl=None, o=rows(),
+    a = dict(cfg=cfg(), n=2, pool=nys.NysPool4(A, 4, 16), lens=A, table=A, w=400, q=rows(), f=None, fl=None, o=rows(),
              lse=None, ws=A, wb=1 << 40, st=None)
     a.update(kw)
     return nys._lib.nys_attn4(a["cfg"], a["n"], a["pool"], a["lens"], a["table"], a["w"], a["q"], a["f"], a["fl"],
@@ -132,9 +132,9 @@ def test_attention_refusals(kw, code):
 
 
 def test_workspace():
-    need = nys.nys_attn4_workspace_bytes(cfg(), 2, 320)
+    need = nys.nys_attn4_workspace_bytes(cfg(), 2, 6400)
     assert need > 0 and nys.nys_attn4_workspace_bytes(cfg(), 2, 16) == 0
-    assert nys.nys_attn4_workspace_bytes(cfg(), 0, 320) == 0
+    assert nys.nys_attn4_workspace_bytes(cfg(), 0, 6400) == 0
     assert _attn(ws=None, wb=0) == _attn(wb=need - 1) == B
     for n, k in ((-1, 1), (1, -1), (1 << 31, 1), (1, 1 << 31)):
         with pytest.raises(nys.NysError):
