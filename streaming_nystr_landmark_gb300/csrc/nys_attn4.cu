@@ -91,14 +91,7 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ uint4 lds128(uint32_t at) {
-  uint4 x;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-               : "r"(at)
-               : "memory");
-  return x;
-}
+__device__ __forceinline__ uint4 lds128(const unsigned char* at) { return *reinterpret_cast<const uint4*>(at); }
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -371,7 +364,7 @@ __device__ __forceinline__ void make_query(Query<G, R>& q, const RawQuery<G, R>&
 // Scores of this lane's head for the tokens 2c, 2c + 1, 2c + 8, 2c + 9 of a block, unscaled.  The
 // own groups' scales are `own` 64-byte steps apart from key_scales on.
 template <int G, Rows4 R>
-__device__ __forceinline__ void scores(const Query<G, R>& q, uint32_t at, int lane, float (&s)[4]) {
+__device__ __forceinline__ void scores(const Query<G, R>& q, const unsigned char* at, int lane, float (&s)[4]) {
   constexpr int kSlots = Lane<G, R>::kSlots;
   const int c = lane & 3, slot = Lane<G, R>::slot(lane >> 2);
   Two s2[2] = {{0.f, 0.f}, {0.f, 0.f}};
@@ -492,7 +485,7 @@ __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* roo
   for (int t = t0; t < t1; t += kBoth) {
     cp_wait<kStages - 2>();
     __syncwarp();
-    const uint32_t at = ring + stage * kStage;
+    const unsigned char* at = room + stage * kStage;
     float s[kBoth][4];
 #pragma unroll
     for (int e = 0; e < kBoth; ++e) scores(q, at + e * kBytes, lane, s[e]);
