@@ -6,15 +6,18 @@
 //   sum_j (p_j step_j) code_j + sum_j p_j mid_j.
 //
 // The products (mma.sync m16n8k16 in f16: memory is to set the time, and the 128-row
-// tensor-memory form would be empty for the most part) take codes less 8, whole numbers from -8
-// to 7, and never see a scale: keys' scales multiply a group's product, values' scales the
-// weights.  A code becomes a number by a mask into the mantissa of 1024 or, 4 bits higher, of 64,
-// and one subtraction.  Queries go in as two f16 pieces (22 bits, after a power of two that fits
-// the row) in rows r and r + 8, which the lane that needs their sum holds both; weights p_j step_j as two
-// f16 pieces too, after a power of two that follows the largest step so far (so that a weight is held to
-// 2^-35 of the largest).  The product's 8 rows and columns hold up to 8 heads; where there are at most 4, or
-// 2, the free ones hold the weights' second pieces, and the other half of the groups, so that a lane scales half
-// of them.  Sums, maxima and the middles' part are f32.
+// tensor-memory form would be empty for the most part) take codes and never see a scale: keys'
+// scales multiply a group's product, values' scales the weights.  A code is an f16 number as it lies:
+// c in bits 0-3 is c 2^-24, in bits 4-7 c 2^-20, both below the smallest normal number, which the matrix
+// units take; so unpacking is a mask, and a shift for every second byte.  What a code stands for is
+// (mid - 8 step) + step c.  In sums over keys the two cancel in part, by a factor that grows with the root of the
+// keys' number: nothing next to a 16-bit result's rounding, but in f32 calls the codes have 8 taken off first
+// (1024 + c or 64 + c, by a mask, less 1032 or 72).  Queries go in as two f16 pieces (22 bits,
+// after a power of two that fits the row) in rows r and r + 8, which the lane that needs their sum holds both;
+// weights p_j step_j as two f16 pieces too, after a power of two that follows the largest step so far (so that
+// a weight is held to 2^-35 of the largest).  The product's 8 rows and columns hold up to 8 heads; where
+// there are at most 4, or 2, the free ones hold the weights' second pieces, and the other half of the groups, so
+// that a lane scales half of them.  Sums, maxima and the middles' part are f32.
 //
 // A warp works by itself: it streams pairs of blocks of 16 tokens (1,152 bytes a group of 64
 // each) through a ring of its own in shared memory with cp.async, and takes a range of one or
@@ -25,6 +28,8 @@
 //
 // Blocks outside the pool are zeros, tokens past the length have weight 0 whatever their
 // bytes are.
+#pragma once
+
 #include <cmath>
 #include <cstdint>
 
@@ -111,23 +116,22 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// (x & mask) | bits: a code into the mantissa of a power of two.
-__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
+// (x & mask) | bits, less `less`: codes in the mantissas of a power of two, and whole numbers.
+__device__ __forceinline__ uint32_t centred(uint32_t x, uint32_t mask, uint32_t bits, uint16_t less) {
   uint32_t y;
   asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "r"(mask), "r"(bits));
-  return y;
-}
-// The two codes at bits 0-3 of the halves as code - 8: 1024 + code, less 1032.
-__device__ __forceinline__ uint32_t low_codes(uint32_t x) {
-  const uint32_t y = and_or(x, 0x000f000fu, 0x64006400u);
-  const __half2 z = __hsub2(*reinterpret_cast<const __half2*>(&y), __half2half2(__ushort_as_half(0x6408)));
+  const __half2 z = __hsub2(*reinterpret_cast<const __half2*>(&y), __half2half2(__ushort_as_half(less)));
   return *reinterpret_cast<const uint32_t*>(&z);
 }
-// The two at bits 4-7: 64 + code, less 72.
-__device__ __forceinline__ uint32_t high_codes(uint32_t x) {
-  const uint32_t y = and_or(x, 0x00f000f0u, 0x54005400u);
-  const __half2 z = __hsub2(*reinterpret_cast<const __half2*>(&y), __half2half2(__ushort_as_half(0x5480)));
-  return *reinterpret_cast<const uint32_t*>(&z);
+// The two codes at bits 0-3, and at bits 4-7, of the halves as f16: as they lie, times 2^-24 and 2^-20; or
+// (Centred) code - 8, from 1024 + code less 1032, and 64 + code less 72.
+template <bool Centred>
+__device__ __forceinline__ uint32_t low(uint32_t x) {
+  return Centred ? centred(x, 0x000f000fu, 0x64006400u, 0x6408) : x & 0x000f000fu;
+}
+template <bool Centred>
+__device__ __forceinline__ uint32_t high(uint32_t x) {
+  return Centred ? centred(x, 0x00f000f0u, 0x54005400u, 0x5480) : x & 0x00f000f0u;
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 z = __floats2half2_rn(lo, hi);
@@ -139,6 +143,12 @@ __device__ __forceinline__ Two unpack_f16(uint32_t x) {
 }
 __device__ __forceinline__ float step_of(uint32_t scale) { return __uint_as_float(scale & 0xffff0000u); }
 __device__ __forceinline__ float mid_of(uint32_t scale) { return __uint_as_float(scale << 16); }
+// What a product's 0 stands for: mid, or (codes as they lie) mid - 8 step.
+template <bool Centred>
+__device__ __forceinline__ Two middle(const Two& step, uint32_t a0, uint32_t a1) {
+  const Two mid = {mid_of(a0), mid_of(a1)};
+  return Centred ? mid : fma(step, {-8.f, -8.f}, mid);
+}
 
 __device__ __forceinline__ float read_as(const void* p, int64_t i, int dtype) {
   return dtype == NYS_F32    ? static_cast<const float*>(p)[i]
@@ -246,7 +256,7 @@ struct Lane {
 template <int G, Rows4 R>
 struct Query {
   uint32_t a[G][2][2][4];
-  float sum[Lane<G, R>::kOwn];  // of the own groups' numbers
+  float sum[Lane<G, R>::kOwn];  // of the own groups' numbers, in the products' units
   float scale;                  // of the scores, to base 2
 };
 // A unit's query rows on their way to shared memory: 4 numbers a lane and chunk, as they are or, where rows
@@ -290,7 +300,7 @@ __device__ __forceinline__ void load_query(RawQuery<G, R>& q, const Attn4Args& a
   }
 }
 // By way of `room` in shared memory (8 heads of 64 G numbers).
-template <int G, Rows4 R>
+template <int G, Rows4 R, bool F32>
 __device__ __forceinline__ void make_query(Query<G, R>& q, const RawQuery<G, R>& raw, const Attn4Args& a, int n_heads,
                                            float* room) {
   const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
@@ -328,7 +338,7 @@ __device__ __forceinline__ void make_query(Query<G, R>& q, const RawQuery<G, R>&
   // Numbers below 2^15; a row that is not finite has no scores.
   const int exp = (int)(__float_as_uint(most) >> 23 & 255);
   const float up = __uint_as_float((uint32_t)(min(14 - (exp - 127), 126) + 127) << 23);
-  q.scale = exp == 255 ? __uint_as_float(0x7fc00000u) : a.scale * kLog2e / up;
+  q.scale = exp == 255 ? __uint_as_float(0x7fc00000u) : a.scale * kLog2e * (F32 ? 1.f : 0x1p24f) / up;
 #pragma unroll
   for (int o = 0; o < Lane<G, R>::kOwn; ++o) q.sum[o] = 0.f;
 #pragma unroll
@@ -348,8 +358,9 @@ __device__ __forceinline__ void make_query(Query<G, R>& q, const RawQuery<G, R>&
       for (int s = 0; s < 2; ++s)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          q.a[g][e][s][2 * i] = pack_f16(y[2 * s + i], y[2 * s + i + 4]);
-          q.a[g][e][s][2 * i + 1] = pack_f16(low[2 * s + i], low[2 * s + i + 4]);
+          const float f = F32 || i == 0 ? 1.f : 0.0625f;  // the codes' 2^-24 and 2^-20
+          q.a[g][e][s][2 * i] = pack_f16(y[2 * s + i] * f, y[2 * s + i + 4] * f);
+          q.a[g][e][s][2 * i + 1] = pack_f16(low[2 * s + i] * f, low[2 * s + i + 4] * f);
         }
     }
     q.sum[g / Lane<G, R>::kSlots] += sum;
@@ -358,12 +369,13 @@ __device__ __forceinline__ void make_query(Query<G, R>& q, const RawQuery<G, R>&
   for (int o = 0; o < Lane<G, R>::kOwn; ++o) {
     q.sum[o] += __shfl_xor_sync(0xffffffffu, q.sum[o], 1);
     q.sum[o] += __shfl_xor_sync(0xffffffffu, q.sum[o], 2);
+    if (!F32) q.sum[o] *= 0x1p-24f;
   }
 }
 
 // Scores of this lane's head for the tokens 2c, 2c + 1, 2c + 8, 2c + 9 of a block, unscaled.  The
 // own groups' scales are `own` 64-byte steps apart from key_scales on.
-template <int G, Rows4 R>
+template <int G, Rows4 R, bool F32>
 __device__ __forceinline__ void scores(const Query<G, R>& q, const unsigned char* at, int lane, float (&s)[4]) {
   constexpr int kSlots = Lane<G, R>::kSlots;
   const int c = lane & 3, slot = Lane<G, R>::slot(lane >> 2);
@@ -382,9 +394,9 @@ __device__ __forceinline__ void scores(const Query<G, R>& q, const unsigned char
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const uint32_t y = words[j][e], z = y >> 8;
-          if (x == 0 && e == 0) mma_f16<true>(acc[j], q.a[g][e][0], low_codes(y), high_codes(y));
-          else mma_f16<false>(acc[j], q.a[g][e][0], low_codes(y), high_codes(y));
-          mma_f16<false>(acc[j], q.a[g][e][1], low_codes(z), high_codes(z));
+          if (x == 0 && e == 0) mma_f16<true>(acc[j], q.a[g][e][0], low<F32>(y), high<F32>(y));
+          else mma_f16<false>(acc[j], q.a[g][e][0], low<F32>(y), high<F32>(y));
+          mma_f16<false>(acc[j], q.a[g][e][1], low<F32>(z), high<F32>(z));
         }
     }
     // (A last group that there is not: the row is 0, any scales do.)
@@ -395,7 +407,8 @@ __device__ __forceinline__ void scores(const Query<G, R>& q, const unsigned char
     for (int j = 0; j < 2; ++j) {
       const Two dot = fma({acc[j][2], acc[j][3]}, {0x1p-11f, 0x1p-11f}, {acc[j][0], acc[j][1]});
       const uint32_t a0 = scales[j][0], a1 = scales[j][1];
-      s2[j] = fma({step_of(a0), step_of(a1)}, dot, fma({mid_of(a0), mid_of(a1)}, {q.sum[o], q.sum[o]}, s2[j]));
+      const Two step = {step_of(a0), step_of(a1)};
+      s2[j] = fma(step, dot, fma(middle<F32>(step, a0, a1), {q.sum[o], q.sum[o]}, s2[j]));
     }
   }
   s2[0].get(s[0], s[1]);
@@ -421,7 +434,7 @@ constexpr bool left_fits = sizeof(Left<G>) <= Shape<G>::kRoom;
 static_assert(left_fits<1> && left_fits<2> && left_fits<3> && left_fits<4>, "Left has a warp's ring");
 
 // Blocks [t0, t1) of unit (b, kvh, heads h0 ..) -> `left`, which is the ring's place.
-template <int G, Rows4 R>
+template <int G, Rows4 R, bool F32>
 __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* room, int b, int kvh, int h0,
                                           int t0, int t1) {
   constexpr int kStages = Shape<G>::kStages, kBytes = block4_bytes(G), kStage = Shape<G>::kStage;
@@ -466,7 +479,7 @@ __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* roo
   for (int i = 0; i < kStages - 1; ++i) fetch(ring + i * kStage);
 
   Query<G, R> q;
-  make_query(q, raw, a, n_heads, reinterpret_cast<float*>(room + (kStages - 1) * kStage));
+  make_query<G, R, F32>(q, raw, a, n_heads, reinterpret_cast<float*>(room + (kStages - 1) * kStage));
 
   // Results: numbers 64 g + 8 r + 2 x (elements 2, 3: and one more) by columns 2c, 2c + 1 of the
   // product, which are what the rows are.
@@ -488,7 +501,7 @@ __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* roo
     const unsigned char* at = room + stage * kStage;
     float s[kBoth][4];
 #pragma unroll
-    for (int e = 0; e < kBoth; ++e) scores(q, at + e * kBytes, lane, s[e]);
+    for (int e = 0; e < kBoth; ++e) scores<G, R, F32>(q, at + e * kBytes, lane, s[e]);
     uint32_t v_scales[kBoth][kOwn][4];
 #pragma unroll
     for (int e = 0; e < kBoth; ++e)
@@ -582,8 +595,9 @@ __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* roo
         for (int j = 0; j < 2; ++j) {
           const uint32_t a0 = v_scales[e][x][2 * j], a1 = v_scales[e][x][2 * j + 1];
           const Two y = {p[e][2 * j], p[e][2 * j + 1]};
-          o_mid[x] = fma(y, {mid_of(a0), mid_of(a1)}, o_mid[x]);
-          const Two z = mul(mul(y, {step_of(a0), step_of(a1)}), {up[x], up[x]});
+          const Two step = {step_of(a0), step_of(a1)};
+          o_mid[x] = fma(y, middle<F32>(step, a0, a1), o_mid[x]);
+          const Two z = mul(mul(y, step), {up[x], up[x]});
           float x0, x1, y0, y1;
           z.get(x0, x1);
           pb[0][j] = pack_f16(x0, x1);
@@ -600,7 +614,7 @@ __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* roo
 #pragma unroll
           for (int z = 0; z < 4; ++z) {
             const uint32_t wa = z & 1 ? va[z / 2] >> 8 : va[z / 2], wb = z & 1 ? vb[z / 2] >> 8 : vb[z / 2];
-            const uint32_t av[4] = {low_codes(wa), high_codes(wa), low_codes(wb), high_codes(wb)};
+            const uint32_t av[4] = {low<F32>(wa), high<F32>(wa), low<F32>(wb), high<F32>(wb)};
             mma_f16<false>(o[g][z], av, pb[0][0], pb[0][1]);
             if (!kColumns) mma_f16<false>(o[g][z], av, pb[1][0], pb[1][1]);
           }
@@ -644,7 +658,7 @@ __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* roo
       float y[8];
 #pragma unroll
       for (int z = 0; z < 8; ++z) {
-        y[z] = o[g][z / 2][i + 2 * (z & 1)] * down;
+        y[z] = o[g][z / 2][i + 2 * (z & 1)] * (F32 ? down : z & 1 ? down * 0x1p20f : down * 0x1p24f);
         if (kColumns) y[z] += __shfl_xor_sync(0xffffffffu, y[z], 2);  // the second pieces' columns
       }
       const int column = 2 * c + i, h = Lane<G, R>::head(column);
@@ -695,7 +709,7 @@ __device__ __forceinline__ void emit(const Attn4Args& a, const Work4& w, const u
   }
 }
 
-template <int G, Rows4 R, bool Large>
+template <int G, Rows4 R, bool Large, bool F32>
 __global__ void __launch_bounds__(Cta<G, Large>::kThreads, Cta<G, Large>::kOfSm)
 attn4_kernel(Attn4Args a, Work4 w) {
   constexpr int kWarps = Cta<G, Large>::kWarps, kThreads = Cta<G, Large>::kThreads;
@@ -811,7 +825,7 @@ attn4_kernel(Attn4Args a, Work4 w) {
       }
       w.units[(int64_t)b * per_request + u] = {(int32_t)(pieces ? x : 2 * id + 1), count};
     }
-    run_range<G, R>(a, room, b, kvh, h0, mine, mine_end);
+    run_range<G, R, F32>(a, room, b, kvh, h0, mine, mine_end);
     const int n_heads = min(kHeads, a.group - h0);
     if (together) __syncthreads();
     else __syncwarp();
@@ -988,15 +1002,15 @@ Plan4 plan_of(int G, int64_t n, int kv_heads, int group, int64_t keys) {
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-template <int G, Rows4 R, bool Large>
+template <int G, Rows4 R, bool Large, bool F32>
 cudaError_t launch_main(const Attn4Args& a, const Work4& w, unsigned ctas, cudaStream_t stream) {
   using C = Cta<G, Large>;
-  const cudaError_t e = ensure_smem<attn4_kernel<G, R, Large>>(C::kSmem);
+  const cudaError_t e = ensure_smem<attn4_kernel<G, R, Large, F32>>(C::kSmem);
   if (e != cudaSuccess) return e;
-  attn4_kernel<G, R, Large><<<ctas, C::kThreads, C::kSmem, stream>>>(a, w);
+  attn4_kernel<G, R, Large, F32><<<ctas, C::kThreads, C::kSmem, stream>>>(a, w);
   return cudaGetLastError();
 }
-template <int G, Rows4 R>
+template <int G, Rows4 R, bool F32>
 cudaError_t launch(const Attn4Args& a, void* workspace, cudaStream_t stream) {
   const Plan4 p = plan<G>(a.n, a.kv_heads, a.group, (int64_t)a.width * a.page_blocks * kBlock4);
   Work4 w{};
@@ -1009,8 +1023,8 @@ cudaError_t launch(const Attn4Args& a, void* workspace, cudaStream_t stream) {
     at += up256(p.pieces * p.heads * sizeof(float2));
     w.results = reinterpret_cast<float*>(at);
   }
-  const cudaError_t e = p.large ? launch_main<G, R, true>(a, w, p.ctas, stream)
-                                : launch_main<G, R, false>(a, w, p.ctas, stream);
+  const cudaError_t e = p.large ? launch_main<G, R, true, F32>(a, w, p.ctas, stream)
+                                : launch_main<G, R, false, F32>(a, w, p.ctas, stream);
   if (e != cudaSuccess || p.pieces == 0) return e;
   const int64_t rows = p.units * p.heads;
   if (rows <= kSms * 4)
@@ -1020,31 +1034,21 @@ cudaError_t launch(const Attn4Args& a, void* workspace, cudaStream_t stream) {
                           stream, a, w);
 }
 
-template <int G>
+template <int G, bool F32>
 cudaError_t launch_of(const Attn4Args& a, void* workspace, cudaStream_t stream) {
-  if (a.group > 4) return launch<G, kEight>(a, workspace, stream);
-  if (a.group > 2 || G == 1) return launch<G, kFour>(a, workspace, stream);
-  return launch<G, G == 1 ? kFour : kTwo>(a, workspace, stream);
+  if (a.group > 4) return launch<G, kEight, F32>(a, workspace, stream);
+  if (a.group > 2 || G == 1) return launch<G, kFour, F32>(a, workspace, stream);
+  return launch<G, G == 1 ? kFour : kTwo, F32>(a, workspace, stream);
 }
-
-}  // namespace
-
-size_t attn4_workspace(const nys_attn_config& c, int64_t n, int64_t keys) {
-  if (n == 0) return 0;
-  const int G = groups4(c.d, c.dv);
-  const Plan4 p = plan_of(G, n, c.kv_heads, c.heads / c.kv_heads, keys);
-  if (p.pieces == 0) return 0;
-  return up256(p.units * sizeof(Cut4)) + up256(p.pieces * p.heads * sizeof(float2)) +
-         up256(p.pieces * p.heads * sizeof(float) * 64 * G);
-}
-
-cudaError_t launch_attn4(const Attn4Args& a, void* workspace, cudaStream_t stream) {
+template <bool F32>
+cudaError_t launch_any(const Attn4Args& a, void* workspace, cudaStream_t stream) {
   switch (groups4(a.d, a.dv)) {
-    case 1: return launch_of<1>(a, workspace, stream);
-    case 2: return launch_of<2>(a, workspace, stream);
-    case 3: return launch_of<3>(a, workspace, stream);
-    default: return launch_of<4>(a, workspace, stream);
+    case 1: return launch_of<1, F32>(a, workspace, stream);
+    case 2: return launch_of<2, F32>(a, workspace, stream);
+    case 3: return launch_of<3, F32>(a, workspace, stream);
+    default: return launch_of<4, F32>(a, workspace, stream);
   }
 }
 
+}  // namespace
 }  // namespace nys

@@ -140,6 +140,8 @@ cudaError_t launch_read4_bf16(const Read4Args& a, cudaStream_t stream);
 cudaError_t launch_read4_f16(const Read4Args& a, cudaStream_t stream);
 cudaError_t launch_qk(const QkArgs& a, cudaStream_t stream);
 cudaError_t launch_read4(const Read4Args& a, cudaStream_t stream);
+cudaError_t launch_attn4_16(const Attn4Args& a, void* workspace, cudaStream_t stream);
+cudaError_t launch_attn4_f32(const Attn4Args& a, void* workspace, cudaStream_t stream);
 cudaError_t launch_attn4(const Attn4Args& a, void* workspace, cudaStream_t stream);
 size_t attn4_workspace(const nys_attn_config& c, int64_t n, int64_t keys);
 

@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 4) qk_kernel(QkArgs a, int parts) {
   __shared__ __align__(16) float s_stage[kWarps][292];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t w = (int64_t)blockIdx.x * kWarps + warp;
-  Token t;
+  Token t{};
   t.at = parts == 1 ? w : w / parts;
   if (t.at >= a.tokens) return;
   const int part = (int)(w - t.at * parts);
