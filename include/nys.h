@@ -572,7 +572,7 @@ int nys_kv_append(const nys_attn_config* cfg, const nys_qk_prepare* prep, const 
 typedef struct {
   void* data;
   int64_t n_pages;
-  int32_t page; /* tokens a page, a positive multiple of 16 */
+  int32_t page; /* tokens a page, a positive multiple of 16; a page is below 2^31 bytes */
 } nys_pool4;
 
 /* Bytes of a page of this geometry.  Host arithmetic only.  Errors: NYS_E_INVAL,
@@ -608,12 +608,13 @@ int nys_attn4_workspace_bytes(const nys_attn_config* cfg, int64_t n, int64_t key
 
 /* One token of attention for n requests over their keys in a 4-bit cache: query
  * row b of q sees the lens[b] tokens in pages table[b * width + 0 ..], taken as
- * exactly the values they stand for.  Scores take queries to 22 bits, weights are
- * held to 16 bits (fp32 calls: 24) for the second product; sums run in fp32.  A
- * request without keys gets 0 (lse -INF).  Pages outside the pool count as keys
- * and values of 0 (NYS_ATTN_BAD_PAGE), lengths are taken clamped into their table
- * (NYS_ATTN_BAD_LENGTH); entries past a length are not read.  A query row that is
- * not finite gives NaN.
+ * exactly the values they stand for.  Scores take queries of 16-bit types as they
+ * are (to 2^-39 of the row's largest number), fp32 ones to 22 bits; weights are
+ * held to 22 bits for the second product (to 2^-35 of the largest); sums run in
+ * fp32.  A request without keys gets 0 (lse -INF).  Pages outside the pool count as
+ * keys and values of 0 (NYS_ATTN_BAD_PAGE), lengths are taken clamped into their
+ * table (NYS_ATTN_BAD_LENGTH); entries past a length are not read.  A query row
+ * that is not finite gives NaN.
  * first, first_lse (both or neither): the result [n][heads][dv] and log-sums
  * [n][heads] of the same queries over other keys (a shared prefix,
  * nys_attn_shared), which are joined in; first may be out itself, and first_lse

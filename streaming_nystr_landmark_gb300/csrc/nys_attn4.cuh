@@ -145,9 +145,8 @@ __device__ __forceinline__ float step_of(uint32_t scale) { return __uint_as_floa
 __device__ __forceinline__ float mid_of(uint32_t scale) { return __uint_as_float(scale << 16); }
 // What a product's 0 stands for: mid, or (codes as they lie) mid - 8 step.
 template <bool Centred>
-__device__ __forceinline__ Two middle(const Two& step, uint32_t a0, uint32_t a1) {
-  const Two mid = {mid_of(a0), mid_of(a1)};
-  return Centred ? mid : fma(step, {-8.f, -8.f}, mid);
+__device__ __forceinline__ float middle(float step, uint32_t word) {
+  return Centred ? mid_of(word) : fmaf(step, -8.f, mid_of(word));
 }
 
 __device__ __forceinline__ float read_as(const void* p, int64_t i, int dtype) {
@@ -251,14 +250,17 @@ struct Lane {
   static __device__ __forceinline__ int head(int r) { return r & (kHeadRows - 1); }
   static __device__ __forceinline__ int slot(int r) { return R == kTwo ? r >> 1 & 1 : 0; }
 };
+// (A lane's place: r = lane / 4, c = lane % 4.  It makes the B operands of column r, and has the products'
+// columns 2c and 2c + 1, whose slot is the same.)
 
-// A query row in pieces: this lane's A operands of the products, and what goes with them.
-template <int G, Rows4 R>
+// Query rows in pieces: this lane's B operands (of column r), and what goes with columns 2c and 2c + 1.
+template <int G, Rows4 R, bool F32>
 struct Query {
-  uint32_t a[G][2][2][4];
-  float sum[Lane<G, R>::kOwn];  // of the own groups' numbers, in the products' units
-  float scale;                  // of the scores, to base 2
+  uint32_t b[G][2][2][F32 ? 4 : 2];     // first pieces for low and high codes, then second ones
+  float sum[Lane<G, R>::kOwn][2];       // of the own groups' numbers, in the products' units
+  float scale[2];                       // of the scores, to base 2
 };
+
 // A unit's query rows on their way to shared memory: 4 numbers a lane and chunk, as they are or, where rows
 // are not aligned to them, as f32.
 template <int G, Rows4 R>
@@ -301,8 +303,8 @@ __device__ __forceinline__ void load_query(RawQuery<G, R>& q, const Attn4Args& a
 }
 // By way of `room` in shared memory (8 heads of 64 G numbers).
 template <int G, Rows4 R, bool F32>
-__device__ __forceinline__ void make_query(Query<G, R>& q, const RawQuery<G, R>& raw, const Attn4Args& a, int n_heads,
-                                           float* room) {
+__device__ __forceinline__ void make_query(Query<G, R, F32>& q, const RawQuery<G, R>& raw, const Attn4Args& a,
+                                           int n_heads, float* room) {
   const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
   const int h = Lane<G, R>::head(r), slot = Lane<G, R>::slot(r);
 #pragma unroll
@@ -336,22 +338,21 @@ __device__ __forceinline__ void make_query(Query<G, R>& q, const RawQuery<G, R>&
   most = largest(most, __shfl_xor_sync(0xffffffffu, most, 1));
   most = largest(most, __shfl_xor_sync(0xffffffffu, most, 2));
   // Numbers below 2^15; a row that is not finite has no scores.
+  constexpr int kOwn = Lane<G, R>::kOwn, kSlots = Lane<G, R>::kSlots;
   const int exp = (int)(__float_as_uint(most) >> 23 & 255);
   const float up = __uint_as_float((uint32_t)(min(14 - (exp - 127), 126) + 127) << 23);
-  q.scale = exp == 255 ? __uint_as_float(0x7fc00000u) : a.scale * kLog2e * (F32 ? 1.f : 0x1p24f) / up;
-#pragma unroll
-  for (int o = 0; o < Lane<G, R>::kOwn; ++o) q.sum[o] = 0.f;
+  const float scale = exp == 255 ? __uint_as_float(0x7fc00000u) : a.scale * kLog2e * (F32 ? 1.f : 0x1p24f) / up;
+  float sums[kOwn] = {};
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    const bool own = g % Lane<G, R>::kSlots == slot;
-    float sum = 0.f;
+    const bool own = g % kSlots == slot;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       float y[8], low[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         y[i] = own ? x[g][e][i] * up : 0.f;
-        sum += y[i];
+        sums[g / kSlots] += y[i];
         low[i] = (y[i] - __half2float(__float2half_rn(y[i]))) * 2048.f;
       }
 #pragma unroll
@@ -359,64 +360,87 @@ __device__ __forceinline__ void make_query(Query<G, R>& q, const RawQuery<G, R>&
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const float f = F32 || i == 0 ? 1.f : 0.0625f;  // the codes' 2^-24 and 2^-20
-          q.a[g][e][s][2 * i] = pack_f16(y[2 * s + i] * f, y[2 * s + i + 4] * f);
-          q.a[g][e][s][2 * i + 1] = pack_f16(low[2 * s + i] * f, low[2 * s + i + 4] * f);
+          q.b[g][e][s][i] = pack_f16(y[2 * s + i] * f, y[2 * s + i + 4] * f);
+          if (F32) q.b[g][e][s][F32 ? 2 + i : 0] = pack_f16(low[2 * s + i], low[2 * s + i + 4]);
         }
     }
-    q.sum[g / Lane<G, R>::kSlots] += sum;
   }
 #pragma unroll
-  for (int o = 0; o < Lane<G, R>::kOwn; ++o) {
-    q.sum[o] += __shfl_xor_sync(0xffffffffu, q.sum[o], 1);
-    q.sum[o] += __shfl_xor_sync(0xffffffffu, q.sum[o], 2);
-    if (!F32) q.sum[o] *= 0x1p-24f;
+  for (int o = 0; o < kOwn; ++o) {
+    sums[o] += __shfl_xor_sync(0xffffffffu, sums[o], 1);
+    sums[o] += __shfl_xor_sync(0xffffffffu, sums[o], 2);
+    if (!F32) sums[o] *= 0x1p-24f;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {  // from the columns' lanes
+    q.scale[i] = __shfl_sync(0xffffffffu, scale, 8 * c + 4 * i);
+#pragma unroll
+    for (int o = 0; o < kOwn; ++o) q.sum[o][i] = __shfl_sync(0xffffffffu, sums[o], 8 * c + 4 * i);
   }
 }
 
-// Scores of this lane's head for the tokens 2c, 2c + 1, 2c + 8, 2c + 9 of a block, unscaled.  The
-// own groups' scales are `own` 64-byte steps apart from key_scales on.
+// A token's scale word of group g, r = token % 8, of the first or second 8 of a block.
+__device__ __forceinline__ uint32_t scale_at(const unsigned char* scales, int g, int r, int second) {
+  return reinterpret_cast<const uint32_t*>(scales)[g * 16 + r / 2 * 4 + second * 2 + (r & 1)];
+}
+
+// Scores s[token r, r + 8][column 2c, 2c + 1] of a block, unscaled: the keys' codes are the product's A
+// operand, 16 tokens, so that the block takes 4 products a group.
 template <int G, Rows4 R, bool F32>
-__device__ __forceinline__ void scores(const Query<G, R>& q, const unsigned char* at, int lane, float (&s)[4]) {
-  constexpr int kSlots = Lane<G, R>::kSlots;
-  const int c = lane & 3, slot = Lane<G, R>::slot(lane >> 2);
-  Two s2[2] = {{0.f, 0.f}, {0.f, 0.f}};
+__device__ __forceinline__ void scores(const Query<G, R, F32>& q, const unsigned char* at, int lane, float (&s)[2][2]) {
+  constexpr int kSlots = Lane<G, R>::kSlots, kOwn = Lane<G, R>::kOwn;
+  const int r = lane >> 2, slot = Lane<G, R>::slot(2 * (lane & 3));
+  s[0][0] = s[0][1] = s[1][0] = s[1][1] = 0.f;
 #pragma unroll
-  for (int o = 0; o < Lane<G, R>::kOwn; ++o) {
-    float acc[2][4];
+  for (int o = 0; o < kOwn; ++o) {
+    float acc[4], low_acc[4];
 #pragma unroll
     for (int x = 0; x < kSlots; ++x) {
       const int g = o * kSlots + x;
       if (g >= G) continue;
       const uint4 k = lds128(at + g * 512 + lane * 16);
-      const uint32_t words[2][2] = {{k.x, k.y}, {k.z, k.w}};
+      const uint32_t words[2][2] = {{k.x, k.z}, {k.y, k.w}};  // [e][token r, r + 8]
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t y = words[j][e], z = y >> 8;
-          if (x == 0 && e == 0) mma_f16<true>(acc[j], q.a[g][e][0], low<F32>(y), high<F32>(y));
-          else mma_f16<false>(acc[j], q.a[g][e][0], low<F32>(y), high<F32>(y));
-          mma_f16<false>(acc[j], q.a[g][e][1], low<F32>(z), high<F32>(z));
+        for (int z = 0; z < 2; ++z) {
+          const uint32_t y0 = z ? words[e][0] >> 8 : words[e][0], y1 = z ? words[e][1] >> 8 : words[e][1];
+          const uint32_t av[4] = {low<F32>(y0), low<F32>(y1), high<F32>(y0), high<F32>(y1)};
+          if (x == 0 && e == 0 && z == 0) {
+            mma_f16<true>(acc, av, q.b[g][e][z][0], q.b[g][e][z][1]);
+            if (F32) mma_f16<true>(low_acc, av, q.b[g][e][z][F32 ? 2 : 0], q.b[g][e][z][F32 ? 3 : 0]);
+          } else {
+            mma_f16<false>(acc, av, q.b[g][e][z][0], q.b[g][e][z][1]);
+            if (F32) mma_f16<false>(low_acc, av, q.b[g][e][z][F32 ? 2 : 0], q.b[g][e][z][F32 ? 3 : 0]);
+          }
         }
     }
-    // (A last group that there is not: the row is 0, any scales do.)
-    const int g = o * kSlots + (G % kSlots && o == Lane<G, R>::kOwn - 1 ? 0 : slot);
-    const uint4 sc = lds128(at + key_scales4(G) + g * 64 + c * 16);
-    const uint32_t scales[2][2] = {{sc.x, sc.y}, {sc.z, sc.w}};
+    // (A last group that there is not: the column is 0, any scales do.)
+    const int g = o * kSlots + (G % kSlots && o == kOwn - 1 ? 0 : slot);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const Two dot = fma({acc[j][2], acc[j][3]}, {0x1p-11f, 0x1p-11f}, {acc[j][0], acc[j][1]});
-      const uint32_t a0 = scales[j][0], a1 = scales[j][1];
-      const Two step = {step_of(a0), step_of(a1)};
-      s2[j] = fma(step, dot, fma(middle<F32>(step, a0, a1), {q.sum[o], q.sum[o]}, s2[j]));
+    for (int t = 0; t < 2; ++t) {
+      const uint32_t word = scale_at(at + key_scales4(G), g, r, t);
+      const float step = step_of(word), mid = middle<F32>(step, word);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float dot = F32 ? fmaf(low_acc[2 * t + i], 0x1p-11f, acc[2 * t + i]) : acc[2 * t + i];
+        s[t][i] = fmaf(step, dot, fmaf(mid, q.sum[o][i], s[t][i]));
+      }
     }
   }
-  s2[0].get(s[0], s[1]);
-  s2[1].get(s[2], s[3]);
-  if (R == kTwo) {  // the other groups' lanes
+  if (R == kTwo) {  // the other groups' columns
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], 8);
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) s[t][i] += __shfl_xor_sync(0xffffffffu, s[t][i], 1);
   }
+}
+
+// An 8 x 8 matrix of f16, a row over 4 lanes, turned round.
+__device__ __forceinline__ uint32_t turned(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 // What a warp leaves in shared memory of its range: results [heads][64 G] without the middles' part,
@@ -441,7 +465,7 @@ __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* roo
   constexpr int kWords = kBytes / 16, kSlots = Lane<G, R>::kSlots, kOwn = Lane<G, R>::kOwn;
   constexpr bool kColumns = R != kEight;  // second pieces are columns of their own
   const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-  const int slot = Lane<G, R>::slot(r);
+  const int slot = Lane<G, R>::slot(2 * c);
   const uint32_t ring = tc::sptr(room);
   const int len = len_of(a, b, false);
   const int n_heads = min(kHeads, a.group - h0);
@@ -456,14 +480,15 @@ __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* roo
   const int32_t* page_at = next < end ? a.table + (int64_t)b * a.width + t0 / a.page_blocks : a.lens;
   int ahead = *page_at;
   bool bad = false;
-  const int64_t head_bytes = (int64_t)a.page_blocks * kBytes, page_bytes = a.kv_heads * head_bytes;
+  const uint32_t head_bytes = a.page_blocks * kBytes, page_bytes = a.kv_heads * head_bytes;  // (below 2^31)
   const uint8_t* head_at = a.blocks + kvh * head_bytes + lane * 16;
   const auto fetch = [&](uint32_t dst) {
 #pragma unroll
     for (int e = 0; e < kBoth; ++e) {
       const bool wanted = next < end, there = wanted && (uint32_t)ahead < (uint32_t)a.n_pages;
       bad |= wanted && !there;
-      const uint8_t* src = head_at + (there ? ahead * page_bytes + in_page * kBytes : 0);
+      // (Of a page that there is not, nothing is read: any address does.)
+      const uint8_t* src = head_at + (uint64_t)(there ? ahead : 0) * page_bytes + in_page * kBytes;
       ++next;
       const bool turn = ++in_page == a.page_blocks;
       in_page = turn ? 0 : in_page;
@@ -478,19 +503,20 @@ __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* roo
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) fetch(ring + i * kStage);
 
-  Query<G, R> q;
+  Query<G, R, F32> q;
   make_query<G, R, F32>(q, raw, a, n_heads, reinterpret_cast<float*>(room + (kStages - 1) * kStage));
 
   // Results: numbers 64 g + 8 r + 2 x (elements 2, 3: and one more) by columns 2c, 2c + 1 of the
-  // product, which are what the rows are.
+  // product.  For each of the two columns: the maximum, from where on it is followed, and this lane's tokens'
+  // weights and their middles' part.
   float o[G][4][4] = {};
-  Two o_mid[kOwn], l = {0.f, 0.f};
-  float m = -INFINITY, m_next = -INFINITY;  // the maximum, and from where on it is followed
-  float up[kOwn];                           // weights are p step up,
-  uint32_t limit[kOwn];                     // where steps are below this (their bits)
+  float o_mid[kOwn][2], l[2] = {0.f, 0.f};
+  float m[2] = {-INFINITY, -INFINITY}, m_next[2] = {-INFINITY, -INFINITY};
+  float up[kOwn];        // weights are p step up,
+  uint32_t limit[kOwn];  // where steps are below this (their bits)
 #pragma unroll
   for (int x = 0; x < kOwn; ++x) {
-    o_mid[x] = {0.f, 0.f};
+    o_mid[x][0] = o_mid[x][1] = 0.f;
     limit[x] = __float_as_uint(kLeastStep4);
     up[x] = 1.f;
   }
@@ -499,73 +525,80 @@ __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* roo
     cp_wait<kStages - 2>();
     __syncwarp();
     const unsigned char* at = room + stage * kStage;
-    float s[kBoth][4];
+    float s[kBoth][2][2];
 #pragma unroll
     for (int e = 0; e < kBoth; ++e) scores<G, R, F32>(q, at + e * kBytes, lane, s[e]);
-    uint32_t v_scales[kBoth][kOwn][4];
+    uint32_t v_scales[kBoth][kOwn][2];
 #pragma unroll
     for (int e = 0; e < kBoth; ++e)
 #pragma unroll
-      for (int x = 0; x < kOwn; ++x) {
-        const int g = x * kSlots + slot;
-        uint4 sc = make_uint4(0, 0, 0, 0);
-        if (G % kSlots == 0 || g < G) sc = lds128(at + e * kBytes + value_scales4(G) + g * 64 + c * 16);
-        v_scales[e][x][0] = sc.x, v_scales[e][x][1] = sc.y, v_scales[e][x][2] = sc.z, v_scales[e][x][3] = sc.w;
-      }
+      for (int x = 0; x < kOwn; ++x)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int g = x * kSlots + slot;
+          v_scales[e][x][u] = 0;
+          if (G % kSlots == 0 || g < G) v_scales[e][x][u] = scale_at(at + e * kBytes + value_scales4(G), g, r, u);
+        }
     // Tokens past the length, and blocks that are another warp's.
     if (t + kBoth > t1 || len - t * kBlock4 < kBoth * kBlock4) {
 #pragma unroll
       for (int e = 0; e < kBoth; ++e) {
         const int left = t + e < t1 ? len - (t + e) * kBlock4 : 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (2 * c + (i & 1) + (i >> 1) * 8 >= left) {
-            s[e][i] = -INFINITY;
+        for (int u = 0; u < 2; ++u)
+          if (r + 8 * u >= left) {
+            s[e][u][0] = s[e][u][1] = -INFINITY;
 #pragma unroll
-            for (int x = 0; x < kOwn; ++x) v_scales[e][x][i] = 0;
+            for (int x = 0; x < kOwn; ++x) v_scales[e][x][u] = 0;
           }
       }
     }
-    // Whether a lane's scores pass what is followed; the row's maximum is looked for only then.
-    float top = -INFINITY;
+    // Whether a lane's scores pass what is followed; the columns' maxima are looked for only then.
+    float top[2];
 #pragma unroll
-    for (int e = 0; e < kBoth; ++e) top = fmaxf(top, fmaxf(fmaxf(s[e][0], s[e][1]), fmaxf(s[e][2], s[e][3])));
-    top *= q.scale;
-    bool follow = top > m_next;
+    for (int i = 0; i < 2; ++i) {
+      top[i] = fmaxf(s[0][0][i], s[0][1][i]);
+#pragma unroll
+      for (int e = 1; e < kBoth; ++e) top[i] = fmaxf(top[i], fmaxf(s[e][0][i], s[e][1][i]));
+      top[i] *= q.scale[i];
+    }
+    bool follow = top[0] > m_next[0] || top[1] > m_next[1];
     uint32_t steps[kOwn];
 #pragma unroll
     for (int x = 0; x < kOwn; ++x) {
       steps[x] = 0;
 #pragma unroll
-      for (int e = 0; e < kBoth; ++e)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) steps[x] = max(steps[x], v_scales[e][x][i]);
+      for (int e = 0; e < kBoth; ++e) steps[x] = max(steps[x], max(v_scales[e][x][0], v_scales[e][x][1]));
       follow |= steps[x] >= limit[x];
     }
     if (__any_sync(0xffffffffu, follow)) {
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const float now = top > m_next ? fmaxf(m, top) : m;
-      const float by = m == -INFINITY ? 0.f : exp2_fast(m - now);
-      m = now;
-      m_next = m == -INFINITY ? m : m + kLazy;
-      l = mul(l, {by, by});
+      float by[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int u = 4; u < 32; u <<= 1) top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], u));
+        const float now = top[i] > m_next[i] ? fmaxf(m[i], top[i]) : m[i];
+        by[i] = m[i] == -INFINITY ? 0.f : exp2_fast(m[i] - now);
+        m[i] = now;
+        m_next[i] = now == -INFINITY ? now : now + kLazy;
+        l[i] *= by[i];
+      }
 #pragma unroll
       for (int x = 0; x < kOwn; ++x) {
-        o_mid[x] = mul(o_mid[x], {by, by});
-        float f = by;
-        uint32_t most = max(steps[x], __shfl_xor_sync(0xffffffffu, steps[x], 1));
-        most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        uint32_t most = steps[x];
+#pragma unroll
+        for (int u = 4; u < 32; u <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, u));
         // The next power of two; a step of NaN has a middle of NaN, which decides.
+        float less = 1.f;
         if (most >= limit[x] && most < 0x7f800000u) {
           const uint32_t exp = (most >> 23) + 1;
           limit[x] = exp << 23;
           const float was = up[x];
           up[x] = __uint_as_float((127u + 127u + kUnits - exp) << 23);
-          f *= up[x] / was;
+          less = up[x] / was;
         }
-        // Factors of this lane's columns.
-        const float f0 = __shfl_sync(0xffffffffu, f, 8 * c), f1 = __shfl_sync(0xffffffffu, f, 8 * c + 4);
+        const float f0 = by[0] * less, f1 = by[1] * less;
+        o_mid[x][0] *= by[0], o_mid[x][1] *= by[1];
 #pragma unroll
         for (int g = x * kSlots; g < x * kSlots + kSlots && g < G; ++g)
 #pragma unroll
@@ -575,36 +608,35 @@ __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* roo
           }
       }
     }
-    const float from = m == -INFINITY ? 0.f : -m;
-    float p[kBoth][4];
+    const float from[2] = {m[0] == -INFINITY ? 0.f : -m[0], m[1] == -INFINITY ? 0.f : -m[1]};
 #pragma unroll
     for (int e = 0; e < kBoth; ++e)
 #pragma unroll
-      for (int j = 0; j < 4; j += 2) {
-        fma({s[e][j], s[e][j + 1]}, {q.scale, q.scale}, {from, from}).get(p[e][j], p[e][j + 1]);
-        p[e][j] = exp2_fast(p[e][j]);
-        p[e][j + 1] = exp2_fast(p[e][j + 1]);
-        l = add(l, {p[e][j], p[e][j + 1]});
-      }
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          s[e][u][i] = exp2_fast(fmaf(s[e][u][i], q.scale[i], from[i]));
+          l[i] += s[e][u][i];
+        }
 #pragma unroll
     for (int e = 0; e < kBoth; ++e)
 #pragma unroll
       for (int x = 0; x < kOwn; ++x) {
         uint32_t pb[2][2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint32_t a0 = v_scales[e][x][2 * j], a1 = v_scales[e][x][2 * j + 1];
-          const Two y = {p[e][2 * j], p[e][2 * j + 1]};
-          const Two step = {step_of(a0), step_of(a1)};
-          o_mid[x] = fma(y, middle<F32>(step, a0, a1), o_mid[x]);
-          const Two z = mul(mul(y, step), {up[x], up[x]});
-          float x0, x1, y0, y1;
-          z.get(x0, x1);
-          pb[0][j] = pack_f16(x0, x1);
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t word = v_scales[e][x][u];
+          const float step = step_of(word), mid = middle<F32>(step, word), f = step * up[x];
+          o_mid[x][0] = fmaf(s[e][u][0], mid, o_mid[x][0]);
+          o_mid[x][1] = fmaf(s[e][u][1], mid, o_mid[x][1]);
+          const float x0 = s[e][u][0] * f, x1 = s[e][u][1] * f;
+          uint32_t y = pack_f16(x0, x1);
           // The second piece: less what was taken (exact).
-          fma(unpack_f16(pb[0][j]), {-1.f, -1.f}, z).get(y0, y1);
-          pb[1][j] = pack_f16(y0, y1);
-          if (kColumns && r >= 4) pb[0][j] = pb[1][j];
+          const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&y));
+          const uint32_t second = pack_f16(x0 - z.x, x1 - z.y);
+          if (kColumns) y = c >= 2 ? second : y;
+          pb[0][u] = turned(y);
+          if (!kColumns) pb[1][u] = turned(second);
         }
 #pragma unroll
         for (int g = x * kSlots; g < x * kSlots + kSlots && g < G; ++g) {
@@ -630,29 +662,30 @@ __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* roo
 
   // The ring is done with.
   Left<G>& left = *reinterpret_cast<Left<G>*>(room);
-  const auto sum_of = [](const Two& x) {
-    float y, z;
-    x.get(y, z);
-    y += z;
-    y += __shfl_xor_sync(0xffffffffu, y, 1);
-    return y + __shfl_xor_sync(0xffffffffu, y, 2);
-  };
-  const float l_sum = sum_of(l);
-  const int head = Lane<G, R>::head(r);
-  const bool mine = head < n_heads && c == 0 && (!kColumns || r < 4);
-  if (mine && slot == 0) {
-    left.sum[head] = make_float2(m, l_sum);
-    left.first[head] = first_sum(a, b, kvh * a.group + h0 + head);
-  }
+  const auto sum_of = [](float x) {
 #pragma unroll
-  for (int x = 0; x < kOwn; ++x) {
-    const float y = sum_of(o_mid[x]);
-    const int g = x * kSlots + slot;
-    if (mine && g < G) left.mid[head][g] = y;
+    for (int u = 4; u < 32; u <<= 1) x += __shfl_xor_sync(0xffffffffu, x, u);
+    return x;
+  };
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int column = 2 * c + i, head = Lane<G, R>::head(column);
+    const bool mine = head < n_heads && r == 0 && (!kColumns || column < 4);
+    const float l_sum = sum_of(l[i]);
+    if (mine && slot == 0) {
+      left.sum[head] = make_float2(m[i], l_sum);
+      left.first[head] = first_sum(a, b, kvh * a.group + h0 + head);
+    }
+#pragma unroll
+    for (int x = 0; x < kOwn; ++x) {
+      const float y = sum_of(o_mid[x][i]);
+      const int g = x * kSlots + slot;
+      if (mine && g < G) left.mid[head][g] = y;
+    }
   }
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    const float down = 1.f / __shfl_sync(0xffffffffu, up[g / kSlots], 4 * Lane<G, R>::kHeadRows * (g % kSlots));
+    const float down = 1.f / up[g / kSlots];  // (of columns whose slot has the group)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       float y[8];
@@ -662,7 +695,7 @@ __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* roo
         if (kColumns) y[z] += __shfl_xor_sync(0xffffffffu, y[z], 2);  // the second pieces' columns
       }
       const int column = 2 * c + i, h = Lane<G, R>::head(column);
-      if (h < n_heads && (!kColumns || column < 4) && Lane<G, R>::slot(column) == g % kSlots) {
+      if (h < n_heads && (!kColumns || column < 4) && slot == g % kSlots) {
 #pragma unroll
         for (int z = 0; z < 8; z += 4)
           *reinterpret_cast<float4*>(&left.result[h][64 * g + 8 * r + z]) =

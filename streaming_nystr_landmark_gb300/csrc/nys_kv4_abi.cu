@@ -10,6 +10,10 @@ using namespace nys;
 
 namespace {
 
+int64_t page4_bytes(const nys_attn_config& c, int32_t page) {
+  return (int64_t)c.kv_heads * (page / kBlock4) * block4_bytes(groups4(c.d, c.dv));
+}
+
 // Rows that a caller may leave out.
 Rows rows_or_none(const nys_rows* r) { return r ? rows_of(r) : Rows{}; }
 
@@ -24,10 +28,12 @@ int check_prepare(const nys_qk_prepare* p, const nys_attn_config& c, int64_t tok
   return NYS_OK;
 }
 
-int check_pool4(const nys_pool4* p) {
+// (A page's bytes fit 31 bits: kernels take them so.)
+int check_pool4(const nys_pool4* p, const nys_attn_config& c) {
   if (!p || p->n_pages < 0 || p->page < kBlock4 || p->page % kBlock4) return NYS_E_INVAL;
   if (p->n_pages > 0 && !p->data) return NYS_E_INVAL;
-  if (p->n_pages > INT32_MAX || p->page > (1 << 20)) return NYS_E_UNSUPPORTED;
+  if (p->n_pages > INT32_MAX || p->page > (1 << 20) || page4_bytes(c, p->page) > INT32_MAX)
+    return NYS_E_UNSUPPORTED;
   return aligned(p->data, 16) ? NYS_OK : NYS_E_ALIGN;
 }
 
@@ -106,7 +112,7 @@ int nys_kv4_append(const nys_attn_config* cfg, const nys_qk_prepare* prep, const
   if (!k || !v) return NYS_E_INVAL;
   QkArgs a{};
   int rc = fill(a, cfg, prep, tokens, q, k, v, positions, q_out, k_out);
-  if (rc || (rc = check_pool4(pool))) return rc;
+  if (rc || (rc = check_pool4(pool, *cfg))) return rc;
   if (tokens > 0 && !slots) return NYS_E_INVAL;
   if (!aligned(slots, 8)) return NYS_E_ALIGN;
   a.slots = slots;
@@ -131,7 +137,7 @@ int nys_kv4_read(const nys_attn_config* cfg, const nys_pool4* pool, int64_t toke
   if (rc) return rc;
   if (tokens < 0 || tokens > INT32_MAX) return NYS_E_INVAL;
   const int es = elem_size(cfg->dtype);
-  if ((rc = check_pool4(pool)) || (rc = check_rows(k_out, tokens, es)) ||
+  if ((rc = check_pool4(pool, *cfg)) || (rc = check_rows(k_out, tokens, es)) ||
       (rc = check_rows(v_out, tokens, es)))
     return rc;
   if (!aligned(slots, 8)) return NYS_E_ALIGN;
@@ -157,8 +163,8 @@ int nys_kv4_page_bytes(const nys_attn_config* cfg, int32_t page, size_t* bytes) 
   const int rc = check_attn(cfg);
   if (rc) return rc;
   if (!bytes || page < kBlock4 || page % kBlock4) return NYS_E_INVAL;
-  if (page > (1 << 20)) return NYS_E_UNSUPPORTED;
-  *bytes = (size_t)cfg->kv_heads * (page / kBlock4) * block4_bytes(groups4(cfg->d, cfg->dv));
+  if (page > (1 << 20) || page4_bytes(*cfg, page) > INT32_MAX) return NYS_E_UNSUPPORTED;
+  *bytes = (size_t)page4_bytes(*cfg, page);
   return NYS_OK;
 }
 
@@ -178,7 +184,7 @@ int nys_attn4(const nys_attn_config* cfg, int64_t n, const nys_pool4* pool, cons
   if (rc) return rc;
   if (n < 0 || n > INT32_MAX / 64 || width < 0) return NYS_E_INVAL;
   const int es = elem_size(cfg->dtype);
-  if ((rc = check_pool4(pool)) || (rc = check_rows(q, n, es)) || (rc = check_rows(out, n, es)))
+  if ((rc = check_pool4(pool, *cfg)) || (rc = check_rows(q, n, es)) || (rc = check_rows(out, n, es)))
     return rc;
   if (first && (rc = check_rows(first, n, es))) return rc;
   if (!first != !first_lse) return NYS_E_INVAL;

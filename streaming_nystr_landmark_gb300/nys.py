@@ -13,7 +13,6 @@ from __future__ import annotations
 import ctypes
 import math
 import os
-from fractions import Fraction
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnys.so")
 
@@ -811,8 +810,8 @@ class Rotation:
     position: pair i turns by base^(-2i / rot), or by freqs[i], radians a position.  Pairs
     are numbers i and i + rot/2, or 2i and 2i + 1 (interleaved)."""
 
-    # 2 pi to 50 digits.
-    _TURN = Fraction(62831853071795864769252867665590057683943387987502, 10 ** 49)
+    # 2 pi to 50 digits, times 10^49.
+    _TURN = 62831853071795864769252867665590057683943387987502
 
     def __init__(self, d, base=10000.0, rot=None, interleaved=False, freqs=None, device="cuda"):
         import torch
@@ -827,9 +826,13 @@ class Rotation:
         self.d, self.rot, self.interleaved = d, rot, bool(interleaved)
         self.device = _cuda_device(device)
         # Fractions of a turn in 64 bits; torch holds them as int64.
-        turns = [round(Fraction(f) / self._TURN * 2 ** 64) % 2 ** 64 for f in freqs]
-        self.turns = torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns],
-                                  dtype=torch.int64).to(self.device)
+        turns = []
+        for f in freqs:
+            a, b = f.as_integer_ratio()
+            a, b = a * 10 ** 49 << 64, b * self._TURN
+            t = (2 * a + b) // (2 * b) % 2 ** 64      # to the nearest
+            turns.append(t - 2 ** 64 if t >= 2 ** 63 else t)
+        self.turns = torch.tensor(turns, dtype=torch.int64, device=self.device)
 
 
 class QKPrepare(_OnDevice):

@@ -307,6 +307,54 @@ def test_unusual_values(cuda_device):
     assert not bool(out.isnan().any()) and att.status() == 0
 
 
+def test_empty_tables_and_pools(cuda_device):
+    """No columns, no pages, no requests: zeros, or what is joined in."""
+    torch, ref, nys = _mods()
+    dev = cuda_device
+    att = nys.ExactAttention(4, 2, 64, 64, device=dev)
+    q = torch.randn((3, 4, 64), generator=torch.Generator(dev).manual_seed(1), device=dev)
+    none = torch.zeros(3, dtype=torch.int32, device=dev)
+    for n_pages, width in ((0, 0), (2, 0), (0, 3)):
+        cache = nys.PagedKV4(n_pages, 16, 2, 64, 64, device=dev)
+        table = torch.zeros((3, width), dtype=torch.int32, device=dev)
+        out, lse = torch.full_like(q, 7.0), torch.full((3, 4), 7.0, device=dev)
+        att.paged4(q, cache, none, table, out, lse=lse)
+        assert not bool(out.any()) and bool((lse == -math.inf).all()) and att.status() == 0
+        first, first_lse = torch.randn_like(q), torch.randn_like(lse)
+        att.paged4(q, cache, none, table, out, first=first, first_lse=first_lse, lse=lse)
+        assert torch.allclose(out, first, rtol=1e-6) and torch.allclose(lse, first_lse, rtol=1e-5, atol=1e-6)
+        # Lengths that nothing holds are taken as nothing, and said so.
+        att.paged4(q, cache, none + 5, table, out)
+        assert att.status() == (nys.NYS_ATTN_BAD_PAGE if width else nys.NYS_ATTN_BAD_LENGTH) and not bool(out.any())
+        att.clear_status()
+        cache.write(torch.zeros((2, 2, 64), device=dev), torch.zeros((2, 2, 64), device=dev),
+                    torch.full((2,), -1, dtype=torch.int64, device=dev))
+    empty = torch.empty((0, 4, 64), device=dev)
+    assert att.paged4(empty, cache, none[:0], table[:0], empty) is empty
+    rows = torch.empty((0, 2, 64), device=dev)
+    cache.write(rows, rows, torch.empty(0, dtype=torch.int64, device=dev))
+    cache.read(torch.empty(0, dtype=torch.int64, device=dev), rows, rows)
+    prep = nys.QKPrepare(4, 2, 64, rotation=nys.Rotation(64, device=dev), device=dev)
+    prep.rows(empty, rows, none[:0])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("lens", [[40000], [9000, 30011, 5], [1500] * 7])
+def test_long_requests(cuda_device, dtype, lens):
+    """Units cut into many pieces, of CTAs whose warps joined and of some that did not."""
+    torch, ref, nys = _mods()
+    dt, dev = getattr(torch, dtype), cuda_device
+    for heads, kv, d in ((16, 2, 128), (4, 2, 64)):
+        g = torch.Generator(device=dev).manual_seed(13)
+        cache, table, slots = _cache(torch, nys, dev, g, lens, kv, d, d, 64, dt)
+        q = torch.randn((len(lens), heads, d), generator=g, device=dev).to(dt)
+        out, lse = torch.empty_like(q), torch.empty((len(lens), heads), device=dev)
+        at = torch.tensor(lens, dtype=torch.int32, device=dev)
+        att = nys.ExactAttention(heads, kv, d, d, dtype=dt, device=dev)
+        att.paged4(q, cache, at, table, out, lse=lse)
+        _check(torch, ref, cache, slots, q, out, lse, heads, 1 / math.sqrt(d), dt)
+
+
 def test_wide_pool_offsets(cuda_device):
     """Pages whose bytes lie past 32 bits."""
     torch, ref, nys = _mods()

@@ -112,6 +112,12 @@ def test_bad_pool(pool, code):
     assert _append(True, pool=pool) == _write(pool=pool) == _read(pool=pool) == _attn(pool=pool) == code
 
 
+def test_pages_past_31_bits():
+    c, pool = cfg(d=256, dv=256), nys.NysPool4(A, 1, 1 << 20)     # 2.4 GB
+    assert _append(True, cfg=c, pool=pool) == _write(cfg=c, pool=pool) == _read(cfg=c, pool=pool) == U
+    assert _attn(cfg=c, pool=pool, w=1) == U
+
+
 @pytest.mark.parametrize("call", [_write, _read])
 @pytest.mark.parametrize("kw,code", [
     (dict(n=-1), E), (dict(n=1 << 31), E), (dict(k=None), E), (dict(v=None), E), (dict(k=rows(p=None)), E),
@@ -144,9 +150,9 @@ def test_workspace():
 @pytest.mark.parametrize("d,dv,groups", [(4, 4, 1), (64, 64, 1), (68, 4, 2), (128, 128, 2), (80, 200, 4)])
 def test_page_bytes(d, dv, groups):
     assert nys.nys_kv4_page_bytes(cfg(d=d, dv=dv), 48) == 8 * 3 * 1152 * groups
-    for page in (0, 8, 24, -16):
+    for page in (0, 8, 24, -16, 1 << 20):
         with pytest.raises(nys.NysError):
-            nys.nys_kv4_page_bytes(cfg(), page)
+            nys.nys_kv4_page_bytes(cfg(heads=128, kv_heads=128), page)
 
 
 def test_turns():
@@ -157,3 +163,66 @@ def test_turns():
         for pos in (1, 12345, -7):
             turn = (t * pos % 2 ** 64) / 2 ** 64
             assert abs(math.remainder(turn * 2 * math.pi - pos * f, 2 * math.pi)) < 1e-9
+
+
+def _objects(monkeypatch, index):
+    """This module's classes on a machine with two GPUs that need not be there."""
+    torch = pytest.importorskip("torch")
+    from test_attn_host import _Device, _Tensor
+    fake, dev = _Device(monkeypatch), torch.device("cuda", index)
+    for name in ("nys_qk_rows", "nys_kv_append", "nys_kv4_append", "nys_kv4_write", "nys_kv4_read", "nys_attn4"):
+        monkeypatch.setattr(nys, name, lambda *a, name=name: fake.calls.append((name, fake.now, a[-1])))
+    c = nys.NysAttnConfig(2, 2, 8, 8, nys.NYS_F32, 0.0)
+    prep = nys.QKPrepare.__new__(nys.QKPrepare)
+    vars(prep).update(torch=fake, device=dev, dtype=torch.float32, heads=2, kv_heads=2, d=8, cfg=c, _int32=torch.int32,
+                      _prep=nys.NysQkPrepare(None, None, 1e-6, A, 8, 0, 0))
+    att = nys.ExactAttention.__new__(nys.ExactAttention)
+    vars(att).update(torch=fake, device=dev, dtype=torch.float32, heads=2, kv_heads=2, d=8, dv=8, cfg=c, _work=None,
+                     _work_ptr=None, _work_bytes=0, _sizes=None, _captured=False, _held=[], _status_ptr=A)
+    full, four = nys.PagedKV.__new__(nys.PagedKV), nys.PagedKV4.__new__(nys.PagedKV4)
+    for cache, pool in ((full, nys.NysPool(A, A, 2, 16)), (four, nys.NysPool4(A, 2, 16))):
+        vars(cache).update(torch=fake, device=dev, dtype=torch.float32, kv_heads=2, d=8, dv=8, page=16, n_pages=2,
+                           _cfg=c, _pool=pool)
+    f = lambda *s: _Tensor(s, torch.float32, index)
+    i32 = lambda *s: _Tensor(s, torch.int32, index)
+    i64 = lambda *s: _Tensor(s, torch.int64, index)
+    rows = lambda: f(3, 2, 8)
+    return _Tensor, fake, {
+        "nys_qk_rows": (prep.rows, [rows(), rows(), i32(3), rows(), rows()]),
+        "nys_kv_append": (prep.append, [rows(), rows(), rows(), i32(3), i64(3), full, rows(), rows()]),
+        "nys_kv4_append": (prep.append, [rows(), rows(), rows(), i32(3), i64(3), four, rows(), rows(), 7]),
+        "nys_kv4_write": (four.write, [rows(), rows(), i64(3)]),
+        "nys_kv4_read": (four.read, [i64(3), rows(), rows()]),
+        "nys_attn4": (att.paged4, [rows(), four, i32(3), i32(3, 2), rows(), rows(), f(3, 2), f(3, 2)]),
+    }
+
+
+NAMES = ["nys_qk_rows", "nys_kv_append", "nys_kv4_append", "nys_kv4_write", "nys_kv4_read", "nys_attn4"]
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_calls_run_on_their_objects_device(monkeypatch, name):
+    for index in (0, 1):
+        _, fake, calls = _objects(monkeypatch, index)
+        fn, args = calls[name]
+        fn(*args)
+        assert fake.calls == [(name, index, 1000 + index)] and fake.now == 0
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_tensors_of_another_device_are_refused(monkeypatch, name):
+    _Tensor, fake, calls = _objects(monkeypatch, 1)
+    fn, args = calls[name]
+    for a in args:
+        if isinstance(a, _Tensor):
+            a.index = 0
+            with pytest.raises(ValueError, match="cuda:0"):
+                fn(*args)
+            a.index = 1
+        elif isinstance(a, (nys.PagedKV, nys.PagedKV4)):
+            import torch
+            a.device = torch.device("cuda", 0)
+            with pytest.raises(ValueError, match="cuda:0"):
+                fn(*args)
+            a.device = torch.device("cuda", 1)
+    assert fake.calls == []
