@@ -61,16 +61,12 @@ struct Shape {
   // The query's rows go through one stage, and what a warp leaves (Left) takes the ring's place.
   static_assert(kStage >= kHeads * 64 * G * 4 && kStages >= 2, "a stage holds 8 rows of 64 G floats");
 };
-// CTAs: of 4 warps, several on an SM; or, where there are fewer units than SMs, one of as many
-// warps as an SM's registers take (4 requests of 3 to 345 tokens: 9.6 us with 4 warps, WIDE_US with 12).
-template <int G, bool Large>
-struct Cta {
-  static constexpr int kWarps = !Large ? 4 : G <= 2 ? 12 : 8;
-  static constexpr int kOfSm = Large ? 1 : G <= 2 ? 3 : 2;
-  static constexpr int kThreads = kWarps * 32;
-  static constexpr int kSmem = kWarps * Shape<G>::kRoom;
-  static constexpr int kPieces = kWarps * kPiece;
-};
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+// CTAs of an SM: as many as its registers take.
+template <int G>
+constexpr int kOfSm = G <= 2 ? 3 : 2;
+constexpr int kPieceBlocks = kWarps * kPiece;
 
 // Pieces of cut units: in the workspace, first the units' records, then each piece's
 // [heads] maxima and sums, then its results [heads][64 G].
@@ -510,7 +506,8 @@ __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* roo
   // product.  For each of the two columns: the maximum, from where on it is followed, and this lane's tokens'
   // weights and their middles' part.
   float o[G][4][4] = {};
-  float o_mid[kOwn][2], l[2] = {0.f, 0.f};
+  float o_mid[kOwn][2];
+  Two l = {0.f, 0.f};
   float m[2] = {-INFINITY, -INFINITY}, m_next[2] = {-INFINITY, -INFINITY};
   float up[kOwn];        // weights are p step up,
   uint32_t limit[kOwn];  // where steps are below this (their bits)
@@ -581,8 +578,8 @@ __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* roo
         by[i] = m[i] == -INFINITY ? 0.f : exp2_fast(m[i] - now);
         m[i] = now;
         m_next[i] = now == -INFINITY ? now : now + kLazy;
-        l[i] *= by[i];
       }
+      l = mul(l, {by[0], by[1]});
 #pragma unroll
       for (int x = 0; x < kOwn; ++x) {
         uint32_t most = steps[x];
@@ -612,12 +609,12 @@ __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* roo
 #pragma unroll
     for (int e = 0; e < kBoth; ++e)
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          s[e][u][i] = exp2_fast(fmaf(s[e][u][i], q.scale[i], from[i]));
-          l[i] += s[e][u][i];
-        }
+      for (int u = 0; u < 2; ++u) {
+        fma({s[e][u][0], s[e][u][1]}, {q.scale[0], q.scale[1]}, {from[0], from[1]}).get(s[e][u][0], s[e][u][1]);
+        s[e][u][0] = exp2_fast(s[e][u][0]);
+        s[e][u][1] = exp2_fast(s[e][u][1]);
+        l = add(l, {s[e][u][0], s[e][u][1]});
+      }
 #pragma unroll
     for (int e = 0; e < kBoth; ++e)
 #pragma unroll
@@ -667,11 +664,13 @@ __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* roo
     for (int u = 4; u < 32; u <<= 1) x += __shfl_xor_sync(0xffffffffu, x, u);
     return x;
   };
+  float sums[2];
+  l.get(sums[0], sums[1]);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int column = 2 * c + i, head = Lane<G, R>::head(column);
     const bool mine = head < n_heads && r == 0 && (!kColumns || column < 4);
-    const float l_sum = sum_of(l[i]);
+    const float l_sum = sum_of(sums[i]);
     if (mine && slot == 0) {
       left.sum[head] = make_float2(m[i], l_sum);
       left.first[head] = first_sum(a, b, kvh * a.group + h0 + head);
@@ -742,11 +741,8 @@ __device__ __forceinline__ void emit(const Attn4Args& a, const Work4& w, const u
   }
 }
 
-template <int G, Rows4 R, bool Large, bool F32>
-__global__ void __launch_bounds__(Cta<G, Large>::kThreads, Cta<G, Large>::kOfSm)
-attn4_kernel(Attn4Args a, Work4 w) {
-  constexpr int kWarps = Cta<G, Large>::kWarps, kThreads = Cta<G, Large>::kThreads;
-  constexpr int kPiece = Cta<G, Large>::kPieces;
+template <int G, Rows4 R, bool F32>
+__global__ void __launch_bounds__(kThreads, kOfSm<G>) attn4_kernel(Attn4Args a, Work4 w) {
   extern __shared__ __align__(128) unsigned char smem[];
   constexpr int kRoom = Shape<G>::kRoom;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -770,7 +766,7 @@ attn4_kernel(Attn4Args a, Work4 w) {
   const int64_t warps = (int64_t)gridDim.x * kWarps;
   // The first rule: pieces of a CTA; the second: even shares of the warps, `share` blocks and one more in
   // the first `more` warps.
-  const bool pieces = total / kPiece + units <= gridDim.x;
+  const bool pieces = total / kPieceBlocks + units <= gridDim.x;
   const int64_t share = total > UINT32_MAX ? total / warps : (uint32_t)total / (uint32_t)warps;
   const int64_t more = total - share * warps;
   const int64_t first_warp = (int64_t)blockIdx.x * kWarps;
@@ -784,7 +780,7 @@ attn4_kernel(Attn4Args a, Work4 w) {
       for (int i = 0; i < 4; ++i) {
         const int t = c0 == 0 ? first[i] : blocks_at(c0 + 4 * lane + i, false);
         mine[i] = all;
-        all += (int64_t)per_request * (pieces ? (t + kPiece - 1) / kPiece : t);
+        all += (int64_t)per_request * (pieces ? (t + kPieceBlocks - 1) / kPieceBlocks : t);
       }
       int64_t scan = all;
 #pragma unroll
@@ -827,7 +823,7 @@ attn4_kernel(Attn4Args a, Work4 w) {
     t = blocks_at(b, false);
     at = x - before;
   }
-  const int np = pieces ? (t + kPiece - 1) / kPiece : 1;
+  const int np = pieces ? (t + kPieceBlocks - 1) / kPieceBlocks : 1;
   while (x < end) {
     // Unit u's blocks [lo, hi), this warp's of them [mine, mine_end).
     const int per = pieces ? np : t;
@@ -998,30 +994,22 @@ struct Plan4 {
   unsigned ctas;
   int64_t units, pieces;  // pieces: 0 where no unit can be cut
   int heads;
-  bool large;
 };
-template <int G, bool Large>
-void plan_ctas(Plan4& p, int64_t blocks) {
-  using C = Cta<G, Large>;
-  // CTAs that run at once; fewer only where the pieces of the longest requests need fewer.
-  const int64_t most = kSms * C::kOfSm;
-  const int64_t cut = (blocks + C::kPieces - 1) / C::kPieces;
-  const int64_t ctas = cut > most ? most : p.units * (cut + 1);
-  p.ctas = (unsigned)(ctas < most ? ctas : most);
-  // (blocks / kPieces <= 1 piece a unit and one more for each: the first rule, and no cut.)
-  const bool never = cut == 1 && p.units * 2 <= p.ctas;
-  p.pieces = never ? 0 : 2 * (int64_t)p.ctas * C::kWarps;
-}
 template <int G>
 Plan4 plan(int64_t n, int kv_heads, int group, int64_t keys) {
-  Plan4 p{};
+  Plan4 p;
   const int tiles = (group + kHeads - 1) / kHeads;
   p.units = n * kv_heads * tiles;
   p.heads = group < kHeads ? group : kHeads;
   const int64_t blocks = keys > kBlock4 ? (keys + kBlock4 - 1) / kBlock4 : 1;
-  p.large = p.units * 2 <= kSms && blocks <= Cta<G, true>::kPieces;
-  if (p.large) plan_ctas<G, true>(p, blocks);
-  else plan_ctas<G, false>(p, blocks);
+  // CTAs that run at once; fewer only where the pieces of the longest requests need fewer.
+  const int64_t most = kSms * kOfSm<G>;
+  const int64_t cut = (blocks + kPieceBlocks - 1) / kPieceBlocks;
+  const int64_t ctas = cut > most ? most : p.units * (cut + 1);
+  p.ctas = (unsigned)(ctas < most ? ctas : most);
+  // (Units of one piece, and a CTA more for each: the first rule, and no cut.)
+  const bool never = cut == 1 && p.units * 2 <= p.ctas;
+  p.pieces = never ? 0 : 2 * (int64_t)p.ctas * kWarps;
   return p;
 }
 Plan4 plan_of(int G, int64_t n, int kv_heads, int group, int64_t keys) {
@@ -1035,14 +1023,6 @@ Plan4 plan_of(int G, int64_t n, int kv_heads, int group, int64_t keys) {
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-template <int G, Rows4 R, bool Large, bool F32>
-cudaError_t launch_main(const Attn4Args& a, const Work4& w, unsigned ctas, cudaStream_t stream) {
-  using C = Cta<G, Large>;
-  const cudaError_t e = ensure_smem<attn4_kernel<G, R, Large, F32>>(C::kSmem);
-  if (e != cudaSuccess) return e;
-  attn4_kernel<G, R, Large, F32><<<ctas, C::kThreads, C::kSmem, stream>>>(a, w);
-  return cudaGetLastError();
-}
 template <int G, Rows4 R, bool F32>
 cudaError_t launch(const Attn4Args& a, void* workspace, cudaStream_t stream) {
   const Plan4 p = plan<G>(a.n, a.kv_heads, a.group, (int64_t)a.width * a.page_blocks * kBlock4);
@@ -1056,8 +1036,11 @@ cudaError_t launch(const Attn4Args& a, void* workspace, cudaStream_t stream) {
     at += up256(p.pieces * p.heads * sizeof(float2));
     w.results = reinterpret_cast<float*>(at);
   }
-  const cudaError_t e = p.large ? launch_main<G, R, true, F32>(a, w, p.ctas, stream)
-                                : launch_main<G, R, false, F32>(a, w, p.ctas, stream);
+  constexpr int kSmem = kWarps * Shape<G>::kRoom;
+  cudaError_t e = ensure_smem<attn4_kernel<G, R, F32>>(kSmem);
+  if (e != cudaSuccess) return e;
+  attn4_kernel<G, R, F32><<<p.ctas, kThreads, kSmem, stream>>>(a, w);
+  e = cudaGetLastError();
   if (e != cudaSuccess || p.pieces == 0) return e;
   const int64_t rows = p.units * p.heads;
   if (rows <= kSms * 4)
