@@ -5,19 +5,26 @@
 //   step * (q . code) + mid * sum(q), and its part of the output
 //   sum_j (p_j step_j) code_j + sum_j p_j mid_j.
 //
-// The products (mma.sync m16n8k16 in f16: memory is to set the time, and the 128-row
-// tensor-memory form would be empty for the most part) take codes and never see a scale: keys'
-// scales multiply a group's product, values' scales the weights.  A code is an f16 number as it lies:
-// c in bits 0-3 is c 2^-24, in bits 4-7 c 2^-20, both below the smallest normal number, which the matrix
-// units take; so unpacking is a mask, and a shift for every second byte.  What a code stands for is
-// (mid - 8 step) + step c.  In sums over keys the two cancel in part, by a factor that grows with the root of the
-// keys' number: nothing next to a 16-bit result's rounding, but in f32 calls the codes have 8 taken off first
-// (1024 + c or 64 + c, by a mask, less 1032 or 72).  Queries go in as two f16 pieces (22 bits,
-// after a power of two that fits the row) in rows r and r + 8, which the lane that needs their sum holds both;
-// weights p_j step_j as two f16 pieces too, after a power of two that follows the largest step so far (so that
-// a weight is held to 2^-35 of the largest).  The product's 8 rows and columns hold up to 8 heads; where
-// there are at most 4, or 2, the free ones hold the weights' second pieces, and the other half of the groups, so
-// that a lane scales half of them.  Sums, maxima and the middles' part are f32.
+// The products are mma.sync m16n8k16 in f16: what is multiplied is 4-bit codes by at most 8 heads, so the
+// 128-row tensor-memory form would be empty for the most part.  They take codes and never see a scale: keys'
+// scales multiply a group's product, values' scales the weights.  The many go into the product's 16 rows (A:
+// 16 tokens of keys, 16 numbers of values), the heads into its 8 columns (B): 4 products a block and group for
+// the scores, 4 for the results.  Weights come out of the scores' product with a token a row and go into the
+// other with a token a row of B, which movmatrix turns them to.
+//
+// Codes become f16 in one of two ways.  As they lie: c in bits 0-3 is c 2^-24, in bits 4-7 c 2^-20, below the
+// smallest normal number, which the matrix units take whole, for a mask, and a shift for every second byte.  Or
+// centred, c - 8, from 1024 + c less 1032 and 64 + c less 72, an operation more.  Values' are centred: the matrix
+// units cut sums towards zero, and of numbers of one sign that is a bias, which the sums over many keys, that
+// cancel, would show (over 200,000 keys 8e-4 of the result).  Keys' codes as they lie cancel once, in a group's
+// product, which costs a score 4 bits of 24: taken for 16-bit queries, not for f32.
+//
+// Queries of 16-bit types go in as they are, of f32 as two f16 pieces (22 bits), after a power of two that fits
+// the row; the second pieces have products of their own.  Weights p_j step_j are two f16 pieces (22 bits) after
+// a power of two that follows the largest step so far, so that a weight is held to 2^-35 of the largest.
+// Columns are heads; where there are at most 4, the other columns are the weights' second pieces, for which there
+// is a second product else; where at most 2, columns are halves of the groups too, so that a lane scales half of
+// them.  Sums, maxima and the middles' part are f32.
 //
 // A warp works by itself: it streams pairs of blocks of 16 tokens (1,152 bytes a group of 64
 // each) through a ring of its own in shared memory with cp.async, and takes a range of one or
@@ -25,6 +32,12 @@
 // few (request, KV head) units are cut into pieces of up to 32 blocks for a CTA, whose warps join their
 // results in shared memory; else the units are laid end to end and every warp takes an even share
 // (joined in the CTA where all four are of one unit).  What cuts leave is joined by a second launch.
+//
+// What bounds it: instructions, not memory.  128 requests of 517 to 8,192 tokens, 16 heads over 8 of 128
+// numbers, bf16 (412 MB): 87 us, 4.7 TB/s of the 6.7 of a copy; counters at such a size: ALU pipe 58%, tensor 28%, DRAM 66%
+// busy.  2 requests of 131,075 and 200,000, 32 heads over 4 (191 MB): 59 us, 3.2 TB/s: 8 heads need the second
+// products.  64 chats of 97 to 3,025 in f32 (65 MB): 34 us, where ranges are 20 blocks and start, drain and join
+// weigh; 4 young requests: 8.3 us, the two launches and one range's chain of loads.
 //
 // Blocks outside the pool are zeros, tokens past the length have weight 0 whatever their
 // bytes are.
@@ -47,6 +60,8 @@ constexpr int kPiece = 8;       // blocks of a warp's part of a CTA's piece, at 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 5.f;    // weights stay below 2^kLazy of the followed maximum's
+// Beyond this a product's rounding (2^-24 of it) may not be left in the difference to the maximum.
+constexpr float kFar = 0x1p20f;
 constexpr int kSms = 152;
 constexpr float kLeastStep4 = 0x1p-100f;  // but for 0
 constexpr uint32_t kUnits = 10;           // steps times up stay below 2^kUnits, weights below 2^15
@@ -137,6 +152,7 @@ __device__ __forceinline__ Two unpack_f16(uint32_t x) {
   const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&x));
   return {y.x, y.y};
 }
+__device__ __forceinline__ float from_of(float m) { return m == -INFINITY ? 0.f : -m; }
 __device__ __forceinline__ float step_of(uint32_t scale) { return __uint_as_float(scale & 0xffff0000u); }
 __device__ __forceinline__ float mid_of(uint32_t scale) { return __uint_as_float(scale << 16); }
 // What a product's 0 stands for: mid, or (codes as they lie) mid - 8 step.
@@ -333,11 +349,12 @@ __device__ __forceinline__ void make_query(Query<G, R, F32>& q, const RawQuery<G
       }
   most = largest(most, __shfl_xor_sync(0xffffffffu, most, 1));
   most = largest(most, __shfl_xor_sync(0xffffffffu, most, 2));
-  // Numbers below 2^15; a row that is not finite has no scores.
+  // Numbers below 2^15; a row that is not finite, or whose units' factor is not, has no scores.
   constexpr int kOwn = Lane<G, R>::kOwn, kSlots = Lane<G, R>::kSlots;
   const int exp = (int)(__float_as_uint(most) >> 23 & 255);
   const float up = __uint_as_float((uint32_t)(min(14 - (exp - 127), 126) + 127) << 23);
-  const float scale = exp == 255 ? __uint_as_float(0x7fc00000u) : a.scale * kLog2e * (F32 ? 1.f : 0x1p24f) / up;
+  float scale = a.scale * kLog2e * (F32 ? 1.f : 0x1p24f) / up;
+  if (exp == 255 || !isfinite(scale)) scale = __uint_as_float(0x7fc00000u);
   float sums[kOwn] = {};
 #pragma unroll
   for (int g = 0; g < G; ++g) {
@@ -509,6 +526,7 @@ __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* roo
   float o_mid[kOwn][2];
   Two l = {0.f, 0.f};
   float m[2] = {-INFINITY, -INFINITY}, m_next[2] = {-INFINITY, -INFINITY};
+  bool far = false;      // one of them is, so that scores are rounded as the maximum was before it is taken off
   float up[kOwn];        // weights are p step up,
   uint32_t limit[kOwn];  // where steps are below this (their bits)
 #pragma unroll
@@ -557,7 +575,7 @@ __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* roo
       top[i] = fmaxf(s[0][0][i], s[0][1][i]);
 #pragma unroll
       for (int e = 1; e < kBoth; ++e) top[i] = fmaxf(top[i], fmaxf(s[e][0][i], s[e][1][i]));
-      top[i] *= q.scale[i];
+      top[i] = __fmul_rn(top[i], q.scale[i]);
     }
     bool follow = top[0] > m_next[0] || top[1] > m_next[1];
     uint32_t steps[kOwn];
@@ -577,9 +595,10 @@ __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* roo
         const float now = top[i] > m_next[i] ? fmaxf(m[i], top[i]) : m[i];
         by[i] = m[i] == -INFINITY ? 0.f : exp2_fast(m[i] - now);
         m[i] = now;
-        m_next[i] = now == -INFINITY ? now : now + kLazy;
+        m_next[i] = __fadd_rd(now, kLazy);  // (no more than kLazy also where that is less than a unit of m)
       }
       l = mul(l, {by[0], by[1]});
+      far = __any_sync(0xffffffffu, fabsf(from_of(m[0])) > kFar || fabsf(from_of(m[1])) > kFar);
 #pragma unroll
       for (int x = 0; x < kOwn; ++x) {
         uint32_t most = steps[x];
@@ -605,12 +624,17 @@ __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* roo
           }
       }
     }
-    const float from[2] = {m[0] == -INFINITY ? 0.f : -m[0], m[1] == -INFINITY ? 0.f : -m[1]};
+    const float from[2] = {from_of(m[0]), from_of(m[1])};
 #pragma unroll
     for (int e = 0; e < kBoth; ++e)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        fma({s[e][u][0], s[e][u][1]}, {q.scale[0], q.scale[1]}, {from[0], from[1]}).get(s[e][u][0], s[e][u][1]);
+        if (far) {
+          s[e][u][0] = __fadd_rn(__fmul_rn(s[e][u][0], q.scale[0]), from[0]);
+          s[e][u][1] = __fadd_rn(__fmul_rn(s[e][u][1], q.scale[1]), from[1]);
+        } else {
+          fma({s[e][u][0], s[e][u][1]}, {q.scale[0], q.scale[1]}, {from[0], from[1]}).get(s[e][u][0], s[e][u][1]);
+        }
         s[e][u][0] = exp2_fast(s[e][u][0]);
         s[e][u][1] = exp2_fast(s[e][u][1]);
         l = add(l, {s[e][u][0], s[e][u][1]});
@@ -623,7 +647,7 @@ __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* roo
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const uint32_t word = v_scales[e][x][u];
-          const float step = step_of(word), mid = middle<F32>(step, word), f = step * up[x];
+          const float mid = mid_of(word), f = step_of(word) * up[x];
           o_mid[x][0] = fmaf(s[e][u][0], mid, o_mid[x][0]);
           o_mid[x][1] = fmaf(s[e][u][1], mid, o_mid[x][1]);
           const float x0 = s[e][u][0] * f, x1 = s[e][u][1] * f;
@@ -643,7 +667,7 @@ __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* roo
 #pragma unroll
           for (int z = 0; z < 4; ++z) {
             const uint32_t wa = z & 1 ? va[z / 2] >> 8 : va[z / 2], wb = z & 1 ? vb[z / 2] >> 8 : vb[z / 2];
-            const uint32_t av[4] = {low<F32>(wa), high<F32>(wa), low<F32>(wb), high<F32>(wb)};
+            const uint32_t av[4] = {low<true>(wa), high<true>(wa), low<true>(wb), high<true>(wb)};
             mma_f16<false>(o[g][z], av, pb[0][0], pb[0][1]);
             if (!kColumns) mma_f16<false>(o[g][z], av, pb[1][0], pb[1][1]);
           }
@@ -690,7 +714,7 @@ __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* roo
       float y[8];
 #pragma unroll
       for (int z = 0; z < 8; ++z) {
-        y[z] = o[g][z / 2][i + 2 * (z & 1)] * (F32 ? down : z & 1 ? down * 0x1p20f : down * 0x1p24f);
+        y[z] = o[g][z / 2][i + 2 * (z & 1)] * down;
         if (kColumns) y[z] += __shfl_xor_sync(0xffffffffu, y[z], 2);  // the second pieces' columns
       }
       const int column = 2 * c + i, h = Lane<G, R>::head(column);

@@ -355,6 +355,54 @@ def test_long_requests(cuda_device, dtype, lens):
         _check(torch, ref, cache, slots, q, out, lse, heads, 1 / math.sqrt(d), dt)
 
 
+def test_many_keys_keep_their_digits(cuda_device):
+    """Over 200,000 keys that have nothing in common the result is 1/270 of a value, and sums of
+    one sign over that many would be 500 of it: what products cut off must not add up.  The
+    result's own rounding is 2^-11 of each number at most, and a third of that squared on average: all
+    errors together stay below 2^-11 if those of the sums are below 1.6 times the rounding's."""
+    torch, ref, nys = _mods()
+    dev, n, kv, d = cuda_device, 200000, 2, 128
+    g = torch.Generator(device=dev).manual_seed(21)
+    cache, table, slots = _cache(torch, nys, dev, g, [n], kv, d, d, 64, torch.float16)
+    k, v = (torch.empty((n, kv, d), device=dev) for _ in range(2))
+    nys.PagedKV4(*cache.data.shape[:1], 64, kv, d, d, device=dev, data=cache.data).read(slots[0].to(dev), k, v)
+    at = torch.tensor([n], dtype=torch.int32, device=dev)
+    for heads in (2, 4, 8, 16):
+        q = torch.randn((1, heads, d), generator=g, device=dev).half()
+        out = torch.empty_like(q)
+        nys.ExactAttention(heads, kv, d, d, dtype=torch.float16, device=dev).paged4(q, cache, at, table, out)
+        for h in range(heads):
+            j = h // (heads // kv)
+            p = (k[:, j].double() @ q[0, h].double() / math.sqrt(d)).softmax(0)
+            want = p @ v[:, j].double()
+            assert float((out[0, h].double() - want).norm() / want.norm()) <= 2.0 ** -11
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_large_queries(cuda_device, dtype):
+    """Scores whose size no longer fits are NaN, never a result that looks like one; up to
+    there the largest key wins."""
+    torch, ref, nys = _mods()
+    dt, dev = getattr(torch, dtype), cuda_device
+    g = torch.Generator(device=dev).manual_seed(3)
+    cache, table, _ = _cache(torch, nys, dev, g, [40], 1, 64, 64, 16, dt)
+    at = torch.tensor([40], dtype=torch.int32, device=dev)
+    k, v = (torch.empty((40, 1, 64), dtype=dt, device=dev) for _ in range(2))
+    cache.read(table[0].repeat_interleave(16)[:40].long() * 16 + torch.arange(40, device=dev) % 16, k, v)
+    att = nys.ExactAttention(1, 1, 64, 64, dtype=dt, device=dev, scale=1.0)
+    for sign in (1.0, -1.0):
+        for e in (60, 112, 118, 126):
+            q = torch.zeros((1, 1, 64), dtype=dt, device=dev)
+            q[..., 5] = sign * 2.0 ** e
+            out = att.paged4(q, cache, at, table, torch.empty_like(q))
+            if e <= 112:
+                assert torch.equal(out[0, 0], v[int((sign * k[:, 0, 5]).argmax()), 0])
+            elif dtype == "bfloat16":
+                assert bool(torch.isnan(out).all())
+            else:
+                assert bool(torch.isnan(out).all()) or torch.equal(out[0, 0], v[int((sign * k[:, 0, 5]).argmax()), 0])
+
+
 def test_wide_pool_offsets(cuda_device):
     """Pages whose bytes lie past 32 bits."""
     torch, ref, nys = _mods()
