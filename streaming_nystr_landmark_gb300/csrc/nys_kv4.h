@@ -15,9 +15,9 @@ namespace nys {
 // a code of 4 bits a number: value = middle + step * (code - 8).  Keys and values take
 // the groups of the wider of the two.  A page's tokens lie in blocks of 16, one KV
 // head's 16 tokens together: the unit that an attention warp copies and multiplies.
-// Its 32-bit words are in the order in which a warp's lanes need them for the products
-// of 8 x 16 x 16 (keys) and 16 x 16 x 8 (values), so that every read of shared memory is
-// one 16-byte word a lane, without conflicts:
+// Its 32-bit words are in the order in which a warp's lanes need them for products whose
+// 16 rows are the block's tokens (keys) or 16 of a group's numbers (values), so that
+// every read of shared memory is one 16-byte word a lane, without conflicts:
 //   keys' codes    [group][token % 8][c][token / 8][h]   of numbers 64 group + 32 h + 8 c ..
 //   values' codes  [group][r][token % 8 / 2][token / 8][token % 2]    64 group + 8 r ..
 //   keys' scales, values' scales  [group][token % 8 / 2][token / 8][token % 2]
@@ -44,7 +44,8 @@ __device__ __forceinline__ int value_word4(int g, int t, int x) {
   return g * 128 + x * 16 + place4(t);
 }
 
-// Two f32 operations an instruction, each rounded as its own.
+// Two f32 operations an instruction.  (A product and a sum that takes it may become one
+// operation, rounded once, by measurement: where both roundings count, they are scalar.)
 struct Two {
   uint64_t w;
   __device__ __forceinline__ Two() {}
