@@ -614,8 +614,7 @@ int nys_attn4_workspace_bytes(const nys_attn_config* cfg, int64_t n, int64_t key
  * fp32.  A request without keys gets 0 (lse -INF).  Pages outside the pool count as
  * keys and values of 0 (NYS_ATTN_BAD_PAGE), lengths are taken clamped into their
  * table (NYS_ATTN_BAD_LENGTH); entries past a length are not read.  A query row
- * that is not finite, or whose largest number times the scale is 2^116 or more,
- * gives NaN.
+ * that is not finite, or whose scores pass fp32, gives NaN.
  * first, first_lse (both or neither): the result [n][heads][dv] and log-sums
  * [n][heads] of the same queries over other keys (a shared prefix,
  * nys_attn_shared), which are joined in; first may be out itself, and first_lse

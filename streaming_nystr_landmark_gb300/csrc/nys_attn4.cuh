@@ -12,12 +12,12 @@
 // the scores, 4 for the results.  Weights come out of the scores' product with a token a row and go into the
 // other with a token a row of B, which movmatrix turns them to.
 //
-// Codes become f16 in one of two ways.  As they lie: c in bits 0-3 is c 2^-24, in bits 4-7 c 2^-20, below the
-// smallest normal number, which the matrix units take whole, for a mask, and a shift for every second byte.  Or
-// centred, c - 8, from 1024 + c less 1032 and 64 + c less 72, an operation more.  Values' are centred: the matrix
-// units cut sums towards zero, and of numbers of one sign that is a bias, which the sums over many keys, that
-// cancel, would show (over 200,000 keys 8e-4 of the result).  Keys' codes as they lie cancel once, in a group's
-// product, which costs a score 4 bits of 24: taken for 16-bit queries, not for f32.
+// Codes become f16 centred: c - 8, from 1024 + c less 1032 (bits 0-3) and 64 + c less 72 (bits 4-7), a mask and a
+// difference for two, and a shift for every second byte.  As they lie they are numbers too, c 2^-24 and c 2^-20,
+// below the smallest normal one, which the matrix units take; that was 5% faster (128 requests as below: 87 us,
+// with values as they lie too 82).  But the units cut sums towards zero: sums of one sign over many
+// values show it (over 200,000 keys 8e-4 of the result), and scores of such small numbers are off by 2e-6 of
+// the row instead of 1e-7.
 //
 // Queries of 16-bit types go in as they are, of f32 as two f16 pieces (22 bits), after a power of two that fits
 // the row; the second pieces have products of their own.  Weights p_j step_j are two f16 pieces (22 bits) after
@@ -34,10 +34,10 @@
 // (joined in the CTA where all four are of one unit).  What cuts leave is joined by a second launch.
 //
 // What bounds it: instructions, not memory.  128 requests of 517 to 8,192 tokens, 16 heads over 8 of 128
-// numbers, bf16 (412 MB): 87 us, 4.7 TB/s of the 6.7 of a copy; counters at such a size: ALU pipe 58%, tensor 28%, DRAM 66%
-// busy.  2 requests of 131,075 and 200,000, 32 heads over 4 (191 MB): 59 us, 3.2 TB/s: 8 heads need the second
+// numbers, bf16 (412 MB): 91 us, 4.5 TB/s of the 6.7 of a copy; counters at such a size: ALU pipe 58%, tensor 28%, DRAM 66%
+// busy.  2 requests of 131,075 and 200,000, 32 heads over 4 (191 MB): 60 us, 3.2 TB/s: 8 heads need the second
 // products.  64 chats of 97 to 3,025 in f32 (65 MB): 34 us, where ranges are 20 blocks and start, drain and join
-// weigh; 4 young requests: 8.3 us, the two launches and one range's chain of loads.
+// weigh; 4 young requests: 8.5 us, a launch and one range's chain of loads.
 //
 // Blocks outside the pool are zeros, tokens past the length have weight 0 whatever their
 // bytes are.
@@ -134,16 +134,10 @@ __device__ __forceinline__ uint32_t centred(uint32_t x, uint32_t mask, uint32_t 
   const __half2 z = __hsub2(*reinterpret_cast<const __half2*>(&y), __half2half2(__ushort_as_half(less)));
   return *reinterpret_cast<const uint32_t*>(&z);
 }
-// The two codes at bits 0-3, and at bits 4-7, of the halves as f16: as they lie, times 2^-24 and 2^-20; or
-// (Centred) code - 8, from 1024 + code less 1032, and 64 + code less 72.
-template <bool Centred>
-__device__ __forceinline__ uint32_t low(uint32_t x) {
-  return Centred ? centred(x, 0x000f000fu, 0x64006400u, 0x6408) : x & 0x000f000fu;
-}
-template <bool Centred>
-__device__ __forceinline__ uint32_t high(uint32_t x) {
-  return Centred ? centred(x, 0x00f000f0u, 0x54005400u, 0x5480) : x & 0x00f000f0u;
-}
+// The two codes at bits 0-3, and at bits 4-7, of the halves as f16, less 8: from 1024 + code less 1032, and
+// 64 + code less 72.
+__device__ __forceinline__ uint32_t low(uint32_t x) { return centred(x, 0x000f000fu, 0x64006400u, 0x6408); }
+__device__ __forceinline__ uint32_t high(uint32_t x) { return centred(x, 0x00f000f0u, 0x54005400u, 0x5480); }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 z = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&z);
@@ -155,11 +149,6 @@ __device__ __forceinline__ Two unpack_f16(uint32_t x) {
 __device__ __forceinline__ float from_of(float m) { return m == -INFINITY ? 0.f : -m; }
 __device__ __forceinline__ float step_of(uint32_t scale) { return __uint_as_float(scale & 0xffff0000u); }
 __device__ __forceinline__ float mid_of(uint32_t scale) { return __uint_as_float(scale << 16); }
-// What a product's 0 stands for: mid, or (codes as they lie) mid - 8 step.
-template <bool Centred>
-__device__ __forceinline__ float middle(float step, uint32_t word) {
-  return Centred ? mid_of(word) : fmaf(step, -8.f, mid_of(word));
-}
 
 __device__ __forceinline__ float read_as(const void* p, int64_t i, int dtype) {
   return dtype == NYS_F32    ? static_cast<const float*>(p)[i]
@@ -353,7 +342,7 @@ __device__ __forceinline__ void make_query(Query<G, R, F32>& q, const RawQuery<G
   constexpr int kOwn = Lane<G, R>::kOwn, kSlots = Lane<G, R>::kSlots;
   const int exp = (int)(__float_as_uint(most) >> 23 & 255);
   const float up = __uint_as_float((uint32_t)(min(14 - (exp - 127), 126) + 127) << 23);
-  float scale = a.scale * kLog2e * (F32 ? 1.f : 0x1p24f) / up;
+  float scale = a.scale * kLog2e / up;
   if (exp == 255 || !isfinite(scale)) scale = __uint_as_float(0x7fc00000u);
   float sums[kOwn] = {};
 #pragma unroll
@@ -372,8 +361,7 @@ __device__ __forceinline__ void make_query(Query<G, R, F32>& q, const RawQuery<G
       for (int s = 0; s < 2; ++s)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float f = F32 || i == 0 ? 1.f : 0.0625f;  // the codes' 2^-24 and 2^-20
-          q.b[g][e][s][i] = pack_f16(y[2 * s + i] * f, y[2 * s + i + 4] * f);
+          q.b[g][e][s][i] = pack_f16(y[2 * s + i], y[2 * s + i + 4]);
           if (F32) q.b[g][e][s][F32 ? 2 + i : 0] = pack_f16(low[2 * s + i], low[2 * s + i + 4]);
         }
     }
@@ -382,7 +370,6 @@ __device__ __forceinline__ void make_query(Query<G, R, F32>& q, const RawQuery<G
   for (int o = 0; o < kOwn; ++o) {
     sums[o] += __shfl_xor_sync(0xffffffffu, sums[o], 1);
     sums[o] += __shfl_xor_sync(0xffffffffu, sums[o], 2);
-    if (!F32) sums[o] *= 0x1p-24f;
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {  // from the columns' lanes
@@ -418,7 +405,7 @@ __device__ __forceinline__ void scores(const Query<G, R, F32>& q, const unsigned
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
           const uint32_t y0 = z ? words[e][0] >> 8 : words[e][0], y1 = z ? words[e][1] >> 8 : words[e][1];
-          const uint32_t av[4] = {low<F32>(y0), low<F32>(y1), high<F32>(y0), high<F32>(y1)};
+          const uint32_t av[4] = {low(y0), low(y1), high(y0), high(y1)};
           if (x == 0 && e == 0 && z == 0) {
             mma_f16<true>(acc, av, q.b[g][e][z][0], q.b[g][e][z][1]);
             if (F32) mma_f16<true>(low_acc, av, q.b[g][e][z][F32 ? 2 : 0], q.b[g][e][z][F32 ? 3 : 0]);
@@ -433,7 +420,7 @@ __device__ __forceinline__ void scores(const Query<G, R, F32>& q, const unsigned
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const uint32_t word = scale_at(at + key_scales4(G), g, r, t);
-      const float step = step_of(word), mid = middle<F32>(step, word);
+      const float step = step_of(word), mid = mid_of(word);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float dot = F32 ? fmaf(low_acc[2 * t + i], 0x1p-11f, acc[2 * t + i]) : acc[2 * t + i];
@@ -667,7 +654,7 @@ __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* roo
 #pragma unroll
           for (int z = 0; z < 4; ++z) {
             const uint32_t wa = z & 1 ? va[z / 2] >> 8 : va[z / 2], wb = z & 1 ? vb[z / 2] >> 8 : vb[z / 2];
-            const uint32_t av[4] = {low<true>(wa), high<true>(wa), low<true>(wb), high<true>(wb)};
+            const uint32_t av[4] = {low(wa), high(wa), low(wb), high(wb)};
             mma_f16<false>(o[g][z], av, pb[0][0], pb[0][1]);
             if (!kColumns) mma_f16<false>(o[g][z], av, pb[1][0], pb[1][1]);
           }
