@@ -34,7 +34,7 @@
 // (joined in the CTA where all four are of one unit).  What cuts leave is joined by a second launch.
 //
 // What bounds it: instructions, not memory.  128 requests of 517 to 8,192 tokens, 16 heads over 8 of 128
-// numbers, bf16 (412 MB): 91 us, 4.5 TB/s of the 6.7 of a copy; counters at such a size: ALU pipe 58%, tensor 28%, DRAM 66%
+// numbers, bf16 (412 MB): 91 us, 4.5 TB/s of the 6.7 of a copy; counters at such a size: ALU pipe 53%, tensor 25%, DRAM 60%
 // busy.  2 requests of 131,075 and 200,000, 32 heads over 4 (191 MB): 60 us, 3.2 TB/s: 8 heads need the second
 // products.  64 chats of 97 to 3,025 in f32 (65 MB): 34 us, where ranges are 20 blocks and start, drain and join
 // weigh; 4 young requests: 8.5 us, a launch and one range's chain of loads.
