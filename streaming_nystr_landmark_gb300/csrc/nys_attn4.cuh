@@ -12,12 +12,15 @@
 // the scores, 4 for the results.  Weights come out of the scores' product with a token a row and go into the
 // other with a token a row of B, which movmatrix turns them to.
 //
-// Codes become f16 centred: c - 8, from 1024 + c less 1032 (bits 0-3) and 64 + c less 72 (bits 4-7), a mask and a
-// difference for two, and a shift for every second byte.  As they lie they are numbers too, c 2^-24 and c 2^-20,
-// below the smallest normal one, which the matrix units take; that was 5% faster (128 requests as below: 87 us,
-// with values as they lie too 82).  But the units cut sums towards zero: sums of one sign over many
-// values show it (over 200,000 keys 8e-4 of the result), and scores of such small numbers are off by 2e-6 of
-// the row instead of 1e-7.
+// Codes become f16 centred: keys' as c - 8, from 1024 + c less 1032 (bits 0-3) and 64 + c less 72 (bits 4-7),
+// a mask and a difference for two, and a shift for every second byte; values' as 2c - 15, in the same way after a
+// shift for every byte.  As they lie they are numbers too, c 2^-24 and c 2^-20, below the smallest normal one,
+// which the matrix units take, and faster (128 requests as below: 8 us of 95).  But the units cut every sum
+// towards zero, and scores of such small numbers are off by 2e-6 of the row instead of 1e-7.  Sums of one sign
+// over very many values show the cuts, because the result is small beside them: of codes as they lie 8e-4 of the
+// result over 200,000 keys, of c - 8, which is -1/2 on average, 3e-5.  So values' codes have a mean of 0, as far as
+// numbers lie evenly about a group's middle, and the products' sums end after 32 tokens, where f32 additions take
+// them: 2e-7, as elsewhere (the two long requests as below: 60.2 -> 61.8 us; with c - 8 61.4 and 2e-6).
 //
 // Queries of 16-bit types go in as they are, of f32 as two f16 pieces (22 bits), after a power of two that fits
 // the row; the second pieces have products of their own.  Weights p_j step_j are two f16 pieces (22 bits) after
@@ -64,7 +67,7 @@ constexpr float kLazy = 5.f;    // weights stay below 2^kLazy of the followed ma
 constexpr float kFar = 0x1p20f;
 constexpr int kSms = 152;
 constexpr float kLeastStep4 = 0x1p-100f;  // but for 0
-constexpr uint32_t kUnits = 10;           // steps times up stay below 2^kUnits, weights below 2^15
+constexpr uint32_t kUnits = 11;           // steps times up stay below 2^kUnits, weights (half of that) below 2^15
 
 constexpr int kBoth = 2;        // blocks that are multiplied together: 32 tokens
 
@@ -113,10 +116,9 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// c = a b (First) or c + a b.
-template <bool First>
-__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  if (First)
+// c = a b (first) or c + a b; first is known where loops are unrolled.
+__device__ __forceinline__ void mma_f16(bool first, float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (first)
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
         "{%10,%10,%10,%10};"
         : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
@@ -138,6 +140,9 @@ __device__ __forceinline__ uint32_t centred(uint32_t x, uint32_t mask, uint32_t 
 // 64 + code less 72.
 __device__ __forceinline__ uint32_t low(uint32_t x) { return centred(x, 0x000f000fu, 0x64006400u, 0x6408); }
 __device__ __forceinline__ uint32_t high(uint32_t x) { return centred(x, 0x00f000f0u, 0x54005400u, 0x5480); }
+// Those of bits 1-4, and 5-8, less 7.5 and times 2: from 1024 + 2 code less 1039, and 64 + 2 code less 79.
+__device__ __forceinline__ uint32_t twice_low(uint32_t x) { return centred(x, 0x001e001eu, 0x64006400u, 0x640f); }
+__device__ __forceinline__ uint32_t twice_high(uint32_t x) { return centred(x, 0x01e001e0u, 0x54005400u, 0x54f0); }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 z = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&z);
@@ -406,13 +411,9 @@ __device__ __forceinline__ void scores(const Query<G, R, F32>& q, const unsigned
         for (int z = 0; z < 2; ++z) {
           const uint32_t y0 = z ? words[e][0] >> 8 : words[e][0], y1 = z ? words[e][1] >> 8 : words[e][1];
           const uint32_t av[4] = {low(y0), low(y1), high(y0), high(y1)};
-          if (x == 0 && e == 0 && z == 0) {
-            mma_f16<true>(acc, av, q.b[g][e][z][0], q.b[g][e][z][1]);
-            if (F32) mma_f16<true>(low_acc, av, q.b[g][e][z][F32 ? 2 : 0], q.b[g][e][z][F32 ? 3 : 0]);
-          } else {
-            mma_f16<false>(acc, av, q.b[g][e][z][0], q.b[g][e][z][1]);
-            if (F32) mma_f16<false>(low_acc, av, q.b[g][e][z][F32 ? 2 : 0], q.b[g][e][z][F32 ? 3 : 0]);
-          }
+          const bool first = x == 0 && e == 0 && z == 0;
+          mma_f16(first, acc, av, q.b[g][e][z][0], q.b[g][e][z][1]);
+          if (F32) mma_f16(first, low_acc, av, q.b[g][e][z][F32 ? 2 : 0], q.b[g][e][z][F32 ? 3 : 0]);
         }
     }
     // (A last group that there is not: the column is 0, any scales do.)
@@ -514,7 +515,7 @@ __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* roo
   Two l = {0.f, 0.f};
   float m[2] = {-INFINITY, -INFINITY}, m_next[2] = {-INFINITY, -INFINITY};
   bool far = false;      // one of them is, so that scores are rounded as the maximum was before it is taken off
-  float up[kOwn];        // weights are p step up,
+  float up[kOwn];        // weights are p step up / 2,
   uint32_t limit[kOwn];  // where steps are below this (their bits)
 #pragma unroll
   for (int x = 0; x < kOwn; ++x) {
@@ -627,14 +628,15 @@ __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* roo
         l = add(l, {s[e][u][0], s[e][u][1]});
       }
 #pragma unroll
-    for (int e = 0; e < kBoth; ++e)
+    for (int x = 0; x < kOwn; ++x) {
+      uint32_t pb[kBoth][2][2];
 #pragma unroll
-      for (int x = 0; x < kOwn; ++x) {
-        uint32_t pb[2][2];
+      for (int e = 0; e < kBoth; ++e)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const uint32_t word = v_scales[e][x][u];
-          const float mid = mid_of(word), f = step_of(word) * up[x];
+          // Of codes less 7.5, for which the middle is half a step lower.
+          const float mid = fmaf(-0.5f, step_of(word), mid_of(word)), f = step_of(word) * (0.5f * up[x]);
           o_mid[x][0] = fmaf(s[e][u][0], mid, o_mid[x][0]);
           o_mid[x][1] = fmaf(s[e][u][1], mid, o_mid[x][1]);
           const float x0 = s[e][u][0] * f, x1 = s[e][u][1] * f;
@@ -643,23 +645,34 @@ __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* roo
           const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&y));
           const uint32_t second = pack_f16(x0 - z.x, x1 - z.y);
           if (kColumns) y = c >= 2 ? second : y;
-          pb[0][u] = turned(y);
-          if (!kColumns) pb[1][u] = turned(second);
+          pb[e][0][u] = turned(y);
+          if (!kColumns) pb[e][1][u] = turned(second);
         }
 #pragma unroll
-        for (int g = x * kSlots; g < x * kSlots + kSlots && g < G; ++g) {
+      for (int g = x * kSlots; g < x * kSlots + kSlots && g < G; ++g) {
+        float acc[4][4];
+#pragma unroll
+        for (int e = 0; e < kBoth; ++e) {
           const uint4 v = lds128(at + e * kBytes + values4(G) + g * 512 + lane * 16);
           const uint32_t va[2] = {__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632)};
           const uint32_t vb[2] = {__byte_perm(v.z, v.w, 0x5410), __byte_perm(v.z, v.w, 0x7632)};
 #pragma unroll
           for (int z = 0; z < 4; ++z) {
-            const uint32_t wa = z & 1 ? va[z / 2] >> 8 : va[z / 2], wb = z & 1 ? vb[z / 2] >> 8 : vb[z / 2];
-            const uint32_t av[4] = {low(wa), high(wa), low(wb), high(wb)};
-            mma_f16<false>(o[g][z], av, pb[0][0], pb[0][1]);
-            if (!kColumns) mma_f16<false>(o[g][z], av, pb[1][0], pb[1][1]);
+            const uint32_t wa = z & 1 ? va[z / 2] >> 7 : va[z / 2] << 1, wb = z & 1 ? vb[z / 2] >> 7 : vb[z / 2] << 1;
+            const uint32_t av[4] = {twice_low(wa), twice_high(wa), twice_low(wb), twice_high(wb)};
+            // (Second pieces first: what is cut goes by the sum so far.)
+            if (!kColumns) mma_f16(e == 0, acc[z], av, pb[e][1][0], pb[e][1][1]);
+            mma_f16(kColumns && e == 0, acc[z], av, pb[e][0][0], pb[e][0][1]);
           }
         }
+        // (Added up here, rounded to the nearest, not by the products.)
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+#pragma unroll
+          for (int i = 0; i < 4; i += 2)
+            add({o[g][z][i], o[g][z][i + 1]}, {acc[z][i], acc[z][i + 1]}).get(o[g][z][i], o[g][z][i + 1]);
       }
+    }
     __syncwarp();
     fetch(ring + (stage == 0 ? kStages - 1 : stage - 1) * kStage);
     stage = stage == kStages - 1 ? 0 : stage + 1;

@@ -1,0 +1,59 @@
+"""Attention over the 4-bit cache where a request, a row or a scale is unusual: what the
+header says comes out, by whichever way the call takes."""
+import math
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = ["float32", "bfloat16", "float16"]
+# heads, kv_heads, d, dv: 1 to 2, 3 to 4 and 5 to 8 heads a KV head, and more; 1 to 4 groups
+GEOMETRIES = [(16, 8, 128, 128), (4, 1, 64, 64), (32, 4, 128, 96), (20, 2, 192, 192), (2, 1, 256, 256)]
+
+
+def _mods():
+    import torch
+    import kv4_reference as ref
+    from streaming_nystr_landmark_gb300 import nys
+    return torch, ref, nys
+
+
+def _made(torch, nys, dev, lens, geo, dt, scale=None, seed=3):
+    from test_gpu_kv4 import _cache
+    heads, kv, d, dv = geo
+    g = torch.Generator(device=dev).manual_seed(seed)
+    cache, table, slots = _cache(torch, nys, dev, g, lens, kv, d, dv, 16, dt)
+    q = torch.randn((len(lens), heads, d), generator=g, device=dev).to(dt)
+    at = torch.tensor(lens, dtype=torch.int32, device=dev)
+    att = nys.ExactAttention(heads, kv, d, dv, dtype=dt, device=dev, scale=scale)
+    out = torch.full((len(lens), heads, dv), 7.0, dtype=dt, device=dev)
+    lse = torch.full((len(lens), heads), 7.0, device=dev)
+    return cache, table, slots, q, at, att, out, lse
+
+
+@pytest.mark.parametrize("heads", [8, 16, 32, 64])
+def test_many_keys_in_f32(cuda_device, heads):
+    """Over 400,000 keys that have nothing in common the result is 1/630 of a value's size, and
+    the codes less 8, of -1/2 on average, are sums of one sign.  The matrix units cut every sum
+    towards zero, by up to 2^-23 of it, half that on average: in at most 4 products over 32
+    tokens, whose sum is 16 steps in the end and half of that on the way, 2 * 2^-24 * 16 steps of
+    0.32 of a value's size for 32 tokens, or 0.32 * 2^-24 of it for one; times 630, 1.2e-5."""
+    torch, ref, nys = _mods()
+    dev, n, kv, d = cuda_device, 400000, 8, 128
+    g = torch.Generator(device=dev).manual_seed(23)
+    cache = nys.PagedKV4(n // 64, 64, kv, d, d, device=dev)
+    every = torch.arange(n, device=dev)
+    k, v = (torch.randn((n, kv, d), generator=g, device=dev) for _ in range(2))
+    cache.write(k, v, every)
+    cache.read(every, k, v)
+    at = torch.tensor([n], dtype=torch.int32, device=dev)
+    table = torch.randperm(n // 64, generator=g, device=dev).int()[None]
+    q = torch.randn((1, heads, d), generator=g, device=dev)
+    out = torch.empty_like(q)
+    nys.ExactAttention(heads, kv, d, d, device=dev).paged4(q, cache, at, table, out)
+    want = torch.empty((heads, d), dtype=torch.float64, device=dev)
+    for j in range(kv):
+        kj, vj = k[:, j].double(), v[:, j].double()
+        for h in range(j * heads // kv, (j + 1) * heads // kv):
+            want[h] = (kj @ q[0, h].double() / math.sqrt(d)).softmax(0) @ vj
+    assert float((out[0].double() - want).norm() / want.norm()) <= 2.0 ** -16
