@@ -611,7 +611,7 @@ int nys_attn4_workspace_bytes(const nys_attn_config* cfg, int64_t n, int64_t key
  * exactly the values they stand for.  Scores take queries of 16-bit types as they
  * are (to 2^-39 of the row's largest number), fp32 ones to 22 bits; weights are
  * held to 22 bits for the second product (to 2^-35 of the largest); sums run in
- * fp32.  A request without keys gets 0 (lse -INF).  Pages outside the pool count as
+ * fp32.  A request without keys gets 0 (lse -INF), whatever its query row holds.  Pages outside the pool count as
  * keys and values of 0 (NYS_ATTN_BAD_PAGE), lengths are taken clamped into their
  * table (NYS_ATTN_BAD_LENGTH); entries past a length are not read.  A query row
  * that is not finite, or whose scores pass fp32, gives NaN.

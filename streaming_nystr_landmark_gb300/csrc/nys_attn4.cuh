@@ -470,9 +470,11 @@ __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* roo
   const uint32_t ring = tc::sptr(room);
   const int len = len_of(a, b, false);
   const int n_heads = min(kHeads, a.group - h0);
+  // Without keys the rows count as 0: what is no number in them would meet the masked scores.
+  const int q_heads = len > 0 ? n_heads : 0;
 
   RawQuery<G, R> raw;
-  load_query(raw, a, b, kvh * a.group + h0, n_heads);
+  load_query(raw, a, b, kvh * a.group + h0, q_heads);
 
   // The next block's page is looked up one block ahead; blocks that there are none of are zeros.  (A
   // request without keys has no table to look into.)
@@ -505,7 +507,7 @@ __device__ __forceinline__ void run_range(const Attn4Args& a, unsigned char* roo
   for (int i = 0; i < kStages - 1; ++i) fetch(ring + i * kStage);
 
   Query<G, R, F32> q;
-  make_query<G, R, F32>(q, raw, a, n_heads, reinterpret_cast<float*>(room + (kStages - 1) * kStage));
+  make_query<G, R, F32>(q, raw, a, q_heads, reinterpret_cast<float*>(room + (kStages - 1) * kStage));
 
   // Results: numbers 64 g + 8 r + 2 x (elements 2, 3: and one more) by columns 2c, 2c + 1 of the
   // product.  For each of the two columns: the maximum, from where on it is followed, and this lane's tokens'

@@ -57,3 +57,27 @@ def test_many_keys_in_f32(cuda_device, heads):
         for h in range(j * heads // kv, (j + 1) * heads // kv):
             want[h] = (kj @ q[0, h].double() / math.sqrt(d)).softmax(0) @ vj
     assert float((out[0].double() - want).norm() / want.norm()) <= 2.0 ** -16
+
+
+@pytest.mark.parametrize("geo", GEOMETRIES)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("long", [33, 2500])
+def test_no_keys_whatever_the_query(cuda_device, dtype, geo, long):
+    """Places of a batch that hold no request: their query rows may be anything."""
+    torch, ref, nys = _mods()
+    dt = getattr(torch, dtype)
+    lens = [0, long, 0, 17, 0]
+    cache, table, slots, q, at, att, out, lse = _made(torch, nys, cuda_device, lens, geo, dt)
+    clean = att.paged4(q, cache, at, table, out.clone())
+    q[0], q[2, -1], q[4, :, 1] = math.nan, math.inf, -math.inf
+    att.paged4(q, cache, at, table, out, lse=lse)
+    for i in (0, 2, 4):
+        assert not bool(out[i].any()) and bool((lse[i] == -math.inf).all())
+    for i in (1, 3):
+        assert torch.equal(out[i], clean[i]) and bool(lse[i].isfinite().all())
+    first, first_lse = torch.randn_like(out), torch.randn_like(lse)
+    att.paged4(q, cache, at, table, out, first=first, first_lse=first_lse, lse=lse)
+    for i in (0, 2, 4):
+        # By a factor of 1 and, for the log-sum, to base 2 and back: two roundings and two functions.
+        assert torch.equal(out[i], first[i])
+        assert bool(((lse[i] - first_lse[i]).abs() <= 8 * ref.U * first_lse[i].abs()).all())
