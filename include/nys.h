@@ -609,12 +609,14 @@ int nys_attn4_workspace_bytes(const nys_attn_config* cfg, int64_t n, int64_t key
 /* One token of attention for n requests over their keys in a 4-bit cache: query
  * row b of q sees the lens[b] tokens in pages table[b * width + 0 ..], taken as
  * exactly the values they stand for.  Scores take queries of 16-bit types as they
- * are (to 2^-39 of the row's largest number), fp32 ones to 22 bits; weights are
- * held to 22 bits for the second product (to 2^-35 of the largest); sums run in
- * fp32.  A request without keys gets 0 (lse -INF), whatever its query row holds.  Pages outside the pool count as
- * keys and values of 0 (NYS_ATTN_BAD_PAGE), lengths are taken clamped into their
- * table (NYS_ATTN_BAD_LENGTH); entries past a length are not read.  A query row
- * that is not finite, or whose scores pass fp32, gives NaN.
+ * are (to 2^-39 of the row's largest number, or 2^-150 / scale where that is more),
+ * fp32 ones to 22 bits; weights are held to 22 bits for the second product (to 2^-35
+ * of the largest); sums run in fp32.  A request without keys gets 0 (lse -INF), whatever
+ * its query row holds.  Pages outside the pool count as keys and values of 0
+ * (NYS_ATTN_BAD_PAGE), lengths are taken clamped into their table (NYS_ATTN_BAD_LENGTH);
+ * entries past a length are not read.  A query row that is not finite, or whose scores
+ * pass fp32, gives NaN; rows are multiplied with their largest number brought to 2^14, so
+ * that scores over keys of 2^100 and more may pass it sooner than their own size does.
  * first, first_lse (both or neither): the result [n][heads][dv] and log-sums
  * [n][heads] of the same queries over other keys (a shared prefix,
  * nys_attn_shared), which are joined in; first may be out itself, and first_lse

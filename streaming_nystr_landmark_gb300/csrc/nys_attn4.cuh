@@ -343,11 +343,14 @@ __device__ __forceinline__ void make_query(Query<G, R, F32>& q, const RawQuery<G
       }
   most = largest(most, __shfl_xor_sync(0xffffffffu, most, 1));
   most = largest(most, __shfl_xor_sync(0xffffffffu, most, 2));
-  // Numbers below 2^15; a row that is not finite, or whose units' factor is not, has no scores.
+  // Numbers below 2^15, and a scale that is no subnormal number (of 0 it would make NaN of masked scores); a row
+  // that is not finite, or whose units' factor is not, has no scores.
   constexpr int kOwn = Lane<G, R>::kOwn, kSlots = Lane<G, R>::kSlots;
   const int exp = (int)(__float_as_uint(most) >> 23 & 255);
-  const float up = __uint_as_float((uint32_t)(min(14 - (exp - 127), 126) + 127) << 23);
-  float scale = a.scale * kLog2e / up;
+  const float to_two = a.scale * kLog2e;
+  const int fit = min(126, isfinite(to_two) ? 126 + ilogbf(to_two) : 126);
+  const float up = __uint_as_float((uint32_t)(min(14 - (exp - 127), fit) + 127) << 23);
+  float scale = to_two / up;
   if (exp == 255 || !isfinite(scale)) scale = __uint_as_float(0x7fc00000u);
   float sums[kOwn] = {};
 #pragma unroll

@@ -81,3 +81,20 @@ def test_no_keys_whatever_the_query(cuda_device, dtype, geo, long):
         # By a factor of 1 and, for the log-sum, to base 2 and back: two roundings and two functions.
         assert torch.equal(out[i], first[i])
         assert bool(((lse[i] - first_lse[i]).abs() <= 8 * ref.U * first_lse[i].abs()).all())
+
+
+@pytest.mark.parametrize("geo", GEOMETRIES)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("scale", [1e-8, 1e-30, 1e-44])
+def test_small_scales(cuda_device, dtype, geo, scale):
+    """Scores that a scale or a query row of zeros makes small leave the values' mean, in
+    requests that end inside a pair of blocks too."""
+    from test_gpu_kv4 import _check
+    torch, ref, nys = _mods()
+    dt, lens = getattr(torch, dtype), [40, 33, 5, 2500]
+    cache, table, slots, q, at, att, out, lse = _made(torch, nys, cuda_device, lens, geo, dt, scale)
+    q[0] = 0
+    q[1] *= 1e-4
+    q[2, 0] = 0
+    att.paged4(q, cache, at, table, out, lse=lse)
+    _check(torch, ref, cache, slots, q, out, lse, geo[0], scale, dt)
