@@ -228,7 +228,8 @@ __device__ __forceinline__ float first_sum(const Attn4Args& a, int b, int h) {
 }
 __device__ __forceinline__ Joint join_first(float wide, float m, float l) {
   const float top = fmaxf(m, wide);
-  if (top == -INFINITY && l == 0.f) return {0.f, 0.f, -INFINITY};
+  // (The maximum passes over a log-sum of NaN, which has to arrive.)
+  if (m == -INFINITY && wide == -INFINITY && l == 0.f) return {0.f, 0.f, -INFINITY};
   const float mine = m == -INFINITY ? 0.f : exp2f(m - top);
   const float other = wide == -INFINITY ? 0.f : exp2f(wide - top);
   const float sum = l * mine + other;

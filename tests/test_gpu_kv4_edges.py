@@ -98,3 +98,19 @@ def test_small_scales(cuda_device, dtype, geo, scale):
     q[2, 0] = 0
     att.paged4(q, cache, at, table, out, lse=lse)
     _check(torch, ref, cache, slots, q, out, lse, geo[0], scale, dt)
+
+
+@pytest.mark.parametrize("geo", GEOMETRIES)
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_a_first_result_that_is_nan(cuda_device, dtype, geo):
+    """NaN in the log-sum of what is joined in reaches the result, of a request without keys too."""
+    torch, ref, nys = _mods()
+    dt, lens = getattr(torch, dtype), [0, 40, 2500, 0]
+    cache, table, slots, q, at, att, out, lse = _made(torch, nys, cuda_device, lens, geo, dt)
+    first, first_lse = torch.randn_like(out), torch.randn_like(lse)
+    first[:3, 0], first_lse[:3, 0] = math.nan, math.nan
+    for o, s in ((out, lse), (first, first_lse)):      # apart, and in place
+        att.paged4(q, cache, at, table, o, first=first, first_lse=first_lse, lse=s)
+        assert bool(o[:3, 0].isnan().all()) and bool(s[:3, 0].isnan().all())
+        assert not bool(o[:, 1:].isnan().any()) and not bool(s[:, 1:].isnan().any())
+        assert not bool(o[3].isnan().any()) and not bool(s[3].isnan().any())
