@@ -615,7 +615,8 @@ int nys_attn4_workspace_bytes(const nys_attn_config* cfg, int64_t n, int64_t key
  * its query row holds.  Pages outside the pool count as keys and values of 0
  * (NYS_ATTN_BAD_PAGE), lengths are taken clamped into their table (NYS_ATTN_BAD_LENGTH);
  * entries past a length are not read.  A query row that is not finite, or whose scores
- * pass fp32, gives NaN; rows are multiplied with their largest number brought to 2^14, so
+ * pass fp32, gives NaN (scores below fp32 beside others, or beside a result that is
+ * joined in, weigh nothing); rows are multiplied with their largest number brought to 2^14, so
  * that scores over keys of 2^100 and more may pass it sooner than their own size does.
  * first, first_lse (both or neither): the result [n][heads][dv] and log-sums
  * [n][heads] of the same queries over other keys (a shared prefix,

@@ -226,10 +226,14 @@ struct Joint {
 __device__ __forceinline__ float first_sum(const Attn4Args& a, int b, int h) {
   return a.first.p ? a.first_lse[(int64_t)b * a.heads + h] * kLog2e : -INFINITY;
 }
-__device__ __forceinline__ Joint join_first(float wide, float m, float l) {
+__device__ __forceinline__ Joint join_first(const Attn4Args& a, int b, float wide, float m, float l) {
   const float top = fmaxf(m, wide);
   // (The maximum passes over a log-sum of NaN, which has to arrive.)
-  if (m == -INFINITY && wide == -INFINITY && l == 0.f) return {0.f, 0.f, -INFINITY};
+  if (m == -INFINITY && wide == -INFINITY && l == 0.f) {
+    // No keys; or all scores below what fp32 holds.
+    const float nan = __uint_as_float(0x7fc00000u);
+    return len_of(a, b, false) > 0 ? Joint{nan, 0.f, nan} : Joint{0.f, 0.f, -INFINITY};
+  }
   const float mine = m == -INFINITY ? 0.f : exp2f(m - top);
   const float other = wide == -INFINITY ? 0.f : exp2f(wide - top);
   const float sum = l * mine + other;
@@ -765,7 +769,7 @@ __device__ __forceinline__ void emit(const Attn4Args& a, const Work4& w, const u
       *reinterpret_cast<float4*>(w.results + (piece * w.heads + h) * (64 * G) + d) = y;
       continue;
     }
-    const Joint z = join_first(reinterpret_cast<const Left<G>*>(room)->first[h], top, l);
+    const Joint z = join_first(a, b, reinterpret_cast<const Left<G>*>(room)->first[h], top, l);
     if (d < a.dv) put_result(a, b, head0 + h, d, y, z);
     if (a.lse && d == 0) a.lse[(int64_t)b * a.heads + head0 + h] = z.lse;
   }
@@ -991,7 +995,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join4_kernel(Attn4Args a, Wor
     const float wide = first_sum(a, b, head);  // before any log-sum is written
     if (Alone) {
       __syncwarp();
-      const Joint z = join_first(wide, top, l);
+      const Joint z = join_first(a, b, wide, top, l);
       if (a.lse && lane == 0) a.lse[(int64_t)b * a.heads + head] = z.lse;
 #pragma unroll
       for (int e = 0; e < kEach; ++e)
@@ -1013,7 +1017,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join4_kernel(Attn4Args a, Wor
         y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
         l += s_sum[i].y;
       }
-      const Joint z = join_first(wide, top, l);
+      const Joint z = join_first(a, b, wide, top, l);
       if (a.lse && tid == 0) a.lse[(int64_t)b * a.heads + head] = z.lse;
       if (4 * tid < a.dv) put_result(a, b, head, 4 * tid, y, z);
     }

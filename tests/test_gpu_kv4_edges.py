@@ -114,3 +114,28 @@ def test_a_first_result_that_is_nan(cuda_device, dtype, geo):
         assert bool(o[:3, 0].isnan().all()) and bool(s[:3, 0].isnan().all())
         assert not bool(o[:, 1:].isnan().any()) and not bool(s[:, 1:].isnan().any())
         assert not bool(o[3].isnan().any()) and not bool(s[3].isnan().any())
+
+
+@pytest.mark.parametrize("geo", GEOMETRIES)
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_scores_below_fp32(cuda_device, dtype, geo):
+    """A row whose scores are all below what fp32 holds is NaN, not a request without keys;
+    beside another result whose log-sum it does hold they weigh nothing."""
+    torch, ref, nys = _mods()
+    dt, dev = getattr(torch, dtype), cuda_device
+    lens = [1, 40, 2500, 0]
+    cache, table, slots, q, at, att, out, lse = _made(torch, nys, dev, lens, geo, dt, 1.0)
+    heads, kv, d, dv = geo
+    k = torch.zeros((sum(lens), kv, d), dtype=dt, device=dev)
+    k[..., 5] = 96.0
+    v = torch.randn((sum(lens), kv, dv), device=dev).to(dt)
+    cache.write(k, v, torch.cat(slots).to(dev))
+    q[:] = 0
+    q[..., 5] = -2.0 ** 126                       # scores of about -2^132
+    att.paged4(q, cache, at, table, out, lse=lse)
+    assert bool(out[:3].isnan().all()) and bool(lse[:3].isnan().all())
+    assert not bool(out[3].any()) and bool((lse[3] == -math.inf).all())
+    first, first_lse = torch.randn_like(out), torch.randn_like(lse)
+    att.paged4(q, cache, at, table, out, first=first, first_lse=first_lse, lse=lse)
+    assert torch.equal(out, first)
+    assert bool(((lse - first_lse).abs() <= 8 * ref.U * first_lse.abs()).all())
