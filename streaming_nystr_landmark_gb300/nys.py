@@ -838,7 +838,13 @@ class Rotation:
 class QKPrepare(_OnDevice):
     """What stands between a layer's projections and its attention: RMS norms of queries
     and keys for each head (weights [d] or None) and their rotation (a Rotation or None),
-    in one pass (``rows``), or in one with the write into the cache's pages (``append``)."""
+    in one pass (``rows``), or in one with the write into the cache's pages (``append``).
+    Calls on any stream may follow the constructor, which waits for its copies of the
+    weights; the object's memory stays until the calls that are queued are through.  One
+    whose calls a CUDA graph has captured has to stay for the graph's replays."""
+
+    _private = ()             # tensors of this object's own
+    _streams = frozenset()    # that their allocator knows to be reading them
 
     def __init__(self, heads, kv_heads, d, dtype=None, q_weight=None, k_weight=None, eps=1e-6,
                  rotation=None, device="cuda"):
@@ -861,6 +867,11 @@ class QKPrepare(_OnDevice):
                     raise ValueError(f"{name}: shape {tuple(w.shape)} != ({d},)")
                 w = w.detach().to(device=self.device, dtype=torch.float32, copy=True).contiguous()
             self._weights.append(w)
+        self._private = [w for w in self._weights if w is not None]
+        if self.device.type == "cuda" and self._private and not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(self.device).synchronize()
+        if rotation is not None:
+            self._private.append(rotation.turns)
         self._int32 = torch.int32
         self.cfg = NysAttnConfig(heads, kv_heads, d, d, _dtype_code(self.dtype), 0.0)
         at = [None if w is None else w.data_ptr() for w in self._weights]
@@ -868,6 +879,15 @@ class QKPrepare(_OnDevice):
         self._prep = NysQkPrepare(*at, eps, rotation.turns.data_ptr() if rot else None, rot,
                                   int(rot > 0 and rotation.interleaved), 0)
         nys_qk_rows(self.cfg, self._prep, 0, NysRows(), None, None, NysRows(), None)
+
+    def _stream(self):
+        stream = super()._stream()
+        if stream not in self._streams:
+            # The memory of tensors that nobody else knows goes back only after what this stream reads.
+            for t in self._private:
+                t.record_stream(self.torch.cuda.current_stream(self.device))
+            self._streams |= {stream}
+        return stream
 
     def _shifted(self, shift):
         """The arguments of the C calls for this shift."""
