@@ -819,6 +819,8 @@ class Rotation:
         if rot < 0 or rot % 2 or rot > d:
             raise ValueError(f"rot {rot}: need an even number of at most {d}")
         if freqs is None:
+            if rot and not 1e-300 <= base < float("inf"):
+                raise ValueError(f"base {base}: need a positive finite number")
             freqs = [float(base) ** (-2.0 * i / rot) for i in range(rot // 2)]
         freqs = [float(f) for f in freqs]
         if len(freqs) != rot // 2 or not all(math.isfinite(f) for f in freqs):
