@@ -17,3 +17,10 @@ def test_frequencies_need_no_base():
     assert nys.Rotation(4, base=0, freqs=[1.0, 0.5], device="cpu").turns.shape == (2,)
     assert nys.Rotation(4, base=0, rot=0, device="cpu").turns.shape == (0,)
     assert nys.Rotation(4, base=0.5, device="cpu").turns.shape == (2,)
+
+
+@pytest.mark.parametrize("scale", [1e-46, 1e-300, 1e39, 1e308])
+def test_scales_that_f32_does_not_hold(scale):
+    """0 would be taken for 1/sqrt(d)."""
+    with pytest.raises(ValueError, match="scale"):
+        nys.ExactAttention(2, 1, 64, 64, scale=scale, device="cpu")
