@@ -517,8 +517,10 @@ int nys_debug_stall_attn_once(int32_t role);
  *
  * the pairs being numbers i and i + rot/2 of a head, or 2i and 2i + 1
  * (interleaved), i < rot/2; numbers from rot on are not rotated.  All in fp32,
- * rounded once.  turns[i] is frequency_i / (2 pi) * 2^64, rounded, modulo 2^64:
- * the angle is then exact to 2^-31 of half a turn at every position. */
+ * rounded once: of a row whose squares pass fp32 finite numbers become 0 (as long as
+ * they hold their weight) and infinite ones NaN.  turns[i] is frequency_i / (2 pi) * 2^64,
+ * rounded, modulo 2^64: the angle is then off by 2^-25 of half a turn at most, its rounding
+ * to fp32, at every position. */
 typedef struct {
   const float* q_weight; /* device fp32 [d], or NULL: queries are not normalised */
   const float* k_weight; /* the same for keys                                    */
@@ -541,6 +543,7 @@ int nys_qk_rows(const nys_attn_config* cfg, const nys_qk_prepare* prep, int64_t 
 /* The same, with the prepared keys and the values v [tokens][kv_heads][dv] (as
  * they are) going into the pool's slots as in nys_kv_write, in the same launch.
  * q and q_out may be NULL (both), k_out too: keys then go to the pool alone.
+ * Two tokens with one slot leave a mixture of the two.
  * A token whose slot lies outside the pool gets its q_out and k_out rows all the
  * same.  Errors: NYS_E_INVAL, NYS_E_UNSUPPORTED, NYS_E_ALIGN, NYS_E_CUDA. */
 int nys_kv_append(const nys_attn_config* cfg, const nys_qk_prepare* prep, const nys_pool* pool,
