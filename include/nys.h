@@ -519,8 +519,8 @@ int nys_debug_stall_attn_once(int32_t role);
  * (interleaved), i < rot/2; numbers from rot on are not rotated.  All in fp32,
  * rounded once: of a row whose squares pass fp32 finite numbers become 0 (as long as
  * they hold their weight) and infinite ones NaN.  turns[i] is frequency_i / (2 pi) * 2^64,
- * rounded, modulo 2^64: the angle is then off by 2^-25 of half a turn at most, its rounding
- * to fp32, at every position. */
+ * rounded, modulo 2^64: the angle is then off by little more than 2^-25 of half a turn,
+ * its rounding to fp32, at every position. */
 typedef struct {
   const float* q_weight; /* device fp32 [d], or NULL: queries are not normalised */
   const float* k_weight; /* the same for keys                                    */
@@ -614,13 +614,14 @@ int nys_attn4_workspace_bytes(const nys_attn_config* cfg, int64_t n, int64_t key
  * exactly the values they stand for.  Scores take queries of 16-bit types as they
  * are (to 2^-39 of the row's largest number, or 2^-150 / scale where that is more),
  * fp32 ones to 22 bits; weights are held to 22 bits for the second product (to 2^-35
- * of the largest); sums run in fp32.  A request without keys gets 0 (lse -INF), whatever
- * its query row holds.  Pages outside the pool count as keys and values of 0
+ * of the largest); sums run in fp32.  A request without keys gets 0 (lse -INF),
+ * whatever its query row holds.  Pages outside the pool count as keys and values of 0
  * (NYS_ATTN_BAD_PAGE), lengths are taken clamped into their table (NYS_ATTN_BAD_LENGTH);
  * entries past a length are not read.  A query row that is not finite, or whose scores
  * pass fp32, gives NaN (scores below fp32 beside others, or beside a result that is
- * joined in, weigh nothing); rows are multiplied with their largest number brought to 2^14, so
- * that scores over keys of 2^100 and more may pass it sooner than their own size does.
+ * joined in, weigh nothing); rows are multiplied with their largest number brought to
+ * 2^14, so that scores over keys of 2^100 and more may pass it sooner than their own
+ * size does.
  * first, first_lse (both or neither): the result [n][heads][dv] and log-sums
  * [n][heads] of the same queries over other keys (a shared prefix,
  * nys_attn_shared), which are joined in; first may be out itself, and first_lse

@@ -15,12 +15,13 @@
 // Codes become f16 centred: keys' as c - 8, from 1024 + c less 1032 (bits 0-3) and 64 + c less 72 (bits 4-7),
 // a mask and a difference for two, and a shift for every second byte; values' as 2c - 15, in the same way after a
 // shift for every byte.  As they lie they are numbers too, c 2^-24 and c 2^-20, below the smallest normal one,
-// which the matrix units take, and faster (128 requests as below: 8 us of 95).  But the units cut every sum
+// which the matrix units take, and faster (128 requests as below: 82 us).  But the units cut every sum
 // towards zero, and scores of such small numbers are off by 2e-6 of the row instead of 1e-7.  Sums of one sign
 // over very many values show the cuts, because the result is small beside them: of codes as they lie 8e-4 of the
 // result over 200,000 keys, of c - 8, which is -1/2 on average, 3e-5.  So values' codes have a mean of 0, as far as
 // numbers lie evenly about a group's middle, and the products' sums end after 32 tokens, where f32 additions take
-// them: 2e-7, as elsewhere (the two long requests as below: 60.2 -> 61.8 us; with c - 8 61.4 and 2e-6).
+// them: 2e-7, as elsewhere (the two long requests as below 60 -> 61 us, the 128 91 -> 94; sums of c - 8 that end
+// after 32 tokens were off by 2e-6).
 //
 // Queries of 16-bit types go in as they are, of f32 as two f16 pieces (22 bits), after a power of two that fits
 // the row; the second pieces have products of their own.  Weights p_j step_j are two f16 pieces (22 bits) after
@@ -30,17 +31,18 @@
 // them.  Sums, maxima and the middles' part are f32.
 //
 // A warp works by itself: it streams pairs of blocks of 16 tokens (1,152 bytes a group of 64
-// each) through a ring of its own in shared memory with cp.async, and takes a range of one or
-// more requests' blocks.  Ranges come from the lengths, on the GPU, by either of two rules:
+// each) through a ring of its own in shared memory (three pairs; two of more than 192 numbers) with cp.async,
+// and takes a range of one or more requests' blocks.  Ranges come from the lengths, on the GPU, by either of two rules:
 // few (request, KV head) units are cut into pieces of up to 32 blocks for a CTA, whose warps join their
 // results in shared memory; else the units are laid end to end and every warp takes an even share
 // (joined in the CTA where all four are of one unit).  What cuts leave is joined by a second launch.
 //
 // What bounds it: instructions, not memory.  128 requests of 517 to 8,192 tokens, 16 heads over 8 of 128
-// numbers, bf16 (412 MB): 91 us, 4.5 TB/s of the 6.7 of a copy; counters at such a size: ALU pipe 53%, tensor 25%, DRAM 60%
-// busy.  2 requests of 131,075 and 200,000, 32 heads over 4 (191 MB): 60 us, 3.2 TB/s: 8 heads need the second
-// products.  64 chats of 97 to 3,025 in f32 (65 MB): 34 us, where ranges are 20 blocks and start, drain and join
-// weigh; 4 young requests: 8.5 us, a launch and one range's chain of loads.
+// numbers, bf16 (412 MB): 94 us, 4.4 TB/s of the 6.7 of a copy; counters at such a size: ALU pipe 52%, tensor 24%,
+// DRAM 58% busy.  2 requests of 131,075 and 200,000, 32 heads over 4 (191 MB): 61 us, 3.1 TB/s: 8 heads need the second
+// products.  64 chats of 97 to 3,025 in f32 (65 MB): 35 us, where ranges are 20 blocks and start, drain and join
+// weigh; 4 young requests: 8.5 us, a launch and one range's chain of loads.  64 of 517 to 8,192 with 8 heads over 1
+// of 256 numbers (52 MB): 40 us, 1.3 TB/s: two pairs in the ring, so that a warp's copies and products take turns.
 //
 // Blocks outside the pool are zeros, tokens past the length have weight 0 whatever their
 // bytes are.
@@ -59,7 +61,9 @@ namespace nys {
 namespace {
 
 constexpr int kHeads = 8;       // heads of a unit
-constexpr int kPiece = 8;       // blocks of a warp's part of a CTA's piece, at most
+// Blocks of a warp's part of a CTA's piece, at most (4, 16 and 32, against 8: 4 young requests 10.1, 8.1, 8.1 and
+// 8.0 us, one of 1,500 tokens 10.4, 12.6, 13.5 and 11.6).
+constexpr int kPiece = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 5.f;    // weights stay below 2^kLazy of the followed maximum's
@@ -1077,6 +1081,8 @@ cudaError_t launch(const Attn4Args& a, void* workspace, cudaStream_t stream) {
   e = cudaGetLastError();
   if (e != cudaSuccess || p.pieces == 0) return e;
   const int64_t rows = p.units * p.heads;
+  // A CTA a head where there are few, of many pieces each (2 very long requests 61 us, a warp a head 74); a warp a
+  // head else (128 requests of 517 to 8,192 94 us, a CTA a head 98).
   if (rows <= kSms * 4)
     return launch_dependent(join4_kernel<G, false>, dim3((unsigned)rows), kJoinWarps * 32, 0, stream, a, w);
   const int64_t ctas = (rows + kJoinWarps - 1) / kJoinWarps;

@@ -9,8 +9,8 @@
 //
 // Angles: f_i comes as turns a position, a 64-bit binary fraction F_i.  The product with
 // the position modulo 2^64 is the exact fraction of a turn for any 32-bit position, off
-// by position * 2^-65 turns for the rounding of F_i; its upper 32 bits go to sinpi and
-// cospi.  (In f32 the angle of position 10^6 would be off by 0.06.)
+// by position * 2^-65 turns for the rounding of F_i; its upper 32 bits, rounded to f32 (2^-25 of
+// half a turn), go to sinpi and cospi.  (In f32 the angle of position 10^6 would be off by 0.06.)
 //
 // 4 bits: for a group of 64 numbers with least lo and largest hi
 //   mid  = bf16(lo + (hi - lo) 8/15),  step = bf16 up(max((hi - mid) / 7, (mid - lo) / 8)),
@@ -31,8 +31,9 @@
 // into pages 89 us (537 MB, 90%); 32,768 of 32 + 4 in bf16 107 us (604 MB, 84%; issue slots 64% busy).  A part
 // of each row turned with an odd half (4,099 tokens of 18 rows of 80, 26 pairs, fp16) 16 us for 24 MB: pairs go
 // through shared memory, a warp makes one token and starts late.  4 bits are bound by instructions: 16,384
-// tokens of 8 + 8 rows of 128 in bf16 32 us in (86 MB; issue slots 67% busy), 19 us out (ALU pipe 68%).  One
-// token, or 64: 3.6 us, the launch and one chain of loads.
+// tokens of 8 + 8 rows of 128 in bf16 34 us in (86 MB; issue slots 67% busy), 18 us out (ALU pipe 68%), in f32 36 and
+// 39 us (153 MB); with 16 rows of queries, norm and rotation 68 us in bf16 (220 MB), 86 in f32 (422 MB).  One
+// token, or 64: 3.3 to 4.2 us, the launch and one chain of loads.
 #pragma once
 
 #include <cstdint>
@@ -236,7 +237,10 @@ template <typename T, int L, bool Q4, Turn R, Form F, Kind K>
 __device__ __forceinline__ void run_rows(const QkArgs& a, const Token& t, int first, int end,
                                          const float2* turns, float* stage) {
   constexpr int kPer = 32 / L;
-  constexpr int kAhead = sizeof(T) == 4 || Q4 ? 2 : R == kOdd ? 3 : 4;  // steps whose loads are in flight
+  // Steps whose loads are in flight, as many as 64 registers are good for.  1, 2, 3, 4: 64 prompts of 256 in f32 72,
+  // 68, 72, 78 us; 32,768 tokens in bf16 139, 116, 109, 107; 16,384 into 4 bits and back 56, 51, 49, 50; pairs that
+  // cross lanes (4,099 tokens, fp16) 14.8, 15.7, 16.1, 16.8.
+  constexpr int kAhead = sizeof(T) == 4 || Q4 ? 2 : R == kOdd ? 3 : 4;
   constexpr Turn S = K == kValues ? kNone : R;
   constexpr bool kInARow = S != kSides;
   const int lane = threadIdx.x & 31, l = lane & (L - 1), sub = lane / L;
@@ -433,7 +437,9 @@ __device__ __forceinline__ int64_t block_of(int64_t slot, int kv_heads, int page
   return page * kv_heads * page_blocks + (block - page * page_blocks);
 }
 
-// A warp takes part `w % parts` of token w / parts's steps of 32 / L rows.
+// A warp takes part `w % parts` of token w / parts's steps of 32 / L rows.  4 CTAs an SM, for which forms that
+// rotate spill 16 to 120 bytes a thread; with 3, where few spill and less, f32 prompts took 66.8 us instead of 67.7,
+// but bf16 ones 115 instead of 107, 4 bits 55 instead of 51.
 template <typename T, int L, bool Q4, Turn R, Form F>
 __global__ void __launch_bounds__(kThreads, 4) qk_kernel(QkArgs a, int parts) {
   constexpr int kPer = 32 / L;
@@ -523,7 +529,8 @@ cudaError_t launch_of(const QkArgs& a, cudaStream_t stream) {
 
 // Rows of a 4-bit cache as the values they stand for; a slot outside it gives zeros.  Warps
 // and lanes as above: a lane takes a code word of keys and one of values, four heads at a time, all their loads
-// before the first is used (scattered words of 4 bytes: a token's lie 16 or 64 bytes apart).
+// before the first is used (scattered words of 4 bytes: a token's lie 16 or 64 bytes apart).  16,384 tokens of 8
+// rows in and out, two, four, eight heads at a time: 51.0, 51.2, 54.5 us.
 template <typename T, int L, Form F>
 __global__ void __launch_bounds__(kThreads) read4_kernel(Read4Args a, int parts) {
   constexpr int kPer = 32 / L, kHeads = 4;
