@@ -133,7 +133,7 @@ __device__ __forceinline__ void mma_f16(bool first, float (&c)[4], const uint32_
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// (x & mask) | bits, less `less`: codes in the mantissas of a power of two, and whole numbers.
+// (x & mask) | bits, less `less`: codes in the mantissas of a power of two, and whole numbers (a widely known step).
 __device__ __forceinline__ uint32_t centred(uint32_t x, uint32_t mask, uint32_t bits, uint16_t less) {
   uint32_t y;
   asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "r"(mask), "r"(bits));
