@@ -179,10 +179,11 @@ def test_16_bit_results_of_all_forms(cuda_device, dtype, geo):
 @pytest.mark.parametrize("heads", [8, 16, 32, 64])
 def test_many_keys_in_f32(cuda_device, heads):
     """Over 400,000 keys that have nothing in common the result is 1/630 of a value's size, and
-    the codes less 8, of -1/2 on average, are sums of one sign.  The matrix units cut every sum
-    towards zero, by up to 2^-23 of it, half that on average: in at most 4 products over 32
-    tokens, whose sum is 16 steps in the end and half of that on the way, 2 * 2^-24 * 16 steps of
-    0.32 of a value's size for 32 tokens, or 0.32 * 2^-24 of it for one; times 630, 1.2e-5."""
+    codes less 8, which are -1/2 on average, would be sums of one sign.  The matrix units cut
+    every sum towards zero, by up to 2^-23 of it, half that on average: even so in at most 4
+    products over 32 tokens, whose sum is 16 steps in the end and half of that on the way, that is
+    2 * 2^-24 * 16 steps of 0.32 of a value's size for 32 tokens, or 0.32 * 2^-24 of it for
+    one; times 630, 1.2e-5.  (Sums that go on for all of a warp's keys are off by more.)"""
     torch, ref, nys = _mods()
     dev, n, kv, d = cuda_device, 400000, 8, 128
     g = torch.Generator(device=dev).manual_seed(23)
